@@ -15,6 +15,7 @@
 
 #include "fa.h"
 #include "fa_internal.h"
+#include "fa_serve.h"
 
 namespace {
 
@@ -107,6 +108,15 @@ int device_setup(unsigned **status) {
   }
   *status = g_status[dev];
   return FA_OK;
+}
+
+// sm_103 check of the current device alone (no device memory is touched).
+int device_check() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
+  if (dev < 0 || dev >= kMaxDevices) return FA_ERR_UNSUPPORTED;
+  std::lock_guard<std::mutex> lock(g_mu);
+  return check_sm103(dev);
 }
 
 int get_encoder() {
@@ -1204,3 +1214,18 @@ extern "C" int fa_bwd_varlen(const void *q, const void *k, const void *v, const 
                              s);
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
+
+// ---------------------------------------------------------------------------
+// Host helpers of the serving operators (fa_serve_api.cu).
+// ---------------------------------------------------------------------------
+namespace fa {
+
+int api_device_check() { return device_check(); }
+int api_device_status(unsigned **status) { return device_setup(status); }
+int api_sm_count() { return sm_count(); }
+unsigned long long api_wait_limit() {
+  const unsigned long long lim = g_wait_limit_ns.load();
+  return lim ? lim : kDefaultWaitLimitNs;
+}
+
+}  // namespace fa

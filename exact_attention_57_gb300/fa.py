@@ -1,8 +1,9 @@
 """ctypes binding of ``libfa.so`` (the C ABI in include/fa.h).
 
 The ``fa_*`` functions mirror the C entry points one to one and only marshal
-arguments.  ``attention``, ``attention_varlen`` and ``attention_backward`` are
-convenience wrappers for torch tensors: they allocate outputs and workspaces
+arguments.  ``attention``, ``attention_varlen``, ``attention_backward`` and the serving
+operators (``kv_plan``, ``rotary``, ``kv4_append``, ``kv4_gather``,
+``attention_kv4``) are convenience wrappers for torch tensors: they allocate outputs and workspaces
 with torch (device memory is the only thing torch provides here) and call the
 C entry points.
 
@@ -35,7 +36,9 @@ EXPORTED = ("fa_fwd", "fa_fwd_host", "fa_fwd_status", "fa_status_string", "fa_ve
             "fa_fwd_noalloc",
             "fa_fwd_splitkv", "fa_fwd_splitkv_workspace",
             "fa_fwd_varlen", "fa_bwd", "fa_bwd_workspace", "fa_fwd_staged",
-            "fa_fwd_staged_workspace", "fa_bwd_varlen", "fa_bwd_varlen_workspace")
+            "fa_fwd_staged_workspace", "fa_bwd_varlen", "fa_bwd_varlen_workspace",
+            "fa_kv_plan", "fa_rope_table", "fa_rope", "fa_kv4_append", "fa_kv4_gather",
+            "fa_fwd_kv4", "fa_fwd_kv4_workspace")
 
 _lib = None
 
@@ -104,6 +107,21 @@ def load(path: str | None = None):
     lib.fa_fwd_schedule.restype = i
     lib.fa_fwd_schedule_covers.argtypes = [i] * 5
     lib.fa_fwd_schedule_covers.restype = i
+    ll, ull = ctypes.c_longlong, ctypes.c_ulonglong
+    lib.fa_kv_plan.argtypes = [vp] * 10 + [i] * 5 + [vp]
+    lib.fa_kv_plan.restype = i
+    lib.fa_rope_table.argtypes = [vp, vp, i, vp]
+    lib.fa_rope_table.restype = i
+    lib.fa_rope.argtypes = [vp, vp, vp, i, vp, vp, vp, i, vp, i, vp] + [i] * 7 + [vp]
+    lib.fa_rope.restype = i
+    lib.fa_kv4_append.argtypes = [vp, vp, ll, ll, vp, i, vp, vp, vp, vp] + [i] * 7 + [vp]
+    lib.fa_kv4_append.restype = i
+    lib.fa_kv4_gather.argtypes = [vp, i] + [vp] * 6 + [i] * 7 + [vp]
+    lib.fa_kv4_gather.restype = i
+    lib.fa_fwd_kv4.argtypes = [vp] * 10 + [i] * 10 + [f] + [i] * 4 + [vp, ull, vp]
+    lib.fa_fwd_kv4.restype = i
+    lib.fa_fwd_kv4_workspace.argtypes = [i] * 5
+    lib.fa_fwd_kv4_workspace.restype = ull
     if path is None:
         _lib = lib
     return lib
@@ -405,4 +423,330 @@ def attention(q, k, v, scale: float | None = None, causal: bool = False, impl: s
             where = "fa_fwd_splitkv"
     if st != FA_OK:
         raise FaError(st, where)
+    return out, lse
+
+
+# ----------------------------------------------------------- serving operators
+def fa_kv_plan(cached_lens, new_lens, free_blocks, free_head, block_table, slots, positions,
+               cu_seqlens, seq_lens, counts, B, max_blocks, block_size, num_free, capacity,
+               stream) -> int:
+    return load().fa_kv_plan(cached_lens, new_lens, free_blocks, free_head, block_table, slots,
+                             positions, cu_seqlens, seq_lens, counts, B, max_blocks, block_size,
+                             num_free, capacity, stream)
+
+
+def fa_rope_table(inv_freq, axis, n, table) -> int:
+    return load().fa_rope_table(inv_freq, axis, n, table)
+
+
+def fa_rope(q, q_out, q_strides, Hq, k, k_out, k_strides, Hk, positions, num_axes, table, B, N, d,
+            d_rot, interleaved, inverse, dtype, stream) -> int:
+    return load().fa_rope(q, q_out, q_strides, Hq, k, k_out, k_strides, Hk, positions, num_axes,
+                          table, B, N, d, d_rot, int(interleaved), int(inverse), dtype, stream)
+
+
+def fa_kv4_append(k, v, k_stride, v_stride, slots, T, k_codes, k_scales, v_codes, v_scales,
+                  num_blocks, Hk, block_size, d, k_exp, v_exp, dtype, stream) -> int:
+    return load().fa_kv4_append(k, v, k_stride, v_stride, slots, T, k_codes, k_scales, v_codes,
+                                v_scales, num_blocks, Hk, block_size, d, k_exp, v_exp, dtype,
+                                stream)
+
+
+def fa_kv4_gather(slots, R, k_codes, k_scales, v_codes, v_scales, k_out, v_out, num_blocks, Hk,
+                  block_size, d, k_exp, v_exp, dtype, stream) -> int:
+    return load().fa_kv4_gather(slots, R, k_codes, k_scales, v_codes, v_scales, k_out, v_out,
+                                num_blocks, Hk, block_size, d, k_exp, v_exp, dtype, stream)
+
+
+def fa_fwd_kv4(q, o, lse, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens_k,
+               cu_seqlens_q, B, Hq, Hk, total_q, max_seqlen_q, max_seqlen_k, num_blocks,
+               block_size, max_blocks, d, scale, causal, k_exp, v_exp, dtype, workspace,
+               workspace_bytes, stream) -> int:
+    return load().fa_fwd_kv4(q, o, lse, k_codes, k_scales, v_codes, v_scales, block_table,
+                             seq_lens_k, cu_seqlens_q, B, Hq, Hk, total_q, max_seqlen_q,
+                             max_seqlen_k, num_blocks, block_size, max_blocks, d, scale, causal,
+                             k_exp, v_exp, dtype, workspace, workspace_bytes, stream)
+
+
+def fa_fwd_kv4_workspace(B, Hq, Hk, max_seqlen_q, d) -> int:
+    return load().fa_fwd_kv4_workspace(B, Hq, Hk, max_seqlen_q, d)
+
+
+def _same_device(first, *tensors):
+    """The CUDA device of `first`; every tensor given has to live there."""
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError("CUDA tensors expected")
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError("tensors on one device expected")
+    return dev
+
+
+def _call(where, dev, stream, fn, *args):
+    """fn(*args, stream) with `dev` current (its current stream unless one is
+    given); FaError on failure."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(dev).cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream)
+    if st != FA_OK:
+        raise FaError(st, where)
+
+
+def _need(t, dtype, what):
+    if t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous {dtype} tensor expected")
+
+
+def kv_plan(cached_lens, new_lens, free_blocks, block_table, block_size: int, capacity: int,
+            free_head=None, out=None, stream=None):
+    """Block tables and slot maps of a paged cache from request lengths.
+
+    cached_lens, new_lens: int32 [B]; free_blocks: int32 ids of free blocks
+    (free_head: int32 [1], how many are used already); block_table: int32
+    [B, max_blocks], updated in place.  capacity: length of the token arrays.
+    Returns (slots int64 [capacity], positions int32 [capacity], cu_seqlens
+    int32 [B+1], seq_lens int32 [B], counts int32 [2]: blocks needed, tokens);
+    out: those five tensors, to write to.  Raises FaError on failure."""
+    import torch
+    dev = _same_device(cached_lens, new_lens, free_blocks, block_table, free_head, *(out or ()))
+    B = cached_lens.numel()
+    i32 = torch.int32
+    for t, what in ((cached_lens, "cached_lens"), (new_lens, "new_lens"),
+                    (free_blocks, "free_blocks"), (block_table, "block_table")):
+        _need(t, i32, what)
+    if free_head is not None:
+        _need(free_head, i32, "free_head")
+        if free_head.numel() < 1:
+            raise ValueError("free_head: one element expected")
+    if new_lens.numel() != B or block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("cached_lens [B], new_lens [B], block_table [B, max_blocks] expected")
+    if out is None:
+        out = (torch.empty(capacity, dtype=torch.int64, device=dev),
+               torch.empty(capacity, dtype=i32, device=dev),
+               torch.empty(B + 1, dtype=i32, device=dev), torch.empty(B, dtype=i32, device=dev),
+               torch.empty(2, dtype=i32, device=dev))
+    else:
+        for t, dt, n in zip(out, (torch.int64, i32, i32, i32, i32), (capacity, capacity, B + 1, B, 2),
+                            strict=True):
+            _need(t, dt, "out")
+            if t.numel() != n:
+                raise ValueError("out: slots, positions [capacity], cu_seqlens [B+1], "
+                                 "seq_lens [B], counts [2] expected")
+    slots, positions, cu, lens, counts = out
+    _call("fa_kv_plan", dev, stream, load().fa_kv_plan, cached_lens.data_ptr(),
+          new_lens.data_ptr(), free_blocks.data_ptr(),
+          free_head.data_ptr() if free_head is not None else None, block_table.data_ptr(),
+          slots.data_ptr(), positions.data_ptr(), cu.data_ptr(), lens.data_ptr(),
+          counts.data_ptr(), B, block_table.shape[1], block_size, free_blocks.numel(), capacity)
+    return out
+
+
+def rotary_table(inv_freq, axes=None, device="cuda"):
+    """The int64 table rotary() takes: inv_freq, radians per position of each
+    pair; axes, the axis (0 .. 3) that turns it (default 0)."""
+    import torch
+    n = len(inv_freq)
+    f = (ctypes.c_double * n)(*[float(x) for x in inv_freq])
+    a = None
+    if axes is not None:
+        if len(axes) != n:
+            raise ValueError("one axis a pair expected")
+        a = (ctypes.c_int * n)(*[int(x) for x in axes])
+    t = torch.empty(n, dtype=torch.int64)
+    st = load().fa_rope_table(f, a, n, t.data_ptr())
+    if st != FA_OK:
+        raise FaError(st, "fa_rope_table")
+    return t.to(device)
+
+
+def _rope_strides(x, y):
+    a, b = x.stride(), y.stride()
+    if x.dim() == 4:  # [B, H, N, d]
+        return (ctypes.c_longlong * 6)(a[0], a[1], a[2], b[0], b[1], b[2])
+    return (ctypes.c_longlong * 6)(0, a[1], a[0], 0, b[1], b[0])  # [T, H, d]
+
+
+def rotary(q, k, positions, table, interleaved: bool = False, q_out=None, k_out=None,
+           stream=None, inverse: bool = False):
+    """Rotary positions on q and k: [B, H, N, d] with positions int32
+    [axes, B, N], or token-major [T, H, d] with positions int32 [axes, T]; any
+    strides with contiguous rows (slices of a fused projection); k may be
+    None.  table: rotary_table() over d_rot/2 pairs.  q_out, k_out: where to
+    write (q and k themselves rotate in place; default: new tensors).
+    Returns (q_out, k_out).  Raises FaError on failure."""
+    import torch
+    dev = _same_device(q, k, positions, table, q_out, k_out)
+    nd = q.dim()
+    if nd not in (3, 4):
+        raise ValueError("q [B,H,N,d] or [T,H,d] expected")
+    if nd == 4:
+        B, Hq, N, d = q.shape
+        rows = (B, N)
+    else:
+        N, Hq, d = q.shape
+        B, rows = 1, (N,)
+    _need(positions, torch.int32, "positions")
+    _need(table, torch.int64, "table")
+    if positions.shape[1:] != rows:
+        raise ValueError("positions [axes, B, N] (or [axes, T]) expected")
+    if q_out is None:
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    Hk = 0
+    if k is not None:
+        Hk = k.shape[1]
+        want = (B, Hk, N, d) if nd == 4 else (N, Hk, d)
+        if k_out is None:
+            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+        if k.shape != want or k.dtype != q.dtype or k_out.shape != want or k_out.dtype != q.dtype \
+                or k.stride(-1) != 1 or k_out.stride(-1) != 1:
+            raise ValueError("k, k_out: q's shape but for the heads, its dtype, contiguous rows")
+    if q_out.shape != q.shape or q_out.dtype != q.dtype or q.stride(-1) != 1 \
+            or q_out.stride(-1) != 1:
+        raise ValueError("q, q_out: one shape and dtype, contiguous rows")
+    _call("fa_rope", dev, stream, load().fa_rope, q.data_ptr(), q_out.data_ptr(),
+          _rope_strides(q, q_out), Hq, k.data_ptr() if Hk else None,
+          k_out.data_ptr() if Hk else None, _rope_strides(k, k_out) if Hk else None, Hk,
+          positions.data_ptr(), positions.shape[0], table.data_ptr(), B, N, d, 2 * table.numel(),
+          int(interleaved), int(inverse), _any_dtype(q))
+    return q_out, k_out
+
+
+def rotary_backward(dq, dk, positions, table, interleaved: bool = False, q_out=None, k_out=None,
+                    stream=None):
+    """Gradients of rotary()'s inputs from those of its outputs: the inverse
+    rotation, with rotary()'s arguments."""
+    return rotary(dq, dk, positions, table, interleaved, q_out, k_out, stream, inverse=True)
+
+
+def _any_dtype(t) -> int:
+    import torch
+    if t.dtype == torch.bfloat16:
+        return FA_DTYPE_BF16
+    if t.dtype == torch.float16:
+        return FA_DTYPE_F16
+    if t.dtype == torch.float32:
+        return FA_DTYPE_F32
+    raise ValueError(f"unsupported dtype {t.dtype}")
+
+
+def _cache_shape(k_codes, k_scales, v_codes, v_scales):
+    """(num_blocks, Hk, block_size, d) of the cache's four arrays."""
+    import torch
+    blocks, Hk, bs, half = k_codes.shape
+    for t, n in ((k_codes, half), (v_codes, half), (k_scales, half // 8), (v_scales, half // 8)):
+        if t.dtype != torch.uint8 or t.shape != (blocks, Hk, bs, n) or not t.is_contiguous():
+            raise ValueError("cache: contiguous uint8 codes [blocks, Hk, block_size, d/2] and "
+                             "scales [blocks, Hk, block_size, d/16] expected")
+    return blocks, Hk, bs, 2 * half
+
+
+def kv4_cache(num_blocks: int, Hk: int, block_size: int, d: int, device="cuda"):
+    """A zeroed 4-bit cache: (k_codes, k_scales, v_codes, v_scales)."""
+    import torch
+    shape = (num_blocks, Hk, block_size)
+    return tuple(torch.zeros(shape + (n,), dtype=torch.uint8, device=device)
+                 for n in (d // 2, d // 16, d // 2, d // 16))
+
+
+def kv4_append(k, v, slots, k_codes, k_scales, v_codes, v_scales, k_exp: int = 0, v_exp: int = 0,
+               stream=None):
+    """Write rows k, v [T, Hk, d] (bf16, fp16 or fp32; rows of any stride, e.g.
+    slices of a fused projection) into the 4-bit cache at slots int64 [T]
+    (-1 skips a row).  Raises FaError on failure."""
+    import torch
+    dev = _same_device(k, v, slots, k_codes, k_scales, v_codes, v_scales)
+    blocks, Hk, bs, d = _cache_shape(k_codes, k_scales, v_codes, v_scales)
+    T = slots.numel()
+    _need(slots, torch.int64, "slots")
+    for x in (k, v):
+        st = x.stride()
+        if x.shape != (T, Hk, d) or x.dtype != k.dtype or st[2] != 1 or (Hk > 1 and st[1] != d):
+            raise ValueError("k, v [T, Hk, d] of one dtype with contiguous rows expected")
+    row = Hk * d
+    _call("fa_kv4_append", dev, stream, load().fa_kv4_append, k.data_ptr(), v.data_ptr(),
+          k.stride(0) if T > 1 else row, v.stride(0) if T > 1 else row, slots.data_ptr(), T,
+          k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), blocks,
+          Hk, bs, d, k_exp, v_exp, _any_dtype(k))
+
+
+def kv4_gather(slots, k_codes, k_scales, v_codes, v_scales, dtype=None, k_exp: int = 0,
+               v_exp: int = 0, out=None, stream=None):
+    """Rows of the 4-bit cache at slots int64 [R] (-1 reads zeros) as (k, v),
+    each [R, Hk, d] of `dtype` (default bf16); out: those two tensors, to write
+    to.  Raises FaError on failure."""
+    import torch
+    dev = _same_device(slots, k_codes, k_scales, v_codes, v_scales, *(out or ()))
+    blocks, Hk, bs, d = _cache_shape(k_codes, k_scales, v_codes, v_scales)
+    R = slots.numel()
+    _need(slots, torch.int64, "slots")
+    if out is None:
+        dtype = torch.bfloat16 if dtype is None else dtype
+        out = (torch.empty((R, Hk, d), dtype=dtype, device=dev),
+               torch.empty((R, Hk, d), dtype=dtype, device=dev))
+    k, v = out
+    for x in out:
+        if x.shape != (R, Hk, d) or not x.is_contiguous() or x.dtype != k.dtype \
+                or (dtype is not None and x.dtype != dtype):
+            raise ValueError("out: two contiguous [R, Hk, d] tensors of the dtype expected")
+    _call("fa_kv4_gather", dev, stream, load().fa_kv4_gather, slots.data_ptr(), R,
+          k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
+          k.data_ptr(), v.data_ptr(), blocks, Hk, bs, d, k_exp, v_exp, _any_dtype(k))
+    return k, v
+
+
+def attention_kv4(q, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens_k,
+                  max_seqlen_k: int, cu_seqlens_q=None, max_seqlen_q: int = 1,
+                  scale: float | None = None, causal: bool = True, k_exp: int = 0, v_exp: int = 0,
+                  out=None, lse=None, workspace=None, stream=None):
+    """Attention of q [total_q, Hq, d] (bf16 or fp16) over the 4-bit paged cache.
+
+    block_table int32 [B, max_blocks], seq_lens_k int32 [B]; cu_seqlens_q
+    int32 [B+1] (None: one query a sequence).  Returns (o [total_q, Hq, d],
+    lse [Hq, total_q]).  The workspace (fa_fwd_kv4_workspace bytes) is
+    allocated with torch unless given.  Raises FaError on failure."""
+    import torch
+    dev = _same_device(q, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens_k,
+                       cu_seqlens_q, out, lse, workspace)
+    blocks, Hk, bs, d = _cache_shape(k_codes, k_scales, v_codes, v_scales)
+    total_q, Hq, dq = q.shape
+    if dq != d or not q.is_contiguous():
+        raise ValueError("q: a contiguous [total_q, Hq, d] tensor expected")
+    B = seq_lens_k.numel()
+    _need(seq_lens_k, torch.int32, "seq_lens_k")
+    _need(block_table, torch.int32, "block_table")
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table [B, max_blocks] expected")
+    if cu_seqlens_q is not None:
+        _need(cu_seqlens_q, torch.int32, "cu_seqlens_q")
+        if cu_seqlens_q.numel() != B + 1:
+            raise ValueError("cu_seqlens_q [B+1] expected")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+        raise ValueError("out: a contiguous tensor like q expected")
+    if lse is None:
+        lse = torch.empty((Hq, total_q), device=dev, dtype=torch.float32)
+    elif lse.shape != (Hq, total_q) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError("lse: a contiguous float32 [Hq, total_q] tensor expected")
+    lib = load()
+    if workspace is None:
+        need = lib.fa_fwd_kv4_workspace(B, Hq, Hk, max_seqlen_q, d)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _call("fa_fwd_kv4", dev, stream, lib.fa_fwd_kv4, q.data_ptr(), out.data_ptr(), lse.data_ptr(),
+          k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
+          block_table.data_ptr(), seq_lens_k.data_ptr(),
+          cu_seqlens_q.data_ptr() if cu_seqlens_q is not None else None, B, Hq, Hk, total_q,
+          max_seqlen_q, max_seqlen_k, blocks, bs, block_table.shape[1], d, scale,
+          int(bool(causal)), k_exp, v_exp, _any_dtype(q),
+          workspace.data_ptr() if workspace is not None else None,
+          workspace.numel() * workspace.element_size() if workspace is not None else 0)
     return out, lse

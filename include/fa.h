@@ -322,6 +322,172 @@ FA_API int fa_bwd_varlen(const void *q, const void *k, const void *v, const void
  * 0 for invalid arguments. */
 FA_API unsigned long long fa_bwd_varlen_workspace(int B, int H, int total_q, int max_seqlen_q, int d);
 
+/* ------------------------------------------------------------------------
+ * Serving: what a decoding server runs around the attention itself, in the
+ * order of one step: block tables and slot maps of a paged cache
+ * (fa_kv_plan), rotary positions on queries and keys (fa_rope), the new keys
+ * and values into a cache held in 4 bits (fa_kv4_append), and attention of the
+ * new queries over that cache (fa_fwd_kv4).  The pages have no counterpart to
+ * these; conventions (ownership, streams, errors) are those above, every array
+ * lies in device memory unless it says host, and buffers that a call writes
+ * overlap none that it reads.  All of them can be captured into a CUDA graph
+ * once each has been called on the device (fa_fwd_kv4 and fa_fwd share the
+ * status word that the first call makes).
+ *
+ * The 4-bit cache: num_blocks blocks of block_size tokens (16, 32, 64 or 128)
+ * for each of Hk key heads; four arrays, all contiguous and 16-byte aligned,
+ *   k_codes, v_codes    uint8 [num_blocks, Hk, block_size, d/2]: element x of
+ *                       a row is an e2m1 number in byte x/2, the low half for
+ *                       even x;
+ *   k_scales, v_scales  uint8 [num_blocks, Hk, block_size, d/16]: one e4m3
+ *                       number for 16 consecutive elements.
+ * An element is code * scale * 2^k_exp (v_exp for values), exponents in
+ * -64 .. 64 that move the range of the scales (2^-9 .. 448) to where the
+ * tensor's values lie; 4.5 bits an element.  A token's slot is
+ * block * block_size + offset.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * fa_kv_plan — block tables and slot maps from request lengths, on the GPU.
+ *
+ * Request b holds cached_lens[b] tokens in the cache and brings new_lens[b]
+ * more (negative lengths count as 0).  It gets the blocks it lacks from
+ * free_blocks, in order, behind those of the requests before it; its new
+ * tokens follow those of the requests before it.
+ *
+ * cached_lens, new_lens  int32 [B].
+ * free_blocks  int32 [num_free] ids of blocks that nobody holds (NULL when
+ *              num_free is 0).  free_head: device int32, how many of them are
+ *              used already, or NULL for 0; it is read, not advanced.
+ * block_table  int32 [B, max_blocks], in and out: the first
+ *              ceil(cached/block_size) entries of a row are read, the entries
+ *              for its new blocks written, the others left alone.
+ * slots        int64 [capacity] and positions int32 [capacity], out: slot and
+ *              position (cached + index) of every new token; entries behind
+ *              the last token get slot -1 and position 0, so that a padded
+ *              batch can pass them on.
+ * cu_seqlens   int32 [B+1], out: offsets of the requests' new tokens (the
+ *              cu_seqlens_q of fa_fwd_kv4), at most capacity each.
+ * seq_lens     int32 [B], out: cached + new, at most max_blocks * block_size.
+ * counts       int32 [2], out: blocks needed, tokens.  More blocks needed than
+ *              num_free minus free_head holds: the blocks missing are -1 in
+ *              the table and their tokens' slots -1.  More tokens than
+ *              capacity: those behind it are not written.  A token past
+ *              max_blocks * block_size gets slot -1 and no block.
+ * B 1 .. 65535; max_blocks * block_size <= 2^31 - 1.
+ * The call keeps nothing: the same inputs give the same outputs again.
+ */
+FA_API int fa_kv_plan(const int *cached_lens, const int *new_lens, const int *free_blocks,
+               const int *free_head, int *block_table, long long *slots, int *positions,
+               int *cu_seqlens, int *seq_lens, int *counts, int B, int max_blocks,
+               int block_size, int num_free, int capacity, void *stream);
+
+/*
+ * fa_rope_table — host-only: the table fa_rope takes, for n = d_rot/2 pairs.
+ * inv_freq  host doubles, radians per position, |f| <= 1e6.  axis: host ints
+ *           0 .. 3, the axis whose position turns the pair, or NULL for 0.
+ * table     host uint64 [n], out: f / (2 pi) modulo one turn, scaled by 2^64,
+ *           the two low bits holding the axis.  The caller copies it to the
+ *           device once.
+ */
+FA_API int fa_rope_table(const double *inv_freq, const int *axis, int n,
+                  unsigned long long *table);
+
+/*
+ * fa_rope — rotary positions with up to four axes (text: one; images and
+ * video: height, width, time) on the queries and keys of one layer, in one
+ * launch; with inverse = 1 the inverse rotation, which is the gradient: dq and
+ * dk from fa_bwd in, the gradients before the rotation out.
+ *
+ * q, k          inputs [B, Hq, N, d] and [B, Hk, N, d]; q_out, k_out outputs,
+ *               either the input itself (in place, the same strides) or
+ *               overlapping no input.  k may be NULL with Hk = 0.
+ * q_strides, k_strides  host arrays of six element strides, {batch, head, row}
+ *               of the input, then of the output, none negative (rows are d
+ *               contiguous elements; rows of an output lie apart); NULL:
+ *               contiguous.  Token-major [T, H, d] is B = 1, N = T, head
+ *               stride d, row stride H*d, and a slice of a fused projection
+ *               has that projection's row stride.
+ * positions     int32 [num_axes, B, N], any int32.
+ * table         uint64 [d_rot/2] from fa_rope_table, on the device.
+ * d_rot         even, 2 .. d: the first d_rot elements of a row turn, the
+ *               others are copied.  interleaved = 0: pair i is elements
+ *               (i, i + d_rot/2); 1: (2i, 2i+1).
+ * d 1 .. 256 (else FA_ERR_UNSUPPORTED); bf16, fp16 and fp32, computed in fp32
+ * and rounded once.  Pointers need their type's alignment only; 16-byte
+ * aligned rows run faster.
+ */
+FA_API int fa_rope(const void *q, void *q_out, const long long *q_strides, int Hq, const void *k,
+            void *k_out, const long long *k_strides, int Hk, const int *positions, int num_axes,
+            const unsigned long long *table, int B, int N, int d, int d_rot, int interleaved,
+            int inverse, int dtype, void *stream);
+
+/*
+ * fa_kv4_append — T rows of keys and values into the 4-bit cache.
+ *
+ * k, v     [T, Hk, d], rows k_stride and v_stride elements apart (at least
+ *          Hk*d; 16-byte aligned rows), bf16, fp16 or fp32.
+ * slots    int64 [T]; a slot outside [0, num_blocks * block_size) skips its
+ *          row.  Slots must differ: of two rows with one slot the stored one
+ *          may be a mixture.
+ * A group of 16 elements is stored with the scale e4m3(max|x| * 2^-exp / 6)
+ * and the codes e2m1(x * 2^-exp / scale), both rounded to nearest, ties to
+ * even, saturating; a NaN is stored as +6, a group whose scale rounds to zero
+ * as zeros.
+ * d a multiple of 16 up to 256 (else FA_ERR_UNSUPPORTED).
+ */
+FA_API int fa_kv4_append(const void *k, const void *v, long long k_stride, long long v_stride,
+                  const long long *slots, int T, void *k_codes, void *k_scales, void *v_codes,
+                  void *v_scales, int num_blocks, int Hk, int block_size, int d, int k_exp,
+                  int v_exp, int dtype, void *stream);
+
+/*
+ * fa_kv4_gather — R rows of the 4-bit cache as bf16, fp16 or fp32 (the input
+ * of fa_fwd or fa_fwd_varlen on a cached prefix).  slots int64 [R]; a slot
+ * outside the cache reads zeros.  k_out, v_out [R, Hk, d], contiguous, 16-byte
+ * aligned.  The values are exact in every type unless an exponent moves them
+ * out of its range.
+ */
+FA_API int fa_kv4_gather(const long long *slots, int R, const void *k_codes, const void *k_scales,
+                  const void *v_codes, const void *v_scales, void *k_out, void *v_out,
+                  int num_blocks, int Hk, int block_size, int d, int k_exp, int v_exp, int dtype,
+                  void *stream);
+
+/*
+ * fa_fwd_kv4 — attention of new queries over the 4-bit paged cache.
+ *
+ * q, o          [total_q, Hq, d], contiguous, bf16 or fp16, 16-byte aligned;
+ *               lse [Hq, total_q] fp32.  Query head h reads key head
+ *               h / (Hq/Hk); Hk divides Hq.
+ * cu_seqlens_q  int32 [B+1] offsets of the sequences' queries, or NULL: one
+ *               query a sequence (total_q = B, max_seqlen_q = 1).  Rows of o
+ *               and lse outside every sequence are left as they were.
+ * seq_lens_k    int32 [B] tokens of each sequence in the cache, its new ones
+ *               among them.  block_table int32 [B, max_blocks]: the blocks of
+ *               sequence b in order.  A table entry outside [0, num_blocks)
+ *               takes its tokens out of the softmax.
+ * max_seqlen_q, max_seqlen_k  bounds on the lengths; longer sequences are cut
+ *               to them (max_blocks * block_size bounds the keys too).  A loose
+ *               max_seqlen_k costs nothing.
+ * causal        1: query i of n_q sees key j iff j <= n_k - n_q + i (aligned
+ *               at the end, as the new tokens are the last cached ones); 0:
+ *               all keys.  A row that sees no key gets O = 0, LSE = -inf.
+ * d 64 or 128 (else FA_ERR_UNSUPPORTED); fp32 types are FA_ERR_UNSUPPORTED.
+ * workspace     fa_fwd_kv4_workspace(...) bytes, 256-byte aligned (NULL when
+ *               that is 0).  Calls that share it must not overlap on the GPU.
+ * The lengths, offsets and tables are read on the device and not checked on
+ * the host; whatever they hold, no access leaves the buffers.
+ */
+FA_API int fa_fwd_kv4(const void *q, void *o, float *lse, const void *k_codes, const void *k_scales,
+               const void *v_codes, const void *v_scales, const int *block_table,
+               const int *seq_lens_k, const int *cu_seqlens_q, int B, int Hq, int Hk, int total_q,
+               int max_seqlen_q, int max_seqlen_k, int num_blocks, int block_size,
+               int max_blocks, int d, float scale, int causal, int k_exp, int v_exp, int dtype,
+               void *workspace, unsigned long long workspace_bytes, void *stream);
+
+/* Bytes of workspace fa_fwd_kv4 needs; 0 for invalid arguments. */
+FA_API unsigned long long fa_fwd_kv4_workspace(int B, int Hq, int Hk, int max_seqlen_q, int d);
+
 /*
  * fa_fwd_host — the same forward on HOST buffers.
  *

@@ -1,0 +1,233 @@
+"""Host-side checks of the serving operators (no GPU work: every call here is
+refused, or is host-only) and the reference helpers of their GPU tests."""
+import ctypes
+import math
+import os
+from fractions import Fraction
+
+import pytest
+import torch
+
+import serve_util as ref
+from exact_attention_57_gb300 import fa
+
+# 1 / (2 pi) to 75 digits
+INV_2PI = Fraction("0.15915494309189533576888376337251436203445964574045644874766734405889679763")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    if not os.path.exists(fa.LIB_PATH):
+        from exact_attention_57_gb300 import build
+        build.build_library()
+    return fa.load()
+
+
+def A(i):
+    """Fake device addresses, 16 TB apart; never dereferenced."""
+    return (i + 1) << 44
+
+
+# ------------------------------------------------------------------ plan
+PLAN = dict(cached=A(0), new=A(1), free=A(2), head=None, table=A(3), slots=A(4), pos=A(5),
+            cu=A(6), lens=A(7), counts=A(8), B=3, width=4, bs=16, num_free=9, cap=20)
+
+
+def plan(**kw):
+    a = dict(PLAN, **kw)
+    return fa.fa_kv_plan(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(cached=None), dict(new=None), dict(free=None), dict(table=None), dict(slots=None),
+    dict(pos=None), dict(cu=None), dict(lens=None), dict(counts=None),
+    dict(B=0), dict(B=65536), dict(width=0), dict(bs=8), dict(bs=48), dict(bs=256),
+    dict(num_free=-1), dict(cap=0), dict(width=1 << 28),
+    dict(slots=A(4) + 4), dict(table=A(3) + 2), dict(head=A(9) + 1),
+    dict(slots=A(0)), dict(lens=A(1) + 4), dict(pos=A(4) + 8), dict(counts=A(2) + 32),
+    dict(head=A(3) + 8),
+], ids=str)
+def test_plan_refusals(kw):
+    assert plan(**kw) == fa.FA_ERR_INVALID_ARG
+
+
+# ------------------------------------------------------------------ rope
+def L6(*v):
+    return (ctypes.c_longlong * 6)(*v)
+
+
+ROPE = dict(q=A(0), qo=A(1), qs=None, Hq=4, k=A(2), ko=A(3), ks=None, Hk=2, pos=A(4), axes=2,
+            table=A(5), B=2, N=7, d=64, rot=64, inter=0, inv=0, dtype=fa.FA_DTYPE_BF16)
+
+
+def rope(**kw):
+    return fa.fa_rope(*dict(ROPE, **kw).values(), None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(q=None), dict(qo=None), dict(k=None), dict(ko=None), dict(pos=None), dict(table=None),
+    dict(Hq=0), dict(Hk=-1), dict(B=0), dict(N=0), dict(d=0), dict(axes=0), dict(axes=5),
+    dict(rot=0), dict(rot=63), dict(rot=66), dict(inter=2), dict(inv=-1), dict(dtype=4),
+    dict(q=A(0) + 1), dict(pos=A(4) + 2), dict(table=A(5) + 4),
+    dict(qo=A(0) + 64),                                     # shifted onto its own input
+    dict(qo=A(0), qs=L6(1792, 448, 64, 1792, 64, 256)),     # in place at other strides
+    dict(qs=L6(1792, 448, 64, 1792, 448, 63)),              # rows of the output meet
+    dict(qs=L6(1792, 448, 64, 0, 448, 64)),
+    dict(qs=L6(1792, 448, 64, 1792, 64, 64)),
+    dict(qs=L6(1792, -448, 64, 1792, 448, 64)),
+    dict(ko=A(4)), dict(ko=A(5)),
+], ids=str)
+def test_rope_refusals(kw):
+    assert rope(**kw) == fa.FA_ERR_INVALID_ARG
+
+
+def test_rope_head_dim_above_256_is_unsupported():
+    assert rope(d=264) == fa.FA_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("f", [1.0, 0.31, 1e-4, 2 * math.pi, 7.25, 12345.678, 1e6, -0.5, -1e-9,
+                               0.0, 5e-324])
+@pytest.mark.parametrize("axis", [0, 3])
+def test_rope_table_is_the_turn_fraction(f, axis):
+    """table = f / (2 pi) mod 1, scaled by 2^64, axis in the low bits.  The
+    two doubles that stand for 1 / (2 pi) are off by 2^-108 of it (f <= 1e6 <
+    2^20: 2^-27 of a unit at 2^64), the two truncations and the rounding by
+    less than 2.5 units, the cleared bits by 3; fma's own rounding of the
+    remainder is below 2^-53 * 2^-53 * 2^18."""
+    t = (ctypes.c_ulonglong * 1)()
+    assert fa.fa_rope_table((ctypes.c_double * 1)(f), (ctypes.c_int * 1)(axis), 1, t) == fa.FA_OK
+    assert t[0] & 3 == axis
+    want = Fraction(f) * INV_2PI * 2 ** 64
+    off = (Fraction(t[0] & ~3) - want) % 2 ** 64
+    assert min(off, 2 ** 64 - off) < 6
+
+
+@pytest.mark.parametrize("f,axis", [(float("nan"), 0), (float("inf"), 0), (1.1e6, 0), (1.0, 4),
+                                    (1.0, -1)])
+def test_rope_table_refusals(f, axis):
+    t = (ctypes.c_ulonglong * 1)(7)
+    r = fa.fa_rope_table((ctypes.c_double * 1)(f), (ctypes.c_int * 1)(axis), 1, t)
+    assert r == fa.FA_ERR_INVALID_ARG and t[0] == 7
+    assert fa.fa_rope_table(None, None, 1, t) == fa.FA_ERR_INVALID_ARG
+    assert fa.fa_rope_table((ctypes.c_double * 1)(1.0), None, 0, t) == fa.FA_ERR_INVALID_ARG
+
+
+# ------------------------------------------------------------------ cache
+STORE = dict(kc=A(10), ks=A(11), vc=A(12), vs=A(13))
+TAIL = dict(blocks=5, Hk=2, bs=16, d=64, ke=0, ve=0)
+
+
+def append(**kw):
+    a = dict(dict(k=A(0), v=A(1), kst=128, vst=128, slots=A(2), T=3), **STORE, **TAIL,
+             dtype=fa.FA_DTYPE_BF16)
+    a.update(kw)
+    return fa.fa_kv4_append(*a.values(), None)
+
+
+def gather(**kw):
+    a = dict(dict(slots=A(2), R=3), **STORE, ko=A(3), vo=A(4), **TAIL, dtype=fa.FA_DTYPE_BF16)
+    a.update(kw)
+    return fa.fa_kv4_gather(*a.values(), None)
+
+
+BAD_STORE = [dict(kc=None), dict(ks=None), dict(vc=None), dict(vs=None), dict(kc=A(10) + 8),
+             dict(vs=A(13) + 1), dict(blocks=0), dict(Hk=0), dict(bs=24), dict(bs=0), dict(ke=65),
+             dict(ve=-65), dict(dtype=9), dict(d=0)]
+
+
+@pytest.mark.parametrize("kw", BAD_STORE + [
+    dict(k=None), dict(v=None), dict(slots=None), dict(T=0), dict(kst=127), dict(kst=132),
+    dict(vst=120), dict(k=A(0) + 8), dict(slots=A(2) + 4), dict(vc=A(10) + 1024),
+    dict(kc=A(0)), dict(vs=A(2) + 16),
+], ids=str)
+def test_append_refusals(kw):
+    assert append(**kw) == fa.FA_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw", BAD_STORE + [
+    dict(slots=None), dict(ko=None), dict(vo=None), dict(R=0), dict(ko=A(3) + 8), dict(vo=A(3)),
+    dict(ko=A(10)), dict(vo=A(2) + 16),
+], ids=str)
+def test_gather_refusals(kw):
+    assert gather(**kw) == fa.FA_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("d", [8, 72, 272])
+def test_cache_head_dims_outside_the_set_are_unsupported(d):
+    assert append(d=d, kst=2 * d, vst=2 * d) == fa.FA_ERR_UNSUPPORTED
+    assert gather(d=d) == fa.FA_ERR_UNSUPPORTED
+
+
+# ------------------------------------------------------------------ attention
+ATTN = dict(q=A(0), o=A(1), lse=A(2), **STORE, table=A(5), lens=A(6), cu=A(7), B=3, Hq=4, Hk=2,
+            total=9, max_q=5, max_k=64, blocks=5, bs=16, width=4, d=64, scale=0.125, causal=1,
+            ke=0, ve=0, dtype=fa.FA_DTYPE_BF16, ws=A(14), wsb=1 << 40)
+
+
+def attn(**kw):
+    return fa.fa_fwd_kv4(*dict(ATTN, **kw).values(), None)
+
+
+@pytest.mark.parametrize("kw", BAD_STORE + [
+    dict(q=None), dict(o=None), dict(lse=None), dict(table=None), dict(lens=None),
+    dict(cu=None), dict(cu=None, max_q=1), dict(B=0), dict(B=65536), dict(Hq=0), dict(Hq=3),
+    dict(total=0), dict(max_q=0), dict(max_q=10), dict(max_k=-1), dict(width=0),
+    dict(width=1 << 28), dict(scale=float("nan")), dict(scale=float("inf")),
+    dict(scale=3e38, ke=64), dict(causal=2), dict(q=A(0) + 8), dict(o=A(1) + 2),
+    dict(lse=A(2) + 2), dict(table=A(5) + 1), dict(cu=A(7) + 2), dict(o=A(0)), dict(lse=A(1) + 16),
+    dict(o=A(10) + 16), dict(lse=A(6) + 4),
+], ids=str)
+def test_attention_refusals(kw):
+    assert attn(**kw) == fa.FA_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw", [dict(d=32), dict(d=256), dict(d=80), dict(dtype=fa.FA_DTYPE_F32),
+                                dict(dtype=fa.FA_DTYPE_F32_SIMT)], ids=str)
+def test_attention_outside_the_set_is_unsupported(kw):
+    assert attn(**kw) == fa.FA_ERR_UNSUPPORTED
+
+
+def test_wrappers_refuse_cpu_tensors_and_wrong_shapes():
+    i32 = torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        fa.kv_plan(i32, i32, i32, torch.zeros(3, 2, dtype=torch.int32), 16, 4)
+    cache = fa.kv4_cache(2, 1, 16, 64, device="cpu")
+    assert [tuple(t.shape) for t in cache] == [(2, 1, 16, 32), (2, 1, 16, 4)] * 2
+    x = torch.zeros(3, 1, 64)
+    with pytest.raises(ValueError):
+        fa.kv4_append(x, x, torch.zeros(3, dtype=torch.int64), *cache)
+    with pytest.raises(ValueError):
+        fa.rotary(x, None, torch.zeros(1, 3, dtype=torch.int32), torch.zeros(32, dtype=torch.int64))
+
+
+# ------------------------------------------------------------------ the references
+def test_reference_quantiser_picks_the_nearest_value():
+    """Brute force over all codes, and the borders' ties."""
+    x = torch.randn(50, 32, dtype=torch.float64, generator=torch.Generator().manual_seed(3))
+    codes, scales = ref.quantise(x)
+    got = ref.values(codes, scales)
+    grid = torch.cat([ref.CODES, -ref.CODES])
+    for r in range(50):
+        for g in range(2):
+            s = ref.SCALES[int(scales[r, g])]
+            for e in range(16):
+                v = x[r, 16 * g + e]
+                assert abs(got[r, 16 * g + e] - v) == (grid * s - v).abs().min()
+    tie = torch.tensor([6.0, 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0] * 2, dtype=torch.float64)
+    codes, scales = ref.quantise(tie[None])
+    assert ref.values(codes, scales)[0, :8].tolist() == [6.0, 0.0, 1.0, 1.0, 2.0, 2.0, 4.0, 4.0]
+
+
+@pytest.mark.parametrize("causal", [False, True])
+def test_reference_attention_matches_a_loop(causal):
+    g = torch.Generator().manual_seed(5)
+    q, K, V = (torch.randn(s, dtype=torch.float64, generator=g) for s in
+               ((3, 4, 16), (5, 2, 16), (5, 2, 16)))
+    o, lse, _, _ = ref.attend(q, K, V, 0.3, causal)
+    for i in range(3):
+        for h in range(4):
+            js = [j for j in range(5) if not causal or j <= 2 + i]
+            w = [math.exp(0.3 * float(q[i, h] @ K[j, h // 2])) for j in js]
+            assert abs(lse[h, i] - math.log(sum(w))) < 1e-12
+            want = sum(x * V[j, h // 2] for x, j in zip(w, js)) / sum(w)
+            assert (o[i, h] - want).abs().max() < 1e-12

@@ -1,0 +1,670 @@
+"""The serving operators on the GPU against 64-bit references: block tables,
+rotary positions, the 4-bit cache, attention over it, and a run of them
+together (needs a GB300)."""
+import math
+import random
+
+import pytest
+import torch
+
+import serve_util as ref
+from exact_attention_57_gb300 import fa
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+HALF_STEP = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}
+
+
+def ints(x, dtype=torch.int32):
+    return torch.tensor(x, dtype=dtype, device=DEV)
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+# ------------------------------------------------------------------ plan
+def run_plan(cached, new, free, table, bs, cap, head=0, **kw):
+    t = ints(table)
+    got = fa.kv_plan(ints(cached), ints(new), ints(free), t, bs, cap,
+                     free_head=ints([head]) if head else None, **kw)
+    return [t.tolist()] + [x.tolist() for x in got]
+
+
+def check_plan(cached, new, free, table, bs, cap, head=0):
+    got = run_plan(cached, new, free, table, bs, cap, head)
+    want = ref.plan(cached, new, free, head, table, bs, cap)
+    for name, a, b in zip(("table", "slots", "positions", "cu", "lens", "counts"), got, want):
+        assert a == list(b), name
+
+
+def plan_case(B, bs, top_cached, top_new, seed, spare=3, width_more=0):
+    r = random.Random(seed)
+    cached = [r.randrange(0, top_cached + 1) for _ in range(B)]
+    new = [r.choice([0, 1, r.randrange(0, top_new + 1)]) for _ in range(B)]
+    width = max(-(-(c + n) // bs) for c, n in zip(cached, new)) + width_more or 1
+    need = sum(-(-(c + n) // bs) + -(-c // bs) for c, n in zip(cached, new)) + spare
+    ids = list(range(need))
+    r.shuffle(ids)
+    table = []
+    for c in cached:
+        have = -(-c // bs)
+        table.append(ids[:have] + [-7] * (width - have))
+        ids = ids[have:]
+    return cached, new, ids, table
+
+
+@pytest.mark.parametrize("B,bs,top_cached,top_new,extra", [
+    (1, 16, 0, 1, 0), (1, 16, 15, 40, 5), (3, 32, 100, 70, 1), (17, 64, 1000, 500, 0),
+    (256, 16, 300, 2, 40), (257, 128, 700, 3, 0), (1000, 16, 60, 9, 2000), (5, 16, 10, 9000, 77),
+    (2, 16, 0, 0, 3),
+])
+def test_plan_matches_reference(B, bs, top_cached, top_new, extra):
+    cached, new, free, table = plan_case(B, bs, top_cached, top_new, seed=B + bs)
+    cap = max(1, sum(new) + extra)
+    check_plan(cached, new, free or [0], table, bs, cap)
+
+
+def test_plan_many_requests():
+    """More requests than one CTA takes at a time, each CTA's rounds apart."""
+    B, bs = 20000, 16
+    r = random.Random(1)
+    cached = [r.randrange(0, 40) for _ in range(B)]
+    new = [r.choice([0, 1, 1, 2, 30]) for _ in range(B)]
+    width = 5
+    table = [[b * 5 + j for j in range(width)] for b in range(B)]
+    free = list(range(10 ** 6, 10 ** 6 + 60000))
+    check_plan(cached, new, free, table, bs, sum(new) + 5000)
+
+
+def test_plan_head_short_list_full_table_and_small_capacity():
+    cached, new, free, table = plan_case(9, 16, 50, 60, seed=8)
+    check_plan(cached, new, [5, 6, 7] + free, table, 16, sum(new), head=3)
+    check_plan(cached, new, free[:4], table, 16, sum(new) + 1)          # blocks run out
+    check_plan(cached, new, free[:4], table, 16, sum(new) + 1, head=2)
+    check_plan(cached, new, free, table, 16, 7)                         # more tokens than capacity
+    # a table too narrow: tokens past it get no slot and no block
+    check_plan([30, 5, 40], [10, 60, 3], list(range(50, 70)),
+               [[1, 2], [3, -1], [4, 5]], 16, 80)
+    # negative lengths count as none
+    check_plan([-5, 4, 20], [3, -2, 1], [9, 8, 7], [[-1, -1], [1, -1], [2, 3]], 16, 6)
+
+
+def test_plan_without_free_blocks_and_twice():
+    table = [[4, -1], [6, 7]]
+    t = ints(table)
+    none = torch.empty(0, dtype=torch.int32, device=DEV)
+    for _ in range(2):  # the call keeps nothing: the same again
+        got = fa.kv_plan(ints([3, 20]), ints([2, 20]), none, t, 16, 30)
+        want = ref.plan([3, 20], [2, 20], [], 0, table, 16, 30)
+        assert t.tolist() == want[0] and [x.tolist() for x in got] == [list(x) for x in want[1:]]
+
+
+# ------------------------------------------------------------------ rotary
+def ladder(rot, axes):
+    half = rot // 2
+    return ([10000.0 ** (-2.0 * i / rot) for i in range(half)],
+            [min(axes - 1, i * axes // half) for i in range(half)])
+
+
+ROPE_CASES = [
+    # B, N, Hq, Hk, d, rot, axes, interleaved
+    (1, 1, 1, 0, 64, 64, 1, False), (2, 37, 4, 2, 128, 128, 3, False), (1, 5, 3, 1, 72, 72, 2, False),
+    (3, 11, 2, 2, 80, 64, 2, True), (2, 9, 5, 5, 256, 256, 4, False), (1, 300, 8, 1, 96, 48, 3, True),
+    (2, 3, 1, 1, 2, 2, 1, False), (1, 7, 2, 1, 30, 14, 2, True), (1, 6, 17, 4, 33, 10, 1, False),
+    (1, 1000, 40, 8, 128, 128, 1, True),
+]
+
+
+@pytest.mark.parametrize("case", ROPE_CASES, ids=str)
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("inverse", [False, True])
+def test_rotary_matches_reference(case, dtype, inverse):
+    """Tolerance: the angle's fraction of a turn is exact to 2^-32 before it
+    is rounded to fp32 (half a unit of an angle below pi: 2^-24 * pi), sine
+    and cosine are within 2 units (2^-22), the products and their sum round
+    three times: with s = |x1| + |x2|, off by (2^-24 pi + 2^-22 + 3 * 2^-24) s
+    < 2^-21 s, and half a step of the output type."""
+    B, N, Hq, Hk, d, rot, axes, inter = case
+    g = gen(N + d)
+    q, k = (torch.randn(B, h, N, d, generator=g).to(DT[dtype]) for h in (Hq, max(Hk, 1)))
+    pos = torch.randint(-70, 200000, (axes, B, N), generator=g, dtype=torch.int32)
+    pos[0, 0, 0] = 2 ** 31 - 1
+    freq, axis = ladder(rot, axes)
+    table = fa.rotary_table(freq, axis, device=DEV)
+    fn = fa.rotary_backward if inverse else fa.rotary
+    gq, gk = fn(q.to(DEV), k.to(DEV) if Hk else None, pos.to(DEV), table, interleaved=inter)
+    for x, y in ((q, gq),) + (((k, gk),) if Hk else ()):
+        want = ref.rotate(x, pos, torch.tensor(freq, dtype=torch.float64), torch.tensor(axis), rot,
+                          inter, inverse)
+        s = x.double().abs()
+        if inter:
+            pair = s[..., :rot].unflatten(-1, (-1, 2)).sum(-1).repeat_interleave(2, -1)
+        else:
+            pair = (s[..., :rot // 2] + s[..., rot // 2:rot]).repeat(1, 1, 1, 2)
+        tol = HALF_STEP[DT[dtype]] * want.abs() + 2.0 ** -25
+        tol[..., :rot] += 2.0 ** -21 * pair
+        assert ((y.double().cpu() - want).abs() <= tol).all()
+        assert torch.equal(y[..., rot:].cpu(), x[..., rot:])
+
+
+def test_rotary_layouts_strides_and_in_place():
+    """Token-major slices of a fused projection, at an odd offset too (the
+    scalar path), in place and into another slice, against the contiguous
+    call, bit for bit; everything around them stays as it was."""
+    T, Hq, Hk, d = 13, 4, 2, 64
+    g = gen(4)
+    table = fa.rotary_table(*ladder(64, 2), device=DEV)
+    pos = torch.randint(0, 5000, (2, T), generator=g, dtype=torch.int32).to(DEV)
+    for shift in (0, 1, 4):
+        flat = torch.randn(T * (Hq + 2 * Hk) * d + 8, generator=g).bfloat16().to(DEV)
+        qkv = flat[shift:shift + T * (Hq + 2 * Hk) * d].view(T, Hq + 2 * Hk, d)
+        q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hk], qkv[:, Hq + Hk:]
+        bh = [x.transpose(0, 1)[None].contiguous() for x in (q, k)]
+        wq, wk = fa.rotary(*bh, pos.view(2, 1, T), table)
+        oq, ok = fa.rotary(q, k, pos, table)
+        assert torch.equal(oq, wq[0].transpose(0, 1)) and torch.equal(ok, wk[0].transpose(0, 1))
+        v0, edge = v.clone(), flat[T * (Hq + 2 * Hk) * d + shift:].clone()
+        a, b = fa.rotary(q, k, pos, table, q_out=q, k_out=k)
+        assert a is q and torch.equal(q, oq) and torch.equal(k, ok) and torch.equal(v, v0)
+        assert torch.equal(flat[T * (Hq + 2 * Hk) * d + shift:], edge)
+        # there and back is the input, up to two roundings of the type
+        r, _ = fa.rotary_backward(oq, None, pos, table)
+        assert (r.double() - bh[0][0].transpose(0, 1).double()).abs().max() <= 4 * 2 * 2.0 ** -8 * 2
+
+
+def test_rotary_gradient_is_the_transpose():
+    """<rotary(x), y> = <x, rotary_backward(y)>, and differences: the rotation
+    is linear, so rotary(x + h e) - rotary(x) over h is column e for any h."""
+    B, H, N, d = 1, 2, 5, 32
+    g = gen(6)
+    x, y = (torch.randn(B, H, N, d, generator=g).to(DEV) for _ in range(2))
+    pos = torch.randint(0, 900, (1, B, N), generator=g, dtype=torch.int32).to(DEV)
+    table = fa.rotary_table(*ladder(d, 1), device=DEV)
+    fx = fa.rotary(x, None, pos, table)[0]
+    by = fa.rotary_backward(y, None, pos, table)[0]
+    lhs, rhs = (fx.double() * y.double()).sum(), (x.double() * by.double()).sum()
+    # every element within 2^-21 (|x1| + |x2|) (see above): 320 products of numbers below 6
+    assert abs(lhs - rhs) <= 2 * 320 * 2.0 ** -21 * 12 * 6
+    e = torch.zeros_like(x)
+    e[0, 1, 3, 7] = 1.0
+    col = (fa.rotary(x + e, None, pos, table)[0].double() - fx.double())
+    lhs, rhs = (col * y.double()).sum(), by[0, 1, 3, 7].double()
+    assert abs(lhs - rhs) <= 2 * 2 * 2.0 ** -21 * 12 * 6 + 2.0 ** -21 * 12
+
+
+# ------------------------------------------------------------------ cache
+def rows_of(cache, slots, bs):
+    """(codes, scales) rows [R, Hk, ...] of K and V at slots, on the CPU."""
+    s = slots.cpu()
+    return [c.cpu()[s // bs, :, s % bs] for c in cache]
+
+
+CACHE_CASES = [
+    # T, Hk, d, bs, dtype, k_exp, v_exp
+    (1, 1, 16, 16, "bf16", 0, 0), (37, 3, 64, 16, "fp16", 0, 0), (65, 8, 128, 64, "bf16", 0, 0),
+    (100, 2, 48, 32, "fp32", 0, 0), (9, 1, 256, 128, "fp32", -4, 3), (33, 2, 80, 16, "bf16", 5, -6),
+    (300, 4, 128, 32, "fp32", 0, 0),
+]
+
+
+@pytest.mark.parametrize("T,Hk,d,bs,dtype,ke,ve", CACHE_CASES)
+def test_cache_write_and_read(T, Hk, d, bs, dtype, ke, ve):
+    """Codes and scales are the nearest ones bit for bit (fp32 divisions and
+    the rounded products decide no border differently from 64 bits: the proof
+    is beside the kernel); reading back is exact."""
+    g = gen(T + d)
+    blocks = T // bs + 3
+    x = torch.randn(T, 3 * Hk, d, generator=g) * torch.rand(T, 3 * Hk, 1, generator=g)
+    x[:, :, ::16] *= 30
+    x[T // 2, 0, :16] = 0.0                       # a group of zeros
+    x[T // 3, Hk - 1, :16] = torch.tensor([6.0, 0.25, -0.75, 1.25, -1.75, 2.5, 3.5, -5.0] * 2)  # ties
+    x[T // 4, 0, d - 16:] *= 1e-4                 # scales in the subnormal range
+    x = x.to(DT[dtype])
+    kv = x.to(DEV)
+    k, v = kv[:, :Hk], kv[:, 2 * Hk:]
+    cache = fa.kv4_cache(blocks, Hk, bs, d, device=DEV)
+    for c in cache:
+        c.fill_(0xAB)
+    slots = torch.randperm(blocks * bs, generator=g)[:T]
+    skip = torch.rand(T, generator=g) < 0.2
+    sent = torch.where(skip, torch.tensor([-1, -9, blocks * bs])[torch.arange(T) % 3], slots)
+    fa.kv4_append(k, v, sent.to(DEV), *cache, k_exp=ke, v_exp=ve)
+    want = ref.quantise(x[:, :Hk], ke) + ref.quantise(x[:, 2 * Hk:], ve)
+    got = rows_of(cache, slots, bs)
+    for a, b in zip(got, want):
+        # -0 and +0 are one value: compare codes where not both zero
+        if a.shape[-1] == d // 2:
+            for sh in (0, 4):
+                p, q = (a >> sh) & 15, (b >> sh) & 15
+                assert torch.equal(torch.where(p == 8, 0, p)[~skip], torch.where(q == 8, 0, q)[~skip])
+        else:
+            assert torch.equal(a[~skip], b[~skip])
+        assert (a[skip] == 0xAB).all()
+    # untouched rows
+    mask = torch.ones(blocks * bs, dtype=torch.bool)
+    mask[slots[~skip]] = False
+    rest = mask.nonzero().flatten()
+    for c in rows_of(cache, rest, bs):
+        assert (c == 0xAB).all()
+    # read back, with rows outside the cache
+    back = torch.cat([torch.where(skip, -1, slots), torch.tensor([blocks * bs, -1])])
+    for out in DT.values():
+        gk, gv = fa.kv4_gather(back.to(DEV), *cache, dtype=out, k_exp=ke, v_exp=ve)
+        for y, (c, s), e in ((gk, want[:2], ke), (gv, want[2:], ve)):
+            val = ref.values(c, s, e)
+            val[skip] = 0
+            if out == torch.float16:
+                # an exponent can move values below fp16's normal range
+                assert ((y[:T].double().cpu() - val).abs() <= 2.0 ** -25).all()
+            else:
+                assert torch.equal(y[:T].double().cpu(), val)
+            assert (y[T:] == 0).all()
+
+
+def test_cache_borders_of_every_type():
+    """x at s * border for every scale and border, and one step of its type to
+    either side: the code is the nearest value's, ties the even one's."""
+    for dtype in (torch.bfloat16, torch.float16, torch.float32):
+        rows = []
+        for s in ref.SCALES[8::3].tolist():
+            if dtype == torch.float16 and 6 * s > 6e4:
+                continue
+            row = [6.0 * s]
+            for b in (0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0):
+                t = torch.tensor(b * s, dtype=dtype)
+                row += [float(t), float(torch.nextafter(t, torch.tensor(9e9, dtype=dtype)))]
+            row.append(-float(torch.nextafter(torch.tensor(2.5 * s, dtype=dtype),
+                                              torch.tensor(0.0, dtype=dtype))))
+            rows.append(row)
+        x = torch.tensor(rows, dtype=torch.float64).to(dtype)[:, None]
+        T = x.shape[0]
+        cache = fa.kv4_cache(8, 1, 16, 16, device=DEV)
+        slots = torch.arange(T)
+        fa.kv4_append(x.to(DEV), (-x).contiguous().to(DEV), slots.to(DEV), *cache)
+        got = rows_of(cache, slots, 16)
+        for a, b in zip(got, ref.quantise(x) + ref.quantise(-x)):
+            assert torch.equal(a, b)
+
+
+def test_cache_non_finite_input_saturates():
+    x = torch.ones(1, 1, 32)
+    x[0, 0, 3], x[0, 0, 4], x[0, 0, 20] = math.inf, -math.inf, math.nan
+    for dtype in DT.values():
+        cache = fa.kv4_cache(1, 1, 16, 32, device=DEV)
+        y = x.to(dtype).to(DEV)
+        fa.kv4_append(y, y, ints([2], torch.int64), *cache)
+        k, v = fa.kv4_gather(ints([2], torch.int64), *cache, dtype=torch.float32)
+        assert torch.isfinite(k).all() and torch.equal(k, v)
+        assert k[0, 0, 3] == 6 * 448 and k[0, 0, 4] == -6 * 448 and k[0, 0, 0] == 0
+        # the second group's scale is e4m3(1 / 6) = 0.171875; the NaN is stored as +6
+        assert k[0, 0, 20] == 6 * 0.171875 and k[0, 0, 21] == 6 * 0.171875
+
+
+# ------------------------------------------------------------------ attention
+def random_cache(blocks, Hk, bs, d, g):
+    """Every code, scales 2^-2 .. 1: scores and values of the usual size."""
+    def one():
+        return (torch.randint(0, 256, (blocks, Hk, bs, d // 2), generator=g, dtype=torch.uint8),
+                torch.randint(0x28, 0x39, (blocks, Hk, bs, d // 16), generator=g, dtype=torch.uint8))
+    return one() + one()
+
+
+def attention_tolerance(want, lse, a, big, scale, d, dtype):
+    """|dO|, |dLSE| allowed.  Scores: products of at most 17 significant bits
+    (fp16 or bf16 query, six-bit key), exact in fp32, d of them added: each
+    addition is off by 2^-23 of the sum of magnitudes at most (the tensor
+    cores truncate), so |ds| <= scale (d + 8) 2^-23 sum|q||k|; a weight is off
+    by e^(2 ds) times 2^-21 (exponential, sum and quotient) and, rounded to
+    fp16, by 2^-11 of itself.  O adds half a step of its type and 2^-24 for
+    fp16's subnormals."""
+    ds = abs(scale) * (d + 8) * 2.0 ** -23 * big + 2.0 ** -21
+    w = (2 * ds.transpose(0, 1)[..., None] + 2.0 ** -11 + 2.0 ** -20) * a
+    tol_o = HALF_STEP[dtype] * want.abs() + w * 1.01 + 2.0 ** -24 * (1 + a)
+    tol_l = ds + 2.0 ** -20 + 2.0 ** -22 * torch.nan_to_num(lse, neginf=0.0).abs()
+    return tol_o, tol_l
+
+
+def check_attention(q, cache, table, lens, nqs, bs, d, scale, causal, o, lse, dtype, exps=(0, 0),
+                    max_k=None, label=""):
+    """Every row of every sequence against the reference."""
+    K, V = ref.values(cache[0], cache[1], exps[0]), ref.values(cache[2], cache[3], exps[1])
+    blocks = K.shape[0]
+    row = 0
+    o, lse = o.double().cpu(), lse.double().cpu()
+    for b, (n, nq) in enumerate(zip(lens, nqs)):
+        n = min(n, len(table[b]) * bs)
+        if max_k is not None:
+            n = min(n, max_k)
+        ids = torch.tensor([table[b][j // bs] for j in range(n)], dtype=torch.long)
+        ok = (ids >= 0) & (ids < blocks)
+        at = ids.clamp(0, blocks - 1), torch.arange(n) % bs
+        Kb, Vb = K[at[0], :, at[1]], V[at[0], :, at[1]]
+        Vb = torch.where(ok[:, None, None], Vb, 0.0)
+        Kb = torch.where(ok[:, None, None], Kb, 0.0)
+        want, wl, a, big = ref.attend(q[row:row + nq].double(), Kb, Vb, scale, causal, ok)
+        tol_o, tol_l = attention_tolerance(want, wl, a, big, scale, d, dtype)
+        got, gl = o[row:row + nq], lse[:, row:row + nq]
+        none = wl == -math.inf
+        assert torch.equal(gl == -math.inf, none), f"{label} seq {b}: rows without keys"
+        assert (got.transpose(0, 1)[none] == 0).all(), f"{label} seq {b}"
+        off = (got - want).abs()
+        assert (off <= tol_o).all(), f"{label} seq {b} n={n} nq={nq}: O off by {off.max():.3e}"
+        off = torch.where(none, 0.0, (gl - wl).abs())
+        assert (off <= tol_l).all(), f"{label} seq {b} n={n} nq={nq}: LSE off by {off.max():.3e}"
+        row += nq
+
+
+def paged(lens, bs, blocks, g, more=1):
+    """Block table rows (ids shuffled over the cache); entries behind a
+    sequence's last block are wild."""
+    ids = torch.randperm(blocks, generator=g).tolist()
+    width = max(-(-n // bs) for n in lens) + more
+    table = []
+    for n in lens:
+        need = -(-n // bs)
+        table.append(ids[:need] + [-1, 2 ** 31 - 1, -2 ** 31][:width - need]
+                     + [10 ** 9] * max(0, width - need - 3))
+        ids = ids[need:]
+    return table
+
+
+def poison_tails(cache, table, lens, bs):
+    """NaN scales and full codes in every row no sequence holds."""
+    blocks, Hk = cache[0].shape[:2]
+    used = torch.zeros(blocks, bs, dtype=torch.bool)
+    for row, n in zip(table, lens):
+        for j in range(min(n, len(row) * bs)):
+            if 0 <= row[j // bs] < blocks:
+                used[row[j // bs], j % bs] = True
+    for c in cache:
+        c.transpose(1, 2)[~used] = 0xFF
+
+
+ATTN_CASES = [
+    # key lengths, query lengths (None: one each, no offsets), Hq, Hk, d, bs, dtype
+    ([1], None, 1, 1, 64, 16, "bf16"),
+    ([5, 0, 16, 17, 300], None, 8, 2, 128, 16, "bf16"),
+    ([1023], None, 32, 8, 128, 16, "bf16"),
+    ([1000, 31, 64, 2, 0, 777, 129], None, 5, 1, 64, 32, "fp16"),
+    ([4097, 130], None, 16, 1, 128, 64, "fp16"),
+    ([200, 513], None, 40, 2, 64, 128, "bf16"),
+    ([65, 257], None, 48, 1, 128, 16, "fp16"),
+    ([40] * 70, None, 4, 4, 64, 16, "bf16"),
+    ([100, 9, 0, 33, 2], [4, 1, 3, 0, 5], 16, 16, 64, 32, "fp16"),
+    ([300, 1, 128], [2, 8, 3], 6, 2, 128, 16, "bf16"),
+    ([64, 65], [8, 2], 8, 2, 128, 64, "bf16"),
+    ([130, 70], [130, 1], 4, 1, 128, 16, "bf16"),
+    ([300, 500, 20, 0], [129, 257, 60, 4], 6, 3, 64, 64, "fp16"),
+    ([700, 1500], [200, 3], 8, 8, 128, 32, "bf16"),
+    ([1000], [1000], 2, 1, 128, 128, "fp16"),
+    ([513, 100], [64, 33], 20, 4, 64, 16, "bf16"),
+]
+
+
+@pytest.mark.parametrize("case", ATTN_CASES, ids=[str(i) for i in range(len(ATTN_CASES))])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attention_matches_reference(case, causal):
+    lens, nqs, Hq, Hk, d, bs, dt = case
+    g = gen(len(lens) + Hq + d)
+    blocks = sum(-(-n // bs) for n in lens) + 2
+    cache = random_cache(blocks, Hk, bs, d, g)
+    table = paged(lens, bs, blocks, g)
+    poison_tails(cache, table, lens, bs)
+    total = len(lens) if nqs is None else sum(nqs) + 3  # rows behind the last sequence
+    q = torch.randn(total, Hq, d, generator=g).to(DT[dt])
+    scale = 1.0 / math.sqrt(d)
+    o = torch.full((total, Hq, d), 7.0, dtype=DT[dt], device=DEV)
+    lse = torch.full((Hq, total), 7.0, device=DEV)
+    cu = None
+    if nqs is not None:
+        cu = ints([sum(nqs[:i]) for i in range(len(nqs) + 1)])
+    fa.attention_kv4(q.to(DEV), *(c.to(DEV) for c in cache), ints(table), ints(lens),
+                     max(max(lens), 1), cu_seqlens_q=cu, max_seqlen_q=1 if nqs is None else max(nqs),
+                     scale=scale, causal=causal, out=o, lse=lse)
+    st, word = fa.fa_fwd_status(torch.cuda.current_stream().cuda_stream)
+    assert st == fa.FA_OK, word
+    nq = [1] * len(lens) if nqs is None else nqs
+    check_attention(q, cache, table, lens, nq, bs, d, scale, causal, o, lse, DT[dt])
+    assert (o[sum(nq):] == 7.0).all() and (lse[:, sum(nq):] == 7.0).all()
+
+
+def small(seed, lens=(90, 33), nqs=(1, 1), Hq=8, Hk=2, d=128, bs=16, dt="bf16"):
+    g = gen(seed)
+    blocks = sum(-(-n // bs) for n in lens) + 2
+    cache = random_cache(blocks, Hk, bs, d, g)
+    table = paged(lens, bs, blocks, g)
+    q = torch.randn(sum(nqs), Hq, d, generator=g).to(DT[dt])
+    cu = [sum(nqs[:i]) for i in range(len(nqs) + 1)]
+    return q, cache, table, cu
+
+
+def call(q, cache, table, lens, cu, nqs, max_k=None, **kw):
+    return fa.attention_kv4(q.to(DEV), *(c.to(DEV) for c in cache), ints(table), ints(list(lens)),
+                            max(lens) if max_k is None else max_k, cu_seqlens_q=ints(cu),
+                            max_seqlen_q=max(nqs), **kw)
+
+
+@pytest.mark.parametrize("nqs", [(1, 1), (5, 40)])
+@pytest.mark.parametrize("scale", [0.0, -0.2, 0.6])
+def test_attention_scales_and_exponents(nqs, scale):
+    lens, exps = (90, 133), (3, -5)
+    q, cache, table, cu = small(11, lens, nqs)
+    s = scale / 8
+    o, lse = call(q, cache, table, lens, cu, nqs, scale=s, k_exp=exps[0], v_exp=exps[1])
+    check_attention(q, cache, table, lens, nqs, 16, 128, s, True, o, lse, torch.bfloat16, exps)
+
+
+@pytest.mark.parametrize("nqs", [(1, 1), (4, 2), (70, 90)])
+def test_attention_missing_pages_and_bounds(nqs):
+    """Entries outside the cache in the middle of a sequence take their tokens
+    out; lengths past the table, past max_seqlen_k or below zero are cut."""
+    lens = (190, 160)
+    q, cache, table, cu = small(12, lens, nqs, bs=32)
+    table[0][2], table[1][0], table[1][4] = -1, len(cache[0]), -2 ** 31
+    o, lse = call(q, cache, table, lens, cu, nqs)
+    check_attention(q, cache, table, lens, nqs, 32, 128, 128 ** -0.5, True, o, lse, torch.bfloat16)
+    q, cache, table, cu = small(13, lens, nqs, bs=32)
+    o, lse = call(q, cache, table, (10 ** 9, 2 ** 31 - 1), cu, nqs, max_k=100)
+    check_attention(q, cache, table, (100, 100), nqs, 32, 128, 128 ** -0.5, True, o, lse,
+                    torch.bfloat16)
+    o, lse = call(q, cache, table, (-5, 77), cu, nqs, max_k=200)
+    check_attention(q, cache, table, (0, 77), nqs, 32, 128, 128 ** -0.5, True, o, lse,
+                    torch.bfloat16)
+
+
+def test_attention_wild_offsets_stay_inside():
+    """Query offsets outside [0, total_q]: rows are cut, nothing else is written."""
+    lens, nqs = (90, 33), (4, 4)
+    q, cache, table, _ = small(14, lens, nqs)
+    o = torch.full((12, 8, 128), 7.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((8 * 12,), 7.0, device=DEV)
+    call(q, cache, table, lens, [-100, 4, 2 ** 31 - 1], nqs, out=o[:8], lse=lse[:64].view(8, 8))
+    assert fa.fa_fwd_status(torch.cuda.current_stream().cuda_stream)[0] == fa.FA_OK
+    assert (o[8:] == 7.0).all() and (lse[64:] == 7.0).all()
+    check_attention(q, cache, table, lens, nqs, 16, 128, 128 ** -0.5, True, o[:8],
+                    lse[:64].view(8, 8), torch.bfloat16)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_attention_queries_of_extreme_size(dt):
+    """Rows whose elements spread over the type's whole range, and a row of
+    zeros: the query is rescaled by a power of two on its way to fp16, which
+    costs an element below 2^-14 of its row's largest an absolute 2^-25 of
+    that largest; the tolerance gets d * 2^-25 * max|q| * max|k| * scale."""
+    lens, nqs = (70, 50, 20), (1, 1, 1)
+    q, cache, table, cu = small(15, lens, nqs, dt=dt)
+    q = q.double()
+    big = 2.0 ** 100 if dt == "bf16" else 2.0 ** 12
+    q[0] *= big
+    q[1] *= 2.0 ** -12
+    q[1, :, ::3] *= 2.0 ** -12
+    q[2] = 0
+    q = q.to(DT[dt])
+    scale = 0.05 / big
+    for b, s in ((0, scale), (1, 0.05), (2, 0.05)):
+        o, lse = call(q[b:b + 1], cache, [table[b]], (lens[b],), [0, 1], (1,), scale=s)
+        K, V = ref.values(*cache[:2]), ref.values(*cache[2:])
+        ids = torch.tensor([table[b][j // 16] for j in range(lens[b])])
+        at = ids, torch.arange(lens[b]) % 16
+        want, wl, a, size = ref.attend(q[b:b + 1].double(), K[at[0], :, at[1]], V[at[0], :, at[1]], s,
+                                       True)
+        extra = 128 * 2.0 ** -25 * float(q[b].double().abs().max()) * 6 * s
+        tol_o, tol_l = attention_tolerance(want, wl, a, size, s, 128, DT[dt])
+        assert ((o.double().cpu() - want).abs() <= tol_o + 2 * extra * a).all()
+        assert ((lse.double().cpu() - wl).abs() <= tol_l + extra).all()
+
+
+def test_attention_long_context():
+    """A long sequence (split over many CTAs) against the float64 sums."""
+    n, Hq, Hk, d, bs = 70001, 4, 1, 128, 64
+    g = gen(21)
+    blocks = -(-n // bs) + 1
+    cache = random_cache(blocks, Hk, bs, d, g)
+    table = paged([n], bs, blocks, g)
+    poison_tails(cache, table, [n], bs)
+    q = torch.randn(1, Hq, d, generator=g).bfloat16()
+    o, lse = call(q, cache, table, (n,), [0, 1], (1,))
+    check_attention(q, cache, table, [n], [1], bs, d, d ** -0.5, True, o, lse, torch.bfloat16)
+
+
+def test_attention_cache_beyond_32_bit_offsets():
+    """A cache of more than 2^32 bytes of codes: blocks at both ends of it."""
+    Hk, d, bs = 8, 128, 128
+    blocks = (1 << 32) // (Hk * bs * d // 2) + 40  # codes alone pass 4 GB
+    kc = torch.empty(blocks, Hk, bs, d // 2, dtype=torch.uint8, device=DEV)
+    ks = torch.empty(blocks, Hk, bs, d // 16, dtype=torch.uint8, device=DEV)
+    g = gen(22)
+    lens, ids = [300], [blocks - 1, 0, blocks - 17]
+    part = random_cache(3, Hk, bs, d, g)
+    for i, b in enumerate(ids):
+        kc[b], ks[b] = part[0][i].to(DEV), part[1][i].to(DEV)
+    q = torch.randn(1, 16, d, generator=g).bfloat16()
+    o, lse = fa.attention_kv4(q.to(DEV), kc, ks, kc, ks, ints([ids]), ints(lens), 300)
+    check_attention(q, (part[0], part[1]) * 2, [[0, 1, 2]], lens, [1], bs, d, d ** -0.5, True, o, lse,
+                    torch.bfloat16)
+    slots = torch.tensor([b * bs + 5 for b in ids])
+    k, _ = fa.kv4_gather(slots.to(DEV), kc, ks, kc, ks)
+    want = torch.stack([ref.values(part[0][i, :, 5], part[1][i, :, 5]) for i in range(3)])
+    assert torch.equal(k.double().cpu(), want)
+
+
+# ------------------------------------------------------------------ together
+@pytest.mark.parametrize("graph", [False, True])
+def test_a_served_batch_step_by_step(graph):
+    """A prompt step and decode steps of a ragged batch: tables from lengths,
+    rotary positions, the new rows into the cache, attention over it; against
+    the same in 64 bits from the stored cache.  With `graph` the decode step
+    is captured once and replayed with the lengths fed back on the GPU."""
+    B, Hq, Hk, d, bs, width, steps = 3, 8, 2, 64, 16, 12, 5
+    g = gen(31)
+    blocks = B * width + 1
+    cache = fa.kv4_cache(blocks, Hk, bs, d, device=DEV)
+    for c in cache:
+        c.fill_(0xFF)
+    table = torch.full((B, width), -1, dtype=torch.int32, device=DEV)
+    free = torch.randperm(blocks, generator=g).int().to(DEV)
+    freq, axis = ladder(d, 1)
+    rt = fa.rotary_table(freq, axis, device=DEV)
+    lens, head = torch.zeros(B, dtype=torch.int32, device=DEV), ints([0])
+    history = [[] for _ in range(B)]
+
+    def step(new, qkv, cap, max_q):
+        slots, pos, cu, seq, counts = fa.kv_plan(lens, new, free, table, bs, cap, free_head=head)
+        q, k = fa.rotary(qkv[:, :Hq], qkv[:, Hq:Hq + Hk], pos.view(1, cap), rt)
+        fa.kv4_append(k, qkv[:, Hq + Hk:], slots, *cache)
+        o, lse = fa.attention_kv4(q, *cache, table, seq, width * bs, cu_seqlens_q=cu,
+                                  max_seqlen_q=max_q)
+        lens.copy_(seq)
+        head.add_(counts[:1])
+        return q, k, o, lse, cu
+
+    def check(new, qkv, q, k, o, lse):
+        row = 0
+        x = qkv.cpu()
+        for b, n in enumerate(new):
+            for t in range(row, row + n):
+                history[b].append((k[t].cpu(), x[t, Hq + Hk:]))
+            K = ref.values(*ref.quantise(torch.stack([h[0] for h in history[b]])))
+            V = ref.values(*ref.quantise(torch.stack([h[1] for h in history[b]])))
+            qb = q[row:row + n].double().cpu()
+            p = torch.arange(len(history[b]) - n, len(history[b])).view(1, 1, n)
+            turned = ref.rotate(x[row:row + n, :Hq].double().transpose(0, 1)[None], p,
+                                torch.tensor(freq, dtype=torch.float64), torch.tensor(axis), d)
+            assert (turned[0].transpose(0, 1) - qb).abs().max() <= 2.0 ** -8 * 6 + 2.0 ** -20
+            want, wl, a, big = ref.attend(qb, K, V, d ** -0.5, True)
+            tol_o, tol_l = attention_tolerance(want, wl, a, big, d ** -0.5, d, torch.bfloat16)
+            assert ((o[row:row + n].double().cpu() - want).abs() <= tol_o).all()
+            assert ((lse[:, row:row + n].double().cpu() - wl).abs() <= tol_l).all()
+            row += n
+
+    new = [37, 5, 64]
+    qkv = torch.randn(sum(new) + 4, Hq + 2 * Hk, d, generator=g).bfloat16().to(DEV)
+    q, k, o, lse, _ = step(ints(new), qkv, sum(new) + 4, max(new))
+    check(new, qkv, q, k, o, lse)
+    ones = ints([1] * B)
+    qkv = torch.randn(B, Hq + 2 * Hk, d, generator=g).bfloat16().to(DEV)
+    if graph:
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        keep = [t.clone() for t in (lens, head, table) + cache]
+        with torch.cuda.stream(side):
+            step(ones, qkv, B, 1)  # warm-up
+            for t, x in zip((lens, head, table) + cache, keep):
+                t.copy_(x)
+            side.synchronize()
+            cg = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(cg, stream=side):
+                q, k, o, lse, _ = step(ones, qkv, B, 1)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(steps):
+        qkv.copy_(torch.randn(qkv.shape, generator=g).bfloat16())
+        if graph:
+            cg.replay()
+        else:
+            q, k, o, lse, _ = step(ones, qkv, B, 1)
+        check([1] * B, qkv, q, k, o, lse)
+    assert lens.tolist() == [n + steps for n in new]
+    assert head.item() == sum(-(-(n + steps) // bs) for n in new)
+
+
+def test_two_streams_at_once():
+    """Two calls on two streams, a workspace each: the results of one alone."""
+    lens, nqs = (5000, 3000), (1, 1)
+    a, b = small(41, lens, nqs), small(42, lens, nqs)
+    args = []
+    for q, cache, table, cu in (a, b):
+        args.append((q.to(DEV), *(c.to(DEV) for c in cache), ints(table), ints(list(lens)), 5000))
+    alone = [fa.attention_kv4(*x) for x in args]
+    torch.cuda.synchronize()
+    s = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        got = []
+        for x, st in zip(args, s):
+            with torch.cuda.stream(st):
+                got.append(fa.attention_kv4(*x))
+        torch.cuda.synchronize()
+        for (o, l), (wo, wl) in zip(got, alone):
+            assert torch.equal(o, wo) and torch.equal(l, wl)
+
+
+def test_wrapper_refusals_on_the_gpu():
+    q, cache, table, cu = small(51)
+    dev = [c.to(DEV) for c in cache]
+    with pytest.raises(ValueError):
+        fa.attention_kv4(q.to(DEV), *dev, ints(table).long(), ints([90, 33]), 90)
+    with pytest.raises(ValueError):
+        fa.attention_kv4(q.to(DEV)[..., :64], *dev, ints(table), ints([90, 33]), 90)
+    with pytest.raises(ValueError):
+        fa.attention_kv4(q, *dev, ints(table), ints([90, 33]), 90)
+    with pytest.raises(ValueError):
+        fa.kv4_append(q.to(DEV), q.to(DEV), ints([1, 2], torch.int64), *dev)
+    with pytest.raises(ValueError):
+        fa.kv4_gather(ints([1, 2]), *dev)
+    with pytest.raises(ValueError):
+        fa.rotary(q.to(DEV), None, torch.zeros(1, 3, dtype=torch.int32, device=DEV),
+                  fa.rotary_table([1.0], device=DEV))
+    with pytest.raises(fa.FaError):
+        fa.attention_kv4(q.float().to(DEV), *dev, ints(table), ints([90, 33]), 90)
