@@ -1,14 +1,43 @@
-// fa_kv4_attn.cu — attention of packed queries over the paged 4-bit cache.
+// fa_kv4_attn.cu — attention of a few queries a sequence over the paged 4-bit
+// cache (decoding and drafted tokens): the cache is read once, and every
+// query row of a sequence that shares a key head rides along.
 //
 // Query token i of sequence b (n_q queries, n_k cached tokens, its own among
 // them) sees key j iff j < n_k and, when causal, j <= n_k - n_q + i; query
-// head h reads key head h / group.  One warp per query row: each lane scores
-// one of 32 keys from its dequantised row, the warp keeps the running maximum
-// and sum, then every lane adds p_j * v_j for its d / 32 columns.
+// head h reads key head h / group.  Row i * group + (h mod group) of key head
+// h / group is one column of the tile: with Q^T as the B operand,
+//   S^T = K Q^T   (m = 16 tokens, n = 8 rows, k = head dim)
+//   O^T += V^T P^T  (m = 16 columns of V, n = 8 rows, k = 16 tokens)
+// the streamed operand is always the wide A of mma.m16n8k16, so eight rows
+// cost no more than one and O^T takes D / 4 registers for eight rows.  (The
+// rows are too few for tcgen05, whose tiles have 128: a decode step is bound
+// by reading the cache, which keeps the tensor pipe below a third of the time.)
+//
+// K and V go from global memory to registers and from there to the tensor
+// core, with no shared memory: the order of k in S^T and of the columns of
+// V^T is free, so lane (r, c) = (lane / 4, lane % 4) takes D / 4 consecutive
+// elements of tokens r, r + 8 of K (one 16-byte load each at D = 128) and
+// D / 8 consecutive columns of tokens 2c, 2c + 1, 2c + 8, 2c + 9 of V.  Codes
+// become fp16 pairs by cvt (V: the nibbles of two tokens are merged into
+// bytes first, since a register holds two tokens of one column), times the
+// scale, exactly: a value has six significant bits.  Q is brought to fp16 by
+// a power of two a row, P is rounded to fp16 (relative 2^-11, one rounding of
+// the order of the output's own), everything is summed in fp32.
+//
+// Work is dealt in units of 128 tokens (16 for each of the 8 warps) of one
+// sequence and key head, in one line over all of them, equal shares to the
+// CTAs of one resident wave: ragged lengths and few long sequences balance
+// alike.  A CTA's first and last sequence may be shared with its neighbours;
+// such parts go to the workspace (two a CTA, whatever the lengths), and a
+// second kernel joins them.
+#include <atomic>
+#include <type_traits>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "fa.h"
+#include "fa_internal.h"
 #include "fa_kv4.cuh"
 #include "fa_serve.h"
 #include "ptx.cuh"
@@ -16,105 +45,584 @@
 namespace fa {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kThreads = 256, kWarps = 8;
+constexpr int kUnit = 16 * kWarps;  // tokens of one unit
 
-template <typename T, int D>
-__global__ void __launch_bounds__(32 * kWarps) fa_kv4_attn_kernel(const Kv4Attn p) {
-  griddep_wait();
-  griddep_launch_dependents();
-  __shared__ float sq[kWarps][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int b = blockIdx.z, h = blockIdx.y;
-  int r0 = b, nq = 1;
-  if (p.cu_q) {
-    r0 = min(max(p.cu_q[b], 0), p.total_q);
-    nq = min(min(max(p.cu_q[b + 1], 0), p.total_q) - r0, p.max_q);
-  }
-  const int i = blockIdx.x * kWarps + warp;
-  if (i >= nq) return;
-  const int bs = 1 << p.c.bs_log2;
-  const int nk = static_cast<int>(min(static_cast<long long>(min(max(p.lens[b], 0), p.max_k)),
-                                      static_cast<long long>(p.width) << p.c.bs_log2));
-  const int last = p.causal ? min(nk, nk - nq + i + 1) : nk;  // keys [0, last)
-  const long long row = static_cast<long long>(r0 + i) * p.Hq + h;
-  const T *q = static_cast<const T *>(p.q) + row * D;
-  for (int x = lane; x < D; x += 32) sq[warp][x] = static_cast<float>(q[x]) * p.scale_log2;
-  __syncwarp();
-  const int hk = h / p.group;
-  float m = -INFINITY, l = 0.f, acc[D / 32] = {};
-  for (int j0 = 0; j0 < last; j0 += 32) {
-    const int j = j0 + lane;
-    const int id = j < last ? p.table[static_cast<long long>(b) * p.width + (j >> p.c.bs_log2)] : -1;
-    const bool ok = static_cast<unsigned>(id) < static_cast<unsigned>(p.c.num_blocks);
-    const long long at =
-        ok ? ((static_cast<long long>(id) * p.c.Hk + hk) << p.c.bs_log2) + (j & (bs - 1)) : 0;
-    float sc = -INFINITY;
-    if (ok) {
-      sc = 0.f;
-      for (int g = 0; g < D / 16; ++g) {
-        const uint2 w = reinterpret_cast<const uint2 *>(p.c.k_codes)[at * (D / 16) + g];
-        const float s = f16x2_f32(e4m3x2_f16x2(p.c.k_scales[at * (D / 16) + g])).x;
-        const uint32_t pr[8] = {e2m1x2_f16x2<0>(w.x), e2m1x2_f16x2<1>(w.x), e2m1x2_f16x2<2>(w.x),
-                                e2m1x2_f16x2<3>(w.x), e2m1x2_f16x2<0>(w.y), e2m1x2_f16x2<1>(w.y),
-                                e2m1x2_f16x2<2>(w.y), e2m1x2_f16x2<3>(w.y)};
-        float dot = 0.f;
-        for (int n = 0; n < 8; ++n) {
-          const float2 f = f16x2_f32(pr[n]);
-          dot += f.x * sq[warp][g * 16 + 2 * n] + f.y * sq[warp][g * 16 + 2 * n + 1];
-        }
-        sc += dot * s;
-      }
-    }
-    float mt = sc;
-    for (int o = 16; o; o /= 2) mt = fmaxf(mt, __shfl_xor_sync(~0u, mt, o));
-    if (mt == -INFINITY) continue;
-    const float mn = fmaxf(m, mt), f = exp2f(m - mn), pj = exp2f(sc - mn);
-    m = mn;
-    l = l * f + pj;
-    for (float &a : acc) a *= f;
-    for (int t = 0; t < 32; ++t) {
-      const float w = __shfl_sync(~0u, pj, t);
-      const long long vt = __shfl_sync(~0u, at, t);
-      if (w == 0.f) continue;
-#pragma unroll
-      for (int n = 0; n < D / 32; ++n) {
-        const int x = lane + 32 * n;
-        const uint32_t byte = p.c.v_codes[vt * (D / 2) + x / 2];
-        const float2 f2 = f16x2_f32(e2m1x2_f16x2<0>(byte));
-        const float s = f16x2_f32(e4m3x2_f16x2(p.c.v_scales[vt * (D / 16) + x / 16])).x;
-        acc[n] += w * s * ((x & 1) ? f2.y : f2.x);
-      }
-    }
-  }
-  for (int o = 16; o; o /= 2) l += __shfl_xor_sync(~0u, l, o);
-  T *out = static_cast<T *>(p.o) + row * D;
-  const float inv = l > 0.f ? p.v_mul / l : 0.f;
-  for (int n = 0; n < D / 32; ++n) out[lane + 32 * n] = static_cast<T>(acc[n] * inv);
-  if (lane == 0)
-    p.lse[static_cast<long long>(h) * p.total_q + r0 + i] =
-        l > 0.f ? m * 0.6931471805599453f + logf(l) : -INFINITY;
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <typename T, int D>
-cudaError_t launch(const Kv4Attn &p, cudaStream_t s) {
+// Transposes an 8 x 8 matrix of 16-bit numbers held as mma fragments.
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t y;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  return y;
+}
+
+template <int W>
+__device__ __forceinline__ void load_words(uint32_t (&x)[W], const uint8_t *p) {
+  if constexpr (W == 4)
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "l"(p));
+  else if constexpr (W == 2)
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
+                 : "=r"(x[0]), "=r"(x[1]) : "l"(p));
+  else
+    asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(x[0]) : "l"(p));
+}
+
+// One sequence as this kernel sees it.
+struct Seq {
+  int r0, nq, nk;
+};
+
+__device__ __forceinline__ Seq load_seq(const Kv4Attn &p, int b) {
+  Seq s = {b, 1, 0};
+  if (p.cu_q) {
+    s.r0 = min(max(p.cu_q[b], 0), p.total_q);
+    s.nq = min(max(min(max(p.cu_q[b + 1], 0), p.total_q) - s.r0, 0), p.max_q);
+  }
+  s.nk = static_cast<int>(min(static_cast<long long>(min(max(p.lens[b], 0), p.max_k)),
+                              static_cast<long long>(p.width) << p.c.bs_log2));
+  return s;
+}
+
+// Units of one key head of a sequence; a sequence without keys still has one
+// (its rows get their zeros), one with more than `rows` rows none (the
+// kernel for many queries takes it).
+__device__ __forceinline__ int units_of(const Seq &s, int group, int rows) {
+  if (s.nq == 0 || static_cast<long long>(s.nq) * group > rows) return 0;
+  return max(1, (s.nk + kUnit - 1) / kUnit);
+}
+
+// Where a unit lies in the line of all units.
+struct Place {
+  long long total;   // units in all
+  long long before;  // units before sequence b
+  int b;
+};
+
+// The place of unit floor(total * num / den) (all threads get it).  `sums`
+// holds kThreads + 1 prefix sums.
+__device__ Place find_unit(const Kv4Attn &p, int rows, int num, int *den, long long *target,
+                           long long *sums, long long (*warp_sums)[kWarps]) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  Place at = {0, 0, 0};
+  // total first, where one round of requests does not show it
+  if (p.B > kThreads) {
+    long long n = 0;
+    for (int b = tid; b < p.B; b += kThreads) n += units_of(load_seq(p, b), p.group, rows);
+    for (int o = 16; o; o /= 2) n += __shfl_xor_sync(~0u, n, o);
+    if (lane == 0) warp_sums[1][warp] = n;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) at.total += warp_sums[1][w];
+    at.total *= p.c.Hk;
+  }
+  for (int base = 0;; base += kThreads) {
+    const int b = base + tid;
+    long long n = b < p.B ? units_of(load_seq(p, b), p.group, rows) : 0;
+    n *= p.c.Hk;
+    long long incl = n;
+    for (int o = 1; o < 32; o *= 2) {
+      const long long x = __shfl_up_sync(~0u, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 31) warp_sums[0][warp] = incl;
+    __syncthreads();
+    long long pre = at.before, all = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) pre += warp_sums[0][w];
+      all += warp_sums[0][w];
+    }
+    sums[tid] = pre + incl - n;
+    __syncthreads();
+    if (p.B <= kThreads) at.total = all;
+    if (base == 0) {
+      *den = static_cast<int>(min(static_cast<long long>(*den), at.total));
+      if (num >= *den) return at;  // more CTAs than units
+      *target = at.total * num / *den;
+    }
+    if (*target < at.before + all || base + kThreads >= p.B) {
+      int i = 0;
+      for (int step = kThreads / 2; step > 0; step /= 2)
+        if (sums[i + step] <= *target) i += step;
+      at.b = base + i;
+      at.before = sums[i];
+      return at;
+    }
+    at.before += all;
+    __syncthreads();
+  }
+}
+
+// 16 tokens of one page as lane (r, c) holds them.
+template <int D>
+struct Tile {
+  uint32_t k[2][D / 32], v[4][D / 64];
+  uint32_t ks[2], vs[4];
+};
+
+template <typename T>
+__device__ __forceinline__ float2 pair_f32(uint32_t x) {
+  if constexpr (sizeof(T) == 2) {
+    const T *e = reinterpret_cast<const T *>(&x);
+    return make_float2(static_cast<float>(e[0]), static_cast<float>(e[1]));
+  }
+}
+
+template <int NT, int D>
+constexpr int smem_bytes() {
+  return kWarps * NT * 8 * (D + 4 + 2) * 4;
+}
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
+    fa_kv4_attn_kernel(const Kv4Attn p, float *ws) {
+  constexpr int R = NT * 8;              // rows of the tile
+  constexpr int KS = D / 16;             // k steps of S^T, m tiles of O^T
+  constexpr int LD = D + 4;
+  extern __shared__ float smem[];
+  __shared__ long long s_sums[kThreads], s_warp[2][kWarps];
+  float *s_o = smem;                     // [warp][R][LD]
+  float *s_m = smem + kWarps * R * LD;   // [warp][R]
+  float *s_l = s_m + kWarps * R;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int r = lane >> 2, c = lane & 3;
+  griddep_wait();
+  griddep_launch_dependents();
+  int den = gridDim.x;
+  long long u = 0;
+  const Place at = find_unit(p, R, blockIdx.x, &den, &u, s_sums, s_warp);
+  if (static_cast<int>(blockIdx.x) >= den) return;
+  const long long u1 = at.total * (blockIdx.x + 1) / den;
+  const int bs = 1 << p.c.bs_log2;
+
+  int b = at.b;
+  Seq sq = load_seq(p, b);
+  int n_units = units_of(sq, p.group, R);
+  const long long into = u - at.before;
+  int h = static_cast<int>(into / n_units), unit = static_cast<int>(into - static_cast<long long>(h) * n_units);
+  while (u < u1) {
+    while (n_units == 0) {  // another sequence of this kernel follows, since u < total
+      sq = load_seq(p, ++b);
+      n_units = units_of(sq, p.group, R);
+      h = 0;
+    }
+    const int t_lo = unit;
+    const int t_hi = static_cast<int>(min(static_cast<long long>(n_units), t_lo + (u1 - u)));
+    const int rows = sq.nq * p.group;
+
+    // Q fragments: lane (r, c) holds D / 4 elements of row nt * 8 + r
+    uint32_t qf[NT][D / 8];
+    float qs[NT][2];
+    int lim[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = nt * 8 + r;
+      const int i = row / p.group, j = row - i * p.group;
+      float x[D / 4], amax = 0.f;
+      if (row < rows) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(
+            static_cast<const T *>(p.q) +
+            (static_cast<long long>(sq.r0 + i) * p.Hq + h * p.group + j) * D + c * (D / 4));
+#pragma unroll
+        for (int n = 0; n < D / 32; ++n) {
+          const uint4 w = src[n];
+          const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const float2 f = pair_f32<T>(e[y]);
+            x[n * 8 + 2 * y] = f.x;
+            x[n * 8 + 2 * y + 1] = f.y;
+            amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+          }
+        }
+      } else {
+#pragma unroll
+        for (int n = 0; n < D / 4; ++n) x[n] = 0.f;
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 2));
+      // 2^e brings the row's largest element to 1 .. 2 (an exact scaling)
+      const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -126), 126);
+      const float mul = pow2(-e), back = p.scale_log2 * pow2(e);
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+        qf[nt][n] = pack_f16x2(x[2 * n] * mul, x[2 * n + 1] * mul);
+      // this lane's columns of S^T and O^T are rows 2c, 2c + 1
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        qs[nt][y] = __shfl_sync(~0u, back, (2 * c + y) * 4);
+        const int qi = (nt * 8 + 2 * c + y) / p.group;
+        lim[nt][y] = p.causal && qi < sq.nq ? sq.nk - sq.nq + qi + 1 : sq.nk;
+      }
+    }
+    // keys below this are seen by every row
+    const int all_see = p.causal ? sq.nk - sq.nq + 1 : sq.nk;
+
+    float o[NT][KS][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int y = 0; y < 2; ++y) m[nt][y] = -INFINITY, l[nt][y] = 0.f;
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) o[nt][s][y] = 0.f;
+    }
+
+    // tokens [t_lo, t_hi) units, every kWarps-th tile of 16
+    const int end = min(t_hi * kUnit, sq.nk);
+    const int *ids = p.table + static_cast<long long>(b) * p.width;
+    const uint8_t *kc = p.c.k_codes + r * (D / 2) + c * (D / 8);
+    const uint8_t *ks = p.c.k_scales + r * (D / 16) + (D == 128 ? 2 * c : c);
+    const uint8_t *vc = p.c.v_codes + 2 * c * (D / 2) + r * (D / 16);
+    const uint8_t *vs = p.c.v_scales + 2 * c * (D / 16) + (D == 128 ? r : r / 2);
+    auto page = [&](int t) { return t < end ? ids[t >> p.c.bs_log2] : -1; };
+    auto load = [&](Tile<D> &x, int t, int id) {
+      if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.c.num_blocks)) return;
+      const long long row =
+          ((static_cast<long long>(id) * p.c.Hk + h) << p.c.bs_log2) + (t & (bs - 1));
+      const uint8_t *a = kc + row * (D / 2), *w = vc + row * (D / 2);
+      load_words(x.k[0], a);
+      load_words(x.k[1], a + 8 * (D / 2));
+      load_words(x.v[0], w);
+      load_words(x.v[1], w + D / 2);
+      load_words(x.v[2], w + 8 * (D / 2));
+      load_words(x.v[3], w + 9 * (D / 2));
+      const uint8_t *f = ks + row * (D / 16), *y = vs + row * (D / 16);
+      if constexpr (D == 128) {
+        x.ks[0] = __ldg(reinterpret_cast<const uint16_t *>(f));
+        x.ks[1] = __ldg(reinterpret_cast<const uint16_t *>(f + 8 * (D / 16)));
+      } else {
+        x.ks[0] = __ldg(f);
+        x.ks[1] = __ldg(f + 8 * (D / 16));
+      }
+      x.vs[0] = __ldg(y);
+      x.vs[1] = __ldg(y + D / 16);
+      x.vs[2] = __ldg(y + 8 * (D / 16));
+      x.vs[3] = __ldg(y + 9 * (D / 16));
+    };
+    auto compute = [&](const Tile<D> &x, int t, int id) {
+      if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.c.num_blocks)) return;
+      float s[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) s[nt][y] = 0.f;
+      // scales of tokens r and r + 8, as pairs of one number
+      const uint32_t f0 = e4m3x2_f16x2(x.ks[0]), f1 = e4m3x2_f16x2(x.ks[1]);
+      const uint32_t a_lo = __byte_perm(f0, 0, 0x1010), a_hi = __byte_perm(f0, 0, 0x3232);
+      const uint32_t b_lo = __byte_perm(f1, 0, 0x1010), b_hi = __byte_perm(f1, 0, 0x3232);
+#pragma unroll
+      for (int st = 0; st < KS; ++st) {
+        const bool hi = D == 128 && st >= KS / 2;
+        const uint32_t w0 = x.k[0][st / 2], w1 = x.k[1][st / 2];
+        const uint32_t fa = hi ? a_hi : a_lo, fb = hi ? b_hi : b_lo;
+        uint32_t a[4];
+        if (st & 1) {
+          a[0] = e2m1x2_f16x2<2>(w0), a[1] = e2m1x2_f16x2<2>(w1);
+          a[2] = e2m1x2_f16x2<3>(w0), a[3] = e2m1x2_f16x2<3>(w1);
+        } else {
+          a[0] = e2m1x2_f16x2<0>(w0), a[1] = e2m1x2_f16x2<0>(w1);
+          a[2] = e2m1x2_f16x2<1>(w0), a[3] = e2m1x2_f16x2<1>(w1);
+        }
+        a[0] = hmul2(a[0], fa), a[1] = hmul2(a[1], fb);
+        a[2] = hmul2(a[2], fa), a[3] = hmul2(a[3], fb);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma_f16(s[nt], a[0], a[1], a[2], a[3], qf[nt][2 * st], qf[nt][2 * st + 1]);
+      }
+      uint32_t pf[NT][2];
+      bool grow = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int y = 0; y < 4; ++y) s[nt][y] *= qs[nt][y & 1];
+        if (t + 16 > all_see) {
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            if (t + r + (y >> 1) * 8 >= lim[nt][y & 1]) s[nt][y] = -INFINITY;
+        }
+        // the exponent's offset follows the maximum only when that has grown
+        // by more than 8 (a factor of 256, which fp16 holds)
+        grow |= fmaxf(s[nt][0], s[nt][2]) > m[nt][0] + 8.f;
+        grow |= fmaxf(s[nt][1], s[nt][3]) > m[nt][1] + 8.f;
+      }
+      if (__any_sync(~0u, grow)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float f[2];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            float v = fmaxf(s[nt][y], s[nt][y + 2]);
+            v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
+            v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
+            v = fmaxf(v, __shfl_xor_sync(~0u, v, 16));
+            v = fmaxf(v, m[nt][y]);
+            f[y] = v == -INFINITY ? 1.f : ex2_approx(m[nt][y] - v);
+            m[nt][y] = v;
+            l[nt][y] *= f[y];
+          }
+#pragma unroll
+          for (int st = 0; st < KS; ++st)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) o[nt][st][y] *= f[y & 1];
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float e[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const float off = m[nt][y & 1] == -INFINITY ? 0.f : m[nt][y & 1];
+          e[y] = ex2_approx(s[nt][y] - off);
+        }
+        l[nt][0] += e[0] + e[2];
+        l[nt][1] += e[1] + e[3];
+        pf[nt][0] = movmatrix(pack_f16x2(e[0], e[1]));
+        pf[nt][1] = movmatrix(pack_f16x2(e[2], e[3]));
+      }
+      // scales of tokens (2c, 2c + 1) and (2c + 8, 2c + 9); a token behind the
+      // sequence has P = 0, and its scale, which may be anything, becomes 0
+      uint32_t v0 = x.vs[0] | x.vs[1] << 8, v1 = x.vs[2] | x.vs[3] << 8;
+      if (t + 16 > sq.nk) {
+        const int left = sq.nk - t - 2 * c;
+        v0 &= left > 1 ? 0xFFFFu : left == 1 ? 0xFFu : 0u;
+        v1 &= left > 9 ? 0xFFFFu : left == 9 ? 0xFFu : 0u;
+      }
+      const uint32_t g0 = e4m3x2_f16x2(v0), g1 = e4m3x2_f16x2(v1);
+#pragma unroll
+      for (int w = 0; w < D / 64; ++w) {
+        // byte n: column 2n (even) or 2n + 1 (odd) of the word's 8, of both tokens
+        constexpr uint32_t M = 0x0F0F0F0Fu;
+        const uint32_t ev0 = (x.v[0][w] & M) | ((x.v[1][w] << 4) & ~M);
+        const uint32_t od0 = ((x.v[0][w] >> 4) & M) | (x.v[1][w] & ~M);
+        const uint32_t ev1 = (x.v[2][w] & M) | ((x.v[3][w] << 4) & ~M);
+        const uint32_t od1 = ((x.v[2][w] >> 4) & M) | (x.v[3][w] & ~M);
+        auto step = [&](auto n) {
+          constexpr int N = decltype(n)::value;
+          const uint32_t a0 = hmul2(e2m1x2_f16x2<N>(ev0), g0), a1 = hmul2(e2m1x2_f16x2<N>(od0), g0);
+          const uint32_t a2 = hmul2(e2m1x2_f16x2<N>(ev1), g1), a3 = hmul2(e2m1x2_f16x2<N>(od1), g1);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma_f16(o[nt][w * 4 + N], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+        };
+        step(std::integral_constant<int, 0>{});
+        step(std::integral_constant<int, 1>{});
+        step(std::integral_constant<int, 2>{});
+        step(std::integral_constant<int, 3>{});
+      }
+    };
+
+    {
+      int t = (t_lo * kWarps + warp) * 16;
+      Tile<D> x0, x1;
+      int id0 = page(t), id1 = page(t + kUnit);
+      load(x0, t, id0);
+      while (t < end) {
+        load(x1, t + kUnit, id1);
+        const int id2 = page(t + 2 * kUnit);
+        compute(x0, t, id0);
+        t += kUnit;
+        if (t >= end) break;
+        load(x0, t + kUnit, id2);
+        const int id3 = page(t + 2 * kUnit);
+        compute(x1, t, id1);
+        t += kUnit;
+        id0 = id2;
+        id1 = id3;
+      }
+    }
+
+    // the warps' parts meet in shared memory
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        float v = l[nt][y];
+        v += __shfl_xor_sync(~0u, v, 4);
+        v += __shfl_xor_sync(~0u, v, 8);
+        v += __shfl_xor_sync(~0u, v, 16);
+        const int row = nt * 8 + 2 * c + y;
+        float *dst = s_o + (warp * R + row) * LD + r * (D / 8);
+#pragma unroll
+        for (int st = 0; st < KS; st += 2)
+          *reinterpret_cast<float4 *>(dst + 2 * st) =
+              make_float4(o[nt][st][y], o[nt][st][y + 2], o[nt][st + 1][y], o[nt][st + 1][y + 2]);
+        if (r == 0) {
+          s_m[warp * R + row] = m[nt][y];
+          s_l[warp * R + row] = v;
+        }
+      }
+    __syncthreads();
+    const bool whole = t_lo == 0 && t_hi == n_units;
+    const int slot = 2 * blockIdx.x + (t_lo == 0 ? 1 : 0);
+    for (int x = tid; x < R * (D / 4); x += kThreads) {
+      const int row = x / (D / 4), col = (x - row * (D / 4)) * 4;
+      if (row >= rows) break;
+      float mm = -INFINITY, ll = 0.f, f[kWarps];
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_m[w * R + row]);
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        f[w] = mm == -INFINITY ? 0.f : ex2_approx(s_m[w * R + row] - mm);
+        ll += f[w] * s_l[w * R + row];
+        const float4 v = *reinterpret_cast<const float4 *>(s_o + (w * R + row) * LD + col);
+        sum.x += f[w] * v.x, sum.y += f[w] * v.y, sum.z += f[w] * v.z, sum.w += f[w] * v.w;
+      }
+      if (whole) {
+        const int i = row / p.group, j = row - i * p.group;
+        const long long out = static_cast<long long>(sq.r0 + i) * p.Hq + h * p.group + j;
+        const float inv = ll > 0.f ? p.v_mul / ll : 0.f;
+        alignas(8) T e[4] = {static_cast<T>(sum.x * inv), static_cast<T>(sum.y * inv),
+                             static_cast<T>(sum.z * inv), static_cast<T>(sum.w * inv)};
+        *reinterpret_cast<uint2 *>(static_cast<T *>(p.o) + out * D + col) =
+            *reinterpret_cast<const uint2 *>(e);
+        if (col == 0)
+          p.lse[static_cast<long long>(h * p.group + j) * p.total_q + sq.r0 + i] =
+              ll > 0.f ? mm * 0.6931471805599453f + logf(ll) : -INFINITY;
+      } else {
+        float *dst = ws + static_cast<long long>(slot) * R * (D + 2);
+        *reinterpret_cast<float4 *>(dst + row * D + col) = sum;
+        if (col == 0) {
+          dst[R * D + 2 * row] = mm;
+          dst[R * D + 2 * row + 1] = ll;
+        }
+      }
+    }
+    __syncthreads();
+    u += t_hi - t_lo;
+    unit = 0;
+    if (++h == p.c.Hk) n_units = 0;
+  }
+}
+
+// Joins the parts of the sequences that more than one CTA shared: CTA n of
+// this grid looks at the border between CTAs n and n + 1 of the grid above
+// and, where a sequence and key head first crosses one there, sums its parts
+// (n's last, then the first ones of n + 1, n + 2, ...).  One warp a row.
+template <typename T, int D, int R>
+__global__ void __launch_bounds__(kThreads)
+    fa_kv4_join_kernel(const Kv4Attn p, const float *ws, int ctas) {
+  __shared__ long long s_sums[kThreads], s_warp[2][kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = blockIdx.x;
+  griddep_wait();
+  griddep_launch_dependents();
+  int den = ctas;
+  long long u = 0;
+  const Place at = find_unit(p, R, first + 1, &den, &u, s_sums, s_warp);
+  if (first + 1 >= den) return;
+  const Seq sq = load_seq(p, at.b);
+  const int n_units = units_of(sq, p.group, R);
+  const int h = static_cast<int>((u - at.before) / n_units);
+  const long long begin = at.before + static_cast<long long>(h) * n_units;
+  if (begin == u || at.total * first / den > begin) return;  // no crossing, or not the first
+  const long long stop = begin + n_units;
+  int last = first + 1;
+  while (last + 1 < den && at.total * (last + 1) / den < stop) ++last;
+  auto part = [&](int n) {  // n = first, first + 1, ... last
+    return ws + static_cast<long long>(2 * n + (n == first ? 1 : 0)) * R * (D + 2);
+  };
+  for (int row = warp; row < sq.nq * p.group; row += kWarps) {
+    float mm = -INFINITY;
+    for (int n = first + lane; n <= last; n += 32) mm = fmaxf(mm, part(n)[R * D + 2 * row]);
+    for (int o = 16; o; o /= 2) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, o));
+    constexpr int W = D / 32;
+    float ll = 0.f, sum[W] = {};
+#pragma unroll 4
+    for (int n = first; n <= last; ++n) {
+      const float *src = part(n);
+      const float f = mm == -INFINITY ? 0.f : ex2_approx(src[R * D + 2 * row] - mm);
+      ll += f * src[R * D + 2 * row + 1];
+      float v[W];
+      if constexpr (W == 4)
+        *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(src + row * D + lane * 4);
+      else
+        *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(src + row * D + lane * 2);
+#pragma unroll
+      for (int y = 0; y < W; ++y) sum[y] += f * v[y];
+    }
+    const int i = row / p.group, j = row - i * p.group;
+    T *out = static_cast<T *>(p.o) +
+             (static_cast<long long>(sq.r0 + i) * p.Hq + h * p.group + j) * D + lane * W;
+    const float inv = ll > 0.f ? p.v_mul / ll : 0.f;
+#pragma unroll
+    for (int y = 0; y < W; ++y) out[y] = static_cast<T>(sum[y] * inv);
+    if (lane == 0)
+      p.lse[static_cast<long long>(h * p.group + j) * p.total_q + sq.r0 + i] =
+          ll > 0.f ? mm * 0.6931471805599453f + logf(ll) : -INFINITY;
+  }
+}
+
+template <typename T, int D, int NT>
+cudaError_t launch(const Kv4Attn &p, float *ws, int num_sms, cudaStream_t s) {
+  static std::atomic<unsigned long long> attr_done{0};
+  constexpr int smem = smem_bytes<NT, D>();
+  cudaError_t e = smem_attr_once(fa_kv4_attn_kernel<T, D, NT>, smem, &attr_done);
+  if (e != cudaSuccess) return e;
+  // one resident wave, no more CTAs than there can be units
+  long long ctas = static_cast<long long>(num_sms > 0 ? num_sms : 1) * (NT == 1 ? 2 : 1);
+  const long long most = static_cast<long long>(p.B) * p.c.Hk *
+                         (p.max_k < kUnit ? 1 : (p.max_k + kUnit - 1) / kUnit);
+  if (ctas > most) ctas = most;
+  if (ctas > kKv4MaxCtas) ctas = kKv4MaxCtas;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((p.max_q + kWarps - 1) / kWarps, p.Hq, p.B);
-  cfg.blockDim = dim3(32 * kWarps);
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fa_kv4_attn_kernel<T, D>, p);
+  e = cudaLaunchKernelEx(&cfg, fa_kv4_attn_kernel<T, D, NT>, p, ws);
+  if (e != cudaSuccess || ctas == 1) return e;
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas - 1));
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, fa_kv4_join_kernel<T, D, NT * 8>, p,
+                            static_cast<const float *>(ws), static_cast<int>(ctas));
+}
+
+template <typename T, int D>
+cudaError_t launch_rows(const Kv4Attn &p, int rows, float *ws, int num_sms, cudaStream_t s) {
+  if (rows == 8) return launch<T, D, 1>(p, ws, num_sms, s);
+  if (rows == 16) return launch<T, D, 2>(p, ws, num_sms, s);
+  return launch<T, D, 4>(p, ws, num_sms, s);
 }
 
 }  // namespace
 
-cudaError_t launch_kv4_attn(const Kv4Attn &p, int dtype, cudaStream_t s) {
+int kv4_tile_rows(int group, int max_q) {
+  auto fit = [](long long n) { return n <= 8 ? 8 : n <= 16 ? 16 : n <= 32 ? 32 : 0; };
+  const int all = fit(static_cast<long long>(group) * max_q);
+  return all ? all : fit(group);
+}
+
+size_t kv4_workspace(int rows, int d) {
+  return static_cast<size_t>(2 * kKv4MaxCtas) * rows * (d + 2) * sizeof(float);
+}
+
+cudaError_t launch_kv4_attn(const Kv4Attn &p, int rows, int dtype, float *ws, int num_sms,
+                            cudaStream_t s) {
   if (dtype == FA_DTYPE_BF16)
-    return p.c.d == 64 ? launch<__nv_bfloat16, 64>(p, s) : launch<__nv_bfloat16, 128>(p, s);
-  return p.c.d == 64 ? launch<__half, 64>(p, s) : launch<__half, 128>(p, s);
+    return p.c.d == 64 ? launch_rows<__nv_bfloat16, 64>(p, rows, ws, num_sms, s)
+                       : launch_rows<__nv_bfloat16, 128>(p, rows, ws, num_sms, s);
+  return p.c.d == 64 ? launch_rows<__half, 64>(p, rows, ws, num_sms, s)
+                     : launch_rows<__half, 128>(p, rows, ws, num_sms, s);
 }
 
 }  // namespace fa

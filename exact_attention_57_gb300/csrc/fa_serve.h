@@ -3,6 +3,7 @@
 // host API (fa_serve_api.cu) and their translation units.
 #pragma once
 
+#include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -78,6 +79,15 @@ struct Kv4Attn {
   float v_mul;                    // 2^v_exp
   int causal;
 };
-cudaError_t launch_kv4_attn(const Kv4Attn &p, int dtype, cudaStream_t s);
+// Sequences with at most `rows` rows (queries x group) go through
+// launch_kv4_attn's tile of that many rows, longer ones through
+// launch_kv4_many.  kv4_tile_rows: 8, 16 or 32, the smallest that holds the
+// longest sequence, else the smallest that holds one query; 0: none does.
+constexpr int kKv4MaxCtas = 304;  // two on each of 152 SMs
+int kv4_tile_rows(int group, int max_q);
+size_t kv4_workspace(int rows, int d);
+cudaError_t launch_kv4_attn(const Kv4Attn &p, int rows, int dtype, float *ws, int num_sms,
+                            cudaStream_t s);
+cudaError_t launch_kv4_many(const Kv4Attn &p, int tile_rows, int dtype, cudaStream_t s);
 
 }  // namespace fa

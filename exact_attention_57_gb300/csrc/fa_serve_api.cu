@@ -276,7 +276,8 @@ extern "C" int fa_kv4_gather(const long long *slots, int R, const void *k_codes,
 
 extern "C" unsigned long long fa_fwd_kv4_workspace(int B, int Hq, int Hk, int max_seqlen_q, int d) {
   if (B < 1 || Hq < 1 || Hk < 1 || Hq % Hk != 0 || max_seqlen_q < 1 || d < 1) return 0;
-  return 0;
+  const int tile = fa::kv4_tile_rows(Hq / Hk, max_seqlen_q);
+  return tile ? fa::kv4_workspace(tile, d) : 0;
 }
 
 extern "C" int fa_fwd_kv4(const void *q, void *o, float *lse, const void *k_codes,
@@ -339,5 +340,12 @@ extern "C" int fa_fwd_kv4(const void *q, void *o, float *lse, const void *k_code
   p.scale_log2 = scale_log2;
   p.v_mul = static_cast<float>(std::ldexp(1.0, v_exp));
   p.causal = causal;
-  return done(fa::launch_kv4_attn(p, dtype, static_cast<cudaStream_t>(stream)));
+  const int tile = fa::kv4_tile_rows(p.group, max_seqlen_q);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (tile > 0)
+    e = fa::launch_kv4_attn(p, tile, dtype, static_cast<float *>(workspace), fa::api_sm_count(), s);
+  if (e == cudaSuccess && static_cast<long long>(max_seqlen_q) * p.group > tile)
+    e = fa::launch_kv4_many(p, tile, dtype, s);
+  return done(e);
 }
