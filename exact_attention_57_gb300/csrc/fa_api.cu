@@ -1227,5 +1227,6 @@ unsigned long long api_wait_limit() {
   const unsigned long long lim = g_wait_limit_ns.load();
   return lim ? lim : kDefaultWaitLimitNs;
 }
+int api_skip_load() { return g_skip_v_load.load(); }
 
 }  // namespace fa

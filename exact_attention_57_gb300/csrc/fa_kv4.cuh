@@ -53,6 +53,13 @@ __device__ __forceinline__ uint32_t f32x2_e2m1x2(float lo, float hi) {
   return r;
 }
 
+// Product of two fp16 pairs.
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t y;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  return y;
+}
+
 // 2^e for e in [-126, 127].
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((127 + e) << 23); }
 

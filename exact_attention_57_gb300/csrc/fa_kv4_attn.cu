@@ -38,9 +38,7 @@
 
 #include "fa.h"
 #include "fa_internal.h"
-#include "fa_kv4.cuh"
-#include "fa_serve.h"
-#include "ptx.cuh"
+#include "fa_kv4_split.cuh"
 
 namespace fa {
 namespace {
@@ -64,12 +62,6 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   return y;
 }
 
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t y;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
-  return y;
-}
-
 template <int W>
 __device__ __forceinline__ void load_words(uint32_t (&x)[W], const uint8_t *p) {
   if constexpr (W == 4)
@@ -82,88 +74,12 @@ __device__ __forceinline__ void load_words(uint32_t (&x)[W], const uint8_t *p) {
     asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(x[0]) : "l"(p));
 }
 
-// One sequence as this kernel sees it.
-struct Seq {
-  int r0, nq, nk;
-};
-
-__device__ __forceinline__ Seq load_seq(const Kv4Attn &p, int b) {
-  Seq s = {b, 1, 0};
-  if (p.cu_q) {
-    s.r0 = min(max(p.cu_q[b], 0), p.total_q);
-    s.nq = min(max(min(max(p.cu_q[b + 1], 0), p.total_q) - s.r0, 0), p.max_q);
-  }
-  s.nk = static_cast<int>(min(static_cast<long long>(min(max(p.lens[b], 0), p.max_k)),
-                              static_cast<long long>(p.width) << p.c.bs_log2));
-  return s;
-}
-
 // Units of one key head of a sequence; a sequence without keys still has one
 // (its rows get their zeros), one with more than `rows` rows none (the
 // kernel for many queries takes it).
 __device__ __forceinline__ int units_of(const Seq &s, int group, int rows) {
   if (s.nq == 0 || static_cast<long long>(s.nq) * group > rows) return 0;
   return max(1, (s.nk + kUnit - 1) / kUnit);
-}
-
-// Where a unit lies in the line of all units.
-struct Place {
-  long long total;   // units in all
-  long long before;  // units before sequence b
-  int b;
-};
-
-// The place of unit floor(total * num / den) (all threads get it).  `sums`
-// holds kThreads + 1 prefix sums.
-__device__ Place find_unit(const Kv4Attn &p, int rows, int num, int *den, long long *target,
-                           long long *sums, long long (*warp_sums)[kWarps]) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  Place at = {0, 0, 0};
-  // total first, where one round of requests does not show it
-  if (p.B > kThreads) {
-    long long n = 0;
-    for (int b = tid; b < p.B; b += kThreads) n += units_of(load_seq(p, b), p.group, rows);
-    for (int o = 16; o; o /= 2) n += __shfl_xor_sync(~0u, n, o);
-    if (lane == 0) warp_sums[1][warp] = n;
-    __syncthreads();
-    for (int w = 0; w < kWarps; ++w) at.total += warp_sums[1][w];
-    at.total *= p.c.Hk;
-  }
-  for (int base = 0;; base += kThreads) {
-    const int b = base + tid;
-    long long n = b < p.B ? units_of(load_seq(p, b), p.group, rows) : 0;
-    n *= p.c.Hk;
-    long long incl = n;
-    for (int o = 1; o < 32; o *= 2) {
-      const long long x = __shfl_up_sync(~0u, incl, o);
-      if (lane >= o) incl += x;
-    }
-    if (lane == 31) warp_sums[0][warp] = incl;
-    __syncthreads();
-    long long pre = at.before, all = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) pre += warp_sums[0][w];
-      all += warp_sums[0][w];
-    }
-    sums[tid] = pre + incl - n;
-    __syncthreads();
-    if (p.B <= kThreads) at.total = all;
-    if (base == 0) {
-      *den = static_cast<int>(min(static_cast<long long>(*den), at.total));
-      if (num >= *den) return at;  // more CTAs than units
-      *target = at.total * num / *den;
-    }
-    if (*target < at.before + all || base + kThreads >= p.B) {
-      int i = 0;
-      for (int step = kThreads / 2; step > 0; step /= 2)
-        if (sums[i + step] <= *target) i += step;
-      at.b = base + i;
-      at.before = sums[i];
-      return at;
-    }
-    at.before += all;
-    __syncthreads();
-  }
 }
 
 // 16 tokens of one page as lane (r, c) holds them.
@@ -203,8 +119,17 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
   griddep_launch_dependents();
   int den = gridDim.x;
   long long u = 0;
-  const Place at = find_unit(p, R, blockIdx.x, &den, &u, s_sums, s_warp);
-  if (static_cast<int>(blockIdx.x) >= den) return;
+  const Place at = find_unit<kWarps>(
+      p,
+      [&](int b) {
+        return static_cast<long long>(units_of(load_seq(p, b), p.group, R)) * p.c.Hk;
+      },
+      blockIdx.x, &den, &u, s_sums, s_warp);
+  Share share = {-1, 0, 0, 1};
+  if (static_cast<int>(blockIdx.x) >= den) {
+    if (tid == 0) reinterpret_cast<Share *>(ws)[blockIdx.x] = share;
+    return;
+  }
   const long long u1 = at.total * (blockIdx.x + 1) / den;
   const int bs = 1 << p.c.bs_log2;
 
@@ -467,8 +392,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
         }
       }
     __syncthreads();
-    const bool whole = t_lo == 0 && t_hi == n_units;
-    const int slot = 2 * blockIdx.x + (t_lo == 0 ? 1 : 0);
+    const bool begins = t_lo == 0, ends = t_hi == n_units, whole = begins && ends;
+    if (begins && !ends) share.b = b, share.h = h;
+    if (!begins) share.head_ends = ends;
     for (int x = tid; x < R * (D / 4); x += kThreads) {
       const int row = x / (D / 4), col = (x - row * (D / 4)) * 4;
       if (row >= rows) break;
@@ -495,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
           p.lse[static_cast<long long>(h * p.group + j) * p.total_q + sq.r0 + i] =
               ll > 0.f ? mm * 0.6931471805599453f + logf(ll) : -INFINITY;
       } else {
-        float *dst = ws + static_cast<long long>(slot) * R * (D + 2);
+        float *dst = part_of<D, R>(ws, blockIdx.x, begins);
         *reinterpret_cast<float4 *>(dst + row * D + col) = sum;
         if (col == 0) {
           dst[R * D + 2 * row] = mm;
@@ -508,63 +434,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
     unit = 0;
     if (++h == p.c.Hk) n_units = 0;
   }
-}
-
-// Joins the parts of the sequences that more than one CTA shared: CTA n of
-// this grid looks at the border between CTAs n and n + 1 of the grid above
-// and, where a sequence and key head first crosses one there, sums its parts
-// (n's last, then the first ones of n + 1, n + 2, ...).  One warp a row.
-template <typename T, int D, int R>
-__global__ void __launch_bounds__(kThreads)
-    fa_kv4_join_kernel(const Kv4Attn p, const float *ws, int ctas) {
-  __shared__ long long s_sums[kThreads], s_warp[2][kWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = blockIdx.x;
-  griddep_wait();
-  griddep_launch_dependents();
-  int den = ctas;
-  long long u = 0;
-  const Place at = find_unit(p, R, first + 1, &den, &u, s_sums, s_warp);
-  if (first + 1 >= den) return;
-  const Seq sq = load_seq(p, at.b);
-  const int n_units = units_of(sq, p.group, R);
-  const int h = static_cast<int>((u - at.before) / n_units);
-  const long long begin = at.before + static_cast<long long>(h) * n_units;
-  if (begin == u || at.total * first / den > begin) return;  // no crossing, or not the first
-  const long long stop = begin + n_units;
-  int last = first + 1;
-  while (last + 1 < den && at.total * (last + 1) / den < stop) ++last;
-  auto part = [&](int n) {  // n = first, first + 1, ... last
-    return ws + static_cast<long long>(2 * n + (n == first ? 1 : 0)) * R * (D + 2);
-  };
-  for (int row = warp; row < sq.nq * p.group; row += kWarps) {
-    float mm = -INFINITY;
-    for (int n = first + lane; n <= last; n += 32) mm = fmaxf(mm, part(n)[R * D + 2 * row]);
-    for (int o = 16; o; o /= 2) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, o));
-    constexpr int W = D / 32;
-    float ll = 0.f, sum[W] = {};
-#pragma unroll 4
-    for (int n = first; n <= last; ++n) {
-      const float *src = part(n);
-      const float f = mm == -INFINITY ? 0.f : ex2_approx(src[R * D + 2 * row] - mm);
-      ll += f * src[R * D + 2 * row + 1];
-      float v[W];
-      if constexpr (W == 4)
-        *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(src + row * D + lane * 4);
-      else
-        *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(src + row * D + lane * 2);
-#pragma unroll
-      for (int y = 0; y < W; ++y) sum[y] += f * v[y];
-    }
-    const int i = row / p.group, j = row - i * p.group;
-    T *out = static_cast<T *>(p.o) +
-             (static_cast<long long>(sq.r0 + i) * p.Hq + h * p.group + j) * D + lane * W;
-    const float inv = ll > 0.f ? p.v_mul / ll : 0.f;
-#pragma unroll
-    for (int y = 0; y < W; ++y) out[y] = static_cast<T>(sum[y] * inv);
-    if (lane == 0)
-      p.lse[static_cast<long long>(h * p.group + j) * p.total_q + sq.r0 + i] =
-          ll > 0.f ? mm * 0.6931471805599453f + logf(ll) : -INFINITY;
-  }
+  if (tid == 0) reinterpret_cast<Share *>(ws)[blockIdx.x] = share;
 }
 
 template <typename T, int D, int NT>
@@ -591,10 +461,12 @@ cudaError_t launch(const Kv4Attn &p, float *ws, int num_sms, cudaStream_t s) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, fa_kv4_attn_kernel<T, D, NT>, p, ws);
   if (e != cudaSuccess || ctas == 1) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas - 1));
+  const long long rows = static_cast<long long>(p.max_q) * p.group;
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas - 1),
+                     static_cast<unsigned>((min(rows, NT * 8LL) + kJoinRows - 1) / kJoinRows));
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, fa_kv4_join_kernel<T, D, NT * 8>, p,
-                            static_cast<const float *>(ws), static_cast<int>(ctas));
+  return cudaLaunchKernelEx(&cfg, fa_kv4_join_kernel<T, D, NT * 8>, p, ws,
+                            static_cast<int>(ctas), p.max_q);
 }
 
 template <typename T, int D>
@@ -613,7 +485,9 @@ int kv4_tile_rows(int group, int max_q) {
 }
 
 size_t kv4_workspace(int rows, int d) {
-  return static_cast<size_t>(2 * kKv4MaxCtas) * rows * (d + 2) * sizeof(float);
+  const int ctas = rows == kKv4ManyRows ? kKv4ManyCtas : kKv4MaxCtas;
+  return kKv4MaxCtas * sizeof(Share) +
+         static_cast<size_t>(2 * ctas) * rows * (d + 2) * sizeof(float);
 }
 
 cudaError_t launch_kv4_attn(const Kv4Attn &p, int rows, int dtype, float *ws, int num_sms,

@@ -1,123 +1,712 @@
 // fa_kv4_many.cu — attention of sequences with many queries over the paged
-// 4-bit cache (those that fa_kv4_attn.cu leaves out).
+// 4-bit cache (chunks of prompts; the sequences that fa_kv4_attn.cu's tiles do
+// not hold), on tcgen05.
 //
-// Query token i of sequence b (n_q queries, n_k cached tokens, its own among
-// them) sees key j iff j < n_k and, when causal, j <= n_k - n_q + i; query
-// head h reads key head h / group.  One warp per query row: each lane scores
-// one of 32 keys from its dequantised row, the warp keeps the running maximum
-// and sum, then every lane adds p_j * v_j for its d / 32 columns.
+// A tile is 128 rows of one sequence and key head: row r is head r % group of
+// query token t * tokens + r / group, tokens = 128 / group, so the heads that
+// share a key head share its expanded keys and values.  Work is dealt as in
+// fa_kv4_split.cuh, a unit being 128 keys of one tile: one CTA on each SM,
+// equal shares, whatever the lengths, the mask and the number of tiles.
+//
+// Warps 0-3    softmax, correction and epilogue, one row a thread; they also
+//              bring the row's Q into shared memory, as fp16 times a power of
+//              two, before the previous tile's epilogue.
+// Warps 4-7    expand the codes: thread r loads token r of the 128 (a page
+//              lookup, D / 2 bytes of codes, D / 16 of scales, one tile
+//              ahead), turns them into fp16 (exact: six significant bits) and
+//              writes them as a 128-byte-swizzled row, K two tiles ahead of V.
+//              Tokens behind the sequence or on a missing page become zeros
+//              and are reported in a bit mask.
+// Warp 8, 9    issue S = Q K^T (three score buffers) and O += P V (P in tensor
+//              memory), kind::f16, fp32 accumulators; warp 8 owns the tensor
+//              memory.
+//
+// The products of a 128 x 128 step need about 1000 cycles of the tensor pipe
+// and the softmax 850 of its warps; expanding the step's K and V costs 512
+// conversions, 512 multiplications and 128 16-byte stores a warp, which four
+// warps of their own hide beside them.
+//
+// Every wait is bounded; on expiry the CTA raises its abort flag, records the
+// role in the status word, drains its products, frees tensor memory and ends.
+#include <atomic>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "fa.h"
-#include "fa_kv4.cuh"
-#include "fa_serve.h"
-#include "ptx.cuh"
+#include "fa_internal.h"
+#include "fa_kv4_split.cuh"
+#include "fa_wait.cuh"
 
 namespace fa {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kThreads = 384, kWarps = 12;
+constexpr int R = kKv4ManyRows;
+
+struct ManyCtl {
+  unsigned *status;
+  unsigned long long wait_limit_ns;
+  int skip_load, tile_rows, tokens;  // tokens of a tile
+};
+
+template <int D>
+struct ManyCfg {
+  static constexpr int NCH = D / 64;               // 128-byte chunks of a row
+  static constexpr int CHUNK = 128 * 128;
+  static constexpr int TILE = NCH * CHUNK;
+  static constexpr int NS = 3;                     // score buffers
+  static constexpr int ST = D == 128 ? 3 : 4;      // K and V stages
+  static constexpr int MASKS = 8;                  // tiles whose key masks are kept
+  static constexpr uint32_t COL_O = NS * 128;
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_K = OFF_Q + TILE;
+  static constexpr int OFF_V = OFF_K + ST * TILE;
+  static constexpr int OFF_MASK = OFF_V + ST * TILE;
+  static constexpr int OFF_BAR = OFF_MASK + MASKS * 16;
+  // qfull, qempty, ofree, fin[2], kfull, kempty, vfull, vempty [ST], sfull,
+  // pfull, odone [NS]
+  static constexpr int NBAR = 5 + 4 * ST + 3 * NS;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int OFF_SUMS = OFF_K;           // before the first tile arrives
+  static constexpr int SMEM = OFF_MISC + 16 + 1024;
+  static_assert(SMEM <= 227 * 1024, "shared memory budget");
+};
+constexpr uint32_t kRegSoftmax = 240, kRegExpand = 152, kRegIssue = 104;
+static_assert(128 * (kRegSoftmax + kRegExpand + kRegIssue) <= kThreads * 168,
+              "the register split must fit in what the block is launched with");
+
+// Sum over i in [0, n) of floor((a i + b) / m), for n, a, b >= 0, m > 0.
+__device__ long long floor_sum(long long n, long long m, long long a, long long b) {
+  long long s = 0;
+  for (;;) {
+    s += (n - 1) * n / 2 * (a / m) + n * (b / m);
+    a %= m;
+    b %= m;
+    const long long top = a * n + b;
+    if (top < m) return s;
+    n = top / m;
+    b = top % m;
+    const long long t = m;
+    m = a;
+    a = t;
+  }
+}
+
+__device__ __forceinline__ int ceil128(int x) { return (x + 127) >> 7; }
+
+// Tiles of one key head of a sequence (0: the other kernel's, or no queries).
+__device__ __forceinline__ int tiles_of(const Kv4Attn &p, const ManyCtl &c, const Seq &s) {
+  if (static_cast<long long>(s.nq) * p.group <= c.tile_rows) return 0;
+  return static_cast<int>((static_cast<long long>(s.nq) + c.tokens - 1) / c.tokens);
+}
+
+// Units of tile t of n.  A tile that sees no key has one, for its zeros.
+__device__ __forceinline__ int tile_units(const Kv4Attn &p, const ManyCtl &c, const Seq &s, int t,
+                                          int n) {
+  const long long seen = !p.causal || t == n - 1
+                             ? s.nk
+                             : static_cast<long long>(s.nk) - s.nq + (t + 1LL) * c.tokens;
+  return seen <= 0 ? 1 : ceil128(static_cast<int>(seen));
+}
+
+// Units of the first t of n tiles, in closed form (tile x sees nk - nq +
+// (x + 1) tokens keys when causal, the last one all).
+__device__ long long units_before(const Kv4Attn &p, const ManyCtl &c, const Seq &s, int t, int n) {
+  if (t == 0) return 0;
+  const long long full = s.nk > 0 ? ceil128(s.nk) : 1;
+  if (!p.causal) return t * full;
+  const int m = min(t, n - 1);  // without the last tile
+  const long long v0 = static_cast<long long>(s.nk) - s.nq;
+  const long long none = v0 < 0 ? min(static_cast<long long>(m), -v0 / c.tokens) : 0;
+  long long sum = none + (t == n ? full : 0);
+  if (m > none)
+    sum += floor_sum(m - none, 128, c.tokens, v0 + (none + 1) * c.tokens + 127);
+  return sum;
+}
+
+// A CTA's share as a list of parts of tiles; every role walks it by itself.
+struct Part {
+  int b, h, qt, lo, hi, units;  // steps [lo, hi) of `units`
+  Seq s;
+};
+struct Walk {
+  long long u, u1;
+  int b, h, qt, unit, n;  // n tiles of sequence b
+  Seq s;
+  __device__ __forceinline__ bool next(const Kv4Attn &p, const ManyCtl &c, Part &x) {
+    if (u >= u1) return false;
+    while (qt >= n) {
+      if (n > 0 && h + 1 < p.c.Hk) {
+        ++h;
+      } else {  // another sequence of this kernel follows, since u < the total
+        s = load_seq(p, ++b);
+        n = tiles_of(p, c, s);
+        h = 0;
+      }
+      qt = 0;
+    }
+    x.b = b, x.h = h, x.qt = qt, x.s = s;
+    x.units = tile_units(p, c, s, qt, n);
+    x.lo = unit;
+    x.hi = static_cast<int>(min(static_cast<long long>(x.units), unit + (u1 - u)));
+    u += x.hi - x.lo;
+    unit = 0;
+    ++qt;
+    return true;
+  }
+};
 
 template <typename T, int D>
-__global__ void __launch_bounds__(32 * kWarps)
-    fa_kv4_many_kernel(const Kv4Attn p, int tile_rows) {
+__global__ void __launch_bounds__(kThreads, 1)
+    fa_kv4_many_kernel(const Kv4Attn p, const ManyCtl ctl, float *ws) {
+  using C = ManyCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t sQ = sbase + C::OFF_Q, sK = sbase + C::OFF_K, sV = sbase + C::OFF_V;
+  const uint32_t bQfull = sbase + C::OFF_BAR, bQempty = bQfull + 8, bOfree = bQempty + 8;
+  const uint32_t bFin = bOfree + 8;                // + 8 * issuer
+  const uint32_t bKfull = bFin + 16, bKempty = bKfull + 8 * C::ST;
+  const uint32_t bVfull = bKempty + 8 * C::ST, bVempty = bVfull + 8 * C::ST;
+  const uint32_t bSfull = bVempty + 8 * C::ST, bPfull = bSfull + 8 * C::NS;
+  const uint32_t bOdone = bPfull + 8 * C::NS;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
+  long long *s_sums = reinterpret_cast<long long *>(smem + C::OFF_SUMS);
+  auto s_warp = reinterpret_cast<long long (*)[kWarps]>(s_sums + kThreads);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    mbar_init(bQfull, 128);
+    mbar_init(bQempty, 1);
+    mbar_init(bOfree, 128);
+    mbar_init(bFin, 1);
+    mbar_init(bFin + 8, 1);
+#pragma unroll
+    for (int s = 0; s < C::ST; ++s) {
+      mbar_init(bKfull + 8 * s, 128);
+      mbar_init(bKempty + 8 * s, 1);
+      mbar_init(bVfull + 8 * s, 128);
+      mbar_init(bVempty + 8 * s, 1);
+    }
+#pragma unroll
+    for (int s = 0; s < C::NS; ++s) {
+      mbar_init(bSfull + 8 * s, 1);
+      mbar_init(bPfull + 8 * s, 128);
+      mbar_init(bOdone + 8 * s, 1);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
   griddep_wait();
   griddep_launch_dependents();
-  __shared__ float sq[kWarps][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int b = blockIdx.z, h = blockIdx.y;
-  int r0 = b, nq = 1;
-  if (p.cu_q) {
-    r0 = min(max(p.cu_q[b], 0), p.total_q);
-    nq = min(min(max(p.cu_q[b + 1], 0), p.total_q) - r0, p.max_q);
+  // this CTA's share of the line of units
+  int den = gridDim.x;
+  Walk walk = {};
+  const Place at = find_unit<kWarps>(
+      p,
+      [&](int b) {
+        const Seq s = load_seq(p, b);
+        const int n = tiles_of(p, ctl, s);
+        return units_before(p, ctl, s, n, n) * p.c.Hk;
+      },
+      blockIdx.x, &den, &walk.u, s_sums, s_warp);
+  if (static_cast<int>(blockIdx.x) >= den) {
+    if (threadIdx.x == 0) reinterpret_cast<Share *>(ws)[blockIdx.x] = Share{-1, 0, 0, 1};
+    return;
   }
-  const int i = blockIdx.x * kWarps + warp;
-  if (i >= nq || static_cast<long long>(nq) * p.group <= tile_rows) return;
-  const int bs = 1 << p.c.bs_log2;
-  const int nk = static_cast<int>(min(static_cast<long long>(min(max(p.lens[b], 0), p.max_k)),
-                                      static_cast<long long>(p.width) << p.c.bs_log2));
-  const int last = p.causal ? min(nk, nk - nq + i + 1) : nk;  // keys [0, last)
-  const long long row = static_cast<long long>(r0 + i) * p.Hq + h;
-  const T *q = static_cast<const T *>(p.q) + row * D;
-  for (int x = lane; x < D; x += 32) sq[warp][x] = static_cast<float>(q[x]) * p.scale_log2;
-  __syncwarp();
-  const int hk = h / p.group;
-  float m = -INFINITY, l = 0.f, acc[D / 32] = {};
-  for (int j0 = 0; j0 < last; j0 += 32) {
-    const int j = j0 + lane;
-    const int id = j < last ? p.table[static_cast<long long>(b) * p.width + (j >> p.c.bs_log2)] : -1;
-    const bool ok = static_cast<unsigned>(id) < static_cast<unsigned>(p.c.num_blocks);
-    const long long at =
-        ok ? ((static_cast<long long>(id) * p.c.Hk + hk) << p.c.bs_log2) + (j & (bs - 1)) : 0;
-    float sc = -INFINITY;
-    if (ok) {
-      sc = 0.f;
-      for (int g = 0; g < D / 16; ++g) {
-        const uint2 w = reinterpret_cast<const uint2 *>(p.c.k_codes)[at * (D / 16) + g];
-        const float s = f16x2_f32(e4m3x2_f16x2(p.c.k_scales[at * (D / 16) + g])).x;
-        const uint32_t pr[8] = {e2m1x2_f16x2<0>(w.x), e2m1x2_f16x2<1>(w.x), e2m1x2_f16x2<2>(w.x),
-                                e2m1x2_f16x2<3>(w.x), e2m1x2_f16x2<0>(w.y), e2m1x2_f16x2<1>(w.y),
-                                e2m1x2_f16x2<2>(w.y), e2m1x2_f16x2<3>(w.y)};
-        float dot = 0.f;
-        for (int n = 0; n < 8; ++n) {
-          const float2 f = f16x2_f32(pr[n]);
-          dot += f.x * sq[warp][g * 16 + 2 * n] + f.y * sq[warp][g * 16 + 2 * n + 1];
-        }
-        sc += dot * s;
-      }
+  walk.u1 = at.total * (blockIdx.x + 1) / den;
+  walk.b = at.b;
+  walk.s = load_seq(p, at.b);
+  walk.n = tiles_of(p, ctl, walk.s);
+  {
+    const long long per_head = units_before(p, ctl, walk.s, walk.n, walk.n);
+    const long long into = walk.u - at.before;
+    walk.h = static_cast<int>(into / per_head);
+    const long long rest = into - walk.h * per_head;
+    int lo = 0, hi = walk.n;  // the last tile that begins at or before `rest`
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (units_before(p, ctl, walk.s, mid, walk.n) <= rest) lo = mid;
+      else hi = mid;
     }
-    float mt = sc;
-    for (int o = 16; o; o /= 2) mt = fmaxf(mt, __shfl_xor_sync(~0u, mt, o));
-    if (mt == -INFINITY) continue;
-    const float mn = fmaxf(m, mt), f = exp2f(m - mn), pj = exp2f(sc - mn);
-    m = mn;
-    l = l * f + pj;
-    for (float &a : acc) a *= f;
-    for (int t = 0; t < 32; ++t) {
-      const float w = __shfl_sync(~0u, pj, t);
-      const long long vt = __shfl_sync(~0u, at, t);
-      if (w == 0.f) continue;
+    walk.qt = lo;
+    walk.unit = static_cast<int>(rest - units_before(p, ctl, walk.s, lo, walk.n));
+  }
+  if (warp == 8) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  WaitCtl w{abort_flag, ctl.status, ctl.wait_limit_ns, 0u};
+
+  if (warp >= 8) {
+    setmaxnreg_dec<kRegIssue>();
+    w.role = kStatusMma;
+    if (warp == 8 && lane == 0) {
+      // ---------------------------------------------- S = Q K^T
+      constexpr uint32_t kIdesc = make_idesc(0u, 128, 128, 0u, 0u);
+      bool ok = true;
+      int b = 0, bph = 0, s = 0, sph = 0, issued = 0;
+      Part x;
+      for (int g = 0; ok && walk.next(p, ctl, x); ++g) {
+        if (!(ok = bounded_wait(bQfull, g & 1, w))) break;
+        for (int j = x.lo; j < x.hi; ++j, ++issued) {
+          // score buffer b last held P of three steps ago
+          if (issued >= C::NS && !(ok = bounded_wait(bOdone + 8 * b, bph ^ 1, w))) break;
+          if (!(ok = bounded_wait(bKfull + 8 * s, sph, w))) break;
+          tc_fence_after();
 #pragma unroll
-      for (int n = 0; n < D / 32; ++n) {
-        const int x = lane + 32 * n;
-        const uint32_t byte = p.c.v_codes[vt * (D / 2) + x / 2];
-        const float2 f2 = f16x2_f32(e2m1x2_f16x2<0>(byte));
-        const float s = f16x2_f32(e4m3x2_f16x2(p.c.v_scales[vt * (D / 16) + x / 16])).x;
-        acc[n] += w * s * ((x & 1) ? f2.y : f2.x);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * C::CHUNK + (kk & 3) * 32;
+            umma_ss<false>(tmem + b * 128, sdesc_sw128(sQ + off, 16, 1024),
+                           sdesc_sw128(sK + s * C::TILE + off, 16, 1024), kIdesc, kk > 0 ? 1u : 0u);
+          }
+          tc_commit(bKempty + 8 * s);
+          tc_commit(bSfull + 8 * b);
+          if (++b == C::NS) b = 0, bph ^= 1;
+          if (++s == C::ST) s = 0, sph ^= 1;
+        }
+        if (ok) tc_commit(bQempty);
       }
+      tc_commit(bFin);
+      bounded_wait(bFin, 0, w, false);
+    } else if (warp == 9 && lane == 0) {
+      // ---------------------------------------------- O += P V
+      constexpr uint32_t kIdesc = make_idesc(0u, 128, D, 0u, 1u);
+      bool ok = true;
+      int b = 0, bph = 0, s = 0, sph = 0;
+      Part x;
+      for (int g = 0; ok && walk.next(p, ctl, x); ++g) {
+        // O of the previous tile has been read
+        if (g > 0 && !(ok = bounded_wait(bOfree, (g - 1) & 1, w))) break;
+        for (int j = x.lo; j < x.hi; ++j) {
+          if (!(ok = bounded_wait(bPfull + 8 * b, bph, w))) break;
+          if (!(ok = bounded_wait(bVfull + 8 * s, sph, w))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_ts<false>(tmem + C::COL_O, tmem + b * 128 + kk * 8,
+                           sdesc_sw128(sV + s * C::TILE + kk * 16 * 128, C::CHUNK, 1024), kIdesc,
+                           (j > x.lo || kk > 0) ? 1u : 0u);
+          tc_commit(bVempty + 8 * s);
+          tc_commit(bOdone + 8 * b);
+          if (++b == C::NS) b = 0, bph ^= 1;
+          if (++s == C::ST) s = 0, sph ^= 1;
+        }
+      }
+      tc_commit(bFin + 8);
+      bounded_wait(bFin + 8, 0, w, false);
     }
+    __syncwarp();
+  } else if (warp >= 4) {
+    setmaxnreg_dec<kRegExpand>();
+    // ------------------------------------------------ codes -> fp16 rows
+    w.role = kStatusProducer;
+    const int r = threadIdx.x - 128;  // token of the tile
+    uint4 kc[D / 32], vc[D / 32];
+    uint2 ks = {}, vs = {};
+    auto load = [&](uint4 (&c)[D / 32], uint2 &f, const uint8_t *codes, const uint8_t *scales,
+                    long long row) {
+      if (row < 0) return;
+      const uint4 *src = reinterpret_cast<const uint4 *>(codes + row * (D / 2));
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) c[i] = __ldg(src + i);
+      if constexpr (D == 128)
+        f = __ldg(reinterpret_cast<const uint2 *>(scales + row * (D / 16)));
+      else
+        f.x = __ldg(reinterpret_cast<const uint32_t *>(scales + row * (D / 16)));
+    };
+    // One row as NCH chunks of eight 16-byte units, unit u of chunk n at
+    // u ^ (r & 7): 32 code bits make a unit, two units share a scale.
+    auto expand = [&](const uint4 (&c)[D / 32], const uint2 &f, uint8_t *tile, bool valid) {
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const uint32_t pair = (i < 2 ? f.x : f.y) >> ((i & 1) * 16);
+        const uint32_t two = valid ? e4m3x2_f16x2(pair) : 0u;  // 0 * code = 0
+        const uint32_t sc[2] = {__byte_perm(two, 0, 0x1010), __byte_perm(two, 0, 0x3232)};
+        const uint32_t wd[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int unit = 4 * i + y;  // of the row
+          const uint32_t g = sc[y / 2];
+          uint4 v;
+          v.x = hmul2(e2m1x2_f16x2<0>(wd[y]), g);
+          v.y = hmul2(e2m1x2_f16x2<1>(wd[y]), g);
+          v.z = hmul2(e2m1x2_f16x2<2>(wd[y]), g);
+          v.w = hmul2(e2m1x2_f16x2<3>(wd[y]), g);
+          *reinterpret_cast<uint4 *>(tile + (unit >> 3) * C::CHUNK + r * 128 +
+                                     (((unit & 7) ^ (r & 7)) << 4)) = v;
+        }
+      }
+    };
+    // The cursor runs over the steps of all parts; `id` is its page, loaded
+    // one step before it is used.
+    Part x;
+    bool have = walk.next(p, ctl, x);
+    int j = have ? x.lo : 0, id = -1, off = 0, head = 0;
+    const int bs = 1 << p.c.bs_log2;
+    auto lookup = [&]() {
+      const int t = j * 128 + r;
+      id = have && t < x.s.nk
+               ? p.table[static_cast<long long>(x.b) * p.width + (t >> p.c.bs_log2)]
+               : -1;
+      off = t & (bs - 1);
+      head = x.h;
+    };
+    auto advance = [&]() {
+      if (have && ++j >= x.hi) {
+        have = walk.next(p, ctl, x);
+        j = x.lo;
+      }
+    };
+    auto row_of = [&]() -> long long {
+      if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.c.num_blocks)) return -1;
+      return ((static_cast<long long>(id) * p.c.Hk + head) << p.c.bs_log2) + off;
+    };
+    // rows of steps s, s - 1, s - 2 and s + 1 (k_next); steps known to exist
+    long long row_k = -1, row_1 = -1, row_2 = -1;
+    bool more = have;  // step s exists
+    lookup();
+    row_k = row_of();
+    load(kc, ks, p.c.k_codes, p.c.k_scales, row_k);
+    advance();
+    bool more_next = have;
+    lookup();
+    bool ok = true;
+    int st = 0, ph = 0, vst = 0, vph = 0;
+    int left = 0;  // V steps not yet written
+    for (int s = 0; ok && (more || left > 0); ++s) {
+      long long row_next = -1;
+      if (more) {
+        ok = __all_sync(~0u, s < C::ST || bounded_wait(bKempty + 8 * st, ph ^ 1, w));
+        if (!ok) break;
+        const unsigned bits = __ballot_sync(~0u, row_k >= 0);
+        if (lane == 0)
+          reinterpret_cast<unsigned *>(smem + C::OFF_MASK)[(s % C::MASKS) * 4 + warp - 4] = bits;
+        expand(kc, ks, smem + C::OFF_K + st * C::TILE, row_k >= 0);
+        fence_proxy_async_smem();
+        mbar_arrive(bKfull + 8 * st);
+        if (++st == C::ST) st = 0, ph ^= 1;
+        ++left;
+        if (more_next) {  // the next step's codes, and the page of the one after it
+          row_next = row_of();
+          load(kc, ks, p.c.k_codes, p.c.k_scales, row_next);
+          advance();
+          lookup();
+        }
+      }
+      if (s >= 2) {  // V of step s - 2, loaded a step ago
+        const int n = s - 2;
+        if (ctl.skip_load && n == 0) {  // test hook: the P V issuer's wait runs out
+          if (r == 0) atomicOr(ctl.status, kStatusInjected);
+          ok = false;
+          break;
+        }
+        ok = __all_sync(~0u, n < C::ST || bounded_wait(bVempty + 8 * vst, vph ^ 1, w));
+        if (!ok) break;
+        expand(vc, vs, smem + C::OFF_V + vst * C::TILE, row_2 >= 0);
+        fence_proxy_async_smem();
+        mbar_arrive(bVfull + 8 * vst);
+        if (++vst == C::ST) vst = 0, vph ^= 1;
+        --left;
+      }
+      if (s >= 1 && left > 0) load(vc, vs, p.c.v_codes, p.c.v_scales, row_1);
+      row_2 = row_1;
+      row_1 = row_k;
+      row_k = row_next;
+      more = more && more_next;
+      more_next = more && have;
+    }
+  } else {
+    setmaxnreg_inc<kRegSoftmax>();
+    // ------------------------------------------------ softmax + epilogue
+    w.role = kStatusSoftmax;
+    const int r = threadIdx.x;
+    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t o_tm = tmem + lane_off + C::COL_O;
+    const float mag = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
+    // the sign of the scale goes into Q, a zero scale makes Q zero
+    const float sign = p.scale_log2 == 0.f ? 0.f : p.scale_log2 < 0.f ? -1.f : 1.f;
+    const int ti = r / p.group, tj = r - ti * p.group;  // token of the tile, head of the group
+    // This thread's Q row of part x into shared memory as fp16, times 2^-e
+    // that brings its largest element to 1 .. 2; the factor for its scores.
+    auto stage_q = [&](const Part &x) -> float {
+      const int i = x.qt * ctl.tokens + ti;
+      const bool in = ti < ctl.tokens && i < x.s.nq;
+      uint4 q[D / 8];
+      float amax = 0.f;
+      const uint4 *src = reinterpret_cast<const uint4 *>(
+          static_cast<const T *>(p.q) +
+          (in ? (static_cast<long long>(x.s.r0 + i) * p.Hq + x.h * p.group + tj) * D : 0));
+#pragma unroll
+      for (int u = 0; u < D / 8; ++u) {
+        q[u] = in ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
+        const T *e = reinterpret_cast<const T *>(&q[u]);
+#pragma unroll
+        for (int y = 0; y < 8; ++y) amax = fmaxf(amax, fabsf(static_cast<float>(e[y])));
+      }
+      const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -126), 126);
+      const float mul = pow2(-e) * sign;
+#pragma unroll
+      for (int u = 0; u < D / 8; ++u) {
+        const T *f = reinterpret_cast<const T *>(&q[u]);
+        uint4 v;
+        v.x = pack_f16x2(static_cast<float>(f[0]) * mul, static_cast<float>(f[1]) * mul);
+        v.y = pack_f16x2(static_cast<float>(f[2]) * mul, static_cast<float>(f[3]) * mul);
+        v.z = pack_f16x2(static_cast<float>(f[4]) * mul, static_cast<float>(f[5]) * mul);
+        v.w = pack_f16x2(static_cast<float>(f[6]) * mul, static_cast<float>(f[7]) * mul);
+        *reinterpret_cast<uint4 *>(smem + C::OFF_Q + (u >> 3) * C::CHUNK + r * 128 +
+                                   (((u & 7) ^ (r & 7)) << 4)) = v;
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(bQfull);
+      return mag * pow2(e);
+    };
+    Share share = {-1, 0, 0, 1};
+    bool ok = true;
+    Part x, nx;
+    bool have = walk.next(p, ctl, x);
+    float factor = stage_q(x);
+    int buf = 0, bph = 0, pbuf = C::NS - 1, pbph = 1, step = 0;
+    for (int g = 0; have; ++g) {
+      const int i = x.qt * ctl.tokens + ti;
+      const bool in = ti < ctl.tokens && i < x.s.nq;
+      // keys [0, lim) are this row's
+      const int lim = p.causal && in ? x.s.nk - x.s.nq + i + 1 : x.s.nk;
+      const float sl2 = factor;
+      float m_used = -INFINITY, l = 0.f;
+      for (int j = x.lo; j < x.hi; ++j, ++step) {
+        ok = __all_sync(~0u, bounded_wait(bSfull + 8 * buf, bph, w));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t s_tm = tmem + lane_off + buf * 128;
+        uint32_t sr[4][32];
+        tmem_ld32(s_tm + 0, sr[0]);
+        tmem_ld32(s_tm + 32, sr[1]);
+        tmem_ld32(s_tm + 64, sr[2]);
+        tmem_ld32(s_tm + 96, sr[3]);
+        const uint4 bits = reinterpret_cast<const uint4 *>(smem + C::OFF_MASK)[step % C::MASKS];
+        tmem_ld_wait();
+        reg_fence32(sr[0]);
+        reg_fence32(sr[1]);
+        reg_fence32(sr[2]);
+        reg_fence32(sr[3]);
+        auto S = [&](int c) -> float { return __uint_as_float(sr[c >> 5][c & 31]); };
+        const int cut = lim - j * 128;  // columns [0, cut) are seen
+        if (__any_sync(~0u, cut < 128 || (bits.x & bits.y & bits.z & bits.w) != ~0u)) {
+          const uint32_t word[4] = {bits.x, bits.y, bits.z, bits.w};
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            const int c = cut - 32 * n;
+            const uint32_t see = word[n] & (c >= 32 ? ~0u : c <= 0 ? 0u : (1u << c) - 1u);
+#pragma unroll
+            for (int y = 0; y < 32; ++y)
+              if (!(see >> y & 1)) sr[n][y] = 0xff800000u;  // -inf
+          }
+        }
+        // The offset moves only when a row's maximum grows by more than 2^8.
+        // P is formed with the offset at hand; a row sum of at most 2^8 proves
+        // that no term is above it.  A tile's first step, and rows that have
+        // seen nothing yet, take the maximum first.
+        constexpr float kSumLimit = 256.f, kGrow = 8.f;
+        bool with_max = __any_sync(~0u, m_used == -INFINITY), formed = false;
+        float tsum = 0.f;
+        for (;;) {
+          if (with_max) {
+            float part[8];
+#pragma unroll
+            for (int n = 0; n < 8; ++n) part[n] = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 128; c += 2)
+              part[(c >> 1) & 7] = max3f(part[(c >> 1) & 7], S(c), S(c + 1));
+            const float mx = max3f(max3f(part[0], part[1], part[2]),
+                                   max3f(part[3], part[4], part[5]), fmaxf(part[6], part[7]));
+            const float m_new = fmaxf(m_used, mx * sl2);
+            if (j == x.lo) {
+              m_used = m_new;
+            } else {
+              const bool need = m_new - m_used > kGrow;  // false for -inf - -inf
+              const bool move = __any_sync(~0u, need);
+              if (formed && !move) break;  // P and its sum stand
+              if (move) {
+                // O is rescaled once the last product into it has completed
+                ok = __all_sync(~0u, bounded_wait(bOdone + 8 * pbuf, pbph, w));
+                if (!ok) break;
+                tc_fence_after();
+                const float alpha = need ? ex2_approx(m_used - m_new) : 1.f;
+                const uint64_t a2 = pk2(alpha, alpha);
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                  uint32_t o[32];
+                  tmem_ld32(o_tm + c, o);
+                  tmem_ld_wait();
+                  reg_fence32(o);
+#pragma unroll
+                  for (int n = 0; n < 32; n += 2) {
+                    float lo, hi;
+                    upk2(fmul2(pk2(__uint_as_float(o[n]), __uint_as_float(o[n + 1])), a2), lo, hi);
+                    o[n] = __float_as_uint(lo);
+                    o[n + 1] = __float_as_uint(hi);
+                  }
+                  tmem_st32(o_tm + c, o);
+                }
+                tmem_st_wait();
+                if (need) {
+                  l *= alpha;
+                  m_used = m_new;
+                }
+              }
+            }
+          }
+          const float off = m_used == -INFINITY ? 0.f : -m_used;
+          const uint64_t sl2_2 = pk2(sl2, sl2), nm_2 = pk2(off, off);
+          uint64_t acc[2] = {0ull, 0ull};
+#pragma unroll
+          for (int blk = 0; blk < 2; ++blk) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int n = 0; n < 32; ++n) {
+              const int c0 = 2 * (blk * 32 + n);
+              float x0, x1;
+              upk2(ffma2(pk2(S(c0), S(c0 + 1)), sl2_2, nm_2), x0, x1);
+              const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+              acc[n & 1] = fadd2(acc[n & 1], pk2(p0, p1));
+              pk[n] = pack_f16x2(p0, p1);
+            }
+            tmem_st32(s_tm + blk * 32, pk);
+          }
+          float a0, a1, b0, b1;
+          upk2(acc[0], a0, a1);
+          upk2(acc[1], b0, b1);
+          tsum = (a0 + a1) + (b0 + b1);
+          if (with_max || __all_sync(~0u, tsum <= kSumLimit)) break;
+          with_max = formed = true;
+          tmem_st_wait();  // the second pass rewrites the same columns
+        }
+        if (!ok) break;
+        l += tsum;
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(bPfull + 8 * buf);
+        pbuf = buf;
+        pbph = bph;
+        if (++buf == C::NS) buf = 0, bph ^= 1;
+      }
+      // the next tile's Q goes in while this one's last products run
+      const bool have_next = walk.next(p, ctl, nx);
+      if (ok && have_next) {
+        ok = __all_sync(~0u, bounded_wait(bQempty, g & 1, w));
+        if (ok) factor = stage_q(nx);
+      }
+      if (ok) ok = __all_sync(~0u, bounded_wait(bOdone + 8 * pbuf, pbph, w));
+      if (ok) {
+        tc_fence_after();
+        const bool begins = x.lo == 0, ends = x.hi == x.units;
+        if (begins && !ends) share.b = x.b, share.h = x.h, share.qt = x.qt;
+        if (!begins) share.head_ends = ends;
+        const bool whole = begins && ends;
+        const float inv = l > 0.f ? p.v_mul / l : 0.f;
+        const int head = x.h * p.group + tj;
+        T *out = static_cast<T *>(p.o) +
+                 (in ? (static_cast<long long>(x.s.r0 + i) * p.Hq + head) * D : 0);
+        float *part = part_of<D, R>(ws, blockIdx.x, begins);
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(o_tm + c, o);
+          tmem_ld_wait();
+          reg_fence32(o);
+          if (!in) continue;
+          if (whole) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              alignas(16) T e[8];
+#pragma unroll
+              for (int y = 0; y < 8; ++y)
+                e[y] = static_cast<T>(l > 0.f ? __uint_as_float(o[8 * u + y]) * inv : 0.f);
+              reinterpret_cast<uint4 *>(out + c)[u] = *reinterpret_cast<const uint4 *>(e);
+            }
+          } else {
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              reinterpret_cast<uint4 *>(part + r * D + c)[u] =
+                  make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+          }
+        }
+        if (in && whole)
+          p.lse[static_cast<long long>(head) * p.total_q + x.s.r0 + i] =
+              l > 0.f ? m_used * 0.6931471805599453f + logf(l) : -INFINITY;
+        if (in && !whole)
+          reinterpret_cast<float2 *>(part + R * D)[r] = make_float2(m_used, l);
+        if (have_next) {
+          tc_fence_before();
+          mbar_arrive(bOfree);
+        }
+      }
+      // the four warps take one decision to go on or stop
+      if (named_bar_or(1, 128, !ok || *abort_flag != 0)) break;
+      x = nx;
+      have = have_next;
+    }
+    if (r == 0) reinterpret_cast<Share *>(ws)[blockIdx.x] = share;
   }
-  for (int o = 16; o; o /= 2) l += __shfl_xor_sync(~0u, l, o);
-  T *out = static_cast<T *>(p.o) + row * D;
-  const float inv = l > 0.f ? p.v_mul / l : 0.f;
-  for (int n = 0; n < D / 32; ++n) out[lane + 32 * n] = static_cast<T>(acc[n] * inv);
-  if (lane == 0)
-    p.lse[static_cast<long long>(h) * p.total_q + r0 + i] =
-        l > 0.f ? m * 0.6931471805599453f + logf(l) : -INFINITY;
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
 }
 
 template <typename T, int D>
-cudaError_t launch(const Kv4Attn &p, int tile_rows, cudaStream_t s) {
+cudaError_t launch(const Kv4Attn &p, const ManyCtl &ctl, float *ws, int num_sms, cudaStream_t s) {
+  static std::atomic<unsigned long long> attr_done{0};
+  constexpr int smem = ManyCfg<D>::SMEM;
+  cudaError_t e = smem_attr_once(fa_kv4_many_kernel<T, D>, smem, &attr_done);
+  if (e != cudaSuccess) return e;
+  // one CTA on each SM, no more than there can be units
+  const long long tiles = (static_cast<long long>(p.max_q) + ctl.tokens - 1) / ctl.tokens;
+  const double most = static_cast<double>(p.B) * p.c.Hk * tiles *
+                      (p.max_k < 128 ? 1.0 : (p.max_k + 127.0) / 128.0);
+  int ctas = num_sms > 0 ? min(num_sms, kKv4ManyCtas) : 1;
+  if (ctas > most) ctas = static_cast<int>(most);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((p.max_q + kWarps - 1) / kWarps, p.Hq, p.B);
-  cfg.blockDim = dim3(32 * kWarps);
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fa_kv4_many_kernel<T, D>, p, tile_rows);
+  e = cudaLaunchKernelEx(&cfg, fa_kv4_many_kernel<T, D>, p, ctl, ws);
+  if (e != cudaSuccess || ctas == 1) return e;
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas - 1), R / kJoinRows);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, fa_kv4_join_kernel<T, D, R>, p, ws, ctas, ctl.tokens);
 }
 
 }  // namespace
 
-cudaError_t launch_kv4_many(const Kv4Attn &p, int tile_rows, int dtype, cudaStream_t s) {
+cudaError_t launch_kv4_many(const Kv4Attn &p, int tile_rows, int dtype, float *ws, int num_sms,
+                            unsigned *status, unsigned long long wait_limit_ns, int skip_load,
+                            cudaStream_t s) {
+  const ManyCtl ctl = {status, wait_limit_ns, skip_load, tile_rows, R / p.group};
   if (dtype == FA_DTYPE_BF16)
-    return p.c.d == 64 ? launch<__nv_bfloat16, 64>(p, tile_rows, s)
-                       : launch<__nv_bfloat16, 128>(p, tile_rows, s);
-  return p.c.d == 64 ? launch<__half, 64>(p, tile_rows, s) : launch<__half, 128>(p, tile_rows, s);
+    return p.c.d == 64 ? launch<__nv_bfloat16, 64>(p, ctl, ws, num_sms, s)
+                       : launch<__nv_bfloat16, 128>(p, ctl, ws, num_sms, s);
+  return p.c.d == 64 ? launch<__half, 64>(p, ctl, ws, num_sms, s)
+                     : launch<__half, 128>(p, ctl, ws, num_sms, s);
 }
 
 }  // namespace fa

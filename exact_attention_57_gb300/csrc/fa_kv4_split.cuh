@@ -1,0 +1,213 @@
+// fa_kv4_split.cuh — how the attention kernels over the 4-bit cache deal their
+// work: all tiles of all sequences lie in one line of units (a unit is a step
+// along the keys), every CTA takes an equal share of the line, and tiles that
+// shares cut are joined by a second kernel from parts in the workspace.
+#pragma once
+
+#include "fa_kv4.cuh"
+#include "fa_serve.h"
+#include "ptx.cuh"
+
+namespace fa {
+
+// One sequence as this kernel sees it.
+struct Seq {
+  int r0, nq, nk;
+};
+
+__device__ __forceinline__ Seq load_seq(const Kv4Attn &p, int b) {
+  Seq s = {b, 1, 0};
+  if (p.cu_q) {
+    s.r0 = min(max(p.cu_q[b], 0), p.total_q);
+    s.nq = min(max(min(max(p.cu_q[b + 1], 0), p.total_q) - s.r0, 0), p.max_q);
+  }
+  s.nk = static_cast<int>(min(static_cast<long long>(min(max(p.lens[b], 0), p.max_k)),
+                              static_cast<long long>(p.width) << p.c.bs_log2));
+  return s;
+}
+
+// What a CTA says to the joining kernel, at the workspace's start: the tile
+// (sequence, key head, query tile) whose first part, but not last, is its own
+// (b = -1: none), and whether the one it found begun ends within it.
+struct Share {
+  int b, h, qt, head_ends;
+};
+static_assert(sizeof(Share) == 16, "one 16-byte load");
+
+// Part `which` (0: of a tile begun before the CTA, 1: of one it begins) of
+// CTA n: rows of D sums, then (maximum, sum of weights) a row.
+template <int D, int R>
+__device__ __forceinline__ float *part_of(float *ws, int n, int which) {
+  return ws + kKv4MaxCtas * (sizeof(Share) / sizeof(float)) +
+         static_cast<long long>(2 * n + which) * R * (D + 2);
+}
+
+// Where a unit lies in the line of all units.
+struct Place {
+  long long total;   // units in all
+  long long before;  // units before sequence b
+  int b;
+};
+
+// The place of unit floor(total * num / den), `units(b)` being those of
+// sequence b, all key heads (all kWarps * 32 threads get it); den becomes the
+// smaller of itself and the units in all.  `sums` holds a prefix sum a thread.
+template <int kWarps, typename F>
+__device__ Place find_unit(const Kv4Attn &p, F units, int num, int *den, long long *target,
+                           long long *sums, long long (*warp_sums)[kWarps]) {
+  constexpr int kThreads = kWarps * 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  Place at = {0, 0, 0};
+  // total first, where one round of requests does not show it
+  if (p.B > kThreads) {
+    long long n = 0;
+    for (int b = tid; b < p.B; b += kThreads) n += units(b);
+    for (int o = 16; o; o /= 2) n += __shfl_xor_sync(~0u, n, o);
+    if (lane == 0) warp_sums[1][warp] = n;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) at.total += warp_sums[1][w];
+  }
+  for (int base = 0;; base += kThreads) {
+    const int b = base + tid;
+    const long long n = b < p.B ? units(b) : 0;
+    long long incl = n;
+    for (int o = 1; o < 32; o *= 2) {
+      const long long x = __shfl_up_sync(~0u, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 31) warp_sums[0][warp] = incl;
+    __syncthreads();
+    long long pre = at.before, all = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) pre += warp_sums[0][w];
+      all += warp_sums[0][w];
+    }
+    sums[tid] = pre + incl - n;
+    __syncthreads();
+    if (p.B <= kThreads) at.total = all;
+    if (base == 0) {
+      *den = static_cast<int>(min(static_cast<long long>(*den), at.total));
+      if (num >= *den) return at;  // more CTAs than units
+      *target = at.total * num / *den;
+    }
+    if (*target < at.before + all || base + kThreads >= p.B) {
+      int lo = 0, hi = kThreads;  // the last i with sums[i] <= target
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (sums[mid] <= *target) lo = mid;
+        else hi = mid;
+      }
+      at.b = base + lo;
+      at.before = sums[lo];
+      return at;
+    }
+    at.before += all;
+    __syncthreads();
+  }
+}
+
+// Joins the parts of the tiles that more than one CTA shared: CTA n takes
+// what CTA n of the grid above began and others went on with (n's part 1, then
+// the parts 0 of n + 1, n + 2, ... up to the one that ends it), four rows of
+// it.  The eight warps share the parts, so that a tile split over the whole
+// grid costs a few rounds of loads.  Row r of query tile t is head r % group of
+// token t * tokens + r / group.
+constexpr int kJoinRows = 4;
+
+template <typename T, int D, int R>
+__global__ void __launch_bounds__(256)
+    fa_kv4_join_kernel(const Kv4Attn p, float *ws, int ctas, int tokens) {
+  constexpr int kWarps = 8;
+  constexpr int W = D / 32;  // columns a lane
+  __shared__ float s_sum[kWarps][kJoinRows][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = blockIdx.x;
+  const int row0 = blockIdx.y * kJoinRows;
+  griddep_wait();
+  griddep_launch_dependents();
+  const Share *shares = reinterpret_cast<const Share *>(ws);
+  const Share mine = shares[first];
+  if (mine.b < 0) return;
+  const Seq sq = load_seq(p, mine.b);
+  const int token0 = mine.qt * tokens;
+  const int rows = static_cast<int>(
+      min(static_cast<long long>(min(sq.nq - token0, tokens)) * p.group, static_cast<long long>(R)));
+  if (row0 >= rows) return;
+  int last = first + 1;  // the part that ends it
+  for (;; last += 32) {
+    const int n = last + lane;
+    const unsigned stop = __ballot_sync(~0u, n >= ctas - 1 || shares[n].head_ends != 0);
+    if (stop) {
+      last += __ffs(stop) - 1;
+      break;
+    }
+  }
+  auto part = [&](int n) { return part_of<D, R>(ws, n, n == first); };
+  float mm[kJoinRows], ll[kJoinRows];
+#pragma unroll
+  for (int y = 0; y < kJoinRows; ++y) mm[y] = -INFINITY, ll[y] = 0.f;
+  for (int n = first + lane; n <= last; n += 32) {
+    const float2 *ml = reinterpret_cast<const float2 *>(part(n) + R * D) + row0;
+#pragma unroll
+    for (int y = 0; y < kJoinRows; ++y)
+      if (row0 + y < rows) mm[y] = fmaxf(mm[y], ml[y].x);
+  }
+#pragma unroll
+  for (int y = 0; y < kJoinRows; ++y)
+    for (int o = 16; o; o /= 2) mm[y] = fmaxf(mm[y], __shfl_xor_sync(~0u, mm[y], o));
+  float sum[kJoinRows][W] = {};
+#pragma unroll 2
+  for (int n = first + warp; n <= last; n += kWarps) {
+    const float *src = part(n);
+#pragma unroll
+    for (int y = 0; y < kJoinRows; ++y) {
+      if (row0 + y >= rows) continue;
+      const float2 ml = reinterpret_cast<const float2 *>(src + R * D)[row0 + y];
+      const float f = mm[y] == -INFINITY ? 0.f : ex2_approx(ml.x - mm[y]);
+      ll[y] += f * ml.y;
+      float v[W];
+      if constexpr (W == 4)
+        *reinterpret_cast<float4 *>(v) =
+            *reinterpret_cast<const float4 *>(src + (row0 + y) * D + lane * 4);
+      else
+        *reinterpret_cast<float2 *>(v) =
+            *reinterpret_cast<const float2 *>(src + (row0 + y) * D + lane * 2);
+#pragma unroll
+      for (int x = 0; x < W; ++x) sum[y][x] += f * v[x];
+    }
+  }
+  __shared__ float s_l[kWarps][kJoinRows];
+#pragma unroll
+  for (int y = 0; y < kJoinRows; ++y) {
+#pragma unroll
+    for (int x = 0; x < W; ++x) s_sum[warp][y][lane * W + x] = sum[y][x];
+    if (lane == 0) s_l[warp][y] = ll[y];
+  }
+  __syncthreads();
+  if (warp >= kJoinRows || row0 + warp >= rows) return;
+  float l = 0.f, total[W] = {};
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    l += s_l[w][warp];
+#pragma unroll
+    for (int x = 0; x < W; ++x) total[x] += s_sum[w][warp][lane * W + x];
+  }
+  float m = mm[0];
+#pragma unroll
+  for (int y = 1; y < kJoinRows; ++y) m = warp == y ? mm[y] : m;
+  const int row = row0 + warp, y = row / p.group, j = row - y * p.group, i = token0 + y;
+  const int head = mine.h * p.group + j;
+  T *out = static_cast<T *>(p.o) + (static_cast<long long>(sq.r0 + i) * p.Hq + head) * D + lane * W;
+  const float inv = l > 0.f ? p.v_mul / l : 0.f;
+  alignas(8) T e[W];
+#pragma unroll
+  for (int x = 0; x < W; ++x) e[x] = static_cast<T>(total[x] * inv);
+  if constexpr (W == 4)
+    *reinterpret_cast<uint2 *>(out) = *reinterpret_cast<const uint2 *>(e);
+  else
+    *reinterpret_cast<uint32_t *>(out) = *reinterpret_cast<const uint32_t *>(e);
+  if (lane == 0)
+    p.lse[static_cast<long long>(head) * p.total_q + sq.r0 + i] =
+        l > 0.f ? m * 0.6931471805599453f + logf(l) : -INFINITY;
+}
+
+}  // namespace fa

@@ -17,6 +17,7 @@ int api_device_check();
 int api_device_status(unsigned **status);
 int api_sm_count();
 unsigned long long api_wait_limit();
+int api_skip_load();  // the test hook of fa_set_test_hooks
 
 // ------------------------------------------------------------ block tables
 struct PlanParams {
@@ -83,11 +84,17 @@ struct Kv4Attn {
 // launch_kv4_attn's tile of that many rows, longer ones through
 // launch_kv4_many.  kv4_tile_rows: 8, 16 or 32, the smallest that holds the
 // longest sequence, else the smallest that holds one query; 0: none does.
-constexpr int kKv4MaxCtas = 304;  // two on each of 152 SMs
+constexpr int kKv4MaxCtas = 304;   // two on each of 152 SMs
+constexpr int kKv4ManyCtas = 152;  // launch_kv4_many: one on each
+constexpr int kKv4ManyRows = 128;  // and tiles of that many rows, so group <= 128
 int kv4_tile_rows(int group, int max_q);
-size_t kv4_workspace(int rows, int d);
+size_t kv4_workspace(int rows, int d);  // of either kernel, by its rows
 cudaError_t launch_kv4_attn(const Kv4Attn &p, int rows, int dtype, float *ws, int num_sms,
                             cudaStream_t s);
-cudaError_t launch_kv4_many(const Kv4Attn &p, int tile_rows, int dtype, cudaStream_t s);
+// status: the device's status word; wait_limit_ns bounds its barrier waits;
+// skip_load: the test hook that leaves out a tile's values.
+cudaError_t launch_kv4_many(const Kv4Attn &p, int tile_rows, int dtype, float *ws, int num_sms,
+                            unsigned *status, unsigned long long wait_limit_ns, int skip_load,
+                            cudaStream_t s);
 
 }  // namespace fa

@@ -276,8 +276,13 @@ extern "C" int fa_kv4_gather(const long long *slots, int R, const void *k_codes,
 
 extern "C" unsigned long long fa_fwd_kv4_workspace(int B, int Hq, int Hk, int max_seqlen_q, int d) {
   if (B < 1 || Hq < 1 || Hk < 1 || Hq % Hk != 0 || max_seqlen_q < 1 || d < 1) return 0;
-  const int tile = fa::kv4_tile_rows(Hq / Hk, max_seqlen_q);
-  return tile ? fa::kv4_workspace(tile, d) : 0;
+  const int group = Hq / Hk, tile = fa::kv4_tile_rows(group, max_seqlen_q);
+  if (group > fa::kKv4ManyRows) return 0;
+  const size_t few = tile ? fa::kv4_workspace(tile, d) : 0;
+  const size_t many = static_cast<long long>(max_seqlen_q) * group > tile
+                          ? fa::kv4_workspace(fa::kKv4ManyRows, d)
+                          : 0;
+  return few > many ? few : many;
 }
 
 extern "C" int fa_fwd_kv4(const void *q, void *o, float *lse, const void *k_codes,
@@ -318,10 +323,11 @@ extern "C" int fa_fwd_kv4(const void *q, void *o, float *lse, const void *k_code
                      {cu_seqlens_q, static_cast<size_t>(B + 1) * 4}};
   if (any_meet(out, in)) return FA_ERR_INVALID_ARG;
   if (dtype != FA_DTYPE_BF16 && dtype != FA_DTYPE_F16) return FA_ERR_UNSUPPORTED;
-  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if ((d != 64 && d != 128) || Hq / Hk > fa::kKv4ManyRows) return FA_ERR_UNSUPPORTED;
   if (need > 0 && (!workspace || off_by(workspace, 256) || workspace_bytes < need))
     return FA_ERR_INVALID_ARG;
-  if ((rc = fa::api_device_check()) != FA_OK) return rc;
+  unsigned *status = nullptr;
+  if ((rc = fa::api_device_status(&status)) != FA_OK) return rc;
   fa::Kv4Attn p;
   p.q = q;
   p.o = o;
@@ -342,10 +348,12 @@ extern "C" int fa_fwd_kv4(const void *q, void *o, float *lse, const void *k_code
   p.causal = causal;
   const int tile = fa::kv4_tile_rows(p.group, max_seqlen_q);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int sms = fa::api_sm_count();
+  float *ws = static_cast<float *>(workspace);
   cudaError_t e = cudaSuccess;
-  if (tile > 0)
-    e = fa::launch_kv4_attn(p, tile, dtype, static_cast<float *>(workspace), fa::api_sm_count(), s);
+  if (tile > 0) e = fa::launch_kv4_attn(p, tile, dtype, ws, sms, s);
   if (e == cudaSuccess && static_cast<long long>(max_seqlen_q) * p.group > tile)
-    e = fa::launch_kv4_many(p, tile, dtype, s);
+    e = fa::launch_kv4_many(p, tile, dtype, ws, sms, status, fa::api_wait_limit(),
+                            fa::api_skip_load(), s);
   return done(e);
 }

@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libfa.so")
@@ -472,24 +473,24 @@ def fa_fwd_kv4_workspace(B, Hq, Hk, max_seqlen_q, d) -> int:
     return load().fa_fwd_kv4_workspace(B, Hq, Hk, max_seqlen_q, d)
 
 
-def _same_device(first, *tensors):
-    """The CUDA device of `first`; every tensor given has to live there."""
-    dev = first.device
-    if dev.type != "cuda":
+def _same_device(first, *tensors) -> int:
+    """Index of the CUDA device of `first`; every tensor given has to live there."""
+    dev = first.get_device()
+    if dev < 0:
         raise ValueError("CUDA tensors expected")
     for t in tensors:
-        if t is not None and t.device != dev:
+        if t is not None and t.get_device() != dev:
             raise ValueError("tensors on one device expected")
     return dev
 
 
 def _call(where, dev, stream, fn, *args):
-    """fn(*args, stream) with `dev` current (its current stream unless one is
-    given); FaError on failure."""
+    """fn(*args, stream) with device `dev` current (its current stream unless
+    one is given); FaError on failure."""
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream(dev).cuda_stream
-    if torch.cuda.current_device() == dev.index:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    if torch.cuda.current_device() == dev:
         st = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -565,11 +566,15 @@ def rotary_table(inv_freq, axes=None, device="cuda"):
     return t.to(device)
 
 
+_pack6 = struct.Struct("=6q").pack
+
+
 def _rope_strides(x, y):
+    """Six host int64: batch, head and row strides of x, then of y."""
     a, b = x.stride(), y.stride()
-    if x.dim() == 4:  # [B, H, N, d]
-        return (ctypes.c_longlong * 6)(a[0], a[1], a[2], b[0], b[1], b[2])
-    return (ctypes.c_longlong * 6)(0, a[1], a[0], 0, b[1], b[0])  # [T, H, d]
+    if len(a) == 4:  # [B, H, N, d]
+        return _pack6(a[0], a[1], a[2], b[0], b[1], b[2])
+    return _pack6(0, a[1], a[0], 0, b[1], b[0])  # [T, H, d]
 
 
 def rotary(q, k, positions, table, interleaved: bool = False, q_out=None, k_out=None,
@@ -596,13 +601,13 @@ def rotary(q, k, positions, table, interleaved: bool = False, q_out=None, k_out=
     if positions.shape[1:] != rows:
         raise ValueError("positions [axes, B, N] (or [axes, T]) expected")
     if q_out is None:
-        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     Hk = 0
     if k is not None:
         Hk = k.shape[1]
         want = (B, Hk, N, d) if nd == 4 else (N, Hk, d)
         if k_out is None:
-            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
         if k.shape != want or k.dtype != q.dtype or k_out.shape != want or k_out.dtype != q.dtype \
                 or k.stride(-1) != 1 or k_out.stride(-1) != 1:
             raise ValueError("k, k_out: q's shape but for the heads, its dtype, contiguous rows")
@@ -638,11 +643,15 @@ def _any_dtype(t) -> int:
 def _cache_shape(k_codes, k_scales, v_codes, v_scales):
     """(num_blocks, Hk, block_size, d) of the cache's four arrays."""
     import torch
-    blocks, Hk, bs, half = k_codes.shape
-    for t, n in ((k_codes, half), (v_codes, half), (k_scales, half // 8), (v_scales, half // 8)):
-        if t.dtype != torch.uint8 or t.shape != (blocks, Hk, bs, n) or not t.is_contiguous():
-            raise ValueError("cache: contiguous uint8 codes [blocks, Hk, block_size, d/2] and "
-                             "scales [blocks, Hk, block_size, d/16] expected")
+    codes = k_codes.shape
+    blocks, Hk, bs, half = codes
+    scales, u8 = (blocks, Hk, bs, half // 8), torch.uint8
+    if v_codes.shape != codes or k_scales.shape != scales or v_scales.shape != scales:
+        raise ValueError("cache: codes [blocks, Hk, block_size, d/2] and scales "
+                         "[blocks, Hk, block_size, d/16] expected")
+    for t in (k_codes, v_codes, k_scales, v_scales):
+        if t.dtype is not u8 or not t.is_contiguous():
+            raise ValueError("cache: contiguous uint8 tensors expected")
     return blocks, Hk, bs, 2 * half
 
 
