@@ -11,20 +11,20 @@
 // Warps 0-3    softmax, correction and epilogue, one row a thread; they also
 //              bring the row's Q into shared memory, as fp16 times a power of
 //              two, before the previous tile's epilogue.
-// Warps 4-7    expand the codes: thread r loads token r of the 128 (a page
-//              lookup, D / 2 bytes of codes, D / 16 of scales, one tile
-//              ahead), turns them into fp16 (exact: six significant bits) and
-//              writes them as a 128-byte-swizzled row, K two tiles ahead of V.
+// Warps 4-7    expand the codes of K, warps 8-11 those of V: thread r loads
+//              token r of the 128 (a page lookup, D / 2 bytes of codes, D / 16
+//              of scales, two steps ahead), turns them into fp16 (exact: six
+//              significant bits) and writes them as a 128-byte-swizzled row.
 //              Tokens behind the sequence or on a missing page become zeros
 //              and are reported in a bit mask.
-// Warp 8, 9    issue S = Q K^T (three score buffers) and O += P V (P in tensor
-//              memory), kind::f16, fp32 accumulators; warp 8 owns the tensor
+// Warp 12, 13  issue S = Q K^T (three score buffers) and O += P V (P in tensor
+//              memory), kind::f16, fp32 accumulators; warp 12 owns the tensor
 //              memory.
 //
 // The products of a 128 x 128 step need about 1000 cycles of the tensor pipe
 // and the softmax 850 of its warps; expanding the step's K and V costs 512
-// conversions, 512 multiplications and 128 16-byte stores a warp, which four
-// warps of their own hide beside them.
+// conversions, 512 multiplications and 128 16-byte stores a warp, which the
+// eight warps of their own hide beside them.
 //
 // Every wait is bounded; on expiry the CTA raises its abort flag, records the
 // role in the status word, drains its products, frees tensor memory and ends.
@@ -41,7 +41,7 @@
 namespace fa {
 namespace {
 
-constexpr int kThreads = 384, kWarps = 12;
+constexpr int kThreads = 512, kWarps = 16;
 constexpr int R = kKv4ManyRows;
 
 struct ManyCtl {
@@ -49,6 +49,8 @@ struct ManyCtl {
   unsigned long long wait_limit_ns;
   int skip_load, tile_rows, tokens;  // tokens of a tile
 };
+
+constexpr int WALK_BYTES = 96;
 
 template <int D>
 struct ManyCfg {
@@ -69,11 +71,12 @@ struct ManyCfg {
   static constexpr int NBAR = 5 + 4 * ST + 3 * NS;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int OFF_SUMS = OFF_K;           // before the first tile arrives
-  static constexpr int SMEM = OFF_MISC + 16 + 1024;
+  static constexpr int OFF_WALK = OFF_MISC + 16;     // a walk for each of 14 warps
+  static constexpr int SMEM = OFF_WALK + 14 * WALK_BYTES + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
 };
-constexpr uint32_t kRegSoftmax = 240, kRegExpand = 152, kRegIssue = 104;
-static_assert(128 * (kRegSoftmax + kRegExpand + kRegIssue) <= kThreads * 168,
+constexpr uint32_t kRegSoftmax = 216, kRegExpand = 104, kRegIssue = 88;
+static_assert(128 * (kRegSoftmax + 2 * kRegExpand + kRegIssue) <= kThreads * 128,
               "the register split must fit in what the block is launched with");
 
 // Sum over i in [0, n) of floor((a i + b) / m), for n, a, b >= 0, m > 0.
@@ -125,7 +128,9 @@ __device__ long long units_before(const Kv4Attn &p, const ManyCtl &c, const Seq 
   return sum;
 }
 
-// A CTA's share as a list of parts of tiles; every role walks it by itself.
+// A CTA's share as a list of parts of tiles.  Every warp walks it by itself, in
+// a record of its own in shared memory, which leaves the registers to the
+// inner loops.
 struct Part {
   int b, h, qt, lo, hi, units;  // steps [lo, hi) of `units`
   Seq s;
@@ -134,32 +139,44 @@ struct Walk {
   long long u, u1;
   int b, h, qt, unit, n;  // n tiles of sequence b
   Seq s;
-  __device__ __forceinline__ bool next(const Kv4Attn &p, const ManyCtl &c, Part &x) {
-    if (u >= u1) return false;
-    while (qt >= n) {
-      if (n > 0 && h + 1 < p.c.Hk) {
-        ++h;
-      } else {  // another sequence of this kernel follows, since u < the total
-        s = load_seq(p, ++b);
-        n = tiles_of(p, c, s);
-        h = 0;
-      }
-      qt = 0;
-    }
-    x.b = b, x.h = h, x.qt = qt, x.s = s;
-    x.units = tile_units(p, c, s, qt, n);
-    x.lo = unit;
-    x.hi = static_cast<int>(min(static_cast<long long>(x.units), unit + (u1 - u)));
-    u += x.hi - x.lo;
-    unit = 0;
-    ++qt;
-    return true;
-  }
+  Part part;
+  int more, pad;
 };
+static_assert(sizeof(Walk) == WALK_BYTES, "the layout of shared memory counts on it");
+
+// The next part of the warp's walk, for all its lanes (they converge here).
+__device__ __forceinline__ bool next_part(const Kv4Attn &p, const ManyCtl &c, Walk *k, Part &x) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) {
+    k->more = k->u < k->u1;
+    if (k->more) {
+      while (k->qt >= k->n) {
+        if (k->n > 0 && k->h + 1 < p.c.Hk) {
+          ++k->h;
+        } else {  // another sequence of this kernel follows, since u < the total
+          k->s = load_seq(p, ++k->b);
+          k->n = tiles_of(p, c, k->s);
+          k->h = 0;
+        }
+        k->qt = 0;
+      }
+      const int units = tile_units(p, c, k->s, k->qt, k->n);
+      const int hi = static_cast<int>(min(static_cast<long long>(units), k->unit + (k->u1 - k->u)));
+      k->part = Part{k->b, k->h, k->qt, k->unit, hi, units, k->s};
+      k->u += hi - k->unit;
+      k->unit = 0;
+      ++k->qt;
+    }
+  }
+  __syncwarp();
+  x = k->part;
+  return k->more != 0;
+}
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    fa_kv4_many_kernel(const Kv4Attn p, const ManyCtl ctl, float *ws) {
+    fa_kv4_many_kernel(const __grid_constant__ Kv4Attn p, const __grid_constant__ ManyCtl ctl,
+                       float *ws) {
   using C = ManyCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -205,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_launch_dependents();
   // this CTA's share of the line of units
   int den = gridDim.x;
-  Walk walk = {};
+  long long u0 = 0;
   const Place at = find_unit<kWarps>(
       p,
       [&](int b) {
@@ -213,30 +230,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = tiles_of(p, ctl, s);
         return units_before(p, ctl, s, n, n) * p.c.Hk;
       },
-      blockIdx.x, &den, &walk.u, s_sums, s_warp);
+      blockIdx.x, &den, &u0, s_sums, s_warp);
   if (static_cast<int>(blockIdx.x) >= den) {
     if (threadIdx.x == 0) reinterpret_cast<Share *>(ws)[blockIdx.x] = Share{-1, 0, 0, 1};
     return;
   }
-  walk.u1 = at.total * (blockIdx.x + 1) / den;
-  walk.b = at.b;
-  walk.s = load_seq(p, at.b);
-  walk.n = tiles_of(p, ctl, walk.s);
-  {
-    const long long per_head = units_before(p, ctl, walk.s, walk.n, walk.n);
-    const long long into = walk.u - at.before;
-    walk.h = static_cast<int>(into / per_head);
-    const long long rest = into - walk.h * per_head;
-    int lo = 0, hi = walk.n;  // the last tile that begins at or before `rest`
+  Walk *walk = reinterpret_cast<Walk *>(smem + C::OFF_WALK) + warp;
+  if (warp < 14 && lane == 0) {
+    Walk k = {};
+    k.u = u0;
+    k.u1 = at.total * (blockIdx.x + 1) / den;
+    k.b = at.b;
+    k.s = load_seq(p, at.b);
+    k.n = tiles_of(p, ctl, k.s);
+    const long long per_head = units_before(p, ctl, k.s, k.n, k.n);
+    const long long into = u0 - at.before;
+    k.h = static_cast<int>(into / per_head);
+    const long long rest = into - k.h * per_head;
+    int lo = 0, hi = k.n;  // the last tile that begins at or before `rest`
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
-      if (units_before(p, ctl, walk.s, mid, walk.n) <= rest) lo = mid;
+      if (units_before(p, ctl, k.s, mid, k.n) <= rest) lo = mid;
       else hi = mid;
     }
-    walk.qt = lo;
-    walk.unit = static_cast<int>(rest - units_before(p, ctl, walk.s, lo, walk.n));
+    k.qt = lo;
+    k.unit = static_cast<int>(rest - units_before(p, ctl, k.s, lo, k.n));
+    *walk = k;
   }
-  if (warp == 8) {
+  if (warp == 12) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
@@ -246,92 +267,111 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   WaitCtl w{abort_flag, ctl.status, ctl.wait_limit_ns, 0u};
 
-  if (warp >= 8) {
+  if (warp >= 12) {
     setmaxnreg_dec<kRegIssue>();
     w.role = kStatusMma;
-    if (warp == 8 && lane == 0) {
+    if (warp == 12) {
       // ---------------------------------------------- S = Q K^T
       constexpr uint32_t kIdesc = make_idesc(0u, 128, 128, 0u, 0u);
       bool ok = true;
       int b = 0, bph = 0, s = 0, sph = 0, issued = 0;
       Part x;
-      for (int g = 0; ok && walk.next(p, ctl, x); ++g) {
-        if (!(ok = bounded_wait(bQfull, g & 1, w))) break;
-        for (int j = x.lo; j < x.hi; ++j, ++issued) {
-          // score buffer b last held P of three steps ago
-          if (issued >= C::NS && !(ok = bounded_wait(bOdone + 8 * b, bph ^ 1, w))) break;
-          if (!(ok = bounded_wait(bKfull + 8 * s, sph, w))) break;
-          tc_fence_after();
+      for (int g = 0; ok && next_part(p, ctl, walk, x); ++g) {
+        if (lane == 0) {
+          ok = bounded_wait(bQfull, g & 1, w);
+          for (int j = x.lo; ok && j < x.hi; ++j, ++issued) {
+            // score buffer b last held P of three steps ago
+            if (issued >= C::NS && !(ok = bounded_wait(bOdone + 8 * b, bph ^ 1, w))) break;
+            if (!(ok = bounded_wait(bKfull + 8 * s, sph, w))) break;
+            tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * C::CHUNK + (kk & 3) * 32;
-            umma_ss<false>(tmem + b * 128, sdesc_sw128(sQ + off, 16, 1024),
-                           sdesc_sw128(sK + s * C::TILE + off, 16, 1024), kIdesc, kk > 0 ? 1u : 0u);
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = (kk >> 2) * C::CHUNK + (kk & 3) * 32;
+              umma_ss<false>(tmem + b * 128, sdesc_sw128(sQ + off, 16, 1024),
+                             sdesc_sw128(sK + s * C::TILE + off, 16, 1024), kIdesc,
+                             kk > 0 ? 1u : 0u);
+            }
+            tc_commit(bKempty + 8 * s);
+            tc_commit(bSfull + 8 * b);
+            if (++b == C::NS) b = 0, bph ^= 1;
+            if (++s == C::ST) s = 0, sph ^= 1;
           }
-          tc_commit(bKempty + 8 * s);
-          tc_commit(bSfull + 8 * b);
-          if (++b == C::NS) b = 0, bph ^= 1;
-          if (++s == C::ST) s = 0, sph ^= 1;
+          if (ok) tc_commit(bQempty);
         }
-        if (ok) tc_commit(bQempty);
+        ok = __shfl_sync(~0u, ok, 0);
       }
-      tc_commit(bFin);
-      bounded_wait(bFin, 0, w, false);
-    } else if (warp == 9 && lane == 0) {
+      if (lane == 0) {
+        tc_commit(bFin);
+        bounded_wait(bFin, 0, w, false);
+      }
+    } else if (warp == 13) {
       // ---------------------------------------------- O += P V
       constexpr uint32_t kIdesc = make_idesc(0u, 128, D, 0u, 1u);
       bool ok = true;
       int b = 0, bph = 0, s = 0, sph = 0;
       Part x;
-      for (int g = 0; ok && walk.next(p, ctl, x); ++g) {
-        // O of the previous tile has been read
-        if (g > 0 && !(ok = bounded_wait(bOfree, (g - 1) & 1, w))) break;
-        for (int j = x.lo; j < x.hi; ++j) {
-          if (!(ok = bounded_wait(bPfull + 8 * b, bph, w))) break;
-          if (!(ok = bounded_wait(bVfull + 8 * s, sph, w))) break;
-          tc_fence_after();
+      for (int g = 0; ok && next_part(p, ctl, walk, x); ++g) {
+        if (lane == 0) {
+          // O of the previous tile has been read
+          ok = g == 0 || bounded_wait(bOfree, (g - 1) & 1, w);
+          for (int j = x.lo; ok && j < x.hi; ++j) {
+            if (!(ok = bounded_wait(bPfull + 8 * b, bph, w))) break;
+            if (!(ok = bounded_wait(bVfull + 8 * s, sph, w))) break;
+            tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            umma_ts<false>(tmem + C::COL_O, tmem + b * 128 + kk * 8,
-                           sdesc_sw128(sV + s * C::TILE + kk * 16 * 128, C::CHUNK, 1024), kIdesc,
-                           (j > x.lo || kk > 0) ? 1u : 0u);
-          tc_commit(bVempty + 8 * s);
-          tc_commit(bOdone + 8 * b);
-          if (++b == C::NS) b = 0, bph ^= 1;
-          if (++s == C::ST) s = 0, sph ^= 1;
+            for (int kk = 0; kk < 8; ++kk)
+              umma_ts<false>(tmem + C::COL_O, tmem + b * 128 + kk * 8,
+                             sdesc_sw128(sV + s * C::TILE + kk * 16 * 128, C::CHUNK, 1024), kIdesc,
+                             (j > x.lo || kk > 0) ? 1u : 0u);
+            tc_commit(bVempty + 8 * s);
+            tc_commit(bOdone + 8 * b);
+            if (++b == C::NS) b = 0, bph ^= 1;
+            if (++s == C::ST) s = 0, sph ^= 1;
+          }
         }
+        ok = __shfl_sync(~0u, ok, 0);
       }
-      tc_commit(bFin + 8);
-      bounded_wait(bFin + 8, 0, w, false);
+      if (lane == 0) {
+        tc_commit(bFin + 8);
+        bounded_wait(bFin + 8, 0, w, false);
+      }
     }
     __syncwarp();
   } else if (warp >= 4) {
     setmaxnreg_dec<kRegExpand>();
     // ------------------------------------------------ codes -> fp16 rows
     w.role = kStatusProducer;
-    const int r = threadIdx.x - 128;  // token of the tile
-    uint4 kc[D / 32], vc[D / 32];
-    uint2 ks = {}, vs = {};
-    auto load = [&](uint4 (&c)[D / 32], uint2 &f, const uint8_t *codes, const uint8_t *scales,
-                    long long row) {
+    const bool is_v = warp >= 8;
+    const int r = threadIdx.x & 127;  // token of the tile
+    const uint8_t *codes = is_v ? p.c.v_codes : p.c.k_codes;
+    const uint8_t *scales = is_v ? p.c.v_scales : p.c.k_scales;
+    uint8_t *tiles = smem + (is_v ? C::OFF_V : C::OFF_K);
+    const uint32_t full = is_v ? bVfull : bKfull, empty = is_v ? bVempty : bKempty;
+    struct Row {
+      uint4 c[D / 32];
+      uint2 f;
+      bool valid;
+    };
+    auto load = [&](Row &x, long long row) {
+      x.valid = row >= 0;
       if (row < 0) return;
       const uint4 *src = reinterpret_cast<const uint4 *>(codes + row * (D / 2));
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) c[i] = __ldg(src + i);
+      for (int i = 0; i < D / 32; ++i) x.c[i] = __ldg(src + i);
       if constexpr (D == 128)
-        f = __ldg(reinterpret_cast<const uint2 *>(scales + row * (D / 16)));
+        x.f = __ldg(reinterpret_cast<const uint2 *>(scales + row * (D / 16)));
       else
-        f.x = __ldg(reinterpret_cast<const uint32_t *>(scales + row * (D / 16)));
+        x.f.x = __ldg(reinterpret_cast<const uint32_t *>(scales + row * (D / 16)));
     };
     // One row as NCH chunks of eight 16-byte units, unit u of chunk n at
     // u ^ (r & 7): 32 code bits make a unit, two units share a scale.
-    auto expand = [&](const uint4 (&c)[D / 32], const uint2 &f, uint8_t *tile, bool valid) {
+    auto expand = [&](const Row &x, uint8_t *tile) {
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
-        const uint32_t pair = (i < 2 ? f.x : f.y) >> ((i & 1) * 16);
-        const uint32_t two = valid ? e4m3x2_f16x2(pair) : 0u;  // 0 * code = 0
+        const uint32_t pair = (i < 2 ? x.f.x : x.f.y) >> ((i & 1) * 16);
+        const uint32_t two = x.valid ? e4m3x2_f16x2(pair) : 0u;  // 0 * code = 0
         const uint32_t sc[2] = {__byte_perm(two, 0, 0x1010), __byte_perm(two, 0, 0x3232)};
-        const uint32_t wd[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+        const uint32_t wd[4] = {x.c[i].x, x.c[i].y, x.c[i].z, x.c[i].w};
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
           const int unit = 4 * i + y;  // of the row
@@ -346,83 +386,64 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     };
-    // The cursor runs over the steps of all parts; `id` is its page, loaded
-    // one step before it is used.
+    // The cursor runs over the steps of all parts; it is three steps ahead of
+    // the one that is written: its page `id` is on its way while the codes of
+    // the two steps before it are.
     Part x;
-    bool have = walk.next(p, ctl, x);
+    bool have = next_part(p, ctl, walk, x);
     int j = have ? x.lo : 0, id = -1, off = 0, head = 0;
     const int bs = 1 << p.c.bs_log2;
-    auto lookup = [&]() {
+    auto lookup = [&]() {  // the cursor's page, then one step on; whether there was a step
+      const bool was = have;
       const int t = j * 128 + r;
       id = have && t < x.s.nk
-               ? p.table[static_cast<long long>(x.b) * p.width + (t >> p.c.bs_log2)]
+               ? __ldg(p.table + static_cast<long long>(x.b) * p.width + (t >> p.c.bs_log2))
                : -1;
       off = t & (bs - 1);
       head = x.h;
-    };
-    auto advance = [&]() {
       if (have && ++j >= x.hi) {
-        have = walk.next(p, ctl, x);
+        have = next_part(p, ctl, walk, x);
         j = x.lo;
       }
+      return was;
     };
     auto row_of = [&]() -> long long {
       if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.c.num_blocks)) return -1;
       return ((static_cast<long long>(id) * p.c.Hk + head) << p.c.bs_log2) + off;
     };
-    // rows of steps s, s - 1, s - 2 and s + 1 (k_next); steps known to exist
-    long long row_k = -1, row_1 = -1, row_2 = -1;
-    bool more = have;  // step s exists
-    lookup();
-    row_k = row_of();
-    load(kc, ks, p.c.k_codes, p.c.k_scales, row_k);
-    advance();
-    bool more_next = have;
-    lookup();
-    bool ok = true;
-    int st = 0, ph = 0, vst = 0, vph = 0;
-    int left = 0;  // V steps not yet written
-    for (int s = 0; ok && (more || left > 0); ++s) {
-      long long row_next = -1;
-      if (more) {
-        ok = __all_sync(~0u, s < C::ST || bounded_wait(bKempty + 8 * st, ph ^ 1, w));
-        if (!ok) break;
-        const unsigned bits = __ballot_sync(~0u, row_k >= 0);
+    Row x0, x1;
+    bool m0 = lookup();
+    load(x0, row_of());
+    bool m1 = lookup();
+    load(x1, row_of());
+    bool m2 = lookup();
+    int st = 0, ph = 0, step = 0;
+    // writes the step in `now`, then loads the step whose page is at hand into it
+    auto turn = [&](Row &now) -> bool {
+      if (is_v && ctl.skip_load && step == 0) {  // test hook: the P V issuer's wait runs out
+        if (r == 0) atomicOr(ctl.status, kStatusInjected);
+        return false;
+      }
+      if (!__all_sync(~0u, step < C::ST || bounded_wait(empty + 8 * st, ph ^ 1, w))) return false;
+      if (!is_v) {
+        const unsigned bits = __ballot_sync(~0u, now.valid);
         if (lane == 0)
-          reinterpret_cast<unsigned *>(smem + C::OFF_MASK)[(s % C::MASKS) * 4 + warp - 4] = bits;
-        expand(kc, ks, smem + C::OFF_K + st * C::TILE, row_k >= 0);
-        fence_proxy_async_smem();
-        mbar_arrive(bKfull + 8 * st);
-        if (++st == C::ST) st = 0, ph ^= 1;
-        ++left;
-        if (more_next) {  // the next step's codes, and the page of the one after it
-          row_next = row_of();
-          load(kc, ks, p.c.k_codes, p.c.k_scales, row_next);
-          advance();
-          lookup();
-        }
+          reinterpret_cast<unsigned *>(smem + C::OFF_MASK)[(step % C::MASKS) * 4 + warp - 4] = bits;
       }
-      if (s >= 2) {  // V of step s - 2, loaded a step ago
-        const int n = s - 2;
-        if (ctl.skip_load && n == 0) {  // test hook: the P V issuer's wait runs out
-          if (r == 0) atomicOr(ctl.status, kStatusInjected);
-          ok = false;
-          break;
-        }
-        ok = __all_sync(~0u, n < C::ST || bounded_wait(bVempty + 8 * vst, vph ^ 1, w));
-        if (!ok) break;
-        expand(vc, vs, smem + C::OFF_V + vst * C::TILE, row_2 >= 0);
-        fence_proxy_async_smem();
-        mbar_arrive(bVfull + 8 * vst);
-        if (++vst == C::ST) vst = 0, vph ^= 1;
-        --left;
-      }
-      if (s >= 1 && left > 0) load(vc, vs, p.c.v_codes, p.c.v_scales, row_1);
-      row_2 = row_1;
-      row_1 = row_k;
-      row_k = row_next;
-      more = more && more_next;
-      more_next = more && have;
+      expand(now, tiles + st * C::TILE);
+      fence_proxy_async_smem();
+      mbar_arrive(full + 8 * st);
+      if (++st == C::ST) st = 0, ph ^= 1;
+      ++step;
+      if (m2) load(now, row_of());
+      m0 = m1;
+      m1 = m2;
+      m2 = m2 && lookup();
+      return true;
+    };
+    while (m0) {
+      if (!turn(x0) || !m0) break;
+      if (!turn(x1)) break;
     }
   } else {
     setmaxnreg_inc<kRegSoftmax>();
@@ -472,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Share share = {-1, 0, 0, 1};
     bool ok = true;
     Part x, nx;
-    bool have = walk.next(p, ctl, x);
+    bool have = next_part(p, ctl, walk, x);
     float factor = stage_q(x);
     int buf = 0, bph = 0, pbuf = C::NS - 1, pbph = 1, step = 0;
     for (int g = 0; have; ++g) {
@@ -600,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++buf == C::NS) buf = 0, bph ^= 1;
       }
       // the next tile's Q goes in while this one's last products run
-      const bool have_next = walk.next(p, ctl, nx);
+      const bool have_next = next_part(p, ctl, walk, nx);
       if (ok && have_next) {
         ok = __all_sync(~0u, bounded_wait(bQempty, g & 1, w));
         if (ok) factor = stage_q(nx);
@@ -660,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == 12) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
