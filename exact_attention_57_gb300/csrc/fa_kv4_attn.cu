@@ -27,7 +27,9 @@
 // Work is dealt in units of 128 tokens (16 for each of the 8 warps) of one
 // sequence and key head, in one line over all of them, equal shares to the
 // CTAs of one resident wave: ragged lengths and few long sequences balance
-// alike.  A CTA's first and last sequence may be shared with its neighbours;
+// alike.  A sequence and key head begins with kLead units that stand for what
+// it costs beside its keys (its queries, the pipeline's start, the warps'
+// meeting).  A CTA's first and last sequence may be shared with its neighbours;
 // such parts go to the workspace (two a CTA, whatever the lengths), and a
 // second kernel joins them.
 #include <atomic>
@@ -74,12 +76,14 @@ __device__ __forceinline__ void load_words(uint32_t (&x)[W], const uint8_t *p) {
     asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(x[0]) : "l"(p));
 }
 
-// Units of one key head of a sequence; a sequence without keys still has one
-// (its rows get their zeros), one with more than `rows` rows none (the
-// kernel for many queries takes it).
+constexpr int kLead = 3;
+
+// Units of one key head of a sequence, kLead of them ahead of its keys; a
+// sequence without keys still has one more (its rows get their zeros), one
+// with more than `rows` rows none (the kernel for many queries takes it).
 __device__ __forceinline__ int units_of(const Seq &s, int group, int rows) {
   if (s.nq == 0 || static_cast<long long>(s.nq) * group > rows) return 0;
-  return max(1, (s.nk + kUnit - 1) / kUnit);
+  return kLead + max(1, (s.nk + kUnit - 1) / kUnit);
 }
 
 // 16 tokens of one page as lane (r, c) holds them.
@@ -144,8 +148,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
       n_units = units_of(sq, p.group, R);
       h = 0;
     }
-    const int t_lo = unit;
-    const int t_hi = static_cast<int>(min(static_cast<long long>(n_units), t_lo + (u1 - u)));
+    // units [t_lo, t_hi) of the n_units - kLead with keys
+    const int unit_hi = static_cast<int>(min(static_cast<long long>(n_units), unit + (u1 - u)));
+    const int t_lo = max(unit - kLead, 0), t_hi = max(unit_hi - kLead, 0);
+    u += unit_hi - unit;
+    unit = 0;
+    if (t_lo == t_hi) break;  // only the lead fell to this CTA: its share is done
     const int rows = sq.nq * p.group;
 
     // Q fragments: lane (r, c) holds D / 4 elements of row nt * 8 + r
@@ -392,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
         }
       }
     __syncthreads();
-    const bool begins = t_lo == 0, ends = t_hi == n_units, whole = begins && ends;
+    const bool begins = t_lo == 0, ends = t_hi == n_units - kLead, whole = begins && ends;
     if (begins && !ends) share.b = b, share.h = h;
     if (!begins) share.head_ends = ends;
     for (int x = tid; x < R * (D / 4); x += kThreads) {
@@ -430,8 +438,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
       }
     }
     __syncthreads();
-    u += t_hi - t_lo;
-    unit = 0;
     if (++h == p.c.Hk) n_units = 0;
   }
   if (tid == 0) reinterpret_cast<Share *>(ws)[blockIdx.x] = share;

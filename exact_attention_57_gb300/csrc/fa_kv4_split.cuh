@@ -154,25 +154,38 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
   for (int y = 0; y < kJoinRows; ++y)
     for (int o = 16; o; o /= 2) mm[y] = fmaxf(mm[y], __shfl_xor_sync(~0u, mm[y], o));
+  // two parts at a time, all their loads ahead of the sums (rows behind the
+  // tile's last repeat it: nothing of them is written)
   float sum[kJoinRows][W] = {};
-#pragma unroll 2
-  for (int n = first + warp; n <= last; n += kWarps) {
-    const float *src = part(n);
+  constexpr int AT = 2;
+  for (int n = first + warp; n <= last; n += AT * kWarps) {
+    float2 ml[AT][kJoinRows];
+    float v[AT][kJoinRows][W];
 #pragma unroll
-    for (int y = 0; y < kJoinRows; ++y) {
-      if (row0 + y >= rows) continue;
-      const float2 ml = reinterpret_cast<const float2 *>(src + R * D)[row0 + y];
-      const float f = mm[y] == -INFINITY ? 0.f : ex2_approx(ml.x - mm[y]);
-      ll[y] += f * ml.y;
-      float v[W];
-      if constexpr (W == 4)
-        *reinterpret_cast<float4 *>(v) =
-            *reinterpret_cast<const float4 *>(src + (row0 + y) * D + lane * 4);
-      else
-        *reinterpret_cast<float2 *>(v) =
-            *reinterpret_cast<const float2 *>(src + (row0 + y) * D + lane * 2);
+    for (int x = 0; x < AT; ++x) {
+      const float *src = part(min(n + x * kWarps, last));
 #pragma unroll
-      for (int x = 0; x < W; ++x) sum[y][x] += f * v[x];
+      for (int y = 0; y < kJoinRows; ++y) {
+        const int row = min(row0 + y, rows - 1);
+        ml[x][y] = reinterpret_cast<const float2 *>(src + R * D)[row];
+        if constexpr (W == 4)
+          *reinterpret_cast<float4 *>(v[x][y]) =
+              *reinterpret_cast<const float4 *>(src + row * D + lane * 4);
+        else
+          *reinterpret_cast<float2 *>(v[x][y]) =
+              *reinterpret_cast<const float2 *>(src + row * D + lane * 2);
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < AT; ++x) {
+      if (n + x * kWarps > last) break;
+#pragma unroll
+      for (int y = 0; y < kJoinRows; ++y) {
+        const float f = mm[y] == -INFINITY ? 0.f : ex2_approx(ml[x][y].x - mm[y]);
+        ll[y] += f * ml[x][y].y;
+#pragma unroll
+        for (int z = 0; z < W; ++z) sum[y][z] += f * v[x][y][z];
+      }
     }
   }
   __shared__ float s_l[kWarps][kJoinRows];
