@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
         return static_cast<long long>(units_of(load_seq(p, b), p.group, R)) * p.c.Hk;
       },
       blockIdx.x, &den, &u, s_sums, s_warp);
-  Share share = {-1, 0, 0, 1};
+  Share share = {0, 0, 0, 0};
   if (static_cast<int>(blockIdx.x) >= den) {
     if (tid == 0) reinterpret_cast<Share *>(ws)[blockIdx.x] = share;
     return;
@@ -151,6 +151,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
     // units [t_lo, t_hi) of the n_units - kLead with keys
     const int unit_hi = static_cast<int>(min(static_cast<long long>(n_units), unit + (u1 - u)));
     const int t_lo = max(unit - kLead, 0), t_hi = max(unit_hi - kLead, 0);
+    // the CTA with the last of them
+    const int last = cta_of(u - unit + n_units - 1, at.total, den);
     u += unit_hi - unit;
     unit = 0;
     if (t_lo == t_hi) break;  // only the lead fell to this CTA: its share is done
@@ -401,8 +403,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
       }
     __syncthreads();
     const bool begins = t_lo == 0, ends = t_hi == n_units - kLead, whole = begins && ends;
-    if (begins && !ends) share.b = b, share.h = h;
-    if (!begins) share.head_ends = ends;
+    if (begins && !ends) share = Share{sq.r0, h, rows, last};
     for (int x = tid; x < R * (D / 4); x += kThreads) {
       const int row = x / (D / 4), col = (x - row * (D / 4)) * 4;
       if (row >= rows) break;
@@ -471,8 +472,7 @@ cudaError_t launch(const Kv4Attn &p, float *ws, int num_sms, cudaStream_t s) {
   cfg.gridDim = dim3(static_cast<unsigned>(ctas - 1),
                      static_cast<unsigned>((min(rows, NT * 8LL) + kJoinRows - 1) / kJoinRows));
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, fa_kv4_join_kernel<T, D, NT * 8>, p, ws,
-                            static_cast<int>(ctas), p.max_q);
+  return cudaLaunchKernelEx(&cfg, fa_kv4_join_kernel<T, D, NT * 8>, p, ws);
 }
 
 template <typename T, int D>

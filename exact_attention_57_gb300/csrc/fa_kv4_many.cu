@@ -50,7 +50,7 @@ struct ManyCtl {
   int skip_load, tile_rows, tokens;  // tokens of a tile
 };
 
-constexpr int WALK_BYTES = 96;
+constexpr int WALK_BYTES = 104;
 
 template <int D>
 struct ManyCfg {
@@ -133,14 +133,16 @@ __device__ long long units_before(const Kv4Attn &p, const ManyCtl &c, const Seq 
 // inner loops.
 struct Part {
   int b, h, qt, lo, hi, units;  // steps [lo, hi) of `units`
+  int last;                     // the CTA with the tile's last step
   Seq s;
 };
 struct Walk {
-  long long u, u1;
+  long long u, u1, total;  // units of all CTAs
+  int den;                 // CTAs that share them
   int b, h, qt, unit, n;  // n tiles of sequence b
   Seq s;
   Part part;
-  int more, pad;
+  int more;
 };
 static_assert(sizeof(Walk) == WALK_BYTES, "the layout of shared memory counts on it");
 
@@ -162,7 +164,8 @@ __device__ __forceinline__ bool next_part(const Kv4Attn &p, const ManyCtl &c, Wa
       }
       const int units = tile_units(p, c, k->s, k->qt, k->n);
       const int hi = static_cast<int>(min(static_cast<long long>(units), k->unit + (k->u1 - k->u)));
-      k->part = Part{k->b, k->h, k->qt, k->unit, hi, units, k->s};
+      k->part = Part{k->b, k->h, k->qt, k->unit, hi, units, 0, k->s};
+      if (k->unit == 0 && hi < units) k->part.last = cta_of(k->u + units - 1, k->total, k->den);
       k->u += hi - k->unit;
       k->unit = 0;
       ++k->qt;
@@ -232,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       },
       blockIdx.x, &den, &u0, s_sums, s_warp);
   if (static_cast<int>(blockIdx.x) >= den) {
-    if (threadIdx.x == 0) reinterpret_cast<Share *>(ws)[blockIdx.x] = Share{-1, 0, 0, 1};
+    if (threadIdx.x == 0) reinterpret_cast<Share *>(ws)[blockIdx.x] = Share{0, 0, 0, 0};
     return;
   }
   Walk *walk = reinterpret_cast<Walk *>(smem + C::OFF_WALK) + warp;
@@ -240,6 +243,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     Walk k = {};
     k.u = u0;
     k.u1 = at.total * (blockIdx.x + 1) / den;
+    k.total = at.total;
+    k.den = den;
     k.b = at.b;
     k.s = load_seq(p, at.b);
     k.n = tiles_of(p, ctl, k.s);
@@ -490,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(bQfull);
       return mag * pow2(e);
     };
-    Share share = {-1, 0, 0, 1};
+    Share share = {0, 0, 0, 0};
     bool ok = true;
     Part x, nx;
     bool have = next_part(p, ctl, walk, x);
@@ -630,8 +635,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) {
         tc_fence_after();
         const bool begins = x.lo == 0, ends = x.hi == x.units;
-        if (begins && !ends) share.b = x.b, share.h = x.h, share.qt = x.qt;
-        if (!begins) share.head_ends = ends;
+        if (begins && !ends)
+          share = Share{x.s.r0 + x.qt * ctl.tokens, x.h,
+                        min(x.s.nq - x.qt * ctl.tokens, ctl.tokens) * p.group, x.last};
         const bool whole = begins && ends;
         const float inv = l > 0.f ? p.v_mul / l : 0.f;
         const int head = x.h * p.group + tj;
@@ -714,7 +720,7 @@ cudaError_t launch(const Kv4Attn &p, const ManyCtl &ctl, float *ws, int num_sms,
   cfg.gridDim = dim3(static_cast<unsigned>(ctas - 1), R / kJoinRows);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, fa_kv4_join_kernel<T, D, R>, p, ws, ctas, ctl.tokens);
+  return cudaLaunchKernelEx(&cfg, fa_kv4_join_kernel<T, D, R>, p, ws);
 }
 
 }  // namespace

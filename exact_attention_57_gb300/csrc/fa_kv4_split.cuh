@@ -26,13 +26,20 @@ __device__ __forceinline__ Seq load_seq(const Kv4Attn &p, int b) {
   return s;
 }
 
-// What a CTA says to the joining kernel, at the workspace's start: the tile
-// (sequence, key head, query tile) whose first part, but not last, is its own
-// (b = -1: none), and whether the one it found begun ends within it.
+// What a CTA says to the joining kernel, at the workspace's start, about the
+// tile (sequence, key head, query tile) whose first part, but not last, is its
+// own: the tile's first query row, key head and rows (0: there is no such
+// tile), and the CTA with its last part.
 struct Share {
-  int b, h, qt, head_ends;
+  int row0, h, rows, last;
 };
 static_assert(sizeof(Share) == 16, "one 16-byte load");
+
+// The CTA whose share of `total` units, dealt to `den` CTAs, holds unit u.
+__device__ __forceinline__ int cta_of(long long u, long long total, int den) {
+  // the last n with floor(total * n / den) <= u
+  return static_cast<int>(((u + 1) * den - 1) / total);
+}
 
 // Part `which` (0: of a tile begun before the CTA, 1: of one it begins) of
 // CTA n: rows of D sums, then (maximum, sum of weights) a row.
@@ -58,6 +65,21 @@ __device__ Place find_unit(const Kv4Attn &p, F units, int num, int *den, long lo
   constexpr int kThreads = kWarps * 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   Place at = {0, 0, 0};
+  if (p.B <= 32) {  // one a lane: every warp finds it by itself
+    const long long n = lane < p.B ? units(lane) : 0;
+    long long incl = n;
+    for (int o = 1; o < 32; o *= 2) {
+      const long long x = __shfl_up_sync(~0u, incl, o);
+      if (lane >= o) incl += x;
+    }
+    at.total = __shfl_sync(~0u, incl, 31);
+    *den = static_cast<int>(min(static_cast<long long>(*den), at.total));
+    if (num >= *den) return at;  // more CTAs than units
+    *target = at.total * num / *den;
+    at.b = 31 - __clz(__ballot_sync(~0u, incl - n <= *target));
+    at.before = __shfl_sync(~0u, incl - n, at.b);
+    return at;
+  }
   // total first, where one round of requests does not show it
   if (p.B > kThreads) {
     long long n = 0;
@@ -106,67 +128,42 @@ __device__ Place find_unit(const Kv4Attn &p, F units, int num, int *den, long lo
   }
 }
 
-// Joins the parts of the tiles that more than one CTA shared: CTA n takes
-// what CTA n of the grid above began and others went on with (n's part 1, then
-// the parts 0 of n + 1, n + 2, ... up to the one that ends it), four rows of
-// it.  The eight warps share the parts, so that a tile split over the whole
-// grid costs a few rounds of loads.  Row r of query tile t is head r % group of
-// token t * tokens + r / group.
+// Joins the parts of the tiles that more than one CTA shared: CTA n takes what
+// CTA n of the grid above began and others went on with (n's part 1, then the
+// parts 0 of n + 1, n + 2, ... up to the one that ends it), four rows of it.
+// Row r of a tile is head r % group of its token r / group.  The eight warps
+// share the parts, each with a maximum of its own, so that a tile split over
+// the whole grid costs a few rounds of loads.
 constexpr int kJoinRows = 4;
 
 template <typename T, int D, int R>
-__global__ void __launch_bounds__(256)
-    fa_kv4_join_kernel(const Kv4Attn p, float *ws, int ctas, int tokens) {
+__global__ void __launch_bounds__(256) fa_kv4_join_kernel(const Kv4Attn p, float *ws) {
   constexpr int kWarps = 8;
   constexpr int W = D / 32;  // columns a lane
   __shared__ float s_sum[kWarps][kJoinRows][D];
+  __shared__ float s_m[kWarps][kJoinRows], s_l[kWarps][kJoinRows];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = blockIdx.x;
   const int row0 = blockIdx.y * kJoinRows;
   griddep_wait();
   griddep_launch_dependents();
-  const Share *shares = reinterpret_cast<const Share *>(ws);
-  const Share mine = shares[first];
-  if (mine.b < 0) return;
-  const Seq sq = load_seq(p, mine.b);
-  const int token0 = mine.qt * tokens;
-  const int rows = static_cast<int>(
-      min(static_cast<long long>(min(sq.nq - token0, tokens)) * p.group, static_cast<long long>(R)));
-  if (row0 >= rows) return;
-  int last = first + 1;  // the part that ends it
-  for (;; last += 32) {
-    const int n = last + lane;
-    const unsigned stop = __ballot_sync(~0u, n >= ctas - 1 || shares[n].head_ends != 0);
-    if (stop) {
-      last += __ffs(stop) - 1;
-      break;
-    }
-  }
-  auto part = [&](int n) { return part_of<D, R>(ws, n, n == first); };
-  float mm[kJoinRows], ll[kJoinRows];
-#pragma unroll
-  for (int y = 0; y < kJoinRows; ++y) mm[y] = -INFINITY, ll[y] = 0.f;
-  for (int n = first + lane; n <= last; n += 32) {
-    const float2 *ml = reinterpret_cast<const float2 *>(part(n) + R * D) + row0;
-#pragma unroll
-    for (int y = 0; y < kJoinRows; ++y)
-      if (row0 + y < rows) mm[y] = fmaxf(mm[y], ml[y].x);
-  }
-#pragma unroll
-  for (int y = 0; y < kJoinRows; ++y)
-    for (int o = 16; o; o /= 2) mm[y] = fmaxf(mm[y], __shfl_xor_sync(~0u, mm[y], o));
+  const Share mine = reinterpret_cast<const Share *>(ws)[first];
+  if (row0 >= mine.rows) return;
   // two parts at a time, all their loads ahead of the sums (rows behind the
   // tile's last repeat it: nothing of them is written)
-  float sum[kJoinRows][W] = {};
+  float mm[kJoinRows], ll[kJoinRows], sum[kJoinRows][W] = {};
+#pragma unroll
+  for (int y = 0; y < kJoinRows; ++y) mm[y] = -INFINITY, ll[y] = 0.f;
   constexpr int AT = 2;
-  for (int n = first + warp; n <= last; n += AT * kWarps) {
+  for (int n = first + warp; n <= mine.last; n += AT * kWarps) {
     float2 ml[AT][kJoinRows];
     float v[AT][kJoinRows][W];
 #pragma unroll
     for (int x = 0; x < AT; ++x) {
-      const float *src = part(min(n + x * kWarps, last));
+      const int from = min(n + x * kWarps, mine.last);
+      const float *src = part_of<D, R>(ws, from, from == first);
 #pragma unroll
       for (int y = 0; y < kJoinRows; ++y) {
-        const int row = min(row0 + y, rows - 1);
+        const int row = min(row0 + y, mine.rows - 1);
         ml[x][y] = reinterpret_cast<const float2 *>(src + R * D)[row];
         if constexpr (W == 4)
           *reinterpret_cast<float4 *>(v[x][y]) =
@@ -178,38 +175,40 @@ __global__ void __launch_bounds__(256)
     }
 #pragma unroll
     for (int x = 0; x < AT; ++x) {
-      if (n + x * kWarps > last) break;
+      if (n + x * kWarps > mine.last) break;
 #pragma unroll
       for (int y = 0; y < kJoinRows; ++y) {
-        const float f = mm[y] == -INFINITY ? 0.f : ex2_approx(ml[x][y].x - mm[y]);
-        ll[y] += f * ml[x][y].y;
+        const float to = fmaxf(mm[y], ml[x][y].x);
+        if (to == -INFINITY) continue;
+        const float f = ex2_approx(mm[y] - to), g = ex2_approx(ml[x][y].x - to);
+        mm[y] = to;
+        ll[y] = f * ll[y] + g * ml[x][y].y;
 #pragma unroll
-        for (int z = 0; z < W; ++z) sum[y][z] += f * v[x][y][z];
+        for (int z = 0; z < W; ++z) sum[y][z] = f * sum[y][z] + g * v[x][y][z];
       }
     }
   }
-  __shared__ float s_l[kWarps][kJoinRows];
 #pragma unroll
   for (int y = 0; y < kJoinRows; ++y) {
 #pragma unroll
     for (int x = 0; x < W; ++x) s_sum[warp][y][lane * W + x] = sum[y][x];
-    if (lane == 0) s_l[warp][y] = ll[y];
+    if (lane == 0) s_m[warp][y] = mm[y], s_l[warp][y] = ll[y];
   }
   __syncthreads();
-  if (warp >= kJoinRows || row0 + warp >= rows) return;
-  float l = 0.f, total[W] = {};
+  if (warp >= kJoinRows || row0 + warp >= mine.rows) return;
+  float m = -INFINITY, l = 0.f, total[W] = {};
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_m[w][warp]);
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    l += s_l[w][warp];
+    const float f = m == -INFINITY ? 0.f : ex2_approx(s_m[w][warp] - m);
+    l += f * s_l[w][warp];
 #pragma unroll
-    for (int x = 0; x < W; ++x) total[x] += s_sum[w][warp][lane * W + x];
+    for (int x = 0; x < W; ++x) total[x] += f * s_sum[w][warp][lane * W + x];
   }
-  float m = mm[0];
-#pragma unroll
-  for (int y = 1; y < kJoinRows; ++y) m = warp == y ? mm[y] : m;
-  const int row = row0 + warp, y = row / p.group, j = row - y * p.group, i = token0 + y;
+  const int row = row0 + warp, y = row / p.group, j = row - y * p.group, i = mine.row0 + y;
   const int head = mine.h * p.group + j;
-  T *out = static_cast<T *>(p.o) + (static_cast<long long>(sq.r0 + i) * p.Hq + head) * D + lane * W;
+  T *out = static_cast<T *>(p.o) + (static_cast<long long>(i) * p.Hq + head) * D + lane * W;
   const float inv = l > 0.f ? p.v_mul / l : 0.f;
   alignas(8) T e[W];
 #pragma unroll
@@ -219,7 +218,7 @@ __global__ void __launch_bounds__(256)
   else
     *reinterpret_cast<uint32_t *>(out) = *reinterpret_cast<const uint32_t *>(e);
   if (lane == 0)
-    p.lse[static_cast<long long>(head) * p.total_q + sq.r0 + i] =
+    p.lse[static_cast<long long>(head) * p.total_q + i] =
         l > 0.f ? m * 0.6931471805599453f + logf(l) : -INFINITY;
 }
 
