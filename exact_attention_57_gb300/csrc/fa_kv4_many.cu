@@ -8,18 +8,18 @@
 // fa_kv4_split.cuh, a unit being 128 keys of one tile: one CTA on each SM,
 // equal shares, whatever the lengths, the mask and the number of tiles.
 //
-// Warps 0-3    softmax, correction and epilogue, one row a thread; they also
-//              bring the row's Q into shared memory, as fp16 times a power of
-//              two, before the previous tile's epilogue.
+// Warps 0-3    softmax, correction and epilogue, one row a thread.
 // Warps 4-7    expand the codes of K, warps 8-11 those of V: thread r loads
 //              token r of the 128 (a page lookup, D / 2 bytes of codes, D / 16
-//              of scales, two steps ahead), turns them into fp16 (exact: six
+//              of scales, one step ahead), turns them into fp16 (exact: six
 //              significant bits) and writes them as a 128-byte-swizzled row.
 //              Tokens behind the sequence or on a missing page become zeros
 //              and are reported in a bit mask.
 // Warp 12, 13  issue S = Q K^T (three score buffers) and O += P V (P in tensor
 //              memory), kind::f16, fp32 accumulators; warp 12 owns the tensor
 //              memory.
+// Warp 14, 15  bring the next tile's Q into shared memory (two buffers), as
+//              fp16 times a power of two a row.
 //
 // The products of a 128 x 128 step need about 1000 cycles of the tensor pipe
 // and the softmax 850 of its warps; expanding the step's K and V costs 512
@@ -29,6 +29,7 @@
 // Every wait is bounded; on expiry the CTA raises its abort flag, records the
 // role in the status word, drains its products, frees tensor memory and ends.
 #include <atomic>
+#include <cfloat>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -50,7 +51,7 @@ struct ManyCtl {
   int skip_load, tile_rows, tokens;  // tokens of a tile
 };
 
-constexpr int WALK_BYTES = 104;
+constexpr int WALK_BYTES = 80;
 
 template <int D>
 struct ManyCfg {
@@ -58,21 +59,24 @@ struct ManyCfg {
   static constexpr int CHUNK = 128 * 128;
   static constexpr int TILE = NCH * CHUNK;
   static constexpr int NS = 3;                     // score buffers
-  static constexpr int ST = D == 128 ? 3 : 4;      // K and V stages
+  static constexpr int KST = D == 128 ? 3 : 4;     // K stages
+  static constexpr int VST = D == 128 ? 2 : 4;     // V stages
+  static constexpr int ST = KST > VST ? KST : VST;
   static constexpr int MASKS = 8;                  // tiles whose key masks are kept
   static constexpr uint32_t COL_O = NS * 128;
   static constexpr int OFF_Q = 0;
-  static constexpr int OFF_K = OFF_Q + TILE;
-  static constexpr int OFF_V = OFF_K + ST * TILE;
-  static constexpr int OFF_MASK = OFF_V + ST * TILE;
-  static constexpr int OFF_BAR = OFF_MASK + MASKS * 16;
-  // qfull, qempty, ofree, fin[2], kfull, kempty, vfull, vempty [ST], sfull,
-  // pfull, odone [NS]
-  static constexpr int NBAR = 5 + 4 * ST + 3 * NS;
-  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int OFF_K = OFF_Q + 2 * TILE;
+  static constexpr int OFF_V = OFF_K + KST * TILE;
+  static constexpr int OFF_MASK = OFF_V + VST * TILE;
+  static constexpr int OFF_QE = OFF_MASK + MASKS * 16;  // an exponent a row, two buffers
+  static constexpr int OFF_BAR = OFF_QE + 2 * 128;
+  // qfull[2], qempty[2], ofree, fin[2], kfull, kempty, vfull, vempty [ST],
+  // sfull, pfull, odone [NS]
+  static constexpr int NBAR = 7 + 4 * ST + 3 * NS;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;  // tmem base, abort flag, CTAs, -, units
   static constexpr int OFF_SUMS = OFF_K;           // before the first tile arrives
-  static constexpr int OFF_WALK = OFF_MISC + 16;     // a walk for each of 14 warps
-  static constexpr int SMEM = OFF_WALK + 14 * WALK_BYTES + 1024;
+  static constexpr int OFF_WALK = OFF_MISC + 24;     // a walk for each warp
+  static constexpr int SMEM = OFF_WALK + kWarps * WALK_BYTES + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
 };
 constexpr uint32_t kRegSoftmax = 216, kRegExpand = 104, kRegIssue = 88;
@@ -133,12 +137,10 @@ __device__ long long units_before(const Kv4Attn &p, const ManyCtl &c, const Seq 
 // inner loops.
 struct Part {
   int b, h, qt, lo, hi, units;  // steps [lo, hi) of `units`
-  int last;                     // the CTA with the tile's last step
   Seq s;
 };
 struct Walk {
-  long long u, u1, total;  // units of all CTAs
-  int den;                 // CTAs that share them
+  long long left;         // units of the share not yet walked
   int b, h, qt, unit, n;  // n tiles of sequence b
   Seq s;
   Part part;
@@ -150,12 +152,12 @@ static_assert(sizeof(Walk) == WALK_BYTES, "the layout of shared memory counts on
 __device__ __forceinline__ bool next_part(const Kv4Attn &p, const ManyCtl &c, Walk *k, Part &x) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) {
-    k->more = k->u < k->u1;
+    k->more = k->left > 0;
     if (k->more) {
       while (k->qt >= k->n) {
         if (k->n > 0 && k->h + 1 < p.c.Hk) {
           ++k->h;
-        } else {  // another sequence of this kernel follows, since u < the total
+        } else {  // another sequence of this kernel follows: units are left
           k->s = load_seq(p, ++k->b);
           k->n = tiles_of(p, c, k->s);
           k->h = 0;
@@ -163,10 +165,9 @@ __device__ __forceinline__ bool next_part(const Kv4Attn &p, const ManyCtl &c, Wa
         k->qt = 0;
       }
       const int units = tile_units(p, c, k->s, k->qt, k->n);
-      const int hi = static_cast<int>(min(static_cast<long long>(units), k->unit + (k->u1 - k->u)));
-      k->part = Part{k->b, k->h, k->qt, k->unit, hi, units, 0, k->s};
-      if (k->unit == 0 && hi < units) k->part.last = cta_of(k->u + units - 1, k->total, k->den);
-      k->u += hi - k->unit;
+      const int hi = static_cast<int>(min(static_cast<long long>(units), k->unit + k->left));
+      k->part = Part{k->b, k->h, k->qt, k->unit, hi, units, k->s};
+      k->left -= hi - k->unit;
       k->unit = 0;
       ++k->qt;
     }
@@ -186,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_u32(smem);
   const uint32_t sQ = sbase + C::OFF_Q, sK = sbase + C::OFF_K, sV = sbase + C::OFF_V;
-  const uint32_t bQfull = sbase + C::OFF_BAR, bQempty = bQfull + 8, bOfree = bQempty + 8;
+  const uint32_t bQfull = sbase + C::OFF_BAR, bQempty = bQfull + 16, bOfree = bQempty + 16;
   const uint32_t bFin = bOfree + 8;                // + 8 * issuer
   const uint32_t bKfull = bFin + 16, bKempty = bKfull + 8 * C::ST;
   const uint32_t bVfull = bKempty + 8 * C::ST, bVempty = bVfull + 8 * C::ST;
@@ -194,13 +195,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t bOdone = bPfull + 8 * C::NS;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
+  int *s_den = reinterpret_cast<int *>(smem + C::OFF_MISC + 8);
+  long long *s_total = reinterpret_cast<long long *>(smem + C::OFF_MISC + 16);
   long long *s_sums = reinterpret_cast<long long *>(smem + C::OFF_SUMS);
   auto s_warp = reinterpret_cast<long long (*)[kWarps]>(s_sums + kThreads);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    mbar_init(bQfull, 128);
-    mbar_init(bQempty, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bQfull + 8 * s, 64);
+      mbar_init(bQempty + 8 * s, 1);
+    }
     mbar_init(bOfree, 128);
     mbar_init(bFin, 1);
     mbar_init(bFin + 8, 1);
@@ -234,17 +239,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         return units_before(p, ctl, s, n, n) * p.c.Hk;
       },
       blockIdx.x, &den, &u0, s_sums, s_warp);
-  if (static_cast<int>(blockIdx.x) >= den) {
-    if (threadIdx.x == 0) reinterpret_cast<Share *>(ws)[blockIdx.x] = Share{0, 0, 0, 0};
-    return;
-  }
+  if (threadIdx.x == 0) reinterpret_cast<Share *>(ws)[blockIdx.x] = Share{0, 0, 0, 0};
+  if (static_cast<int>(blockIdx.x) >= den) return;
   Walk *walk = reinterpret_cast<Walk *>(smem + C::OFF_WALK) + warp;
-  if (warp < 14 && lane == 0) {
+  if (lane == 0) {
     Walk k = {};
-    k.u = u0;
-    k.u1 = at.total * (blockIdx.x + 1) / den;
-    k.total = at.total;
-    k.den = den;
+    k.left = at.total * (blockIdx.x + 1) / den - u0;
     k.b = at.b;
     k.s = load_seq(p, at.b);
     k.n = tiles_of(p, ctl, k.s);
@@ -261,6 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     k.qt = lo;
     k.unit = static_cast<int>(rest - units_before(p, ctl, k.s, lo, k.n));
     *walk = k;
+    if (warp == 0) *s_den = den, *s_total = at.total;
   }
   if (warp == 12) {
     tmem_alloc(smem_u32(tmem_slot), 512);
@@ -283,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Part x;
       for (int g = 0; ok && next_part(p, ctl, walk, x); ++g) {
         if (lane == 0) {
-          ok = bounded_wait(bQfull, g & 1, w);
+          ok = bounded_wait(bQfull + 8 * (g & 1), (g >> 1) & 1, w);
           for (int j = x.lo; ok && j < x.hi; ++j, ++issued) {
             // score buffer b last held P of three steps ago
             if (issued >= C::NS && !(ok = bounded_wait(bOdone + 8 * b, bph ^ 1, w))) break;
@@ -292,16 +293,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
               const uint32_t off = (kk >> 2) * C::CHUNK + (kk & 3) * 32;
-              umma_ss<false>(tmem + b * 128, sdesc_sw128(sQ + off, 16, 1024),
+              umma_ss<false>(tmem + b * 128, sdesc_sw128(sQ + (g & 1) * C::TILE + off, 16, 1024),
                              sdesc_sw128(sK + s * C::TILE + off, 16, 1024), kIdesc,
                              kk > 0 ? 1u : 0u);
             }
             tc_commit(bKempty + 8 * s);
             tc_commit(bSfull + 8 * b);
             if (++b == C::NS) b = 0, bph ^= 1;
-            if (++s == C::ST) s = 0, sph ^= 1;
+            if (++s == C::KST) s = 0, sph ^= 1;
           }
-          if (ok) tc_commit(bQempty);
+          if (ok) tc_commit(bQempty + 8 * (g & 1));
         }
         ok = __shfl_sync(~0u, ok, 0);
       }
@@ -331,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_commit(bVempty + 8 * s);
             tc_commit(bOdone + 8 * b);
             if (++b == C::NS) b = 0, bph ^= 1;
-            if (++s == C::ST) s = 0, sph ^= 1;
+            if (++s == C::VST) s = 0, sph ^= 1;
           }
         }
         ok = __shfl_sync(~0u, ok, 0);
@@ -339,6 +340,52 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         tc_commit(bFin + 8);
         bounded_wait(bFin + 8, 0, w, false);
+      }
+    } else {
+      // ---------------------------------------------- Q rows
+      w.role = kStatusProducer;
+      // the sign of the scale goes into Q, a zero scale makes Q zero
+      const float sign = p.scale_log2 == 0.f ? 0.f : p.scale_log2 < 0.f ? -1.f : 1.f;
+      Part x;
+      for (int g = 0; next_part(p, ctl, walk, x); ++g) {
+        if (!__all_sync(~0u, g < 2 || bounded_wait(bQempty + 8 * (g & 1), ((g >> 1) - 1) & 1, w)))
+          break;
+        uint8_t *tile = smem + C::OFF_Q + (g & 1) * C::TILE;
+#pragma unroll 1
+        for (int n = 0; n < 2; ++n) {
+          const int r = (threadIdx.x & 63) + 64 * n;
+          const int ti = r / p.group, tj = r - ti * p.group, i = x.qt * ctl.tokens + ti;
+          const bool in = ti < ctl.tokens && i < x.s.nq;
+          float amax = 0.f;
+          const uint4 *src = reinterpret_cast<const uint4 *>(
+              static_cast<const T *>(p.q) +
+              (in ? (static_cast<long long>(x.s.r0 + i) * p.Hq + x.h * p.group + tj) * D : 0));
+#pragma unroll 4
+          for (int u = 0; u < D / 8; ++u) {
+            const uint4 q = in ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
+            const T *f = reinterpret_cast<const T *>(&q);
+#pragma unroll
+            for (int y = 0; y < 8; ++y) amax = fmaxf(amax, fabsf(static_cast<float>(f[y])));
+          }
+          // 2^e brings the row's largest element to 1 .. 2 (an exact scaling)
+          const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -126), 126);
+          const float mul = pow2(-e) * sign;
+#pragma unroll 4
+          for (int u = 0; u < D / 8; ++u) {
+            const uint4 q = in ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
+            const T *f = reinterpret_cast<const T *>(&q);
+            uint4 v;
+            v.x = pack_f16x2(static_cast<float>(f[0]) * mul, static_cast<float>(f[1]) * mul);
+            v.y = pack_f16x2(static_cast<float>(f[2]) * mul, static_cast<float>(f[3]) * mul);
+            v.z = pack_f16x2(static_cast<float>(f[4]) * mul, static_cast<float>(f[5]) * mul);
+            v.w = pack_f16x2(static_cast<float>(f[6]) * mul, static_cast<float>(f[7]) * mul);
+            *reinterpret_cast<uint4 *>(tile + (u >> 3) * C::CHUNK + r * 128 +
+                                       (((u & 7) ^ (r & 7)) << 4)) = v;
+          }
+          reinterpret_cast<int8_t *>(smem + C::OFF_QE)[(g & 1) * 128 + r] = static_cast<int8_t>(e);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(bQfull + 8 * (g & 1));
       }
     }
     __syncwarp();
@@ -355,10 +402,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     struct Row {
       uint4 c[D / 32];
       uint2 f;
-      bool valid;
+      bool valid, past;  // past: behind the sequence
     };
+    bool past = false;
     auto load = [&](Row &x, long long row) {
       x.valid = row >= 0;
+      x.past = past;
       if (row < 0) return;
       const uint4 *src = reinterpret_cast<const uint4 *>(codes + row * (D / 2));
 #pragma unroll
@@ -391,9 +440,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     };
-    // The cursor runs over the steps of all parts; it is three steps ahead of
-    // the one that is written: its page `id` is on its way while the codes of
-    // the two steps before it are.
+    // The cursor runs over the steps of all parts, two ahead of the one that
+    // is written: its page is on its way while the step before it is loaded.
     Part x;
     bool have = next_part(p, ctl, walk, x);
     int j = have ? x.lo : 0, id = -1, off = 0, head = 0;
@@ -401,7 +449,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto lookup = [&]() {  // the cursor's page, then one step on; whether there was a step
       const bool was = have;
       const int t = j * 128 + r;
-      id = have && t < x.s.nk
+      past = t >= x.s.nk;
+      id = have && !past
                ? __ldg(p.table + static_cast<long long>(x.b) * p.width + (t >> p.c.bs_log2))
                : -1;
       off = t & (bs - 1);
@@ -416,39 +465,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.c.num_blocks)) return -1;
       return ((static_cast<long long>(id) * p.c.Hk + head) << p.c.bs_log2) + off;
     };
-    Row x0, x1;
-    bool m0 = lookup();
-    load(x0, row_of());
-    bool m1 = lookup();
-    load(x1, row_of());
-    bool m2 = lookup();
-    int st = 0, ph = 0, step = 0;
-    // writes the step in `now`, then loads the step whose page is at hand into it
-    auto turn = [&](Row &now) -> bool {
+    const int stages = is_v ? C::VST : C::KST;
+    Row row;
+    bool now = lookup();
+    load(row, row_of());
+    bool next = lookup();
+    for (int step = 0, st = 0, ph = 0; now; ++step) {
       if (is_v && ctl.skip_load && step == 0) {  // test hook: the P V issuer's wait runs out
         if (r == 0) atomicOr(ctl.status, kStatusInjected);
-        return false;
+        break;
       }
-      if (!__all_sync(~0u, step < C::ST || bounded_wait(empty + 8 * st, ph ^ 1, w))) return false;
+      if (!__all_sync(~0u, step < stages || bounded_wait(empty + 8 * st, ph ^ 1, w))) break;
       if (!is_v) {
-        const unsigned bits = __ballot_sync(~0u, now.valid);
+        const unsigned bits = __ballot_sync(~0u, row.valid || row.past);
         if (lane == 0)
           reinterpret_cast<unsigned *>(smem + C::OFF_MASK)[(step % C::MASKS) * 4 + warp - 4] = bits;
       }
-      expand(now, tiles + st * C::TILE);
+      expand(row, tiles + st * C::TILE);
       fence_proxy_async_smem();
       mbar_arrive(full + 8 * st);
-      if (++st == C::ST) st = 0, ph ^= 1;
-      ++step;
-      if (m2) load(now, row_of());
-      m0 = m1;
-      m1 = m2;
-      m2 = m2 && lookup();
-      return true;
-    };
-    while (m0) {
-      if (!turn(x0) || !m0) break;
-      if (!turn(x1)) break;
+      if (++st == stages) st = 0, ph ^= 1;
+      if (next) load(row, row_of());
+      now = next;
+      next = next && lookup();
     }
   } else {
     setmaxnreg_inc<kRegSoftmax>();
@@ -457,86 +496,57 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = threadIdx.x;
     const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
     const uint32_t o_tm = tmem + lane_off + C::COL_O;
-    const float mag = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
-    // the sign of the scale goes into Q, a zero scale makes Q zero
-    const float sign = p.scale_log2 == 0.f ? 0.f : p.scale_log2 < 0.f ? -1.f : 1.f;
     const int ti = r / p.group, tj = r - ti * p.group;  // token of the tile, head of the group
-    // This thread's Q row of part x into shared memory as fp16, times 2^-e
-    // that brings its largest element to 1 .. 2; the factor for its scores.
-    auto stage_q = [&](const Part &x) -> float {
-      const int i = x.qt * ctl.tokens + ti;
-      const bool in = ti < ctl.tokens && i < x.s.nq;
-      uint4 q[D / 8];
-      float amax = 0.f;
-      const uint4 *src = reinterpret_cast<const uint4 *>(
-          static_cast<const T *>(p.q) +
-          (in ? (static_cast<long long>(x.s.r0 + i) * p.Hq + x.h * p.group + tj) * D : 0));
-#pragma unroll
-      for (int u = 0; u < D / 8; ++u) {
-        q[u] = in ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
-        const T *e = reinterpret_cast<const T *>(&q[u]);
-#pragma unroll
-        for (int y = 0; y < 8; ++y) amax = fmaxf(amax, fabsf(static_cast<float>(e[y])));
-      }
-      const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -126), 126);
-      const float mul = pow2(-e) * sign;
-#pragma unroll
-      for (int u = 0; u < D / 8; ++u) {
-        const T *f = reinterpret_cast<const T *>(&q[u]);
-        uint4 v;
-        v.x = pack_f16x2(static_cast<float>(f[0]) * mul, static_cast<float>(f[1]) * mul);
-        v.y = pack_f16x2(static_cast<float>(f[2]) * mul, static_cast<float>(f[3]) * mul);
-        v.z = pack_f16x2(static_cast<float>(f[4]) * mul, static_cast<float>(f[5]) * mul);
-        v.w = pack_f16x2(static_cast<float>(f[6]) * mul, static_cast<float>(f[7]) * mul);
-        *reinterpret_cast<uint4 *>(smem + C::OFF_Q + (u >> 3) * C::CHUNK + r * 128 +
-                                   (((u & 7) ^ (r & 7)) << 4)) = v;
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(bQfull);
-      return mag * pow2(e);
-    };
-    Share share = {0, 0, 0, 0};
+    const float mag = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
     bool ok = true;
-    Part x, nx;
+    Part x;
     bool have = next_part(p, ctl, walk, x);
-    float factor = stage_q(x);
     int buf = 0, bph = 0, pbuf = C::NS - 1, pbph = 1, step = 0;
     for (int g = 0; have; ++g) {
       const int i = x.qt * ctl.tokens + ti;
       const bool in = ti < ctl.tokens && i < x.s.nq;
       // keys [0, lim) are this row's
       const int lim = p.causal && in ? x.s.nk - x.s.nq + i + 1 : x.s.nk;
-      const float sl2 = factor;
-      float m_used = -INFINITY, l = 0.f;
+      float sl2 = 0.f, m_used = -INFINITY, l = 0.f;
       for (int j = x.lo; j < x.hi; ++j, ++step) {
         ok = __all_sync(~0u, bounded_wait(bSfull + 8 * buf, bph, w));
         if (!ok) break;
         tc_fence_after();
         const uint32_t s_tm = tmem + lane_off + buf * 128;
+        if (j == x.lo)  // written before the Q row that this S read
+          sl2 = fmaxf(
+              mag * pow2(reinterpret_cast<const int8_t *>(smem + C::OFF_QE)[(g & 1) * 128 + r]), FLT_MIN);
+        const uint4 bits = reinterpret_cast<const uint4 *>(smem + C::OFF_MASK)[step % C::MASKS];
         uint32_t sr[4][32];
+        const int cut = lim - j * 128;  // columns [0, cut) are seen
+        if (__any_sync(~0u, cut < 128 || (bits.x & bits.y & bits.z & bits.w) != ~0u)) {
+          // scores that do not count become -inf in tensor memory
+#pragma unroll 1
+          for (int n = 0; n < 4; ++n) {
+            const uint32_t word = n == 0 ? bits.x : n == 1 ? bits.y : n == 2 ? bits.z : bits.w;
+            const int c = cut - 32 * n;
+            const uint32_t see = word & (c >= 32 ? ~0u : c <= 0 ? 0u : (1u << c) - 1u);
+            if (__all_sync(~0u, see == ~0u)) continue;
+            tmem_ld32(s_tm + 32 * n, sr[0]);
+            tmem_ld_wait();
+            reg_fence32(sr[0]);
+#pragma unroll
+            for (int y = 0; y < 32; ++y)
+              if (!(see >> y & 1)) sr[0][y] = 0xff800000u;
+            tmem_st32(s_tm + 32 * n, sr[0]);
+          }
+          tmem_st_wait();
+        }
         tmem_ld32(s_tm + 0, sr[0]);
         tmem_ld32(s_tm + 32, sr[1]);
         tmem_ld32(s_tm + 64, sr[2]);
         tmem_ld32(s_tm + 96, sr[3]);
-        const uint4 bits = reinterpret_cast<const uint4 *>(smem + C::OFF_MASK)[step % C::MASKS];
         tmem_ld_wait();
         reg_fence32(sr[0]);
         reg_fence32(sr[1]);
         reg_fence32(sr[2]);
         reg_fence32(sr[3]);
         auto S = [&](int c) -> float { return __uint_as_float(sr[c >> 5][c & 31]); };
-        const int cut = lim - j * 128;  // columns [0, cut) are seen
-        if (__any_sync(~0u, cut < 128 || (bits.x & bits.y & bits.z & bits.w) != ~0u)) {
-          const uint32_t word[4] = {bits.x, bits.y, bits.z, bits.w};
-#pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            const int c = cut - 32 * n;
-            const uint32_t see = word[n] & (c >= 32 ? ~0u : c <= 0 ? 0u : (1u << c) - 1u);
-#pragma unroll
-            for (int y = 0; y < 32; ++y)
-              if (!(see >> y & 1)) sr[n][y] = 0xff800000u;  // -inf
-          }
-        }
         // The offset moves only when a row's maximum grows by more than 2^8.
         // P is formed with the offset at hand; a row sum of at most 2^8 proves
         // that no term is above it.  A tile's first step, and rows that have
@@ -568,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const float alpha = need ? ex2_approx(m_used - m_new) : 1.f;
                 const uint64_t a2 = pk2(alpha, alpha);
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                   uint32_t o[32];
                   tmem_ld32(o_tm + c, o);
@@ -625,26 +635,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         pbph = bph;
         if (++buf == C::NS) buf = 0, bph ^= 1;
       }
-      // the next tile's Q goes in while this one's last products run
-      const bool have_next = next_part(p, ctl, walk, nx);
-      if (ok && have_next) {
-        ok = __all_sync(~0u, bounded_wait(bQempty, g & 1, w));
-        if (ok) factor = stage_q(nx);
-      }
       if (ok) ok = __all_sync(~0u, bounded_wait(bOdone + 8 * pbuf, pbph, w));
       if (ok) {
         tc_fence_after();
         const bool begins = x.lo == 0, ends = x.hi == x.units;
-        if (begins && !ends)
-          share = Share{x.s.r0 + x.qt * ctl.tokens, x.h,
-                        min(x.s.nq - x.qt * ctl.tokens, ctl.tokens) * p.group, x.last};
+        if (r == 0 && begins && !ends) {
+          // the CTA with the tile's last step: `units` from its first on
+          const long long end = *s_total * (blockIdx.x + 1) / *s_den - walk->left - x.hi + x.units;
+          reinterpret_cast<Share *>(ws)[blockIdx.x] =
+              Share{x.s.r0 + x.qt * ctl.tokens, x.h,
+                    min(x.s.nq - x.qt * ctl.tokens, ctl.tokens) * p.group,
+                    cta_of(end - 1, *s_total, *s_den)};
+        }
         const bool whole = begins && ends;
         const float inv = l > 0.f ? p.v_mul / l : 0.f;
         const int head = x.h * p.group + tj;
         T *out = static_cast<T *>(p.o) +
                  (in ? (static_cast<long long>(x.s.r0 + i) * p.Hq + head) * D : 0);
         float *part = part_of<D, R>(ws, blockIdx.x, begins);
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
           tmem_ld32(o_tm + c, o);
@@ -672,17 +681,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               l > 0.f ? m_used * 0.6931471805599453f + logf(l) : -INFINITY;
         if (in && !whole)
           reinterpret_cast<float2 *>(part + R * D)[r] = make_float2(m_used, l);
-        if (have_next) {
-          tc_fence_before();
-          mbar_arrive(bOfree);
-        }
+        tc_fence_before();
+        mbar_arrive(bOfree);
       }
       // the four warps take one decision to go on or stop
       if (named_bar_or(1, 128, !ok || *abort_flag != 0)) break;
-      x = nx;
-      have = have_next;
+      have = next_part(p, ctl, walk, x);
     }
-    if (r == 0) reinterpret_cast<Share *>(ws)[blockIdx.x] = share;
   }
 
   tc_fence_before();
