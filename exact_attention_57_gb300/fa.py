@@ -473,17 +473,9 @@ def fa_fwd_kv4_workspace(B, Hq, Hk, max_seqlen_q, d) -> int:
     return load().fa_fwd_kv4_workspace(B, Hq, Hk, max_seqlen_q, d)
 
 
-def _same_device(first, *tensors) -> int:
-    """Index of the CUDA device of `first`; every tensor given has to live there."""
-    dev = first.get_device()
-    if dev < 0:
-        raise ValueError("CUDA tensors expected")
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("tensors on one device expected")
-    return dev
-
-
+# The wrappers below run once or more in every layer of every step of a server,
+# where a launch costs about 3 us of host time: each checks what it is given
+# once, in line, and leaves the rest to the C entry point.
 def _call(where, dev, stream, fn, *args):
     """fn(*args, stream) with device `dev` current (its current stream unless
     one is given); FaError on failure."""
@@ -499,9 +491,24 @@ def _call(where, dev, stream, fn, *args):
         raise FaError(st, where)
 
 
-def _need(t, dtype, what):
-    if t.dtype != dtype or not t.is_contiguous():
-        raise ValueError(f"{what}: a contiguous {dtype} tensor expected")
+def _same_device(dev, *tensors):
+    if dev < 0:
+        raise ValueError("CUDA tensors expected")
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors on one device expected")
+
+
+def _any_dtype(t) -> int:
+    import torch
+    dt = t.dtype
+    if dt is torch.bfloat16:
+        return FA_DTYPE_BF16
+    if dt is torch.float16:
+        return FA_DTYPE_F16
+    if dt is torch.float32:
+        return FA_DTYPE_F32
+    raise ValueError(f"unsupported dtype {dt}")
 
 
 def kv_plan(cached_lens, new_lens, free_blocks, block_table, block_size: int, capacity: int,
@@ -515,36 +522,36 @@ def kv_plan(cached_lens, new_lens, free_blocks, block_table, block_size: int, ca
     int32 [B+1], seq_lens int32 [B], counts int32 [2]: blocks needed, tokens);
     out: those five tensors, to write to.  Raises FaError on failure."""
     import torch
-    dev = _same_device(cached_lens, new_lens, free_blocks, block_table, free_head, *(out or ()))
+    dev, i32, i64 = cached_lens.get_device(), torch.int32, torch.int64
     B = cached_lens.numel()
-    i32 = torch.int32
-    for t, what in ((cached_lens, "cached_lens"), (new_lens, "new_lens"),
-                    (free_blocks, "free_blocks"), (block_table, "block_table")):
-        _need(t, i32, what)
-    if free_head is not None:
-        _need(free_head, i32, "free_head")
-        if free_head.numel() < 1:
-            raise ValueError("free_head: one element expected")
-    if new_lens.numel() != B or block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError("cached_lens [B], new_lens [B], block_table [B, max_blocks] expected")
     if out is None:
-        out = (torch.empty(capacity, dtype=torch.int64, device=dev),
-               torch.empty(capacity, dtype=i32, device=dev),
-               torch.empty(B + 1, dtype=i32, device=dev), torch.empty(B, dtype=i32, device=dev),
-               torch.empty(2, dtype=i32, device=dev))
-    else:
-        for t, dt, n in zip(out, (torch.int64, i32, i32, i32, i32), (capacity, capacity, B + 1, B, 2),
-                            strict=True):
-            _need(t, dt, "out")
-            if t.numel() != n:
-                raise ValueError("out: slots, positions [capacity], cu_seqlens [B+1], "
-                                 "seq_lens [B], counts [2] expected")
+        d = cached_lens.device
+        out = (torch.empty(capacity, dtype=i64, device=d), torch.empty(capacity, dtype=i32, device=d),
+               torch.empty(B + 1, dtype=i32, device=d), torch.empty(B, dtype=i32, device=d),
+               torch.empty(2, dtype=i32, device=d))
     slots, positions, cu, lens, counts = out
+    _same_device(dev, new_lens, free_blocks, block_table, free_head, *out)
+    for t in (cached_lens, new_lens, free_blocks, block_table, positions, cu, lens, counts):
+        if t.dtype is not i32 or not t.is_contiguous():
+            raise ValueError("contiguous int32 tensors expected (slots: int64)")
+    if slots.dtype is not i64 or not slots.is_contiguous():
+        raise ValueError("slots: a contiguous int64 tensor expected")
+    shape = block_table.shape
+    if len(shape) != 2 or shape[0] != B or new_lens.numel() != B:
+        raise ValueError("cached_lens [B], new_lens [B], block_table [B, max_blocks] expected")
+    if slots.numel() != capacity or positions.numel() != capacity or cu.numel() != B + 1 \
+            or lens.numel() != B or counts.numel() != 2:
+        raise ValueError("out: slots, positions [capacity], cu_seqlens [B+1], seq_lens [B], "
+                         "counts [2] expected")
+    head = None
+    if free_head is not None:
+        if free_head.dtype is not i32 or free_head.numel() < 1:
+            raise ValueError("free_head: an int32 tensor of one element expected")
+        head = free_head.data_ptr()
     _call("fa_kv_plan", dev, stream, load().fa_kv_plan, cached_lens.data_ptr(),
-          new_lens.data_ptr(), free_blocks.data_ptr(),
-          free_head.data_ptr() if free_head is not None else None, block_table.data_ptr(),
+          new_lens.data_ptr(), free_blocks.data_ptr(), head, block_table.data_ptr(),
           slots.data_ptr(), positions.data_ptr(), cu.data_ptr(), lens.data_ptr(),
-          counts.data_ptr(), B, block_table.shape[1], block_size, free_blocks.numel(), capacity)
+          counts.data_ptr(), B, shape[1], block_size, free_blocks.numel(), capacity)
     return out
 
 
@@ -572,6 +579,8 @@ _pack6 = struct.Struct("=6q").pack
 def _rope_strides(x, y):
     """Six host int64: batch, head and row strides of x, then of y."""
     a, b = x.stride(), y.stride()
+    if a[-1] != 1 or b[-1] != 1:
+        raise ValueError("rows of contiguous elements expected")
     if len(a) == 4:  # [B, H, N, d]
         return _pack6(a[0], a[1], a[2], b[0], b[1], b[2])
     return _pack6(0, a[1], a[0], 0, b[1], b[0])  # [T, H, d]
@@ -586,39 +595,43 @@ def rotary(q, k, positions, table, interleaved: bool = False, q_out=None, k_out=
     write (q and k themselves rotate in place; default: new tensors).
     Returns (q_out, k_out).  Raises FaError on failure."""
     import torch
-    dev = _same_device(q, k, positions, table, q_out, k_out)
-    nd = q.dim()
-    if nd not in (3, 4):
-        raise ValueError("q [B,H,N,d] or [T,H,d] expected")
-    if nd == 4:
-        B, Hq, N, d = q.shape
-        rows = (B, N)
+    dev, shape, at = q.get_device(), q.shape, positions.shape
+    if len(shape) == 3:
+        N, Hq, d = shape
+        B = 1
+        fits = len(at) == 2 and at[1] == N
+    elif len(shape) == 4:
+        B, Hq, N, d = shape
+        fits = len(at) == 3 and at[1] == B and at[2] == N
     else:
-        N, Hq, d = q.shape
-        B, rows = 1, (N,)
-    _need(positions, torch.int32, "positions")
-    _need(table, torch.int64, "table")
-    if positions.shape[1:] != rows:
-        raise ValueError("positions [axes, B, N] (or [axes, T]) expected")
+        raise ValueError("q [B,H,N,d] or [T,H,d] expected")
+    if not fits or positions.dtype is not torch.int32 or not positions.is_contiguous():
+        raise ValueError("positions: contiguous int32 [axes, B, N] (or [axes, T]) expected")
+    if table.dtype is not torch.int64 or not table.is_contiguous():
+        raise ValueError("table: the tensor of rotary_table() expected")
+    code = _any_dtype(q)
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = torch.empty_like(q)
+    elif q_out.shape != shape or q_out.dtype is not q.dtype:
+        raise ValueError("q_out: q's shape and dtype expected")
+    st = _rope_strides(q, q_out)
+    kp = ko = ks = None
     Hk = 0
     if k is not None:
-        Hk = k.shape[1]
-        want = (B, Hk, N, d) if nd == 4 else (N, Hk, d)
+        kshape = k.shape
+        Hk = kshape[1]
+        if len(kshape) != len(shape) or kshape[0] != shape[0] or kshape[-1] != d \
+                or (len(shape) == 4 and kshape[2] != N) or k.dtype is not q.dtype:
+            raise ValueError("k: q's shape but for the heads, and its dtype expected")
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        if k.shape != want or k.dtype != q.dtype or k_out.shape != want or k_out.dtype != q.dtype \
-                or k.stride(-1) != 1 or k_out.stride(-1) != 1:
-            raise ValueError("k, k_out: q's shape but for the heads, its dtype, contiguous rows")
-    if q_out.shape != q.shape or q_out.dtype != q.dtype or q.stride(-1) != 1 \
-            or q_out.stride(-1) != 1:
-        raise ValueError("q, q_out: one shape and dtype, contiguous rows")
-    _call("fa_rope", dev, stream, load().fa_rope, q.data_ptr(), q_out.data_ptr(),
-          _rope_strides(q, q_out), Hq, k.data_ptr() if Hk else None,
-          k_out.data_ptr() if Hk else None, _rope_strides(k, k_out) if Hk else None, Hk,
-          positions.data_ptr(), positions.shape[0], table.data_ptr(), B, N, d, 2 * table.numel(),
-          int(interleaved), int(inverse), _any_dtype(q))
+            k_out = torch.empty_like(k)
+        elif k_out.shape != kshape or k_out.dtype is not k.dtype:
+            raise ValueError("k_out: k's shape and dtype expected")
+        kp, ko, ks = k.data_ptr(), k_out.data_ptr(), _rope_strides(k, k_out)
+    _same_device(dev, k, positions, table, q_out, k_out)
+    _call("fa_rope", dev, stream, load().fa_rope, q.data_ptr(), q_out.data_ptr(), st, Hq, kp, ko, ks,
+          Hk, positions.data_ptr(), at[0], table.data_ptr(), B, N, d, 2 * table.numel(),
+          1 if interleaved else 0, 1 if inverse else 0, code)
     return q_out, k_out
 
 
@@ -627,17 +640,6 @@ def rotary_backward(dq, dk, positions, table, interleaved: bool = False, q_out=N
     """Gradients of rotary()'s inputs from those of its outputs: the inverse
     rotation, with rotary()'s arguments."""
     return rotary(dq, dk, positions, table, interleaved, q_out, k_out, stream, inverse=True)
-
-
-def _any_dtype(t) -> int:
-    import torch
-    if t.dtype == torch.bfloat16:
-        return FA_DTYPE_BF16
-    if t.dtype == torch.float16:
-        return FA_DTYPE_F16
-    if t.dtype == torch.float32:
-        return FA_DTYPE_F32
-    raise ValueError(f"unsupported dtype {t.dtype}")
 
 
 def _cache_shape(k_codes, k_scales, v_codes, v_scales):
@@ -669,17 +671,19 @@ def kv4_append(k, v, slots, k_codes, k_scales, v_codes, v_scales, k_exp: int = 0
     slices of a fused projection) into the 4-bit cache at slots int64 [T]
     (-1 skips a row).  Raises FaError on failure."""
     import torch
-    dev = _same_device(k, v, slots, k_codes, k_scales, v_codes, v_scales)
+    dev = k.get_device()
+    _same_device(dev, v, slots, k_codes, k_scales, v_codes, v_scales)
     blocks, Hk, bs, d = _cache_shape(k_codes, k_scales, v_codes, v_scales)
     T = slots.numel()
-    _need(slots, torch.int64, "slots")
-    for x in (k, v):
-        st = x.stride()
-        if x.shape != (T, Hk, d) or x.dtype != k.dtype or st[2] != 1 or (Hk > 1 and st[1] != d):
-            raise ValueError("k, v [T, Hk, d] of one dtype with contiguous rows expected")
-    row = Hk * d
+    if slots.dtype is not torch.int64 or not slots.is_contiguous():
+        raise ValueError("slots: a contiguous int64 tensor expected")
+    want, a, b = (T, Hk, d), k.stride(), v.stride()
+    if k.shape != want or v.shape != want or v.dtype is not k.dtype or a[2] != 1 or b[2] != 1 \
+            or (Hk > 1 and (a[1] != d or b[1] != d)):
+        raise ValueError("k, v [T, Hk, d] of one dtype with contiguous rows expected")
+    row = Hk * d  # of one token, the stride says nothing
     _call("fa_kv4_append", dev, stream, load().fa_kv4_append, k.data_ptr(), v.data_ptr(),
-          k.stride(0) if T > 1 else row, v.stride(0) if T > 1 else row, slots.data_ptr(), T,
+          a[0] if T > 1 else row, b[0] if T > 1 else row, slots.data_ptr(), T,
           k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), blocks,
           Hk, bs, d, k_exp, v_exp, _any_dtype(k))
 
@@ -690,19 +694,23 @@ def kv4_gather(slots, k_codes, k_scales, v_codes, v_scales, dtype=None, k_exp: i
     each [R, Hk, d] of `dtype` (default bf16); out: those two tensors, to write
     to.  Raises FaError on failure."""
     import torch
-    dev = _same_device(slots, k_codes, k_scales, v_codes, v_scales, *(out or ()))
+    dev = slots.get_device()
     blocks, Hk, bs, d = _cache_shape(k_codes, k_scales, v_codes, v_scales)
     R = slots.numel()
-    _need(slots, torch.int64, "slots")
+    if slots.dtype is not torch.int64 or not slots.is_contiguous():
+        raise ValueError("slots: a contiguous int64 tensor expected")
     if out is None:
         dtype = torch.bfloat16 if dtype is None else dtype
-        out = (torch.empty((R, Hk, d), dtype=dtype, device=dev),
-               torch.empty((R, Hk, d), dtype=dtype, device=dev))
-    k, v = out
-    for x in out:
-        if x.shape != (R, Hk, d) or not x.is_contiguous() or x.dtype != k.dtype \
-                or (dtype is not None and x.dtype != dtype):
+        k = torch.empty((R, Hk, d), dtype=dtype, device=slots.device)
+        v = torch.empty((R, Hk, d), dtype=dtype, device=slots.device)
+    else:
+        k, v = out
+        want = (R, Hk, d)
+        if k.shape != want or v.shape != want or v.dtype is not k.dtype \
+                or not k.is_contiguous() or not v.is_contiguous() \
+                or (dtype is not None and k.dtype is not dtype):
             raise ValueError("out: two contiguous [R, Hk, d] tensors of the dtype expected")
+    _same_device(dev, k_codes, k_scales, v_codes, v_scales, k, v)
     _call("fa_kv4_gather", dev, stream, load().fa_kv4_gather, slots.data_ptr(), R,
           k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
           k.data_ptr(), v.data_ptr(), blocks, Hk, bs, d, k_exp, v_exp, _any_dtype(k))
@@ -720,42 +728,45 @@ def attention_kv4(q, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens
     lse [Hq, total_q]).  The workspace (fa_fwd_kv4_workspace bytes) is
     allocated with torch unless given.  Raises FaError on failure."""
     import torch
-    dev = _same_device(q, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens_k,
-                       cu_seqlens_q, out, lse, workspace)
+    dev, i32 = q.get_device(), torch.int32
     blocks, Hk, bs, d = _cache_shape(k_codes, k_scales, v_codes, v_scales)
-    total_q, Hq, dq = q.shape
+    shape = q.shape
+    total_q, Hq, dq = shape
     if dq != d or not q.is_contiguous():
         raise ValueError("q: a contiguous [total_q, Hq, d] tensor expected")
-    B = seq_lens_k.numel()
-    _need(seq_lens_k, torch.int32, "seq_lens_k")
-    _need(block_table, torch.int32, "block_table")
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError("block_table [B, max_blocks] expected")
+    B, table = seq_lens_k.numel(), block_table.shape
+    if seq_lens_k.dtype is not i32 or not seq_lens_k.is_contiguous() \
+            or block_table.dtype is not i32 or not block_table.is_contiguous() \
+            or len(table) != 2 or table[0] != B:
+        raise ValueError("seq_lens_k [B], block_table [B, max_blocks]: contiguous int32 tensors "
+                         "expected")
+    cu = None
     if cu_seqlens_q is not None:
-        _need(cu_seqlens_q, torch.int32, "cu_seqlens_q")
-        if cu_seqlens_q.numel() != B + 1:
-            raise ValueError("cu_seqlens_q [B+1] expected")
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
+        if cu_seqlens_q.dtype is not i32 or cu_seqlens_q.numel() != B + 1 \
+                or not cu_seqlens_q.is_contiguous():
+            raise ValueError("cu_seqlens_q: a contiguous int32 [B+1] tensor expected")
+        cu = cu_seqlens_q.data_ptr()
     if out is None:
         out = torch.empty_like(q)
-    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+    elif out.shape != shape or out.dtype is not q.dtype or not out.is_contiguous():
         raise ValueError("out: a contiguous tensor like q expected")
     if lse is None:
-        lse = torch.empty((Hq, total_q), device=dev, dtype=torch.float32)
-    elif lse.shape != (Hq, total_q) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        lse = torch.empty((Hq, total_q), device=q.device, dtype=torch.float32)
+    elif lse.shape != (Hq, total_q) or lse.dtype is not torch.float32 or not lse.is_contiguous():
         raise ValueError("lse: a contiguous float32 [Hq, total_q] tensor expected")
     lib = load()
     if workspace is None:
         need = lib.fa_fwd_kv4_workspace(B, Hq, Hk, max_seqlen_q, d)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _same_device(dev, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens_k, cu_seqlens_q,
+                 out, lse, workspace)
     _call("fa_fwd_kv4", dev, stream, lib.fa_fwd_kv4, q.data_ptr(), out.data_ptr(), lse.data_ptr(),
           k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
-          block_table.data_ptr(), seq_lens_k.data_ptr(),
-          cu_seqlens_q.data_ptr() if cu_seqlens_q is not None else None, B, Hq, Hk, total_q,
-          max_seqlen_q, max_seqlen_k, blocks, bs, block_table.shape[1], d, scale,
-          int(bool(causal)), k_exp, v_exp, _any_dtype(q),
-          workspace.data_ptr() if workspace is not None else None,
-          workspace.numel() * workspace.element_size() if workspace is not None else 0)
+          block_table.data_ptr(), seq_lens_k.data_ptr(), cu, B, Hq, Hk, total_q, max_seqlen_q,
+          max_seqlen_k, blocks, bs, table[1], d, 1.0 / math.sqrt(d) if scale is None else scale,
+          1 if causal else 0, k_exp, v_exp, _any_dtype(q), ws, ws_bytes)
     return out, lse
