@@ -11,9 +11,19 @@
 // the exact one does (a neighbour x of s * border differs from it by at least
 // 1 / 1.875 units in the quotient's last place, and max|x| / 6 likewise).
 // 16-bit input has at most 11 significant bits and s * border at most 7, so a
-// quotient off a border is off by 2^-11 of it at least: it is enough to
-// multiply by 1 / s (error below 2^-22) and round the product to 14 bits,
-// which puts quotients on a border back there and moves no other across.
+// quotient off a border (0.25 .. 5) is off by 2^-11 of it, 2^-13, at least: it
+// is enough to multiply by 1 / s (error below 2^-22 of it, 2^-19) and round to
+// a multiple of 2^-16, by an addition of 1.5 * 2^7 and its subtraction, which
+// puts quotients on a border back there and moves no other across.
+//
+// Both kernels are bound by memory and near the rate at which instructions are
+// issued, so a thread takes the same 16 elements of K and of V (one slot, one
+// index computation, 32 bytes a load).  16383 fp16 rows of 8 x 128 elements
+// written and 24575 read back (215 MB) take 37.6 us as two launches, 5.7 TB/s or
+// 85% of the measured copy rate (52 us with one group a thread and 64-bit
+// divisions).
+#include <type_traits>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -33,104 +43,179 @@ __device__ __forceinline__ long long cache_row(const Kv4Store &c, long long slot
   return ((block * c.Hk + h) << c.bs_log2) + off;
 }
 
-template <typename T>
-__device__ __forceinline__ void load16(const T *src, float (&x)[16]) {
-  constexpr int W = 16 / sizeof(T);
-#pragma unroll
-  for (int i = 0; i < 16 / W; ++i) {
-    const uint4 v = reinterpret_cast<const uint4 *>(src)[i];
-    const T *e = reinterpret_cast<const T *>(&v);
-#pragma unroll
-    for (int j = 0; j < W; ++j) x[i * W + j] = static_cast<float>(e[j]);
-  }
+// 32 bytes at a time.
+struct alignas(32) B32 {
+  uint32_t w[8];
+};
+__device__ __forceinline__ B32 load32(const void *p) {
+  B32 x;
+  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(x.w[0]), "=r"(x.w[1]), "=r"(x.w[2]), "=r"(x.w[3]), "=r"(x.w[4]), "=r"(x.w[5]),
+                 "=r"(x.w[6]), "=r"(x.w[7])
+               : "l"(p));
+  return x;
+}
+__device__ __forceinline__ void store32(void *p, const B32 &x) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x.w[0]),
+               "r"(x.w[1]), "r"(x.w[2]), "r"(x.w[3]), "r"(x.w[4]), "r"(x.w[5]), "r"(x.w[6]), "r"(x.w[7])
+               : "memory");
 }
 
-// One thread: one group of one row of K (blockIdx.y = 0) or V (1).
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-    fa_kv4_append_kernel(const T *k, const T *v, long long k_stride, long long v_stride,
-                         const long long *slots, int T_, const Kv4Store c) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const bool is_v = blockIdx.y != 0;
-  const int groups = c.d / 16, per_row = c.Hk * groups;
+// Where a thread's 16 elements are: row, and head * (d / 16) + group.
+struct At {
+  long long row;
+  int hg;
+};
+__device__ __forceinline__ At place(const Kv4Store &c) {
+  const int per_row = c.Hk * (c.d / 16);
   const long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
+  if (i >> 32 == 0) {  // the common case: a 32-bit division
+    const unsigned u = static_cast<unsigned>(i), row = u / per_row;
+    return At{row, static_cast<int>(u - row * per_row)};
+  }
   const long long row = i / per_row;
-  if (row >= T_) return;
-  const long long slot = slots[row];
-  if (slot < 0 || slot >= (static_cast<long long>(c.num_blocks) << c.bs_log2)) return;
-  const int hg = static_cast<int>(i - row * per_row), h = hg / groups, g = hg - h * groups;
-  float x[16];
-  load16((is_v ? v + row * v_stride : k + row * k_stride) + hg * 16, x);
-  const float unit = pow2(-(is_v ? c.v_exp : c.k_exp));
-  float amax = 0.f;
+  return At{row, static_cast<int>(i - row * per_row)};
+}
+
+// Index of a slot's 16 elements in the cache, in units of 16.
+__device__ __forceinline__ long long cache_at(const Kv4Store &c, long long slot, int hg) {
+  const int groups = c.d / 16, h = hg / groups;
+  return cache_row(c, slot, h) * groups + (hg - h * groups);
+}
+
+template <typename T>
+struct Group {  // 16 elements
+  uint4 w[sizeof(T)];
+};
+template <typename T>
+__device__ __forceinline__ Group<T> load_group(const T *p, bool wide) {
+  Group<T> x;
+  if (wide) {
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    x[j] *= unit;
-    amax = fmaxf(amax, fabsf(x[j]));
+    for (int n = 0; n < static_cast<int>(sizeof(T)) / 2; ++n)
+      reinterpret_cast<B32 *>(&x)[n] = load32(reinterpret_cast<const uint8_t *>(p) + 32 * n);
+  } else {
+#pragma unroll
+    for (int n = 0; n < static_cast<int>(sizeof(T)); ++n)
+      x.w[n] = __ldg(reinterpret_cast<const uint4 *>(p) + n);
+  }
+  return x;
+}
+
+// Codes and scale of a group.
+template <typename T>
+__device__ __forceinline__ void quantise(const Group<T> &x, float unit, uint2 *codes, uint8_t *scale) {
+  float amax;
+  if constexpr (sizeof(T) == 2) {
+    using P = std::conditional_t<std::is_same_v<T, __half>, __half2, __nv_bfloat162>;
+    const P *p = reinterpret_cast<const P *>(&x);
+    P top = __habs2(p[0]);
+#pragma unroll
+    for (int j = 1; j < 8; ++j) top = __hmax2(top, __habs2(p[j]));  // a NaN does not count
+    amax = fmaxf(static_cast<float>(top.x), static_cast<float>(top.y)) * unit;
+  } else {
+    const float *p = reinterpret_cast<const float *>(&x);
+    amax = 0.f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) amax = fmaxf(amax, fabsf(p[j]));
+    amax *= unit;
   }
   const uint32_t sb = f32_e4m3(__fdiv_rn(amax, 6.f));
   const float s = f16x2_f32(e4m3x2_f16x2(sb)).x;
-  uint32_t codes[2] = {0, 0};
+  uint32_t c[2] = {0, 0};
   if (s > 0.f) {
+    float y[16];
     if constexpr (sizeof(T) == 2) {
-      const float r = __fdiv_rn(1.f, s);
+      const T *p = reinterpret_cast<const T *>(&x);
+      const float r = __fdiv_rn(1.f, s) * unit, C = 192.f;
 #pragma unroll
-      for (int j = 0; j < 16; ++j)  // to 14 significant bits; a NaN becomes 8, stored as +6
-        x[j] = __uint_as_float((__float_as_uint(fminf(x[j] * r, 8.f)) + 0x200u) & ~0x3FFu);
+      for (int j = 0; j < 16; ++j)  // to a multiple of 2^-16
+        y[j] = __fadd_rn(__fmaf_rn(static_cast<float>(p[j]), r, C), -C);
     } else {
+      const float *p = reinterpret_cast<const float *>(&x);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) x[j] = __fdiv_rn(x[j], s);
+      for (int j = 0; j < 16; ++j) y[j] = __fdiv_rn(p[j] * unit, s);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      codes[j / 4] |= f32x2_e2m1x2(x[2 * j], x[2 * j + 1]) << (8 * (j & 3));
+    for (int j = 0; j < 8; ++j) c[j / 4] |= f32x2_e2m1x2(y[2 * j], y[2 * j + 1]) << (8 * (j & 3));
   }
-  const long long at = cache_row(c, slot, h);
-  reinterpret_cast<uint2 *>(is_v ? c.v_codes : c.k_codes)[at * groups + g] =
-      make_uint2(codes[0], codes[1]);
-  (is_v ? c.v_scales : c.k_scales)[at * groups + g] = static_cast<uint8_t>(sb);
+  *codes = make_uint2(c[0], c[1]);
+  *scale = static_cast<uint8_t>(sb);
 }
 
-// One thread: 16 elements of one row of K or V; a slot outside the cache
-// reads zeros.
+// One thread: one group of one row of K and of V.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-    fa_kv4_gather_kernel(const long long *slots, int R, const Kv4Store c, T *k_out, T *v_out) {
+    fa_kv4_append_kernel(const T *k, const T *v, long long k_stride, long long v_stride,
+                         const long long *slots, int T_, const Kv4Store c, bool wide) {
   griddep_wait();
   griddep_launch_dependents();
-  const bool is_v = blockIdx.y != 0;
-  const int groups = c.d / 16, per_row = c.Hk * groups;
-  const long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
-  const long long row = i / per_row;
-  if (row >= R) return;
-  const long long slot = slots[row];
-  const int hg = static_cast<int>(i - row * per_row), h = hg / groups, g = hg - h * groups;
-  uint2 codes = make_uint2(0, 0);
-  float s = 0.f;
-  if (slot >= 0 && slot < (static_cast<long long>(c.num_blocks) << c.bs_log2)) {
-    const long long at = cache_row(c, slot, h);
-    codes = reinterpret_cast<const uint2 *>(is_v ? c.v_codes : c.k_codes)[at * groups + g];
-    s = f16x2_f32(e4m3x2_f16x2((is_v ? c.v_scales : c.k_scales)[at * groups + g])).x *
-        pow2(is_v ? c.v_exp : c.k_exp);
-  }
-  T *out = (is_v ? v_out : k_out) + i * 16;
-  constexpr int W = 16 / sizeof(T);
+  const At at = place(c);
+  if (at.row >= T_) return;
+  const Group<T> kx = load_group(k + at.row * k_stride + at.hg * 16, wide);
+  const Group<T> vx = load_group(v + at.row * v_stride + at.hg * 16, wide);
+  const long long slot = __ldg(slots + at.row);
+  if (slot < 0 || slot >= (static_cast<long long>(c.num_blocks) << c.bs_log2)) return;
+  const long long to = cache_at(c, slot, at.hg);
+  quantise(kx, pow2(-c.k_exp), reinterpret_cast<uint2 *>(c.k_codes) + to, c.k_scales + to);
+  quantise(vx, pow2(-c.v_exp), reinterpret_cast<uint2 *>(c.v_codes) + to, c.v_scales + to);
+}
+
+// 16 elements from their codes and scale.
+template <typename T>
+__device__ __forceinline__ void expand(uint2 codes, uint32_t scale, int exp, T *out, bool wide) {
   const uint32_t pairs[8] = {e2m1x2_f16x2<0>(codes.x), e2m1x2_f16x2<1>(codes.x),
                              e2m1x2_f16x2<2>(codes.x), e2m1x2_f16x2<3>(codes.x),
                              e2m1x2_f16x2<0>(codes.y), e2m1x2_f16x2<1>(codes.y),
                              e2m1x2_f16x2<2>(codes.y), e2m1x2_f16x2<3>(codes.y)};
+  const uint32_t s16 = __byte_perm(e4m3x2_f16x2(scale), 0, 0x1010);
+  alignas(32) T e[16];
+  if (std::is_same_v<T, __half> && exp == 0) {  // the product is exact in fp16
 #pragma unroll
-  for (int n = 0; n < 16 / W; ++n) {
-    alignas(16) T e[W];
+    for (int j = 0; j < 8; ++j) reinterpret_cast<uint32_t *>(e)[j] = hmul2(pairs[j], s16);
+  } else {
+    const float s = f16x2_f32(s16).x * pow2(exp);
 #pragma unroll
-    for (int j = 0; j < W / 2; ++j) {
-      const float2 f = f16x2_f32(pairs[n * W / 2 + j]);
+    for (int j = 0; j < 8; ++j) {
+      const float2 f = f16x2_f32(pairs[j]);
       e[2 * j] = static_cast<T>(f.x * s);
       e[2 * j + 1] = static_cast<T>(f.y * s);
     }
-    reinterpret_cast<uint4 *>(out)[n] = *reinterpret_cast<const uint4 *>(e);
   }
+#pragma unroll
+  for (int n = 0; n < static_cast<int>(sizeof(T)) / 2; ++n) {
+    if (wide) {
+      store32(reinterpret_cast<uint8_t *>(out) + 32 * n, reinterpret_cast<const B32 *>(e)[n]);
+    } else {
+      reinterpret_cast<uint4 *>(out)[2 * n] = reinterpret_cast<const uint4 *>(e)[2 * n];
+      reinterpret_cast<uint4 *>(out)[2 * n + 1] = reinterpret_cast<const uint4 *>(e)[2 * n + 1];
+    }
+  }
+}
+
+// One thread: 16 elements of one row of K and of V; a slot outside the cache
+// reads zeros.
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+    fa_kv4_gather_kernel(const long long *slots, int R, const Kv4Store c, T *k_out, T *v_out,
+                         bool wide) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const At at = place(c);
+  if (at.row >= R) return;
+  const long long slot = __ldg(slots + at.row);
+  uint2 kc = make_uint2(0, 0), vc = make_uint2(0, 0);
+  uint32_t ks = 0, vs = 0;
+  if (slot >= 0 && slot < (static_cast<long long>(c.num_blocks) << c.bs_log2)) {
+    const long long from = cache_at(c, slot, at.hg);
+    kc = __ldg(reinterpret_cast<const uint2 *>(c.k_codes) + from);
+    vc = __ldg(reinterpret_cast<const uint2 *>(c.v_codes) + from);
+    ks = __ldg(c.k_scales + from);
+    vs = __ldg(c.v_scales + from);
+  }
+  const long long to = (at.row * c.Hk * (c.d / 16) + at.hg) * 16;
+  expand(kc, ks, c.k_exp, k_out + to, wide);
+  expand(vc, vs, c.v_exp, v_out + to, wide);
 }
 
 template <typename... A>
@@ -138,7 +223,7 @@ cudaError_t launch(void (*kern)(A...), long long threads, cudaStream_t s, A... a
   cudaLaunchConfig_t cfg = {};
   const long long gx = (threads + kThreads - 1) / kThreads;
   if (gx > 2147483647LL) return cudaErrorInvalidConfiguration;
-  cfg.gridDim = dim3(static_cast<unsigned>(gx), 2);
+  cfg.gridDim = dim3(static_cast<unsigned>(gx));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -152,19 +237,22 @@ cudaError_t launch(void (*kern)(A...), long long threads, cudaStream_t s, A... a
 template <typename T>
 cudaError_t append(const void *k, const void *v, long long ks, long long vs,
                    const long long *slots, int T_, const Kv4Store &c, cudaStream_t s) {
-  return launch<const T *, const T *, long long, long long, const long long *, int,
-                const Kv4Store>(fa_kv4_append_kernel<T>,
-                                static_cast<long long>(T_) * c.Hk * (c.d / 16), s,
-                                static_cast<const T *>(k), static_cast<const T *>(v), ks, vs,
-                                slots, T_, c);
+  const long long es = sizeof(T);
+  const bool wide = (reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) % 32 == 0 &&
+                    ks * es % 32 == 0 && vs * es % 32 == 0;
+  return launch<const T *, const T *, long long, long long, const long long *, int, const Kv4Store,
+                bool>(fa_kv4_append_kernel<T>, static_cast<long long>(T_) * c.Hk * (c.d / 16), s,
+                      static_cast<const T *>(k), static_cast<const T *>(v), ks, vs, slots, T_, c,
+                      wide);
 }
 
 template <typename T>
 cudaError_t gather(const long long *slots, int R, const Kv4Store &c, void *k, void *v,
                    cudaStream_t s) {
-  return launch<const long long *, int, const Kv4Store, T *, T *>(
+  const bool wide = (reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) % 32 == 0;
+  return launch<const long long *, int, const Kv4Store, T *, T *, bool>(
       fa_kv4_gather_kernel<T>, static_cast<long long>(R) * c.Hk * (c.d / 16), s, slots, R, c,
-      static_cast<T *>(k), static_cast<T *>(v));
+      static_cast<T *>(k), static_cast<T *>(v), wide);
 }
 
 }  // namespace

@@ -11,6 +11,11 @@
 // product would be off by whole radians, and fp64 runs at a small fraction of
 // the fp32 rate on this chip).  Its upper 32 bits, as a number in
 // [-1, 1) half turns, go to sincospif.
+//
+// Memory bounds it: 18432 tokens of 32 bf16 heads of 128 elements (302 MB in and
+// out) take 52 us, 5.8 TB/s or 86% of the measured copy rate.  A thread issues
+// one head's loads ahead of its stores; four heads' together (111 registers, so
+// half the warps) took 75 us, streaming cache hints changed nothing.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -41,7 +46,8 @@ struct alignas(sizeof(T) * V) Vec {
 // copy), for `hpt` heads of q and k, so that its sines and cosines serve them
 // all.  INTER: pair i is elements (2i, 2i + 1), else (i, i + d_rot / 2).
 template <typename T, int V, bool INTER>
-__global__ void __launch_bounds__(kThreads) fa_rope_kernel(const RopeParams p, int nvec, int hpt) {
+__global__ void __launch_bounds__(kThreads, 6)
+    fa_rope_kernel(const RopeParams p, int nvec, int hpt) {
   griddep_wait();
   griddep_launch_dependents();
   const int rows_cta = kThreads / nvec;
@@ -117,9 +123,13 @@ cudaError_t launch_vec(const RopeParams &p, int num_sms, cudaStream_t s) {
   const long long gx = (p.rows + rows_cta - 1) / rows_cta;
   if (gx > 2147483647LL) return cudaErrorInvalidConfiguration;
   const int heads = p.q.heads + p.k.heads;
-  // Heads per thread: as many as leave about eight CTAs an SM.
+  // Heads per thread: as many as leave about eight CTAs an SM, up to eight (18432
+  // tokens of 32 heads: 2 ran in 64.9 us, 4 in 53.3, 8 in 52.3, 16 in 54.5; their
+  // sines and cosines cost less than what a short last wave does), in even shares.
   int hpt = static_cast<int>(gx * heads / (8LL * (num_sms > 0 ? num_sms : 1)));
-  hpt = hpt < 1 ? 1 : (hpt > 16 ? 16 : hpt);
+  hpt = hpt < 1 ? 1 : (hpt > 8 ? 8 : hpt);
+  const int shares = (heads + hpt - 1) / hpt;
+  hpt = (heads + shares - 1) / shares;
   while ((heads + hpt - 1) / hpt > 65535) ++hpt;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(gx), static_cast<unsigned>((heads + hpt - 1) / hpt));
