@@ -68,16 +68,24 @@ struct ManyCfg {
   static constexpr int OFF_K = OFF_Q + 2 * TILE;
   static constexpr int OFF_V = OFF_K + KST * TILE;
   static constexpr int OFF_MASK = OFF_V + VST * TILE;
-  static constexpr int OFF_QE = OFF_MASK + MASKS * 16;  // an exponent a row, two buffers
-  static constexpr int OFF_BAR = OFF_QE + 2 * 128;
+  // An exponent a row of the tiles in flight: Q of tile g is written when the
+  // last S of tile g - 2 is complete, and with tiles of one step the softmax
+  // may then still be at tile g - 4 (three score buffers).
+  static constexpr int QES = 8;
+  static constexpr int OFF_QE = OFF_MASK + MASKS * 16;
+  static constexpr int OFF_BAR = OFF_QE + QES * 128;
   // qfull[2], qempty[2], ofree, fin[2], kfull, kempty, vfull, vempty [ST],
   // sfull, pfull, odone [NS]
   static constexpr int NBAR = 7 + 4 * ST + 3 * NS;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;  // tmem base, abort flag, CTAs, -, units
   static constexpr int OFF_SUMS = OFF_K;           // before the first tile arrives
   static constexpr int OFF_WALK = OFF_MISC + 24;     // a walk for each warp
-  static constexpr int SMEM = OFF_WALK + kWarps * WALK_BYTES + 1024;
-  static_assert(SMEM <= 227 * 1024, "shared memory budget");
+  static constexpr int USED = OFF_WALK + kWarps * WALK_BYTES;
+  static constexpr int MAX_SMEM = 227 * 1024;
+  // room to align the base to 1024 bytes, as far as there is any (dynamic shared
+  // memory starts aligned when there is no static one; the kernel checks)
+  static constexpr int SMEM = USED + 1024 <= MAX_SMEM ? USED + 1024 : MAX_SMEM;
+  static_assert(USED <= MAX_SMEM, "shared memory budget");
 };
 constexpr uint32_t kRegSoftmax = 216, kRegExpand = 104, kRegIssue = 88;
 static_assert(128 * (kRegSoftmax + 2 * kRegExpand + kRegIssue) <= kThreads * 128,
@@ -200,6 +208,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   long long *s_sums = reinterpret_cast<long long *>(smem + C::OFF_SUMS);
   auto s_warp = reinterpret_cast<long long (*)[kWarps]>(s_sums + kThreads);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (smem + C::USED > smem_raw + C::SMEM) {  // see ManyCfg::SMEM
+    griddep_wait();
+    if (threadIdx.x == 0) {
+      atomicOr(ctl.status, kStatusSmemLayout);
+      reinterpret_cast<Share *>(ws)[blockIdx.x] = Share{0, 0, 0, 0};
+    }
+    return;
+  }
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
@@ -382,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint4 *>(tile + (u >> 3) * C::CHUNK + r * 128 +
                                        (((u & 7) ^ (r & 7)) << 4)) = v;
           }
-          reinterpret_cast<int8_t *>(smem + C::OFF_QE)[(g & 1) * 128 + r] = static_cast<int8_t>(e);
+          reinterpret_cast<int8_t *>(smem + C::OFF_QE)[g % C::QES * 128 + r] = static_cast<int8_t>(e);
         }
         fence_proxy_async_smem();
         mbar_arrive(bQfull + 8 * (g & 1));
@@ -515,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t s_tm = tmem + lane_off + buf * 128;
         if (j == x.lo)  // written before the Q row that this S read
           sl2 = fmaxf(
-              mag * pow2(reinterpret_cast<const int8_t *>(smem + C::OFF_QE)[(g & 1) * 128 + r]), FLT_MIN);
+              mag * pow2(reinterpret_cast<const int8_t *>(smem + C::OFF_QE)[g % C::QES * 128 + r]), FLT_MIN);
         const uint4 bits = reinterpret_cast<const uint4 *>(smem + C::OFF_MASK)[step % C::MASKS];
         uint32_t sr[4][32];
         const int cut = lim - j * 128;  // columns [0, cut) are seen

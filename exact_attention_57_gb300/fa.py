@@ -13,6 +13,7 @@ functions raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import struct
@@ -469,20 +470,23 @@ def fa_fwd_kv4(q, o, lse, k_codes, k_scales, v_codes, v_scales, block_table, seq
                              k_exp, v_exp, dtype, workspace, workspace_bytes, stream)
 
 
+@functools.lru_cache(maxsize=64)  # a function of these numbers alone
 def fa_fwd_kv4_workspace(B, Hq, Hk, max_seqlen_q, d) -> int:
     return load().fa_fwd_kv4_workspace(B, Hq, Hk, max_seqlen_q, d)
 
 
 # The wrappers below run once or more in every layer of every step of a server,
 # where a launch costs about 3 us of host time: each checks what it is given
-# once, in line, and leaves the rest to the C entry point.
+# once, in line, and leaves the rest to the C entry point.  `stream` is the
+# integer of a cudaStream_t (default: the current one); what it has to wait for,
+# the inputs among it, is the caller's to order.
 def _call(where, dev, stream, fn, *args):
     """fn(*args, stream) with device `dev` current (its current stream unless
     one is given); FaError on failure."""
     import torch
     if stream is None:
         stream = torch._C._cuda_getCurrentRawStream(dev)
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         st = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -491,12 +495,32 @@ def _call(where, dev, stream, fn, *args):
         raise FaError(st, where)
 
 
+def _on(stream, dev):
+    """Where a wrapper allocates: memory made while `stream` (an integer, or
+    None for the current one) is current belongs to it, and is not handed out
+    again before that stream's work on it is done."""
+    import contextlib
+
+    import torch
+    if stream is None or dev < 0:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=dev))
+
+
+def _like(t, stream, dev):
+    import torch
+    if stream is None:
+        return torch.empty_like(t)
+    with _on(stream, dev):
+        return torch.empty_like(t)
+
+
 def _same_device(dev, *tensors):
     if dev < 0:
         raise ValueError("CUDA tensors expected")
     for t in tensors:
         if t is not None and t.get_device() != dev:
-            raise ValueError("tensors on one device expected")
+            raise ValueError("tensors on one CUDA device expected")
 
 
 def _any_dtype(t) -> int:
@@ -526,9 +550,11 @@ def kv_plan(cached_lens, new_lens, free_blocks, block_table, block_size: int, ca
     B = cached_lens.numel()
     if out is None:
         d = cached_lens.device
-        out = (torch.empty(capacity, dtype=i64, device=d), torch.empty(capacity, dtype=i32, device=d),
-               torch.empty(B + 1, dtype=i32, device=d), torch.empty(B, dtype=i32, device=d),
-               torch.empty(2, dtype=i32, device=d))
+        with _on(stream, dev):
+            out = (torch.empty(capacity, dtype=i64, device=d),
+                   torch.empty(capacity, dtype=i32, device=d),
+                   torch.empty(B + 1, dtype=i32, device=d), torch.empty(B, dtype=i32, device=d),
+                   torch.empty(2, dtype=i32, device=d))
     slots, positions, cu, lens, counts = out
     _same_device(dev, new_lens, free_blocks, block_table, free_head, *out)
     for t in (cached_lens, new_lens, free_blocks, block_table, positions, cu, lens, counts):
@@ -611,7 +637,7 @@ def rotary(q, k, positions, table, interleaved: bool = False, q_out=None, k_out=
         raise ValueError("table: the tensor of rotary_table() expected")
     code = _any_dtype(q)
     if q_out is None:
-        q_out = torch.empty_like(q)
+        q_out = _like(q, stream, dev)
     elif q_out.shape != shape or q_out.dtype is not q.dtype:
         raise ValueError("q_out: q's shape and dtype expected")
     st = _rope_strides(q, q_out)
@@ -624,7 +650,7 @@ def rotary(q, k, positions, table, interleaved: bool = False, q_out=None, k_out=
                 or (len(shape) == 4 and kshape[2] != N) or k.dtype is not q.dtype:
             raise ValueError("k: q's shape but for the heads, and its dtype expected")
         if k_out is None:
-            k_out = torch.empty_like(k)
+            k_out = _like(k, stream, dev)
         elif k_out.shape != kshape or k_out.dtype is not k.dtype:
             raise ValueError("k_out: k's shape and dtype expected")
         kp, ko, ks = k.data_ptr(), k_out.data_ptr(), _rope_strides(k, k_out)
@@ -701,8 +727,9 @@ def kv4_gather(slots, k_codes, k_scales, v_codes, v_scales, dtype=None, k_exp: i
         raise ValueError("slots: a contiguous int64 tensor expected")
     if out is None:
         dtype = torch.bfloat16 if dtype is None else dtype
-        k = torch.empty((R, Hk, d), dtype=dtype, device=slots.device)
-        v = torch.empty((R, Hk, d), dtype=dtype, device=slots.device)
+        with _on(stream, dev):
+            k = torch.empty((R, Hk, d), dtype=dtype, device=slots.device)
+            v = torch.empty((R, Hk, d), dtype=dtype, device=slots.device)
     else:
         k, v = out
         want = (R, Hk, d)
@@ -747,24 +774,27 @@ def attention_kv4(q, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens
             raise ValueError("cu_seqlens_q: a contiguous int32 [B+1] tensor expected")
         cu = cu_seqlens_q.data_ptr()
     if out is None:
-        out = torch.empty_like(q)
+        out = _like(q, stream, dev)
     elif out.shape != shape or out.dtype is not q.dtype or not out.is_contiguous():
         raise ValueError("out: a contiguous tensor like q expected")
     if lse is None:
-        lse = torch.empty((Hq, total_q), device=q.device, dtype=torch.float32)
+        with _on(stream, dev):
+            lse = torch.empty((Hq, total_q), device=q.device, dtype=torch.float32)
     elif lse.shape != (Hq, total_q) or lse.dtype is not torch.float32 or not lse.is_contiguous():
         raise ValueError("lse: a contiguous float32 [Hq, total_q] tensor expected")
-    lib = load()
     if workspace is None:
-        need = lib.fa_fwd_kv4_workspace(B, Hq, Hk, max_seqlen_q, d)
-        if need:
+        need = fa_fwd_kv4_workspace(B, Hq, Hk, max_seqlen_q, d)
+        if need and stream is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        elif need:
+            with _on(stream, dev):
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     ws, ws_bytes = None, 0
     if workspace is not None:
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _same_device(dev, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens_k, cu_seqlens_q,
                  out, lse, workspace)
-    _call("fa_fwd_kv4", dev, stream, lib.fa_fwd_kv4, q.data_ptr(), out.data_ptr(), lse.data_ptr(),
+    _call("fa_fwd_kv4", dev, stream, load().fa_fwd_kv4, q.data_ptr(), out.data_ptr(), lse.data_ptr(),
           k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
           block_table.data_ptr(), seq_lens_k.data_ptr(), cu, B, Hq, Hk, total_q, max_seqlen_q,
           max_seqlen_k, blocks, bs, table[1], d, 1.0 / math.sqrt(d) if scale is None else scale,

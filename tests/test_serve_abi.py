@@ -181,10 +181,27 @@ def test_attention_refusals(kw):
     assert attn(**kw) == fa.FA_ERR_INVALID_ARG
 
 
-@pytest.mark.parametrize("kw", [dict(d=32), dict(d=256), dict(d=80), dict(dtype=fa.FA_DTYPE_F32),
+@pytest.mark.parametrize("kw", [dict(d=32), dict(d=256), dict(d=80), dict(Hq=258, Hk=2), dict(dtype=fa.FA_DTYPE_F32),
                                 dict(dtype=fa.FA_DTYPE_F32_SIMT)], ids=str)
 def test_attention_outside_the_set_is_unsupported(kw):
     assert attn(**kw) == fa.FA_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("Hq,Hk,max_q", [(4, 2, 1), (32, 1, 1), (33, 1, 1), (8, 1, 4), (8, 8, 300),
+                                         (128, 1, 9)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_workspace(Hq, Hk, max_q, d):
+    """It does not depend on the lengths; a missing, short or misaligned one is
+    refused."""
+    need = fa.fa_fwd_kv4_workspace(3, Hq, Hk, max_q, d)
+    assert 0 < need < 64 << 20
+    assert need == fa.fa_fwd_kv4_workspace(60000, Hq, Hk, max_q, d)
+    kw = dict(Hq=Hq, Hk=Hk, total=3 * max_q, max_q=max_q, d=d)
+    for bad in (dict(ws=None), dict(wsb=need - 1), dict(ws=A(14) + 128), dict(ws=A(0)), dict(ws=A(11))):
+        assert attn(**kw, **bad) == fa.FA_ERR_INVALID_ARG
+    for args in ((0, Hq, Hk, max_q, d), (3, 0, Hk, max_q, d), (3, 7, 2, max_q, d), (3, Hq, Hk, 0, d),
+                 (3, 129, 1, 1, d), (3, Hq, Hk, max_q, 0)):
+        assert fa.fa_fwd_kv4_workspace(*args) == 0
 
 
 def test_wrappers_refuse_cpu_tensors_and_wrong_shapes():

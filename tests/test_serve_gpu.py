@@ -401,6 +401,17 @@ ATTN_CASES = [
     ([700, 1500], [200, 3], 8, 8, 128, 32, "bf16"),
     ([1000], [1000], 2, 1, 128, 128, "fp16"),
     ([513, 100], [64, 33], 20, 4, 64, 16, "bf16"),
+    ([300, 129, 40], None, 128, 1, 64, 16, "bf16"),              # the largest group
+    ([300, 140, 0, 7], [3, 20, 2, 9], 100, 1, 128, 16, "fp16"),  # a token a tile
+    ([400, 390, 700], [90, 1, 2], 33, 1, 64, 32, "bf16"),
+    ([17 * (i % 23) for i in range(300)], None, 8, 4, 64, 16, "fp16"),   # more than a CTA's threads
+    ([3 * (i % 50) for i in range(600)], [i % 4 for i in range(600)], 8, 1, 64, 16, "bf16"),
+    ([5 + i % 40 for i in range(530)], [33 + (i == 7) for i in range(530)], 2, 2, 64, 16, "bf16"),
+    ([2500, 2049], [700, 2049], 8, 2, 64, 16, "fp16"),
+    # tiles of one and two steps: every ring of the pipeline runs far ahead
+    ([5 + i % 140 for i in range(700)], [34] * 700, 2, 2, 128, 16, "bf16"),
+    ([250, 3, 130, 0] * 20, [300, 260, 129, 131] * 20, 3, 3, 128, 32, "fp16"),
+    ([1537], [1537], 4, 4, 128, 64, "bf16"),
 ]
 
 
@@ -470,6 +481,8 @@ def test_attention_missing_pages_and_bounds(nqs):
     o, lse = call(q, cache, table, (10 ** 9, 2 ** 31 - 1), cu, nqs, max_k=100)
     check_attention(q, cache, table, (100, 100), nqs, 32, 128, 128 ** -0.5, True, o, lse,
                     torch.bfloat16)
+    o, lse = call(q, cache, table, (50, 60), cu, nqs, max_k=0)
+    assert (o == 0).all() and (lse == -math.inf).all()
     o, lse = call(q, cache, table, (-5, 77), cu, nqs, max_k=200)
     check_attention(q, cache, table, (0, 77), nqs, 32, 128, 128 ** -0.5, True, o, lse,
                     torch.bfloat16)
@@ -648,6 +661,65 @@ def test_two_streams_at_once():
         torch.cuda.synchronize()
         for (o, l), (wo, wl) in zip(got, alone):
             assert torch.equal(o, wo) and torch.equal(l, wl)
+
+
+def test_a_stream_of_its_own():
+    """Calls on a stream that is not the current one: what the wrappers
+    allocate belongs to that stream."""
+    side = torch.cuda.Stream()
+    q, cache, table, cu = small(43, (3000, 70), (5, 60))
+    args = (q.to(DEV), *(c.to(DEV) for c in cache), ints(table), ints([3000, 70]), 3000)
+    kw = dict(cu_seqlens_q=ints(cu), max_seqlen_q=60)
+    want = fa.attention_kv4(*args, **kw)
+    pos, rt = ints([list(range(65))]), fa.rotary_table([1.0 / 2 ** i for i in range(64)], device=DEV)
+    turned = fa.rotary(args[0], None, pos, rt)[0]
+    slots = torch.arange(16, device=DEV)
+    rows = fa.kv4_gather(slots, *args[1:5])
+    torch.cuda.synchronize()
+    for _ in range(20):
+        o, lse = fa.attention_kv4(*args, **kw, stream=side.cuda_stream)
+        x = fa.rotary(args[0], None, pos, rt, stream=side.cuda_stream)[0]
+        k, v = fa.kv4_gather(slots, *args[1:5], stream=side.cuda_stream)
+        torch.full((1 << 20,), 9.0, device=DEV)  # would take freed memory of the current stream
+        torch.cuda.synchronize()
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1]) and torch.equal(x, turned)
+        assert torch.equal(k, rows[0]) and torch.equal(v, rows[1])
+
+
+def test_many_queries_report_a_wait_that_runs_out():
+    """A kernel that gives up waiting records it in the status word, and the
+    next call is right again.  The failure is made on the host: the test hook
+    leaves out the first values, and the wait limit is 0.2 s."""
+    lens, nqs = (500, 300), (60, 40)
+    q, cache, table, cu = small(44, lens, nqs)
+    want = call(q, cache, table, lens, cu, nqs)
+    stream = torch.cuda.current_stream().cuda_stream
+    assert fa.fa_fwd_status(stream) == (fa.FA_OK, 0)
+    try:
+        fa.fa_set_test_hooks(skip_v_load=1, wait_limit_ns=200_000_000)
+        call(q, cache, table, lens, cu, nqs)
+    finally:
+        fa.fa_set_test_hooks(0, 0)
+    st, word = fa.fa_fwd_status(stream)
+    assert st == fa.FA_ERR_DEVICE_TIMEOUT
+    assert word & 8, word   # the skipped load was recorded
+    assert word & 2, word   # the issuer gave up waiting for the values
+    got = call(q, cache, table, lens, cu, nqs)
+    assert fa.fa_fwd_status(stream) == (fa.FA_OK, 0)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_repeated_calls_are_the_same_bit_for_bit():
+    """Parts are joined in a fixed order: no result depends on which CTA was
+    first, at one query a sequence and at many."""
+    for nqs in ((1, 1, 1), (3, 200, 1)):
+        lens = (20000, 900, 5000)
+        q, cache, table, cu = small(45, lens, nqs, bs=64)
+        args = (q.to(DEV), *(c.to(DEV) for c in cache), ints(table), ints(list(lens)), max(lens))
+        first = fa.attention_kv4(*args, cu_seqlens_q=ints(cu), max_seqlen_q=max(nqs))
+        for _ in range(5):
+            o, lse = fa.attention_kv4(*args, cu_seqlens_q=ints(cu), max_seqlen_q=max(nqs))
+            assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
 
 
 def test_wrapper_refusals_on_the_gpu():
