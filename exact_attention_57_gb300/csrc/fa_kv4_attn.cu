@@ -22,7 +22,8 @@
 // bytes first, since a register holds two tokens of one column), times the
 // scale, exactly: a value has six significant bits.  Q is brought to fp16 by
 // a power of two a row, P is rounded to fp16 (relative 2^-11, one rounding of
-// the order of the output's own), everything is summed in fp32.
+// the order of the output's own; kHeadroom keeps it from its subnormals),
+// everything is summed in fp32.
 //
 // Work is dealt in units of 128 tokens (16 for each of the 8 warps) of one
 // sequence and key head, in one line over all of them, equal shares to the
@@ -290,10 +291,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
           for (int y = 0; y < 4; ++y)
             if (t + r + (y >> 1) * 8 >= lim[nt][y & 1]) s[nt][y] = -INFINITY;
         }
-        // the exponent's offset follows the maximum only when that has grown
-        // by more than 8 (a factor of 256, which fp16 holds)
-        grow |= fmaxf(s[nt][0], s[nt][2]) > m[nt][0] + 8.f;
-        grow |= fmaxf(s[nt][1], s[nt][3]) > m[nt][1] + 8.f;
+        grow |= fmaxf(s[nt][0], s[nt][2]) > m[nt][0] + (kHeadroom + kGrow);
+        grow |= fmaxf(s[nt][1], s[nt][3]) > m[nt][1] + (kHeadroom + kGrow);
       }
       if (__any_sync(~0u, grow)) {
 #pragma unroll
@@ -305,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
             v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
             v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
             v = fmaxf(v, __shfl_xor_sync(~0u, v, 16));
-            v = fmaxf(v, m[nt][y]);
+            v = fmaxf(v - kHeadroom, m[nt][y]);
             f[y] = v == -INFINITY ? 1.f : ex2_approx(m[nt][y] - v);
             m[nt][y] = v;
             l[nt][y] *= f[y];
@@ -428,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
             *reinterpret_cast<const uint2 *>(e);
         if (col == 0)
           p.lse[static_cast<long long>(h * p.group + j) * p.total_q + sq.r0 + i] =
-              ll > 0.f ? mm * 0.6931471805599453f + logf(ll) : -INFINITY;
+              lse_of(mm, ll);
       } else {
         float *dst = part_of<D, R>(ws, blockIdx.x, begins);
         *reinterpret_cast<float4 *>(dst + row * D + col) = sum;

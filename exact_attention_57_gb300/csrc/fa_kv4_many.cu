@@ -563,11 +563,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         reg_fence32(sr[2]);
         reg_fence32(sr[3]);
         auto S = [&](int c) -> float { return __uint_as_float(sr[c >> 5][c & 31]); };
-        // The offset moves only when a row's maximum grows by more than 2^8.
-        // P is formed with the offset at hand; a row sum of at most 2^8 proves
+        // The offset moves only when a row's maximum grows by more than kGrow.
+        // P is formed with the offset at hand; a row sum of at most 2^15 proves
         // that no term is above it.  A tile's first step, and rows that have
         // seen nothing yet, take the maximum first.
-        constexpr float kSumLimit = 256.f, kGrow = 8.f;
+        constexpr float kSumLimit = 32768.f;
         bool with_max = __any_sync(~0u, m_used == -INFINITY), formed = false;
         float tsum = 0.f;
         for (;;) {
@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               part[(c >> 1) & 7] = max3f(part[(c >> 1) & 7], S(c), S(c + 1));
             const float mx = max3f(max3f(part[0], part[1], part[2]),
                                    max3f(part[3], part[4], part[5]), fmaxf(part[6], part[7]));
-            const float m_new = fmaxf(m_used, mx * sl2);
+            const float m_new = fmaxf(m_used, fmaf(mx, sl2, -kHeadroom));
             if (j == x.lo) {
               m_used = m_new;
             } else {
@@ -693,8 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (in && whole)
-          p.lse[static_cast<long long>(head) * p.total_q + x.s.r0 + i] =
-              l > 0.f ? m_used * 0.6931471805599453f + logf(l) : -INFINITY;
+          p.lse[static_cast<long long>(head) * p.total_q + x.s.r0 + i] = lse_of(m_used, l);
         if (in && !whole)
           reinterpret_cast<float2 *>(part + R * D)[r] = make_float2(m_used, l);
         tc_fence_before();

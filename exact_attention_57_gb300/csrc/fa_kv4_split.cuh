@@ -26,6 +26,21 @@ __device__ __forceinline__ Seq load_seq(const Kv4Attn &p, int b) {
   return s;
 }
 
+// Weights are 2^(s - m) with m = (the maximum so far) - kHeadroom, and m follows
+// the maximum once that has grown by more than kGrow: 2^(kHeadroom + kGrow) at
+// most, which fp16 holds, while a weight down to 2^-21 of the largest is still a
+// normal fp16 number.  Of the largest weight itself, 2^-32 is the most that
+// fp16's subnormals take from one; without the headroom it were 2^-25, which
+// showed in rows whose value comes from a weight of e^-13 alone.
+constexpr float kHeadroom = 7.f, kGrow = 8.f;
+static_assert(kHeadroom + kGrow < 16.f, "weights up to 2^15 are finite in fp16");
+
+// log(sum e^s) of a row, from its m and the sum l of its weights.
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l > 0.f ? (m + kHeadroom) * 0.6931471805599453f + logf(l * 0.0078125f) : -INFINITY;
+}
+static_assert(kHeadroom == 7.f, "lse_of divides by 2^kHeadroom");
+
 // What a CTA says to the joining kernel, at the workspace's start, about the
 // tile (sequence, key head, query tile) whose first part, but not last, is its
 // own: the tile's first query row, key head and rows (0: there is no such
@@ -42,7 +57,7 @@ __device__ __forceinline__ int cta_of(long long u, long long total, int den) {
 }
 
 // Part `which` (0: of a tile begun before the CTA, 1: of one it begins) of
-// CTA n: rows of D sums, then (maximum, sum of weights) a row.
+// CTA n: rows of D sums, then (m, sum of weights) a row.
 template <int D, int R>
 __device__ __forceinline__ float *part_of(float *ws, int n, int which) {
   return ws + kKv4MaxCtas * (sizeof(Share) / sizeof(float)) +
@@ -218,8 +233,7 @@ __global__ void __launch_bounds__(256) fa_kv4_join_kernel(const Kv4Attn p, float
   else
     *reinterpret_cast<uint32_t *>(out) = *reinterpret_cast<const uint32_t *>(e);
   if (lane == 0)
-    p.lse[static_cast<long long>(head) * p.total_q + i] =
-        l > 0.f ? m * 0.6931471805599453f + logf(l) : -INFINITY;
+    p.lse[static_cast<long long>(head) * p.total_q + i] = lse_of(m, l);
 }
 
 }  // namespace fa
