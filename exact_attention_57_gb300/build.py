@@ -9,6 +9,11 @@ statistics (registers, spills, shared memory) are kept in
 ``_build_debug/``) with ``-DFA_DEBUG``: the kernels then check the index of
 every plain global load and store and report a failed check in the status
 word (bit 32) instead of making the access.
+
+``build_binding()`` compiles ``csrc/bind/fa_torch.cpp``, the torch side of the
+serving operators' wrappers, with the host compiler into
+``exact_attention_57_gb300/_fa_torch.so``; ``build_library()`` does it too,
+beside the kernels.
 """
 from __future__ import annotations
 
@@ -24,6 +29,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfa.so")
+BIND = os.path.join(CSRC, "bind", "fa_torch.cpp")
+LIB_BIND = os.path.join(PKG, "_fa_torch.so")
 BUILD_DEBUG = os.path.join(PKG, "_build_debug")
 LIB_DEBUG = os.path.join(PKG, "libfa_debug.so")
 
@@ -51,6 +58,53 @@ def _stale(out: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _start_binding(force: bool):
+    """The binding's running compilation, or None when it is up to date or there
+    is no torch (the C library builds and works without it)."""
+    tag = os.path.join(BUILD, "fa_torch.version")  # headers and ABI are torch's
+    try:
+        import torch
+    except ImportError:
+        return None
+    version = torch.__version__ + "\n" + sys.version
+    fresh = os.path.exists(tag) and open(tag).read() == version
+    deps = [BIND, os.path.join(INCLUDE, "fa.h")]
+    if not force and fresh and not _stale(LIB_BIND, deps):
+        return None
+    import sysconfig
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    tmp = LIB_BIND + f".tmp{os.getpid()}"
+    dirs = [INCLUDE, os.path.join(base, "include"),
+            os.path.join(base, "include", "torch", "csrc", "api", "include"),
+            sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    cmd = ["g++", "-O2", "-std=c++20", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[x for d in dirs for x in ("-isystem", d)], BIND, "-o", tmp,
+           "-L", os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch_python"]
+    proc = subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    return proc, tmp, tag, version
+
+
+def _finish_binding(started) -> None:
+    if started is None:
+        return
+    proc, tmp, tag, version = started
+    out = proc.communicate()[0]
+    if proc.returncode != 0:
+        raise RuntimeError(f"g++ failed for {BIND}:\n{out[-6000:]}")
+    os.replace(tmp, LIB_BIND)
+    with open(tag, "w") as f:
+        f.write(version)
+
+
+def build_binding(force: bool = False) -> str:
+    os.makedirs(BUILD, exist_ok=True)
+    _finish_binding(_start_binding(force))
+    return LIB_BIND
+
+
 def build_library(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
     build_dir, lib = (BUILD_DEBUG, LIB_DEBUG) if debug else (BUILD, LIB)
     flags = NVCC_FLAGS + (["-DFA_DEBUG"] if debug else [])
@@ -59,6 +113,7 @@ def build_library(force: bool = False, verbose: bool = False, debug: bool = Fals
                + glob.glob(os.path.join(INCLUDE, "*.h")))
     srcs = sources()
     objs, procs = [], []
+    binding = None if debug else _start_binding(force)
     for src in srcs:
         obj = os.path.join(build_dir, os.path.basename(src)[:-3] + ".o")
         objs.append(obj)
@@ -66,6 +121,7 @@ def build_library(force: bool = False, verbose: bool = False, debug: bool = Fals
             cmd = [nvcc(), *ARCH, *flags, "-c", src, "-o", obj]
             log = open(obj + ".log", "w")
             procs.append((src, subprocess.Popen(cmd, stdout=log, stderr=subprocess.STDOUT), log))
+    _finish_binding(binding)
     failed = []
     for src, pr, log in procs:
         pr.wait()

@@ -13,13 +13,12 @@ functions raise.
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 import os
-import struct
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libfa.so")
+BIND_PATH = os.path.join(PKG, "_fa_torch.so")
 
 FA_OK = 0
 FA_ERR_INVALID_ARG = 1
@@ -470,69 +469,43 @@ def fa_fwd_kv4(q, o, lse, k_codes, k_scales, v_codes, v_scales, block_table, seq
                              k_exp, v_exp, dtype, workspace, workspace_bytes, stream)
 
 
-@functools.lru_cache(maxsize=64)  # a function of these numbers alone
 def fa_fwd_kv4_workspace(B, Hq, Hk, max_seqlen_q, d) -> int:
     return load().fa_fwd_kv4_workspace(B, Hq, Hk, max_seqlen_q, d)
 
 
 # The wrappers below run once or more in every layer of every step of a server,
-# where a launch costs about 3 us of host time: each checks what it is given
-# once, in line, and leaves the rest to the C entry point.  `stream` is the
-# integer of a cudaStream_t (default: the current one); what it has to wait for,
-# the inputs among it, is the caller's to order.
-def _call(where, dev, stream, fn, *args):
-    """fn(*args, stream) with device `dev` current (its current stream unless
-    one is given); FaError on failure."""
-    import torch
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev)
-    if torch._C._cuda_getDevice() == dev:
-        st = fn(*args, stream)
-    else:
-        with torch.cuda.device(dev):
-            st = fn(*args, stream)
-    if st != FA_OK:
-        raise FaError(st, where)
+# where a launch takes about 3 us of host time.  Their checks, allocations and
+# calls of the C entry points are compiled (csrc/bind/fa_torch.cpp): 2 to 5 us a
+# call, where the same in Python took 8 to 20.  `stream` is the integer of a
+# cudaStream_t (default: the current one); what it has to wait for, the inputs
+# among it, is the caller's to order, and what a wrapper allocates belongs to it.
+_torch = None
 
 
-def _on(stream, dev):
-    """Where a wrapper allocates: memory made while `stream` (an integer, or
-    None for the current one) is current belongs to it, and is not handed out
-    again before that stream's work on it is done."""
-    import contextlib
+def _bind():
+    """The compiled module, bound to the C entry points of load()."""
+    global _torch
+    if not os.path.exists(BIND_PATH):
+        raise RuntimeError(f"{BIND_PATH} is missing: build it with exact_attention_57_gb300.build")
+    import importlib.util
 
-    import torch
-    if stream is None or dev < 0:
-        return contextlib.nullcontext()
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=dev))
-
-
-def _like(t, stream, dev):
-    import torch
-    if stream is None:
-        return torch.empty_like(t)
-    with _on(stream, dev):
-        return torch.empty_like(t)
-
-
-def _same_device(dev, *tensors):
-    if dev < 0:
-        raise ValueError("CUDA tensors expected")
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("tensors on one CUDA device expected")
+    import torch  # noqa: F401  (the module links to its libraries)
+    spec = importlib.util.spec_from_file_location("_fa_torch", BIND_PATH)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    lib = load()
+    mod.bind(*[ctypes.cast(f, ctypes.c_void_p).value
+               for f in (lib.fa_kv_plan, lib.fa_rope, lib.fa_kv4_append, lib.fa_kv4_gather,
+                         lib.fa_fwd_kv4, lib.fa_fwd_kv4_workspace)])
+    _torch = mod
+    return mod
 
 
-def _any_dtype(t) -> int:
-    import torch
-    dt = t.dtype
-    if dt is torch.bfloat16:
-        return FA_DTYPE_BF16
-    if dt is torch.float16:
-        return FA_DTYPE_F16
-    if dt is torch.float32:
-        return FA_DTYPE_F32
-    raise ValueError(f"unsupported dtype {dt}")
+def _done(result, where):
+    """What a compiled wrapper returns: its outputs, or the status of a refusal."""
+    if result.__class__ is int:
+        raise FaError(result, where)
+    return result
 
 
 def kv_plan(cached_lens, new_lens, free_blocks, block_table, block_size: int, capacity: int,
@@ -545,40 +518,9 @@ def kv_plan(cached_lens, new_lens, free_blocks, block_table, block_size: int, ca
     Returns (slots int64 [capacity], positions int32 [capacity], cu_seqlens
     int32 [B+1], seq_lens int32 [B], counts int32 [2]: blocks needed, tokens);
     out: those five tensors, to write to.  Raises FaError on failure."""
-    import torch
-    dev, i32, i64 = cached_lens.get_device(), torch.int32, torch.int64
-    B = cached_lens.numel()
-    if out is None:
-        d = cached_lens.device
-        with _on(stream, dev):
-            out = (torch.empty(capacity, dtype=i64, device=d),
-                   torch.empty(capacity, dtype=i32, device=d),
-                   torch.empty(B + 1, dtype=i32, device=d), torch.empty(B, dtype=i32, device=d),
-                   torch.empty(2, dtype=i32, device=d))
-    slots, positions, cu, lens, counts = out
-    _same_device(dev, new_lens, free_blocks, block_table, free_head, *out)
-    for t in (cached_lens, new_lens, free_blocks, block_table, positions, cu, lens, counts):
-        if t.dtype is not i32 or not t.is_contiguous():
-            raise ValueError("contiguous int32 tensors expected (slots: int64)")
-    if slots.dtype is not i64 or not slots.is_contiguous():
-        raise ValueError("slots: a contiguous int64 tensor expected")
-    shape = block_table.shape
-    if len(shape) != 2 or shape[0] != B or new_lens.numel() != B:
-        raise ValueError("cached_lens [B], new_lens [B], block_table [B, max_blocks] expected")
-    if slots.numel() != capacity or positions.numel() != capacity or cu.numel() != B + 1 \
-            or lens.numel() != B or counts.numel() != 2:
-        raise ValueError("out: slots, positions [capacity], cu_seqlens [B+1], seq_lens [B], "
-                         "counts [2] expected")
-    head = None
-    if free_head is not None:
-        if free_head.dtype is not i32 or free_head.numel() < 1:
-            raise ValueError("free_head: an int32 tensor of one element expected")
-        head = free_head.data_ptr()
-    _call("fa_kv_plan", dev, stream, load().fa_kv_plan, cached_lens.data_ptr(),
-          new_lens.data_ptr(), free_blocks.data_ptr(), head, block_table.data_ptr(),
-          slots.data_ptr(), positions.data_ptr(), cu.data_ptr(), lens.data_ptr(),
-          counts.data_ptr(), B, shape[1], block_size, free_blocks.numel(), capacity)
-    return out
+    return _done((_torch or _bind()).kv_plan(cached_lens, new_lens, free_blocks, block_table,
+                                             block_size, capacity, free_head, out, stream),
+                 "fa_kv_plan")
 
 
 def rotary_table(inv_freq, axes=None, device="cuda"):
@@ -599,19 +541,6 @@ def rotary_table(inv_freq, axes=None, device="cuda"):
     return t.to(device)
 
 
-_pack6 = struct.Struct("=6q").pack
-
-
-def _rope_strides(x, y):
-    """Six host int64: batch, head and row strides of x, then of y."""
-    a, b = x.stride(), y.stride()
-    if a[-1] != 1 or b[-1] != 1:
-        raise ValueError("rows of contiguous elements expected")
-    if len(a) == 4:  # [B, H, N, d]
-        return _pack6(a[0], a[1], a[2], b[0], b[1], b[2])
-    return _pack6(0, a[1], a[0], 0, b[1], b[0])  # [T, H, d]
-
-
 def rotary(q, k, positions, table, interleaved: bool = False, q_out=None, k_out=None,
            stream=None, inverse: bool = False):
     """Rotary positions on q and k: [B, H, N, d] with positions int32
@@ -620,45 +549,8 @@ def rotary(q, k, positions, table, interleaved: bool = False, q_out=None, k_out=
     None.  table: rotary_table() over d_rot/2 pairs.  q_out, k_out: where to
     write (q and k themselves rotate in place; default: new tensors).
     Returns (q_out, k_out).  Raises FaError on failure."""
-    import torch
-    dev, shape, at = q.get_device(), q.shape, positions.shape
-    if len(shape) == 3:
-        N, Hq, d = shape
-        B = 1
-        fits = len(at) == 2 and at[1] == N
-    elif len(shape) == 4:
-        B, Hq, N, d = shape
-        fits = len(at) == 3 and at[1] == B and at[2] == N
-    else:
-        raise ValueError("q [B,H,N,d] or [T,H,d] expected")
-    if not fits or positions.dtype is not torch.int32 or not positions.is_contiguous():
-        raise ValueError("positions: contiguous int32 [axes, B, N] (or [axes, T]) expected")
-    if table.dtype is not torch.int64 or not table.is_contiguous():
-        raise ValueError("table: the tensor of rotary_table() expected")
-    code = _any_dtype(q)
-    if q_out is None:
-        q_out = _like(q, stream, dev)
-    elif q_out.shape != shape or q_out.dtype is not q.dtype:
-        raise ValueError("q_out: q's shape and dtype expected")
-    st = _rope_strides(q, q_out)
-    kp = ko = ks = None
-    Hk = 0
-    if k is not None:
-        kshape = k.shape
-        Hk = kshape[1]
-        if len(kshape) != len(shape) or kshape[0] != shape[0] or kshape[-1] != d \
-                or (len(shape) == 4 and kshape[2] != N) or k.dtype is not q.dtype:
-            raise ValueError("k: q's shape but for the heads, and its dtype expected")
-        if k_out is None:
-            k_out = _like(k, stream, dev)
-        elif k_out.shape != kshape or k_out.dtype is not k.dtype:
-            raise ValueError("k_out: k's shape and dtype expected")
-        kp, ko, ks = k.data_ptr(), k_out.data_ptr(), _rope_strides(k, k_out)
-    _same_device(dev, k, positions, table, q_out, k_out)
-    _call("fa_rope", dev, stream, load().fa_rope, q.data_ptr(), q_out.data_ptr(), st, Hq, kp, ko, ks,
-          Hk, positions.data_ptr(), at[0], table.data_ptr(), B, N, d, 2 * table.numel(),
-          1 if interleaved else 0, 1 if inverse else 0, code)
-    return q_out, k_out
+    return _done((_torch or _bind()).rotary(q, k, positions, table, interleaved, q_out, k_out,
+                                            stream, inverse), "fa_rope")
 
 
 def rotary_backward(dq, dk, positions, table, interleaved: bool = False, q_out=None, k_out=None,
@@ -666,21 +558,6 @@ def rotary_backward(dq, dk, positions, table, interleaved: bool = False, q_out=N
     """Gradients of rotary()'s inputs from those of its outputs: the inverse
     rotation, with rotary()'s arguments."""
     return rotary(dq, dk, positions, table, interleaved, q_out, k_out, stream, inverse=True)
-
-
-def _cache_shape(k_codes, k_scales, v_codes, v_scales):
-    """(num_blocks, Hk, block_size, d) of the cache's four arrays."""
-    import torch
-    codes = k_codes.shape
-    blocks, Hk, bs, half = codes
-    scales, u8 = (blocks, Hk, bs, half // 8), torch.uint8
-    if v_codes.shape != codes or k_scales.shape != scales or v_scales.shape != scales:
-        raise ValueError("cache: codes [blocks, Hk, block_size, d/2] and scales "
-                         "[blocks, Hk, block_size, d/16] expected")
-    for t in (k_codes, v_codes, k_scales, v_scales):
-        if t.dtype is not u8 or not t.is_contiguous():
-            raise ValueError("cache: contiguous uint8 tensors expected")
-    return blocks, Hk, bs, 2 * half
 
 
 def kv4_cache(num_blocks: int, Hk: int, block_size: int, d: int, device="cuda"):
@@ -696,22 +573,8 @@ def kv4_append(k, v, slots, k_codes, k_scales, v_codes, v_scales, k_exp: int = 0
     """Write rows k, v [T, Hk, d] (bf16, fp16 or fp32; rows of any stride, e.g.
     slices of a fused projection) into the 4-bit cache at slots int64 [T]
     (-1 skips a row).  Raises FaError on failure."""
-    import torch
-    dev = k.get_device()
-    _same_device(dev, v, slots, k_codes, k_scales, v_codes, v_scales)
-    blocks, Hk, bs, d = _cache_shape(k_codes, k_scales, v_codes, v_scales)
-    T = slots.numel()
-    if slots.dtype is not torch.int64 or not slots.is_contiguous():
-        raise ValueError("slots: a contiguous int64 tensor expected")
-    want, a, b = (T, Hk, d), k.stride(), v.stride()
-    if k.shape != want or v.shape != want or v.dtype is not k.dtype or a[2] != 1 or b[2] != 1 \
-            or (Hk > 1 and (a[1] != d or b[1] != d)):
-        raise ValueError("k, v [T, Hk, d] of one dtype with contiguous rows expected")
-    row = Hk * d  # of one token, the stride says nothing
-    _call("fa_kv4_append", dev, stream, load().fa_kv4_append, k.data_ptr(), v.data_ptr(),
-          a[0] if T > 1 else row, b[0] if T > 1 else row, slots.data_ptr(), T,
-          k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), blocks,
-          Hk, bs, d, k_exp, v_exp, _any_dtype(k))
+    _done((_torch or _bind()).kv4_append(k, v, slots, k_codes, k_scales, v_codes, v_scales, k_exp,
+                                         v_exp, stream), "fa_kv4_append")
 
 
 def kv4_gather(slots, k_codes, k_scales, v_codes, v_scales, dtype=None, k_exp: int = 0,
@@ -719,29 +582,8 @@ def kv4_gather(slots, k_codes, k_scales, v_codes, v_scales, dtype=None, k_exp: i
     """Rows of the 4-bit cache at slots int64 [R] (-1 reads zeros) as (k, v),
     each [R, Hk, d] of `dtype` (default bf16); out: those two tensors, to write
     to.  Raises FaError on failure."""
-    import torch
-    dev = slots.get_device()
-    blocks, Hk, bs, d = _cache_shape(k_codes, k_scales, v_codes, v_scales)
-    R = slots.numel()
-    if slots.dtype is not torch.int64 or not slots.is_contiguous():
-        raise ValueError("slots: a contiguous int64 tensor expected")
-    if out is None:
-        dtype = torch.bfloat16 if dtype is None else dtype
-        with _on(stream, dev):
-            k = torch.empty((R, Hk, d), dtype=dtype, device=slots.device)
-            v = torch.empty((R, Hk, d), dtype=dtype, device=slots.device)
-    else:
-        k, v = out
-        want = (R, Hk, d)
-        if k.shape != want or v.shape != want or v.dtype is not k.dtype \
-                or not k.is_contiguous() or not v.is_contiguous() \
-                or (dtype is not None and k.dtype is not dtype):
-            raise ValueError("out: two contiguous [R, Hk, d] tensors of the dtype expected")
-    _same_device(dev, k_codes, k_scales, v_codes, v_scales, k, v)
-    _call("fa_kv4_gather", dev, stream, load().fa_kv4_gather, slots.data_ptr(), R,
-          k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
-          k.data_ptr(), v.data_ptr(), blocks, Hk, bs, d, k_exp, v_exp, _any_dtype(k))
-    return k, v
+    return _done((_torch or _bind()).kv4_gather(slots, k_codes, k_scales, v_codes, v_scales, dtype,
+                                                k_exp, v_exp, out, stream), "fa_kv4_gather")
 
 
 def attention_kv4(q, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens_k,
@@ -754,49 +596,6 @@ def attention_kv4(q, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens
     int32 [B+1] (None: one query a sequence).  Returns (o [total_q, Hq, d],
     lse [Hq, total_q]).  The workspace (fa_fwd_kv4_workspace bytes) is
     allocated with torch unless given.  Raises FaError on failure."""
-    import torch
-    dev, i32 = q.get_device(), torch.int32
-    blocks, Hk, bs, d = _cache_shape(k_codes, k_scales, v_codes, v_scales)
-    shape = q.shape
-    total_q, Hq, dq = shape
-    if dq != d or not q.is_contiguous():
-        raise ValueError("q: a contiguous [total_q, Hq, d] tensor expected")
-    B, table = seq_lens_k.numel(), block_table.shape
-    if seq_lens_k.dtype is not i32 or not seq_lens_k.is_contiguous() \
-            or block_table.dtype is not i32 or not block_table.is_contiguous() \
-            or len(table) != 2 or table[0] != B:
-        raise ValueError("seq_lens_k [B], block_table [B, max_blocks]: contiguous int32 tensors "
-                         "expected")
-    cu = None
-    if cu_seqlens_q is not None:
-        if cu_seqlens_q.dtype is not i32 or cu_seqlens_q.numel() != B + 1 \
-                or not cu_seqlens_q.is_contiguous():
-            raise ValueError("cu_seqlens_q: a contiguous int32 [B+1] tensor expected")
-        cu = cu_seqlens_q.data_ptr()
-    if out is None:
-        out = _like(q, stream, dev)
-    elif out.shape != shape or out.dtype is not q.dtype or not out.is_contiguous():
-        raise ValueError("out: a contiguous tensor like q expected")
-    if lse is None:
-        with _on(stream, dev):
-            lse = torch.empty((Hq, total_q), device=q.device, dtype=torch.float32)
-    elif lse.shape != (Hq, total_q) or lse.dtype is not torch.float32 or not lse.is_contiguous():
-        raise ValueError("lse: a contiguous float32 [Hq, total_q] tensor expected")
-    if workspace is None:
-        need = fa_fwd_kv4_workspace(B, Hq, Hk, max_seqlen_q, d)
-        if need and stream is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        elif need:
-            with _on(stream, dev):
-                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    ws, ws_bytes = None, 0
-    if workspace is not None:
-        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _same_device(dev, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens_k, cu_seqlens_q,
-                 out, lse, workspace)
-    _call("fa_fwd_kv4", dev, stream, load().fa_fwd_kv4, q.data_ptr(), out.data_ptr(), lse.data_ptr(),
-          k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
-          block_table.data_ptr(), seq_lens_k.data_ptr(), cu, B, Hq, Hk, total_q, max_seqlen_q,
-          max_seqlen_k, blocks, bs, table[1], d, 1.0 / math.sqrt(d) if scale is None else scale,
-          1 if causal else 0, k_exp, v_exp, _any_dtype(q), ws, ws_bytes)
-    return out, lse
+    return _done((_torch or _bind()).attention_kv4(
+        q, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens_k, max_seqlen_k, cu_seqlens_q,
+        max_seqlen_q, scale, causal, k_exp, v_exp, (out, lse), workspace, stream), "fa_fwd_kv4")
