@@ -82,7 +82,7 @@ def _start_binding(force: bool):
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *[x for d in dirs for x in ("-isystem", d)], BIND, "-o", tmp,
            "-L", os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
-           "-ltorch_python"]
+           "-ltorch_cuda", "-ltorch_python"]
     proc = subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
     return proc, tmp, tag, version
 

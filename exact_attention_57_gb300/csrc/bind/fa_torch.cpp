@@ -8,9 +8,9 @@
 // library, so that this module and ctypes share one libfa.so.
 #include <Python.h>
 
+#include <ATen/ExpandUtils.h>
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
-#include <ATen/ops/empty_like.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -79,6 +79,21 @@ struct Call {
       stream = reinterpret_cast<cudaStream_t>(static_cast<uintptr_t>(integer(s)));
       own.emplace(c10::cuda::getStreamFromExternal(stream, static_cast<c10::DeviceIndex>(dev)));
     }
+  }
+  // Memory from torch's allocator, without the dispatcher (half the time of
+  // at::empty for tensors that are plain outputs).
+  Tensor make(at::IntArrayRef sizes, at::ScalarType type) const {
+    return Tensor(at::detail::empty_cuda(
+        sizes, type, at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(dev)), std::nullopt));
+  }
+  // One like x: its strides, or dense ones in their order.
+  Tensor like(const Tensor &x) const {
+    if (x.is_contiguous()) return make(x.sizes(), x.scalar_type());
+    const at::Device d(at::kCUDA, static_cast<c10::DeviceIndex>(dev));
+    if (x.is_non_overlapping_and_dense())
+      return Tensor(at::detail::empty_strided_cuda(x.sizes(), x.strides(), x.scalar_type(), d));
+    return Tensor(at::detail::empty_strided_cuda(
+        x.sizes(), at::infer_dense_strides(x.sizes(), x.strides()), x.scalar_type(), d));
   }
   void here(const Tensor &t) const {
     if (!t.is_cuda() || t.get_device() != dev)
@@ -195,8 +210,7 @@ PyObject *kv_plan(PyObject *const *a) {
     }
   } else {
     for (int i = 0; i < 5; ++i)
-      out[i] = at::empty({sizes[i] > 0 ? sizes[i] : 0},
-                         table.options().dtype(i == 0 ? at::kLong : at::kInt));
+      out[i] = call.make({sizes[i] > 0 ? sizes[i] : 0}, i == 0 ? at::kLong : at::kInt);
   }
   const int st = run(p_kv_plan, ptr<int>(cached), ptr<int>(fresh), ptr<int>(free_blocks), head,
                      ptr<int>(table), ptr<long long>(out[0]), ptr<int>(out[1]), ptr<int>(out[2]),
@@ -243,7 +257,7 @@ PyObject *rotary(PyObject *const *a) {
   flat(table, at::kLong, "table: the tensor of rotary_table() expected");
   const int code = dtype_code(q);
   auto output = [&](const Tensor &x, PyObject *o) -> Tensor {
-    if (none(o)) return at::empty_like(x);
+    if (none(o)) return call.like(x);
     const Tensor &y = tensor(o, "q_out, k_out: tensors expected");
     call.here(y);
     if (y.sizes() != x.sizes() || y.scalar_type() != x.scalar_type())
@@ -343,9 +357,9 @@ PyObject *gather(PyObject *const *a) {
     if (given && out[0].scalar_type() != type)
       throw Bad{"out: two contiguous [R, Hk, d] tensors of the dtype expected"};
     if (!given)
-      for (Tensor &t : out) t = at::empty({R, c.Hk, c.d}, slots.options().dtype(type));
+      for (Tensor &t : out) t = call.make({R, c.Hk, c.d}, type);
   } else if (!given) {
-    for (Tensor &t : out) t = at::empty({R, c.Hk, c.d}, slots.options().dtype(at::kBFloat16));
+    for (Tensor &t : out) t = call.make({R, c.Hk, c.d}, at::kBFloat16);
   }
   const int code = dtype_code(out[0]);
   const int st = run(p_gather, ptr<long long>(slots), R, ptr(*c.kc), ptr(*c.ks), ptr(*c.vc),
@@ -401,7 +415,7 @@ PyObject *attention(PyObject *const *a) {
   PyObject *const *g = a + 14;  // (out, lse), workspace
   PyObject *po = PyTuple_GET_ITEM(g[0], 0), *pl = PyTuple_GET_ITEM(g[0], 1);
   if (none(po)) {
-    out = at::empty_like(q);
+    out = call.like(q);
   } else {
     out = tensor(po, "out: a contiguous tensor like q expected");
     call.here(out);
@@ -409,7 +423,7 @@ PyObject *attention(PyObject *const *a) {
       throw Bad{"out: a contiguous tensor like q expected"};
   }
   if (none(pl)) {
-    lse = at::empty({Hq, total}, q.options().dtype(at::kFloat));
+    lse = call.make({Hq, total}, at::kFloat);
   } else {
     lse = tensor(pl, "lse: a contiguous float32 [Hq, total_q] tensor expected");
     call.here(lse);
@@ -421,7 +435,7 @@ PyObject *attention(PyObject *const *a) {
   if (none(g[1])) {
     ws_bytes = p_workspace(B, Hq, c.Hk, max_q, c.d);
     if (ws_bytes > 0)
-      ws = at::empty({static_cast<int64_t>(ws_bytes)}, q.options().dtype(at::kByte));
+      ws = call.make({static_cast<int64_t>(ws_bytes)}, at::kByte);
   } else {
     ws = tensor(g[1], "workspace: a tensor expected");
     call.here(ws);
