@@ -13,9 +13,10 @@
 // [-1, 1) half turns, go to sincospif.
 //
 // Memory bounds it: 18432 tokens of 32 bf16 heads of 128 elements (302 MB in and
-// out) take 52 us, 5.8 TB/s or 86% of the measured copy rate.  A thread issues
-// one head's loads ahead of its stores; four heads' together (111 registers, so
-// half the warps) took 75 us, streaming cache hints changed nothing.
+// out) take 50 us, 6.0 TB/s or 89% of the measured copy rate; 64 tokens take the
+// 2.5 us of a launch.  A thread issues one head's loads ahead of its stores; four
+// heads' together (111 registers, so half the warps) took 75 us, one head ahead
+// 53 to 64, streaming cache hints changed nothing.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -44,9 +45,13 @@ struct alignas(sizeof(T) * V) Vec {
 
 // One thread: V pairs of one row (or, behind the rotated part, V elements to
 // copy), for `hpt` heads of q and k, so that its sines and cosines serve them
-// all.  INTER: pair i is elements (2i, 2i + 1), else (i, i + d_rot / 2).
-template <typename T, int V, bool INTER>
-__global__ void __launch_bounds__(kThreads, 6)
+// all.  INTER: pair i is elements (2i, 2i + 1), else (i, i + d_rot / 2).  TAIL:
+// there are elements to copy; a warp's threads then load together before they
+// part (apart, a partial rotation of fp32 rows took 58 us instead of 45), which
+// full rotations do without (50 us instead of 57).  Eight pairs and a tail spill
+// at six CTAs an SM (34 us, 31 at five).
+template <typename T, int V, bool INTER, bool TAIL>
+__global__ void __launch_bounds__(kThreads, V == 8 && TAIL ? 5 : 6)
     fa_rope_kernel(const RopeParams p, int nvec, int hpt) {
   griddep_wait();
   griddep_launch_dependents();
@@ -57,8 +62,17 @@ __global__ void __launch_bounds__(kThreads, 6)
   const int half = p.d_rot / 2, nrot = half / V;
   const long long b = row / p.N, n = row - b * p.N;
   const int h0 = blockIdx.y * hpt, h1 = min(h0 + hpt, p.q.heads + p.k.heads);
-  const bool rot = vec < nrot;
-
+  const bool rot = !TAIL || vec < nrot;
+  const int e0 = !rot ? p.d_rot + (vec - nrot) * V : INTER ? vec * 2 * V : vec * V;
+  const int e1 = INTER ? e0 + V : e0 + half;
+  Vec<T, V> x, y;
+  auto load = [&](int h) {
+    const RopeTensor &t = h < p.q.heads ? p.q : p.k;
+    const T *in = static_cast<const T *>(t.in) + b * t.ib +
+                  (h < p.q.heads ? h : h - p.q.heads) * t.ih + n * t.in_row;
+    x = *reinterpret_cast<const Vec<T, V> *>(in + e0);
+    if (rot) y = *reinterpret_cast<const Vec<T, V> *>(in + e1);
+  };
   float c[V], s[V];
   if (rot) {
 #pragma unroll
@@ -74,15 +88,11 @@ __global__ void __launch_bounds__(kThreads, 6)
     }
   }
   for (int h = h0; h < h1; ++h) {
-    const bool is_q = h < p.q.heads;
-    const RopeTensor &t = is_q ? p.q : p.k;
-    const int hh = is_q ? h : h - p.q.heads;
-    const T *in = static_cast<const T *>(t.in) + b * t.ib + hh * t.ih + n * t.in_row;
-    T *out = static_cast<T *>(t.out) + b * t.ob + hh * t.oh + n * t.out_row;
+    load(h);
+    const RopeTensor &t = h < p.q.heads ? p.q : p.k;
+    T *out = static_cast<T *>(t.out) + b * t.ob + (h < p.q.heads ? h : h - p.q.heads) * t.oh +
+             n * t.out_row;
     if (rot) {
-      const int e0 = INTER ? vec * 2 * V : vec * V, e1 = INTER ? e0 + V : e0 + half;
-      const Vec<T, V> x = *reinterpret_cast<const Vec<T, V> *>(in + e0);
-      const Vec<T, V> y = *reinterpret_cast<const Vec<T, V> *>(in + e1);
       Vec<T, V> u, w;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
@@ -103,8 +113,7 @@ __global__ void __launch_bounds__(kThreads, 6)
       *reinterpret_cast<Vec<T, V> *>(out + e0) = u;
       *reinterpret_cast<Vec<T, V> *>(out + e1) = w;
     } else {
-      const int e = p.d_rot + (vec - nrot) * V;
-      *reinterpret_cast<Vec<T, V> *>(out + e) = *reinterpret_cast<const Vec<T, V> *>(in + e);
+      *reinterpret_cast<Vec<T, V> *>(out + e0) = x;
     }
   }
 }
@@ -140,8 +149,11 @@ cudaError_t launch_vec(const RopeParams &p, int num_sms, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return p.interleaved ? cudaLaunchKernelEx(&cfg, fa_rope_kernel<T, V, true>, p, nvec, hpt)
-                       : cudaLaunchKernelEx(&cfg, fa_rope_kernel<T, V, false>, p, nvec, hpt);
+  if (p.d_rot < p.d)
+    return p.interleaved ? cudaLaunchKernelEx(&cfg, fa_rope_kernel<T, V, true, true>, p, nvec, hpt)
+                         : cudaLaunchKernelEx(&cfg, fa_rope_kernel<T, V, false, true>, p, nvec, hpt);
+  return p.interleaved ? cudaLaunchKernelEx(&cfg, fa_rope_kernel<T, V, true, false>, p, nvec, hpt)
+                       : cudaLaunchKernelEx(&cfg, fa_rope_kernel<T, V, false, false>, p, nvec, hpt);
 }
 
 template <typename T>
@@ -151,6 +163,9 @@ cudaError_t launch_type(const RopeParams &p, int num_sms, cudaStream_t s) {
     return p.d_rot / 2 % v == 0 && (p.d - p.d_rot) % v == 0 && aligned(p.q, v * es, es) &&
            aligned(p.k, v * es, es);
   };
+  // 16-byte accesses where strides and addresses allow them, 8-byte ones where
+  // only those (18432 bf16 tokens: 50 us, 56 with 8 bytes, 131 an element at a
+  // time; 6001 fp32 tokens of 40 heads: 42 and 61 us)
   if (fits(W)) return launch_vec<T, W>(p, num_sms, s);
   if (es == 2 && fits(4)) return launch_vec<T, 4>(p, num_sms, s);
   return launch_vec<T, 1>(p, num_sms, s);
