@@ -25,7 +25,7 @@
 // the order of the output's own; kHeadroom keeps it from its subnormals),
 // everything is summed in fp32.
 //
-// Work is dealt in units of 128 tokens (16 for each of the 8 warps) of one
+// Work is dealt in units of 128 tokens (16 for each of 8 warps) of one
 // sequence and key head, in one line over all of them, equal shares to the
 // CTAs of one resident wave: ragged lengths and few long sequences balance
 // alike.  A sequence and key head begins with kLead units that stand for what
@@ -46,8 +46,21 @@
 namespace fa {
 namespace {
 
-constexpr int kThreads = 256, kWarps = 8;
-constexpr int kUnit = 16 * kWarps;  // tokens of one unit
+// Warps of a CTA, resident CTAs, and the units that stand for a sequence's cost
+// beside its keys, by rows (8 NT) and head dim.  Measured, in us, at 64 sequences
+// of up to 8192 keys and 8 key heads, D = 128 unless said:
+//   8 rows   two CTAs of 8 warps 70, three (with Q in shared memory) 93; D = 64:
+//            50, three CTAs 50; lead 0/1/2/3/5/8: 92/84/79/78/79/81
+//   16 rows  the registers of two CTAs would spill; lead 3/4/6/8: 121/117/110/111;
+//            D = 64: one CTA 89, two 63, lead 4/6/8: 63/64/65
+//   32 rows  lead 3/4/6/8: 266/258/259/263, two CTAs of 4 warps 246, but 18 instead
+//            of 15 for one sequence of 4096; D = 64: 8 warps 109, twice 4 101
+template <int NT, int D>
+struct Shape {
+  static constexpr int kWarps = NT == 4 && D == 64 ? 4 : 8;
+  static constexpr int kCtas = NT == 1 || D == 64 ? 2 : 1;
+  static constexpr int kLead = NT == 1 ? 3 : NT == 2 && D == 64 ? 4 : 6;
+};
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -77,11 +90,10 @@ __device__ __forceinline__ void load_words(uint32_t (&x)[W], const uint8_t *p) {
     asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(x[0]) : "l"(p));
 }
 
-constexpr int kLead = 3;
-
 // Units of one key head of a sequence, kLead of them ahead of its keys; a
 // sequence without keys still has one more (its rows get their zeros), one
 // with more than `rows` rows none (the kernel for many queries takes it).
+template <int kUnit, int kLead>
 __device__ __forceinline__ int units_of(const Seq &s, int group, int rows) {
   if (s.nq == 0 || static_cast<long long>(s.nq) * group > rows) return 0;
   return kLead + max(1, (s.nk + kUnit - 1) / kUnit);
@@ -104,13 +116,15 @@ __device__ __forceinline__ float2 pair_f32(uint32_t x) {
 
 template <int NT, int D>
 constexpr int smem_bytes() {
-  return kWarps * NT * 8 * (D + 4 + 2) * 4;
+  return Shape<NT, D>::kWarps * NT * 8 * (D + 4 + 2) * 4;
 }
 
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(Shape<NT, D>::kWarps * 32, Shape<NT, D>::kCtas)
     fa_kv4_attn_kernel(const Kv4Attn p, float *ws) {
   constexpr int R = NT * 8;              // rows of the tile
+  constexpr int kWarps = Shape<NT, D>::kWarps, kThreads = kWarps * 32, kUnit = kWarps * 16;
+  constexpr int kLead = Shape<NT, D>::kLead;
   constexpr int KS = D / 16;             // k steps of S^T, m tiles of O^T
   constexpr int LD = D + 4;
   extern __shared__ float smem[];
@@ -127,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
   const Place at = find_unit<kWarps>(
       p,
       [&](int b) {
-        return static_cast<long long>(units_of(load_seq(p, b), p.group, R)) * p.c.Hk;
+        return static_cast<long long>(units_of<kUnit, kLead>(load_seq(p, b), p.group, R)) * p.c.Hk;
       },
       blockIdx.x, &den, &u, s_sums, s_warp);
   Share share = {0, 0, 0, 0};
@@ -140,13 +154,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
 
   int b = at.b;
   Seq sq = load_seq(p, b);
-  int n_units = units_of(sq, p.group, R);
+  int n_units = units_of<kUnit, kLead>(sq, p.group, R);
   const long long into = u - at.before;
   int h = static_cast<int>(into / n_units), unit = static_cast<int>(into - static_cast<long long>(h) * n_units);
   while (u < u1) {
     while (n_units == 0) {  // another sequence of this kernel follows, since u < total
       sq = load_seq(p, ++b);
-      n_units = units_of(sq, p.group, R);
+      n_units = units_of<kUnit, kLead>(sq, p.group, R);
       h = 0;
     }
     // units [t_lo, t_hi) of the n_units - kLead with keys
@@ -446,18 +460,18 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
 template <typename T, int D, int NT>
 cudaError_t launch(const Kv4Attn &p, float *ws, int num_sms, cudaStream_t s) {
   static std::atomic<unsigned long long> attr_done{0};
-  constexpr int smem = smem_bytes<NT, D>();
+  constexpr int smem = smem_bytes<NT, D>(), kUnit = Shape<NT, D>::kWarps * 16;
   cudaError_t e = smem_attr_once(fa_kv4_attn_kernel<T, D, NT>, smem, &attr_done);
   if (e != cudaSuccess) return e;
   // one resident wave, no more CTAs than there can be units
-  long long ctas = static_cast<long long>(num_sms > 0 ? num_sms : 1) * (NT == 1 ? 2 : 1);
+  long long ctas = static_cast<long long>(num_sms > 0 ? num_sms : 1) * Shape<NT, D>::kCtas;
   const long long most = static_cast<long long>(p.B) * p.c.Hk *
                          (p.max_k < kUnit ? 1 : (p.max_k + kUnit - 1) / kUnit);
   if (ctas > most) ctas = most;
   if (ctas > kKv4MaxCtas) ctas = kKv4MaxCtas;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Shape<NT, D>::kWarps * 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -468,6 +482,7 @@ cudaError_t launch(const Kv4Attn &p, float *ws, int num_sms, cudaStream_t s) {
   e = cudaLaunchKernelEx(&cfg, fa_kv4_attn_kernel<T, D, NT>, p, ws);
   if (e != cudaSuccess || ctas == 1) return e;
   const long long rows = static_cast<long long>(p.max_q) * p.group;
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.gridDim = dim3(static_cast<unsigned>(ctas - 1),
                      static_cast<unsigned>((min(rows, NT * 8LL) + kJoinRows - 1) / kJoinRows));
   cfg.dynamicSmemBytes = 0;
@@ -483,10 +498,14 @@ cudaError_t launch_rows(const Kv4Attn &p, int rows, float *ws, int num_sms, cuda
 
 }  // namespace
 
-int kv4_tile_rows(int group, int max_q) {
+int kv4_tile_rows(int group, int max_q, int d, long long keys) {
   auto fit = [](long long n) { return n <= 8 ? 8 : n <= 16 ? 16 : n <= 32 ? 32 : 0; };
-  const int all = fit(static_cast<long long>(group) * max_q);
-  return all ? all : fit(group);
+  int rows = fit(static_cast<long long>(group) * max_q);
+  if (rows == 0) rows = fit(group);
+  // 32 rows of 128 elements fill the registers; where there is work for every
+  // tile of the other kernel, that is faster (8 heads, 32 rows: 1 x 131071 keys 99
+  // us here, 93 there; 64 x 8192 259 and 212; 16 x 4096 45 and 52; 1 x 1023 14 and 18)
+  return rows == 32 && d == 128 && keys >= 1000000 ? 0 : rows;
 }
 
 size_t kv4_workspace(int rows, int d) {

@@ -738,7 +738,7 @@ cudaError_t launch(const Kv4Attn &p, const ManyCtl &ctl, float *ws, int num_sms,
   e = cudaLaunchKernelEx(&cfg, fa_kv4_many_kernel<T, D>, p, ctl, ws);
   if (e != cudaSuccess || ctas == 1) return e;
   cfg.gridDim = dim3(static_cast<unsigned>(ctas - 1), R / kJoinRows);
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, fa_kv4_join_kernel<T, D, R>, p, ws);
 }

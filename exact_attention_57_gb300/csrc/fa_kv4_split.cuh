@@ -149,11 +149,11 @@ __device__ Place find_unit(const Kv4Attn &p, F units, int num, int *den, long lo
 // Row r of a tile is head r % group of its token r / group.  The eight warps
 // share the parts, each with a maximum of its own, so that a tile split over
 // the whole grid costs a few rounds of loads.
-constexpr int kJoinRows = 4;
+constexpr int kJoinRows = 4, kJoinThreads = 256;
 
 template <typename T, int D, int R>
-__global__ void __launch_bounds__(256) fa_kv4_join_kernel(const Kv4Attn p, float *ws) {
-  constexpr int kWarps = 8;
+__global__ void __launch_bounds__(kJoinThreads) fa_kv4_join_kernel(const Kv4Attn p, float *ws) {
+  constexpr int kWarps = kJoinThreads / 32;
   constexpr int W = D / 32;  // columns a lane
   __shared__ float s_sum[kWarps][kJoinRows][D];
   __shared__ float s_m[kWarps][kJoinRows], s_l[kWarps][kJoinRows];

@@ -83,11 +83,13 @@ struct Kv4Attn {
 // Sequences with at most `rows` rows (queries x group) go through
 // launch_kv4_attn's tile of that many rows, longer ones through
 // launch_kv4_many.  kv4_tile_rows: 8, 16 or 32, the smallest that holds the
-// longest sequence, else the smallest that holds one query; 0: none does.
+// longest sequence, else the smallest that holds one query; 0: none, either
+// because none does or because the other kernel is faster at so many keys (the
+// longest sequence's, times sequences and key heads).
 constexpr int kKv4MaxCtas = 304;   // two on each of 152 SMs
 constexpr int kKv4ManyCtas = 152;  // launch_kv4_many: one on each
 constexpr int kKv4ManyRows = 128;  // and tiles of that many rows, so group <= 128
-int kv4_tile_rows(int group, int max_q);
+int kv4_tile_rows(int group, int max_q, int d, long long keys);
 size_t kv4_workspace(int rows, int d);  // of either kernel, by its rows
 cudaError_t launch_kv4_attn(const Kv4Attn &p, int rows, int dtype, float *ws, int num_sms,
                             cudaStream_t s);

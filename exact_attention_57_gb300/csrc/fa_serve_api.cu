@@ -276,10 +276,11 @@ extern "C" int fa_kv4_gather(const long long *slots, int R, const void *k_codes,
 
 extern "C" unsigned long long fa_fwd_kv4_workspace(int B, int Hq, int Hk, int max_seqlen_q, int d) {
   if (B < 1 || Hq < 1 || Hk < 1 || Hq % Hk != 0 || max_seqlen_q < 1 || d < 1) return 0;
-  const int group = Hq / Hk, tile = fa::kv4_tile_rows(group, max_seqlen_q);
+  const int group = Hq / Hk, tile = fa::kv4_tile_rows(group, max_seqlen_q, d, 0);
   if (group > fa::kKv4ManyRows) return 0;
   const size_t few = tile ? fa::kv4_workspace(tile, d) : 0;
-  const size_t many = static_cast<long long>(max_seqlen_q) * group > tile
+  // (with many keys the other kernel may take what 32 rows hold)
+  const size_t many = static_cast<long long>(max_seqlen_q) * group > tile || tile == 32
                           ? fa::kv4_workspace(fa::kKv4ManyRows, d)
                           : 0;
   return few > many ? few : many;
@@ -346,7 +347,8 @@ extern "C" int fa_fwd_kv4(const void *q, void *o, float *lse, const void *k_code
   p.scale_log2 = scale_log2;
   p.v_mul = static_cast<float>(std::ldexp(1.0, v_exp));
   p.causal = causal;
-  const int tile = fa::kv4_tile_rows(p.group, max_seqlen_q);
+  const int tile =
+      fa::kv4_tile_rows(p.group, max_seqlen_q, d, static_cast<long long>(B) * Hk * max_seqlen_k);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int sms = fa::api_sm_count();
   float *ws = static_cast<float *>(workspace);

@@ -709,6 +709,21 @@ def test_many_queries_report_a_wait_that_runs_out():
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("nqs", [(4, 2), (1, 3), (40, 4)])
+def test_attention_of_32_rows_and_a_bound_of_many_keys(nqs):
+    """Rows that fill a tile go to the kernel for many queries when max_seqlen_k
+    leaves room for a million keys, whatever the lengths are; the workspace is
+    the same."""
+    lens = (700, 33)
+    q, cache, table, cu = small(57, lens, nqs, Hq=16, Hk=2)
+    need = fa.fa_fwd_kv4_workspace(2, 16, 2, max(nqs), 128)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)
+    for max_k in (700, 1 << 20):
+        o, lse = call(q, cache, table, lens, cu, nqs, max_k=max_k, workspace=ws)
+        check_attention(q, cache, table, lens, nqs, 16, 128, 128 ** -0.5, True, o, lse,
+                        torch.bfloat16, label=str(max_k))
+
+
 def test_repeated_calls_are_the_same_bit_for_bit():
     """Parts are joined in a fixed order: no result depends on which CTA was
     first, at one query a sequence and at many."""
