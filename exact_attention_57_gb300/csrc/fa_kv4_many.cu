@@ -26,6 +26,15 @@
 // conversions, 512 multiplications and 128 16-byte stores a warp, which the
 // eight warps of their own hide beside them.
 //
+// Two prompts' chunks of 2048 queries (32 query heads on 8 key heads of 128,
+// causal) take 454 us, 1040 TFLOP/s or 53% of the measured bf16 rate; 1024 queries
+// on 65536 keys 906 us, 1200 TFLOP/s.  Without expanding the codes the first takes
+// 400: what bounds it is the softmax warps and the tensor pipe (46% busy) waiting
+// for each other.  A tile of 256 rows as two halves that take turns took 641 us (64
+// registers fewer a softmax thread), masks applied in registers 475, queries brought
+// by the expanding warps 612, K and V expanded by the same four warps (with those
+// queries) 695.
+//
 // Every wait is bounded; on expiry the CTA raises its abort flag, records the
 // role in the status word, drains its products, frees tensor memory and ends.
 #include <atomic>

@@ -80,7 +80,9 @@ __device__ Place find_unit(const Kv4Attn &p, F units, int num, int *den, long lo
   constexpr int kThreads = kWarps * 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   Place at = {0, 0, 0};
-  if (p.B <= 32) {  // one a lane: every warp finds it by itself
+  if (p.B <= 32) {
+    // one a lane: every warp finds it by itself (0.4 us less than by way of shared
+    // memory, of 8.0 for one sequence of 1023 keys, 16.8 for 16 of up to 3001)
     const long long n = lane < p.B ? units(lane) : 0;
     long long incl = n;
     for (int o = 1; o < 32; o *= 2) {
@@ -148,7 +150,9 @@ __device__ Place find_unit(const Kv4Attn &p, F units, int num, int *den, long lo
 // parts 0 of n + 1, n + 2, ... up to the one that ends it), four rows of it.
 // Row r of a tile is head r % group of its token r / group.  The eight warps
 // share the parts, each with a maximum of its own, so that a tile split over
-// the whole grid costs a few rounds of loads.
+// the whole grid costs a few rounds of loads: about 4 us, a launch and two
+// dependent loads (the counts of finished parts that would let the last CTA join
+// them would have to be zero before the call, and the workspace is the caller's).
 constexpr int kJoinRows = 4, kJoinThreads = 256;
 
 template <typename T, int D, int R>

@@ -468,15 +468,21 @@ FA_API int fa_kv4_gather(const long long *slots, int R, const void *k_codes, con
  *               takes its tokens out of the softmax.
  * max_seqlen_q, max_seqlen_k  bounds on the lengths; longer sequences are cut
  *               to them (max_blocks * block_size bounds the keys too).  A loose
- *               max_seqlen_k costs nothing.
+ *               max_seqlen_k costs little: it is what the kernel is chosen by
+ *               where there are 17 to 32 queries a key head, and bounds the grid.
  * causal        1: query i of n_q sees key j iff j <= n_k - n_q + i (aligned
  *               at the end, as the new tokens are the last cached ones); 0:
  *               all keys.  A row that sees no key gets O = 0, LSE = -inf.
- * d 64 or 128 (else FA_ERR_UNSUPPORTED); fp32 types are FA_ERR_UNSUPPORTED.
- * workspace     fa_fwd_kv4_workspace(...) bytes, 256-byte aligned (NULL when
- *               that is 0).  Calls that share it must not overlap on the GPU.
+ * d 64 or 128, Hq/Hk at most 128 (else FA_ERR_UNSUPPORTED); fp32 types are
+ * FA_ERR_UNSUPPORTED.  A query times a key is exact, scores, softmax and sums
+ * are fp32, and a weight is rounded to fp16 (half a step, 2^-11 of itself) for
+ * its product with the values.
+ * workspace     fa_fwd_kv4_workspace(...) bytes, 256-byte aligned, whatever
+ *               they hold.  Calls that share it must not overlap on the GPU.
  * The lengths, offsets and tables are read on the device and not checked on
- * the host; whatever they hold, no access leaves the buffers.
+ * the host; whatever they hold, no access leaves the buffers.  Sequences of
+ * more than 32 rows (queries times Hq/Hk) run a kernel whose waits are bounded:
+ * one that runs out is reported through fa_fwd_status.
  */
 FA_API int fa_fwd_kv4(const void *q, void *o, float *lse, const void *k_codes, const void *k_scales,
                const void *v_codes, const void *v_scales, const int *block_table,
@@ -485,7 +491,8 @@ FA_API int fa_fwd_kv4(const void *q, void *o, float *lse, const void *k_codes, c
                int max_blocks, int d, float scale, int causal, int k_exp, int v_exp, int dtype,
                void *workspace, unsigned long long workspace_bytes, void *stream);
 
-/* Bytes of workspace fa_fwd_kv4 needs; 0 for invalid arguments. */
+/* Bytes of workspace fa_fwd_kv4 needs: a function of Hq/Hk, max_seqlen_q and d,
+ * not of the lengths or the batch; 0 for invalid or unsupported arguments. */
 FA_API unsigned long long fa_fwd_kv4_workspace(int B, int Hq, int Hk, int max_seqlen_q, int d);
 
 /*
@@ -518,7 +525,7 @@ FA_API int fa_fwd_host(const void *q_h, const void *k_h, const void *v_h,
  * 0 when every kernel finished normally; otherwise bit r set means a warp of
  * role r gave up on a bounded wait (1 = TMA producer, 2 = MMA issuer,
  * 4 = softmax/epilogue warps, 8 = fault injected by the test hook,
- * 16 = shared memory not aligned as the backward kernel needs, 32 = an index
+ * 16 = shared memory not aligned as the kernel needs, 32 = an index
  * check of the debug build failed and the access was skipped).
  * Returns FA_OK, FA_ERR_DEVICE_TIMEOUT (word != 0) or FA_ERR_CUDA.
  */
@@ -532,8 +539,8 @@ FA_API int fa_version(void);
 
 /*
  * fa_set_test_hooks — testing aid, process-wide.
- * skip_v_load != 0 makes the next launches of the tensor-core kernels skip the
- * first V-tile load, so the MMA issuer's bounded wait runs out and the kernel
+ * skip_v_load != 0 makes the next launches of the tensor-core kernels (of
+ * fa_fwd_kv4, the one for many queries) skip the first V-tile load, so the MMA issuer's bounded wait runs out and the kernel
  * returns through its error path (status bit 8 plus the role bits).
  * wait_limit_ns sets the bounded-wait limit in nanoseconds (0 = default,
  * 2e9).  Returns FA_OK.
