@@ -93,6 +93,8 @@ def _finish_binding(started) -> None:
     proc, tmp, tag, version = started
     out = proc.communicate()[0]
     if proc.returncode != 0:
+        if os.path.exists(tmp):
+            os.unlink(tmp)
         raise RuntimeError(f"g++ failed for {BIND}:\n{out[-6000:]}")
     os.replace(tmp, LIB_BIND)
     with open(tag, "w") as f:

@@ -1,11 +1,11 @@
 """ctypes binding of ``libfa.so`` (the C ABI in include/fa.h).
 
 The ``fa_*`` functions mirror the C entry points one to one and only marshal
-arguments.  ``attention``, ``attention_varlen``, ``attention_backward`` and the serving
-operators (``kv_plan``, ``rotary``, ``kv4_append``, ``kv4_gather``,
-``attention_kv4``) are convenience wrappers for torch tensors: they allocate outputs and workspaces
-with torch (device memory is the only thing torch provides here) and call the
-C entry points.
+arguments.  ``attention``, ``attention_varlen``, ``attention_backward`` and the
+serving operators (``kv_plan``, ``rotary``, ``kv4_append``, ``kv4_gather``,
+``attention_kv4``) are convenience wrappers for torch tensors: they allocate
+outputs and workspaces with torch (device memory is the only thing torch
+provides here) and call the C entry points.
 
 There is no fallback: if the library is missing or its call fails, these
 functions raise.
@@ -519,7 +519,8 @@ def kv_plan(cached_lens, new_lens, free_blocks, block_table, block_size: int, ca
     int32 [B+1], seq_lens int32 [B], counts int32 [2]: blocks needed, tokens);
     out: those five tensors, to write to.  Raises FaError on failure."""
     return _done((_torch or _bind()).kv_plan(cached_lens, new_lens, free_blocks, block_table,
-                                             block_size, capacity, free_head, out, stream),
+                                             block_size, capacity, free_head,
+                                             out if out is None else tuple(out), stream),
                  "fa_kv_plan")
 
 
@@ -583,7 +584,8 @@ def kv4_gather(slots, k_codes, k_scales, v_codes, v_scales, dtype=None, k_exp: i
     each [R, Hk, d] of `dtype` (default bf16); out: those two tensors, to write
     to.  Raises FaError on failure."""
     return _done((_torch or _bind()).kv4_gather(slots, k_codes, k_scales, v_codes, v_scales, dtype,
-                                                k_exp, v_exp, out, stream), "fa_kv4_gather")
+                                                k_exp, v_exp, out if out is None else tuple(out),
+                                                stream), "fa_kv4_gather")
 
 
 def attention_kv4(q, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens_k,

@@ -755,3 +755,117 @@ def test_wrapper_refusals_on_the_gpu():
                   fa.rotary_table([1.0], device=DEV))
     with pytest.raises(fa.FaError):
         fa.attention_kv4(q.float().to(DEV), *dev, ints(table), ints([90, 33]), 90)
+
+
+def test_wrapper_arguments_one_by_one():
+    """Every tensor of every wrapper in a wrong type, shape, layout or place is
+    refused, and the same call with the right one works before and after."""
+    q, cache, table, cu = small(53)
+    dev = [c.to(DEV) for c in cache]
+    qd = q.to(DEV)
+    k = torch.randn(2, 2, 128, device=DEV).bfloat16()
+
+    def refused(fn, args, at, bad, **kw):
+        fn(*args, **kw)
+        for b in bad:
+            with pytest.raises((ValueError, fa.FaError)):
+                fn(*args[:at], b, *args[at + 1:], **kw)
+        fn(*args, **kw)
+
+    def spoiled(t):
+        wide = torch.stack([t, t], -1)[..., 0]  # strided
+        return [t.cpu(), t.double(), wide if t.numel() > 1 else t.cpu(), t[:-1], 7, None]
+
+    attn = (qd, *dev, ints(table), ints([90, 33]), 90)
+    for at in (*range(1, 5), 5, 6):
+        refused(fa.attention_kv4, attn, at, spoiled(attn[at]))
+    for bad in (q, qd.transpose(0, 1), qd[..., ::2], 3):
+        refused(fa.attention_kv4, attn, 0, [bad])
+    lse = torch.empty(8, 2, device=DEV)
+    for kw in (dict(out=q), dict(out=qd.float()), dict(out=qd[:1]), dict(lse=lse.half()),
+               dict(lse=lse[:7]), dict(lse=lse.t()), dict(cu_seqlens_q=ints([0, 1])),
+               dict(cu_seqlens_q=ints([0, 1, 2]).long()), dict(workspace=lse.t()),
+               dict(workspace=lse.cpu())):
+        with pytest.raises(ValueError):
+            fa.attention_kv4(*attn, **kw)
+    with pytest.raises(fa.FaError):
+        fa.attention_kv4(*attn, workspace=lse)  # too small
+    with pytest.raises(TypeError):
+        fa.attention_kv4(*attn[:-1], 90.5)
+
+    put = (k, k.clone(), ints([1, 2], torch.int64), *dev)
+    for at in range(1, 7):
+        refused(fa.kv4_append, put, at, spoiled(put[at]))
+    get = (ints([1, 2], torch.int64), *dev)
+    for at in range(5):
+        bad = spoiled(get[at])
+        refused(fa.kv4_gather, get, at, [b for b in bad if at or b is not bad[3]])
+    for out in ((k,), (k, k.float()), (k, k[:1]), (k, k.cpu()), (k, k.transpose(0, 1))):
+        with pytest.raises(ValueError):
+            fa.kv4_gather(*get, out=out)
+    with pytest.raises(ValueError):
+        fa.kv4_gather(*get, dtype="bf16")
+    with pytest.raises(ValueError):
+        fa.kv4_gather(*get, dtype=torch.float64)
+
+    turn = (qd, qd[:, :2], ints([[3, 4]]), fa.rotary_table([1.0, 0.1], device=DEV))
+    for at in (2, 3):
+        bad = spoiled(turn[at])
+        refused(fa.rotary, turn, at, [b for b in bad if at == 2 or b is not bad[3]])
+    for bad in (q, qd.float(), qd[..., :64], qd[:1], 3):
+        refused(fa.rotary, turn, 1, [bad])
+    for kw in (dict(q_out=q), dict(q_out=qd[:, :4]), dict(k_out=qd), dict(k_out=qd[:, :2].half())):
+        with pytest.raises(ValueError):
+            fa.rotary(*turn, **kw)
+
+    plan = (ints([0, 5]), ints([3, 1]), ints([1, 2, 3]), torch.full((2, 4), -1, device=DEV).int(),
+            16, 8)
+    for at in (0, 1, 3):
+        refused(fa.kv_plan, plan, at, spoiled(plan[at]))
+    refused(fa.kv_plan, plan, 2, [plan[2].cpu(), plan[2].long(), 7, None])
+    outs = fa.kv_plan(*plan)
+    for i in range(5):
+        bad = [*outs]
+        bad[i] = bad[i][:-1]
+        with pytest.raises(ValueError):
+            fa.kv_plan(*plan, out=bad)
+    with pytest.raises(ValueError):
+        fa.kv_plan(*plan, out=outs[:4])
+
+
+def test_wrappers_hand_back_what_they_are_given_and_keep_nothing():
+    import sys
+    q, cache, table, cu = small(59)
+    dev, qd = [c.to(DEV) for c in cache], q.to(DEV)
+    t, n, s = ints(table), ints([90, 33]), ints([1, 2], torch.int64)
+    pos, rot = ints([[3, 4]]), fa.rotary_table([1.0, 0.1], device=DEV)
+    plan = (ints([0, 5]), ints([3, 1]), ints([1, 2, 3]), torch.full((2, 4), -1, device=DEV).int(),
+            16, 8)
+    o, lse = torch.empty_like(qd), torch.empty(8, 2, device=DEV)
+    kv = (torch.empty(2, 2, 128, device=DEV), torch.empty(2, 2, 128, device=DEV))
+    outs = fa.kv_plan(*plan)
+    fused = torch.randn(2, 12, 128, device=DEV).bfloat16()  # rows of q, k, v side by side
+
+    def calls(given):
+        if given:
+            a = fa.attention_kv4(qd, *dev, t, n, 90, out=o, lse=lse)
+            assert a[0] is o and a[1] is lse
+            assert fa.kv4_gather(s, *dev, out=kv) is kv
+            assert fa.kv_plan(*plan, out=outs) is outs
+            r = fa.rotary(qd, None, pos, rot, q_out=o)
+            assert r[0] is o and r[1] is None
+            return fa.kv_plan(*plan, out=list(outs)), fa.kv4_gather(s, *dev, out=list(kv))
+        r = fa.rotary(fused[:, :8], fused[:, 8:10], pos, rot)
+        assert r[0].is_contiguous() and r[1].is_contiguous()
+        swapped = fused.view(2, 12, 1, 128).transpose(0, 1).transpose(1, 2)  # [12, 1, 2, d]
+        turned = fa.rotary(swapped, None, ints([[[3, 4]] * 12]), rot)[0]
+        assert turned.shape == swapped.shape and turned.stride() == torch.empty_like(swapped).stride()
+        return fa.attention_kv4(qd, *dev, t, n, 90), fa.kv4_gather(s, *dev), fa.kv_plan(*plan)
+
+    held = (o, lse, outs, kv, qd, dev[0], t, pos, rot, plan)
+    for given in (True, False):
+        calls(given)
+        before = [sys.getrefcount(x) for x in held], torch.cuda.memory_allocated()
+        for _ in range(20):
+            calls(given)
+        assert ([sys.getrefcount(x) for x in held], torch.cuda.memory_allocated()) == before
