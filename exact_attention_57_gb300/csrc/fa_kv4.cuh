@@ -9,6 +9,24 @@
 
 namespace fa {
 
+// 32 bytes at a time.
+struct alignas(32) B32 {
+  uint32_t w[8];
+};
+__device__ __forceinline__ B32 load32(const void *p) {
+  B32 x;
+  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(x.w[0]), "=r"(x.w[1]), "=r"(x.w[2]), "=r"(x.w[3]), "=r"(x.w[4]), "=r"(x.w[5]),
+                 "=r"(x.w[6]), "=r"(x.w[7])
+               : "l"(p));
+  return x;
+}
+__device__ __forceinline__ void store32(void *p, const B32 &x) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x.w[0]),
+               "r"(x.w[1]), "r"(x.w[2]), "r"(x.w[3]), "r"(x.w[4]), "r"(x.w[5]), "r"(x.w[6]), "r"(x.w[7])
+               : "memory");
+}
+
 // Byte `I` of w (two e2m1 codes) as two fp16 values, the low half first.
 template <int I>
 __device__ __forceinline__ uint32_t e2m1x2_f16x2(uint32_t w) {

@@ -44,24 +44,6 @@ __device__ __forceinline__ long long cache_row(const Kv4Store &c, long long slot
   return ((block * c.Hk + h) << c.bs_log2) + off;
 }
 
-// 32 bytes at a time.
-struct alignas(32) B32 {
-  uint32_t w[8];
-};
-__device__ __forceinline__ B32 load32(const void *p) {
-  B32 x;
-  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(x.w[0]), "=r"(x.w[1]), "=r"(x.w[2]), "=r"(x.w[3]), "=r"(x.w[4]), "=r"(x.w[5]),
-                 "=r"(x.w[6]), "=r"(x.w[7])
-               : "l"(p));
-  return x;
-}
-__device__ __forceinline__ void store32(void *p, const B32 &x) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x.w[0]),
-               "r"(x.w[1]), "r"(x.w[2]), "r"(x.w[3]), "r"(x.w[4]), "r"(x.w[5]), "r"(x.w[6]), "r"(x.w[7])
-               : "memory");
-}
-
 // Where a thread's 16 elements are: row, and head * (d / 16) + group.
 struct At {
   long long row;
