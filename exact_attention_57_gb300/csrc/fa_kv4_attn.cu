@@ -32,12 +32,14 @@
 // it costs beside its keys (its queries, the pipeline's start, the warps'
 // meeting).  A CTA's first and last sequence may be shared with its neighbours;
 // such parts go to the workspace (two a CTA, whatever the lengths), and a
-// second kernel joins them.
+// second kernel joins them.  Where one wave of CTAs holds a cluster of 1, 2, 4 or
+// 8 for every sequence and key head, and their caches are short, a cluster takes
+// the keys of one instead and joins its parts through shared memory.
 //
 // Measured at 8 key heads of 128 elements, four query heads each: 64 sequences of
 // up to 8192 keys (327 MB of cache) 70 us, 4.7 TB/s or 69% of the measured copy
 // rate, the loads alone without a product 65; one of 131071 (151 MB) 35 us; one of
-// 1023 7.3 us, the latencies of two launches.  What bounds it is the time that
+// 1023 5.0 us, the latencies of one launch.  What bounds it is the time that
 // loads of 64-byte rows take at two tiles in flight a warp, and about 330
 // instructions a tile of 16 tokens.  Not faster: codes through shared memory by
 // bulk copies (75 to 87 us), tiles of 32 tokens (91), a third tile in registers
@@ -109,6 +111,39 @@ __device__ __forceinline__ int units_of(const Seq &s, int group, int rows) {
   return kLead + max(1, (s.nk + kUnit - 1) / kUnit);
 }
 
+
+// Units a CTA of a cluster may have at most.  Measured in us, one query a sequence,
+// 8 key heads of 128, as a cluster and along the line: 1 x 1023 keys 5.0 and 8.0,
+// 1 x 8192 (8 units of 128 a CTA) 9.7 and 11.1, 1 x 16384 14.9 and 13.0; 8 x 4096
+// (clusters of 4) 12.3 and 14.0; 16 x 2048 (of 2) 12.0 and 13.0, 16 x 4096 19.0 and
+// 16.7; 32 x 1023 (of 1) 11.0 and 13.8.  More clusters than one wave holds lose:
+// 64 x 1023 24 to 70 us in clusters of 2 to 8, 20 along the line.
+constexpr int kClusterUnits = 8;
+
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Shared memory address `addr` as CTA `rank` of the cluster has it.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, int rank) {
+  uint32_t y;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(y) : "r"(addr), "r"(rank));
+  return y;
+}
+__device__ __forceinline__ float4 cluster_load4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 cluster_load2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+               : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
 // 16 tokens of one page as lane (r, c) holds them.
 template <int D>
 struct Tile {
@@ -126,10 +161,13 @@ __device__ __forceinline__ float2 pair_f32(uint32_t x) {
 
 template <int NT, int D>
 constexpr int smem_bytes() {
-  return Shape<NT, D>::kWarps * NT * 8 * (D + 4 + 2) * 4;
+  return (Shape<NT, D>::kWarps * (D + 4 + 2) + D + 4) * NT * 8 * 4;
 }
 
-template <typename T, int D, int NT>
+// CL > 0: the CTAs of a cluster, as many, share one sequence and key head and join
+// their parts through shared memory; 0: every CTA takes its share of the line of
+// all units, and the join is another kernel's.
+template <typename T, int D, int NT, int CL>
 __global__ void __launch_bounds__(Shape<NT, D>::kWarps * 32, Shape<NT, D>::kCtas)
     fa_kv4_attn_kernel(const Kv4Attn p, float *ws) {
   constexpr int R = NT * 8;              // rows of the tile
@@ -142,45 +180,73 @@ __global__ void __launch_bounds__(Shape<NT, D>::kWarps * 32, Shape<NT, D>::kCtas
   float *s_o = smem;                     // [warp][R][LD]
   float *s_m = smem + kWarps * R * LD;   // [warp][R]
   float *s_l = s_m + kWarps * R;
+  float *s_part = s_l + kWarps * R;      // [R][LD], CL: this CTA's part
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, c = lane & 3;
   griddep_wait();
   griddep_launch_dependents();
-  int den = gridDim.x;
-  long long u = 0;
-  const Place at = find_unit<kWarps>(
-      p,
-      [&](int b) {
-        return static_cast<long long>(units_of<kUnit, kLead>(load_seq(p, b), p.group, R)) * p.c.Hk;
-      },
-      blockIdx.x, &den, &u, s_sums, s_warp);
-  Share share = {0, 0, 0, 0};
-  if (static_cast<int>(blockIdx.x) >= den) {
-    if (tid == 0) reinterpret_cast<Share *>(ws)[blockIdx.x] = share;
-    return;
-  }
-  const long long u1 = at.total * (blockIdx.x + 1) / den;
+  // four columns of a finished row
+  auto put = [&](int i, int head, int col, float4 sum, float m, float l) {
+    const long long out = static_cast<long long>(i) * p.Hq + head;
+    const float inv = l > 0.f ? p.v_mul / l : 0.f;
+    alignas(8) T e[4] = {static_cast<T>(sum.x * inv), static_cast<T>(sum.y * inv),
+                         static_cast<T>(sum.z * inv), static_cast<T>(sum.w * inv)};
+    *reinterpret_cast<uint2 *>(static_cast<T *>(p.o) + out * D + col) =
+        *reinterpret_cast<const uint2 *>(e);
+    if (col == 0) p.lse[static_cast<long long>(head) * p.total_q + i] = lse_of(m, l);
+  };
   const int bs = 1 << p.c.bs_log2;
-
-  int b = at.b;
-  Seq sq = load_seq(p, b);
-  int n_units = units_of<kUnit, kLead>(sq, p.group, R);
-  const long long into = u - at.before;
-  int h = static_cast<int>(into / n_units), unit = static_cast<int>(into - static_cast<long long>(h) * n_units);
-  while (u < u1) {
-    while (n_units == 0) {  // another sequence of this kernel follows, since u < total
-      sq = load_seq(p, ++b);
-      n_units = units_of<kUnit, kLead>(sq, p.group, R);
-      h = 0;
+  int den = gridDim.x, b, h, unit = 0, n_units;
+  long long u = 0, u1 = 0;
+  Place at = {0, 0, 0};
+  Seq sq;
+  Share share = {0, 0, 0, 0};
+  if constexpr (CL > 0) {
+    const int item = blockIdx.x / CL;
+    b = item / p.c.Hk;
+    h = item - b * p.c.Hk;
+    sq = load_seq(p, b);
+    n_units = units_of<kUnit, kLead>(sq, p.group, R);
+    if (n_units == 0) return;  // the whole cluster
+  } else {
+    at = find_unit<kWarps>(
+        p,
+        [&](int b) {
+          return static_cast<long long>(units_of<kUnit, kLead>(load_seq(p, b), p.group, R)) * p.c.Hk;
+        },
+        blockIdx.x, &den, &u, s_sums, s_warp);
+    if (static_cast<int>(blockIdx.x) >= den) {
+      if (tid == 0) reinterpret_cast<Share *>(ws)[blockIdx.x] = share;
+      return;
     }
-    // units [t_lo, t_hi) of the n_units - kLead with keys
-    const int unit_hi = static_cast<int>(min(static_cast<long long>(n_units), unit + (u1 - u)));
-    const int t_lo = max(unit - kLead, 0), t_hi = max(unit_hi - kLead, 0);
-    // the CTA with the last of them
-    const int last = cta_of(u - unit + n_units - 1, at.total, den);
-    u += unit_hi - unit;
-    unit = 0;
-    if (t_lo == t_hi) break;  // only the lead fell to this CTA: its share is done
+    u1 = at.total * (blockIdx.x + 1) / den;
+    b = at.b;
+    sq = load_seq(p, b);
+    n_units = units_of<kUnit, kLead>(sq, p.group, R);
+    const long long into = u - at.before;
+    h = static_cast<int>(into / n_units);
+    unit = static_cast<int>(into - static_cast<long long>(h) * n_units);
+  }
+  do {
+    int t_lo, t_hi, last = 0;  // units [t_lo, t_hi) of the n_units - kLead with keys
+    if constexpr (CL > 0) {
+      const int rank = blockIdx.x % CL;
+      t_lo = static_cast<int>(static_cast<long long>(n_units - kLead) * rank / CL);
+      t_hi = static_cast<int>(static_cast<long long>(n_units - kLead) * (rank + 1) / CL);
+    } else {
+      while (n_units == 0) {  // another sequence of this kernel follows, since u < total
+        sq = load_seq(p, ++b);
+        n_units = units_of<kUnit, kLead>(sq, p.group, R);
+        h = 0;
+      }
+      const int unit_hi = static_cast<int>(min(static_cast<long long>(n_units), unit + (u1 - u)));
+      t_lo = max(unit - kLead, 0), t_hi = max(unit_hi - kLead, 0);
+      // the CTA with the last of them
+      last = cta_of(u - unit + n_units - 1, at.total, den);
+      u += unit_hi - unit;
+      unit = 0;
+      if (t_lo == t_hi) break;  // only the lead fell to this CTA: its share is done
+    }
     const int rows = sq.nq * p.group;
 
     // Q fragments: lane (r, c) holds D / 4 elements of row nt * 8 + r
@@ -441,17 +507,12 @@ __global__ void __launch_bounds__(Shape<NT, D>::kWarps * 32, Shape<NT, D>::kCtas
         const float4 v = *reinterpret_cast<const float4 *>(s_o + (w * R + row) * LD + col);
         sum.x += f[w] * v.x, sum.y += f[w] * v.y, sum.z += f[w] * v.z, sum.w += f[w] * v.w;
       }
-      if (whole) {
+      if constexpr (CL > 0) {
+        *reinterpret_cast<float4 *>(s_part + row * LD + col) = sum;
+        if (col == 0) *reinterpret_cast<float2 *>(s_part + row * LD + D) = make_float2(mm, ll);
+      } else if (whole) {
         const int i = row / p.group, j = row - i * p.group;
-        const long long out = static_cast<long long>(sq.r0 + i) * p.Hq + h * p.group + j;
-        const float inv = ll > 0.f ? p.v_mul / ll : 0.f;
-        alignas(8) T e[4] = {static_cast<T>(sum.x * inv), static_cast<T>(sum.y * inv),
-                             static_cast<T>(sum.z * inv), static_cast<T>(sum.w * inv)};
-        *reinterpret_cast<uint2 *>(static_cast<T *>(p.o) + out * D + col) =
-            *reinterpret_cast<const uint2 *>(e);
-        if (col == 0)
-          p.lse[static_cast<long long>(h * p.group + j) * p.total_q + sq.r0 + i] =
-              lse_of(mm, ll);
+        put(sq.r0 + i, h * p.group + j, col, sum, mm, ll);
       } else {
         float *dst = part_of<D, R>(ws, blockIdx.x, begins);
         *reinterpret_cast<float4 *>(dst + row * D + col) = sum;
@@ -461,42 +522,94 @@ __global__ void __launch_bounds__(Shape<NT, D>::kWarps * 32, Shape<NT, D>::kCtas
         }
       }
     }
-    __syncthreads();
-    if (++h == p.c.Hk) n_units = 0;
+    if constexpr (CL == 0) {
+      __syncthreads();
+      if (++h == p.c.Hk) n_units = 0;
+    }
+  } while (CL == 0 && u < u1);
+  if constexpr (CL > 0) {
+    cluster_barrier();
+    for (int x = tid; x < R / CL * (D / 4); x += kThreads) {  // row by row to the CTAs
+      const int row = blockIdx.x % CL + CL * (x / (D / 4)), col = x % (D / 4) * 4;
+      if (row >= sq.nq * p.group) break;
+      const uint32_t src = smem_u32(s_part + row * LD);
+      float2 ml[CL];
+      float4 v[CL], sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int n = 0; n < CL; ++n) {
+        const uint32_t from = cluster_addr(src, n);
+        ml[n] = cluster_load2(from + D * 4);
+        v[n] = cluster_load4(from + col * 4);
+      }
+      float m = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int n = 0; n < CL; ++n) m = fmaxf(m, ml[n].x);
+#pragma unroll
+      for (int n = 0; n < CL; ++n) {
+        const float f = m == -INFINITY ? 0.f : ex2_approx(ml[n].x - m);
+        l += f * ml[n].y;
+        sum.x += f * v[n].x, sum.y += f * v[n].y, sum.z += f * v[n].z, sum.w += f * v[n].w;
+      }
+      const int i = row / p.group, j = row - i * p.group;
+      put(sq.r0 + i, h * p.group + j, col, sum, m, l);
+    }
+    cluster_barrier();  // the others may still read this CTA's part
+  } else {
+    if (tid == 0) reinterpret_cast<Share *>(ws)[blockIdx.x] = share;
   }
-  if (tid == 0) reinterpret_cast<Share *>(ws)[blockIdx.x] = share;
 }
 
-template <typename T, int D, int NT>
-cudaError_t launch(const Kv4Attn &p, float *ws, int num_sms, cudaStream_t s) {
+template <typename T, int D, int NT, int CL>
+cudaError_t launch_kernel(const Kv4Attn &p, float *ws, long long ctas, cudaStream_t s) {
   static std::atomic<unsigned long long> attr_done{0};
-  constexpr int smem = smem_bytes<NT, D>(), kUnit = Shape<NT, D>::kWarps * 16;
-  cudaError_t e = smem_attr_once(fa_kv4_attn_kernel<T, D, NT>, smem, &attr_done);
+  constexpr int smem = smem_bytes<NT, D>();
+  cudaError_t e = smem_attr_once(fa_kv4_attn_kernel<T, D, NT, CL>, smem, &attr_done);
   if (e != cudaSuccess) return e;
-  // one resident wave, no more CTAs than there can be units
-  long long ctas = static_cast<long long>(num_sms > 0 ? num_sms : 1) * Shape<NT, D>::kCtas;
-  const long long most = static_cast<long long>(p.B) * p.c.Hk *
-                         (p.max_k < kUnit ? 1 : (p.max_k + kUnit - 1) / kUnit);
-  if (ctas > most) ctas = most;
-  if (ctas > kKv4MaxCtas) ctas = kKv4MaxCtas;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(Shape<NT, D>::kWarps * 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CL;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, fa_kv4_attn_kernel<T, D, NT>, p, ws);
-  if (e != cudaSuccess || ctas == 1) return e;
+  cfg.numAttrs = CL > 1 ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, fa_kv4_attn_kernel<T, D, NT, CL>, p, ws);
+  if (e != cudaSuccess || CL > 0 || ctas == 1) return e;
   const long long rows = static_cast<long long>(p.max_q) * p.group;
   cfg.blockDim = dim3(kJoinThreads);
   cfg.gridDim = dim3(static_cast<unsigned>(ctas - 1),
                      static_cast<unsigned>((min(rows, NT * 8LL) + kJoinRows - 1) / kJoinRows));
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, fa_kv4_join_kernel<T, D, NT * 8>, p, ws);
+}
+
+template <typename T, int D, int NT>
+cudaError_t launch(const Kv4Attn &p, float *ws, int num_sms, cudaStream_t s) {
+  constexpr int kUnit = Shape<NT, D>::kWarps * 16;
+  const long long wave = static_cast<long long>(num_sms > 0 ? num_sms : 1) * Shape<NT, D>::kCtas;
+  const long long heads = static_cast<long long>(p.B) * p.c.Hk;
+  const long long units = p.max_k < kUnit ? 1 : (p.max_k + kUnit - 1) / kUnit;
+  if constexpr (NT <= 2) {
+    // the largest cluster of which one wave holds one for every sequence and key
+    // head, if that leaves a CTA at most kClusterUnits units: one launch
+    if (heads * 8 <= wave && units <= 8 * kClusterUnits)
+      return launch_kernel<T, D, NT, 8>(p, ws, heads * 8, s);
+    if (heads * 4 <= wave && units <= 4 * kClusterUnits)
+      return launch_kernel<T, D, NT, 4>(p, ws, heads * 4, s);
+    if (heads * 2 <= wave && units <= 2 * kClusterUnits)
+      return launch_kernel<T, D, NT, 2>(p, ws, heads * 2, s);
+    if (heads <= wave && units <= kClusterUnits)
+      return launch_kernel<T, D, NT, 1>(p, ws, heads, s);
+  }
+  // one resident wave, no more CTAs than there can be units
+  long long ctas = wave < heads * units ? wave : heads * units;
+  if (ctas > kKv4MaxCtas) ctas = kKv4MaxCtas;
+  return launch_kernel<T, D, NT, 0>(p, ws, ctas, s);
 }
 
 template <typename T, int D>

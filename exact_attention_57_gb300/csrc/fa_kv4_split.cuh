@@ -82,7 +82,7 @@ __device__ Place find_unit(const Kv4Attn &p, F units, int num, int *den, long lo
   Place at = {0, 0, 0};
   if (p.B <= 32) {
     // one a lane: every warp finds it by itself (0.4 us less than by way of shared
-    // memory, of 8.0 for one sequence of 1023 keys, 16.8 for 16 of up to 3001)
+    // memory, of 16.8 for 16 sequences of up to 3001 keys)
     const long long n = lane < p.B ? units(lane) : 0;
     long long incl = n;
     for (int o = 1; o < 32; o *= 2) {

@@ -468,8 +468,9 @@ FA_API int fa_kv4_gather(const long long *slots, int R, const void *k_codes, con
  *               takes its tokens out of the softmax.
  * max_seqlen_q, max_seqlen_k  bounds on the lengths; longer sequences are cut
  *               to them (max_blocks * block_size bounds the keys too).  A loose
- *               max_seqlen_k costs little: it is what the kernel is chosen by
- *               where there are 17 to 32 queries a key head, and bounds the grid.
+ *               max_seqlen_k costs little: it bounds the grid, and up to a few
+ *               thousand keys it is what says that a small batch needs one launch
+ *               instead of two.
  * causal        1: query i of n_q sees key j iff j <= n_k - n_q + i (aligned
  *               at the end, as the new tokens are the last cached ones); 0:
  *               all keys.  A row that sees no key gets O = 0, LSE = -inf.

@@ -709,6 +709,39 @@ def test_many_queries_report_a_wait_that_runs_out():
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq", [3, 8, 12, 16])  # rows a sequence: tiles of 8 and 16
+@pytest.mark.parametrize("B", [1, 17, 40, 100, 200])
+def test_attention_of_small_batches(B, Hq, d):
+    """Up to one sequence a CTA, by a tight and by a loose bound on the keys: the
+    bound decides how many CTAs a sequence gets and who joins their parts."""
+    lens = [(137 * b + 1000) % 1025 if b % 7 != 3 else b % 2 for b in range(B)]
+    nqs = [1] * B
+    q, cache, table, _ = small(61 + B, lens, nqs, Hq=Hq, Hk=1, d=d)
+    for max_k in (1024, 1 << 20):
+        o, lse = fa.attention_kv4(q.to(DEV), *(c.to(DEV) for c in cache), ints(table), ints(lens),
+                                  max_k)
+        check_attention(q, cache, table, lens, nqs, 16, d, d ** -0.5, True, o, lse, torch.bfloat16,
+                        label=str(max_k))
+        again = fa.attention_kv4(q.to(DEV), *(c.to(DEV) for c in cache), ints(table), ints(lens),
+                                 max_k)
+        assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("lens,max_k", [((8192, 5000), 8192), ((2000,) * 3, 2048),
+                                        ((4096, 0, 1, 4000) * 2, 4096), ((127, 129, 128), 130)])
+def test_attention_of_few_long_sequences(lens, max_k):
+    """The longest caches that a cluster takes, drafted tokens among their queries,
+    and one sequence of the batch with more queries than a tile holds."""
+    nqs = [1 + b % 2 for b in range(len(lens))]
+    for extra in (0, 9):
+        nqs[-1] += extra
+        q, cache, table, cu = small(67, lens, nqs, Hq=8, Hk=2, bs=64)
+        o, lse = call(q, cache, table, lens, cu, nqs, max_k=max_k)
+        check_attention(q, cache, table, lens, nqs, 64, 128, 128 ** -0.5, True, o, lse,
+                        torch.bfloat16, max_k=max_k, label=str(extra))
+
+
 @pytest.mark.parametrize("nqs", [(4, 2), (1, 3), (40, 4)])
 def test_attention_of_32_rows_and_a_bound_of_many_keys(nqs):
     """Rows that fill a tile go to the kernel for many queries when max_seqlen_k
