@@ -111,7 +111,6 @@ __device__ __forceinline__ int units_of(const Seq &s, int group, int rows) {
   return kLead + max(1, (s.nk + kUnit - 1) / kUnit);
 }
 
-
 // Units a CTA of a cluster may have at most.  Measured in us, one query a sequence,
 // 8 key heads of 128, as a cluster and along the line: 1 x 1023 keys 5.0 and 8.0,
 // 1 x 8192 (8 units of 128 a CTA) 9.7 and 11.1, 1 x 16384 14.9 and 13.0; 8 x 4096

@@ -475,9 +475,10 @@ FA_API int fa_kv4_gather(const long long *slots, int R, const void *k_codes, con
  *               at the end, as the new tokens are the last cached ones); 0:
  *               all keys.  A row that sees no key gets O = 0, LSE = -inf.
  * d 64 or 128, Hq/Hk at most 128 (else FA_ERR_UNSUPPORTED); fp32 types are
- * FA_ERR_UNSUPPORTED.  A query times a key is exact, scores, softmax and sums
- * are fp32, and a weight is rounded to fp16 (half a step, 2^-11 of itself) for
- * its product with the values.
+ * FA_ERR_UNSUPPORTED.  Queries become fp16 times a power of two a row (exact but
+ * for elements below 2^-14 of the row's largest, off by 2^-25 of it at most),
+ * weights are rounded to fp16 (half a step, 2^-11 of itself); keys and values are exact, and
+ * products, softmax and sums are fp32.
  * workspace     fa_fwd_kv4_workspace(...) bytes, 256-byte aligned, whatever
  *               they hold.  Calls that share it must not overlap on the GPU.
  * The lengths, offsets and tables are read on the device and not checked on
