@@ -13,9 +13,10 @@
 // a server that is one round of two loads a thread and a scan, less than a
 // second launch.  CTA c owns kTokens token slots (it finds each one's request
 // by bisection in the 256 prefix sums at hand), and the requests of every
-// gridDim-th round (their table rows, lengths and offsets).  A token whose
-// block is new reads the free list, not the table, so no CTA waits for
-// another's table entries.
+// gridDim-th round (their lengths and offsets).  A token whose block is new reads
+// the free list, not the table, so no CTA waits for another's table entries, and
+// the first token of a new block writes its entry; those of blocks whose tokens
+// lie behind the capacity are CTA 0's.
 //
 // Latency bounds it: 256 requests of one token 2.5 us, a launch; 37 prompts with
 // 148000 tokens (1.8 MB written) 6.0 us, which are the requests' loads, the scan,
@@ -115,10 +116,13 @@ __global__ void __launch_bounds__(kThreads) fa_plan_kernel(const PlanParams p) {
         p.cu[b] = static_cast<int>(min(s_tok[tid], static_cast<long long>(p.capacity)));
         p.lens[b] = static_cast<int>(len);
       }
+    }
+    if (cta == 0 && tok + sum_tok > p.capacity) {
       for (long long j = blk + tid; j < blk + sum_blk; j += kThreads) {
         const int i = bisect(s_blk, j);
-        p.table[(static_cast<long long>(r) * kThreads + i) * p.width + s_have[i] + (j - s_blk[i])] =
-            fresh_block(j);
+        const long long at = s_have[i] + (j - s_blk[i]);
+        if (s_tok[i] + (at << p.bs_log2) - s_cached[i] >= p.capacity)
+          p.table[(static_cast<long long>(r) * kThreads + i) * p.width + at] = fresh_block(j);
       }
     }
     for (long long t = max(t0, tok) + tid; t < min(t1, tok + sum_tok); t += kThreads) {
@@ -127,10 +131,9 @@ __global__ void __launch_bounds__(kThreads) fa_plan_kernel(const PlanParams p) {
       long long slot = -1;
       if (pos < reach) {
         const int j = static_cast<int>(pos >> p.bs_log2);
-        const int block =
-            j < s_have[i]
-                ? p.table[(static_cast<long long>(r) * kThreads + i) * p.width + j]
-                : fresh_block(s_blk[i] + j - s_have[i]);
+        int *entry = p.table + (static_cast<long long>(r) * kThreads + i) * p.width + j;
+        const int block = j < s_have[i] ? *entry : fresh_block(s_blk[i] + j - s_have[i]);
+        if (j >= s_have[i] && (pos & mask) == 0) *entry = block;
         if (block >= 0) slot = (static_cast<long long>(block) << p.bs_log2) + (pos & mask);
       }
       p.slots[t] = slot;

@@ -79,6 +79,17 @@ def test_plan_many_requests():
     check_plan(cached, new, free, table, bs, sum(new) + 5000)
 
 
+@pytest.mark.parametrize("bs", [16, 128])
+def test_plan_capacity_ends_anywhere(bs):
+    """Table entries of blocks whose tokens lie behind the capacity are written all
+    the same, in whichever round of requests and inside whichever block it ends."""
+    cached, new, free, table = plan_case(600, bs, 3 * bs, 2 * bs, seed=bs)
+    total = sum(new)
+    for cap in (1, 15, 17, 1023, 1024, 1025, sum(new[:256]), sum(new[:256]) + 1, total // 2,
+                total - 1, total):
+        check_plan(cached, new, free, table, bs, cap)
+
+
 def test_plan_head_short_list_full_table_and_small_capacity():
     cached, new, free, table = plan_case(9, 16, 50, 60, seed=8)
     check_plan(cached, new, [5, 6, 7] + free, table, 16, sum(new), head=3)
