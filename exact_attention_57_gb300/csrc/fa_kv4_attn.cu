@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(Shape<NT, D>::kWarps * 32, Shape<NT, D>::kCtas
 }
 
 template <typename T, int D, int NT, int CL>
-cudaError_t launch_kernel(const Kv4Attn &p, float *ws, long long ctas, cudaStream_t s) {
+cudaError_t launch_kernel(const Kv4Attn &p, float *ws, int ctas, cudaStream_t s) {
   static std::atomic<unsigned long long> attr_done{0};
   constexpr int smem = smem_bytes<NT, D>();
   cudaError_t e = smem_attr_once(fa_kv4_attn_kernel<T, D, NT, CL>, smem, &attr_done);
@@ -588,34 +588,42 @@ cudaError_t launch_kernel(const Kv4Attn &p, float *ws, long long ctas, cudaStrea
 }
 
 template <typename T, int D, int NT>
-cudaError_t launch(const Kv4Attn &p, float *ws, int num_sms, cudaStream_t s) {
-  constexpr int kUnit = Shape<NT, D>::kWarps * 16;
-  const long long wave = static_cast<long long>(num_sms > 0 ? num_sms : 1) * Shape<NT, D>::kCtas;
-  const long long heads = static_cast<long long>(p.B) * p.c.Hk;
-  const long long units = p.max_k < kUnit ? 1 : (p.max_k + kUnit - 1) / kUnit;
+cudaError_t launch(const Kv4Attn &p, const Kv4Grid &g, float *ws, cudaStream_t s) {
   if constexpr (NT <= 2) {
+    if (g.cluster == 8) return launch_kernel<T, D, NT, 8>(p, ws, g.ctas, s);
+    if (g.cluster == 4) return launch_kernel<T, D, NT, 4>(p, ws, g.ctas, s);
+    if (g.cluster == 2) return launch_kernel<T, D, NT, 2>(p, ws, g.ctas, s);
+    if (g.cluster == 1) return launch_kernel<T, D, NT, 1>(p, ws, g.ctas, s);
+  }
+  return launch_kernel<T, D, NT, 0>(p, ws, g.ctas, s);
+}
+
+// The grid for `heads` sequences and key heads with up to max_k keys.
+template <int NT, int D>
+void shape_grid(long long heads, int max_k, int num_sms, Kv4Grid *g) {
+  constexpr int kUnit = Shape<NT, D>::kWarps * 16;
+  const long long wave = static_cast<long long>(num_sms) * Shape<NT, D>::kCtas;
+  const long long units = max_k < kUnit ? 1 : (static_cast<long long>(max_k) + kUnit - 1) / kUnit;
+  if (NT <= 2) {
     // the largest cluster of which one wave holds one for every sequence and key
     // head, if that leaves a CTA at most kClusterUnits units: one launch
-    if (heads * 8 <= wave && units <= 8 * kClusterUnits)
-      return launch_kernel<T, D, NT, 8>(p, ws, heads * 8, s);
-    if (heads * 4 <= wave && units <= 4 * kClusterUnits)
-      return launch_kernel<T, D, NT, 4>(p, ws, heads * 4, s);
-    if (heads * 2 <= wave && units <= 2 * kClusterUnits)
-      return launch_kernel<T, D, NT, 2>(p, ws, heads * 2, s);
-    if (heads <= wave && units <= kClusterUnits)
-      return launch_kernel<T, D, NT, 1>(p, ws, heads, s);
+    for (int cl = 8; cl > 0; cl /= 2)
+      if (heads * cl <= wave && units <= cl * kClusterUnits) {
+        g->cluster = cl;
+        g->ctas = static_cast<int>(heads * cl);
+        return;
+      }
   }
   // one resident wave, no more CTAs than there can be units
-  long long ctas = wave < heads * units ? wave : heads * units;
-  if (ctas > kKv4MaxCtas) ctas = kKv4MaxCtas;
-  return launch_kernel<T, D, NT, 0>(p, ws, ctas, s);
+  const long long ctas = wave < heads * units ? wave : heads * units;
+  g->ctas = static_cast<int>(ctas < kKv4MaxCtas ? ctas : kKv4MaxCtas);
 }
 
 template <typename T, int D>
-cudaError_t launch_rows(const Kv4Attn &p, int rows, float *ws, int num_sms, cudaStream_t s) {
-  if (rows == 8) return launch<T, D, 1>(p, ws, num_sms, s);
-  if (rows == 16) return launch<T, D, 2>(p, ws, num_sms, s);
-  return launch<T, D, 4>(p, ws, num_sms, s);
+cudaError_t launch_rows(const Kv4Attn &p, const Kv4Grid &g, float *ws, cudaStream_t s) {
+  if (g.rows == 8) return launch<T, D, 1>(p, g, ws, s);
+  if (g.rows == 16) return launch<T, D, 2>(p, g, ws, s);
+  return launch<T, D, 4>(p, g, ws, s);
 }
 
 }  // namespace
@@ -636,13 +644,38 @@ size_t kv4_workspace(int rows, int d) {
          static_cast<size_t>(2 * ctas) * rows * (d + 2) * sizeof(float);
 }
 
-cudaError_t launch_kv4_attn(const Kv4Attn &p, int rows, int dtype, float *ws, int num_sms,
+Kv4Grid kv4_grid(int B, int Hk, int group, int d, int max_q, int max_k, int num_sms) {
+  const long long heads = static_cast<long long>(B) * Hk;
+  if (num_sms < 1) num_sms = 1;
+  Kv4Grid g = {kv4_tile_rows(group, max_q, d, heads * max_k), 0, 0, 0};
+  if (g.rows == 8)
+    d == 64 ? shape_grid<1, 64>(heads, max_k, num_sms, &g)
+            : shape_grid<1, 128>(heads, max_k, num_sms, &g);
+  else if (g.rows == 16)
+    d == 64 ? shape_grid<2, 64>(heads, max_k, num_sms, &g)
+            : shape_grid<2, 128>(heads, max_k, num_sms, &g);
+  else if (g.rows == 32)
+    d == 64 ? shape_grid<4, 64>(heads, max_k, num_sms, &g)
+            : shape_grid<4, 128>(heads, max_k, num_sms, &g);
+  if (static_cast<long long>(max_q) * group > g.rows) {
+    // one CTA on each SM, no more than there can be units (steps of 128 keys)
+    const int tokens = kKv4ManyRows / group;
+    const long long tiles = (static_cast<long long>(max_q) + tokens - 1) / tokens;
+    const double most = static_cast<double>(heads) * tiles *
+                        (max_k < 128 ? 1.0 : (max_k + 127.0) / 128.0);
+    g.many = num_sms < kKv4ManyCtas ? num_sms : kKv4ManyCtas;
+    if (g.many > most) g.many = static_cast<int>(most);
+  }
+  return g;
+}
+
+cudaError_t launch_kv4_attn(const Kv4Attn &p, const Kv4Grid &g, int dtype, float *ws,
                             cudaStream_t s) {
   if (dtype == FA_DTYPE_BF16)
-    return p.c.d == 64 ? launch_rows<__nv_bfloat16, 64>(p, rows, ws, num_sms, s)
-                       : launch_rows<__nv_bfloat16, 128>(p, rows, ws, num_sms, s);
-  return p.c.d == 64 ? launch_rows<__half, 64>(p, rows, ws, num_sms, s)
-                     : launch_rows<__half, 128>(p, rows, ws, num_sms, s);
+    return p.c.d == 64 ? launch_rows<__nv_bfloat16, 64>(p, g, ws, s)
+                       : launch_rows<__nv_bfloat16, 128>(p, g, ws, s);
+  return p.c.d == 64 ? launch_rows<__half, 64>(p, g, ws, s)
+                     : launch_rows<__half, 128>(p, g, ws, s);
 }
 
 }  // namespace fa

@@ -731,17 +731,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <typename T, int D>
-cudaError_t launch(const Kv4Attn &p, const ManyCtl &ctl, float *ws, int num_sms, cudaStream_t s) {
+cudaError_t launch(const Kv4Attn &p, const ManyCtl &ctl, float *ws, int ctas, cudaStream_t s) {
   static std::atomic<unsigned long long> attr_done{0};
   constexpr int smem = ManyCfg<D>::SMEM;
   cudaError_t e = smem_attr_once(fa_kv4_many_kernel<T, D>, smem, &attr_done);
   if (e != cudaSuccess) return e;
-  // one CTA on each SM, no more than there can be units
-  const long long tiles = (static_cast<long long>(p.max_q) + ctl.tokens - 1) / ctl.tokens;
-  const double most = static_cast<double>(p.B) * p.c.Hk * tiles *
-                      (p.max_k < 128 ? 1.0 : (p.max_k + 127.0) / 128.0);
-  int ctas = num_sms > 0 ? min(num_sms, kKv4ManyCtas) : 1;
-  if (ctas > most) ctas = static_cast<int>(most);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(kThreads);
@@ -762,15 +756,15 @@ cudaError_t launch(const Kv4Attn &p, const ManyCtl &ctl, float *ws, int num_sms,
 
 }  // namespace
 
-cudaError_t launch_kv4_many(const Kv4Attn &p, int tile_rows, int dtype, float *ws, int num_sms,
+cudaError_t launch_kv4_many(const Kv4Attn &p, const Kv4Grid &g, int dtype, float *ws,
                             unsigned *status, unsigned long long wait_limit_ns, int skip_load,
                             cudaStream_t s) {
-  const ManyCtl ctl = {status, wait_limit_ns, skip_load, tile_rows, R / p.group};
+  const ManyCtl ctl = {status, wait_limit_ns, skip_load, g.rows, R / p.group};
   if (dtype == FA_DTYPE_BF16)
-    return p.c.d == 64 ? launch<__nv_bfloat16, 64>(p, ctl, ws, num_sms, s)
-                       : launch<__nv_bfloat16, 128>(p, ctl, ws, num_sms, s);
-  return p.c.d == 64 ? launch<__half, 64>(p, ctl, ws, num_sms, s)
-                     : launch<__half, 128>(p, ctl, ws, num_sms, s);
+    return p.c.d == 64 ? launch<__nv_bfloat16, 64>(p, ctl, ws, g.many, s)
+                       : launch<__nv_bfloat16, 128>(p, ctl, ws, g.many, s);
+  return p.c.d == 64 ? launch<__half, 64>(p, ctl, ws, g.many, s)
+                     : launch<__half, 128>(p, ctl, ws, g.many, s);
 }
 
 }  // namespace fa

@@ -21,8 +21,7 @@ __device__ __forceinline__ Seq load_seq(const Kv4Attn &p, int b) {
     s.r0 = min(max(p.cu_q[b], 0), p.total_q);
     s.nq = min(max(min(max(p.cu_q[b + 1], 0), p.total_q) - s.r0, 0), p.max_q);
   }
-  s.nk = static_cast<int>(min(static_cast<long long>(min(max(p.lens[b], 0), p.max_k)),
-                              static_cast<long long>(p.width) << p.c.bs_log2));
+  s.nk = min(max(p.lens[b], 0), p.max_k);  // (max_k keeps to the table's width)
   return s;
 }
 

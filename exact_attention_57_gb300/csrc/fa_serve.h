@@ -75,7 +75,9 @@ struct Kv4Attn {
   const int *lens;                // [B]
   const int *cu_q;                // [B + 1] or null (one query a sequence)
   int B, Hq, group;               // group = Hq / Hk
-  int total_q, max_q, max_k, width;
+  int total_q, max_q;
+  int max_k;                      // at most width blocks, and kKv4MaxKeys
+  int width;
   float scale_log2;               // scale * 2^k_exp * log2(e)
   float v_mul;                    // 2^v_exp
   int causal;
@@ -89,13 +91,23 @@ struct Kv4Attn {
 constexpr int kKv4MaxCtas = 304;   // two on each of 152 SMs
 constexpr int kKv4ManyCtas = 152;  // launch_kv4_many: one on each
 constexpr int kKv4ManyRows = 128;  // and tiles of that many rows, so group <= 128
+// Keys of a sequence at most: the kernels count in 32 bits and look up to three
+// steps of 128 keys past the last one, and round up to whole steps.
+constexpr int kKv4MaxKeys = 2147483647 - 4095;
 int kv4_tile_rows(int group, int max_q, int d, long long keys);
+// What a call launches: `rows` of launch_kv4_attn's tile (0: not launched), the
+// CTAs of its clusters (0: none, the line of units) and in all; and the CTAs of
+// launch_kv4_many (0: not launched).  max_k as in Kv4Attn.
+struct Kv4Grid {
+  int rows, cluster, ctas, many;
+};
+Kv4Grid kv4_grid(int B, int Hk, int group, int d, int max_q, int max_k, int num_sms);
 size_t kv4_workspace(int rows, int d);  // of either kernel, by its rows
-cudaError_t launch_kv4_attn(const Kv4Attn &p, int rows, int dtype, float *ws, int num_sms,
+cudaError_t launch_kv4_attn(const Kv4Attn &p, const Kv4Grid &g, int dtype, float *ws,
                             cudaStream_t s);
 // status: the device's status word; wait_limit_ns bounds its barrier waits;
 // skip_load: the test hook that leaves out a tile's values.
-cudaError_t launch_kv4_many(const Kv4Attn &p, int tile_rows, int dtype, float *ws, int num_sms,
+cudaError_t launch_kv4_many(const Kv4Attn &p, const Kv4Grid &g, int dtype, float *ws,
                             unsigned *status, unsigned long long wait_limit_ns, int skip_load,
                             cudaStream_t s);
 

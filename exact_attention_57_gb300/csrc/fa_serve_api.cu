@@ -94,6 +94,14 @@ bool disjoint_rows(long long d, Dim a, Dim b, Dim c) {
   return true;
 }
 
+// The bound on a sequence's keys that the kernels get: the caller's, what the
+// table holds, and what they count in 32 bits.
+int kv4_max_keys(int max_seqlen_k, int max_blocks, int bs_log2) {
+  long long n = static_cast<long long>(max_blocks) << bs_log2;
+  if (n > max_seqlen_k) n = max_seqlen_k;
+  return n > fa::kKv4MaxKeys ? fa::kKv4MaxKeys : static_cast<int>(n);
+}
+
 int done(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
 
 }  // namespace
@@ -274,6 +282,26 @@ extern "C" int fa_kv4_gather(const long long *slots, int R, const void *k_codes,
                                     static_cast<cudaStream_t>(stream)));
 }
 
+extern "C" int fa_fwd_kv4_schedule(int B, int Hq, int Hk, int max_seqlen_q, int max_seqlen_k,
+                                   int max_blocks, int block_size, int d, int num_sms,
+                                   int *max_keys, int *tile_rows, int *cluster, int *ctas,
+                                   int *many_ctas) {
+  if (!max_keys || !tile_rows || !cluster || !ctas || !many_ctas) return FA_ERR_INVALID_ARG;
+  const int lg = block_log2(block_size);
+  if (B < 1 || B > 65535 || Hq < 1 || Hq > 65535 || Hk < 1 || Hq % Hk != 0 || max_seqlen_q < 1 ||
+      max_seqlen_k < 0 || max_blocks < 1 || lg < 0 || d < 1 || num_sms < 1)
+    return FA_ERR_INVALID_ARG;
+  if ((static_cast<long long>(max_blocks) << lg) > 2147483647LL) return FA_ERR_INVALID_ARG;
+  if ((d != 64 && d != 128) || Hq / Hk > fa::kKv4ManyRows) return FA_ERR_UNSUPPORTED;
+  *max_keys = kv4_max_keys(max_seqlen_k, max_blocks, lg);
+  const fa::Kv4Grid g = fa::kv4_grid(B, Hk, Hq / Hk, d, max_seqlen_q, *max_keys, num_sms);
+  *tile_rows = g.rows;
+  *cluster = g.cluster;
+  *ctas = g.ctas;
+  *many_ctas = g.many;
+  return FA_OK;
+}
+
 extern "C" unsigned long long fa_fwd_kv4_workspace(int B, int Hq, int Hk, int max_seqlen_q, int d) {
   if (B < 1 || Hq < 1 || Hk < 1 || Hq % Hk != 0 || max_seqlen_q < 1 || d < 1) return 0;
   const int group = Hq / Hk, tile = fa::kv4_tile_rows(group, max_seqlen_q, d, 0);
@@ -342,20 +370,18 @@ extern "C" int fa_fwd_kv4(const void *q, void *o, float *lse, const void *k_code
   p.group = Hq / Hk;
   p.total_q = total_q;
   p.max_q = max_seqlen_q;
-  p.max_k = max_seqlen_k;
+  p.max_k = kv4_max_keys(max_seqlen_k, max_blocks, c.bs_log2);
   p.width = max_blocks;
   p.scale_log2 = scale_log2;
   p.v_mul = static_cast<float>(std::ldexp(1.0, v_exp));
   p.causal = causal;
-  const int tile =
-      fa::kv4_tile_rows(p.group, max_seqlen_q, d, static_cast<long long>(B) * Hk * max_seqlen_k);
+  const fa::Kv4Grid g =
+      fa::kv4_grid(B, Hk, p.group, d, max_seqlen_q, p.max_k, fa::api_sm_count());
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int sms = fa::api_sm_count();
   float *ws = static_cast<float *>(workspace);
   cudaError_t e = cudaSuccess;
-  if (tile > 0) e = fa::launch_kv4_attn(p, tile, dtype, ws, sms, s);
-  if (e == cudaSuccess && static_cast<long long>(max_seqlen_q) * p.group > tile)
-    e = fa::launch_kv4_many(p, tile, dtype, ws, sms, status, fa::api_wait_limit(),
-                            fa::api_skip_load(), s);
+  if (g.rows > 0) e = fa::launch_kv4_attn(p, g, dtype, ws, s);
+  if (e == cudaSuccess && g.many > 0)
+    e = fa::launch_kv4_many(p, g, dtype, ws, status, fa::api_wait_limit(), fa::api_skip_load(), s);
   return done(e);
 }

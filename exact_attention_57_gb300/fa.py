@@ -39,7 +39,7 @@ EXPORTED = ("fa_fwd", "fa_fwd_host", "fa_fwd_status", "fa_status_string", "fa_ve
             "fa_fwd_varlen", "fa_bwd", "fa_bwd_workspace", "fa_fwd_staged",
             "fa_fwd_staged_workspace", "fa_bwd_varlen", "fa_bwd_varlen_workspace",
             "fa_kv_plan", "fa_rope_table", "fa_rope", "fa_kv4_append", "fa_kv4_gather",
-            "fa_fwd_kv4", "fa_fwd_kv4_workspace")
+            "fa_fwd_kv4", "fa_fwd_kv4_workspace", "fa_fwd_kv4_schedule")
 
 _lib = None
 
@@ -123,6 +123,8 @@ def load(path: str | None = None):
     lib.fa_fwd_kv4.restype = i
     lib.fa_fwd_kv4_workspace.argtypes = [i] * 5
     lib.fa_fwd_kv4_workspace.restype = ull
+    lib.fa_fwd_kv4_schedule.argtypes = [i] * 9 + [ctypes.POINTER(i)] * 5
+    lib.fa_fwd_kv4_schedule.restype = i
     if path is None:
         _lib = lib
     return lib
@@ -471,6 +473,17 @@ def fa_fwd_kv4(q, o, lse, k_codes, k_scales, v_codes, v_scales, block_table, seq
 
 def fa_fwd_kv4_workspace(B, Hq, Hk, max_seqlen_q, d) -> int:
     return load().fa_fwd_kv4_workspace(B, Hq, Hk, max_seqlen_q, d)
+
+
+def fa_fwd_kv4_schedule(B, Hq, Hk, max_seqlen_q, max_seqlen_k, max_blocks, block_size, d, num_sms):
+    """(status, bound on the keys, rows of the tile for few rows, CTAs of its
+    clusters, its CTAs, CTAs of the kernel for more rows) of fa_fwd_kv4 on a
+    GPU with num_sms SMs (host-only)."""
+    r = [ctypes.c_int(0) for _ in range(5)]
+    st = load().fa_fwd_kv4_schedule(int(B), int(Hq), int(Hk), int(max_seqlen_q), int(max_seqlen_k),
+                                    int(max_blocks), int(block_size), int(d), int(num_sms),
+                                    *map(ctypes.byref, r))
+    return (st, *(x.value for x in r))
 
 
 # The wrappers below run once or more in every layer of every step of a server,

@@ -467,10 +467,10 @@ FA_API int fa_kv4_gather(const long long *slots, int R, const void *k_codes, con
  *               sequence b in order.  A table entry outside [0, num_blocks)
  *               takes its tokens out of the softmax.
  * max_seqlen_q, max_seqlen_k  bounds on the lengths; longer sequences are cut
- *               to them (max_blocks * block_size bounds the keys too).  A loose
- *               max_seqlen_k costs little: it bounds the grid, and up to a few
+ *               to them.  max_blocks * block_size and 2^31 - 4096 bound the keys
+ *               too.  The least of the three bounds the grid, and up to a few
  *               thousand keys it is what says that a small batch needs one launch
- *               instead of two.
+ *               instead of two (fa_fwd_kv4_schedule shows the choice).
  * causal        1: query i of n_q sees key j iff j <= n_k - n_q + i (aligned
  *               at the end, as the new tokens are the last cached ones); 0:
  *               all keys.  A row that sees no key gets O = 0, LSE = -inf.
@@ -496,6 +496,24 @@ FA_API int fa_fwd_kv4(const void *q, void *o, float *lse, const void *k_codes, c
 /* Bytes of workspace fa_fwd_kv4 needs: a function of Hq/Hk, max_seqlen_q and d,
  * not of the lengths or the batch; 0 for invalid or unsupported arguments. */
 FA_API unsigned long long fa_fwd_kv4_workspace(int B, int Hq, int Hk, int max_seqlen_q, int d);
+
+/*
+ * fa_fwd_kv4_schedule — what fa_fwd_kv4 launches for these sizes on a GPU with
+ * num_sms SMs; a host-only function, for reports and tests.
+ *   *max_keys   the bound on a sequence's keys (see max_seqlen_k above).
+ *   *tile_rows  rows (queries times Hq/Hk) of a sequence and key head that the
+ *               kernel for few rows holds: 8, 16 or 32; 0: it is not launched.
+ *   *cluster    1, 2, 4 or 8: that kernel runs one cluster of so many CTAs for
+ *               every sequence and key head, in one launch; 0: *ctas equal
+ *               shares of all the keys, joined by a second launch.
+ *   *ctas       its CTAs.  *many_ctas: those of the kernel for the sequences
+ *               with more rows (0: not launched; its parts are joined by a
+ *               launch too).
+ * Returns FA_OK, FA_ERR_INVALID_ARG or FA_ERR_UNSUPPORTED as fa_fwd_kv4 does.
+ */
+FA_API int fa_fwd_kv4_schedule(int B, int Hq, int Hk, int max_seqlen_q, int max_seqlen_k,
+                        int max_blocks, int block_size, int d, int num_sms, int *max_keys,
+                        int *tile_rows, int *cluster, int *ctas, int *many_ctas);
 
 /*
  * fa_fwd_host — the same forward on HOST buffers.

@@ -204,6 +204,59 @@ def test_attention_workspace(Hq, Hk, max_q, d):
         assert fa.fa_fwd_kv4_workspace(*args) == 0
 
 
+SM = 152
+MAX_KEYS = 2 ** 31 - 4096
+
+
+@pytest.mark.parametrize("bound", [0, 1, 127, 128, 129, 8191, 8192, 131072, 2 ** 20, 2 ** 30,
+                                   2 ** 31 - 4097, 2 ** 31 - 4096, 2 ** 31 - 129, 2 ** 31 - 127,
+                                   2 ** 31 - 64, 2 ** 31 - 2, 2 ** 31 - 1])
+@pytest.mark.parametrize("Hq,Hk,max_q", [(8, 8, 1), (32, 8, 1), (64, 8, 1), (8, 8, 9), (32, 1, 1),
+                                         (32, 8, 64), (128, 1, 3), (1, 1, 1)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_grid_for_any_bound(bound, Hq, Hk, max_q, d):
+    """The grids for every bound on the keys up to the type's end and 1 to 65535
+    sequences: at least one CTA, none whose parts the workspace does not hold,
+    clusters only where one wave holds them and a CTA gets few units; and the
+    table's width bounds the keys like the argument."""
+    need = fa.fa_fwd_kv4_workspace(1, Hq, Hk, max_q, d)
+    for B in (1, 2, 5, 19, 38, 39, 40, 56, 64, 152, 153, 304, 305, 448, 65535):
+        for bs, width in ((16, 2 ** 27 - 1), (128, 2 ** 24 - 1), (16, 64), (128, 1)):
+            st, keys, rows, cl, ctas, many = fa.fa_fwd_kv4_schedule(B, Hq, Hk, max_q, bound, width,
+                                                                    bs, d, SM)
+            assert st == fa.FA_OK
+            assert keys == min(bound, width * bs, MAX_KEYS)
+            assert rows in (0, 8, 16, 32) and cl in (0, 1, 2, 4, 8)
+            heads, group = B * Hk, Hq // Hk
+            assert rows == 0 or rows >= group
+            assert (many > 0) == (max_q * group > rows) and 0 <= many <= SM
+            if rows == 0:
+                assert ctas == cl == 0 and many > 0
+                continue
+            unit = 64 if rows == 32 and d == 64 else 128
+            units = max(1, -(-keys // unit))
+            if cl:
+                assert ctas == cl * heads <= 2 * SM and units <= 8 * cl
+            else:
+                assert 1 <= ctas <= min(2 * SM, heads * units)
+                part = rows * (d + 2) * 4  # a CTA's record and its two parts
+                assert need >= 304 * 16 + 2 * ctas * part
+                if rows < 32 and heads <= SM:  # even one CTA a cluster would get too many
+                    assert units > 8
+            again = fa.fa_fwd_kv4_schedule(B, Hq, Hk, max_q, keys, width, bs, d, SM)
+            assert again == (st, keys, rows, cl, ctas, many)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(), fa.FA_OK), (dict(B=0), 1), (dict(B=65536), 1), (dict(Hq=0), 1), (dict(Hq=9), 1),
+    (dict(Hk=0), 1), (dict(max_q=0), 1), (dict(max_k=-1), 1), (dict(width=0), 1),
+    (dict(width=2 ** 27), 1), (dict(bs=8), 1), (dict(sms=0), 1), (dict(d=0), 1),
+    (dict(d=32), fa.FA_ERR_UNSUPPORTED), (dict(Hq=516), fa.FA_ERR_UNSUPPORTED)], ids=str)
+def test_attention_schedule_refusals(kw, want):
+    a = dict(dict(B=3, Hq=8, Hk=4, max_q=2, max_k=500, width=40, bs=16, d=128, sms=SM), **kw)
+    assert fa.fa_fwd_kv4_schedule(*a.values())[0] == want
+
+
 def test_wrappers_refuse_cpu_tensors_and_wrong_shapes():
     i32 = torch.zeros(3, dtype=torch.int32)
     with pytest.raises(ValueError):

@@ -768,6 +768,69 @@ def test_attention_of_32_rows_and_a_bound_of_many_keys(nqs):
                         torch.bfloat16, label=str(max_k))
 
 
+@pytest.mark.parametrize("B,Hq,Hk,nq,d", [(1, 32, 8, 1, 128), (3, 8, 8, 3, 64), (40, 8, 8, 1, 64),
+                                          (56, 8, 8, 1, 128), (64, 16, 8, 1, 64), (5, 32, 2, 2, 128),
+                                          (9, 4, 2, 50, 64), (19, 16, 1, 2, 64)])
+def test_attention_without_a_bound_on_the_keys(B, Hq, Hk, nq, d):
+    """max_seqlen_k of 2^31 - 1 is the table's width: the same launches, the same
+    results bit for bit, nothing behind the workspace is written."""
+    lens = [(211 * b + 700) % 900 for b in range(B)]
+    nqs = [nq] * B
+    q, cache, table, cu = small(71 + B, lens, nqs, Hq=Hq, Hk=Hk, d=d)
+    need = fa.fa_fwd_kv4_workspace(B, Hq, Hk, nq, d)
+    got = []
+    for max_k in (len(table[0]) * 16, 2 ** 31 - 128, 2 ** 31 - 1):
+        ws = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device=DEV)
+        got.append(call(q, cache, table, lens, cu, nqs, max_k=max_k, workspace=ws[:need]))
+        assert (ws[need:] == 0x5A).all()
+    assert fa.fa_fwd_status(torch.cuda.current_stream().cuda_stream) == (fa.FA_OK, 0)
+    for o, lse in got[1:]:
+        assert torch.equal(o, got[0][0]) and torch.equal(lse, got[0][1])
+    check_attention(q, cache, table, lens, nqs, 16, d, d ** -0.5, True, *got[0], torch.bfloat16)
+
+
+@pytest.mark.parametrize("B,Hq,Hk,nqs,d", [(1, 3, 1, 1, 64), (1, 16, 1, 1, 128), (17, 8, 1, 1, 128),
+                                           (40, 12, 1, 1, 64), (100, 16, 1, 1, 128), (2, 16, 2, 4, 128),
+                                           (2, 8, 2, 2, 64), (5, 64, 2, 1, 128), (3, 16, 2, 40, 128)])
+def test_attention_of_short_sequences_in_a_wide_table(B, Hq, Hk, nqs, d):
+    """Where table and bound leave room for a million keys the line of units is
+    dealt out and joined, and 32 rows of 128 elements go to the kernel for many
+    queries, however short the sequences are."""
+    lens = [(137 * b + 1000) % 1025 if b % 7 != 3 else b % 2 for b in range(B)]
+    nqs = [nqs] * B
+    q, cache, table, cu = small(81 + B, lens, nqs, Hq=Hq, Hk=Hk, d=d)
+    wide = torch.full((B, 65536), 2 ** 31 - 1, dtype=torch.int32, device=DEV)
+    wide[:, :len(table[0])] = ints(table)
+    rows, cl = fa.fa_fwd_kv4_schedule(B, Hq, Hk, nqs[0], 2 ** 31 - 1, 65536, 16, d, 152)[2:4]
+    assert cl == 0 and rows == (0 if d == 128 and nqs[0] * Hq // Hk == 32 else rows)
+    o, lse = fa.attention_kv4(q.to(DEV), *(c.to(DEV) for c in cache), wide, ints(lens), 2 ** 31 - 1,
+                              cu_seqlens_q=ints(cu), max_seqlen_q=nqs[0])
+    assert fa.fa_fwd_status(torch.cuda.current_stream().cuda_stream) == (fa.FA_OK, 0)
+    check_attention(q, cache, table, lens, nqs, 16, d, d ** -0.5, True, o, lse, torch.bfloat16)
+
+
+@pytest.mark.parametrize("nq", [1, 40])
+def test_attention_of_a_sequence_as_long_as_its_type_allows(nq):
+    """A length of 2^31 - 1 in a table of 2^31 - 16 tokens is cut to 2^31 - 4096:
+    of the few blocks that are there, those at the start, in the middle and at
+    that end count, the ones behind it do not."""
+    bs, d, Hq = 16, 64, 2
+    width = 2 ** 27 - 1
+    end = 2 ** 31 - 4096
+    g = gen(77)
+    cache = random_cache(6, 1, bs, d, g)
+    table = torch.full((1, width), -1, dtype=torch.int32, device=DEV)
+    at = [0, 1, 2 ** 26 + 3, end // bs - 1, end // bs, width - 1]
+    table[0, at] = torch.arange(6, dtype=torch.int32, device=DEV)
+    q = torch.randn(nq, Hq, d, generator=g).bfloat16()
+    o, lse = fa.attention_kv4(q.to(DEV), *(c.to(DEV) for c in cache), table, ints([2 ** 31 - 1]),
+                              2 ** 31 - 1, cu_seqlens_q=ints([0, nq]), max_seqlen_q=nq)
+    assert fa.fa_fwd_status(torch.cuda.current_stream().cuda_stream) == (fa.FA_OK, 0)
+    # the last block's keys are the last 16 of the sequence; the rest everyone sees
+    small_table, n = [[0, 1, 2] + [-1] * (nq // bs + 1) + [3]], (5 + nq // bs) * bs
+    check_attention(q, cache, small_table, [n], [nq], bs, d, d ** -0.5, True, o, lse, torch.bfloat16)
+
+
 def test_repeated_calls_are_the_same_bit_for_bit():
     """Parts are joined in a fixed order: no result depends on which CTA was
     first, at one query a sequence and at many."""
