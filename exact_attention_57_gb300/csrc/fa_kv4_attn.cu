@@ -187,9 +187,10 @@ __global__ void __launch_bounds__(Shape<NT, D>::kWarps * 32, Shape<NT, D>::kCtas
   // four columns of a finished row
   auto put = [&](int i, int head, int col, float4 sum, float m, float l) {
     const long long out = static_cast<long long>(i) * p.Hq + head;
-    const float inv = l > 0.f ? p.v_mul / l : 0.f;
-    alignas(8) T e[4] = {static_cast<T>(sum.x * inv), static_cast<T>(sum.y * inv),
-                         static_cast<T>(sum.z * inv), static_cast<T>(sum.w * inv)};
+    const float inv = p.v_mul / l;
+    alignas(8) T e[4] = {
+        static_cast<T>(value_of(sum.x, l, inv)), static_cast<T>(value_of(sum.y, l, inv)),
+        static_cast<T>(value_of(sum.z, l, inv)), static_cast<T>(value_of(sum.w, l, inv))};
     *reinterpret_cast<uint2 *>(static_cast<T *>(p.o) + out * D + col) =
         *reinterpret_cast<const uint2 *>(e);
     if (col == 0) p.lse[static_cast<long long>(head) * p.total_q + i] = lse_of(m, l);

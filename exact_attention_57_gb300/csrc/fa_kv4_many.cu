@@ -677,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // 32 bytes a store, as rows lie far apart: 16 took 454 us instead of 451 for
         // the two chunks above, 525 instead of 516 for 8 prompts of 2048
         const bool wide = reinterpret_cast<uintptr_t>(p.o) % 32 == 0;
-        const float inv = l > 0.f ? p.v_mul / l : 0.f;
+        const float inv = p.v_mul / l;
         const int head = x.h * p.group + tj;
         T *out = static_cast<T *>(p.o) +
                  (in ? (static_cast<long long>(x.s.r0 + i) * p.Hq + head) * D : 0);
@@ -695,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               alignas(32) T e[16];
 #pragma unroll
               for (int y = 0; y < 16; ++y)
-                e[y] = static_cast<T>(l > 0.f ? __uint_as_float(o[16 * u + y]) * inv : 0.f);
+                e[y] = static_cast<T>(value_of(__uint_as_float(o[16 * u + y]), l, inv));
               if (wide) {
                 store32(out + c + 16 * u, *reinterpret_cast<const B32 *>(e));
               } else {

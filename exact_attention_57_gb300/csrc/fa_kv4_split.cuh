@@ -34,9 +34,17 @@ __device__ __forceinline__ Seq load_seq(const Kv4Attn &p, int b) {
 constexpr float kHeadroom = 7.f, kGrow = 8.f;
 static_assert(kHeadroom + kGrow < 16.f, "weights up to 2^15 are finite in fp16");
 
-// log(sum e^s) of a row, from its m and the sum l of its weights.
+// A row's results from its m, the sum l of its weights and a sum of weighted
+// values (inv = v_mul / l).  l is zero for a row without keys, and for no other
+// row whose scores are numbers: its largest weight is 2^kHeadroom.  A NaN among
+// the scores of a row is in l, whatever m, and so in its results, as in those of
+// fa_fwd; a NaN weight of a part stays one in the sums that join the parts, since
+// 0 * NaN is NaN.
 __device__ __forceinline__ float lse_of(float m, float l) {
-  return l > 0.f ? (m + kHeadroom) * 0.6931471805599453f + logf(l * 0.0078125f) : -INFINITY;
+  return l == 0.f ? -INFINITY : (m + kHeadroom) * 0.6931471805599453f + logf(l * 0.0078125f);
+}
+__device__ __forceinline__ float value_of(float sum, float l, float inv) {
+  return l == 0.f ? 0.f : sum * inv;
 }
 static_assert(kHeadroom == 7.f, "lse_of divides by 2^kHeadroom");
 
@@ -196,9 +204,8 @@ __global__ void __launch_bounds__(kJoinThreads) fa_kv4_join_kernel(const Kv4Attn
       if (n + x * kWarps > mine.last) break;
 #pragma unroll
       for (int y = 0; y < kJoinRows; ++y) {
-        const float to = fmaxf(mm[y], ml[x][y].x);
-        if (to == -INFINITY) continue;
-        const float f = ex2_approx(mm[y] - to), g = ex2_approx(ml[x][y].x - to);
+        const float to = fmaxf(mm[y], ml[x][y].x), off = to == -INFINITY ? 0.f : to;
+        const float f = ex2_approx(mm[y] - off), g = ex2_approx(ml[x][y].x - off);
         mm[y] = to;
         ll[y] = f * ll[y] + g * ml[x][y].y;
 #pragma unroll
@@ -227,10 +234,10 @@ __global__ void __launch_bounds__(kJoinThreads) fa_kv4_join_kernel(const Kv4Attn
   const int row = row0 + warp, y = row / p.group, j = row - y * p.group, i = mine.row0 + y;
   const int head = mine.h * p.group + j;
   T *out = static_cast<T *>(p.o) + (static_cast<long long>(i) * p.Hq + head) * D + lane * W;
-  const float inv = l > 0.f ? p.v_mul / l : 0.f;
+  const float inv = p.v_mul / l;
   alignas(8) T e[W];
 #pragma unroll
-  for (int x = 0; x < W; ++x) e[x] = static_cast<T>(total[x] * inv);
+  for (int x = 0; x < W; ++x) e[x] = static_cast<T>(value_of(total[x], l, inv));
   if constexpr (W == 4)
     *reinterpret_cast<uint2 *>(out) = *reinterpret_cast<const uint2 *>(e);
   else

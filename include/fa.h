@@ -473,7 +473,8 @@ FA_API int fa_kv4_gather(const long long *slots, int R, const void *k_codes, con
  *               instead of two (fa_fwd_kv4_schedule shows the choice).
  * causal        1: query i of n_q sees key j iff j <= n_k - n_q + i (aligned
  *               at the end, as the new tokens are the last cached ones); 0:
- *               all keys.  A row that sees no key gets O = 0, LSE = -inf.
+ *               all keys.  A row that sees no key gets O = 0, LSE = -inf; one with
+ *               a NaN among its scores gets NaN for both.
  * d 64 or 128, Hq/Hk at most 128 (else FA_ERR_UNSUPPORTED); fp32 types are
  * FA_ERR_UNSUPPORTED.  Queries become fp16 times a power of two a row (exact but
  * for elements below 2^-14 of the row's largest, off by 2^-25 of it at most),

@@ -541,6 +541,75 @@ def test_attention_queries_of_extreme_size(dt):
         assert ((lse.double().cpu() - wl).abs() <= tol_l + extra).all()
 
 
+NON_FINITE = [
+    # key lengths, query lengths, Hq, Hk, d, width of the table in blocks (0: what they need)
+    ((300, 33), (1, 1), 8, 2, 128, 0),           # clusters
+    ((300, 33), (3, 1), 4, 1, 64, 65536),        # the line, joined or not
+    ((20000, 90, 5000), (1, 2, 1), 8, 2, 128, 0),
+    ((70, 40), (4, 2), 8, 1, 128, 65536),        # the kernel for many queries at 32 rows
+    ((513, 300), (64, 200), 6, 3, 64, 0),        # whole tiles
+    ((9000, 3000), (70, 90), 4, 1, 128, 0),      # tiles that several CTAs share
+]
+
+
+@pytest.mark.parametrize("case", NON_FINITE, ids=[str(i) for i in range(len(NON_FINITE))])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attention_shows_nan_and_infinity(case, causal):
+    """A query row with a NaN, or with an infinity that some key meets, gets NaN
+    for O and LSE whichever path takes it; a NaN in a key's scale, the rows that
+    see this key.  The other rows are as without it."""
+    lens, nqs, Hq, Hk, d, width = case
+    q, cache, table, cu = small(91, lens, nqs, Hq=Hq, Hk=Hk, d=d)
+    wide = ints(table)
+    if width:
+        wide = torch.full((len(lens), width), -1, dtype=torch.int32, device=DEV)
+        wide[:, :len(table[0])] = ints(table)
+    bad = torch.zeros(q.shape[:2], dtype=torch.bool)
+    spoiled = q.clone()
+    for row, head, value in ((0, 0, math.nan), (cu[1], Hq - 1, math.inf), (cu[-1] - 1, 1, -math.inf)):
+        spoiled[row, head, 5] = value
+        bad[row, head] = True
+    # the last key of the last sequence: its last query alone sees it when causal
+    keys = [c.clone() for c in cache]
+    n = lens[-1]
+    keys[1][table[-1][(n - 1) // 16], Hk - 1, (n - 1) % 16, 2] = 0x7F
+    blind = torch.zeros_like(bad)
+    blind[(-1 if causal else cu[-2]):, -(Hq // Hk):] = True
+    for x, c, off in ((spoiled, cache, bad), (q, keys, blind)):
+        o, lse = fa.attention_kv4(x.to(DEV), *(t.to(DEV) for t in c), wide, ints(list(lens)),
+                                  2 ** 31 - 1, cu_seqlens_q=ints(cu), max_seqlen_q=max(nqs),
+                                  causal=causal)
+        o, lse = o.cpu(), lse.cpu()
+        assert torch.isnan(o[off]).all() and torch.isnan(lse.t()[off]).all()
+        assert not torch.isnan(o[~off]).any() and not torch.isnan(lse.t()[~off]).any()
+        # the rows without one against the reference, the others as if they were whole
+        clean, cl = call(q, cache, table, lens, cu, nqs, causal=causal)
+        o[off], lse.t()[off] = clean.cpu()[off], cl.cpu().t()[off]
+        check_attention(q, cache, table, lens, nqs, 16, d, d ** -0.5, causal, o, lse, torch.bfloat16)
+
+
+@pytest.mark.parametrize("nqs", [(1, 2), (40, 60)])
+def test_attention_of_infinities_that_take_keys_away(nqs):
+    """Scores of -inf have no weight: keys whose element meets the query's infinity
+    with the other sign are as if masked, and where that is all of them the row is
+    one without keys."""
+    lens = (200, 90)
+    q, cache, table, cu = small(93, lens, nqs, Hq=4, Hk=2, d=64)
+    kc = cache[0]
+    kc[..., 0] = (kc[..., 0] & 0xF0) | 0xA       # element 0 of every key is -1 times its scale
+    q[0, 1, 0] = math.inf
+    q[-1, 2, 0] = math.inf
+    kc[table[1][2], :, 7, 0] = 0x0              # an infinity times zero: NaN (token 39)
+    o, lse = call(q, cache, table, lens, cu, nqs)
+    assert (o[0, 1] == 0).all() and lse[1, 0] == -math.inf
+    assert torch.isnan(o[-1, 2]).all() and torch.isnan(lse[2, -1])
+    q[0, 1, 0] = q[-1, 2, 0] = 0.0
+    other = call(q, cache, table, lens, cu, nqs)
+    o[0, 1], lse[1, 0] = other[0][0, 1], other[1][1, 0]
+    o[-1, 2], lse[2, -1] = other[0][-1, 2], other[1][2, -1]
+    check_attention(q, cache, table, lens, nqs, 16, 64, 64 ** -0.5, True, o, lse, torch.bfloat16)
+
+
 def test_attention_long_context():
     """A long sequence (split over many CTAs) against the float64 sums."""
     n, Hq, Hk, d, bs = 70001, 4, 1, 128, 64
