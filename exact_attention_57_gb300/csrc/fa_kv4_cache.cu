@@ -94,8 +94,9 @@ __device__ __forceinline__ void quantise(const Group<T> &x, float unit, uint2 *c
     const P *p = reinterpret_cast<const P *>(&x);
     P top = __habs2(p[0]);
 #pragma unroll
-    for (int j = 1; j < 8; ++j) top = __hmax2(top, __habs2(p[j]));  // a NaN does not count
-    amax = fmaxf(static_cast<float>(top.x), static_cast<float>(top.y)) * unit;
+    for (int j = 1; j < 8; ++j) top = __hmax2(top, __habs2(p[j]));
+    // a NaN does not count, and where there is nothing else the maximum is zero
+    amax = fmaxf(fmaxf(static_cast<float>(top.x), static_cast<float>(top.y)), 0.f) * unit;
   } else {
     const float *p = reinterpret_cast<const float *>(&x);
     amax = 0.f;

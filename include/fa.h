@@ -432,8 +432,9 @@ FA_API int fa_rope(const void *q, void *q_out, const long long *q_strides, int H
  *          may be a mixture.
  * A group of 16 elements is stored with the scale e4m3(max|x| * 2^-exp / 6)
  * and the codes e2m1(x * 2^-exp / scale), both rounded to nearest, ties to
- * even, saturating; a NaN is stored as +6, a group whose scale rounds to zero
- * as zeros.
+ * even, saturating.  NaNs take no part in the maximum and are stored as +6
+ * times the scale; a group whose scale rounds to zero, one of nothing but NaNs
+ * among them, is stored as zeros.  No scale is ever stored as NaN.
  * d a multiple of 16 up to 256 (else FA_ERR_UNSUPPORTED).
  */
 FA_API int fa_kv4_append(const void *k, const void *v, long long k_stride, long long v_stride,

@@ -314,6 +314,55 @@ def test_cache_non_finite_input_saturates():
         assert k[0, 0, 20] == 6 * 0.171875 and k[0, 0, 21] == 6 * 0.171875
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_cache_groups_of_nothing_but_nan(dtype):
+    """Stored as zeros in every type, with zeros or numbers that round to zero
+    among them too; other groups of the row are as they were."""
+    nan = math.nan
+    x = torch.ones(3, 1, 64)
+    x[0, 0, 16:32] = nan
+    x[1, 0, :] = nan
+    x[2, 0, 32:48] = torch.tensor([nan, 0.0, -nan, 1e-7] * 4)
+    x[2, 0, 48:] = torch.tensor([nan] * 15 + [6.0])
+    y = x.to(DT[dtype]).to(DEV)
+    cache = fa.kv4_cache(1, 1, 16, 64, device=DEV)
+    for c in cache:
+        c.fill_(0xAB)
+    slots = ints([3, 0, 15], torch.int64)
+    fa.kv4_append(y, y, slots, *cache)
+    k, v = fa.kv4_gather(slots, *cache, dtype=torch.float32)
+    one = 6 * 0.171875  # e4m3(1 / 6) times e2m1(1 / that) = 6
+    want = torch.full((3, 1, 64), one)
+    want[0, 0, 16:32] = want[1] = 0.0
+    want[2, 0, 32:48] = 0.0
+    want[2, 0, 48:] = 6.0
+    assert torch.equal(k.cpu(), want) and torch.equal(v.cpu(), want)
+    for c in (cache[1], cache[3]):
+        assert ((c[0, 0, [3, 0, 15]] & 0x7F) != 0x7F).all()
+
+
+@pytest.mark.parametrize("nqs", [(4, 3), (70, 50)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_attention_of_queries_ahead_of_a_token_of_nan(nqs, dtype):
+    """A token whose key and value are NaN, hidden from all queries but the last,
+    changes nothing for the others."""
+    lens, Hq, Hk, d, bs = (90, 133), 4, 2, 64, 16
+    g = gen(95)
+    blocks = sum(-(-n // bs) for n in lens)
+    table = paged(lens, bs, blocks, g)
+    cache = fa.kv4_cache(blocks, Hk, bs, d, device=DEV)
+    slots = torch.tensor([t[j // bs] * bs + j % bs for t, n in zip(table, lens) for j in range(n)])
+    rows = [torch.randn(sum(lens), Hk, d, generator=g).to(DT[dtype]) for _ in range(2)]
+    for x in rows:
+        x[lens[0] - 1] = x[-1] = math.nan
+    fa.kv4_append(*(x.to(DEV) for x in rows), slots.to(DEV), *cache)
+    q = torch.randn(sum(nqs), Hq, d, generator=g).bfloat16()
+    cpu = [c.cpu() for c in cache]
+    o, lse = call(q, cpu, table, lens, [0, nqs[0], sum(nqs)], nqs)
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+    check_attention(q, cpu, table, lens, nqs, bs, d, d ** -0.5, True, o, lse, torch.bfloat16)
+
+
 # ------------------------------------------------------------------ attention
 def random_cache(blocks, Hk, bs, d, g):
     """Every code, scales 2^-2 .. 1: scores and values of the usual size."""
