@@ -79,6 +79,49 @@ struct Dim {
   int count;
 };
 
+// Rows of `row` bytes at every combination of three strides (bytes, not negative).
+struct Rows {
+  const void *p;
+  long long row;
+  Dim dims[3];
+  // From the first byte to behind the last.  (Below 2^63: see kMaxExtent.)
+  long long extent() const {
+    long long n = row;
+    for (const Dim &x : dims) n += x.stride * (x.count - 1);
+    return n;
+  }
+};
+// Each dimension's reach, in bytes: the sum of three and their products below
+// stay far from 64 bits, and no address space is larger.
+constexpr long long kMaxExtent = 1LL << 56;
+
+// Whether a byte may be in both: their spans meet, and no pitch keeps them apart.
+// A pitch is one of their strides; the strides that are multiples of it only move
+// rows by whole pitches, so the two lie apart where the columns modulo the pitch
+// that the others cover do (q and k as slices of one projection's rows).  Rows
+// that interleave in another way count as meeting.
+bool may_meet(const Rows &a, const Rows &b) {
+  if (!a.p || !b.p) return false;
+  if (!meet(Span{a.p, static_cast<size_t>(a.extent())}, Span{b.p, static_cast<size_t>(b.extent())}))
+    return false;
+  for (const Rows *from : {&a, &b})
+    for (const Dim &x : from->dims) {
+      const long long pitch = x.stride;
+      if (x.count == 1 || pitch == 0) continue;
+      auto columns = [&](const Rows &r) {
+        long long n = r.row;
+        for (const Dim &y : r.dims)
+          if (y.stride % pitch != 0) n += y.stride * (y.count - 1);
+        return n;
+      };
+      const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+      const long long down = static_cast<long long>((pa < pb ? pb - pa : pa - pb) % pitch);
+      const long long ahead = pa < pb || down == 0 ? down : pitch - down;  // of a to b
+      if (ahead >= columns(a) && ahead + columns(b) <= pitch) return false;
+    }
+  return true;
+}
+
 // Whether the rows of d elements at every combination of three strides lie
 // apart: taken by ascending stride, each stride covers what lies below it.
 bool disjoint_rows(long long d, Dim a, Dim b, Dim c) {
@@ -204,29 +247,36 @@ extern "C" int fa_rope(const void *q, void *q_out, const long long *q_strides, i
   fa::RopeParams p = {tensor(q, q_out, q_strides, Hq), tensor(k, k_out, k_strides, Hk), positions,
                       table, static_cast<long long>(B) * N, N, d, d_rot, num_axes, interleaved,
                       inverse};
-  // Every byte touched, as one span a tensor: outputs overlap nothing but, in
-  // place, their own input at its own strides.
-  auto span = [&](const void *base, long long sb, long long sh, long long sn, int heads) {
-    return Span{base, heads == 0 ? 0
-                                 : static_cast<size_t>((B - 1) * sb + (heads - 1) * sh +
-                                                       (N - 1) * sn + d) * es};
+  // Outputs overlap nothing but, in place, their own input at its own strides.
+  auto rows = [&](const void *base, long long sb, long long sh, long long sn, int heads) {
+    auto dim = [&](long long s, int n) { return Dim{n == 1 ? 0 : s * es, n}; };
+    return Rows{base, static_cast<long long>(d) * es, {dim(sb, B), dim(sh, heads), dim(sn, N)}};
   };
-  for (const fa::RopeTensor *t : {&p.q, &p.k}) {
-    if (t->heads == 0) continue;
-    if (t->ib < 0 || t->ih < 0 || t->in_row < 0 || t->ob < 0 || t->oh < 0 || t->out_row < 0)
+  auto in_reach = [&](long long stride, int count) {
+    return stride >= 0 && (count == 1 || stride <= kMaxExtent / es / (count - 1));
+  };
+  Rows in[2] = {}, out[2] = {};
+  for (int i = 0; i < 2; ++i) {
+    const fa::RopeTensor &t = i == 0 ? p.q : p.k;
+    if (t.heads == 0) continue;
+    if (!in_reach(t.ib, B) || !in_reach(t.ih, t.heads) || !in_reach(t.in_row, N) ||
+        !in_reach(t.ob, B) || !in_reach(t.oh, t.heads) || !in_reach(t.out_row, N))
       return FA_ERR_INVALID_ARG;
-    if (!disjoint_rows(d, {t->ob, B}, {t->oh, t->heads}, {t->out_row, N}))
+    if (!disjoint_rows(d, {t.ob, B}, {t.oh, t.heads}, {t.out_row, N})) return FA_ERR_INVALID_ARG;
+    in[i] = rows(t.in, t.ib, t.ih, t.in_row, t.heads);
+    out[i] = rows(t.out, t.ob, t.oh, t.out_row, t.heads);
+    const bool same = t.in == t.out;
+    if (same ? (B > 1 && t.ib != t.ob) || (t.heads > 1 && t.ih != t.oh) ||
+                   (N > 1 && t.in_row != t.out_row)
+             : may_meet(out[i], in[i]))
       return FA_ERR_INVALID_ARG;
-    const bool same = t->in == t->out;
-    if (same && ((B > 1 && t->ib != t->ob) || (t->heads > 1 && t->ih != t->oh) ||
-                 (N > 1 && t->in_row != t->out_row)))
-      return FA_ERR_INVALID_ARG;
-    const Span out[] = {span(t->out, t->ob, t->oh, t->out_row, t->heads)};
-    const Span in[] = {{positions, static_cast<size_t>(num_axes) * p.rows * 4},
-                       {table, static_cast<size_t>(d_rot / 2) * 8},
-                       same ? Span{nullptr, 0} : span(t->in, t->ib, t->ih, t->in_row, t->heads)};
-    if (any_meet(out, in)) return FA_ERR_INVALID_ARG;
+    const Span to[] = {{out[i].p, static_cast<size_t>(out[i].extent())}};
+    const Span from[] = {{positions, static_cast<size_t>(num_axes) * p.rows * 4},
+                         {table, static_cast<size_t>(d_rot / 2) * 8}};
+    if (any_meet(to, from)) return FA_ERR_INVALID_ARG;
   }
+  if (may_meet(out[0], out[1]) || may_meet(out[0], in[1]) || may_meet(out[1], in[0]))
+    return FA_ERR_INVALID_ARG;
   int rc;
   if ((rc = fa::api_device_check()) != FA_OK) return rc;
   return done(fa::launch_rope(p, dtype, fa::api_sm_count(), static_cast<cudaStream_t>(stream)));

@@ -400,8 +400,11 @@ FA_API int fa_rope_table(const double *inv_freq, const int *axis, int n,
  * dk from fa_bwd in, the gradients before the rotation out.
  *
  * q, k          inputs [B, Hq, N, d] and [B, Hk, N, d]; q_out, k_out outputs,
- *               either the input itself (in place, the same strides) or
- *               overlapping no input.  k may be NULL with Hk = 0.
+ *               either their own input (in place, the same strides) or
+ *               overlapping no input, and never one another
+ *               (FA_ERR_INVALID_ARG).  Rows may interleave with another
+ *               tensor's at a common pitch, as slices of one projection do.
+ *               k may be NULL with Hk = 0.
  * q_strides, k_strides  host arrays of six element strides, {batch, head, row}
  *               of the input, then of the output, none negative (rows are d
  *               contiguous elements; rows of an output lie apart); NULL:

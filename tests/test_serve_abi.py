@@ -81,6 +81,97 @@ def test_rope_refusals(kw):
     assert rope(**kw) == fa.FA_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("kw", [
+    dict(qo=A(2)), dict(ko=A(0)), dict(qo=A(3)), dict(ko=A(1) + 4096), dict(qo=A(2), ko=A(0)),
+    dict(q=A(2), qo=A(2)), dict(k=A(0), ko=A(0), qo=A(0), Hk=4),          # one tensor twice, in place
+    dict(k=A(0) + 128, ko=A(0) + 128, qo=A(0)),                           # in place, shifted
+    dict(qo=A(2) + 512, ks=L6(896, 448, 64, 896, 448, 64)),
+    # slices of one projection's rows of 512 elements: columns that meet by one element
+    dict(q=A(0), qo=A(0), qs=L6(3584, 64, 512, 3584, 64, 512),
+         k=A(0) + 510, ko=A(0) + 510, ks=L6(3584, 64, 512, 3584, 64, 512)),
+    dict(qs=L6(1 << 62, 448, 64, 1792, 448, 64)), dict(ks=L6(896, 448, 64, 1 << 62, 448, 64)),
+], ids=str)
+def test_rope_refuses_outputs_on_the_other_tensor(kw):
+    assert rope(**kw) == fa.FA_ERR_INVALID_ARG
+
+
+host_only = pytest.mark.skipif(torch.cuda.is_available(), reason="host-only: fake device addresses")
+
+
+@host_only
+@pytest.mark.parametrize("kw", [
+    dict(qo=A(0)), dict(qo=A(0), ko=A(2)), dict(),
+    # rows of 512 elements: q's four heads, then k's two, in place, or moved behind them
+    dict(qo=A(0), qs=L6(3584, 64, 512, 3584, 64, 512), k=A(0) + 512, ko=A(0) + 512,
+         ks=L6(3584, 64, 512, 3584, 64, 512)),
+    dict(q=A(0), qo=A(0), qs=L6(3584, 64, 512, 3584, 64, 512), k=A(0) + 512, ko=A(0) + 768,
+         ks=L6(3584, 64, 512, 3584, 64, 512)),
+    # heads in one buffer, [B, 6, N, d]
+    dict(qo=A(0), qs=L6(2688, 448, 64, 2688, 448, 64), k=A(0) + 3584, ko=A(0) + 3584,
+         ks=L6(2688, 448, 64, 2688, 448, 64)),
+    # the halves of rows of 128 elements
+    dict(qo=A(0), Hk=4, qs=L6(3584, 896, 128, 3584, 896, 128), k=A(0) + 128, ko=A(0) + 128,
+         ks=L6(3584, 896, 128, 3584, 896, 128)),
+    dict(B=1, N=1, qs=L6(1 << 62, 64, 1 << 62, 1 << 62, 64, 1 << 62)),
+], ids=str)
+def test_rope_takes_rows_that_lie_apart(kw):
+    """These pass all checks and end at the device's, as there is none."""
+    assert rope(**kw) in (fa.FA_ERR_CUDA, fa.FA_ERR_UNSUPPORTED)
+
+
+@host_only
+def test_rope_overlap_check_against_the_elements_themselves():
+    """Random layouts in one small arena: a call whose outputs share an element
+    with the other tensor, with each other or, unless in place, with their own
+    input is refused; one at a common pitch that shares none is not."""
+    import itertools
+    import random
+    r = random.Random(7)
+    taken = refused = 0
+    for _ in range(4000):
+        B, N, H, d = r.choice([1, 2]), r.choice([1, 2, 3]), r.choice([1, 2, 3]), r.choice([2, 4])
+        pitch = d * r.choice([2 * H, 2 * H + 1, 3 * H])
+        fused = (N * pitch, d, pitch)
+
+        def layout():
+            kind = r.choice(["fused", "fused", "fused", "rows", "heads", "any"])
+            if kind == "any":
+                return tuple(r.randrange(0, 40) for _ in range(3))
+            return {"fused": fused, "rows": (H * N * d, N * d, d), "heads": (N * H * d, d, H * d)}[kind]
+
+        def where():
+            return r.randrange(0, 3 * pitch) if r.random() < 0.5 else r.choice([0, d, H * d, 2 * H * d])
+
+        def elements(at, st):
+            return [at + b * st[0] + h * st[1] + n * st[2] + x for b, h, n, x in
+                    itertools.product(range(B), range(H), range(N), range(d))]
+
+        t = {}
+        for name in ("q", "k"):
+            t[name] = (where(), layout())
+            t[name + "o"] = t[name] if r.random() < 0.4 else (where(), layout())
+        e = {n: elements(*v) for n, v in t.items()}
+        bad = any(len(set(e[n])) < len(e[n]) for n in ("qo", "ko"))
+        clash = [("qo", "ko"), ("qo", "k"), ("ko", "q")]
+        for n in ("q", "k"):
+            if t[n][0] == t[n + "o"][0]:  # in place: the strides that count are the same
+                bad |= any(c > 1 and a != b for c, a, b in zip((B, H, N), t[n][1], t[n + "o"][1]))
+            else:
+                clash.append((n, n + "o"))
+        bad |= any(set(e[a]) & set(e[b]) for a, b in clash)
+        st = rope(q=A(0) + 2 * t["q"][0], qo=A(0) + 2 * t["qo"][0], qs=L6(*t["q"][1], *t["qo"][1]),
+                  Hq=H, k=A(0) + 2 * t["k"][0], ko=A(0) + 2 * t["ko"][0],
+                  ks=L6(*t["k"][1], *t["ko"][1]), Hk=H, B=B, N=N, d=d, rot=d)
+        if bad:
+            assert st == fa.FA_ERR_INVALID_ARG, (t, B, N, H, d)
+            refused += 1
+        elif all(v[1] == fused for v in t.values()):
+            assert st != fa.FA_ERR_INVALID_ARG or any(
+                (v[0] % pitch) + H * d > pitch for v in t.values()), (t, B, N, H, d)
+            taken += st != fa.FA_ERR_INVALID_ARG
+    assert taken > 20 and refused > 500
+
+
 def test_rope_head_dim_above_256_is_unsupported():
     assert rope(d=264) == fa.FA_ERR_UNSUPPORTED
 

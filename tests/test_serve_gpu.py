@@ -186,6 +186,30 @@ def test_rotary_layouts_strides_and_in_place():
         assert (r.double() - bh[0][0].transpose(0, 1).double()).abs().max() <= 4 * 2 * 2.0 ** -8 * 2
 
 
+def test_rotary_from_one_slice_of_a_buffer_into_another():
+    """Outputs in other columns of the rows that hold the inputs, and the halves of
+    one row in place; an output on the other tensor is refused, nothing written."""
+    T, H, d = 11, 3, 64
+    g = gen(8)
+    table = fa.rotary_table(*ladder(64, 1), device=DEV)
+    pos = torch.randint(0, 5000, (1, T), generator=g, dtype=torch.int32).to(DEV)
+    buf = torch.randn(T, 4 * H, d, generator=g).bfloat16().to(DEV)
+    q, k, a, b = (buf[:, n * H:(n + 1) * H] for n in range(4))
+    want = fa.rotary(q, k, pos, table)
+    before = buf.clone()
+    for bad in (dict(q_out=k), dict(q_out=q, k_out=q), dict(q_out=a, k_out=a), dict(k_out=q),
+                dict(q_out=buf[:, 2 * H - 1:3 * H - 1])):
+        with pytest.raises(fa.FaError):
+            fa.rotary(q, k, pos, table, **bad)
+    assert torch.equal(buf, before)
+    fa.rotary(q, k, pos, table, q_out=a, k_out=b)
+    assert torch.equal(a, want[0]) and torch.equal(b, want[1])
+    assert torch.equal(buf[:, :2 * H], before[:, :2 * H])
+    both = torch.stack([q, k], 2)  # [T, H, 2, d]: a head's q beside its k
+    fa.rotary(both[:, :, 0], both[:, :, 1], pos, table, q_out=both[:, :, 0], k_out=both[:, :, 1])
+    assert torch.equal(both[:, :, 0], want[0]) and torch.equal(both[:, :, 1], want[1])
+
+
 def test_rotary_gradient_is_the_transpose():
     """<rotary(x), y> = <x, rotary_backward(y)>, and differences: the rotation
     is linear, so rotary(x + h e) - rotary(x) over h is column e for any h."""
