@@ -119,7 +119,10 @@ __device__ __forceinline__ int units_of(const Seq &s, int group, int rows) {
 // 64 x 1023 24 to 70 us in clusters of 2 to 8, 20 along the line.
 constexpr int kClusterUnits = 8;
 
+// Of the whole CTA; its aligned instructions want every warp together, which the
+// loops before it leave row by row.
 __device__ __forceinline__ void cluster_barrier() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }

@@ -289,6 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     *walk = k;
     if (warp == 0) *s_den = den, *s_total = at.total;
   }
+  __syncwarp();  // tcgen05's aligned instructions want the warp together
   if (warp == 12) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
@@ -624,6 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   l *= alpha;
                   m_used = m_new;
                 }
+                __syncwarp();  // ahead of P's stores
               }
             }
           }
@@ -685,6 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           alignas(32) uint32_t o[32];
+          __syncwarp();  // rows without a query left the loop's last turn early
           tmem_ld32(o_tm + c, o);
           tmem_ld_wait();
           reg_fence32(o);

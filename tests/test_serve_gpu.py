@@ -881,6 +881,20 @@ def test_attention_of_small_batches(B, Hq, d):
         assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
 
 
+@pytest.mark.parametrize("nq", [1, 3, 61])
+@pytest.mark.parametrize("Hq", [1, 3, 5, 7, 11, 13])
+@pytest.mark.parametrize("B", [1, 70, 140, 290])
+def test_attention_of_odd_rows(B, Hq, nq):
+    """Rows that end inside a warp at the joins of clusters (64 elements: 16 threads
+    a row) and inside a warp's rows of a tile."""
+    lens = [(91 * b + 300) % 350 for b in range(B if nq < 61 else 3)]
+    nqs = [nq] * len(lens)
+    q, cache, table, cu = small(101 + B, lens, nqs, Hq=Hq, Hk=1, d=64)
+    o, lse = call(q, cache, table, lens, cu, nqs)
+    assert fa.fa_fwd_status(torch.cuda.current_stream().cuda_stream) == (fa.FA_OK, 0)
+    check_attention(q, cache, table, lens, nqs, 16, 64, 0.125, True, o, lse, torch.bfloat16)
+
+
 @pytest.mark.parametrize("lens,max_k", [((8192, 5000), 8192), ((2000,) * 3, 2048),
                                         ((4096, 0, 1, 4000) * 2, 4096), ((127, 129, 128), 130)])
 def test_attention_of_few_long_sequences(lens, max_k):
