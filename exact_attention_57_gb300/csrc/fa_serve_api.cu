@@ -137,6 +137,11 @@ bool disjoint_rows(long long d, Dim a, Dim b, Dim c) {
   return true;
 }
 
+// The head dims and groups that attention over the cache is built for.
+bool kv4_attends(int d, int group) {
+  return (d == 64 || d == 128) && group <= fa::kKv4ManyRows;
+}
+
 // The bound on a sequence's keys that the kernels get: the caller's, what the
 // table holds, and what they count in 32 bits.
 int kv4_max_keys(int max_seqlen_k, int max_blocks, int bs_log2) {
@@ -342,7 +347,7 @@ extern "C" int fa_fwd_kv4_schedule(int B, int Hq, int Hk, int max_seqlen_q, int 
       max_seqlen_k < 0 || max_blocks < 1 || lg < 0 || d < 1 || num_sms < 1)
     return FA_ERR_INVALID_ARG;
   if ((static_cast<long long>(max_blocks) << lg) > 2147483647LL) return FA_ERR_INVALID_ARG;
-  if ((d != 64 && d != 128) || Hq / Hk > fa::kKv4ManyRows) return FA_ERR_UNSUPPORTED;
+  if (!kv4_attends(d, Hq / Hk)) return FA_ERR_UNSUPPORTED;
   *max_keys = kv4_max_keys(max_seqlen_k, max_blocks, lg);
   const fa::Kv4Grid g = fa::kv4_grid(B, Hk, Hq / Hk, d, max_seqlen_q, *max_keys, num_sms);
   *tile_rows = g.rows;
@@ -353,9 +358,9 @@ extern "C" int fa_fwd_kv4_schedule(int B, int Hq, int Hk, int max_seqlen_q, int 
 }
 
 extern "C" unsigned long long fa_fwd_kv4_workspace(int B, int Hq, int Hk, int max_seqlen_q, int d) {
-  if (B < 1 || Hq < 1 || Hk < 1 || Hq % Hk != 0 || max_seqlen_q < 1 || d < 1) return 0;
+  if (B < 1 || Hq < 1 || Hk < 1 || Hq % Hk != 0 || max_seqlen_q < 1) return 0;
+  if (!kv4_attends(d, Hq / Hk)) return 0;
   const int group = Hq / Hk, tile = fa::kv4_tile_rows(group, max_seqlen_q, d, 0);
-  if (group > fa::kKv4ManyRows) return 0;
   const size_t few = tile ? fa::kv4_workspace(tile, d) : 0;
   // (with many keys the other kernel may take what 32 rows hold)
   const size_t many = static_cast<long long>(max_seqlen_q) * group > tile || tile == 32
@@ -402,7 +407,7 @@ extern "C" int fa_fwd_kv4(const void *q, void *o, float *lse, const void *k_code
                      {cu_seqlens_q, static_cast<size_t>(B + 1) * 4}};
   if (any_meet(out, in)) return FA_ERR_INVALID_ARG;
   if (dtype != FA_DTYPE_BF16 && dtype != FA_DTYPE_F16) return FA_ERR_UNSUPPORTED;
-  if ((d != 64 && d != 128) || Hq / Hk > fa::kKv4ManyRows) return FA_ERR_UNSUPPORTED;
+  if (!kv4_attends(d, Hq / Hk)) return FA_ERR_UNSUPPORTED;
   if (need > 0 && (!workspace || off_by(workspace, 256) || workspace_bytes < need))
     return FA_ERR_INVALID_ARG;
   unsigned *status = nullptr;

@@ -295,6 +295,14 @@ def test_attention_workspace(Hq, Hk, max_q, d):
         assert fa.fa_fwd_kv4_workspace(*args) == 0
 
 
+@pytest.mark.parametrize("d", [-128, 1, 16, 32, 63, 80, 96, 192, 256])
+def test_attention_needs_no_workspace_where_it_is_unsupported(d):
+    for Hq, max_q in ((2, 1), (32, 9), (256, 1)):
+        assert fa.fa_fwd_kv4_workspace(3, Hq, 2, max_q, d) == 0
+        if d > 0 and d % 16 == 0:
+            assert attn(Hq=Hq, total=max_q * 3, max_q=max_q, d=d) == fa.FA_ERR_UNSUPPORTED
+
+
 SM = 152
 MAX_KEYS = 2 ** 31 - 4096
 
