@@ -13,7 +13,9 @@ word (bit 32) instead of making the access.
 ``build_binding()`` compiles ``csrc/bind/fa_torch.cpp``, the torch side of the
 serving operators' wrappers, with the host compiler into
 ``exact_attention_57_gb300/_fa_torch.so``; ``build_library()`` does it too,
-beside the kernels.
+beside the kernels.  The C library needs neither torch nor that compiler's
+success: it is linked first, and a compilation of the binding that failed is
+reported after it.
 """
 from __future__ import annotations
 
@@ -22,6 +24,7 @@ import os
 import shutil
 import subprocess
 import sys
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -59,12 +62,15 @@ def _stale(out: str, deps) -> bool:
 
 
 def _start_binding(force: bool):
-    """The binding's running compilation, or None when it is up to date or there
-    is no torch (the C library builds and works without it)."""
+    """The binding's running compilation, or None when it is up to date, there is
+    no torch with CUDA, or no g++ (with a warning: the serving wrappers then raise
+    when they are called)."""
     tag = os.path.join(BUILD, "fa_torch.version")  # headers and ABI are torch's
     try:
         import torch
     except ImportError:
+        return None
+    if torch.version.cuda is None:
         return None
     version = torch.__version__ + "\n" + sys.version
     fresh = os.path.exists(tag) and open(tag).read() == version
@@ -83,7 +89,11 @@ def _start_binding(force: bool):
            *[x for d in dirs for x in ("-isystem", d)], BIND, "-o", tmp,
            "-L", os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
            "-ltorch_cuda", "-ltorch_python"]
-    proc = subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    try:
+        proc = subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    except FileNotFoundError:
+        warnings.warn(f"{BIND} is not built: there is no g++")
+        return None
     return proc, tmp, tag, version
 
 
@@ -123,13 +133,17 @@ def build_library(force: bool = False, verbose: bool = False, debug: bool = Fals
             cmd = [nvcc(), *ARCH, *flags, "-c", src, "-o", obj]
             log = open(obj + ".log", "w")
             procs.append((src, subprocess.Popen(cmd, stdout=log, stderr=subprocess.STDOUT), log))
-    _finish_binding(binding)
     failed = []
     for src, pr, log in procs:
         pr.wait()
         log.close()
         if pr.returncode != 0:
             failed.append(src)
+    binding_error = None
+    try:
+        _finish_binding(binding)
+    except RuntimeError as e:
+        binding_error = e
     with open(os.path.join(build_dir, "ptxas.log"), "w") as out:
         for obj in objs:
             if os.path.exists(obj + ".log"):
@@ -143,6 +157,8 @@ def build_library(force: bool = False, verbose: bool = False, debug: bool = Fals
         cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"]
         subprocess.run(cmd, check=True)
         os.replace(tmp, lib)
+    if binding_error is not None:
+        raise binding_error
     if verbose:
         print(open(os.path.join(build_dir, "ptxas.log")).read())
     return lib
