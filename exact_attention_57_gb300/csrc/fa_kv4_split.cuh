@@ -204,6 +204,12 @@ __global__ void __launch_bounds__(kJoinThreads) fa_kv4_join_kernel(const Kv4Attn
       if (n + x * kWarps > mine.last) break;
 #pragma unroll
       for (int y = 0; y < kJoinRows; ++y) {
+        // A part without weights adds nothing.  Leaving it out keeps both parts'
+        // loads ahead of the sums (94 registers instead of 66), which a join of few
+        // rows wants, whose latency counts (one sequence of 131071 keys 35.5 us
+        // instead of 36.2); the many CTAs of a join of 128 rows want the registers
+        // (428 us for two chunks of 2048 queries, 437 with it).
+        if (R < kKv4ManyRows && ml[x][y].y == 0.f) continue;
         const float to = fmaxf(mm[y], ml[x][y].x), off = to == -INFINITY ? 0.f : to;
         const float f = ex2_approx(mm[y] - off), g = ex2_approx(ml[x][y].x - off);
         mm[y] = to;
