@@ -39,12 +39,12 @@
 // Measured at 8 key heads of 128 elements, four query heads each: 64 sequences of
 // up to 8192 keys (327 MB of cache) 70 us, 4.7 TB/s or 69% of the measured copy
 // rate, the loads alone without a product 65; one of 131071 (151 MB) 35 us; one of
-// 1023 5.0 us, the latencies of one launch.  What bounds it is the time that
-// loads of 64-byte rows take at two tiles in flight a warp, and about 330
-// instructions a tile of 16 tokens.  Not faster: codes through shared memory by
-// bulk copies (75 to 87 us), tiles of 32 tokens (91), a third tile in registers
-// (77 to 80 at 128 elements, spilling; no change at 64), prefetches into L2 two
-// tiles ahead (83).
+// 1023 4.3 us in a captured graph, the latencies of one launch (5.1 to 5.6 a call).
+// What bounds it is the time that loads of 64-byte rows take at two tiles in flight
+// a warp, and about 330 instructions a tile of 16 tokens.  Not faster: codes through
+// shared memory by bulk copies (75 to 87 us), tiles of 32 tokens (91), a third tile
+// in registers (77 to 80 at 128 elements, spilling; no change at 64), prefetches
+// into L2 two tiles ahead (83).
 #include <atomic>
 #include <type_traits>
 
@@ -65,7 +65,8 @@ namespace {
 //            50, three CTAs 50; lead 0/1/2/3/5/8: 92/84/79/78/79/81
 //   16 rows  the registers of two CTAs would spill; lead 3/4/6/8: 121/117/110/111;
 //            D = 64: one CTA 89, two 63, lead 4/6/8: 63/64/65
-//   32 rows  lead 3/4/6/8: 266/258/259/263, two CTAs of 4 warps 246, but 18 instead
+//   32 rows  (all 255 registers and some spilling: 260 bytes stored, 364 loaded)
+//            lead 3/4/6/8: 266/258/259/263, two CTAs of 4 warps 246, but 18 instead
 //            of 15 for one sequence of 4096; D = 64: 8 warps 109, twice 4 101
 template <int NT, int D>
 struct Shape {

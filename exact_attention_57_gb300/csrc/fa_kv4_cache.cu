@@ -21,8 +21,11 @@
 // index computation, 32 bytes a load).  16383 fp16 rows of 8 x 128 elements
 // written and 24575 read back (215 MB) take 37.6 us as two launches, 5.7 TB/s or
 // 85% of the measured copy rate (52 us with one group a thread and 64-bit
-// divisions; 45 with 16-byte accesses, which rows off 32 bytes get).  64 rows
-// written and read back take 3.3 us, two launches.
+// divisions; 45 with 16-byte accesses, which rows off 32 bytes get); fp32 rows 63 us
+// of 57 at the copy rate.  The writing alone takes 16 us from 16-bit rows (5.2 to
+// 5.5 TB/s) and 26 from fp32 ones (5.9 TB/s: their divisions hide behind twice the
+// bytes).  64 rows written and read back take 3.4 us in a captured graph, two
+// launches, and 6 as two calls.
 #include <type_traits>
 
 #include <cuda_bf16.h>

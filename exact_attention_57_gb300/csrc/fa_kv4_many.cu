@@ -27,13 +27,14 @@
 // eight warps of their own hide beside them.
 //
 // Two prompts' chunks of 2048 queries (32 query heads on 8 key heads of 128,
-// causal) take 451 us, 1040 TFLOP/s or 53% of the measured bf16 rate; 1024 queries
-// on 65536 keys 906 us, 1200 TFLOP/s.  Without expanding the codes the first takes
-// 400: what bounds it is the softmax warps and the tensor pipe (46% busy) waiting
-// for each other.  A tile of 256 rows as two halves that take turns took 641 us (64
-// registers fewer a softmax thread), masks applied in registers 475, queries brought
-// by the expanding warps 612, K and V expanded by the same four warps (with those
-// queries) 695.
+// causal) take 428 us, 1100 TFLOP/s or 56% of the measured bf16 rate; 1024 queries
+// on 65536 keys 866 us, 1260 TFLOP/s.  Without expanding the codes the first took
+// 400 (of 451 then): what bounds it is the softmax warps and the tensor pipe (46%
+// busy) waiting for each other, and every query tile of a sequence and key head
+// expands the same codes.  Against 451: a tile of 256 rows as two halves that take
+// turns took 641 us (64 registers fewer a softmax thread), masks applied in registers
+// 475, queries brought by the expanding warps 612, K and V expanded by the same four
+// warps (with those queries) 695.
 //
 // Every wait is bounded; on expiry the CTA raises its abort flag, records the
 // role in the status word, drains its products, frees tensor memory and ends.
@@ -101,7 +102,10 @@ constexpr uint32_t kRegSoftmax = 216, kRegExpand = 104, kRegIssue = 88;
 static_assert(128 * (kRegSoftmax + 2 * kRegExpand + kRegIssue) <= kThreads * 128,
               "the register split must fit in what the block is launched with");
 
-// Sum over i in [0, n) of floor((a i + b) / m), for n, a, b >= 0, m > 0.
+// Sum over i in [0, n) of floor((a i + b) / m), for n, a, b >= 0, m > 0, by the
+// well-known reduction that goes like Euclid's algorithm on (m, a): whole quotients
+// are taken out, and the lattice points below the rest are counted along the other
+// axis.
 __device__ long long floor_sum(long long n, long long m, long long a, long long b) {
   long long s = 0;
   for (;;) {
@@ -676,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     cta_of(end - 1, *s_total, *s_den)};
         }
         const bool whole = begins && ends;
-        // 32 bytes a store, as rows lie far apart: 16 took 454 us instead of 451 for
+        // 32 bytes a store, as rows lie far apart: 16 took 454 us instead of then 451 for
         // the two chunks above, 525 instead of 516 for 8 prompts of 2048
         const bool wide = reinterpret_cast<uintptr_t>(p.o) % 32 == 0;
         const float inv = p.v_mul / l;

@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kJoinThreads) fa_kv4_join_kernel(const Kv4Attn
 #pragma unroll
       for (int y = 0; y < kJoinRows; ++y) {
         // A part without weights adds nothing.  Leaving it out keeps both parts'
-        // loads ahead of the sums (94 registers instead of 66), which a join of few
+        // loads ahead of the sums (89 registers instead of 66), which a join of few
         // rows wants, whose latency counts (one sequence of 131071 keys 35.5 us
         // instead of 36.2); the many CTAs of a join of 128 rows want the registers
         // (428 us for two chunks of 2048 queries, 437 with it).

@@ -18,9 +18,10 @@
 // the first token of a new block writes its entry; those of blocks whose tokens
 // lie behind the capacity are CTA 0's.
 //
-// Latency bounds it: 256 requests of one token 2.5 us, a launch; 37 prompts with
-// 148000 tokens (1.8 MB written) 4.7 us, which are the requests' loads, the scan,
-// the bisection and the table's loads one after the other.
+// Latency bounds it: in a captured graph 256 requests of one token take 2.3 us, a
+// launch (a call 3.2, the host's), and 37 prompts with 148000 tokens (1.8 MB
+// written) 3.9 us (a call 4.1 to 4.7), which are the requests' loads, the scan, the
+// bisection and the table's loads one after the other.
 #include "fa_serve.h"
 #include "ptx.cuh"
 
@@ -178,9 +179,10 @@ cudaError_t launch_plan(const PlanParams &p, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  // One request a thread where a round then holds them all, four otherwise (2000
-  // requests of 500 tokens 16 us instead of 22, 30000 of 2 42 instead of 93; 37 of
-  // 4000 5.4 instead of 3.9).
+  // One request a thread where a round then holds them all, four otherwise.  In a
+  // captured graph, one and four: 37 requests of 4000 tokens 3.9 and 4.5 us, 256 of
+  // one 2.1 and 2.6; 257 of one 3.4 and 3.0, 1000 6.0 and 4.4, 2000 of 500 22 and 16,
+  // 30000 of 2 93 and 41.
   return p.B <= kThreads ? cudaLaunchKernelEx(&cfg, fa_plan_kernel<1>, p)
                          : cudaLaunchKernelEx(&cfg, fa_plan_kernel<4>, p);
 }

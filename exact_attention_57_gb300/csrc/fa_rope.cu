@@ -13,10 +13,13 @@
 // [-1, 1) half turns, go to sincospif.
 //
 // Memory bounds it: 18432 tokens of 32 bf16 heads of 128 elements (302 MB in and
-// out) take 50 us, 6.0 TB/s or 89% of the measured copy rate; 64 tokens take the
-// 2.5 us of a launch.  A thread issues one head's loads ahead of its stores; four
-// heads' together (111 registers, so half the warps) took 75 us, one head ahead
-// 53 to 64, streaming cache hints changed nothing.
+// out) take 50 us, 6.0 TB/s or 89% of the measured copy rate; 64 tokens take 2.5 us
+// in a captured graph, a launch, and 5.3 to 6 as a call, the host's.  Rows whose
+// half of d_rot is no multiple of 4 go an element at a time: 18432 tokens of 32 heads
+// of 72 elements with 36 turned take 104 us in bf16 where all 72 take 34, in fp32 106
+// and 53.  A thread issues one head's loads ahead of its stores; four heads' together
+// (111 registers, so half the warps) took 75 us, one head ahead 53 to 64, streaming
+// cache hints changed nothing.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -1,7 +1,7 @@
 // fa_serve_api.cu — host side of the serving operators declared in
 // include/fa.h: argument checks, device checks and dispatch.  Nothing here
-// computes; the kernels are in fa_plan.cu, fa_rope.cu, fa_kv4_cache.cu and
-// fa_kv4_attn.cu.
+// computes; the kernels are in fa_plan.cu, fa_rope.cu, fa_kv4_cache.cu,
+// fa_kv4_attn.cu and fa_kv4_many.cu.
 #include <cmath>
 #include <cstdint>
 #include <utility>

@@ -488,8 +488,9 @@ def fa_fwd_kv4_schedule(B, Hq, Hk, max_seqlen_q, max_seqlen_k, max_blocks, block
 
 # The wrappers below run once or more in every layer of every step of a server,
 # where a launch takes about 3 us of host time.  Their checks, allocations and
-# calls of the C entry points are compiled (csrc/bind/fa_torch.cpp): 2 to 5 us a
-# call, where the same in Python took 8 to 20.  `stream` is the integer of a
+# calls of the C entry points are compiled (csrc/bind/fa_torch.cpp): 2.5 to 6.5 us a
+# call, 10 where the attention launches two kernels and their joins, where the same
+# in Python took 8 to 20.  `stream` is the integer of a
 # cudaStream_t (default: the current one); what it has to wait for, the inputs
 # among it, is the caller's to order, and what a wrapper allocates belongs to it.
 _torch = None

@@ -372,8 +372,10 @@ FA_API unsigned long long fa_bwd_varlen_workspace(int B, int H, int total_q, int
  * counts       int32 [2], out: blocks needed, tokens.  More blocks needed than
  *              num_free minus free_head holds: the blocks missing are -1 in
  *              the table and their tokens' slots -1.  More tokens than
- *              capacity: those behind it are not written.  A token past
- *              max_blocks * block_size gets slot -1 and no block.
+ *              capacity: those behind it are not written, while block_table and
+ *              seq_lens are those of all tokens, so such a step is to be planned
+ *              again and not run.  A token past max_blocks * block_size gets slot
+ *              -1 and no block.
  * B 1 .. 65535; max_blocks * block_size <= 2^31 - 1.
  * The call keeps nothing: the same inputs give the same outputs again.
  */
@@ -412,7 +414,8 @@ FA_API int fa_rope_table(const double *inv_freq, const int *axis, int n,
  *               stride d, row stride H*d, and a slice of a fused projection
  *               has that projection's row stride.
  * positions     int32 [num_axes, B, N], any int32.
- * table         uint64 [d_rot/2] from fa_rope_table, on the device.
+ * table         uint64 [d_rot/2] from fa_rope_table, on the device.  A pair whose
+ *               axis is num_axes or more turns by the last axis.
  * d_rot         even, 2 .. d: the first d_rot elements of a row turn, the
  *               others are copied.  interleaved = 0: pair i is elements
  *               (i, i + d_rot/2); 1: (2i, 2i+1).
@@ -446,11 +449,12 @@ FA_API int fa_kv4_append(const void *k, const void *v, long long k_stride, long 
                   int v_exp, int dtype, void *stream);
 
 /*
- * fa_kv4_gather — R rows of the 4-bit cache as bf16, fp16 or fp32 (the input
- * of fa_fwd or fa_fwd_varlen on a cached prefix).  slots int64 [R]; a slot
- * outside the cache reads zeros.  k_out, v_out [R, Hk, d], contiguous, 16-byte
- * aligned.  The values are exact in every type unless an exponent moves them
- * out of its range.
+ * fa_kv4_gather — R rows of the 4-bit cache as bf16, fp16 or fp32.  slots
+ * int64 [R]; a slot outside the cache reads zeros.  k_out, v_out [R, Hk, d],
+ * contiguous, 16-byte aligned: token-major, the layout of fa_fwd_varlen's keys,
+ * which takes them where Hq = Hk and, as its causal mask is aligned at the top,
+ * without that mask or for whole sequences.  The values are exact in every type
+ * unless an exponent moves them out of its range.
  */
 FA_API int fa_kv4_gather(const long long *slots, int R, const void *k_codes, const void *k_scales,
                   const void *v_codes, const void *v_scales, void *k_out, void *v_out,
@@ -470,11 +474,14 @@ FA_API int fa_kv4_gather(const long long *slots, int R, const void *k_codes, con
  *               among them.  block_table int32 [B, max_blocks]: the blocks of
  *               sequence b in order.  A table entry outside [0, num_blocks)
  *               takes its tokens out of the softmax.
- * max_seqlen_q, max_seqlen_k  bounds on the lengths; longer sequences are cut
- *               to them.  max_blocks * block_size and 2^31 - 4096 bound the keys
- *               too.  The least of the three bounds the grid, and up to a few
- *               thousand keys it is what says that a small batch needs one launch
- *               instead of two (fa_fwd_kv4_schedule shows the choice).
+ * max_seqlen_q, max_seqlen_k  bounds on the lengths (1 .. total_q, and from 0);
+ *               longer sequences are cut to them.  max_blocks * block_size and
+ *               2^31 - 4096 bound the keys too.  The least of the three bounds the
+ *               grid.  Up to a few thousand keys it is also what says that a small
+ *               batch needs one launch instead of two, and with 17 to 32 rows
+ *               (queries times Hq/Hk) of 128 elements it chooses the kernel, so a
+ *               tight bound is worth having (fa_fwd_kv4_schedule shows the
+ *               choice).
  * causal        1: query i of n_q sees key j iff j <= n_k - n_q + i (aligned
  *               at the end, as the new tokens are the last cached ones); 0:
  *               all keys.  A row that sees no key gets O = 0, LSE = -inf; one with
@@ -487,9 +494,15 @@ FA_API int fa_kv4_gather(const long long *slots, int R, const void *k_codes, con
  * workspace     fa_fwd_kv4_workspace(...) bytes, 256-byte aligned, whatever
  *               they hold.  Calls that share it must not overlap on the GPU.
  * The lengths, offsets and tables are read on the device and not checked on
- * the host; whatever they hold, no access leaves the buffers.  Sequences of
- * more than 32 rows (queries times Hq/Hk) run a kernel whose waits are bounded:
- * one that runs out is reported through fa_fwd_status.
+ * the host; whatever they hold, no access leaves the buffers.  A NaN in the
+ * scale of a value reaches every query of its sequence, also those from which
+ * the causal mask hides it (fa_kv4_append stores none).
+ * Two kernels share the work.  One takes the sequences of up to 8, 16 or 32 rows
+ * (queries times Hq/Hk): the least of these that holds max_seqlen_q queries, or,
+ * where none does, one query; it takes none where one query has more than 32
+ * rows, and none where that is 32 rows of 128 elements and B * Hk times the bound
+ * on the keys reaches a million.  The other takes the longer ones.  Its waits are
+ * bounded: one that runs out is reported through fa_fwd_status.
  */
 FA_API int fa_fwd_kv4(const void *q, void *o, float *lse, const void *k_codes, const void *k_scales,
                const void *v_codes, const void *v_scales, const int *block_table,
