@@ -344,7 +344,8 @@ extern "C" int fa_fwd_kv4_schedule(int B, int Hq, int Hk, int max_seqlen_q, int 
   if (!max_keys || !tile_rows || !cluster || !ctas || !many_ctas) return FA_ERR_INVALID_ARG;
   const int lg = block_log2(block_size);
   if (B < 1 || B > 65535 || Hq < 1 || Hq > 65535 || Hk < 1 || Hq % Hk != 0 || max_seqlen_q < 1 ||
-      max_seqlen_k < 0 || max_blocks < 1 || lg < 0 || d < 1 || num_sms < 1)
+      max_seqlen_k < 0 || max_blocks < 1 || lg < 0 || d < 1 || num_sms < 1 ||
+      num_sms > 65535)
     return FA_ERR_INVALID_ARG;
   if ((static_cast<long long>(max_blocks) << lg) > 2147483647LL) return FA_ERR_INVALID_ARG;
   if (!kv4_attends(d, Hq / Hk)) return FA_ERR_UNSUPPORTED;

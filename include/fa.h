@@ -363,9 +363,9 @@ FA_API unsigned long long fa_bwd_varlen_workspace(int B, int H, int total_q, int
  *              ceil(cached/block_size) entries of a row are read, the entries
  *              for its new blocks written, the others left alone.
  * slots        int64 [capacity] and positions int32 [capacity], out: slot and
- *              position (cached + index) of every new token; entries behind
- *              the last token get slot -1 and position 0, so that a padded
- *              batch can pass them on.
+ *              position (cached + index, 2^31 - 1 at most) of every new token;
+ *              entries behind the last token get slot -1 and position 0, so that a
+ *              padded batch can pass them on.
  * cu_seqlens   int32 [B+1], out: offsets of the requests' new tokens (the
  *              cu_seqlens_q of fa_fwd_kv4), at most capacity each.
  * seq_lens     int32 [B], out: cached + new, at most max_blocks * block_size.
@@ -517,7 +517,7 @@ FA_API unsigned long long fa_fwd_kv4_workspace(int B, int Hq, int Hk, int max_se
 
 /*
  * fa_fwd_kv4_schedule — what fa_fwd_kv4 launches for these sizes on a GPU with
- * num_sms SMs; a host-only function, for reports and tests.
+ * num_sms SMs (1 .. 65535); a host-only function, for reports and tests.
  *   *max_keys   the bound on a sequence's keys (see max_seqlen_k above).
  *   *tile_rows  rows (queries times Hq/Hk) of a sequence and key head that the
  *               kernel for few rows holds: 8, 16 or 32; 0: it is not launched.

@@ -349,7 +349,8 @@ def test_attention_grid_for_any_bound(bound, Hq, Hk, max_q, d):
 @pytest.mark.parametrize("kw,want", [
     (dict(), fa.FA_OK), (dict(B=0), 1), (dict(B=65536), 1), (dict(Hq=0), 1), (dict(Hq=9), 1),
     (dict(Hk=0), 1), (dict(max_q=0), 1), (dict(max_k=-1), 1), (dict(width=0), 1),
-    (dict(width=2 ** 27), 1), (dict(bs=8), 1), (dict(sms=0), 1), (dict(d=0), 1),
+    (dict(width=2 ** 27), 1), (dict(bs=8), 1), (dict(sms=0), 1), (dict(sms=65536), 1),
+    (dict(sms=2 ** 31 - 1), 1), (dict(d=0), 1),
     (dict(d=32), fa.FA_ERR_UNSUPPORTED), (dict(Hq=516), fa.FA_ERR_UNSUPPORTED)], ids=str)
 def test_attention_schedule_refusals(kw, want):
     a = dict(dict(B=3, Hq=8, Hk=4, max_q=2, max_k=500, width=40, bs=16, d=128, sms=SM), **kw)

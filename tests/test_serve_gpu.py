@@ -816,6 +816,65 @@ def test_two_streams_at_once():
             assert torch.equal(o, wo) and torch.equal(l, wl)
 
 
+def test_two_graphs_at_once():
+    """Two captured calls, whose workspaces the wrapper allocated in the captures,
+    replayed on two streams: the results of one alone.  One joins the shares of a
+    line of units, the other the tiles of many queries."""
+    cases = [((20000, 900), (1, 2)), ((5000, 300), (200, 130))]
+    graphs, streams = [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for n, (lens, nqs) in enumerate(cases):
+        q, cache, table, cu = small(46 + n, lens, nqs, bs=64)
+        args = (q.to(DEV), *(c.to(DEV) for c in cache), ints(table), ints(list(lens)), max(lens))
+        kw = dict(cu_seqlens_q=ints(cu), max_seqlen_q=max(nqs))
+        want = fa.attention_kv4(*args, **kw)
+        torch.cuda.synchronize()
+        cg = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(cg, stream=streams[n]):
+            got = fa.attention_kv4(*args, **kw)
+        graphs.append((cg, got, want, args, kw))
+    for _ in range(10):
+        for cg, got, *_ in graphs:
+            got[0].fill_(9.0), got[1].fill_(9.0)
+        torch.cuda.synchronize()
+        for (cg, *_), st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                cg.replay()
+        torch.cuda.synchronize()
+        for _, got, want, *_ in graphs:
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_calls_from_several_threads():
+    """The wrappers let go of the interpreter's lock: threads with a stream each get
+    what one thread gets."""
+    import threading
+    work = []
+    for n, (lens, nqs) in enumerate((((3000, 70), (1, 1)), ((900, 5), (60, 4)), ((64, 64), (1, 1)))):
+        q, cache, table, cu = small(48 + n, lens, nqs)
+        args = (q.to(DEV), *(c.to(DEV) for c in cache), ints(table), ints(list(lens)), max(lens))
+        kw = dict(cu_seqlens_q=ints(cu), max_seqlen_q=max(nqs))
+        work.append((args, kw, fa.attention_kv4(*args, **kw)))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def run(args, kw, want):
+        st = torch.cuda.Stream()
+        with torch.cuda.stream(st):
+            for _ in range(50):
+                got = fa.attention_kv4(*args, **kw)
+                st.synchronize()
+                if not (torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])):
+                    wrong.append(args)
+
+    threads = [threading.Thread(target=run, args=w) for w in work * 2]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+    assert fa.fa_fwd_status(torch.cuda.current_stream().cuda_stream) == (fa.FA_OK, 0)
+
+
 def test_a_stream_of_its_own():
     """Calls on a stream that is not the current one: what the wrappers
     allocate belongs to that stream."""
