@@ -1,0 +1,566 @@
+"""Measured cases of the 8-bit cache and of the pages of a cache.
+
+Five operators of a server over a paged cache:
+
+  cache8   new keys and values written into a cache held in 8 bits, with a scale
+           for each block of tokens and head, and rows of it read back
+  attn8    attention of the new queries over that cache
+  copy     pages of a cache copied
+  beam     requests forked (full blocks shared, the last one copied) and the
+           blocks that no request holds any more collected
+  compact  pages moved to the front of the cache, tables renumbered
+
+`own` selects what `run` executes: False, the plain form in elementary torch
+operations; True, the calls of exact_attention_57_gb300.fa.
+
+Cache format: a block holds `bs` tokens; codes e4m3 [blocks, Hk, bs, d], scales
+float32 [blocks, Hk]; an element is code * scale.
+"""
+import math
+
+import torch
+
+own = False
+
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+F8 = torch.float8_e4m3fn
+
+
+# ------------------------------------------------------------------ cases
+def listed():
+    return [
+        # a decode step: one token more for each of 64 requests, into blocks begun before
+        dict(name="cache8 decode b64", op="cache8", B=64, cached=2001, new=1, Hk=8, d=128, bs=16,
+             dtype="bf16"),
+        # four ragged prompts written behind cached prefixes, read back for a whole-prompt pass
+        dict(name="cache8 prefill b4 t8192", op="cache8", B=4, cached=1023, new=8192, Hk=8, d=128,
+             bs=64, dtype="fp16"),
+        # one user, a short context: latency
+        dict(name="attn8 decode b1 k1023", op="attn8", B=1, nq=1, k_max=1023, Hq=32, Hk=8, d=128,
+             bs=16, dtype="bf16"),
+        # a batch of users with ragged contexts: a server's usual step
+        dict(name="attn8 decode b64 k8192", op="attn8", B=64, nq=1, k_max=8192, Hq=32, Hk=8, d=128,
+             bs=16, dtype="bf16"),
+        # a few drafted tokens checked at once, one key head a query head
+        dict(name="attn8 draft b16 k3001", op="attn8", B=16, nq=4, k_max=3001, Hq=16, Hk=16, d=64,
+             bs=32, dtype="fp16"),
+        # a chunk of a prompt against what is cached
+        dict(name="attn8 chunk b2 q2048", op="attn8", B=2, nq=2048, k_max=8192, Hq=32, Hk=8, d=128,
+             bs=64, dtype="bf16"),
+        # a few pages of a small model's cache, rows of scales shorter than 16 bytes
+        dict(name="copy n9 bs16", op="copy", n=9, blocks=64, Hk=2, d=64, bs=16, kind="kv8"),
+        # a prefix of 60000 tokens taken over into another request's pages
+        dict(name="copy n938 bs64", op="copy", n=938, blocks=2048, Hk=8, d=128, bs=64, kind="kv4"),
+        # one step of a beam search of eight beams
+        dict(name="beam b8 k1023", op="beam", B=8, n=8, k_max=1023, Hk=8, d=128, bs=16, spare=64,
+             end=True, kind="kv8"),
+        # four answers sampled from each of 64 prompts, which stay
+        dict(name="beam b64 n256 k8192", op="beam", B=64, n=256, k_max=8192, Hk=8, d=128, bs=64,
+             spare=512, end=False, kind="kv8"),
+        # a small cache with a few requests left
+        dict(name="compact b5 k501", op="compact", B=5, k_max=501, Hk=4, d=64, bs=16, spare=200,
+             kind="kv4"),
+        # half of a large cache given back
+        dict(name="compact b32 k8192", op="compact", B=32, k_max=8192, Hk=8, d=128, bs=64,
+             spare=2100, kind="kv8"),
+    ]
+
+
+def _log(rng, lo, hi):
+    return min(hi, max(lo, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi + 0.49)))))))
+
+
+def draw(rng):
+    op = rng.choice(["cache8", "cache8", "attn8", "attn8", "attn8", "copy", "beam", "compact"])
+    if op == "cache8":
+        d, Hk = rng.choice([16, 64, 80, 128, 256]), rng.choice([1, 2, 3, 4, 8])
+        bs = rng.choice([16, 32, 64, 128])
+        dtype = rng.choice(["bf16", "fp16", "fp32"])
+        B = _log(rng, 1, 256)
+        new = rng.choice([1, 1, _log(rng, 2, 8192)])
+        while sum(_lens(B, new, 1)) * Hk * d * (2 if dtype == "fp32" else 1) > 17000 * 8 * 128:
+            B, new = (B // 2, new) if B > 1 else (1, new // 2)
+        return dict(op="cache8", B=B, cached=_log(rng, 1, 2001), new=new, Hk=Hk, d=d, bs=bs,
+                    dtype=dtype)
+    if op == "attn8":
+        d, Hk = rng.choice([64, 128]), rng.choice([1, 2, 3, 4, 8])
+        g = rng.choice([1, 2, 4, 5, 8, 16])
+        bs, dtype = rng.choice([16, 32, 64, 128]), rng.choice(["bf16", "fp16"])
+        kind = rng.choice(["decode", "decode", "draft", "chunk"])
+        if kind == "decode":
+            nq, B, k_max = 1, _log(rng, 1, 128), _log(rng, 1, 65536)
+        elif kind == "draft":
+            nq, B, k_max = rng.randrange(2, 9), _log(rng, 1, 64), _log(rng, 16, 16384)
+        else:
+            nq, B = _log(rng, 9, 2048), rng.choice([1, 2, 3])
+            k_max = max(nq, _log(rng, 64, 8192))
+        # no larger than the listed ones: tokens * heads of the cache, and scores
+        while B * k_max * Hk * d > 64 * 8192 * 8 * 128 or B * nq * Hk * g * k_max > 2 ** 30:
+            B, k_max = (B // 2, k_max) if B > 1 else (1, k_max // 2)
+            nq = min(nq, k_max)
+        return dict(op="attn8", B=B, nq=nq, k_max=k_max, Hq=Hk * g, Hk=Hk, d=d, bs=bs, dtype=dtype)
+    Hk, d = rng.choice([1, 2, 3, 4, 8]), rng.choice([64, 128])
+    bs, kind = rng.choice([16, 32, 64, 128]), rng.choice(["kv4", "kv8"])
+    page = 2 * Hk * bs * d  # bytes of a page in 8 bits, the more
+    if op == "copy":
+        n = _log(rng, 1, min(8192, (128 << 20) // page))
+        return dict(op="copy", n=n, blocks=2 * n + rng.randrange(0, 99), Hk=Hk, d=d, bs=bs,
+                    kind=kind)
+    if op == "beam":
+        B = _log(rng, 1, 64)
+        n = _log(rng, 1, min(256, max(8, (32 << 20) // page)))
+        k_max = _log(rng, 1, max(bs, min(8192, (512 << 20) // page * bs // B)))
+        return dict(op="beam", B=B, n=n, k_max=k_max, Hk=Hk, d=d, bs=bs,
+                    spare=n + rng.randrange(1, 200), end=rng.random() < 0.5, kind=kind)
+    B = _log(rng, 1, 64)
+    k_max = _log(rng, 1, max(bs, min(8192, (256 << 20) // page * bs // B)))
+    return dict(op="compact", B=B, k_max=k_max, Hk=Hk, d=d, bs=bs,
+                spare=_log(rng, 1, min(2100, max(64, (256 << 20) // page))), kind=kind)
+
+
+# ------------------------------------------------------------------ inputs
+def _lens(n, top, low=0):
+    """n ragged lengths in low .. top, the longest first: the same for every
+    seed, so that a case's work is known; prepare() puts them in an order."""
+    return [top] + [low + (top - low) * ((i * 7919 + 13) % 997) // 996 for i in range(1, n)]
+
+
+def _gen(seed):
+    return torch.Generator("cuda").manual_seed(seed)
+
+
+def _shuffled(values, g):
+    t = torch.tensor(values, dtype=torch.int64, device="cuda")
+    return t[torch.randperm(len(values), device="cuda", generator=g)]
+
+
+def _k_lens(case):
+    return _lens(case["B"], case["k_max"], case["nq"]) if case["B"] > 1 else [case["k_max"]]
+
+
+def _held(case):
+    """Lengths of the requests of a case about pages."""
+    return _lens(case["B"], case["k_max"], 1)
+
+
+def _random_cache8(blocks, Hk, bs, d, g):
+    """Codes and scales of normal numbers whose size differs by block and channel."""
+    codes = torch.empty(blocks, Hk, bs, d, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(blocks, Hk, device="cuda")
+    step = max(1, (1 << 26) // (Hk * bs * d))
+    for b in range(0, blocks, step):
+        n = min(step, blocks - b)
+        x = torch.randn(n, Hk, bs, d, device="cuda", generator=g)
+        x[..., ::16] *= 2.0  # a few large channels
+        x *= 0.5 + torch.rand(n, Hk, 1, 1, device="cuda", generator=g)
+        scales[b:b + n] = _scale_of(x.abs().amax((2, 3)))
+        codes[b:b + n] = (x / scales[b:b + n, :, None, None]).to(F8).view(torch.uint8)
+    return [codes.view(F8), scales]
+
+
+def _random_pages(case, blocks, g):
+    """The arrays of a cache: pages of codes and of scales, any bytes."""
+    Hk, bs, d = case["Hk"], case["bs"], case["d"]
+
+    def byte(*shape):
+        return torch.randint(0, 256, shape, dtype=torch.uint8, device="cuda", generator=g)
+
+    if case["kind"] == "kv4":
+        return [byte(blocks, Hk, bs, n) for n in (d // 2, d // 16, d // 2, d // 16)]
+    return [x for _ in "kv" for x in (byte(blocks, Hk, bs, d).view(F8),
+                                      torch.rand(blocks, Hk, device="cuda", generator=g))]
+
+
+def _random_table(lens, bs, width, ids):
+    """A block table over the first of `ids`, and how many it takes."""
+    need = (lens + bs - 1) // bs
+    table = torch.full((lens.numel(), width), -1, dtype=torch.int32, device="cuda")
+    inside = torch.arange(width, device="cuda")[None] < need[:, None]
+    total = int(need.sum())
+    table[inside] = ids[:total].int()
+    return table, total
+
+
+def _prepare_cache8(case, g):
+    B, Hk, d, bs = (case[k] for k in ("B", "Hk", "d", "bs"))
+    cached = _shuffled(_lens(B, case["cached"]), g)
+    new = _shuffled(_lens(B, case["new"], 1), g)
+    total = cached + new
+    need = (total + bs - 1) // bs
+    blocks = int(need.sum()) + 8
+    ids = torch.randperm(blocks, device="cuda", generator=g)
+    table, _ = _random_table(total, bs, int(need.max()), ids)
+    # new tokens, sequence after sequence; rows read: from the block that holds the first
+    # new one on (its older tokens were stored at another scale)
+    start = cached // bs * bs
+    write, read = [], []
+    for b, (lo, mid, hi) in enumerate(zip(start.tolist(), cached.tolist(), total.tolist())):
+        t = torch.arange(lo, hi, device="cuda")
+        slots = table[b, t // bs].long() * bs + t % bs
+        write.append(slots[mid - lo:])
+        read.append(slots)
+    write, read = torch.cat(write), torch.cat(read)
+    T, R, dt = write.numel(), read.numel(), DT[case["dtype"]]
+    qkv = torch.randn(T, 4 * Hk, d, device="cuda", generator=g)
+    qkv[:, :, ::16] *= 2.0
+    qkv = (qkv * (0.5 + torch.rand(T, 1, 1, device="cuda", generator=g))).to(dt)
+    cache = _random_cache8(blocks, Hk, bs, d, g) + _random_cache8(blocks, Hk, bs, d, g)
+    out = tuple(torch.empty(R, Hk, d, dtype=dt, device="cuda") for _ in range(2))
+    return dict(k=qkv[:, 2 * Hk:3 * Hk], v=qkv[:, 3 * Hk:], write=write, read=read, cache=cache,
+                out=out)
+
+
+def _prepare_attn8(case, g):
+    B, nq, Hq, Hk, d, bs = (case[k] for k in ("B", "nq", "Hq", "Hk", "d", "bs"))
+    lens = _shuffled(_k_lens(case), g)
+    blocks = int(((lens + bs - 1) // bs).sum()) + 8
+    cache = _random_cache8(blocks, Hk, bs, d, g) + _random_cache8(blocks, Hk, bs, d, g)
+    table, _ = _random_table(lens, bs, -(-case["k_max"] // bs),
+                             torch.randperm(blocks, device="cuda", generator=g))
+    q = torch.randn(B * nq, Hq, d, device="cuda", generator=g).to(DT[case["dtype"]])
+    cu = torch.arange(0, (B + 1) * nq, nq, dtype=torch.int32, device="cuda")
+    return dict(q=q, cu=cu, lens=lens.int(), table=table, cache=cache, out=torch.empty_like(q),
+                lse=torch.empty(Hq, B * nq, device="cuda"))
+
+
+def _prepare_copy(case, g):
+    ids = torch.randperm(case["blocks"], device="cuda", generator=g).int()
+    n = case["n"]
+    return dict(src=ids[:n].contiguous(), dst=ids[n:2 * n].contiguous(),
+                cache=_random_pages(case, case["blocks"], g))
+
+
+def _prepare_beam(case, g):
+    B, n, bs = case["B"], case["n"], case["bs"]
+    lens = _shuffled(_held(case), g)
+    blocks = sum(-(-x // bs) for x in _held(case)) + case["spare"]
+    ids = torch.randperm(blocks, device="cuda", generator=g)
+    width = -(-case["k_max"] // bs)
+    table, used = _random_table(lens, bs, width, ids)
+    if case["end"]:  # the best beams go on more than once, others not at all
+        parents = torch.randint(0, B, (n,), device="cuda", generator=g).int()
+    else:
+        parents = (torch.arange(n, device="cuda") * B // n).int()
+    out = (torch.empty(n, width, dtype=torch.int32, device="cuda"),
+           torch.empty(n, dtype=torch.int32, device="cuda"),
+           torch.empty(2, dtype=torch.int32, device="cuda"))
+    # a few of the children are at their end already
+    ended = torch.rand(n, device="cuda", generator=g) < 0.1
+    free = (torch.empty(blocks, dtype=torch.int32, device="cuda"),
+            torch.empty(1, dtype=torch.int32, device="cuda"))
+    return dict(table=table, lens=lens.int(), parents=parents, ended=ended, blocks=blocks,
+                free=ids[used:].int().contiguous(), cache=_random_pages(case, blocks, g), out=out,
+                free_out=free)
+
+
+def _prepare_compact(case, g):
+    B, bs = case["B"], case["bs"]
+    lens = _shuffled(_held(case), g)
+    blocks = sum(-(-x // bs) for x in _held(case)) + case["spare"]
+    table, _ = _random_table(lens, bs, -(-case["k_max"] // bs),
+                             torch.randperm(blocks, device="cuda", generator=g))
+    out = (torch.empty_like(table), torch.empty(blocks, dtype=torch.int32, device="cuda"),
+           torch.empty(2, dtype=torch.int32, device="cuda"))
+    return dict(table=table, lens=lens.int(), blocks=blocks, cache=_random_pages(case, blocks, g),
+                out=out)
+
+
+def prepare(case, seed):
+    g = _gen(seed)
+    state = {"cache8": _prepare_cache8, "attn8": _prepare_attn8, "copy": _prepare_copy,
+             "beam": _prepare_beam, "compact": _prepare_compact}[case["op"]](case, g)
+    return dict(case, **state)
+
+
+# ------------------------------------------------------------- plain forms
+def _scale_of(amax):
+    """2^e, e the least integer in -40 .. 40 with amax <= 448 * 2^e."""
+    m, x = torch.frexp(amax)
+    e = torch.where(amax > 0, x - 9 + (m > 0.875), -40).clamp(-40, 40)
+    return torch.ldexp(torch.ones_like(amax), e)
+
+
+def _plain_cache8(s):
+    bs, Hk = s["bs"], s["Hk"]
+    w, r = s["write"], s["read"]
+    h = torch.arange(Hk, device=w.device)[None]
+    block, off = w // bs, w % bs
+    got = {}
+    for name, x, codes, scales in (("k", s["k"], s["cache"][0], s["cache"][1]),
+                                   ("v", s["v"], s["cache"][2], s["cache"][3])):
+        codes = codes.view(torch.uint8)
+        x = x.float()
+        amax = torch.zeros_like(scales)
+        amax.scatter_reduce_(0, block[:, None].expand(-1, Hk), x.abs().amax(-1), "amax")
+        first = torch.full((scales.shape[0],), bs, dtype=torch.int64, device=w.device)
+        first.scatter_reduce_(0, block, off, "amin")  # the first token that is written
+        touched = torch.unique(block)
+        old = scales[touched]
+        fit = _scale_of(amax[touched])
+        new = torch.where((first[touched] == 0)[:, None], fit, torch.maximum(old, fit))
+        c = codes[touched]  # the tokens before it, at the new scale
+        y = (c.view(F8).float() * (old / new)[:, :, None, None]).to(F8).view(torch.uint8)
+        keep = torch.arange(bs, device=w.device)[None] < first[touched][:, None]
+        codes[touched] = torch.where(keep[:, None, :, None], y, c)
+        scales[touched] = new
+        codes[block[:, None], h, off[:, None]] = \
+            (x / scales[block][..., None]).to(F8).view(torch.uint8)
+        at = (r // bs)[:, None], h, (r % bs)[:, None]
+        got[name] = (codes[at].view(F8).float() * scales[r // bs][..., None]).to(s["k"].dtype)
+        got[name + "_scales"] = scales
+    return got
+
+
+def _plain_attn8(s):
+    B, nq, Hq, Hk, d, bs = (s[k] for k in ("B", "nq", "Hq", "Hk", "d", "bs"))
+    kc, ks, vc, vs = s["cache"]
+    page = s["table"].clamp(min=0).long()
+
+    def rows(codes, scales):  # [B, Hk, tokens, d]
+        x = codes.view(torch.uint8)[page].view(F8).float() * scales[page][..., None, None]
+        return x.transpose(1, 2).flatten(2, 3)[:, :, :s["k_max"]]
+
+    K, V = rows(kc, ks), rows(vc, vs)
+    q = s["q"].float().view(B, nq, Hk, Hq // Hk, d).permute(0, 2, 3, 1, 4).flatten(2, 3)
+    S = (q @ K.transpose(-1, -2)) * d ** -0.5  # [B, Hk, g * nq, tokens]
+    S = S.unflatten(2, (Hq // Hk, nq))
+    lens = s["lens"].long()
+    last = lens[:, None] - nq + torch.arange(nq, device=q.device)  # a query sees keys <= last
+    j = torch.arange(S.shape[-1], device=q.device)
+    seen = (j <= last[..., None]) & (j < lens[:, None, None])
+    S = S.masked_fill(~seen[:, None, None], -math.inf)
+    m = S.amax(-1, keepdim=True)
+    m = torch.where(m == -math.inf, 0.0, m)
+    P = (S - m).exp()
+    l = P.sum(-1, keepdim=True)
+    O = (P.flatten(2, 3) @ V).unflatten(2, (Hq // Hk, nq))
+    O = torch.where(l > 0, O / l, 0.0)
+    lse = (l.log() + m).squeeze(-1)
+    return dict(o=O.permute(0, 3, 1, 2, 4).reshape(B * nq, Hq, d).to(s["q"].dtype),
+                lse=lse.permute(1, 2, 0, 3).reshape(Hq, B * nq))
+
+
+def _bytes(cache):
+    return [x.view(torch.uint8) for x in cache]
+
+
+def _plain_copy(s):
+    src, dst = s["src"].long(), s["dst"].long()
+    for x in _bytes(s["cache"]):
+        x[dst] = x[src]
+    return dict(cache=_bytes(s["cache"]))
+
+
+def _plain_free(table, lens, blocks, bs):
+    """(list of the ids that no row holds, at the end of an array; where it begins)."""
+    need = (lens.long() + bs - 1) // bs
+    inside = torch.arange(table.shape[1], device=table.device)[None] < need[:, None]
+    held = torch.zeros(blocks + 1, dtype=torch.bool, device=table.device)
+    held[torch.where(inside & (table >= 0), table, blocks).flatten().long()] = True
+    free = torch.nonzero(~held[:blocks]).flatten()
+    out = torch.full((blocks,), -1, dtype=torch.int32, device=table.device)
+    out[blocks - free.numel():] = free.int()
+    return out, torch.tensor([blocks - free.numel()], dtype=torch.int32, device=table.device)
+
+
+def _plain_beam(s):
+    bs, n = s["bs"], s["n"]
+    parents = s["parents"].long()
+    lens = s["lens"][parents]
+    full, part = lens.long() // bs, lens % bs > 0
+    if s["end"]:  # a parent's first child takes its last block over
+        same = parents[:, None] == parents[None]
+        part = part & torch.tril(same, -1).any(1)
+    table = s["table"][parents]
+    col = torch.arange(table.shape[1], device=table.device)[None]
+    last = full.clamp(max=table.shape[1] - 1)
+    src = table[torch.arange(n, device=table.device), last].long()
+    rank = part.long().cumsum(0) - part.long()
+    fresh = s["free"][rank.clamp(max=s["free"].numel() - 1)]
+    table = torch.where(part[:, None] & (col == full[:, None]), fresh[:, None], table)
+    for x in _bytes(s["cache"]):
+        x[fresh[part].long()] = x[src[part]]
+    counts = part.sum().repeat(2).int()
+    lens_after = torch.where(s["ended"], 0, lens)
+    free, head = _plain_free(table, lens_after, s["blocks"], bs)
+    return dict(table=table, lens=lens_after, counts=counts, free=free, head=head,
+                cache=_bytes(s["cache"]))
+
+
+def _plain_compact(s):
+    bs, blocks = s["bs"], s["blocks"]
+    table = s["table"]
+    free, head = _plain_free(table, s["lens"], blocks, bs)
+    free = free[free >= 0].long()
+    held = torch.ones(blocks, dtype=torch.bool, device=table.device)
+    held[free] = False
+    held = torch.nonzero(held).flatten()
+    src, dst = held[held >= held.numel()], free[free < held.numel()]
+    new_ids = torch.full((blocks,), -1, dtype=torch.int32, device=table.device)
+    new_ids[held] = held.int()
+    new_ids[src] = dst.int()
+    for x in _bytes(s["cache"]):
+        x[dst] = x[src]
+    inside = torch.arange(table.shape[1], device=table.device)[None] < \
+        ((s["lens"].long() + bs - 1) // bs)[:, None]
+    counts = torch.tensor([held.numel(), src.numel()], dtype=torch.int32, device=table.device)
+    return dict(table=torch.where(inside, new_ids[table.clamp(min=0).long()], -1), new_ids=new_ids,
+                counts=counts, cache=_bytes(s["cache"]))
+
+
+# ------------------------------------------------------- the library's calls
+def _own(s):
+    from exact_attention_57_gb300 import fa
+    op = s["op"]
+    if op == "cache8":
+        fa.kv8_append(s["k"], s["v"], s["write"], *s["cache"])
+        k, v = fa.kv8_gather(s["read"], *s["cache"], dtype=s["k"].dtype, out=s["out"])
+        return dict(k=k, v=v, k_scales=s["cache"][1], v_scales=s["cache"][3])
+    if op == "attn8":
+        o, lse = fa.attention_kv8(s["q"], *s["cache"], s["table"], s["lens"], s["k_max"],
+                                  cu_seqlens_q=s["cu"], max_seqlen_q=s["nq"], causal=True,
+                                  out=s["out"], lse=s["lse"])
+        return dict(o=o, lse=lse)
+    if op == "copy":
+        fa.kv_copy(s["src"], s["dst"], s["cache"])
+        return dict(cache=_bytes(s["cache"]))
+    if op == "beam":
+        table, lens, counts = fa.kv_fork(s["table"], s["lens"], s["parents"], s["free"], s["bs"],
+                                         s["cache"], parents_end=s["end"], out=s["out"])
+        free, head = fa.kv_free(table, lens, s["blocks"], s["bs"], ended=s["ended"],
+                                out=s["free_out"])
+        return dict(table=table, lens=lens, counts=counts, free=free, head=head,
+                    cache=_bytes(s["cache"]))
+    table, new_ids, counts = fa.kv_compact(s["table"], s["lens"], s["cache"], s["bs"],
+                                           out=s["out"])
+    return dict(table=table, new_ids=new_ids, counts=counts, cache=_bytes(s["cache"]))
+
+
+def run(state):
+    if own:
+        return _own(state)
+    return {"cache8": _plain_cache8, "attn8": _plain_attn8, "copy": _plain_copy,
+            "beam": _plain_beam, "compact": _plain_compact}[state["op"]](state)
+
+
+# ------------------------------------------------------------------ work
+def _page_bytes(case):
+    row = case["d"] * 9 // 16 if case["kind"] == "kv4" else case["d"]
+    return 2 * case["Hk"] * (case["bs"] * row + (4 if case["kind"] == "kv8" else 0))
+
+
+def work(case):
+    op, bs = case["op"], case["bs"]
+    if op == "cache8":
+        es = 4 if case["dtype"] == "fp32" else 2
+        row = case["Hk"] * case["d"]
+        # (the order of the lengths moves the tokens read back by a block a sequence at most)
+        cached, new = _lens(case["B"], case["cached"]), _lens(case["B"], case["new"], 1)
+        T = sum(new)
+        R = T + sum(c % bs for c in cached)
+        touched = sum(-(-(c % bs + n) // bs) for c, n in zip(cached, new))
+        return {"bytes": 2 * row * (es + 1) * (T + R) + 8 * (T + R) + 16 * touched * case["Hk"],
+                "flops": 2 * row * (3 * T + R)}
+    if op == "attn8":
+        nq, Hq, Hk, d = case["nq"], case["Hq"], case["Hk"], case["d"]
+        es, lens = 2, _k_lens(case)
+        pairs = sum(nq * (n - nq) + nq * (nq + 1) // 2 for n in lens)
+        blocks = sum(-(-n // bs) for n in lens)
+        return {"bytes": sum(lens) * Hk * d * 2 + blocks * (4 + 8 * Hk)
+                + case["B"] * nq * Hq * (2 * d * es + 4), "flops": 4 * pairs * Hq * d}
+    page = _page_bytes(case)
+    if op == "copy":
+        return {"bytes": 2 * case["n"] * page + 8 * case["n"], "flops": 0}
+    held = _held(case)
+    used = sum(-(-n // bs) for n in held)
+    blocks = used + case["spare"]
+    width = -(-case["k_max"] // bs)
+    if op == "beam":
+        n, B = case["n"], case["B"]
+        if case["end"]:  # on average, of n draws among B
+            copies = n - B * (1 - (1 - 1 / B) ** n)
+        else:
+            copies = n
+        copies *= sum(x % bs > 0 for x in held) / B
+        return {"bytes": 2 * copies * page + 4 * (used + 2 * n * width + blocks), "flops": 0}
+    # on average, the pages that lie behind the first `used`
+    moved = used * case["spare"] / blocks
+    return {"bytes": 2 * moved * page + 4 * (used + case["B"] * width + blocks), "flops": 0}
+
+
+# ------------------------------------------------------------------ exact
+def _exact_codes():
+    """float64 values of the 256 e4m3 codes, from their bits."""
+    v = [(math.ldexp(n % 8, -9) if n // 8 % 16 == 0 else math.ldexp(8 + n % 8, n // 8 % 16 - 10))
+         * (-1 if n >= 128 else 1) for n in range(256)]
+    return torch.tensor(v, dtype=torch.float64, device="cuda")
+
+
+def _exact_cache8(s):
+    grid = _exact_codes()
+    up = grid[:127]  # 0 .. 448
+
+    def nearest(y):  # the even index where two are as near
+        a = y.abs().clamp(max=448.0).contiguous()
+        hi = torch.searchsorted(up, a).clamp(1, 126)
+        lo = hi - 1
+        dl, dh = a - up[lo], up[hi] - a
+        return up[torch.where((dl < dh) | ((dl == dh) & (lo % 2 == 0)), lo, hi)] * y.sign()
+
+    bs = s["bs"]
+    w, r = s["write"].cpu(), s["read"].cpu()
+    runs, begin = [], 0  # tokens [begin, end) of the call lie in one block
+    for t in range(1, w.numel() + 1):
+        if t == w.numel() or w[t] // bs != w[begin] // bs:
+            runs.append((begin, t))
+            begin = t
+    got = {}
+    for name, x, (codes, scales) in (("k", s["k"], s["cache"][:2]), ("v", s["v"], s["cache"][2:])):
+        rows = grid[codes.view(torch.uint8).long()]
+        unit = scales.double().clone()
+        for begin, end in runs:
+            b, off = int(w[begin]) // bs, int(w[begin]) % bs
+            y = x[begin:end].double()  # [tokens, Hk, d]
+            fit = torch.tensor([2.0 ** min(40, max(-40, math.ceil(math.log2(a / 448)))) if a > 0
+                                else 2.0 ** -40 for a in y.abs().amax((0, 2)).tolist()],
+                               dtype=torch.float64, device="cuda")
+            new = fit if off == 0 else torch.maximum(unit[b], fit)
+            rows[b, :, :off] = nearest(rows[b, :, :off] * (unit[b] / new)[:, None, None])
+            rows[b, :, off:off + end - begin] = nearest((y / new[:, None]).transpose(0, 1))
+            unit[b] = new
+        rows *= unit[:, :, None, None]
+        got[name] = rows[(r // bs).cuda(), :, (r % bs).cuda()]
+        got[name + "_scales"] = unit
+    return got
+
+
+def _exact_attn8(s):
+    B, nq, Hq, Hk, d, bs = (s[k] for k in ("B", "nq", "Hq", "Hk", "d", "bs"))
+    G = Hq // Hk
+    grid = _exact_codes()
+    O = torch.zeros(B * nq, Hq, d, dtype=torch.float64, device="cuda")
+    L = torch.full((Hq, B * nq), -math.inf, dtype=torch.float64, device="cuda")
+    for b, n in enumerate(s["lens"].tolist()):
+        if n == 0:
+            continue
+        ids = s["table"][b, :-(-n // bs)].long()
+        for h in range(Hk):
+            K, V = ((grid[c.view(torch.uint8)[ids, h].long()] * f[ids, h].double()[:, None, None])
+                    .flatten(0, 1)[:n] for c, f in (s["cache"][:2], s["cache"][2:]))
+            for x in range(h * G, h * G + G):
+                S = s["q"][b * nq:b * nq + nq, x].double() @ K.T / math.sqrt(d)
+                if nq > 1:
+                    hide = torch.ones(nq, n, dtype=torch.bool, device="cuda").triu(n - nq + 1)
+                    S[hide] = -math.inf
+                lse = S.logsumexp(-1)
+                p = (S - lse[:, None]).exp()
+                O[b * nq:b * nq + nq, x] = torch.where(lse[:, None] > -math.inf, p @ V, 0.0)
+                L[x, b * nq:b * nq + nq] = lse
+    return dict(o=O, lse=L)
+
+
+def exact(case, seed):
+    if case["op"] not in ("cache8", "attn8"):
+        return None  # whole numbers, and bytes that are copied
+    s = prepare(case, seed)
+    return _exact_attn8(s) if case["op"] == "attn8" else _exact_cache8(s)
