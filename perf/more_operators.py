@@ -183,8 +183,9 @@ def _random_table(lens, bs, width, ids):
 
 def _prepare_cache8(case, g):
     B, Hk, d, bs = (case[k] for k in ("B", "Hk", "d", "bs"))
-    cached = _shuffled(_lens(B, case["cached"]), g)
-    new = _shuffled(_lens(B, case["new"], 1), g)
+    order = torch.randperm(B, device="cuda", generator=g)
+    cached = torch.tensor(_lens(B, case["cached"]), device="cuda")[order]
+    new = torch.tensor(_lens(B, case["new"], 1), device="cuda")[order]
     total = cached + new
     need = (total + bs - 1) // bs
     blocks = int(need.sum()) + 8
@@ -454,7 +455,6 @@ def work(case):
     if op == "cache8":
         es = 4 if case["dtype"] == "fp32" else 2
         row = case["Hk"] * case["d"]
-        # (the order of the lengths moves the tokens read back by a block a sequence at most)
         cached, new = _lens(case["B"], case["cached"]), _lens(case["B"], case["new"], 1)
         T = sum(new)
         R = T + sum(c % bs for c in cached)
