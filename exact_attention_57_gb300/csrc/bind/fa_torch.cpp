@@ -18,8 +18,11 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <array>
 #include <cmath>
 #include <optional>
+#include <type_traits>
+#include <vector>
 
 #include "fa.h"
 
@@ -33,6 +36,15 @@ decltype(&fa_kv4_append) p_append = nullptr;
 decltype(&fa_kv4_gather) p_gather = nullptr;
 decltype(&fa_fwd_kv4) p_attention = nullptr;
 decltype(&fa_fwd_kv4_workspace) p_workspace = nullptr;
+decltype(&fa_kv8_append) p_append8 = nullptr;
+decltype(&fa_kv8_gather) p_gather8 = nullptr;
+decltype(&fa_fwd_kv8) p_attention8 = nullptr;
+decltype(&fa_fwd_kv8_workspace) p_workspace8 = nullptr;
+decltype(&fa_kv_copy) p_copy = nullptr;
+decltype(&fa_kv_fork) p_fork = nullptr;
+decltype(&fa_kv_free) p_free = nullptr;
+decltype(&fa_kv_compact) p_compact = nullptr;
+decltype(&fa_kv_compact_workspace) p_compact_workspace = nullptr;
 
 struct Bad {  // becomes a ValueError
   const char *what;
@@ -134,7 +146,8 @@ int run(F *f, A... args) {
 
 PyObject *status(int st) { return PyLong_FromLong(st); }
 
-// The four arrays of a 4-bit cache.
+// The four arrays of a cache in 4 bits or 8.
+template <int kBits>
 struct Cache {
   const Tensor *kc, *ks, *vc, *vs;
   int blocks, Hk, bs, d;
@@ -143,25 +156,29 @@ struct Cache {
       : kc(&tensor(a[0], kWhat)), ks(&tensor(a[1], kWhat)), vc(&tensor(a[2], kWhat)),
         vs(&tensor(a[3], kWhat)) {
     for (const Tensor *t : {kc, ks, vc, vs}) {
-      flat(*t, at::kByte, kWhat);
-      if (t->dim() != 4) throw Bad{kWhat};
+      const bool scale = t == ks || t == vs;
+      flat(*t, kBits == 4 ? at::kByte : scale ? at::kFloat : at::kFloat8_e4m3fn, kWhat);
+      if (t->dim() != (kBits == 8 && scale ? 2 : 4)) throw Bad{kWhat};
       call.here(*t);
     }
     const auto n = kc->sizes();
-    for (const Tensor *t : {ks, vc, vs}) {
+    if (vc->sizes() != n) throw Bad{kWhat};
+    for (const Tensor *t : {ks, vs}) {
       const auto m = t->sizes();
-      if (m[0] != n[0] || m[1] != n[1] || m[2] != n[2] || m[3] != (t == vc ? n[3] : n[3] / 8))
+      if (m[0] != n[0] || m[1] != n[1] || (kBits == 4 && (m[2] != n[2] || m[3] != n[3] / 8)))
         throw Bad{kWhat};
     }
     if (n[0] > 2147483647 || n[1] > 65535 || n[2] > 65535 || n[3] > 65535) throw Bad{kWhat};
     blocks = static_cast<int>(n[0]);
     Hk = static_cast<int>(n[1]);
     bs = static_cast<int>(n[2]);
-    d = static_cast<int>(2 * n[3]);
+    d = static_cast<int>(kBits == 4 ? 2 * n[3] : n[3]);
   }
   static constexpr const char *kWhat =
-      "cache: contiguous uint8 codes [blocks, Hk, block_size, d/2] and scales "
-      "[blocks, Hk, block_size, d/16] expected";
+      kBits == 4 ? "cache: contiguous uint8 codes [blocks, Hk, block_size, d/2] and scales "
+                   "[blocks, Hk, block_size, d/16] expected"
+                 : "cache: contiguous float8_e4m3fn codes [blocks, Hk, block_size, d] and float32 "
+                   "scales [blocks, Hk] expected";
 };
 
 int count(int64_t n) {
@@ -303,15 +320,20 @@ PyObject *rotary(PyObject *const *a) {
 }
 
 // ------------------------------------------------------------------ cache
+// The arguments of the two widths differ in the exponents, which the 8-bit cache has
+// none of: those behind them come `kExps` earlier.
+template <int kBits>
+constexpr int kExps = kBits == 4 ? 2 : 0;
+
+template <int kBits>
 PyObject *append(PyObject *const *a) {
   const Tensor &k = tensor(a[0], "k: a tensor expected");
   const Tensor &v = tensor(a[1], "v: a tensor expected");
   const Tensor &slots = tensor(a[2], "slots: a tensor expected");
-  const Call call(k, a[9]);
+  const Call call(k, a[7 + kExps<kBits>]);
   call.here(v);
   call.here(slots);
-  const Cache c(a + 3, call);
-  const int ke = int32(a[7]), ve = int32(a[8]);
+  const Cache<kBits> c(a + 3, call);
   flat(slots, at::kLong, "slots: a contiguous int64 tensor expected");
   const int T = count(slots.numel());
   for (const Tensor *x : {&k, &v}) {
@@ -323,22 +345,30 @@ PyObject *append(PyObject *const *a) {
   const long long row = static_cast<long long>(c.Hk) * c.d;  // of one token, the stride says nothing
   const long long ks = T > 1 ? k.stride(0) : row, vs = T > 1 ? v.stride(0) : row;
   const int code = dtype_code(k);
-  const int st = run(p_append, ptr(k), ptr(v), ks, vs, ptr<long long>(slots), T, ptr(*c.kc),
-                     ptr(*c.ks), ptr(*c.vc), ptr(*c.vs), c.blocks, c.Hk, c.bs, c.d, ke, ve, code,
-                     call.stream);
+  int st;
+  if constexpr (kBits == 4) {
+    const int ke = int32(a[7]), ve = int32(a[8]);
+    st = run(p_append, ptr(k), ptr(v), ks, vs, ptr<long long>(slots), T, ptr(*c.kc), ptr(*c.ks),
+             ptr(*c.vc), ptr(*c.vs), c.blocks, c.Hk, c.bs, c.d, ke, ve, code, call.stream);
+  } else {
+    st = run(p_append8, ptr(k), ptr(v), ks, vs, ptr<long long>(slots), T, ptr(*c.kc),
+             ptr<float>(*c.ks), ptr(*c.vc), ptr<float>(*c.vs), c.blocks, c.Hk, c.bs, c.d, code,
+             call.stream);
+  }
   if (st != FA_OK) return status(st);
   Py_RETURN_NONE;
 }
 
+template <int kBits>
 PyObject *gather(PyObject *const *a) {
   const Tensor &slots = tensor(a[0], "slots: a tensor expected");
-  const Call call(slots, a[9]);
-  const Cache c(a + 1, call);
-  const int ke = int32(a[6]), ve = int32(a[7]);
+  PyObject *const *b = a + 6 + kExps<kBits>;  // out, stream
+  const Call call(slots, b[1]);
+  const Cache<kBits> c(a + 1, call);
   flat(slots, at::kLong, "slots: a contiguous int64 tensor expected");
   const int R = count(slots.numel());
   Tensor out[2];
-  PyObject *given = none(a[8]) ? nullptr : a[8];
+  PyObject *given = none(b[0]) ? nullptr : b[0];
   if (given) {
     if (!PyTuple_Check(given) || PyTuple_GET_SIZE(given) != 2)
       throw Bad{"out: a tuple of two tensors expected"};
@@ -362,9 +392,16 @@ PyObject *gather(PyObject *const *a) {
     for (Tensor &t : out) t = call.make({R, c.Hk, c.d}, at::kBFloat16);
   }
   const int code = dtype_code(out[0]);
-  const int st = run(p_gather, ptr<long long>(slots), R, ptr(*c.kc), ptr(*c.ks), ptr(*c.vc),
-                     ptr(*c.vs), ptr(out[0]), ptr(out[1]), c.blocks, c.Hk, c.bs, c.d, ke, ve, code,
-                     call.stream);
+  int st;
+  if constexpr (kBits == 4) {
+    const int ke = int32(a[6]), ve = int32(a[7]);
+    st = run(p_gather, ptr<long long>(slots), R, ptr(*c.kc), ptr(*c.ks), ptr(*c.vc), ptr(*c.vs),
+             ptr(out[0]), ptr(out[1]), c.blocks, c.Hk, c.bs, c.d, ke, ve, code, call.stream);
+  } else {
+    st = run(p_gather8, ptr<long long>(slots), R, ptr(*c.kc), ptr<float>(*c.ks), ptr(*c.vc),
+             ptr<float>(*c.vs), ptr(out[0]), ptr(out[1]), c.blocks, c.Hk, c.bs, c.d, code,
+             call.stream);
+  }
   if (st != FA_OK) return status(st);
   if (given) {
     Py_INCREF(given);
@@ -377,17 +414,18 @@ PyObject *gather(PyObject *const *a) {
 }
 
 // ------------------------------------------------------------------ attention
+template <int kBits>
 PyObject *attention(PyObject *const *a) {
   const Tensor &q = tensor(a[0], "q: a tensor expected");
   const Tensor &table = tensor(a[5], "block_table: a tensor expected");
   const Tensor &lens = tensor(a[6], "seq_lens_k: a tensor expected");
-  const Call call(q, a[16]);
+  PyObject *const *g = a + 12 + kExps<kBits>;  // (out, lse), workspace, stream
+  const Call call(q, g[2]);
   call.here(table);
   call.here(lens);
-  const Cache c(a + 1, call);
+  const Cache<kBits> c(a + 1, call);
   const int max_k = int32(a[7]), max_q = int32(a[9]);
   const bool causal = truth(a[11]);
-  const int ke = int32(a[12]), ve = int32(a[13]);
   if (q.dim() != 3 || q.size(2) != c.d || !q.is_contiguous())
     throw Bad{"q: a contiguous [total_q, Hq, d] tensor expected"};
   constexpr const char *kInts =
@@ -412,7 +450,6 @@ PyObject *attention(PyObject *const *a) {
   }
   const int code = dtype_code(q);
   Tensor out, lse, ws;
-  PyObject *const *g = a + 14;  // (out, lse), workspace
   PyObject *po = PyTuple_GET_ITEM(g[0], 0), *pl = PyTuple_GET_ITEM(g[0], 1);
   if (none(po)) {
     out = call.like(q);
@@ -433,7 +470,7 @@ PyObject *attention(PyObject *const *a) {
   }
   unsigned long long ws_bytes = 0;
   if (none(g[1])) {
-    ws_bytes = p_workspace(B, Hq, c.Hk, max_q, c.d);
+    ws_bytes = (kBits == 4 ? p_workspace : p_workspace8)(B, Hq, c.Hk, max_q, c.d);
     if (ws_bytes > 0)
       ws = call.make({static_cast<int64_t>(ws_bytes)}, at::kByte);
   } else {
@@ -442,11 +479,20 @@ PyObject *attention(PyObject *const *a) {
     if (!ws.is_contiguous()) throw Bad{"workspace: a contiguous tensor expected"};
     ws_bytes = ws.nbytes();
   }
-  const int st = run(p_attention, ptr(q), ptr(out), ptr<float>(lse), ptr(*c.kc), ptr(*c.ks),
-                     ptr(*c.vc), ptr(*c.vs), ptr<int>(table), ptr<int>(lens), cu, B, Hq, c.Hk,
-                     total, max_q, max_k, c.blocks, c.bs, count(table.size(1)), c.d,
-                     static_cast<float>(scale), causal, ke, ve, code, ws.defined() ? ptr(ws) :
-                     nullptr, ws_bytes, call.stream);
+  void *wsp = ws.defined() ? ptr(ws) : nullptr;
+  int st;
+  if constexpr (kBits == 4) {
+    const int ke = int32(a[12]), ve = int32(a[13]);
+    st = run(p_attention, ptr(q), ptr(out), ptr<float>(lse), ptr(*c.kc), ptr(*c.ks), ptr(*c.vc),
+             ptr(*c.vs), ptr<int>(table), ptr<int>(lens), cu, B, Hq, c.Hk, total, max_q, max_k,
+             c.blocks, c.bs, count(table.size(1)), c.d, static_cast<float>(scale), causal, ke, ve,
+             code, wsp, ws_bytes, call.stream);
+  } else {
+    st = run(p_attention8, ptr(q), ptr(out), ptr<float>(lse), ptr(*c.kc), ptr<float>(*c.ks),
+             ptr(*c.vc), ptr<float>(*c.vs), ptr<int>(table), ptr<int>(lens), cu, B, Hq, c.Hk, total,
+             max_q, max_k, c.blocks, c.bs, count(table.size(1)), c.d, static_cast<float>(scale),
+             causal, code, wsp, ws_bytes, call.stream);
+  }
   if (st != FA_OK) return status(st);
   PyObject *r = PyTuple_New(2);
   if (!r) return nullptr;
@@ -458,6 +504,194 @@ PyObject *attention(PyObject *const *a) {
   PyTuple_SET_ITEM(r, 0, give(out, po));
   PyTuple_SET_ITEM(r, 1, give(lse, pl));
   return r;
+}
+
+// ------------------------------------------------------------------ pages
+// The arrays of a cache, [blocks, ...] each, as the library takes them.
+struct PageList {
+  std::vector<void *> at;
+  std::vector<unsigned long long> bytes;
+  int64_t blocks = -1;
+
+  PageList(PyObject *o, const Call &call) {
+    constexpr const char *kWhat = "caches: a list of contiguous tensors [blocks, ...] expected";
+    if (!PyTuple_Check(o)) throw Bad{kWhat};
+    const Py_ssize_t n = PyTuple_GET_SIZE(o);
+    at.reserve(n);
+    bytes.reserve(n);
+    for (Py_ssize_t i = 0; i < n; ++i) {
+      const Tensor &t = tensor(PyTuple_GET_ITEM(o, i), kWhat);
+      if (t.dim() < 1 || !t.is_contiguous() || t.numel() == 0) throw Bad{kWhat};
+      call.here(t);
+      if (blocks >= 0 && t.size(0) != blocks) throw Bad{"caches: arrays of as many blocks expected"};
+      blocks = t.size(0);
+      at.push_back(ptr(t));
+      bytes.push_back(t.nbytes() / static_cast<unsigned long long>(blocks));
+    }
+  }
+};
+
+constexpr const char *kTable =
+    "block_table [B, max_blocks] and seq_lens [B]: contiguous int32 tensors expected";
+
+void table_of(const Tensor &table, const Tensor &lens, const Call &call) {
+  for (const Tensor *t : {&table, &lens}) {
+    flat(*t, at::kInt, kTable);
+    call.here(*t);
+  }
+  if (table.dim() != 2 || lens.numel() != table.size(0)) throw Bad{kTable};
+}
+
+// Outputs given as a tuple of int32 tensors of these sizes, or made.
+template <int N>
+PyObject *int_outputs(PyObject *given, const Call &call, const std::array<std::vector<int64_t>, N> &sizes,
+                      Tensor (&out)[N], const char *what) {
+  if (none(given)) {
+    for (int i = 0; i < N; ++i) out[i] = call.make(sizes[i], at::kInt);
+    return nullptr;
+  }
+  if (!PyTuple_Check(given) || PyTuple_GET_SIZE(given) != N) throw Bad{what};
+  for (int i = 0; i < N; ++i) {
+    out[i] = tensor(PyTuple_GET_ITEM(given, i), what);
+    flat(out[i], at::kInt, what);
+    call.here(out[i]);
+    if (out[i].sizes() != at::IntArrayRef(sizes[i])) throw Bad{what};
+  }
+  return given;
+}
+template <int N>
+PyObject *results(PyObject *given, const Tensor (&out)[N]) {
+  if (given) {
+    Py_INCREF(given);
+    return given;
+  }
+  PyObject *r = PyTuple_New(N);
+  if (!r) return nullptr;
+  for (int i = 0; i < N; ++i) PyTuple_SET_ITEM(r, i, THPVariable_Wrap(out[i]));
+  return r;
+}
+
+// src, dst, arrays, arrays to write to (or None), stream
+PyObject *kv_copy(PyObject *const *a) {
+  const Tensor &src = tensor(a[0], "src: a tensor expected");
+  const Tensor &dst = tensor(a[1], "dst: a tensor expected");
+  const Call call(src, a[4]);
+  call.here(dst);
+  constexpr const char *kIds = "src, dst: contiguous int32 tensors of one length expected";
+  flat(src, at::kInt, kIds);
+  flat(dst, at::kInt, kIds);
+  if (src.numel() != dst.numel()) throw Bad{kIds};
+  const PageList from(a[2], call);
+  const bool other = !none(a[3]);
+  const PageList to(other ? a[3] : a[2], call);
+  if (from.bytes != to.bytes) throw Bad{"caches: arrays with the same pages expected"};
+  const int st = run(p_copy, ptr<int>(src), ptr<int>(dst), count(src.numel()),
+                     const_cast<const void *const *>(from.at.data()), to.at.data(), from.bytes.data(),
+                     count(from.at.size()), count(from.blocks), count(to.blocks), call.stream);
+  if (st != FA_OK) return status(st);
+  Py_RETURN_NONE;
+}
+
+// block_table, seq_lens, parents, free_blocks, block_size, arrays, num_blocks (or
+// None: the arrays'), free_head, parents_end, out, stream
+PyObject *kv_fork(PyObject *const *a) {
+  const Tensor &table = tensor(a[0], kTable);
+  const Tensor &lens = tensor(a[1], kTable);
+  const Tensor &parents = tensor(a[2], "parents: a tensor expected");
+  const Tensor &free_blocks = tensor(a[3], "free_blocks: a tensor expected");
+  const int bs = int32(a[4]);
+  const Call call(table, a[10]);
+  table_of(table, lens, call);
+  for (const Tensor *t : {&parents, &free_blocks}) {
+    flat(*t, at::kInt, "parents, free_blocks: contiguous int32 tensors expected");
+    call.here(*t);
+  }
+  const PageList pages(a[5], call);
+  if (none(a[6]) && pages.blocks < 0) throw Bad{"num_blocks: expected where there are no caches"};
+  const int blocks = none(a[6]) ? count(pages.blocks) : int32(a[6]);
+  if (pages.blocks >= 0 && pages.blocks != blocks)
+    throw Bad{"num_blocks: the caches' number of blocks expected"};
+  const int *head = nullptr;
+  if (!none(a[7])) {
+    const Tensor &h = tensor(a[7], "free_head: a tensor expected");
+    call.here(h);
+    if (h.scalar_type() != at::kInt || h.numel() < 1)
+      throw Bad{"free_head: an int32 tensor of one element expected"};
+    head = ptr<int>(h);
+  }
+  const bool end = truth(a[8]);
+  const int64_t n = parents.numel(), w = table.size(1);
+  Tensor out[3];
+  PyObject *given = int_outputs<3>(a[9], call, {{{n, w}, {n}, {2}}}, out,
+                                   "out: contiguous int32 block_table [n, max_blocks], seq_lens [n] "
+                                   "and counts [2] expected");
+  const int st = run(p_fork, ptr<int>(table), ptr<int>(lens), ptr<int>(parents),
+                     ptr<int>(free_blocks), head, ptr<int>(out[0]), ptr<int>(out[1]),
+                     ptr<int>(out[2]), count(lens.numel()), count(n), count(w), bs,
+                     count(free_blocks.numel()), blocks, end, pages.at.data(), pages.bytes.data(),
+                     count(pages.at.size()), call.stream);
+  return st != FA_OK ? status(st) : results(given, out);
+}
+
+// block_table, seq_lens, num_blocks, block_size, ended, out, stream
+PyObject *kv_free(PyObject *const *a) {
+  const Tensor &table = tensor(a[0], kTable);
+  const Tensor &lens = tensor(a[1], kTable);
+  const int blocks = int32(a[2]), bs = int32(a[3]);
+  const Call call(table, a[6]);
+  table_of(table, lens, call);
+  const unsigned char *ended = nullptr;
+  if (!none(a[4])) {
+    constexpr const char *kEnded = "ended: a contiguous bool tensor [B] expected";
+    const Tensor &t = tensor(a[4], kEnded);
+    flat(t, at::kBool, kEnded);
+    call.here(t);
+    if (t.numel() != lens.numel()) throw Bad{kEnded};
+    ended = ptr<unsigned char>(t);
+  }
+  Tensor out[2];
+  PyObject *given = int_outputs<2>(a[5], call, {{{blocks > 0 ? blocks : 0}, {1}}}, out,
+                                   "out: contiguous int32 free_blocks [num_blocks] and free_head [1] "
+                                   "expected");
+  const int st = run(p_free, ptr<int>(table), ptr<int>(lens), ended, ptr<int>(out[0]),
+                     ptr<int>(out[1]), count(lens.numel()), count(table.size(1)), bs, blocks,
+                     call.stream);
+  return st != FA_OK ? status(st) : results(given, out);
+}
+
+// block_table, seq_lens, arrays, num_blocks (or None: the arrays'), block_size, out,
+// workspace, stream
+PyObject *kv_compact(PyObject *const *a) {
+  const Tensor &table = tensor(a[0], kTable);
+  const Tensor &lens = tensor(a[1], kTable);
+  const int bs = int32(a[4]);
+  const Call call(table, a[7]);
+  table_of(table, lens, call);
+  const PageList pages(a[2], call);
+  if (none(a[3]) && pages.blocks < 0) throw Bad{"num_blocks: expected where there are no caches"};
+  const int blocks = none(a[3]) ? count(pages.blocks) : int32(a[3]);
+  if (pages.blocks >= 0 && pages.blocks != blocks)
+    throw Bad{"num_blocks: the caches' number of blocks expected"};
+  const int64_t n = lens.numel(), w = table.size(1);
+  Tensor out[3], ws;
+  PyObject *given = int_outputs<3>(a[5], call, {{{n, w}, {blocks > 0 ? blocks : 0}, {2}}}, out,
+                                   "out: contiguous int32 block_table [B, max_blocks], new_ids "
+                                   "[num_blocks] and counts [2] expected");
+  unsigned long long ws_bytes = 0;
+  if (none(a[6])) {
+    ws_bytes = p_compact_workspace(blocks);
+    if (ws_bytes > 0) ws = call.make({static_cast<int64_t>(ws_bytes)}, at::kByte);
+  } else {
+    ws = tensor(a[6], "workspace: a tensor expected");
+    call.here(ws);
+    if (!ws.is_contiguous()) throw Bad{"workspace: a contiguous tensor expected"};
+    ws_bytes = ws.nbytes();
+  }
+  const int st = run(p_compact, ptr<int>(table), ptr<int>(lens), ptr<int>(out[0]), ptr<int>(out[1]),
+                     ptr<int>(out[2]), count(n), count(w), bs, blocks, pages.at.data(),
+                     pages.bytes.data(), count(pages.at.size()), ws.defined() ? ptr(ws) : nullptr,
+                     ws_bytes, call.stream);
+  return st != FA_OK ? status(st) : results(given, out);
 }
 
 // One entry: the number of arguments, and exceptions on their way to Python.
@@ -481,26 +715,26 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// bind(addresses of the six C entry points)
+// bind(addresses of the C entry points, in the order of fa.py)
 PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
-  if (n != 6) {
-    PyErr_SetString(PyExc_TypeError, "six addresses expected");
+  constexpr Py_ssize_t N = 15;
+  if (n != N) {
+    PyErr_Format(PyExc_ValueError, "%zd addresses expected", N);
     return nullptr;
   }
-  void *p[6];
-  for (int i = 0; i < 6; ++i) {
+  void *p[N];
+  for (Py_ssize_t i = 0; i < N; ++i) {
     p[i] = PyLong_AsVoidPtr(args[i]);
     if (!p[i]) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "an address is null");
       return nullptr;
     }
   }
-  p_kv_plan = reinterpret_cast<decltype(p_kv_plan)>(p[0]);
-  p_rope = reinterpret_cast<decltype(p_rope)>(p[1]);
-  p_append = reinterpret_cast<decltype(p_append)>(p[2]);
-  p_gather = reinterpret_cast<decltype(p_gather)>(p[3]);
-  p_attention = reinterpret_cast<decltype(p_attention)>(p[4]);
-  p_workspace = reinterpret_cast<decltype(p_workspace)>(p[5]);
+  int i = 0;
+  auto take = [&](auto &f) { f = reinterpret_cast<std::decay_t<decltype(f)>>(p[i++]); };
+  take(p_kv_plan), take(p_rope), take(p_append), take(p_gather), take(p_attention);
+  take(p_workspace), take(p_append8), take(p_gather8), take(p_attention8), take(p_workspace8);
+  take(p_copy), take(p_fork), take(p_free), take(p_compact), take(p_compact_workspace);
   Py_RETURN_NONE;
 }
 
@@ -510,8 +744,12 @@ PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
 PyMethodDef g_methods[] = {
     {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind)), METH_FASTCALL,
      nullptr},
-    ENTRY("kv_plan", kv_plan, 9), ENTRY("rotary", rotary, 9), ENTRY("kv4_append", append, 10),
-    ENTRY("kv4_gather", gather, 10), ENTRY("attention_kv4", attention, 17),
+    ENTRY("kv_plan", kv_plan, 9), ENTRY("rotary", rotary, 9), ENTRY("kv4_append", append<4>, 10),
+    ENTRY("kv4_gather", gather<4>, 10), ENTRY("attention_kv4", attention<4>, 17),
+    ENTRY("kv8_append", append<8>, 8), ENTRY("kv8_gather", gather<8>, 8),
+    ENTRY("attention_kv8", attention<8>, 15), ENTRY("kv_copy", kv_copy, 5),
+    ENTRY("kv_fork", kv_fork, 11), ENTRY("kv_free", kv_free, 7),
+    ENTRY("kv_compact", kv_compact, 8),
     {nullptr, nullptr, 0, nullptr}};
 #undef ENTRY
 

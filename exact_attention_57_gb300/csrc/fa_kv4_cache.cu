@@ -42,7 +42,7 @@ namespace {
 constexpr int kThreads = 256;
 
 // Byte-row index of (slot, head) in the cache; slot in [0, num_blocks * bs).
-__device__ __forceinline__ long long cache_row(const Kv4Store &c, long long slot, int h) {
+__device__ __forceinline__ long long cache_row(const KvStore &c, long long slot, int h) {
   const long long block = slot >> c.bs_log2, off = slot & ((1 << c.bs_log2) - 1);
   return ((block * c.Hk + h) << c.bs_log2) + off;
 }
@@ -52,7 +52,7 @@ struct At {
   long long row;
   int hg;
 };
-__device__ __forceinline__ At place(const Kv4Store &c) {
+__device__ __forceinline__ At place(const KvStore &c) {
   const int per_row = c.Hk * (c.d / 16);
   const long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
   if (i >> 32 == 0) {  // the common case: a 32-bit division
@@ -64,7 +64,7 @@ __device__ __forceinline__ At place(const Kv4Store &c) {
 }
 
 // Index of a slot's 16 elements in the cache, in units of 16.
-__device__ __forceinline__ long long cache_at(const Kv4Store &c, long long slot, int hg) {
+__device__ __forceinline__ long long cache_at(const KvStore &c, long long slot, int hg) {
   const int groups = c.d / 16, h = hg / groups;
   return cache_row(c, slot, h) * groups + (hg - h * groups);
 }
@@ -134,7 +134,7 @@ __device__ __forceinline__ void quantise(const Group<T> &x, float unit, uint2 *c
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
     fa_kv4_append_kernel(const T *k, const T *v, long long k_stride, long long v_stride,
-                         const long long *slots, int T_, const Kv4Store c, bool wide) {
+                         const long long *slots, int T_, const KvStore c, bool wide) {
   griddep_wait();
   griddep_launch_dependents();
   const At at = place(c);
@@ -184,7 +184,7 @@ __device__ __forceinline__ void expand(uint2 codes, uint32_t scale, int exp, T *
 // reads zeros.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-    fa_kv4_gather_kernel(const long long *slots, int R, const Kv4Store c, T *k_out, T *v_out,
+    fa_kv4_gather_kernel(const long long *slots, int R, const KvStore c, T *k_out, T *v_out,
                          bool wide) {
   griddep_wait();
   griddep_launch_dependents();
@@ -223,21 +223,21 @@ cudaError_t launch(void (*kern)(A...), long long threads, cudaStream_t s, A... a
 
 template <typename T>
 cudaError_t append(const void *k, const void *v, long long ks, long long vs,
-                   const long long *slots, int T_, const Kv4Store &c, cudaStream_t s) {
+                   const long long *slots, int T_, const KvStore &c, cudaStream_t s) {
   const long long es = sizeof(T);
   const bool wide = (reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) % 32 == 0 &&
                     ks * es % 32 == 0 && vs * es % 32 == 0;
-  return launch<const T *, const T *, long long, long long, const long long *, int, const Kv4Store,
+  return launch<const T *, const T *, long long, long long, const long long *, int, const KvStore,
                 bool>(fa_kv4_append_kernel<T>, static_cast<long long>(T_) * c.Hk * (c.d / 16), s,
                       static_cast<const T *>(k), static_cast<const T *>(v), ks, vs, slots, T_, c,
                       wide);
 }
 
 template <typename T>
-cudaError_t gather(const long long *slots, int R, const Kv4Store &c, void *k, void *v,
+cudaError_t gather(const long long *slots, int R, const KvStore &c, void *k, void *v,
                    cudaStream_t s) {
   const bool wide = (reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) % 32 == 0;
-  return launch<const long long *, int, const Kv4Store, T *, T *, bool>(
+  return launch<const long long *, int, const KvStore, T *, T *, bool>(
       fa_kv4_gather_kernel<T>, static_cast<long long>(R) * c.Hk * (c.d / 16), s, slots, R, c,
       static_cast<T *>(k), static_cast<T *>(v), wide);
 }
@@ -245,7 +245,7 @@ cudaError_t gather(const long long *slots, int R, const Kv4Store &c, void *k, vo
 }  // namespace
 
 cudaError_t launch_kv4_append(const void *k, const void *v, long long k_stride, long long v_stride,
-                              const long long *slots, int T, const Kv4Store &c, int dtype,
+                              const long long *slots, int T, const KvStore &c, int dtype,
                               cudaStream_t s) {
   if (dtype == FA_DTYPE_BF16)
     return append<__nv_bfloat16>(k, v, k_stride, v_stride, slots, T, c, s);
@@ -253,7 +253,7 @@ cudaError_t launch_kv4_append(const void *k, const void *v, long long k_stride, 
   return append<float>(k, v, k_stride, v_stride, slots, T, c, s);
 }
 
-cudaError_t launch_kv4_gather(const long long *slots, int R, const Kv4Store &c, void *k_out,
+cudaError_t launch_kv4_gather(const long long *slots, int R, const KvStore &c, void *k_out,
                               void *v_out, int dtype, cudaStream_t s) {
   if (dtype == FA_DTYPE_BF16) return gather<__nv_bfloat16>(slots, R, c, k_out, v_out, s);
   if (dtype == FA_DTYPE_F16) return gather<__half>(slots, R, c, k_out, v_out, s);

@@ -1,0 +1,134 @@
+// fa_kv8_attn.cu — attention of a few queries a sequence over the paged 8-bit
+// cache: the kernel of fa_kv_attn.cuh for codes of e4m3 with one scale for a block
+// of tokens of a key head.
+//
+// Codes become fp16 pairs by cvt, exactly (V: the bytes of two tokens are paired
+// first, since a register holds two tokens of one column); the block's scales enter
+// the softmax instead (BlockScale), one multiplication and addition a score.
+#include "fa_kv8.cuh"
+#include "fa_kv_attn.cuh"
+
+namespace fa {
+namespace {
+
+template <int D_>
+struct Cache8 {
+  static constexpr int D = D_, KS = D / 16;
+
+  template <int NT>
+  struct Shape {
+    static constexpr int kWarps = 8;
+    static constexpr int kCtas = D == 64 && NT <= 2 ? 2 : 1;
+    static constexpr int kLead = NT == 1 ? 3 : NT == 2 && D == 64 ? 4 : 6;
+  };
+
+  struct Tile {
+    uint32_t k[2][D / 16], v[4][D / 32];
+    float ks, vs;
+  };
+
+  struct Lane {
+    const uint8_t *kc, *vc;
+    int h;
+    __device__ __forceinline__ Lane(const KvStore &p, int h, int r, int c)
+        : kc(p.k_codes + r * D + c * (D / 4)), vc(p.v_codes + 2 * c * D + r * (D / 8)), h(h) {}
+    // Tokens off .. off + 15 of block id.
+    __device__ __forceinline__ void load(Tile &x, const KvStore &p, int id, int off) const {
+      const long long block = static_cast<long long>(id) * p.Hk + h;
+      const long long row = (block << p.bs_log2) + off;
+      const uint8_t *a = kc + row * D, *w = vc + row * D;
+      load_words(x.k[0], a);
+      load_words(x.k[1], a + 8 * D);
+      load_words(x.v[0], w);
+      load_words(x.v[1], w + D);
+      load_words(x.v[2], w + 8 * D);
+      load_words(x.v[3], w + 9 * D);
+      x.ks = __ldg(reinterpret_cast<const float *>(p.k_scales) + block);
+      x.vs = __ldg(reinterpret_cast<const float *>(p.v_scales) + block);
+    }
+  };
+
+  struct Scale : BlockScale {
+    __device__ __forceinline__ float score(float s, float q) const { return fmaf(s, q * k, v_log); }
+    __device__ __forceinline__ float add(float l, float w) const { return fmaf(w, v_inv, l); }
+  };
+  static __device__ __forceinline__ Scale scale_of(const Tile &x) {
+    Scale s;
+    s.set(x.ks, x.vs);
+    return s;
+  }
+
+  template <int NT>
+  static __device__ __forceinline__ void scores(const Tile &x, const uint32_t (&qf)[NT][D / 8],
+                                                float (&s)[NT][4]) {
+#pragma unroll
+    for (int st = 0; st < KS; ++st) {
+      const uint32_t w0 = x.k[0][st], w1 = x.k[1][st];
+      const uint32_t a0 = e4m3x2_f16x2(w0), a1 = e4m3x2_f16x2(w1);
+      const uint32_t a2 = e4m3x2_f16x2_hi(w0), a3 = e4m3x2_f16x2_hi(w1);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        mma_f16(s[nt], a0, a1, a2, a3, qf[nt][2 * st], qf[nt][2 * st + 1]);
+    }
+  }
+
+  // `left`: tokens of the sequence from the tile's first on.
+  template <int NT>
+  static __device__ __forceinline__ void values(const Tile &x, int left, int c,
+                                                const uint32_t (&pf)[NT][2], float (&o)[NT][KS][4]) {
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) {
+      uint32_t v[4] = {x.v[0][w], x.v[1][w], x.v[2][w], x.v[3][w]};
+      if (left < 16) {  // a token behind the sequence has P = 0, and codes that may be anything
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+          if (2 * c + (n & 1) + 4 * (n & 2) >= left) v[n] = 0;
+      }
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {  // columns 4w + 2n and one on, of tokens (0, 1) and (2, 3)
+        const uint32_t e = __byte_perm(v[0], v[1], n ? 0x7362 : 0x5140);
+        const uint32_t f = __byte_perm(v[2], v[3], n ? 0x7362 : 0x5140);
+        const uint32_t a0 = e4m3x2_f16x2(e), a1 = e4m3x2_f16x2_hi(e);
+        const uint32_t a2 = e4m3x2_f16x2(f), a3 = e4m3x2_f16x2_hi(f);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma_f16(o[nt][2 * w + n], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+      }
+    }
+  }
+};
+
+}  // namespace
+
+int kv8_tile_rows(int group, int max_q, int d) {
+  const int rows = fit_rows(group, max_q);
+  // (two tiles of codes beside 32 rows' sums would not fit the registers)
+  return rows == 32 && d == 128 ? 0 : rows;
+}
+
+KvGrid kv8_grid(int B, int Hk, int group, int d, int max_q, int max_k, int num_sms) {
+  const long long heads = static_cast<long long>(B) * Hk;
+  if (num_sms < 1) num_sms = 1;
+  KvGrid g = {kv8_tile_rows(group, max_q, d), 0, 0, 0};
+  if (d == 64)
+    rows_grid<Cache8<64>>(heads, max_k, num_sms, &g);
+  else
+    rows_grid<Cache8<128>>(heads, max_k, num_sms, &g);
+  many_grid(heads, group, max_q, max_k, num_sms, &g);
+  return g;
+}
+
+template <typename T>
+cudaError_t launch_type(const KvAttn &p, const KvGrid &g, float *ws, cudaStream_t s) {
+  if (p.c.d == 64) return launch_rows<T, Cache8<64>>(p, g, ws, s);
+  return g.rows == 8 ? launch<T, Cache8<128>, 1>(p, g, ws, s)
+                     : launch<T, Cache8<128>, 2>(p, g, ws, s);
+}
+
+cudaError_t launch_kv8_attn(const KvAttn &p, const KvGrid &g, int dtype, float *ws,
+                            cudaStream_t s) {
+  return dtype == FA_DTYPE_BF16 ? launch_type<__nv_bfloat16>(p, g, ws, s)
+                                : launch_type<__half>(p, g, ws, s);
+}
+
+}  // namespace fa

@@ -1,4 +1,4 @@
-// fa_kv4_split.cuh — how the attention kernels over the 4-bit cache deal their
+// fa_kv_split.cuh — how the attention kernels over the 4-bit cache deal their
 // work: all tiles of all sequences lie in one line of units (a unit is a step
 // along the keys), every CTA takes an equal share of the line, and tiles that
 // shares cut are joined by a second kernel from parts in the workspace.
@@ -15,7 +15,7 @@ struct Seq {
   int r0, nq, nk;
 };
 
-__device__ __forceinline__ Seq load_seq(const Kv4Attn &p, int b) {
+__device__ __forceinline__ Seq load_seq(const KvAttn &p, int b) {
   Seq s = {b, 1, 0};
   if (p.cu_q) {
     s.r0 = min(max(p.cu_q[b], 0), p.total_q);
@@ -67,7 +67,7 @@ __device__ __forceinline__ int cta_of(long long u, long long total, int den) {
 // CTA n: rows of D sums, then (m, sum of weights) a row.
 template <int D, int R>
 __device__ __forceinline__ float *part_of(float *ws, int n, int which) {
-  return ws + kKv4MaxCtas * (sizeof(Share) / sizeof(float)) +
+  return ws + kKvMaxCtas * (sizeof(Share) / sizeof(float)) +
          static_cast<long long>(2 * n + which) * R * (D + 2);
 }
 
@@ -82,7 +82,7 @@ struct Place {
 // sequence b, all key heads (all kWarps * 32 threads get it); den becomes the
 // smaller of itself and the units in all.  `sums` holds a prefix sum a thread.
 template <int kWarps, typename F>
-__device__ Place find_unit(const Kv4Attn &p, F units, int num, int *den, long long *target,
+__device__ Place find_unit(const KvAttn &p, F units, int num, int *den, long long *target,
                            long long *sums, long long (*warp_sums)[kWarps]) {
   constexpr int kThreads = kWarps * 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -163,7 +163,7 @@ __device__ Place find_unit(const Kv4Attn &p, F units, int num, int *den, long lo
 constexpr int kJoinRows = 4, kJoinThreads = 256;
 
 template <typename T, int D, int R>
-__global__ void __launch_bounds__(kJoinThreads) fa_kv4_join_kernel(const Kv4Attn p, float *ws) {
+__global__ void __launch_bounds__(kJoinThreads) fa_kv_join_kernel(const KvAttn p, float *ws) {
   constexpr int kWarps = kJoinThreads / 32;
   constexpr int W = D / 32;  // columns a lane
   __shared__ float s_sum[kWarps][kJoinRows][D];
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kJoinThreads) fa_kv4_join_kernel(const Kv4Attn
         // rows wants, whose latency counts (one sequence of 131071 keys 35.5 us
         // instead of 36.2); the many CTAs of a join of 128 rows want the registers
         // (428 us for two chunks of 2048 queries, 437 with it).
-        if (R < kKv4ManyRows && ml[x][y].y == 0.f) continue;
+        if (R < kKvManyRows && ml[x][y].y == 0.f) continue;
         const float to = fmaxf(mm[y], ml[x][y].x), off = to == -INFINITY ? 0.f : to;
         const float f = ex2_approx(mm[y] - off), g = ex2_approx(ml[x][y].x - off);
         mm[y] = to;

@@ -51,63 +51,117 @@ struct RopeParams {
 // dtype: FA_DTYPE_BF16, FA_DTYPE_F16 or FA_DTYPE_F32.
 cudaError_t launch_rope(const RopeParams &p, int dtype, int num_sms, cudaStream_t s);
 
-// ------------------------------------------------------------ 4-bit cache
-// Row (block, head, offset) of the cache: d/2 bytes of codes and d/16 bytes
+// ------------------------------------------------------------ caches
+// Row (block, head, offset) of the 4-bit cache: d/2 bytes of codes and d/16 bytes
 // of scales, rows in that order.
-struct Kv4Store {
+struct KvStore {
   uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
   int num_blocks, Hk, bs_log2, d;
   int k_exp, v_exp;
 };
 cudaError_t launch_kv4_append(const void *k, const void *v, long long k_stride, long long v_stride,
-                              const long long *slots, int T, const Kv4Store &c, int dtype,
+                              const long long *slots, int T, const KvStore &c, int dtype,
                               cudaStream_t s);
-cudaError_t launch_kv4_gather(const long long *slots, int R, const Kv4Store &c, void *k_out,
+cudaError_t launch_kv4_gather(const long long *slots, int R, const KvStore &c, void *k_out,
                               void *v_out, int dtype, cudaStream_t s);
 
+// The 8-bit cache: d bytes of codes a row, an fp32 scale for (block, head) in
+// k_scales and v_scales; k_exp and v_exp are 0.
+cudaError_t launch_kv8_append(const void *k, const void *v, long long k_stride, long long v_stride,
+                              const long long *slots, int T, const KvStore &c, int dtype,
+                              cudaStream_t s);
+cudaError_t launch_kv8_gather(const long long *slots, int R, const KvStore &c, void *k_out,
+                              void *v_out, int dtype, cudaStream_t s);
+
+// ------------------------------------------------------------ pages
+// The arrays of a cache, pages of bytes[i] bytes: read from, written to.
+constexpr int kMaxArrays = 256;
+constexpr int kMaxSweep = 1 << 23;  // blocks that launch_kv_free and launch_kv_compact take
+struct Pages {
+  const void *const *from;
+  void *const *to;
+  const unsigned long long *bytes;
+  int num;
+};
+cudaError_t launch_kv_copy(const Pages &pages, const int *src, const int *dst, int n, int from_blocks,
+                           int to_blocks, int num_sms, cudaStream_t s);
+struct ForkParams {
+  const int *table, *lens;        // [B][width], [B]
+  const int *parents;             // [n]
+  const int *free_blocks;         // [num_free]
+  const int *free_head;           // entries of free_blocks already used, or null
+  int *table_out, *lens_out;      // [n][width], [n]
+  int *counts;                    // {blocks needed, entries of free_blocks used}
+  int B, n, width, bs_log2, num_free, num_blocks, parents_end;
+};
+cudaError_t launch_kv_fork(const Pages &pages, const ForkParams &p, int num_sms, cudaStream_t s);
+struct FreeParams {
+  const int *table;               // [B][width]
+  int *lens;                      // [B]
+  const unsigned char *ended;     // [B] or null
+  int *free_blocks, *free_head;   // [num_blocks], {blocks held}
+  int B, width, bs_log2, num_blocks;
+};
+cudaError_t launch_kv_free(const FreeParams &p, cudaStream_t s);
+struct CompactParams {
+  const int *table, *lens;        // [B][width], [B]
+  int *table_out, *new_ids;       // [B][width], [num_blocks]
+  int *counts;                    // {blocks held, pages moved}
+  int *moves;                     // [2][num_blocks / 2]
+  int B, width, bs_log2, num_blocks;
+};
+cudaError_t launch_kv_compact(const Pages &pages, const CompactParams &p, int num_sms, cudaStream_t s);
+
 // ------------------------------------------------------------ attention
-struct Kv4Attn {
+struct KvAttn {
   const void *q;                  // [total_q][Hq][d]
   void *o;
   float *lse;                     // [Hq][total_q]
-  Kv4Store c;
+  KvStore c;
   const int *table;               // [B][width]
   const int *lens;                // [B]
   const int *cu_q;                // [B + 1] or null (one query a sequence)
   int B, Hq, group;               // group = Hq / Hk
   int total_q, max_q;
-  int max_k;                      // at most width blocks, and kKv4MaxKeys
+  int max_k;                      // at most width blocks, and kKvMaxKeys
   int width;
   float scale_log2;               // scale * 2^k_exp * log2(e)
   float v_mul;                    // 2^v_exp
   int causal;
 };
 // Sequences with at most `rows` rows (queries x group) go through
-// launch_kv4_attn's tile of that many rows, longer ones through
-// launch_kv4_many.  kv4_tile_rows: 8, 16 or 32, the smallest that holds the
+// launch_kv4_attn's (kv8) tile of that many rows, longer ones through
+// launch_kv4_many (kv8).  kv4_tile_rows: 8, 16 or 32, the smallest that holds the
 // longest sequence, else the smallest that holds one query; 0: none, either
 // because none does or because the other kernel is faster at so many keys (the
 // longest sequence's, times sequences and key heads).
-constexpr int kKv4MaxCtas = 304;   // two on each of 152 SMs
-constexpr int kKv4ManyCtas = 152;  // launch_kv4_many: one on each
-constexpr int kKv4ManyRows = 128;  // and tiles of that many rows, so group <= 128
+constexpr int kKvMaxCtas = 304;   // two on each of 152 SMs
+constexpr int kKvManyCtas = 152;  // launch_kv4_many: one on each
+constexpr int kKvManyRows = 128;  // and tiles of that many rows, so group <= 128
 // Keys of a sequence at most: the kernels count in 32 bits and look up to three
 // steps of 128 keys past the last one, and round up to whole steps.
-constexpr int kKv4MaxKeys = 2147483647 - 4095;
+constexpr int kKvMaxKeys = 2147483647 - 4095;
 int kv4_tile_rows(int group, int max_q, int d, long long keys);
+int kv8_tile_rows(int group, int max_q, int d);
 // What a call launches: `rows` of launch_kv4_attn's tile (0: not launched), the
 // CTAs of its clusters (0: none, the line of units) and in all; and the CTAs of
-// launch_kv4_many (0: not launched).  max_k as in Kv4Attn.
-struct Kv4Grid {
+// launch_kv4_many (0: not launched).  max_k as in KvAttn.
+struct KvGrid {
   int rows, cluster, ctas, many;
 };
-Kv4Grid kv4_grid(int B, int Hk, int group, int d, int max_q, int max_k, int num_sms);
-size_t kv4_workspace(int rows, int d);  // of either kernel, by its rows
-cudaError_t launch_kv4_attn(const Kv4Attn &p, const Kv4Grid &g, int dtype, float *ws,
+KvGrid kv4_grid(int B, int Hk, int group, int d, int max_q, int max_k, int num_sms);
+KvGrid kv8_grid(int B, int Hk, int group, int d, int max_q, int max_k, int num_sms);
+size_t kv_workspace(int rows, int d);  // of either kernel, by its rows
+cudaError_t launch_kv4_attn(const KvAttn &p, const KvGrid &g, int dtype, float *ws,
                             cudaStream_t s);
 // status: the device's status word; wait_limit_ns bounds its barrier waits;
 // skip_load: the test hook that leaves out a tile's values.
-cudaError_t launch_kv4_many(const Kv4Attn &p, const Kv4Grid &g, int dtype, float *ws,
+cudaError_t launch_kv8_attn(const KvAttn &p, const KvGrid &g, int dtype, float *ws,
+                            cudaStream_t s);
+cudaError_t launch_kv4_many(const KvAttn &p, const KvGrid &g, int dtype, float *ws,
+                            unsigned *status, unsigned long long wait_limit_ns, int skip_load,
+                            cudaStream_t s);
+cudaError_t launch_kv8_many(const KvAttn &p, const KvGrid &g, int dtype, float *ws,
                             unsigned *status, unsigned long long wait_limit_ns, int skip_load,
                             cudaStream_t s);
 

@@ -3,7 +3,8 @@
 The ``fa_*`` functions mirror the C entry points one to one and only marshal
 arguments.  ``attention``, ``attention_varlen``, ``attention_backward`` and the
 serving operators (``kv_plan``, ``rotary``, ``kv4_append``, ``kv4_gather``,
-``attention_kv4``) are convenience wrappers for torch tensors: they allocate
+``attention_kv4``, the same over 8 bits, ``kv_copy``, ``kv_fork``, ``kv_free``,
+``kv_compact``) are convenience wrappers for torch tensors: they allocate
 outputs and workspaces with torch (device memory is the only thing torch
 provides here) and call the C entry points.
 
@@ -39,7 +40,10 @@ EXPORTED = ("fa_fwd", "fa_fwd_host", "fa_fwd_status", "fa_status_string", "fa_ve
             "fa_fwd_varlen", "fa_bwd", "fa_bwd_workspace", "fa_fwd_staged",
             "fa_fwd_staged_workspace", "fa_bwd_varlen", "fa_bwd_varlen_workspace",
             "fa_kv_plan", "fa_rope_table", "fa_rope", "fa_kv4_append", "fa_kv4_gather",
-            "fa_fwd_kv4", "fa_fwd_kv4_workspace", "fa_fwd_kv4_schedule")
+            "fa_fwd_kv4", "fa_fwd_kv4_workspace", "fa_fwd_kv4_schedule",
+            "fa_kv8_append", "fa_kv8_gather", "fa_fwd_kv8", "fa_fwd_kv8_workspace",
+            "fa_fwd_kv8_schedule", "fa_kv_copy", "fa_kv_fork", "fa_kv_free", "fa_kv_compact",
+            "fa_kv_compact_workspace")
 
 _lib = None
 
@@ -125,6 +129,26 @@ def load(path: str | None = None):
     lib.fa_fwd_kv4_workspace.restype = ull
     lib.fa_fwd_kv4_schedule.argtypes = [i] * 9 + [ctypes.POINTER(i)] * 5
     lib.fa_fwd_kv4_schedule.restype = i
+    lib.fa_kv8_append.argtypes = [vp, vp, ll, ll, vp, i, vp, vp, vp, vp] + [i] * 5 + [vp]
+    lib.fa_kv8_append.restype = i
+    lib.fa_kv8_gather.argtypes = [vp, i] + [vp] * 6 + [i] * 5 + [vp]
+    lib.fa_kv8_gather.restype = i
+    lib.fa_fwd_kv8.argtypes = [vp] * 10 + [i] * 10 + [f] + [i] * 2 + [vp, ull, vp]
+    lib.fa_fwd_kv8.restype = i
+    lib.fa_fwd_kv8_workspace.argtypes = [i] * 5
+    lib.fa_fwd_kv8_workspace.restype = ull
+    lib.fa_fwd_kv8_schedule.argtypes = [i] * 9 + [ctypes.POINTER(i)] * 5
+    lib.fa_fwd_kv8_schedule.restype = i
+    lib.fa_kv_copy.argtypes = [vp, vp, i, vp, vp, vp, i, i, i, vp]
+    lib.fa_kv_copy.restype = i
+    lib.fa_kv_fork.argtypes = [vp] * 8 + [i] * 7 + [vp, vp, i, vp]
+    lib.fa_kv_fork.restype = i
+    lib.fa_kv_free.argtypes = [vp] * 5 + [i] * 4 + [vp]
+    lib.fa_kv_free.restype = i
+    lib.fa_kv_compact.argtypes = [vp] * 5 + [i] * 4 + [vp, vp, i, vp, ull, vp]
+    lib.fa_kv_compact.restype = i
+    lib.fa_kv_compact_workspace.argtypes = [i]
+    lib.fa_kv_compact_workspace.restype = ull
     if path is None:
         _lib = lib
     return lib
@@ -486,6 +510,82 @@ def fa_fwd_kv4_schedule(B, Hq, Hk, max_seqlen_q, max_seqlen_k, max_blocks, block
     return (st, *(x.value for x in r))
 
 
+def fa_kv8_append(k, v, k_stride, v_stride, slots, T, k_codes, k_scales, v_codes, v_scales,
+                  num_blocks, Hk, block_size, d, dtype, stream) -> int:
+    return load().fa_kv8_append(k, v, k_stride, v_stride, slots, T, k_codes, k_scales, v_codes,
+                                v_scales, num_blocks, Hk, block_size, d, dtype, stream)
+
+
+def fa_kv8_gather(slots, R, k_codes, k_scales, v_codes, v_scales, k_out, v_out, num_blocks, Hk,
+                  block_size, d, dtype, stream) -> int:
+    return load().fa_kv8_gather(slots, R, k_codes, k_scales, v_codes, v_scales, k_out, v_out,
+                                num_blocks, Hk, block_size, d, dtype, stream)
+
+
+def fa_fwd_kv8(q, o, lse, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens_k,
+               cu_seqlens_q, B, Hq, Hk, total_q, max_seqlen_q, max_seqlen_k, num_blocks,
+               block_size, max_blocks, d, scale, causal, dtype, workspace, workspace_bytes,
+               stream) -> int:
+    return load().fa_fwd_kv8(q, o, lse, k_codes, k_scales, v_codes, v_scales, block_table,
+                             seq_lens_k, cu_seqlens_q, B, Hq, Hk, total_q, max_seqlen_q,
+                             max_seqlen_k, num_blocks, block_size, max_blocks, d, scale, causal,
+                             dtype, workspace, workspace_bytes, stream)
+
+
+def fa_fwd_kv8_workspace(B, Hq, Hk, max_seqlen_q, d) -> int:
+    return load().fa_fwd_kv8_workspace(B, Hq, Hk, max_seqlen_q, d)
+
+
+def fa_fwd_kv8_schedule(B, Hq, Hk, max_seqlen_q, max_seqlen_k, max_blocks, block_size, d, num_sms):
+    """fa_fwd_kv4_schedule's values for fa_fwd_kv8 (host-only)."""
+    r = [ctypes.c_int(0) for _ in range(5)]
+    st = load().fa_fwd_kv8_schedule(int(B), int(Hq), int(Hk), int(max_seqlen_q), int(max_seqlen_k),
+                                    int(max_blocks), int(block_size), int(d), int(num_sms),
+                                    *map(ctypes.byref, r))
+    return (st, *(x.value for x in r))
+
+
+def _pages(arrays, page_bytes):
+    """Host arrays of device pointers and page sizes, as the C entry points take them."""
+    n = len(page_bytes)
+    return ((ctypes.c_void_p * max(n, 1))(*arrays), (ctypes.c_ulonglong * max(n, 1))(*page_bytes), n)
+
+
+def fa_kv_copy(src, dst, n, from_arrays, to_arrays, page_bytes, from_blocks, to_blocks,
+               stream) -> int:
+    """from_arrays, to_arrays: lists of device addresses; page_bytes: a list of sizes."""
+    f, b, num = _pages(from_arrays, page_bytes)
+    t, _, _ = _pages(to_arrays, page_bytes)
+    return load().fa_kv_copy(src, dst, n, f, t, b, num, from_blocks, to_blocks, stream)
+
+
+def fa_kv_fork(block_table, seq_lens, parents, free_blocks, free_head, table_out, lens_out, counts,
+               B, n, max_blocks, block_size, num_free, num_blocks, parents_end, arrays, page_bytes,
+               stream) -> int:
+    a, b, num = _pages(arrays, page_bytes)
+    return load().fa_kv_fork(block_table, seq_lens, parents, free_blocks, free_head, table_out,
+                             lens_out, counts, B, n, max_blocks, block_size, num_free, num_blocks,
+                             int(parents_end), a, b, num, stream)
+
+
+def fa_kv_free(block_table, seq_lens, ended, free_blocks, free_head, B, max_blocks, block_size,
+               num_blocks, stream) -> int:
+    return load().fa_kv_free(block_table, seq_lens, ended, free_blocks, free_head, B, max_blocks,
+                             block_size, num_blocks, stream)
+
+
+def fa_kv_compact(block_table, seq_lens, table_out, new_ids, counts, B, max_blocks, block_size,
+                  num_blocks, arrays, page_bytes, workspace, workspace_bytes, stream) -> int:
+    a, b, num = _pages(arrays, page_bytes)
+    return load().fa_kv_compact(block_table, seq_lens, table_out, new_ids, counts, B, max_blocks,
+                                block_size, num_blocks, a, b, num, workspace,
+                                int(workspace_bytes), stream)
+
+
+def fa_kv_compact_workspace(num_blocks) -> int:
+    return load().fa_kv_compact_workspace(num_blocks)
+
+
 # The wrappers below run once or more in every layer of every step of a server,
 # where a launch takes about 3 us of host time.  Their checks, allocations and
 # calls of the C entry points are compiled (csrc/bind/fa_torch.cpp): 2.5 to 6.5 us a
@@ -510,7 +610,10 @@ def _bind():
     lib = load()
     mod.bind(*[ctypes.cast(f, ctypes.c_void_p).value
                for f in (lib.fa_kv_plan, lib.fa_rope, lib.fa_kv4_append, lib.fa_kv4_gather,
-                         lib.fa_fwd_kv4, lib.fa_fwd_kv4_workspace)])
+                         lib.fa_fwd_kv4, lib.fa_fwd_kv4_workspace, lib.fa_kv8_append,
+                         lib.fa_kv8_gather, lib.fa_fwd_kv8, lib.fa_fwd_kv8_workspace,
+                         lib.fa_kv_copy, lib.fa_kv_fork, lib.fa_kv_free, lib.fa_kv_compact,
+                         lib.fa_kv_compact_workspace)])
     _torch = mod
     return mod
 
@@ -615,3 +718,94 @@ def attention_kv4(q, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens
     return _done((_torch or _bind()).attention_kv4(
         q, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens_k, max_seqlen_k, cu_seqlens_q,
         max_seqlen_q, scale, causal, k_exp, v_exp, (out, lse), workspace, stream), "fa_fwd_kv4")
+
+
+def kv8_cache(num_blocks: int, Hk: int, block_size: int, d: int, device="cuda"):
+    """A zeroed 8-bit cache: (k_codes, k_scales, v_codes, v_scales), codes
+    float8_e4m3fn [num_blocks, Hk, block_size, d] and scales float32 [num_blocks, Hk]."""
+    import torch
+    return tuple(x for _ in "kv" for x in (
+        torch.zeros((num_blocks, Hk, block_size, d), dtype=torch.float8_e4m3fn, device=device),
+        torch.zeros((num_blocks, Hk), dtype=torch.float32, device=device)))
+
+
+def kv8_append(k, v, slots, k_codes, k_scales, v_codes, v_scales, stream=None):
+    """Write rows k, v [T, Hk, d] (bf16, fp16 or fp32; rows of any stride, e.g.
+    slices of a fused projection) into the 8-bit cache at slots int64 [T] (-1
+    skips a row); the rows of a block follow one another, as kv_plan deals them.
+    A block's scale grows with its largest element, and what it held keeps its
+    values.  Raises FaError on failure."""
+    _done((_torch or _bind()).kv8_append(k, v, slots, k_codes, k_scales, v_codes, v_scales, stream),
+          "fa_kv8_append")
+
+
+def kv8_gather(slots, k_codes, k_scales, v_codes, v_scales, dtype=None, out=None, stream=None):
+    """Rows of the 8-bit cache at slots int64 [R] (-1 reads zeros) as (k, v),
+    each [R, Hk, d] of `dtype` (default bf16); out: those two tensors, to write
+    to.  Raises FaError on failure."""
+    return _done((_torch or _bind()).kv8_gather(slots, k_codes, k_scales, v_codes, v_scales, dtype,
+                                                out if out is None else tuple(out), stream),
+                 "fa_kv8_gather")
+
+
+def attention_kv8(q, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens_k,
+                  max_seqlen_k: int, cu_seqlens_q=None, max_seqlen_q: int = 1,
+                  scale: float | None = None, causal: bool = True, out=None, lse=None,
+                  workspace=None, stream=None):
+    """Attention of q [total_q, Hq, d] (bf16 or fp16) over the 8-bit paged cache,
+    with attention_kv4's arguments but for the exponents.  Returns (o
+    [total_q, Hq, d], lse [Hq, total_q]).  Raises FaError on failure."""
+    return _done((_torch or _bind()).attention_kv8(
+        q, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens_k, max_seqlen_k, cu_seqlens_q,
+        max_seqlen_q, scale, causal, (out, lse), workspace, stream), "fa_fwd_kv8")
+
+
+def kv_copy(src, dst, caches, to=None, stream=None):
+    """Copy page src[i] to page dst[i] (int32 [n] each; ids outside the cache skip
+    a pair) of every array in caches, contiguous tensors [num_blocks, ...] such as
+    those of kv4_cache() or kv8_cache(), of all layers; to: arrays of another cache
+    with the same pages, to write to.  Pages written differ, from one another and
+    from those read.  Raises FaError on failure."""
+    _done((_torch or _bind()).kv_copy(src, dst, tuple(caches), to if to is None else tuple(to),
+                                      stream), "fa_kv_copy")
+
+
+def kv_fork(block_table, seq_lens, parents, free_blocks, block_size: int, caches=(),
+            num_blocks: int | None = None, free_head=None, parents_end: bool = False, out=None,
+            stream=None):
+    """Requests begun from others' caches: child i continues row parents[i] (int32
+    [n]) of block_table [B, max_blocks] at its length; it shares the full blocks and
+    gets a copy of the last, partly filled one in a block from free_blocks (with
+    parents_end, a parent's first child keeps that block instead).  caches: the
+    arrays to copy in (kv_copy's).  Returns (block_table [n, max_blocks], seq_lens
+    [n], counts [2]: blocks needed, entries of free_blocks used up); out: those
+    three tensors, to write to.  Raises FaError on failure."""
+    return _done((_torch or _bind()).kv_fork(block_table, seq_lens, parents, free_blocks, block_size,
+                                             tuple(caches), num_blocks, free_head, parents_end,
+                                             out if out is None else tuple(out), stream),
+                 "fa_kv_fork")
+
+
+def kv_free(block_table, seq_lens, num_blocks: int, block_size: int, ended=None, out=None,
+            stream=None):
+    """The blocks that no row of block_table holds, for kv_plan and kv_fork: returns
+    (free_blocks int32 [num_blocks]: -1 for every block held, then the others'
+    ids, ascending; free_head int32 [1]); out: those two tensors, to write to.
+    ended: bool [B], rows that hold nothing any more; their seq_lens become 0.
+    Raises FaError on failure."""
+    return _done((_torch or _bind()).kv_free(block_table, seq_lens, num_blocks, block_size, ended,
+                                             out if out is None else tuple(out), stream),
+                 "fa_kv_free")
+
+
+def kv_compact(block_table, seq_lens, caches, block_size: int, num_blocks: int | None = None,
+               out=None, workspace=None, stream=None):
+    """Bring the blocks that rows hold to the front of the cache: moves their pages
+    in every array of caches (kv_copy's) and returns (block_table with the new ids,
+    new_ids int32 [num_blocks]: -1 for blocks not held, counts [2]: blocks held,
+    pages moved); out: those three tensors, to write to (block_table itself may be
+    one).  The workspace (fa_kv_compact_workspace bytes) is allocated with torch
+    unless given.  Raises FaError on failure."""
+    return _done((_torch or _bind()).kv_compact(block_table, seq_lens, tuple(caches), num_blocks,
+                                                block_size, out if out is None else tuple(out),
+                                                workspace, stream), "fa_kv_compact")

@@ -326,13 +326,15 @@ FA_API unsigned long long fa_bwd_varlen_workspace(int B, int H, int total_q, int
  * Serving: what a decoding server runs around the attention itself, in the
  * order of one step: block tables and slot maps of a paged cache
  * (fa_kv_plan), rotary positions on queries and keys (fa_rope), the new keys
- * and values into a cache held in 4 bits (fa_kv4_append), and attention of the
- * new queries over that cache (fa_fwd_kv4).  The pages have no counterpart to
+ * and values into a cache held in 4 bits or 8 (fa_kv4_append, fa_kv8_append), and
+ * attention of the new queries over that cache (fa_fwd_kv4, fa_fwd_kv8); and
+ * between steps the pages of either cache, forked, collected and moved
+ * (fa_kv_fork, fa_kv_free, fa_kv_compact, fa_kv_copy).  The pages have no counterpart to
  * these; conventions (ownership, streams, errors) are those above, every array
  * lies in device memory unless it says host, and buffers that a call writes
  * overlap none that it reads.  All of them can be captured into a CUDA graph
- * once each has been called on the device (fa_fwd_kv4 and fa_fwd share the
- * status word that the first call makes).
+ * once each has been called on the device (fa_fwd_kv4, fa_fwd_kv8 and fa_fwd share
+ * the status word that the first call makes).
  *
  * The 4-bit cache: num_blocks blocks of block_size tokens (16, 32, 64 or 128)
  * for each of Hk key heads; four arrays, all contiguous and 16-byte aligned,
@@ -533,6 +535,168 @@ FA_API int fa_fwd_kv4_schedule(int B, int Hq, int Hk, int max_seqlen_q, int max_
                         int max_blocks, int block_size, int d, int num_sms, int *max_keys,
                         int *tile_rows, int *cluster, int *ctas, int *many_ctas);
 
+/* ------------------------------------------------------------------------
+ * The 8-bit cache: blocks as above; four contiguous arrays,
+ *   k_codes, v_codes    e4m3 [num_blocks, Hk, block_size, d], 32-byte aligned;
+ *   k_scales, v_scales  float [num_blocks, Hk]: one scale for the block's tokens of
+ *                       a key head.
+ * An element is code * scale; 8 bits an element and 32 a block and head.  Scales are
+ * positive numbers; fa_kv8_append stores powers of two, 2^-40 .. 2^40.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * fa_kv8_append — T rows of keys and values into the 8-bit cache.
+ *
+ * k, v     [T, Hk, d], rows k_stride and v_stride elements apart (at least
+ *          Hk*d; 16-byte aligned rows), bf16, fp16 or fp32.
+ * slots    int64 [T]; a slot outside [0, num_blocks * block_size) skips its
+ *          row.  Slots must differ, and the rows of one block follow one another
+ *          (skipped rows may lie between), as fa_kv_plan's do: else a block's scale
+ *          may be that of some of its rows, and its values are unspecified.
+ * For every block and key head that the call writes to, with a the largest finite
+ * size among the elements written there and e the least integer in -40 .. 40 with
+ * a <= 448 * 2^e: the scale becomes 2^e if the block's first token is among them (what
+ * the block held counts no more), else the larger of 2^e and what it was (one that is
+ * not a positive number counts as 0, and so do the block's values).  Codes are
+ * e4m3(x / scale), rounded to nearest, ties to even, saturating; NaNs are stored as
+ * +448 times the scale, no code is ever stored as NaN.  Where the scale has grown, the
+ * block's tokens ahead of the first one written keep their values: their codes become
+ * e4m3(code * old / new), which is exact but for numbers that become smaller than
+ * 2^-6 of the new scale; tokens behind it are what a sequence has not reached and are
+ * left as codes.
+ * d a multiple of 16 up to 256 (else FA_ERR_UNSUPPORTED).
+ */
+FA_API int fa_kv8_append(const void *k, const void *v, long long k_stride, long long v_stride,
+                  const long long *slots, int T, void *k_codes, float *k_scales, void *v_codes,
+                  float *v_scales, int num_blocks, int Hk, int block_size, int d, int dtype,
+                  void *stream);
+
+/*
+ * fa_kv8_gather — R rows of the 8-bit cache as bf16, fp16 or fp32; slots, k_out and
+ * v_out as for fa_kv4_gather.  code * scale is rounded once, and exact with scales
+ * that are powers of two unless it leaves the type's range.
+ */
+FA_API int fa_kv8_gather(const long long *slots, int R, const void *k_codes, const float *k_scales,
+                  const void *v_codes, const float *v_scales, void *k_out, void *v_out,
+                  int num_blocks, int Hk, int block_size, int d, int dtype, void *stream);
+
+/*
+ * fa_fwd_kv8 — attention of new queries over the 8-bit paged cache: fa_fwd_kv4's
+ * arguments without the exponents, its rules and its workspace's (fa_fwd_kv8_workspace
+ * bytes).  Queries and weights are rounded as there, codes are exact in the products,
+ * and the scales are applied in fp32; a weight is rounded relative to the largest
+ * weight times value scale of its row, so that blocks of any scales may meet in a
+ * sequence.  Scales of values count as the nearest in 2^-40 .. 2^40, a key's scale that
+ * is not positive as 0.  A NaN among the codes of a key shows in the rows that see it;
+ * one among those of a value in every query of its sequence (fa_kv8_append stores
+ * none).  Codes and scales of tokens that no row sees may be anything.
+ * The kernel for few rows holds 8, 16 or, at d = 64, 32; the other takes the longer
+ * sequences.
+ */
+FA_API int fa_fwd_kv8(const void *q, void *o, float *lse, const void *k_codes, const float *k_scales,
+               const void *v_codes, const float *v_scales, const int *block_table,
+               const int *seq_lens_k, const int *cu_seqlens_q, int B, int Hq, int Hk, int total_q,
+               int max_seqlen_q, int max_seqlen_k, int num_blocks, int block_size,
+               int max_blocks, int d, float scale, int causal, int dtype, void *workspace,
+               unsigned long long workspace_bytes, void *stream);
+
+/* As fa_fwd_kv4_workspace and fa_fwd_kv4_schedule, of fa_fwd_kv8. */
+FA_API unsigned long long fa_fwd_kv8_workspace(int B, int Hq, int Hk, int max_seqlen_q, int d);
+FA_API int fa_fwd_kv8_schedule(int B, int Hq, int Hk, int max_seqlen_q, int max_seqlen_k,
+                        int max_blocks, int block_size, int d, int num_sms, int *max_keys,
+                        int *tile_rows, int *cluster, int *ctas, int *many_ctas);
+
+/* ------------------------------------------------------------------------
+ * Pages: what becomes of a cache's blocks between steps.  Which blocks are held
+ * stands in the block tables alone: row b of block_table [B, max_blocks] holds its
+ * first ceil(seq_lens[b] / block_size) entries (as many as there are; entries outside
+ * [0, num_blocks) hold nothing, lengths below zero count as 0), rows may share blocks,
+ * and a request that ends gives its length up.  Nothing counts references, and every
+ * call is a function of its inputs.
+ *
+ * The calls that move data take the arrays of a cache, of all layers that share the
+ * tables: arrays, page_bytes: host arrays of num_arrays device pointers and page
+ * sizes (1 .. 2^31 - 1 bytes), each array being num_blocks contiguous pages; up to 256
+ * (more: FA_ERR_UNSUPPORTED), which overlap neither one another nor the call's other
+ * buffers.  So the four arrays of a 4-bit or an 8-bit cache, whose first dimension is
+ * num_blocks, or any others.  Pages of whole 16-byte units, so aligned, are copied
+ * faster.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * fa_kv_copy — page src[i] of every array in `from` to page dst[i] of its counterpart
+ * in `to`, i < n; from and to may be the same arrays, or of two caches (from_blocks
+ * and to_blocks pages).  src, dst: int32 [n]; a pair with an index outside its cache
+ * is skipped.  Pages written differ from one another and, in one cache, from those
+ * read.
+ */
+FA_API int fa_kv_copy(const int *src, const int *dst, int n, const void *const *from, void *const *to,
+               const unsigned long long *page_bytes, int num_arrays, int from_blocks,
+               int to_blocks, void *stream);
+
+/*
+ * fa_kv_fork — requests begun from others' caches: several answers to one prompt, the
+ * next beams of a search.
+ *
+ * parents      int32 [n]: child i continues row parents[i] of block_table; one outside
+ *              [0, B) makes an empty child.  The same parent may come any number of times.
+ * table_out    int32 [n, max_blocks], lens_out int32 [n], out: a child shares its
+ *              parent's full blocks and has a copy of the last, partly filled one in a
+ *              block of its own, taken from free_blocks in the order of the children;
+ *              the rest of a row is -1.  Lengths are the parents', at most
+ *              max_blocks * block_size.
+ * free_blocks, free_head, num_free  as for fa_kv_plan; read, not advanced.
+ * parents_end  1: the parents do not go on; the first child of each keeps its last
+ *              block, without a copy.
+ * counts       int32 [2], out: blocks needed; entries of free_blocks used up
+ *              (free_head for the next call, num_free at most).
+ * Where the list runs out, or holds an id outside [0, num_blocks), the child's last
+ * entry is -1.  A parent's last entry outside the cache makes its children's -1.
+ * B and n 1 .. 65535; max_blocks * block_size <= 2^31 - 1.  num_arrays may be 0: tables
+ * alone.
+ */
+FA_API int fa_kv_fork(const int *block_table, const int *seq_lens, const int *parents,
+               const int *free_blocks, const int *free_head, int *table_out, int *lens_out,
+               int *counts, int B, int n, int max_blocks, int block_size, int num_free,
+               int num_blocks, int parents_end, void *const *arrays,
+               const unsigned long long *page_bytes, int num_arrays, void *stream);
+
+/*
+ * fa_kv_free — the blocks that no row holds: requests that end give theirs back, but
+ * for those that others share.
+ *
+ * seq_lens     int32 [B], in and out: of the rows with ended[b] != 0 (bytes, or NULL for
+ *              none) set to 0.
+ * free_blocks  int32 [num_blocks], out: -1 for every block held, then the ids of the
+ *              others, ascending.  free_head: int32, out: how many are held.  The two
+ *              are what fa_kv_plan and fa_kv_fork take, num_free = num_blocks.
+ * B 1 .. 65535; num_blocks up to 2^23 (else FA_ERR_UNSUPPORTED);
+ * max_blocks * block_size <= 2^31 - 1.
+ */
+FA_API int fa_kv_free(const int *block_table, int *seq_lens, const unsigned char *ended,
+               int *free_blocks, int *free_head, int B, int max_blocks, int block_size,
+               int num_blocks, void *stream);
+
+/*
+ * fa_kv_compact — the blocks held, brought to the front of the cache: with L of them,
+ * the k-th held id from L on moves to the k-th id below L that is not held, pages and
+ * tables.  What lies behind the first L pages can be given back; the pages moved from
+ * stay as they were.
+ *
+ * table_out    int32 [B, max_blocks], out: block_table (which it may be) with the new
+ *              ids, -1 behind a row's blocks and for entries outside the cache.
+ * new_ids      int32 [num_blocks], out: of each block, -1 for those not held.
+ * counts       int32 [2], out: blocks held, pages moved.
+ * workspace    fa_kv_compact_workspace(num_blocks) bytes, 4-byte aligned, whatever they
+ *              hold.  Calls that share it must not overlap on the GPU.
+ * Sizes as for fa_kv_free; num_arrays may be 0: tables alone.
+ */
+FA_API int fa_kv_compact(const int *block_table, const int *seq_lens, int *table_out, int *new_ids,
+                  int *counts, int B, int max_blocks, int block_size, int num_blocks,
+                  void *const *arrays, const unsigned long long *page_bytes, int num_arrays,
+                  void *workspace, unsigned long long workspace_bytes, void *stream);
+FA_API unsigned long long fa_kv_compact_workspace(int num_blocks);
+
 /*
  * fa_fwd_host — the same forward on HOST buffers.
  *
@@ -578,7 +742,7 @@ FA_API int fa_version(void);
 /*
  * fa_set_test_hooks — testing aid, process-wide.
  * skip_v_load != 0 makes the next launches of the tensor-core kernels (of
- * fa_fwd_kv4, the one for many queries) skip the first V-tile load, so the MMA issuer's bounded wait runs out and the kernel
+ * fa_fwd_kv4 and fa_fwd_kv8, the one for many queries) skip the first V-tile load, so the MMA issuer's bounded wait runs out and the kernel
  * returns through its error path (status bit 8 plus the role bits).
  * wait_limit_ns sets the bounded-wait limit in nanoseconds (0 = default,
  * 2e9).  Returns FA_OK.
