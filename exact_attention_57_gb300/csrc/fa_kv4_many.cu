@@ -24,7 +24,7 @@ namespace {
 template <int D_>
 struct Many4 {
   static constexpr int D = D_;
-  static constexpr bool kBlockScales = false;
+  static constexpr bool kBlockScales = false, kStreams = false;
 
   struct Row {
     uint4 c[D / 32];

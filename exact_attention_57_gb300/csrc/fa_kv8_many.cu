@@ -11,16 +11,58 @@ namespace {
 template <int D_>
 struct Many8 {
   static constexpr int D = D_;
-  static constexpr bool kBlockScales = true;
+  static constexpr bool kBlockScales = true, kStreams = true;
 
+  // Lane l takes 16 codes of every kRows-th token, from the one l / kLanes on, so that
+  // a load of the warp covers whole rows.
+  static constexpr int kLanes = D / 16, kRows = 32 / kLanes, kAt = kLanes;
   struct Row {
-    uint4 c[D / 16];
+    uint4 c[kAt];
     float ks, vs;
 
-    __device__ __forceinline__ void load(const uint8_t *codes, const uint8_t *, long long row) {
-      const uint4 *src = reinterpret_cast<const uint4 *>(codes + row * D);
+    // The codes of one step: tokens 0 .. 15 and 16 .. 31 lie in one block each.
+    struct From {
+      const uint8_t *half[2];
+      unsigned good;  // tokens that there are
+      __device__ __forceinline__ From(const uint8_t *codes, long long row)
+          : good(__ballot_sync(~0u, row >= 0) >> ((threadIdx.x & 31) / kLanes)) {
+        const int lane = threadIdx.x & 31;
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) c[i] = __ldg(src + i);
+        for (int n = 0; n < 2; ++n)
+          half[n] = codes + (__shfl_sync(~0u, row, 16 * n) + lane / kLanes) * D + lane % kLanes * 16;
+      }
+      __device__ __forceinline__ uint4 piece(int i) const {
+        constexpr int kHalf = kAt / 2;
+        return good >> (i * kRows) & 1
+                   ? __ldg(reinterpret_cast<const uint4 *>(half[i / kHalf] + i % kHalf * kRows * D))
+                   : make_uint4(0, 0, 0, 0);
+      }
+    };
+    __device__ __forceinline__ void begin(const uint8_t *codes, long long row) {
+      const From from(codes, row);
+#pragma unroll
+      for (int i = 0; i < kAt; ++i) c[i] = from.piece(i);
+    }
+    // 8 codes make a unit.  The lanes of a row's second half store their units in the
+    // other order, so that eight lanes at a time meet every bank once.
+    __device__ __forceinline__ void stream(const uint8_t *codes, long long next, uint8_t *tile,
+                                           int chunk) {
+      const From from(codes, next);
+      const int lane = threadIdx.x & 31, u = 2 * (lane % kLanes);
+      const bool swap = u >= 8;
+      uint8_t *to = tile + (lane / kLanes) * 128 + (u >> 3) * chunk;
+#pragma unroll
+      for (int i = 0; i < kAt; ++i) {
+        const uint32_t w[4] = {swap ? c[i].z : c[i].x, swap ? c[i].w : c[i].y,
+                               swap ? c[i].x : c[i].z, swap ? c[i].y : c[i].w};
+        c[i] = from.piece(i);
+        const int low = (i * kRows + lane / kLanes) & 7;
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+          *reinterpret_cast<uint4 *>(to + i * kRows * 128 + ((((u + (n != swap)) & 7) ^ low) << 4)) =
+              make_uint4(e4m3x2_f16x2(w[2 * n]), e4m3x2_f16x2_hi(w[2 * n]),
+                         e4m3x2_f16x2(w[2 * n + 1]), e4m3x2_f16x2_hi(w[2 * n + 1]));
+      }
     }
     __device__ __forceinline__ void load_scales(const KvStore &p, long long row) {
       ks = vs = 1.f;  // of a page that is missing: its scores are masked
@@ -28,25 +70,10 @@ struct Many8 {
       ks = __ldg(reinterpret_cast<const float *>(p.k_scales) + (row >> p.bs_log2));
       vs = __ldg(reinterpret_cast<const float *>(p.v_scales) + (row >> p.bs_log2));
     }
-    __device__ __forceinline__ void store_scales(float *to) const {
+    __device__ __forceinline__ float4 scales() const {
       BlockScale s;
       s.set(ks, vs);
-      to[0] = s.k;
-      to[8] = s.v_log;
-      to[16] = s.v_inv;
-    }
-    // 8 codes make a unit.
-    template <typename At>
-    __device__ __forceinline__ void expand(bool valid, At at) const {
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        const uint32_t w[4] = {valid ? c[i].x : 0u, valid ? c[i].y : 0u, valid ? c[i].z : 0u,
-                               valid ? c[i].w : 0u};
-#pragma unroll
-        for (int y = 0; y < 2; ++y)
-          *at(2 * i + y) = make_uint4(e4m3x2_f16x2(w[2 * y]), e4m3x2_f16x2_hi(w[2 * y]),
-                                      e4m3x2_f16x2(w[2 * y + 1]), e4m3x2_f16x2_hi(w[2 * y + 1]));
-      }
+      return make_float4(s.k, s.v_log, s.v_inv, 0.f);
     }
   };
 };

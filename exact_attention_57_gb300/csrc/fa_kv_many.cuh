@@ -22,9 +22,11 @@
 //              fp16 times a power of two a row.
 //
 // A format F has D, kBlockScales (the scales of 16 keys are one number each, which
-// the softmax applies) and Row: load() of a token's codes, expand() to fp16 by
-// 16-byte units; with kBlockScales, load_scales() and store_scales() by the
-// threads of tokens 16 n.
+// the softmax applies), and Row, a thread's share of the codes of its warp's 32
+// tokens.  Without kStreams: load() of the thread's own token, expand() to fp16 by
+// 16-byte units.  With kStreams: begin() loads the first step's, stream() turns one
+// step's into fp16 and each register, once free, over to the next step's codes.  With
+// kBlockScales, load_scales() and scales() by the threads of tokens 16 n.
 //
 // Every wait is bounded; on expiry the CTA raises its abort flag, records the
 // role in the status word, drains its products, frees tensor memory and ends.
@@ -76,9 +78,9 @@ struct ManyCfg {
   // An exponent a row of the tiles in flight: Q of tile g is written when the
   // last S of tile g - 2 is complete, and with tiles of one step the softmax
   // may then still be at tile g - 4 (three score buffers).
-  static constexpr int QES = 6;
-  // Of 16 keys each, eight to a step: K's scale, log2 of V's, and its inverse.
-  static constexpr int SCALES = F::kBlockScales ? 3 * 8 * 4 : 0;
+  static constexpr int QES = 5;
+  // Of 16 keys each, eight to a step: K's scale, log2 of V's, its inverse, nothing.
+  static constexpr int SCALES = F::kBlockScales ? 8 * 16 : 0;
   static constexpr int OFF_SCALE = OFF_MASK + MASKS * 16;
   static constexpr int OFF_QE = OFF_SCALE + MASKS * SCALES;
   static constexpr int OFF_BAR = OFF_QE + QES * 128;
@@ -435,7 +437,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto load = [&](Row &x, long long row) {
       x.valid = row >= 0;
       x.past = past;
-      if (row >= 0) x.load(codes, scales, row);
+      if constexpr (!F::kStreams)
+        if (row >= 0) x.load(codes, scales, row);
       if constexpr (F::kBlockScales)
         if (!is_v && (r & 15) == 0) x.load_scales(p.c, row);
     };
@@ -468,6 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Row row;
     bool now = lookup();
     load(row, row_of());
+    if constexpr (F::kStreams) row.begin(codes, row_of());
     bool next = lookup();
     for (int step = 0, st = 0, ph = 0; now; ++step) {
       if (is_v && ctl.skip_load && step == 0) {  // test hook: the P V issuer's wait runs out
@@ -481,13 +485,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           reinterpret_cast<unsigned *>(smem + C::OFF_MASK)[(step % C::MASKS) * 4 + warp - 4] = bits;
         if constexpr (F::kBlockScales)
           if ((r & 15) == 0)
-            row.store_scales(reinterpret_cast<float *>(smem + C::OFF_SCALE +
-                                                       step % C::MASKS * C::SCALES) + r / 16);
+            reinterpret_cast<float4 *>(smem + C::OFF_SCALE +
+                                       step % C::MASKS * C::SCALES)[r / 16] = row.scales();
       }
-      row.expand(row.valid, [&](int unit) {
-        return reinterpret_cast<uint4 *>(tiles + st * C::TILE + (unit >> 3) * C::CHUNK + r * 128 +
-                                         (((unit & 7) ^ (r & 7)) << 4));
-      });
+      // unit u of a chunk of row y is at u ^ (y & 7)
+      uint8_t *tile = tiles + st * C::TILE;
+      if constexpr (F::kStreams)
+        row.stream(codes, next ? row_of() : -1, tile + (r & ~31) * 128, C::CHUNK);
+      else
+        row.expand(row.valid, [&](int unit) {
+          return reinterpret_cast<uint4 *>(tile + (unit >> 3) * C::CHUNK + r * 128 +
+                                           (((unit & 7) ^ (r & 7)) << 4));
+        });
       fence_proxy_async_smem();
       mbar_arrive(full + 8 * st);
       if (++st == stages) st = 0, ph ^= 1;
@@ -560,20 +569,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr float kSumLimit = 32768.f;
         bool with_max = __any_sync(~0u, m_used == -INFINITY), formed = false;
         float tsum = 0.f, wsum = 0.f;
-        float k_mul[8], v_log[8], v_inv[8];  // of 16 columns each
-        if constexpr (F::kBlockScales) {
-          const float4 *from = reinterpret_cast<const float4 *>(smem + C::OFF_SCALE +
-                                                                step % C::MASKS * C::SCALES);
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            reinterpret_cast<float4 *>(k_mul)[n] = from[n];
-            reinterpret_cast<float4 *>(v_log)[n] = from[2 + n];
-            reinterpret_cast<float4 *>(v_inv)[n] = from[4 + n];
-          }
-          // (positive, for the -inf of a masked score)
-#pragma unroll
-          for (int n = 0; n < 8; ++n) k_mul[n] = fmaxf(k_mul[n] * sl2, FLT_MIN);
-        }
+        // the scales of columns 16 n and on, K's a factor of the score (positive, for the
+        // -inf of a masked one)
+        auto scale_at = [&](int n) {
+          float4 x = reinterpret_cast<const float4 *>(smem + C::OFF_SCALE +
+                                                      step % C::MASKS * C::SCALES)[n];
+          x.x = fmaxf(x.x * sl2, FLT_MIN);
+          return x;
+        };
         for (;;) {
           if (with_max) {
             float part[8];
@@ -586,7 +589,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if constexpr (F::kBlockScales) {
 #pragma unroll
-              for (int n = 0; n < 8; ++n) part[n] = fmaf(part[n], k_mul[n], v_log[n]);
+              for (int n = 0; n < 8; ++n) {
+                const float4 x = scale_at(n);
+                part[n] = fmaf(part[n], x.x, x.y);
+              }
             }
             const float mx = max3f(max3f(part[0], part[1], part[2]),
                                    max3f(part[3], part[4], part[5]), fmaxf(part[6], part[7]));
@@ -632,6 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float off = m_used == -INFINITY ? 0.f : -m_used;
           uint64_t sl2_2 = pk2(sl2, sl2), nm_2 = pk2(off, off);
           uint64_t acc[2] = {0ull, 0ull};
+          float4 scale = {};
           if constexpr (F::kBlockScales) tsum = wsum = 0.f;
 #pragma unroll
           for (int blk = 0; blk < 2; ++blk) {
@@ -640,9 +647,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int n = 0; n < 32; ++n) {
               const int c0 = 2 * (blk * 32 + n);
               if (F::kBlockScales && n % 8 == 0) {
-                const float add = v_log[c0 / 16] + off;
-                sl2_2 = pk2(k_mul[c0 / 16], k_mul[c0 / 16]);
-                nm_2 = pk2(add, add);
+                scale = scale_at(c0 / 16);
+                sl2_2 = pk2(scale.x, scale.x);
+                nm_2 = pk2(scale.y + off, scale.y + off);
                 acc[0] = acc[1] = 0ull;
               }
               float x0, x1;
@@ -654,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float a0, a1;
                 upk2(fadd2(acc[0], acc[1]), a0, a1);
                 tsum += a0 + a1;
-                wsum = fmaf(a0 + a1, v_inv[c0 / 16], wsum);
+                wsum = fmaf(a0 + a1, scale.z, wsum);
               }
             }
             tmem_st32(s_tm + blk * 32, pk);
