@@ -34,7 +34,7 @@ struct Cache4 {
   //   32 rows  (all 255 registers and some spilling: 260 bytes stored, 364 loaded)
   //            lead 3/4/6/8: 266/258/259/263, two CTAs of 4 warps 246, but 18 instead
   //            of 15 for one sequence of 4096; D = 64: 8 warps 109, twice 4 101
-  template <int NT>
+  template <int NT, int>
   struct Shape {
     static constexpr int kWarps = NT == 4 && D == 64 ? 4 : 8;
     static constexpr int kCtas = NT == 1 || D == 64 ? 2 : 1;

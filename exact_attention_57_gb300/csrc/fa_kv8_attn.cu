@@ -15,10 +15,20 @@ template <int D_>
 struct Cache8 {
   static constexpr int D = D_, KS = D / 16;
 
-  template <int NT>
+  // Warps of a CTA, resident CTAs, and the units that stand for a sequence's cost
+  // beside its keys, by rows (8 NT) and head dim; clusters of more than one CTA take 8
+  // warps (one sequence of 1023 keys 4.3 us, 4.7 with six).  Measured along the line, in
+  // us, at 64 sequences of up to 8192 keys and 8 key heads, D = 128 unless said:
+  //   8 rows   CTAs x warps: 1 x 8 113, 1 x 12 100, 1 x 16 106, 2 x 5 102, 2 x 6 97,
+  //            2 x 7 106 and 2 x 8 103 (registers spill); lead 2/3/4: 99/97/97;
+  //            D = 64: 2 x 8 57, 2 x 10 53, 2 x 12 54 (registers spill)
+  //   16 rows  (4 key heads) 1 x 8 67, 1 x 10 91 (registers spill)
+  //   32 rows  D = 64 alone, 1 x 8
+  template <int NT, int CL>
   struct Shape {
-    static constexpr int kWarps = 8;
-    static constexpr int kCtas = D == 64 && NT <= 2 ? 2 : 1;
+    static constexpr bool kLine = NT == 1 && CL < 2;
+    static constexpr int kWarps = !kLine ? 8 : D == 128 ? 6 : 10;
+    static constexpr int kCtas = kLine || (D == 64 && NT <= 2) ? 2 : 1;
     static constexpr int kLead = NT == 1 ? 3 : NT == 2 && D == 64 ? 4 : 6;
   };
 

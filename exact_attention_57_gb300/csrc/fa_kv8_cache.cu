@@ -12,9 +12,11 @@
 // of two for a scale costs no accuracy, both quotients are exact, and growing
 // re-rounds nothing but what becomes subnormal (below scale' * 2^-6).
 //
-// The rows of one block follow one another in a call (as fa_kv_plan deals them), so
-// one warp takes them all, for one key head and for K or V: two passes over a few
-// rows, the maximum and the codes, no communication between warps.
+// The rows of one block follow one another in a call (as fa_kv_plan deals them): a
+// run.  A team of bs / 16 warps takes a run for one key head and for K or V, a warp the
+// rows of 16 of the block's tokens, all loaded at once and kept in registers between
+// the maximum, which the team shares through shared memory, and the codes: each row is
+// read once, and with 4 KB in flight a warp.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -101,123 +103,138 @@ __device__ __forceinline__ float scale_for(float a) {
   return pow2(min(max(e, -kScaleExp), kScaleExp));
 }
 
-// One warp: the runs of rows of one block that begin among rows [t0, t0 + window),
-// one key head, K or V.  A run is the rows of a block that follow one another; rows
-// that are skipped do not end it.
-template <typename T>
-__device__ void append_runs(const T *x, long long stride, const long long *slots, long long t0,
-                            int window, int T_, const KvStore &c, int h, uint8_t *codes,
-                            float *scales) {
-  const int lane = threadIdx.x & 31;
+// Rows that a CTA looks through for runs that begin there, at most.
+constexpr int kWindow = 64;
+
+// The runs that begin among rows [window, window + the CTA's share), for one key head of
+// K or V.  Rows that are skipped do not end a run.  kSteps: rows of a warp by what it
+// loads at a time, 32 / (d / 8), at least ceil(16 / that).
+template <typename T, int kSteps>
+__global__ void __launch_bounds__(kThreads)
+    fa_kv8_append_kernel(const T *k, const T *v, long long k_stride, long long v_stride,
+                         const long long *slots, int T_, int window, const KvStore c) {
+  constexpr int kWarps = kThreads / 32;
+  __shared__ int s_row[kWarps][16];            // a warp's rows by the token in the block
+  __shared__ float s_top[2][kWarps];           // runs in turn
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int heads = 2 * c.Hk, hv = static_cast<int>(blockIdx.x % heads), h = hv / 2;
+  const bool is_v = hv & 1;
+  const T *x = is_v ? v : k;
+  const long long stride = is_v ? v_stride : k_stride;
+  uint8_t *codes = is_v ? c.v_codes : c.k_codes;
+  float *scales = reinterpret_cast<float *>(is_v ? c.v_scales : c.k_scales);
   const long long all = static_cast<long long>(c.num_blocks) << c.bs_log2;
   const int off_mask = (1 << c.bs_log2) - 1;
+  const int team_log2 = c.bs_log2 - 4, team = warp >> team_log2, teams = kWarps >> team_log2;
+  const int mate = warp - (team << team_log2);  // which 16 tokens of the block
   auto slot_at = [&](long long t) -> long long {
     const long long s = t >= 0 && t < T_ ? __ldg(slots + t) : -1;
     return s < all ? s : -1;
   };
-  // the block of each row, and of the last row that counts before the window
-  const long long mine = lane < window ? slot_at(t0 + lane) : -1;
-  const unsigned there = __ballot_sync(~0u, mine >= 0);
-  if (there == 0) return;
-  long long before = -1;
-  for (long long t = t0; t > 0; t -= 32) {
-    const long long s = slot_at(t - 32 + lane);
-    const unsigned some = __ballot_sync(~0u, s >= 0);
-    if (some) {
-      before = __shfl_sync(~0u, s, 31 - __clz(some)) >> c.bs_log2;
-      break;
-    }
-  }
-  const unsigned lower = there & ((1u << lane) - 1u);
-  const long long prev = __shfl_sync(~0u, mine, lower ? 31 - __clz(lower) : 0) >> c.bs_log2;
-  const bool leads = mine >= 0 && (mine >> c.bs_log2) != (lower ? prev : before);
-  unsigned leaders = __ballot_sync(~0u, leads);
-
   // a warp takes `per` rows at a time, d / 8 lanes each
   const int lanes = c.d / 8, per = 32 / lanes, sub = lane / lanes, col = (lane - sub * lanes) * 8;
   const T *src = x + static_cast<long long>(h) * c.d + col;
-  while (leaders) {
-    const int first = __ffs(leaders) - 1;
-    leaders &= leaders - 1;
-    const long long block = __shfl_sync(~0u, mine, first) >> c.bs_log2;
-    // f(row, slot) for each row of the run, by the lanes that have one
-    auto rows = [&](auto f) {
-      bool ends = false;
-      for (long long base = t0 + first; !ends && base < T_; base += 32) {
+  int runs = 0;  // begun in the window so far
+  int turn = 0;
+  const long long w0 = static_cast<long long>(blockIdx.x / heads) * window;
+  long long before = -1;  // the block of the last row that counts ahead of the rows at hand
+  for (int part = 0; part < window; part += 32) {
+    const long long t0 = w0 + part;
+    if (t0 >= T_) break;
+    const long long mine = lane < window - part ? slot_at(t0 + lane) : -1;
+    const unsigned there = __ballot_sync(~0u, mine >= 0);
+    if (there == 0) continue;
+    for (long long t = t0; before < 0 && t > 0; t -= 32) {
+      const long long s = slot_at(t - 32 + lane);
+      const unsigned some = __ballot_sync(~0u, s >= 0);
+      if (some) before = __shfl_sync(~0u, s, 31 - __clz(some)) >> c.bs_log2;
+    }
+    const unsigned lower = there & ((1u << lane) - 1u);
+    const long long prev = __shfl_sync(~0u, mine, lower ? 31 - __clz(lower) : 0) >> c.bs_log2;
+    const bool leads = mine >= 0 && (mine >> c.bs_log2) != (lower ? prev : before);
+    unsigned leaders = __ballot_sync(~0u, leads);
+    before = __shfl_sync(~0u, mine, 31 - __clz(there)) >> c.bs_log2;
+    while (leaders) {
+      const int first = __ffs(leaders) - 1;
+      leaders &= leaders - 1;
+      const long long block = __shfl_sync(~0u, mine, first) >> c.bs_log2;
+      if (runs++ % teams != team) continue;  // (the whole team)
+      // the run's rows among this warp's tokens, and its first token
+      if (lane < 16) s_row[warp][lane] = -1;
+      __syncwarp();
+      int low = off_mask;
+      for (long long base = t0 + first; base < T_; base += 32) {
         const long long s = slot_at(base + lane);
-        const bool other = s >= 0 && (s >> c.bs_log2) != block;
-        const unsigned stop = __ballot_sync(~0u, other);
-        ends = stop != 0;
-        const unsigned in = __ballot_sync(~0u, s >= 0) & (stop ? (stop & (0u - stop)) - 1u : ~0u);
-        if (in == 0) continue;
-        const int hi = 31 - __clz(in);
-#pragma unroll 4
-        for (int j = 0; j <= hi; j += per) {
-          const int row = j + sub;
-          const int off = static_cast<int>(__shfl_sync(~0u, s, row & 31)) & off_mask;
-          if (sub < per && row <= hi && (in >> row & 1)) f(base + row, off);
+        const unsigned stop = __ballot_sync(~0u, s >= 0 && (s >> c.bs_log2) != block);
+        const unsigned in = stop ? (stop & (0u - stop)) - 1u : ~0u;
+        if (s >= 0 && (in >> lane & 1)) {
+          const int off = static_cast<int>(s) & off_mask;
+          low = min(low, off);
+          if (off >> 4 == mate) s_row[warp][off & 15] = static_cast<int>(base + lane);
         }
+        if (stop) break;
       }
-    };
-    float top = 0.f;
-    int lowest = off_mask;
-    rows([&](long long t, int off) {
-      top = size_of<false>(load_eight(src + t * stride), top);
-      lowest = min(lowest, off);
-    });
-    for (int o = 16; o; o /= 2) {
-      top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-      lowest = min(lowest, __shfl_xor_sync(~0u, lowest, o));
-    }
-    if (top == INFINITY) {
-      top = 0.f;
-      rows([&](long long t, int) { top = size_of<true>(load_eight(src + t * stride), top); });
-      for (int o = 16; o; o /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    }
-    float *where = scales + block * c.Hk + h;
-    uint8_t *to = codes + (((block * c.Hk + h) << c.bs_log2) * c.d) + col;
-    const float fit = scale_for(top);
-    float scale = fit;
-    if (lowest > 0) {
+      __syncwarp();
+      Eight<T> e[kSteps];
+      int row[kSteps];
+#pragma unroll
+      for (int n = 0; n < kSteps; ++n) {
+        const int y = n * per + sub;
+        row[n] = sub < per && y < 16 ? s_row[warp][y] : -1;
+        if (row[n] >= 0) e[n] = load_eight(src + row[n] * stride);
+      }
+      float *where = scales + block * c.Hk + h;
       float old = *where;
-      old = old > 0.f && old < INFINITY ? old : 0.f;
-      scale = fmaxf(old, fit);
-      if (scale != old) {
-        const float by = __fdiv_rn(old, scale);
-        for (int off = sub; off < lowest; off += per) {
-          uint2 *p = reinterpret_cast<uint2 *>(to + static_cast<long long>(off) * c.d);
-          if (sub < per) *p = rescaled(*p, by);
+      float top = 0.f;
+#pragma unroll
+      for (int n = 0; n < kSteps; ++n)
+        if (row[n] >= 0) top = size_of<false>(e[n], top);
+      for (int o = 16; o; o /= 2) {
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+        low = min(low, __shfl_xor_sync(~0u, low, o));
+      }
+      float finite = top;
+      if (top == INFINITY) {
+        finite = 0.f;
+#pragma unroll
+        for (int n = 0; n < kSteps; ++n)
+          if (row[n] >= 0) finite = size_of<true>(e[n], finite);
+        for (int o = 16; o; o /= 2) finite = fmaxf(finite, __shfl_xor_sync(~0u, finite, o));
+      }
+      if (team_log2 > 0) {
+        if (lane == 0) s_top[turn][warp] = finite;
+        named_bar_sync(1 + team, 32 << team_log2);
+        for (int n = 0; n < 1 << team_log2; ++n)
+          finite = fmaxf(finite, s_top[turn][(team << team_log2) + n]);
+        turn ^= 1;
+      }
+      const float fit = scale_for(finite);
+      float scale = fit;
+      uint8_t *to = codes + ((((block * c.Hk + h) << c.bs_log2) + 16 * mate) * c.d) + col;
+      if (low > 0) {
+        old = old > 0.f && old < INFINITY ? old : 0.f;
+        scale = fmaxf(old, fit);
+        if (scale != old) {
+          const float by = __fdiv_rn(old, scale);
+          for (int y = sub; y < min(low - 16 * mate, 16); y += per) {
+            uint2 *p = reinterpret_cast<uint2 *>(to + y * c.d);
+            if (sub < per) *p = rescaled(*p, by);
+          }
         }
       }
+      const bool exact = (__float_as_uint(scale) & 0x7FFFFFu) == 0;  // (and not subnormal)
+      const float by = exact ? __frcp_rn(scale) : scale;
+#pragma unroll
+      for (int n = 0; n < kSteps; ++n)
+        if (row[n] >= 0)
+          *reinterpret_cast<uint2 *>(to + (n * per + sub) * c.d) = codes_of(e[n], by, exact);
+      // every warp of the team has read the old scale: one alone here, or the barrier
+      __syncwarp();
+      if (mate == 0 && lane == 0) *where = scale;
     }
-    const bool exact = (__float_as_uint(scale) & 0x7FFFFFu) == 0;  // (and not subnormal)
-    const float by = exact ? __frcp_rn(scale) : scale;
-    rows([&](long long t, int off) {
-      *reinterpret_cast<uint2 *>(to + static_cast<long long>(off) * c.d) =
-          codes_of(load_eight(src + t * stride), by, exact);
-    });
-    __syncwarp();  // (all lanes have read the old scale)
-    if (lane == 0) *where = scale;
   }
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-    fa_kv8_append_kernel(const T *k, const T *v, long long k_stride, long long v_stride,
-                         const long long *slots, int T_, int window, const KvStore c) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const long long id = static_cast<long long>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32;
-  const int heads = 2 * c.Hk;
-  const long long t0 = id / heads * window;
-  const int hv = static_cast<int>(id % heads), h = hv / 2;
-  if (t0 >= T_) return;
-  if (hv & 1)
-    append_runs(v, v_stride, slots, t0, window, T_, c, h, c.v_codes,
-                reinterpret_cast<float *>(c.v_scales));
-  else
-    append_runs(k, k_stride, slots, t0, window, T_, c, h, c.k_codes,
-                reinterpret_cast<float *>(c.k_scales));
 }
 
 // 16 elements from their codes and scale.
@@ -296,18 +313,28 @@ cudaError_t launch(void (*kern)(A...), long long threads, cudaStream_t s, A... a
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+template <typename T, int kSteps>
+cudaError_t append_steps(const void *k, const void *v, long long ks, long long vs,
+                         const long long *slots, int T_, const KvStore &c, cudaStream_t s) {
+  // Windows of as many rows as a CTA has teams where the rows are few (each may begin a
+  // run), of up to 64 where they are many.
+  const long long heads = 2LL * c.Hk;
+  int window = kThreads / 32 >> (c.bs_log2 - 4);
+  while (window < kWindow && (T_ + window - 1LL) / window * heads > 2048) window *= 2;
+  const long long ctas = (T_ + window - 1LL) / window * heads;
+  return launch<const T *, const T *, long long, long long, const long long *, int, int,
+                const KvStore>(fa_kv8_append_kernel<T, kSteps>, ctas * kThreads, s,
+                               static_cast<const T *>(k), static_cast<const T *>(v), ks, vs, slots,
+                               T_, window, c);
+}
+
 template <typename T>
 cudaError_t append(const void *k, const void *v, long long ks, long long vs,
                    const long long *slots, int T_, const KvStore &c, cudaStream_t s) {
-  // Rows a warp looks through for runs that begin there: one where the rows are few
-  // (each may begin one), up to 16 where they are many.
-  int window = 1;
-  const long long heads = 2LL * c.Hk;
-  while (window < 16 && (T_ + window - 1LL) / window * heads > 16384) window *= 2;
-  const long long warps = (T_ + window - 1LL) / window * heads;
-  return launch<const T *, const T *, long long, long long, const long long *, int, int,
-                const KvStore>(fa_kv8_append_kernel<T>, warps * 32, s, static_cast<const T *>(k),
-                               static_cast<const T *>(v), ks, vs, slots, T_, window, c);
+  const int per = 32 / (c.d / 8), steps = (16 + per - 1) / per;
+  if (steps <= 4) return append_steps<T, 4>(k, v, ks, vs, slots, T_, c, s);
+  if (steps <= 8) return append_steps<T, 8>(k, v, ks, vs, slots, T_, c, s);
+  return append_steps<T, 16>(k, v, ks, vs, slots, T_, c, s);
 }
 
 template <typename T>

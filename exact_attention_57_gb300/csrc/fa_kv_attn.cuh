@@ -35,7 +35,8 @@
 // memory.
 //
 // A format F has:
-//   D, Shape<NT>   head dim; kWarps, kCtas and kLead for tiles of 8 NT rows
+//   D, Shape<NT, CL>  head dim; kWarps, kCtas and kLead for tiles of 8 NT rows in
+//                  clusters of CL (0: along the line)
 //   Tile           16 tokens of one page as lane (r, c) holds them
 //   Lane           where that lane reads; load() fills a Tile
 //   scores()       S^T of a Tile, without its scale_of()
@@ -140,25 +141,25 @@ __device__ __forceinline__ float2 pair_f32(uint32_t x) {
   }
 }
 
-template <class F, int NT>
-using Shape = typename F::template Shape<NT>;
+template <class F, int NT, int CL>
+using Shape = typename F::template Shape<NT, CL>;
 
-template <class F, int NT>
+template <class F, int NT, int CL>
 constexpr int smem_bytes() {
   constexpr int D = F::D;
-  return (Shape<F, NT>::kWarps * (D + 4 + 2) + D + 4) * NT * 8 * 4;
+  return (Shape<F, NT, CL>::kWarps * (D + 4 + 2) + D + 4) * NT * 8 * 4;
 }
 
 // CL > 0: the CTAs of a cluster, as many, share one sequence and key head and join
 // their parts through shared memory; 0: every CTA takes its share of the line of
 // all units, and the join is another kernel's.
 template <typename T, class F, int NT, int CL>
-__global__ void __launch_bounds__(Shape<F, NT>::kWarps * 32, Shape<F, NT>::kCtas)
+__global__ void __launch_bounds__(Shape<F, NT, CL>::kWarps * 32, Shape<F, NT, CL>::kCtas)
     fa_kv_attn_kernel(const KvAttn p, float *ws) {
   constexpr int D = F::D;
   constexpr int R = NT * 8;              // rows of the tile
-  constexpr int kWarps = Shape<F, NT>::kWarps, kThreads = kWarps * 32, kUnit = kWarps * 16;
-  constexpr int kLead = Shape<F, NT>::kLead;
+  constexpr int kWarps = Shape<F, NT, CL>::kWarps, kThreads = kWarps * 32, kUnit = kWarps * 16;
+  constexpr int kLead = Shape<F, NT, CL>::kLead;
   constexpr int KS = D / 16;             // k steps of S^T, m tiles of O^T
   constexpr int LD = D + 4;
   extern __shared__ float smem[];
@@ -476,12 +477,12 @@ __global__ void __launch_bounds__(Shape<F, NT>::kWarps * 32, Shape<F, NT>::kCtas
 template <typename T, class F, int NT, int CL>
 cudaError_t launch_kernel(const KvAttn &p, float *ws, int ctas, cudaStream_t s) {
   static std::atomic<unsigned long long> attr_done{0};
-  constexpr int smem = smem_bytes<F, NT>();
+  constexpr int smem = smem_bytes<F, NT, CL>();
   cudaError_t e = smem_attr_once(fa_kv_attn_kernel<T, F, NT, CL>, smem, &attr_done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-  cfg.blockDim = dim3(Shape<F, NT>::kWarps * 32);
+  cfg.blockDim = dim3(Shape<F, NT, CL>::kWarps * 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -513,24 +514,40 @@ cudaError_t launch(const KvAttn &p, const KvGrid &g, float *ws, cudaStream_t s) 
   return launch_kernel<T, F, NT, 0>(p, ws, g.ctas, s);
 }
 
-// The grid for `heads` sequences and key heads with up to max_k keys.
+// Units of a sequence of up to max_k keys.
+template <class S>
+long long units_for(int max_k) {
+  constexpr int kUnit = S::kWarps * 16;
+  return max_k < kUnit ? 1 : (static_cast<long long>(max_k) + kUnit - 1) / kUnit;
+}
+
+// A cluster of CL CTAs for each of `heads` sequences and key heads, if one wave holds
+// them and that leaves a CTA at most kClusterUnits units: one launch.
+template <class F, int NT, int CL>
+bool cluster_grid(long long heads, int max_k, int num_sms, KvGrid *g) {
+  using S = Shape<F, NT, CL>;
+  if (heads * CL > static_cast<long long>(num_sms) * S::kCtas ||
+      units_for<S>(max_k) > CL * kClusterUnits)
+    return false;
+  g->cluster = CL;
+  g->ctas = static_cast<int>(heads * CL);
+  return true;
+}
+
+// The grid for `heads` sequences and key heads with up to max_k keys: the largest
+// cluster that fits, else one resident wave, no more CTAs than there can be units.
 template <class F, int NT>
 void shape_grid(long long heads, int max_k, int num_sms, KvGrid *g) {
-  constexpr int kUnit = Shape<F, NT>::kWarps * 16;
-  const long long wave = static_cast<long long>(num_sms) * Shape<F, NT>::kCtas;
-  const long long units = max_k < kUnit ? 1 : (static_cast<long long>(max_k) + kUnit - 1) / kUnit;
-  if (NT <= 2) {
-    // the largest cluster of which one wave holds one for every sequence and key
-    // head, if that leaves a CTA at most kClusterUnits units: one launch
-    for (int cl = 8; cl > 0; cl /= 2)
-      if (heads * cl <= wave && units <= cl * kClusterUnits) {
-        g->cluster = cl;
-        g->ctas = static_cast<int>(heads * cl);
-        return;
-      }
+  if constexpr (NT <= 2) {
+    if (cluster_grid<F, NT, 8>(heads, max_k, num_sms, g) ||
+        cluster_grid<F, NT, 4>(heads, max_k, num_sms, g) ||
+        cluster_grid<F, NT, 2>(heads, max_k, num_sms, g) ||
+        cluster_grid<F, NT, 1>(heads, max_k, num_sms, g))
+      return;
   }
-  // one resident wave, no more CTAs than there can be units
-  const long long ctas = wave < heads * units ? wave : heads * units;
+  using S = Shape<F, NT, 0>;
+  const long long wave = static_cast<long long>(num_sms) * S::kCtas;
+  const long long most = heads * units_for<S>(max_k), ctas = wave < most ? wave : most;
   g->ctas = static_cast<int>(ctas < kKvMaxCtas ? ctas : kKvMaxCtas);
 }
 

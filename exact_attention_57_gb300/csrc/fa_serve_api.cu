@@ -182,8 +182,8 @@ int pages_args(const void *const *from, void *const *to, const u64 *bytes, int n
     x[n++] = {t, t + bytes[i] * to_blocks, true};
     if (f != t)
       x[n++] = {f, f + bytes[i] * from_blocks, false};
-    else if (from_blocks > to_blocks)
-      x[n - 1].end = f + bytes[i] * from_blocks;
+    else if (from_blocks > to_blocks)  // what is read behind the pages written
+      x[n++] = {t + bytes[i] * to_blocks, f + bytes[i] * from_blocks, false};
   }
   std::sort(x, x + n, [](const Piece &a, const Piece &b) { return a.begin < b.begin; });
   uintptr_t any = 0, out = 0;  // where the arrays so far end, and the written ones

@@ -558,7 +558,7 @@ FA_API int fa_fwd_kv4_schedule(int B, int Hq, int Hk, int max_seqlen_q, int max_
  * a <= 448 * 2^e: the scale becomes 2^e if the block's first token is among them (what
  * the block held counts no more), else the larger of 2^e and what it was (one that is
  * not a positive number counts as 0, and so do the block's values).  Codes are
- * e4m3(x / scale), rounded to nearest, ties to even, saturating; NaNs are stored as
+ * e4m3(x / scale), the fp32 quotient rounded to nearest, ties to even, saturating; NaNs are stored as
  * +448 times the scale, no code is ever stored as NaN.  Where the scale has grown, the
  * block's tokens ahead of the first one written keep their values: their codes become
  * e4m3(code * old / new), which is exact but for numbers that become smaller than
