@@ -13,10 +13,13 @@
 // re-rounds nothing but what becomes subnormal (below scale' * 2^-6).
 //
 // The rows of one block follow one another in a call (as fa_kv_plan deals them): a
-// run.  A team of bs / 16 warps takes a run for one key head and for K or V, a warp the
-// rows of 16 of the block's tokens, all loaded at once and kept in registers between
-// the maximum, which the team shares through shared memory, and the codes: each row is
-// read once, and with 4 KB in flight a warp.
+// run.  A CTA finds the runs that begin in a window of rows and takes them for a share
+// of the pairs (K or V, key head), so that finding them is paid once for several:
+//   few runs (prompts): a team of bs / 16 warps takes a run, pair after pair, a warp the
+//     rows of 16 of the block's tokens, all loaded at once and kept in registers between
+//     the maximum, which the team shares through shared memory, and the codes;
+//   many (new tokens of many requests): a warp takes a run, lanes and registers spread
+//     over the pairs.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -65,22 +68,32 @@ __device__ __forceinline__ float size_of(const Eight<T> &x, float top) {
   return top;
 }
 
-// Eight codes.  `by`: 1 / scale where that is a power of two, else the scale.
+// Eight codes, by 1 / scale, where the scale is a power of two, or by the scale itself
+// (not inlined: eight correctly rounded divisions, which the caches that
+// fa_kv8_append fills never need; in line, they made the kernel's every element pay for
+// their branches).  A NaN becomes 448.
 template <typename T>
-__device__ __forceinline__ uint2 codes_of(const Eight<T> &x, float by, bool exact) {
+__device__ __forceinline__ uint2 codes_by(const Eight<T> &x, float inv) {
   const T *e = reinterpret_cast<const T *>(&x);
   uint32_t c[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    float y[2];
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const float f = static_cast<float>(e[2 * j + n]);
-      y[n] = fminf(exact ? f * by : __fdiv_rn(f, by), 448.f);  // (a NaN becomes 448)
-    }
-    c[j] = f32x2_e4m3x2(y[0], y[1]);
-  }
+  for (int j = 0; j < 4; ++j)
+    c[j] = f32x2_e4m3x2(fminf(static_cast<float>(e[2 * j]) * inv, 448.f),
+                        fminf(static_cast<float>(e[2 * j + 1]) * inv, 448.f));
   return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+}
+template <typename T>
+__device__ __noinline__ uint2 codes_over(Eight<T> x, float scale) {
+  const T *e = reinterpret_cast<const T *>(&x);
+  uint32_t c[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    c[j] = f32x2_e4m3x2(fminf(__fdiv_rn(static_cast<float>(e[2 * j]), scale), 448.f),
+                        fminf(__fdiv_rn(static_cast<float>(e[2 * j + 1]), scale), 448.f));
+  return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+}
+__device__ __forceinline__ bool power_of_two(float scale) {  // (and not subnormal: 2^-40 at least)
+  return (__float_as_uint(scale) & 0x7FFFFFu) == 0;
 }
 
 // Eight codes times `by`, as codes.
@@ -103,136 +116,262 @@ __device__ __forceinline__ float scale_for(float a) {
   return pow2(min(max(e, -kScaleExp), kScaleExp));
 }
 
-// Rows that a CTA looks through for runs that begin there, at most.
-constexpr int kWindow = 64;
+constexpr int kWarps = kThreads / 32;
 
-// The runs that begin among rows [window, window + the CTA's share), for one key head of
-// K or V.  Rows that are skipped do not end a run.  kSteps: rows of a warp by what it
-// loads at a time, 32 / (d / 8), at least ceil(16 / that).
+template <typename T>
+struct Append {
+  const T *k, *v;
+  long long k_stride, v_stride;
+  const long long *slots;
+  int T_;
+  int window;   // rows of a CTA's window
+  int groups;   // CTAs that share a window's pairs
+  int per_cta;  // pairs of each
+  KvStore c;
+
+  // Pair n: key head n of K, then of V.
+  __device__ __forceinline__ const T *rows(int n) const {
+    return n < c.Hk ? k + static_cast<long long>(n) * c.d : v + static_cast<long long>(n - c.Hk) * c.d;
+  }
+  __device__ __forceinline__ long long stride(int n) const { return n < c.Hk ? k_stride : v_stride; }
+  // Index of the pair's scale for a block.
+  __device__ __forceinline__ long long at(int n, long long block) const {
+    return block * c.Hk + (n < c.Hk ? n : n - c.Hk);
+  }
+  __device__ __forceinline__ float *scales(int n) const {
+    return reinterpret_cast<float *>(n < c.Hk ? c.k_scales : c.v_scales);
+  }
+  __device__ __forceinline__ uint8_t *codes(int n) const { return n < c.Hk ? c.k_codes : c.v_codes; }
+  // The slot of row t, -1 for rows that are skipped.
+  __device__ __forceinline__ long long slot(long long t) const {
+    const long long s = t >= 0 && t < T_ ? __ldg(slots + t) : -1;
+    return s < static_cast<long long>(c.num_blocks) << c.bs_log2 ? s : -1;
+  }
+};
+
+// The scale of a block that held `old`; *by: what its codes are multiplied with.
+__device__ __forceinline__ float grown(float old, float fit, float *by) {
+  old = old > 0.f && old < INFINITY ? old : 0.f;
+  const float scale = fmaxf(old, fit);
+  *by = __fdiv_rn(old, scale);
+  return scale;
+}
+
+// A run: the rows of one block that follow one another.  Of rows base .. base + 31 the
+// lanes hold the slots, and `in` has those of the run; `more`: it may go on behind them.
+struct Run {
+  long long base, slot, block;
+  unsigned in;
+  bool more;
+
+  // The part of it among rows `from` .. `from` + 31.
+  template <typename T>
+  __device__ __forceinline__ Run(const Append<T> &p, long long from, long long slot, int first,
+                                 long long block)
+      : base(from), slot(slot), block(block) {
+    const bool ahead = (threadIdx.x & 31) < first;
+    const unsigned stop = __ballot_sync(~0u, !ahead && slot >= 0 && (slot >> p.c.bs_log2) != block);
+    in = __ballot_sync(~0u, !ahead && slot >= 0) & (stop ? (stop & (0u - stop)) - 1u : ~0u);
+    more = stop == 0 && from + 32 < p.T_;
+  }
+  template <typename T>
+  __device__ __forceinline__ Run next(const Append<T> &p) const {
+    return Run(p, base + 32, p.slot(base + 32 + (threadIdx.x & 31)), 0, block);
+  }
+};
+
+// f(row, token of the block) for each row of a run, by the whole warp.
+template <typename T, typename F>
+__device__ __forceinline__ void for_rows(const Append<T> &p, Run run, F f) {
+  const int off_mask = (1 << p.c.bs_log2) - 1;
+  for (;;) {
+    for (unsigned in = run.in; in; in &= in - 1) {
+      const int j = __ffs(in) - 1;
+      f(run.base + j, static_cast<int>(__shfl_sync(~0u, run.slot, j)) & off_mask);
+    }
+    if (!run.more) break;
+    run = run.next(p);
+  }
+}
+
+// A run by one warp, pairs [n0, n1): `lanes` (a power of two) lanes a row, as many pairs
+// side by side as there are lanes for.
+template <typename T>
+__device__ __forceinline__ void append_across(const Append<T> &p, const Run &run, int n0, int n1) {
+  const int lane = threadIdx.x & 31, per_row = p.c.d / 8;
+  const int lanes = 1 << (32 - __clz(per_row - 1)), per = 32 / lanes;  // (per_row 2 .. 32)
+  const int sub = lane / lanes, x = lane - sub * lanes, col = x * 8;
+  for (int n = n0 + sub; n - sub < n1; n += per) {
+    const bool on = n < n1 && x < per_row;
+    const T *src = p.rows(on ? n : n0) + (on ? col : 0);
+    const long long stride = p.stride(on ? n : n0), at = p.at(on ? n : n0, run.block);
+    const float old = p.scales(on ? n : n0)[at];
+    Eight<T> e;
+    float top = 0.f;
+    int low = 1 << p.c.bs_log2, rows = 0;
+    for_rows(p, run, [&](long long row, int off) {
+      low = min(low, off);
+      ++rows;
+      e = load_eight(src + row * stride);
+      if (on) top = size_of<false>(e, top);
+    });
+    for (int o = 1; o < lanes; o *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    if (__any_sync(~0u, top == INFINITY)) {  // infinities, which do not count
+      top = 0.f;
+      for_rows(p, run, [&](long long row, int) {
+        if (on) top = size_of<true>(load_eight(src + row * stride), top);
+      });
+      for (int o = 1; o < lanes; o *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    }
+    float scale = scale_for(top), by = 1.f;
+    if (low > 0) scale = grown(old, scale, &by);
+    uint8_t *to = p.codes(on ? n : n0) + (at << p.c.bs_log2) * p.c.d + col;
+    if (on && by != 1.f) {
+      for (int off = 0; off < low; ++off) {
+        uint2 *c = reinterpret_cast<uint2 *>(to + off * p.c.d);
+        *c = rescaled(*c, by);
+      }
+    }
+    const float inv = __frcp_rn(scale);
+    for_rows(p, run, [&](long long row, int off) {
+      if (rows > 1) e = load_eight(src + row * stride);
+      if (on)
+        *reinterpret_cast<uint2 *>(to + off * p.c.d) =
+            power_of_two(scale) ? codes_by(e, inv) : codes_over(e, scale);
+    });
+    __syncwarp();  // (all lanes have read the old scales)
+    if (on && x == 0) p.scales(n)[at] = scale;
+  }
+}
+
+// A run by a team of bs / 16 warps, pair after pair; a warp takes the block's tokens 16
+// mate and on.  kSteps: rounds of loads for 16 rows.  map: 16 rows a warp; top_of: a
+// number a warp, twice, in turn.
 template <typename T, int kSteps>
-__global__ void __launch_bounds__(kThreads)
-    fa_kv8_append_kernel(const T *k, const T *v, long long k_stride, long long v_stride,
-                         const long long *slots, int T_, int window, const KvStore c) {
-  constexpr int kWarps = kThreads / 32;
-  __shared__ int s_row[kWarps][16];            // a warp's rows by the token in the block
-  __shared__ float s_top[2][kWarps];           // runs in turn
+__device__ __forceinline__ void append_along(const Append<T> &p, const Run &whole, int n0, int n1,
+                                             int *map, float (*top_of)[kWarps], int *turn) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int team_log2 = p.c.bs_log2 - 4, team = warp >> team_log2;
+  const int mate = warp - (team << team_log2), off_mask = (1 << p.c.bs_log2) - 1;
+  const int lanes = p.c.d / 8, per = 32 / lanes, sub = lane / lanes, col = (lane - sub * lanes) * 8;
+  // the run's rows among this warp's tokens, and its first token
+  __syncwarp();
+  if (lane < 16) map[lane] = -1;
+  __syncwarp();
+  int low = off_mask;
+  for (Run run = whole;; run = run.next(p)) {
+    if (run.in >> lane & 1) {
+      const int off = static_cast<int>(run.slot) & off_mask;
+      low = min(low, off);
+      if (off >> 4 == mate) map[off & 15] = static_cast<int>(run.base + lane);
+    }
+    if (!run.more) break;
+  }
+  for (int o = 16; o; o /= 2) low = min(low, __shfl_xor_sync(~0u, low, o));
+  __syncwarp();
+  // the row of round i for this lane, or -1
+  auto row_of = [&](int i) { return sub < per && i * per + sub < 16 ? map[i * per + sub] : -1; };
+  for (int n = n0; n < n1; ++n) {
+    const T *src = p.rows(n) + col;
+    const long long stride = p.stride(n), at = p.at(n, whole.block);
+    Eight<T> e[kSteps];
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const int row = row_of(i);
+      if (row >= 0)
+        e[i] = load_eight(src + row * stride);
+      else
+#pragma unroll
+        for (uint4 &w : e[i].w) w = make_uint4(0, 0, 0, 0);
+    }
+    const float old = p.scales(n)[at];
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) top = size_of<false>(e[i], top);
+    for (int o = 16; o; o /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    if (top == INFINITY) {
+      top = 0.f;
+#pragma unroll 1
+      for (int i = 0; i < kSteps; ++i)
+        if (row_of(i) >= 0) top = size_of<true>(load_eight(src + row_of(i) * stride), top);
+      for (int o = 16; o; o /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    }
+    if (team_log2 > 0) {
+      if (lane == 0) top_of[*turn][warp] = top;
+      named_bar_sync(1 + team, 32 << team_log2);
+      for (int w = 0; w < 1 << team_log2; ++w) top = fmaxf(top, top_of[*turn][(team << team_log2) + w]);
+      *turn ^= 1;
+    }
+    float scale = scale_for(top), by = 1.f;
+    uint8_t *to = p.codes(n) + ((at << p.c.bs_log2) + 16 * mate) * p.c.d + col;
+    if (low > 0) scale = grown(old, scale, &by);
+    if (by != 1.f) {
+      for (int y = sub; y < min(low - 16 * mate, 16); y += per) {
+        uint2 *c = reinterpret_cast<uint2 *>(to + y * p.c.d);
+        if (sub < per) *c = rescaled(*c, by);
+      }
+    }
+    if (power_of_two(scale)) {
+      const float inv = __frcp_rn(scale);
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i)
+        if (row_of(i) >= 0) *reinterpret_cast<uint2 *>(to + (i * per + sub) * p.c.d) = codes_by(e[i], inv);
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < kSteps; ++i)
+        if (row_of(i) >= 0)
+          *reinterpret_cast<uint2 *>(to + (i * per + sub) * p.c.d) =
+              codes_over(load_eight(src + row_of(i) * stride), scale);
+    }
+    // the whole team has read the old scale: a warp alone here, others ahead of the barrier
+    __syncwarp();
+    if (mate == 0 && lane == 0) p.scales(n)[at] = scale;
+  }
+}
+
+template <typename T, int kSteps>
+__global__ void __launch_bounds__(kThreads, kSteps * sizeof(T) <= 16 ? 3 : kSteps * sizeof(T) <= 32 ? 2 : 1)
+    fa_kv8_append_kernel(const __grid_constant__ Append<T> p) {
+  __shared__ int s_map[kWarps][16];
+  __shared__ float s_top[2][kWarps];
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int heads = 2 * c.Hk, hv = static_cast<int>(blockIdx.x % heads), h = hv / 2;
-  const bool is_v = hv & 1;
-  const T *x = is_v ? v : k;
-  const long long stride = is_v ? v_stride : k_stride;
-  uint8_t *codes = is_v ? c.v_codes : c.k_codes;
-  float *scales = reinterpret_cast<float *>(is_v ? c.v_scales : c.k_scales);
-  const long long all = static_cast<long long>(c.num_blocks) << c.bs_log2;
-  const int off_mask = (1 << c.bs_log2) - 1;
-  const int team_log2 = c.bs_log2 - 4, team = warp >> team_log2, teams = kWarps >> team_log2;
-  const int mate = warp - (team << team_log2);  // which 16 tokens of the block
-  auto slot_at = [&](long long t) -> long long {
-    const long long s = t >= 0 && t < T_ ? __ldg(slots + t) : -1;
-    return s < all ? s : -1;
-  };
-  // a warp takes `per` rows at a time, d / 8 lanes each
-  const int lanes = c.d / 8, per = 32 / lanes, sub = lane / lanes, col = (lane - sub * lanes) * 8;
-  const T *src = x + static_cast<long long>(h) * c.d + col;
-  int runs = 0;  // begun in the window so far
-  int turn = 0;
-  const long long w0 = static_cast<long long>(blockIdx.x / heads) * window;
+  const int team_log2 = p.c.bs_log2 - 4, team = warp >> team_log2, teams = kWarps >> team_log2;
+  const int group = static_cast<int>(blockIdx.x % p.groups);
+  const long long w0 = static_cast<long long>(blockIdx.x / p.groups) * p.window;
+  const int n0 = group * p.per_cta, n1 = min(n0 + p.per_cta, 2 * p.c.Hk);
+  int runs = 0, turn = 0;
   long long before = -1;  // the block of the last row that counts ahead of the rows at hand
-  for (int part = 0; part < window; part += 32) {
+  for (int part = 0; part < p.window; part += 32) {
     const long long t0 = w0 + part;
-    if (t0 >= T_) break;
-    const long long mine = lane < window - part ? slot_at(t0 + lane) : -1;
-    const unsigned there = __ballot_sync(~0u, mine >= 0);
+    if (t0 >= p.T_) break;
+    const long long mine = p.slot(t0 + lane);  // (also behind the window)
+    // (with the loads of the window's own: mostly it is the row ahead that tells)
+    const long long ahead = before < 0 ? p.slot(t0 - 32 + lane) : -1;
+    const unsigned own = p.window - part < 32 ? (1u << (p.window - part)) - 1u : ~0u;
+    const unsigned there = __ballot_sync(~0u, mine >= 0) & own;
     if (there == 0) continue;
-    for (long long t = t0; before < 0 && t > 0; t -= 32) {
-      const long long s = slot_at(t - 32 + lane);
+    for (long long t = t0, s = ahead; before < 0 && t > 0; t -= 32, s = p.slot(t - 32 + lane)) {
       const unsigned some = __ballot_sync(~0u, s >= 0);
-      if (some) before = __shfl_sync(~0u, s, 31 - __clz(some)) >> c.bs_log2;
+      if (some) before = __shfl_sync(~0u, s, 31 - __clz(some)) >> p.c.bs_log2;
     }
     const unsigned lower = there & ((1u << lane) - 1u);
-    const long long prev = __shfl_sync(~0u, mine, lower ? 31 - __clz(lower) : 0) >> c.bs_log2;
-    const bool leads = mine >= 0 && (mine >> c.bs_log2) != (lower ? prev : before);
+    const long long prev = __shfl_sync(~0u, mine, lower ? 31 - __clz(lower) : 0) >> p.c.bs_log2;
+    const bool leads = (there >> lane & 1) && (mine >> p.c.bs_log2) != (lower ? prev : before);
     unsigned leaders = __ballot_sync(~0u, leads);
-    before = __shfl_sync(~0u, mine, 31 - __clz(there)) >> c.bs_log2;
+    before = __shfl_sync(~0u, mine, 31 - __clz(there)) >> p.c.bs_log2;
+    // runs of up to four rows, on average: a warp each
+    const bool many = __popc(leaders) * 4 >= __popc(there);
     while (leaders) {
       const int first = __ffs(leaders) - 1;
       leaders &= leaders - 1;
-      const long long block = __shfl_sync(~0u, mine, first) >> c.bs_log2;
-      if (runs++ % teams != team) continue;  // (the whole team)
-      // the run's rows among this warp's tokens, and its first token
-      if (lane < 16) s_row[warp][lane] = -1;
-      __syncwarp();
-      int low = off_mask;
-      for (long long base = t0 + first; base < T_; base += 32) {
-        const long long s = slot_at(base + lane);
-        const unsigned stop = __ballot_sync(~0u, s >= 0 && (s >> c.bs_log2) != block);
-        const unsigned in = stop ? (stop & (0u - stop)) - 1u : ~0u;
-        if (s >= 0 && (in >> lane & 1)) {
-          const int off = static_cast<int>(s) & off_mask;
-          low = min(low, off);
-          if (off >> 4 == mate) s_row[warp][off & 15] = static_cast<int>(base + lane);
-        }
-        if (stop) break;
-      }
-      __syncwarp();
-      Eight<T> e[kSteps];
-      int row[kSteps];
-#pragma unroll
-      for (int n = 0; n < kSteps; ++n) {
-        const int y = n * per + sub;
-        row[n] = sub < per && y < 16 ? s_row[warp][y] : -1;
-        if (row[n] >= 0) e[n] = load_eight(src + row[n] * stride);
-      }
-      float *where = scales + block * c.Hk + h;
-      float old = *where;
-      float top = 0.f;
-#pragma unroll
-      for (int n = 0; n < kSteps; ++n)
-        if (row[n] >= 0) top = size_of<false>(e[n], top);
-      for (int o = 16; o; o /= 2) {
-        top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-        low = min(low, __shfl_xor_sync(~0u, low, o));
-      }
-      float finite = top;
-      if (top == INFINITY) {
-        finite = 0.f;
-#pragma unroll
-        for (int n = 0; n < kSteps; ++n)
-          if (row[n] >= 0) finite = size_of<true>(e[n], finite);
-        for (int o = 16; o; o /= 2) finite = fmaxf(finite, __shfl_xor_sync(~0u, finite, o));
-      }
-      if (team_log2 > 0) {
-        if (lane == 0) s_top[turn][warp] = finite;
-        named_bar_sync(1 + team, 32 << team_log2);
-        for (int n = 0; n < 1 << team_log2; ++n)
-          finite = fmaxf(finite, s_top[turn][(team << team_log2) + n]);
-        turn ^= 1;
-      }
-      const float fit = scale_for(finite);
-      float scale = fit;
-      uint8_t *to = codes + ((((block * c.Hk + h) << c.bs_log2) + 16 * mate) * c.d) + col;
-      if (low > 0) {
-        old = old > 0.f && old < INFINITY ? old : 0.f;
-        scale = fmaxf(old, fit);
-        if (scale != old) {
-          const float by = __fdiv_rn(old, scale);
-          for (int y = sub; y < min(low - 16 * mate, 16); y += per) {
-            uint2 *p = reinterpret_cast<uint2 *>(to + y * c.d);
-            if (sub < per) *p = rescaled(*p, by);
-          }
-        }
-      }
-      const bool exact = (__float_as_uint(scale) & 0x7FFFFFu) == 0;  // (and not subnormal)
-      const float by = exact ? __frcp_rn(scale) : scale;
-#pragma unroll
-      for (int n = 0; n < kSteps; ++n)
-        if (row[n] >= 0)
-          *reinterpret_cast<uint2 *>(to + (n * per + sub) * c.d) = codes_of(e[n], by, exact);
-      // every warp of the team has read the old scale: one alone here, or the barrier
-      __syncwarp();
-      if (mate == 0 && lane == 0) *where = scale;
+      if (runs++ % (many ? kWarps : teams) != (many ? warp : team)) continue;
+      const Run run(p, t0, mine, first, __shfl_sync(~0u, mine, first) >> p.c.bs_log2);
+      if (many)
+        append_across(p, run, n0, n1);
+      else
+        append_along<T, kSteps>(p, run, n0, n1, s_map[warp], s_top, &turn);
     }
   }
 }
@@ -313,28 +452,25 @@ cudaError_t launch(void (*kern)(A...), long long threads, cudaStream_t s, A... a
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-template <typename T, int kSteps>
-cudaError_t append_steps(const void *k, const void *v, long long ks, long long vs,
-                         const long long *slots, int T_, const KvStore &c, cudaStream_t s) {
-  // Windows of as many rows as a CTA has teams where the rows are few (each may begin a
-  // run), of up to 64 where they are many.
-  const long long heads = 2LL * c.Hk;
-  int window = kThreads / 32 >> (c.bs_log2 - 4);
-  while (window < kWindow && (T_ + window - 1LL) / window * heads > 2048) window *= 2;
-  const long long ctas = (T_ + window - 1LL) / window * heads;
-  return launch<const T *, const T *, long long, long long, const long long *, int, int,
-                const KvStore>(fa_kv8_append_kernel<T, kSteps>, ctas * kThreads, s,
-                               static_cast<const T *>(k), static_cast<const T *>(v), ks, vs, slots,
-                               T_, window, c);
-}
-
 template <typename T>
 cudaError_t append(const void *k, const void *v, long long ks, long long vs,
                    const long long *slots, int T_, const KvStore &c, cudaStream_t s) {
-  const int per = 32 / (c.d / 8), steps = (16 + per - 1) / per;
-  if (steps <= 4) return append_steps<T, 4>(k, v, ks, vs, slots, T_, c, s);
-  if (steps <= 8) return append_steps<T, 8>(k, v, ks, vs, slots, T_, c, s);
-  return append_steps<T, 16>(k, v, ks, vs, slots, T_, c, s);
+  Append<T> p = {static_cast<const T *>(k), static_cast<const T *>(v), ks, vs, slots, T_, 0, 0, 0, c};
+  // Windows of a row a warp where the rows are few, since each may begin a run, else of
+  // 16 rows a warp, as teams take them; about a thousand CTAs, but no fewer pairs each
+  // than a warp's lanes hold of one row.
+  p.window = T_ <= 4096 ? kWarps : 16 * kWarps;
+  const long long windows = (T_ + p.window - 1LL) / p.window;
+  const int per = 32 / (c.d / 8), pairs = 2 * c.Hk, most = (pairs + per - 1) / per;
+  const long long want = (1024 + windows - 1) / windows;
+  p.groups = static_cast<int>(want < most ? want : most);
+  p.per_cta = (pairs + p.groups - 1) / p.groups;
+  p.groups = (pairs + p.per_cta - 1) / p.per_cta;
+  const long long threads = windows * p.groups * kThreads;
+  const int steps = (16 + per - 1) / per;
+  if (steps <= 4) return launch<const Append<T>>(fa_kv8_append_kernel<T, 4>, threads, s, p);
+  if (steps <= 8) return launch<const Append<T>>(fa_kv8_append_kernel<T, 8>, threads, s, p);
+  return launch<const Append<T>>(fa_kv8_append_kernel<T, 16>, threads, s, p);
 }
 
 template <typename T>
