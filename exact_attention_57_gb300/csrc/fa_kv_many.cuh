@@ -9,24 +9,28 @@
 // equal shares, whatever the lengths, the mask and the number of tiles.
 //
 // Warps 0-3    softmax, correction and epilogue, one row a thread.
-// Warps 4-7    expand the codes of K, warps 8-11 those of V: thread r loads
-//              token r of the 128 (a page lookup, the codes, the format's scales,
-//              one step ahead), turns them into fp16 (exactly)
-//              and writes them as a 128-byte-swizzled row.
-//              Tokens behind the sequence or on a missing page become zeros
-//              and are reported in a bit mask.
 // Warp 12, 13  issue S = Q K^T (three score buffers) and O += P V (P in tensor
-//              memory), kind::f16, fp32 accumulators; warp 12 owns the tensor
-//              memory.
+//              memory), fp32 accumulators; warp 12 owns the tensor memory.
+// The others bring Q, K and V into shared memory.  Tokens behind the sequence or on a
+// missing page become zeros and are reported in a bit mask.
+//
+// With F::kDirectKeys = false, keys and values become fp16 (exactly) and the products are
+// kind::f16:
+// Warps 4-7    expand the codes of K, warps 8-11 those of V: thread r loads
+//              token r of the 128 (a page lookup, the codes and the scales, one step
+//              ahead), turns them into fp16 and writes them as a 128-byte-swizzled row.
 // Warp 14, 15  bring the next tile's Q into shared memory (two buffers), as
 //              fp16 times a power of two a row.
+// F has D and Row: load() of a token's codes, expand() to fp16 by 16-byte units.
 //
-// A format F has D, kBlockScales (the scales of 16 keys are one number each, which
-// the softmax applies), and Row, a thread's share of the codes of its warp's 32
-// tokens.  Without kStreams: load() of the thread's own token, expand() to fp16 by
-// 16-byte units.  With kStreams: begin() loads the first step's, stream() turns one
-// step's into fp16 and each register, once free, over to the next step's codes.  With
-// kBlockScales, load_scales() and scales() by the threads of tokens 16 n.
+// With F::kDirectKeys = true, the codes of K are e4m3 numbers and go to the tensor core as
+// they are (kind::f8f6f4), with Q as a sum of two or three e4m3 numbers; the scales of 16
+// keys are one number for each of K and V and enter the softmax (BlockScale):
+// Warps 4-11   expand the codes of V to fp16, 16 tokens each.
+// Warp 14      copies those of K by TMA, 16 tokens a copy, and says which keys there are
+//              and their scales.
+// Warp 15      brings the next tile's Q (two buffers).
+// F has D, kTerms<T> (numbers for Q), Keys (a map of the codes) and scales().
 //
 // Every wait is bounded; on expiry the CTA raises its abort flag, records the
 // role in the status word, drains its products, frees tensor memory and ends.
@@ -38,6 +42,7 @@
 
 #include "fa.h"
 #include "fa_internal.h"
+#include "fa_kv8.cuh"
 #include "fa_kv_split.cuh"
 #include "fa_wait.cuh"
 
@@ -56,15 +61,20 @@ struct ManyCtl {
 
 constexpr int WALK_BYTES = 80;
 
-template <class F>
+template <class F, typename T>
 struct ManyCfg {
   static constexpr int D = F::D;
+  static constexpr bool kDirect = F::kDirectKeys;
   static constexpr int NCH = D / 64;               // 128-byte chunks of a row
   static constexpr int CHUNK = 128 * 128;
-  static constexpr int TILE = NCH * CHUNK;
+  static constexpr int TILE = NCH * CHUNK;         // 128 rows in fp16
+  static constexpr int RAW = 128 * D;              // and in bytes
+  static constexpr int TERMS = F::template kTerms<T>;
+  static constexpr int QT = kDirect ? TERMS * RAW : TILE;
+  static constexpr int KT = kDirect ? RAW : TILE;
   static constexpr int NS = 3;                     // score buffers
   static constexpr int KST = D == 128 ? 3 : 4;     // K stages
-  static constexpr int VST = D == 128 ? 2 : 4;     // V stages
+  static constexpr int VST = D == 64 ? 4 : kDirect && TERMS == 2 ? 3 : 2;  // V stages
   static constexpr int ST = KST > VST ? KST : VST;
   // Steps whose key masks (and scales) are kept: K of step n is expanded once S of
   // step n - KST is complete, which was issued when the softmax had done with step
@@ -72,15 +82,15 @@ struct ManyCfg {
   static constexpr int MASKS = KST + NS;
   static constexpr uint32_t COL_O = NS * 128;
   static constexpr int OFF_Q = 0;
-  static constexpr int OFF_K = OFF_Q + 2 * TILE;
-  static constexpr int OFF_V = OFF_K + KST * TILE;
+  static constexpr int OFF_K = OFF_Q + 2 * QT;
+  static constexpr int OFF_V = OFF_K + KST * KT;
   static constexpr int OFF_MASK = OFF_V + VST * TILE;
   // An exponent a row of the tiles in flight: Q of tile g is written when the
   // last S of tile g - 2 is complete, and with tiles of one step the softmax
   // may then still be at tile g - 4 (three score buffers).
   static constexpr int QES = 5;
   // Of 16 keys each, eight to a step: K's scale, log2 of V's, its inverse, nothing.
-  static constexpr int SCALES = F::kBlockScales ? 8 * 16 : 0;
+  static constexpr int SCALES = kDirect ? 8 * 16 : 0;
   static constexpr int OFF_SCALE = OFF_MASK + MASKS * 16;
   static constexpr int OFF_QE = OFF_SCALE + MASKS * SCALES;
   static constexpr int OFF_BAR = OFF_QE + QES * 128;
@@ -201,9 +211,10 @@ __device__ __forceinline__ bool next_part(const KvAttn &p, const ManyCtl &c, Wal
 template <typename T, class F>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_kv_many_kernel(const __grid_constant__ KvAttn p, const __grid_constant__ ManyCtl ctl,
-                       float *ws) {
+                       float *ws, const __grid_constant__ typename F::Keys keys) {
   constexpr int D = F::D;
-  using C = ManyCfg<F>;
+  using C = ManyCfg<F, T>;
+  constexpr int kExpanders = C::kDirect ? 256 : 128;  // threads that expand V
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -233,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
-      mbar_init(bQfull + 8 * s, 64);
+      mbar_init(bQfull + 8 * s, C::kDirect ? 32 : 64);
       mbar_init(bQempty + 8 * s, 1);
     }
     mbar_init(bOfree, 128);
@@ -241,9 +252,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bFin + 8, 1);
 #pragma unroll
     for (int s = 0; s < C::ST; ++s) {
-      mbar_init(bKfull + 8 * s, 128);
+      mbar_init(bKfull + 8 * s, C::kDirect ? 1 : 128);
       mbar_init(bKempty + 8 * s, 1);
-      mbar_init(bVfull + 8 * s, 128);
+      mbar_init(bVfull + 8 * s, kExpanders);
       mbar_init(bVempty + 8 * s, 1);
     }
 #pragma unroll
@@ -321,12 +332,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (issued >= C::NS && !(ok = bounded_wait(bOdone + 8 * b, bph ^ 1, w))) break;
             if (!(ok = bounded_wait(bKfull + 8 * s, sph, w))) break;
             tc_fence_after();
+            if constexpr (C::kDirect) {
+              // the terms of Q one after the other, 32 elements a product
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = (kk >> 2) * C::CHUNK + (kk & 3) * 32;
-              umma_ss<false>(tmem + b * 128, sdesc_sw128(sQ + (g & 1) * C::TILE + off, 16, 1024),
-                             sdesc_sw128(sK + s * C::TILE + off, 16, 1024), kIdesc,
-                             kk > 0 ? 1u : 0u);
+              for (int kk = 0; kk < C::TERMS * (D / 32); ++kk) {
+                const int term = kk / (D / 32), off = kk % (D / 32) * 32;
+                umma_f8(tmem + b * 128,
+                        sdesc_bytes<D>(sQ + (g & 1) * C::QT + term * C::RAW + off),
+                        sdesc_bytes<D>(sK + s * C::RAW + off), kIdesc, kk > 0 ? 1u : 0u);
+              }
+            } else {
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = (kk >> 2) * C::CHUNK + (kk & 3) * 32;
+                umma_ss<false>(tmem + b * 128, sdesc_sw128(sQ + (g & 1) * C::TILE + off, 16, 1024),
+                               sdesc_sw128(sK + s * C::TILE + off, 16, 1024), kIdesc,
+                               kk > 0 ? 1u : 0u);
+              }
             }
             tc_commit(bKempty + 8 * s);
             tc_commit(bSfull + 8 * b);
@@ -372,6 +394,74 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_commit(bFin + 8);
         bounded_wait(bFin + 8, 0, w, false);
       }
+    } else if (C::kDirect && warp == 14) {
+      // ---------------------------------------------- K as it lies in the cache
+      if constexpr (C::kDirect) {
+        // Lane n of the first eight brings keys 16 n and on of the 128, one copy each, and
+        // says what the softmax has to know of them.
+        w.role = kStatusProducer;
+        fence_proxy_async_smem();  // the stages held the prefix sums before
+        Part x;
+        bool have = next_part(p, ctl, walk, x);
+        int j = have ? x.lo : 0, t = 0, id = -1, head = 0;
+        bool past = false;
+        auto lookup = [&]() {  // the cursor's block, then one step on; whether there was a step
+          const bool was = have;
+          t = j * 128 + 16 * lane;
+          past = lane >= 8 || t >= x.s.nk;
+          id = have && !past
+                   ? __ldg(p.table + static_cast<long long>(x.b) * p.width + (t >> p.c.bs_log2))
+                   : -1;
+          head = x.h;
+          if (have && ++j >= x.hi) {
+            have = next_part(p, ctl, walk, x);
+            j = x.lo;
+          }
+          return was;
+        };
+        struct Keys16 {
+          int id, row;  // -1: none; its row among the block's, all heads
+          bool past;    // behind the sequence
+          float ks, vs;
+        } cur;
+        auto take = [&]() {
+          if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.c.num_blocks)) id = -1;
+          cur = Keys16{id, (head << p.c.bs_log2) + (t & ((1 << p.c.bs_log2) - 1)), past, 1.f, 1.f};
+          if (id < 0) return;
+          const long long at = static_cast<long long>(id) * p.c.Hk + head;
+          cur.ks = __ldg(reinterpret_cast<const float *>(p.c.k_scales) + at);
+          cur.vs = __ldg(reinterpret_cast<const float *>(p.c.v_scales) + at);
+        };
+        bool now = lookup();
+        take();
+        bool next = now && lookup();
+        int step = 0, st = 0, ph = 0;
+        while (now) {
+          if (!__all_sync(~0u, step < C::KST || bounded_wait(bKempty + 8 * st, ph ^ 1, w))) break;
+          const unsigned there = __ballot_sync(~0u, cur.id >= 0);
+          const unsigned bits = __ballot_sync(~0u, cur.id >= 0 || cur.past);
+          if (lane < 8)
+            reinterpret_cast<float4 *>(smem + C::OFF_SCALE + step % C::MASKS * C::SCALES)[lane] =
+                F::scales(cur.ks, cur.vs);
+          if (lane < 4)
+            reinterpret_cast<unsigned *>(smem + C::OFF_MASK)[(step % C::MASKS) * 4 + lane] =
+                (bits >> (2 * lane) & 1 ? 0xFFFFu : 0u) | (bits >> (2 * lane + 1) & 1 ? 0xFFFF0000u : 0u);
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(bKfull + 8 * st, __popc(there) * 16 * D);
+          __syncwarp();
+          if (cur.id >= 0)
+            tma_load_3d(sK + st * C::RAW + lane * 16 * D, &keys.map, bKfull + 8 * st, 0, cur.row, cur.id);
+          if (++st == C::KST) st = 0, ph ^= 1;
+          ++step;
+          if (next) take();
+          now = next;
+          next = next && lookup();
+        }
+        // no copy may be on its way when the CTA ends
+        if (lane == 0)
+          for (int n = max(step - C::KST, 0); n < step; ++n)
+            bounded_wait(bKfull + 8 * (n % C::KST), n / C::KST & 1, w, false);
+      }
     } else {
       // ---------------------------------------------- Q rows
       w.role = kStatusProducer;
@@ -381,10 +471,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int g = 0; next_part(p, ctl, walk, x); ++g) {
         if (!__all_sync(~0u, g < 2 || bounded_wait(bQempty + 8 * (g & 1), ((g >> 1) - 1) & 1, w)))
           break;
-        uint8_t *tile = smem + C::OFF_Q + (g & 1) * C::TILE;
+        uint8_t *tile = smem + C::OFF_Q + (g & 1) * C::QT;
 #pragma unroll 1
-        for (int n = 0; n < 2; ++n) {
-          const int r = (threadIdx.x & 63) + 64 * n;
+        for (int n = 0; n < (C::kDirect ? 4 : 2); ++n) {
+          const int r = C::kDirect ? lane + 32 * n : (threadIdx.x & 63) + 64 * n;
           const int ti = r / p.group, tj = r - ti * p.group, i = x.qt * ctl.tokens + ti;
           const bool in = ti < ctl.tokens && i < x.s.nq;
           float amax = 0.f;
@@ -398,22 +488,61 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int y = 0; y < 8; ++y) amax = fmaxf(amax, fabsf(static_cast<float>(f[y])));
           }
-          // 2^e brings the row's largest element to 1 .. 2 (an exact scaling)
-          const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -126), 126);
-          const float mul = pow2(-e) * sign;
+          int qe;  // the row is scaled by 2^-qe
+          if constexpr (C::kDirect) {
+            // Q as a sum of e4m3 numbers, each the rest of the ones before, of elements
+            // scaled to 256 at most: two hold bf16's eight significant bits, three fp16's
+            // eleven, of elements that are not far below the row's largest (what is left
+            // out is 2^-10 at most, 2^-17 of the largest).  A row with an infinity
+            // becomes NaN, as e4m3 has none.
+            const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -119), 127);
+            const float mul = pow2(7 - e) * (amax == INFINITY ? __int_as_float(0x7FC00000) : sign);
+#pragma unroll 2
+            for (int u = 0; u < D / 16; ++u) {
+              uint4 q2[2];
+              q2[0] = in ? __ldg(src + 2 * u) : make_uint4(0, 0, 0, 0);
+              q2[1] = in ? __ldg(src + 2 * u + 1) : make_uint4(0, 0, 0, 0);
+              const T *f = reinterpret_cast<const T *>(q2);
+              float y[16];
+#pragma unroll
+              for (int c = 0; c < 16; ++c) y[c] = static_cast<float>(f[c]) * mul;
+#pragma unroll
+              for (int term = 0; term < C::TERMS; ++term) {
+                uint32_t v[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                  v[c] = f32x2_e4m3x2(y[4 * c], y[4 * c + 1]) |
+                         f32x2_e4m3x2(y[4 * c + 2], y[4 * c + 3]) << 16;
+                  const float2 lo = f16x2_f32(e4m3x2_f16x2(v[c]));
+                  const float2 hi = f16x2_f32(e4m3x2_f16x2(v[c] >> 16));
+                  y[4 * c] -= lo.x, y[4 * c + 1] -= lo.y, y[4 * c + 2] -= hi.x, y[4 * c + 3] -= hi.y;
+                }
+                // 128-byte rows swizzle by the row in eight, 64-byte rows by its half
+                const int at = D == 128 ? u ^ (r & 7) : u ^ (r >> 1 & 3);
+                *reinterpret_cast<uint4 *>(tile + term * C::RAW + r * D + at * 16) =
+                    make_uint4(v[0], v[1], v[2], v[3]);
+              }
+            }
+            qe = e - 7;
+          } else {
+            // 2^e brings the row's largest element to 1 .. 2 (an exact scaling)
+            const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -126), 126);
+            const float mul = pow2(-e) * sign;
 #pragma unroll 4
-          for (int u = 0; u < D / 8; ++u) {
-            const uint4 q = in ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
-            const T *f = reinterpret_cast<const T *>(&q);
-            uint4 v;
-            v.x = pack_f16x2(static_cast<float>(f[0]) * mul, static_cast<float>(f[1]) * mul);
-            v.y = pack_f16x2(static_cast<float>(f[2]) * mul, static_cast<float>(f[3]) * mul);
-            v.z = pack_f16x2(static_cast<float>(f[4]) * mul, static_cast<float>(f[5]) * mul);
-            v.w = pack_f16x2(static_cast<float>(f[6]) * mul, static_cast<float>(f[7]) * mul);
-            *reinterpret_cast<uint4 *>(tile + (u >> 3) * C::CHUNK + r * 128 +
-                                       (((u & 7) ^ (r & 7)) << 4)) = v;
+            for (int u = 0; u < D / 8; ++u) {
+              const uint4 q = in ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
+              const T *f = reinterpret_cast<const T *>(&q);
+              uint4 v;
+              v.x = pack_f16x2(static_cast<float>(f[0]) * mul, static_cast<float>(f[1]) * mul);
+              v.y = pack_f16x2(static_cast<float>(f[2]) * mul, static_cast<float>(f[3]) * mul);
+              v.z = pack_f16x2(static_cast<float>(f[4]) * mul, static_cast<float>(f[5]) * mul);
+              v.w = pack_f16x2(static_cast<float>(f[6]) * mul, static_cast<float>(f[7]) * mul);
+              *reinterpret_cast<uint4 *>(tile + (u >> 3) * C::CHUNK + r * 128 +
+                                         (((u & 7) ^ (r & 7)) << 4)) = v;
+            }
+            qe = e;
           }
-          reinterpret_cast<int8_t *>(smem + C::OFF_QE)[g % C::QES * 128 + r] = static_cast<int8_t>(e);
+          reinterpret_cast<int8_t *>(smem + C::OFF_QE)[g % C::QES * 128 + r] = static_cast<int8_t>(qe);
         }
         fence_proxy_async_smem();
         mbar_arrive(bQfull + 8 * (g & 1));
@@ -424,85 +553,158 @@ __global__ void __launch_bounds__(kThreads, 1)
     setmaxnreg_dec<kRegExpand>();
     // ------------------------------------------------ codes -> fp16 rows
     w.role = kStatusProducer;
-    const bool is_v = warp >= 8;
-    const int r = threadIdx.x & 127;  // token of the tile
-    const uint8_t *codes = is_v ? p.c.v_codes : p.c.k_codes;
-    const uint8_t *scales = is_v ? p.c.v_scales : p.c.k_scales;
-    uint8_t *tiles = smem + (is_v ? C::OFF_V : C::OFF_K);
-    const uint32_t full = is_v ? bVfull : bKfull, empty = is_v ? bVempty : bKempty;
-    bool past = false;
-    struct Row : F::Row {
-      bool valid, past;  // past: behind the sequence
-    };
-    auto load = [&](Row &x, long long row) {
-      x.valid = row >= 0;
-      x.past = past;
-      if constexpr (!F::kStreams)
+    if constexpr (C::kDirect) {
+      // Of V alone, 16 tokens a warp.  Lane l takes 16 codes of every kRows-th token, so
+      // that a load covers whole rows, two steps ahead of the one that is written.
+      constexpr int kLanes = D / 16, kRows = 32 / kLanes, kAt = 16 / kRows;
+      const int v0 = 16 * (warp - 4), y0 = lane / kLanes;
+      Part x;
+      bool have = next_part(p, ctl, walk, x);
+      int j = have ? x.lo : 0, id = -1, t = 0, left = 0, head = 0;
+      auto lookup = [&]() {  // the cursor's block, then one step on; whether there was a step
+        const bool was = have;
+        t = j * 128 + v0;
+        left = x.s.nk - t;
+        id = have && left > 0
+                 ? __ldg(p.table + static_cast<long long>(x.b) * p.width + (t >> p.c.bs_log2))
+                 : -1;
+        head = x.h;
+        if (have && ++j >= x.hi) {
+          have = next_part(p, ctl, walk, x);
+          j = x.lo;
+        }
+        return was;
+      };
+      // Tokens behind the sequence or on a missing page are zeros.
+      auto load = [&](uint4 (&c)[kAt]) {
+        const bool there = static_cast<unsigned>(id) < static_cast<unsigned>(p.c.num_blocks);
+        const long long row = ((static_cast<long long>(id) * p.c.Hk + head) << p.c.bs_log2) +
+                              (t & ((1 << p.c.bs_log2) - 1)) + y0;
+        const uint8_t *from = p.c.v_codes + row * D + lane % kLanes * 16;
+#pragma unroll
+        for (int n = 0; n < kAt; ++n)
+          c[n] = there && n * kRows + y0 < left
+                     ? __ldg(reinterpret_cast<const uint4 *>(from + n * kRows * D))
+                     : make_uint4(0, 0, 0, 0);
+      };
+      int step = 0, st = 0, ph = 0;
+      // 8 codes make a unit of 16 bytes, at u ^ (row & 7) of its chunk.  The lanes of a
+      // row's second half store theirs in the other order, so that eight lanes at a time
+      // meet every bank once.
+      const int u = 2 * (lane % kLanes);
+      const bool swap = u >= 8;
+      auto write = [&](const uint4 (&c)[kAt]) {  // false: to end
+        if (ctl.skip_load && step == 0) {  // test hook: the P V issuer's wait runs out
+          if (threadIdx.x == 128) atomicOr(ctl.status, kStatusInjected);
+          return false;
+        }
+        if (!__all_sync(~0u, step < C::VST || bounded_wait(bVempty + 8 * st, ph ^ 1, w))) return false;
+        uint8_t *to = smem + C::OFF_V + st * C::TILE + (v0 + y0) * 128 + (u >> 3) * C::CHUNK;
+#pragma unroll
+        for (int n = 0; n < kAt; ++n) {
+          const uint32_t e[4] = {swap ? c[n].z : c[n].x, swap ? c[n].w : c[n].y,
+                                 swap ? c[n].x : c[n].z, swap ? c[n].y : c[n].w};
+          const int low = (n * kRows + y0) & 7;
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+            *reinterpret_cast<uint4 *>(to + n * kRows * 128 + ((((u + (y != swap)) & 7) ^ low) << 4)) =
+                make_uint4(e4m3x2_f16x2(e[2 * y]), e4m3x2_f16x2(e[2 * y] >> 16),
+                           e4m3x2_f16x2(e[2 * y + 1]), e4m3x2_f16x2(e[2 * y + 1] >> 16));
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(bVfull + 8 * st);
+        if (++st == C::VST) st = 0, ph ^= 1;
+        ++step;
+        return true;
+      };
+      uint4 c[2][kAt];
+      bool there[2], next = lookup();
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        there[n] = next;
+        if (next) load(c[n]);
+        next = next && lookup();
+      }
+      for (bool on = true; on;) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          if (!there[n] || !write(c[n])) {
+            on = false;
+            break;
+          }
+          there[n] = next;
+          if (next) load(c[n]);
+          next = next && lookup();
+        }
+      }
+    } else {
+      const bool is_v = warp >= 8;
+      const int r = threadIdx.x & 127;  // token of the tile
+      const uint8_t *codes = is_v ? p.c.v_codes : p.c.k_codes;
+      const uint8_t *scales = is_v ? p.c.v_scales : p.c.k_scales;
+      uint8_t *tiles = smem + (is_v ? C::OFF_V : C::OFF_K);
+      const uint32_t full = is_v ? bVfull : bKfull, empty = is_v ? bVempty : bKempty;
+      bool past = false;
+      struct Row : F::Row {
+        bool valid, past;  // past: behind the sequence
+      };
+      auto load = [&](Row &x, long long row) {
+        x.valid = row >= 0;
+        x.past = past;
         if (row >= 0) x.load(codes, scales, row);
-      if constexpr (F::kBlockScales)
-        if (!is_v && (r & 15) == 0) x.load_scales(p.c, row);
-    };
-    // The cursor runs over the steps of all parts, two ahead of the one that
-    // is written: its page is on its way while the step before it is loaded.
-    Part x;
-    bool have = next_part(p, ctl, walk, x);
-    int j = have ? x.lo : 0, id = -1, off = 0, head = 0;
-    const int bs = 1 << p.c.bs_log2;
-    auto lookup = [&]() {  // the cursor's page, then one step on; whether there was a step
-      const bool was = have;
-      const int t = j * 128 + r;
-      past = t >= x.s.nk;
-      id = have && !past
-               ? __ldg(p.table + static_cast<long long>(x.b) * p.width + (t >> p.c.bs_log2))
-               : -1;
-      off = t & (bs - 1);
-      head = x.h;
-      if (have && ++j >= x.hi) {
-        have = next_part(p, ctl, walk, x);
-        j = x.lo;
-      }
-      return was;
-    };
-    auto row_of = [&]() -> long long {
-      if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.c.num_blocks)) return -1;
-      return ((static_cast<long long>(id) * p.c.Hk + head) << p.c.bs_log2) + off;
-    };
-    const int stages = is_v ? C::VST : C::KST;
-    Row row;
-    bool now = lookup();
-    load(row, row_of());
-    if constexpr (F::kStreams) row.begin(codes, row_of());
-    bool next = lookup();
-    for (int step = 0, st = 0, ph = 0; now; ++step) {
-      if (is_v && ctl.skip_load && step == 0) {  // test hook: the P V issuer's wait runs out
-        if (r == 0) atomicOr(ctl.status, kStatusInjected);
-        break;
-      }
-      if (!__all_sync(~0u, step < stages || bounded_wait(empty + 8 * st, ph ^ 1, w))) break;
-      if (!is_v) {
-        const unsigned bits = __ballot_sync(~0u, row.valid || row.past);
-        if (lane == 0)
-          reinterpret_cast<unsigned *>(smem + C::OFF_MASK)[(step % C::MASKS) * 4 + warp - 4] = bits;
-        if constexpr (F::kBlockScales)
-          if ((r & 15) == 0)
-            reinterpret_cast<float4 *>(smem + C::OFF_SCALE +
-                                       step % C::MASKS * C::SCALES)[r / 16] = row.scales();
-      }
-      // unit u of a chunk of row y is at u ^ (y & 7)
-      uint8_t *tile = tiles + st * C::TILE;
-      if constexpr (F::kStreams)
-        row.stream(codes, next ? row_of() : -1, tile + (r & ~31) * 128, C::CHUNK);
-      else
+      };
+      // The cursor runs over the steps of all parts, two ahead of the one that
+      // is written: its page is on its way while the step before it is loaded.
+      Part x;
+      bool have = next_part(p, ctl, walk, x);
+      int j = have ? x.lo : 0, id = -1, off = 0, head = 0;
+      const int bs = 1 << p.c.bs_log2;
+      auto lookup = [&]() {  // the cursor's page, then one step on; whether there was a step
+        const bool was = have;
+        const int t = j * 128 + r;
+        past = t >= x.s.nk;
+        id = have && !past
+                 ? __ldg(p.table + static_cast<long long>(x.b) * p.width + (t >> p.c.bs_log2))
+                 : -1;
+        off = t & (bs - 1);
+        head = x.h;
+        if (have && ++j >= x.hi) {
+          have = next_part(p, ctl, walk, x);
+          j = x.lo;
+        }
+        return was;
+      };
+      auto row_of = [&]() -> long long {
+        if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.c.num_blocks)) return -1;
+        return ((static_cast<long long>(id) * p.c.Hk + head) << p.c.bs_log2) + off;
+      };
+      const int stages = is_v ? C::VST : C::KST;
+      Row row;
+      bool now = lookup();
+      load(row, row_of());
+      bool next = lookup();
+      for (int step = 0, st = 0, ph = 0; now; ++step) {
+        if (is_v && ctl.skip_load && step == 0) {  // test hook: the P V issuer's wait runs out
+          if (r == 0) atomicOr(ctl.status, kStatusInjected);
+          break;
+        }
+        if (!__all_sync(~0u, step < stages || bounded_wait(empty + 8 * st, ph ^ 1, w))) break;
+        if (!is_v) {
+          const unsigned bits = __ballot_sync(~0u, row.valid || row.past);
+          if (lane == 0)
+            reinterpret_cast<unsigned *>(smem + C::OFF_MASK)[(step % C::MASKS) * 4 + warp - 4] = bits;
+        }
         row.expand(row.valid, [&](int unit) {
-          return reinterpret_cast<uint4 *>(tile + (unit >> 3) * C::CHUNK + r * 128 +
+          return reinterpret_cast<uint4 *>(tiles + st * C::TILE + (unit >> 3) * C::CHUNK + r * 128 +
                                            (((unit & 7) ^ (r & 7)) << 4));
         });
-      fence_proxy_async_smem();
-      mbar_arrive(full + 8 * st);
-      if (++st == stages) st = 0, ph ^= 1;
-      if (next) load(row, row_of());
-      now = next;
-      next = next && lookup();
+        fence_proxy_async_smem();
+        mbar_arrive(full + 8 * st);
+        if (++st == stages) st = 0, ph ^= 1;
+        if (next) load(row, row_of());
+        now = next;
+        next = next && lookup();
+      }
     }
   } else {
     setmaxnreg_inc<kRegSoftmax>();
@@ -584,10 +786,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int n = 0; n < 8; ++n) part[n] = -INFINITY;
 #pragma unroll
             for (int c = 0; c < 128; c += 2) {
-              const int n = F::kBlockScales ? c / 16 : (c >> 1) & 7;
+              const int n = C::kDirect ? c / 16 : (c >> 1) & 7;
               part[n] = max3f(part[n], S(c), S(c + 1));
             }
-            if constexpr (F::kBlockScales) {
+            if constexpr (C::kDirect) {
 #pragma unroll
               for (int n = 0; n < 8; ++n) {
                 const float4 x = scale_at(n);
@@ -597,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float mx = max3f(max3f(part[0], part[1], part[2]),
                                    max3f(part[3], part[4], part[5]), fmaxf(part[6], part[7]));
             const float m_new =
-                fmaxf(m_used, F::kBlockScales ? mx - kHeadroom : fmaf(mx, sl2, -kHeadroom));
+                fmaxf(m_used, C::kDirect ? mx - kHeadroom : fmaf(mx, sl2, -kHeadroom));
             if (j == x.lo) {
               m_used = m_new;
             } else {
@@ -639,14 +841,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint64_t sl2_2 = pk2(sl2, sl2), nm_2 = pk2(off, off);
           uint64_t acc[2] = {0ull, 0ull};
           float4 scale = {};
-          if constexpr (F::kBlockScales) tsum = wsum = 0.f;
+          if constexpr (C::kDirect) tsum = wsum = 0.f;
 #pragma unroll
           for (int blk = 0; blk < 2; ++blk) {
             uint32_t pk[32];
 #pragma unroll
             for (int n = 0; n < 32; ++n) {
               const int c0 = 2 * (blk * 32 + n);
-              if (F::kBlockScales && n % 8 == 0) {
+              if (C::kDirect && n % 8 == 0) {
                 scale = scale_at(c0 / 16);
                 sl2_2 = pk2(scale.x, scale.x);
                 nm_2 = pk2(scale.y + off, scale.y + off);
@@ -657,7 +859,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
               acc[n & 1] = fadd2(acc[n & 1], pk2(p0, p1));
               pk[n] = pack_f16x2(p0, p1);
-              if (F::kBlockScales && n % 8 == 7) {
+              if (C::kDirect && n % 8 == 7) {
                 float a0, a1;
                 upk2(fadd2(acc[0], acc[1]), a0, a1);
                 tsum += a0 + a1;
@@ -666,7 +868,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tmem_st32(s_tm + blk * 32, pk);
           }
-          if constexpr (!F::kBlockScales) {
+          if constexpr (!C::kDirect) {
             float a0, a1, b0, b1;
             upk2(acc[0], a0, a1);
             upk2(acc[1], b0, b1);
@@ -677,7 +879,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st_wait();  // the second pass rewrites the same columns
         }
         if (!ok) break;
-        l += F::kBlockScales ? wsum : tsum;
+        l += C::kDirect ? wsum : tsum;
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(bPfull + 8 * buf);
@@ -756,9 +958,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <typename T, class F>
-cudaError_t launch_many(const KvAttn &p, const ManyCtl &ctl, float *ws, int ctas, cudaStream_t s) {
+cudaError_t launch_many(const KvAttn &p, const ManyCtl &ctl, float *ws,
+                        const typename F::Keys &keys, int ctas, cudaStream_t s) {
   static std::atomic<unsigned long long> attr_done{0};
-  constexpr int smem = ManyCfg<F>::SMEM;
+  constexpr int smem = ManyCfg<F, T>::SMEM;
   cudaError_t e = smem_attr_once(fa_kv_many_kernel<T, F>, smem, &attr_done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -771,7 +974,7 @@ cudaError_t launch_many(const KvAttn &p, const ManyCtl &ctl, float *ws, int ctas
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, fa_kv_many_kernel<T, F>, p, ctl, ws);
+  e = cudaLaunchKernelEx(&cfg, fa_kv_many_kernel<T, F>, p, ctl, ws, keys);
   if (e != cudaSuccess || ctas == 1) return e;
   cfg.gridDim = dim3(static_cast<unsigned>(ctas - 1), R / kJoinRows);
   cfg.blockDim = dim3(kJoinThreads);

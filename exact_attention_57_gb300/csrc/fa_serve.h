@@ -5,6 +5,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 namespace fa {
@@ -18,6 +19,9 @@ int api_device_status(unsigned **status);
 int api_sm_count();
 unsigned long long api_wait_limit();
 int api_skip_load();  // the test hook of fa_set_test_hooks
+// A map of bytes [blocks][rows][row of 64 or 128], boxes of 16 rows swizzled by the row's
+// length; 0 or a failure.  (Host work alone.)
+int api_encode_bytes(CUtensorMap *map, const void *base, int row, long long rows, long long blocks);
 
 // ------------------------------------------------------------ block tables
 struct PlanParams {
