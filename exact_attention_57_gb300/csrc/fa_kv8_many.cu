@@ -16,20 +16,16 @@ struct Many8 {
   template <typename T>
   static constexpr int kTerms = std::is_same_v<T, __half> ? 3 : 2;
   struct Keys {
-    CUtensorMap map;  // [block][all heads' tokens][D]
+    CUtensorMap k, v;  // [block][all heads' tokens][D], k's swizzled
   };
-  static __device__ __forceinline__ float4 scales(float k, float v) {
-    BlockScale s;
-    s.set(k, v);
-    return make_float4(s.k, s.v_log, s.v_inv, 0.f);
-  }
 };
 
 template <typename T, int D>
 cudaError_t launch_type(const KvAttn &p, const ManyCtl &ctl, float *ws, int ctas, cudaStream_t s) {
   typename Many8<D>::Keys keys;
-  if (api_encode_bytes(&keys.map, p.c.k_codes, D, static_cast<long long>(p.c.Hk) << p.c.bs_log2,
-                       p.c.num_blocks) != 0)
+  const long long rows = static_cast<long long>(p.c.Hk) << p.c.bs_log2;
+  if (api_encode_bytes(&keys.k, p.c.k_codes, D, rows, p.c.num_blocks, 1 << p.c.bs_log2, true) != 0 ||
+      api_encode_bytes(&keys.v, p.c.v_codes, D, rows, p.c.num_blocks, 1 << p.c.bs_log2, false) != 0)
     return cudaErrorUnknown;
   return launch_many<T, Many8<D>>(p, ctl, ws, keys, ctas, s);
 }
