@@ -1228,23 +1228,5 @@ unsigned long long api_wait_limit() {
   return lim ? lim : kDefaultWaitLimitNs;
 }
 int api_skip_load() { return g_skip_v_load.load(); }
-int api_encode_bytes(CUtensorMap *map, const void *base, int row, long long rows, long long blocks,
-                     int box_rows, bool swizzled) {
-  const int rc = get_encoder();
-  if (rc != FA_OK) return rc;
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(row), static_cast<cuuint64_t>(rows),
-                        static_cast<cuuint64_t>(blocks)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(row), static_cast<cuuint64_t>(row * rows)};
-  cuuint32_t box[3] = {static_cast<cuuint32_t>(row), static_cast<cuuint32_t>(box_rows), 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  const CUresult r = g_encode(
-      map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
-      CU_TENSOR_MAP_INTERLEAVE_NONE,
-      !swizzled    ? CU_TENSOR_MAP_SWIZZLE_NONE
-      : row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
-                   : CU_TENSOR_MAP_SWIZZLE_64B,
-      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
-}
 
 }  // namespace fa

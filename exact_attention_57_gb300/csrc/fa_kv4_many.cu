@@ -24,10 +24,7 @@ namespace {
 template <int D_>
 struct Many4 {
   static constexpr int D = D_;
-  static constexpr bool kDirectKeys = false;
-  template <typename>
-  static constexpr int kTerms = 1;
-  struct Keys {};
+  static constexpr bool kBlockScales = false, kStreams = false;
 
   struct Row {
     uint4 c[D / 32];
@@ -73,10 +70,10 @@ cudaError_t launch_kv4_many(const KvAttn &p, const KvGrid &g, int dtype, float *
                             cudaStream_t s) {
   const ManyCtl ctl = {status, wait_limit_ns, skip_load, g.rows, R / p.group};
   if (dtype == FA_DTYPE_BF16)
-    return p.c.d == 64 ? launch_many<__nv_bfloat16, Many4<64>>(p, ctl, ws, {}, g.many, s)
-                       : launch_many<__nv_bfloat16, Many4<128>>(p, ctl, ws, {}, g.many, s);
-  return p.c.d == 64 ? launch_many<__half, Many4<64>>(p, ctl, ws, {}, g.many, s)
-                     : launch_many<__half, Many4<128>>(p, ctl, ws, {}, g.many, s);
+    return p.c.d == 64 ? launch_many<__nv_bfloat16, Many4<64>>(p, ctl, ws, g.many, s)
+                       : launch_many<__nv_bfloat16, Many4<128>>(p, ctl, ws, g.many, s);
+  return p.c.d == 64 ? launch_many<__half, Many4<64>>(p, ctl, ws, g.many, s)
+                     : launch_many<__half, Many4<128>>(p, ctl, ws, g.many, s);
 }
 
 }  // namespace fa

@@ -24,30 +24,8 @@ __device__ __forceinline__ uint32_t f32x2_e4m3x2(float lo, float hi) {
   return r;
 }
 
-// Two fp16 as e4m3 numbers in the low 16 bits, likewise; a NaN stays one.
-__device__ __forceinline__ uint32_t f16x2_e4m3x2(uint32_t x) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 h;\n\tcvt.rn.satfinite.e4m3x2.f16x2 h, %1;\n\tcvt.u32.u16 %0, h;\n\t}\n"
-      : "=r"(r) : "r"(x));
-  return r;
-}
-
-// Difference of two fp16 pairs.
-__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
-  uint32_t y;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
-  return y;
-}
-
 // Exponents of the scales that are stored.
 constexpr int kScaleExp = 40;
-
-// Values' scales count as the nearest in 2^-40 .. 2^40 (so that sums of weights w, and of
-// w / vs, lose nothing to fp32's range: a weight below 2^-126 of the largest is 2^-46 of
-// the sum at most).
-__device__ __forceinline__ float clamp_scale(float vs) {
-  return fminf(fmaxf(vs, pow2(-kScaleExp)), pow2(kScaleExp));
-}
 
 // What the softmax needs of a block's scales: weights carry the value's scale,
 //   2^(s + log2 vs - m) = e^(score) vs 2^-m,
@@ -55,10 +33,12 @@ __device__ __forceinline__ float clamp_scale(float vs) {
 // weight is above the largest, whatever the scales of other blocks are.
 struct BlockScale {
   float k, v_log, v_inv;
-  // A scale that is not positive counts as zero for keys.
+  // A scale that is not positive counts as zero for keys; values' count as the
+  // nearest in 2^-40 .. 2^40 (so that sums of w and of w / vs lose nothing to fp32's
+  // range: a weight below 2^-126 of the largest is 2^-46 of the sum at most).
   __device__ __forceinline__ void set(float ks, float vs) {
     k = fmaxf(ks, 0.f);
-    vs = clamp_scale(vs);
+    vs = fminf(fmaxf(vs, pow2(-kScaleExp)), pow2(kScaleExp));
     // by the exponent and a number in 1 .. 2, whose logarithm is good to 2^-22; a
     // power of two, as fa_kv8_append stores them, has an exact one
     const uint32_t bits = __float_as_uint(vs);

@@ -1,8 +1,8 @@
 // fa_kv8_many.cu — attention of sequences with many queries over the paged 8-bit
 // cache: the kernel of fa_kv_many.cuh for codes of e4m3 with one scale for a block
-// of tokens of a key head.
-#include <type_traits>
-
+// of tokens of a key head.  Rows become fp16 by one conversion for two elements; the
+// scales go to the softmax, three numbers for 16 keys (BlockScale).
+#include "fa_kv8.cuh"
 #include "fa_kv_many.cuh"
 
 namespace fa {
@@ -11,24 +11,72 @@ namespace {
 template <int D_>
 struct Many8 {
   static constexpr int D = D_;
-  static constexpr bool kDirectKeys = true;
-  // Significant bits of T, four to a number.
-  template <typename T>
-  static constexpr int kTerms = std::is_same_v<T, __half> ? 3 : 2;
-  struct Keys {
-    CUtensorMap k, v;  // [block][all heads' tokens][D], k's swizzled
+  static constexpr bool kBlockScales = true, kStreams = true;
+
+  // Lane l takes 16 codes of every kRows-th token, from the one l / kLanes on, so that
+  // a load of the warp covers whole rows.
+  static constexpr int kLanes = D / 16, kRows = 32 / kLanes, kAt = kLanes;
+  struct Row {
+    uint4 c[kAt];
+    float ks, vs;
+
+    // The codes of one step: tokens 0 .. 15 and 16 .. 31 lie in one block each.
+    struct From {
+      const uint8_t *half[2];
+      unsigned good;  // tokens that there are
+      __device__ __forceinline__ From(const uint8_t *codes, long long row)
+          : good(__ballot_sync(~0u, row >= 0) >> ((threadIdx.x & 31) / kLanes)) {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+          half[n] = codes + (__shfl_sync(~0u, row, 16 * n) + lane / kLanes) * D + lane % kLanes * 16;
+      }
+      __device__ __forceinline__ uint4 piece(int i) const {
+        constexpr int kHalf = kAt / 2;
+        return good >> (i * kRows) & 1
+                   ? __ldg(reinterpret_cast<const uint4 *>(half[i / kHalf] + i % kHalf * kRows * D))
+                   : make_uint4(0, 0, 0, 0);
+      }
+    };
+    __device__ __forceinline__ void begin(const uint8_t *codes, long long row) {
+      const From from(codes, row);
+#pragma unroll
+      for (int i = 0; i < kAt; ++i) c[i] = from.piece(i);
+    }
+    // 8 codes make a unit.  The lanes of a row's second half store their units in the
+    // other order, so that eight lanes at a time meet every bank once.
+    __device__ __forceinline__ void stream(const uint8_t *codes, long long next, uint8_t *tile,
+                                           int chunk) {
+      const From from(codes, next);
+      const int lane = threadIdx.x & 31, u = 2 * (lane % kLanes);
+      const bool swap = u >= 8;
+      uint8_t *to = tile + (lane / kLanes) * 128 + (u >> 3) * chunk;
+#pragma unroll
+      for (int i = 0; i < kAt; ++i) {
+        const uint32_t w[4] = {swap ? c[i].z : c[i].x, swap ? c[i].w : c[i].y,
+                               swap ? c[i].x : c[i].z, swap ? c[i].y : c[i].w};
+        c[i] = from.piece(i);
+        const int low = (i * kRows + lane / kLanes) & 7;
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+          *reinterpret_cast<uint4 *>(to + i * kRows * 128 + ((((u + (n != swap)) & 7) ^ low) << 4)) =
+              make_uint4(e4m3x2_f16x2(w[2 * n]), e4m3x2_f16x2_hi(w[2 * n]),
+                         e4m3x2_f16x2(w[2 * n + 1]), e4m3x2_f16x2_hi(w[2 * n + 1]));
+      }
+    }
+    __device__ __forceinline__ void load_scales(const KvStore &p, long long row) {
+      ks = vs = 1.f;  // of a page that is missing: its scores are masked
+      if (row < 0) return;
+      ks = __ldg(reinterpret_cast<const float *>(p.k_scales) + (row >> p.bs_log2));
+      vs = __ldg(reinterpret_cast<const float *>(p.v_scales) + (row >> p.bs_log2));
+    }
+    __device__ __forceinline__ float4 scales() const {
+      BlockScale s;
+      s.set(ks, vs);
+      return make_float4(s.k, s.v_log, s.v_inv, 0.f);
+    }
   };
 };
-
-template <typename T, int D>
-cudaError_t launch_type(const KvAttn &p, const ManyCtl &ctl, float *ws, int ctas, cudaStream_t s) {
-  typename Many8<D>::Keys keys;
-  const long long rows = static_cast<long long>(p.c.Hk) << p.c.bs_log2;
-  if (api_encode_bytes(&keys.k, p.c.k_codes, D, rows, p.c.num_blocks, 1 << p.c.bs_log2, true) != 0 ||
-      api_encode_bytes(&keys.v, p.c.v_codes, D, rows, p.c.num_blocks, 1 << p.c.bs_log2, false) != 0)
-    return cudaErrorUnknown;
-  return launch_many<T, Many8<D>>(p, ctl, ws, keys, ctas, s);
-}
 
 }  // namespace
 
@@ -37,10 +85,10 @@ cudaError_t launch_kv8_many(const KvAttn &p, const KvGrid &g, int dtype, float *
                             cudaStream_t s) {
   const ManyCtl ctl = {status, wait_limit_ns, skip_load, g.rows, R / p.group};
   if (dtype == FA_DTYPE_BF16)
-    return p.c.d == 64 ? launch_type<__nv_bfloat16, 64>(p, ctl, ws, g.many, s)
-                       : launch_type<__nv_bfloat16, 128>(p, ctl, ws, g.many, s);
-  return p.c.d == 64 ? launch_type<__half, 64>(p, ctl, ws, g.many, s)
-                     : launch_type<__half, 128>(p, ctl, ws, g.many, s);
+    return p.c.d == 64 ? launch_many<__nv_bfloat16, Many8<64>>(p, ctl, ws, g.many, s)
+                       : launch_many<__nv_bfloat16, Many8<128>>(p, ctl, ws, g.many, s);
+  return p.c.d == 64 ? launch_many<__half, Many8<64>>(p, ctl, ws, g.many, s)
+                     : launch_many<__half, Many8<128>>(p, ctl, ws, g.many, s);
 }
 
 }  // namespace fa

@@ -9,41 +9,35 @@
 // equal shares, whatever the lengths, the mask and the number of tiles.
 //
 // Warps 0-3    softmax, correction and epilogue, one row a thread.
-// Warp 12, 13  issue S = Q K^T (three score buffers) and O += P V (P in tensor
-//              memory), fp32 accumulators; warp 12 owns the tensor memory.
-// The others bring Q, K and V into shared memory.  Tokens behind the sequence or on a
-// missing page become zeros and are reported in a bit mask.
-//
-// With F::kDirectKeys = false, keys and values become fp16 (exactly) and the products are
-// kind::f16:
 // Warps 4-7    expand the codes of K, warps 8-11 those of V: thread r loads
-//              token r of the 128 (a page lookup, the codes and the scales, one step
-//              ahead), turns them into fp16 and writes them as a 128-byte-swizzled row.
+//              token r of the 128 (a page lookup, the codes, the format's scales,
+//              one step ahead), turns them into fp16 (exactly)
+//              and writes them as a 128-byte-swizzled row.
+//              Tokens behind the sequence or on a missing page become zeros
+//              and are reported in a bit mask.
+// Warp 12, 13  issue S = Q K^T (three score buffers) and O += P V (P in tensor
+//              memory), kind::f16, fp32 accumulators; warp 12 owns the tensor
+//              memory.
 // Warp 14, 15  bring the next tile's Q into shared memory (two buffers), as
 //              fp16 times a power of two a row.
-// F has D and Row: load() of a token's codes, expand() to fp16 by 16-byte units.
 //
-// With F::kDirectKeys = true, the codes of K are e4m3 numbers and go to the tensor core as
-// they are (kind::f8f6f4), with Q as a sum of two or three e4m3 numbers; the scales of 16
-// keys are one number for each of K and V and enter the softmax (BlockScale):
-// Warp 14      copies the codes by TMA, 16 tokens a copy, and says which there are and
-//              their scales.
-// Warps 4-11   expand those of V to fp16, 16 tokens each, from shared memory.
-// Warp 15      brings the next tile's Q (two buffers).
-// F has D, kTerms<T> (numbers for Q) and Keys (maps of the codes, k and v).
+// A format F has D, kBlockScales (the scales of 16 keys are one number each, which
+// the softmax applies), and Row, a thread's share of the codes of its warp's 32
+// tokens.  Without kStreams: load() of the thread's own token, expand() to fp16 by
+// 16-byte units.  With kStreams: begin() loads the first step's, stream() turns one
+// step's into fp16 and each register, once free, over to the next step's codes.  With
+// kBlockScales, load_scales() and scales() by the threads of tokens 16 n.
 //
 // Every wait is bounded; on expiry the CTA raises its abort flag, records the
 // role in the status word, drains its products, frees tensor memory and ends.
 #include <atomic>
 #include <cfloat>
-#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "fa.h"
 #include "fa_internal.h"
-#include "fa_kv8.cuh"
 #include "fa_kv_split.cuh"
 #include "fa_wait.cuh"
 
@@ -62,45 +56,37 @@ struct ManyCtl {
 
 constexpr int WALK_BYTES = 80;
 
-template <class F, typename T>
+template <class F>
 struct ManyCfg {
   static constexpr int D = F::D;
-  static constexpr bool kDirect = F::kDirectKeys;
   static constexpr int NCH = D / 64;               // 128-byte chunks of a row
   static constexpr int CHUNK = 128 * 128;
-  static constexpr int TILE = NCH * CHUNK;         // 128 rows in fp16
-  static constexpr int RAW = 128 * D;              // and in bytes
-  static constexpr int TERMS = F::template kTerms<T>;
-  static constexpr int QT = kDirect ? TERMS * RAW : TILE;
-  static constexpr int KT = kDirect ? RAW : TILE;
+  static constexpr int TILE = NCH * CHUNK;
   static constexpr int NS = 3;                     // score buffers
-  static constexpr int KST = D == 64 ? 4 : TERMS == 3 ? 2 : 3;  // K stages
+  static constexpr int KST = D == 128 ? 3 : 4;     // K stages
   static constexpr int VST = D == 128 ? 2 : 4;     // V stages
   static constexpr int ST = KST > VST ? KST : VST;
-  static constexpr int RST = kDirect ? 2 : 0;      // stages of V's codes
   // Steps whose key masks (and scales) are kept: K of step n is expanded once S of
   // step n - KST is complete, which was issued when the softmax had done with step
   // n - KST - NS.
   static constexpr int MASKS = KST + NS;
   static constexpr uint32_t COL_O = NS * 128;
   static constexpr int OFF_Q = 0;
-  static constexpr int OFF_K = OFF_Q + 2 * QT;
-  static constexpr int OFF_V = OFF_K + KST * KT;
-  static constexpr int OFF_RAW = OFF_V + VST * TILE;
-  static constexpr int OFF_MASK = OFF_RAW + RST * RAW;
+  static constexpr int OFF_K = OFF_Q + 2 * TILE;
+  static constexpr int OFF_V = OFF_K + KST * TILE;
+  static constexpr int OFF_MASK = OFF_V + VST * TILE;
   // An exponent a row of the tiles in flight: Q of tile g is written when the
   // last S of tile g - 2 is complete, and with tiles of one step the softmax
   // may then still be at tile g - 4 (three score buffers).
   static constexpr int QES = 5;
-  // Of a step: K's scales of 16 keys each; V's, relative to their largest, as fp16 pairs;
-  // tokens that there are; log2 and inverse of V's largest.
-  static constexpr int SCALES = kDirect ? 96 : 0;
+  // Of 16 keys each, eight to a step: K's scale, log2 of V's, its inverse, nothing.
+  static constexpr int SCALES = F::kBlockScales ? 8 * 16 : 0;
   static constexpr int OFF_SCALE = OFF_MASK + MASKS * 16;
   static constexpr int OFF_QE = OFF_SCALE + MASKS * SCALES;
   static constexpr int OFF_BAR = OFF_QE + QES * 128;
   // qfull[2], qempty[2], ofree, fin[2], kfull, kempty, vfull, vempty [ST],
-  // sfull, pfull, odone [NS], rfull, rempty [RST]
-  static constexpr int NBAR = 7 + 4 * ST + 3 * NS + 2 * RST;
+  // sfull, pfull, odone [NS]
+  static constexpr int NBAR = 7 + 4 * ST + 3 * NS;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;  // tmem base, abort flag, CTAs, -, units
   static constexpr int OFF_SUMS = OFF_K;           // before the first tile arrives
   static constexpr int OFF_WALK = OFF_MISC + 24;     // a walk for each warp
@@ -215,10 +201,9 @@ __device__ __forceinline__ bool next_part(const KvAttn &p, const ManyCtl &c, Wal
 template <typename T, class F>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_kv_many_kernel(const __grid_constant__ KvAttn p, const __grid_constant__ ManyCtl ctl,
-                       float *ws, const __grid_constant__ typename F::Keys keys) {
+                       float *ws) {
   constexpr int D = F::D;
-  using C = ManyCfg<F, T>;
-  constexpr int kExpanders = C::kDirect ? 256 : 128;  // threads that expand V
+  using C = ManyCfg<F>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -230,7 +215,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t bVfull = bKempty + 8 * C::ST, bVempty = bVfull + 8 * C::ST;
   const uint32_t bSfull = bVempty + 8 * C::ST, bPfull = bSfull + 8 * C::NS;
   const uint32_t bOdone = bPfull + 8 * C::NS;
-  const uint32_t bRfull = bOdone + 8 * C::NS, bRempty = bRfull + 8 * C::RST;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
   int *s_den = reinterpret_cast<int *>(smem + C::OFF_MISC + 8);
@@ -249,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
-      mbar_init(bQfull + 8 * s, C::kDirect ? 32 : 64);
+      mbar_init(bQfull + 8 * s, 64);
       mbar_init(bQempty + 8 * s, 1);
     }
     mbar_init(bOfree, 128);
@@ -257,9 +241,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bFin + 8, 1);
 #pragma unroll
     for (int s = 0; s < C::ST; ++s) {
-      mbar_init(bKfull + 8 * s, C::kDirect ? 1 : 128);
+      mbar_init(bKfull + 8 * s, 128);
       mbar_init(bKempty + 8 * s, 1);
-      mbar_init(bVfull + 8 * s, kExpanders);
+      mbar_init(bVfull + 8 * s, 128);
       mbar_init(bVempty + 8 * s, 1);
     }
 #pragma unroll
@@ -267,11 +251,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bSfull + 8 * s, 1);
       mbar_init(bPfull + 8 * s, 128);
       mbar_init(bOdone + 8 * s, 1);
-    }
-#pragma unroll
-    for (int s = 0; s < C::RST; ++s) {
-      mbar_init(bRfull + 8 * s, 1);
-      mbar_init(bRempty + 8 * s, 8);
     }
     *abort_flag = 0;
     fence_barrier_init();
@@ -293,10 +272,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) reinterpret_cast<Share *>(ws)[blockIdx.x] = Share{0, 0, 0, 0};
   if (static_cast<int>(blockIdx.x) >= den) return;
   Walk *walk = reinterpret_cast<Walk *>(smem + C::OFF_WALK) + warp;
-  const long long share = at.total * (blockIdx.x + 1) / den - u0;  // steps in all
   if (lane == 0) {
     Walk k = {};
-    k.left = share;
+    k.left = at.total * (blockIdx.x + 1) / den - u0;
     k.b = at.b;
     k.s = load_seq(p, at.b);
     k.n = tiles_of(p, ctl, k.s);
@@ -343,23 +321,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (issued >= C::NS && !(ok = bounded_wait(bOdone + 8 * b, bph ^ 1, w))) break;
             if (!(ok = bounded_wait(bKfull + 8 * s, sph, w))) break;
             tc_fence_after();
-            if constexpr (C::kDirect) {
-              // the terms of Q one after the other, 32 elements a product
 #pragma unroll
-              for (int kk = 0; kk < C::TERMS * (D / 32); ++kk) {
-                const int term = kk / (D / 32), off = kk % (D / 32) * 32;
-                umma_f8(tmem + b * 128,
-                        sdesc_bytes<D>(sQ + (g & 1) * C::QT + term * C::RAW + off),
-                        sdesc_bytes<D>(sK + s * C::RAW + off), kIdesc, kk > 0 ? 1u : 0u);
-              }
-            } else {
-#pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = (kk >> 2) * C::CHUNK + (kk & 3) * 32;
-                umma_ss<false>(tmem + b * 128, sdesc_sw128(sQ + (g & 1) * C::TILE + off, 16, 1024),
-                               sdesc_sw128(sK + s * C::TILE + off, 16, 1024), kIdesc,
-                               kk > 0 ? 1u : 0u);
-              }
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = (kk >> 2) * C::CHUNK + (kk & 3) * 32;
+              umma_ss<false>(tmem + b * 128, sdesc_sw128(sQ + (g & 1) * C::TILE + off, 16, 1024),
+                             sdesc_sw128(sK + s * C::TILE + off, 16, 1024), kIdesc,
+                             kk > 0 ? 1u : 0u);
             }
             tc_commit(bKempty + 8 * s);
             tc_commit(bSfull + 8 * b);
@@ -405,100 +372,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_commit(bFin + 8);
         bounded_wait(bFin + 8, 0, w, false);
       }
-    } else if (C::kDirect && warp == 14) {
-      // ---------------------------------------------- codes as they lie in the cache
-      // Lane n of the first eight has keys 16 n and on of the 128: it says what the others
-      // have to know of them, and where a block begins there it copies K of the block,
-      // lane 8 + n V.
-      if constexpr (C::kDirect) {
-        w.role = kStatusProducer;
-        fence_proxy_async_smem();  // the stages held the prefix sums before
-        const bool with_v = !ctl.skip_load;  // (test hook: the P V issuer's wait runs out)
-        const bool v = lane >= 8;
-        const int off_mask = (1 << p.c.bs_log2) - 1;
-        // a copy is a block (they begin at multiples of their size in a step)
-        const bool begins = lane < 16 && ((lane & 7) * 16 & off_mask) == 0;
-        struct Keys16 {
-          int id, row, left;  // block (-1: none), row of all its heads', tokens from here on
-          float ks, vs;
-        } cur = {}, ahead = {};
-        // A step is looked up three ahead of its copies, its scales are loaded two ahead.
-        Part x;
-        bool have = next_part(p, ctl, walk, x), there[3] = {false, false, false};
-        int j = have ? x.lo : 0, t = 0, id = -1, head = 0, left = 0;
-        int done = 0, st = 0, ph = 0, sr = 0, rph = 0;
-        for (int turn = 0; turn < 3 || there[0]; ++turn) {
-          if (there[0]) {
-            bool ok = done < C::KST || bounded_wait(bKempty + 8 * st, ph ^ 1, w);
-            if (with_v && ok) ok = done < C::RST || bounded_wait(bRempty + 8 * sr, rph ^ 1, w);
-            if (!__all_sync(~0u, ok)) break;
-            const bool is = cur.id >= 0;
-            if (is && begins && (!v || with_v))
-              tma_load_3d((v ? sbase + C::OFF_RAW + sr * C::RAW : sK + st * C::RAW) +
-                              (lane & 7) * 16 * D,
-                          v ? &keys.v : &keys.k, v ? bRfull + 8 * sr : bKfull + 8 * st, 0, cur.row,
-                          cur.id);
-            const unsigned copies = __popc(__ballot_sync(~0u, is && begins) & 0xFFu);
-            const unsigned bits = __ballot_sync(~0u, is || cur.left <= 0);
-            uint8_t *to = smem + C::OFF_SCALE + done % C::MASKS * C::SCALES;
-            const float mine = clamp_scale(is ? cur.vs : 0.f);
-            float top = mine;
-#pragma unroll
-            for (int o = 1; o < 8; o *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-            BlockScale sc;
-            sc.set(is ? cur.ks : 0.f, top);
-            if (lane < 8) {
-              const float part = __fdividef(mine, top);
-              reinterpret_cast<float *>(to)[lane] = sc.k;
-              reinterpret_cast<uint32_t *>(to)[8 + lane] = pack_f16x2(part, part);
-              reinterpret_cast<uint16_t *>(to)[32 + lane] =
-                  static_cast<uint16_t>(!is ? 0 : cur.left >= 16 ? 0xFFFF : (1 << cur.left) - 1);
-              if (lane == 0)
-                *reinterpret_cast<float2 *>(to + 80) = make_float2(sc.v_log, sc.v_inv);
-              if (lane < 4)
-                reinterpret_cast<unsigned *>(smem + C::OFF_MASK)[(done % C::MASKS) * 4 + lane] =
-                    (bits >> (2 * lane) & 1 ? 0xFFFFu : 0u) |
-                    (bits >> (2 * lane + 1) & 1 ? 0xFFFF0000u : 0u);
-            }
-            __syncwarp();
-            if ((lane == 0 || lane == 8) && (!v || with_v))
-              mbar_arrive_expect_tx(v ? bRfull + 8 * sr : bKfull + 8 * st, copies * (D << p.c.bs_log2));
-            if (++st == C::KST) st = 0, ph ^= 1;
-            if (with_v && ++sr == C::RST) sr = 0, rph ^= 1;
-            ++done;
-          }
-          cur = ahead;
-          if (there[2]) {  // the block that was looked up
-            ahead.id = static_cast<unsigned>(id) < static_cast<unsigned>(p.c.num_blocks) ? id : -1;
-            ahead.left = left;
-            ahead.row = (head << p.c.bs_log2) + (t & off_mask);
-            if (ahead.id >= 0) {
-              const long long at = static_cast<long long>(ahead.id) * p.c.Hk + head;
-              ahead.ks = __ldg(reinterpret_cast<const float *>(p.c.k_scales) + at);
-              ahead.vs = __ldg(reinterpret_cast<const float *>(p.c.v_scales) + at);
-            }
-          }
-          there[0] = there[1], there[1] = there[2], there[2] = have;
-          if (have) {  // the cursor's block, then one step on
-            t = j * 128 + 16 * (lane & 7);
-            left = x.s.nk - t;
-            id = left > 0 ? __ldg(p.table + static_cast<long long>(x.b) * p.width + (t >> p.c.bs_log2))
-                          : -1;
-            head = x.h;
-            if (++j >= x.hi) {
-              have = next_part(p, ctl, walk, x);
-              j = x.lo;
-            }
-          }
-        }
-        // no copy may be on its way when the CTA ends
-        if (lane == 0)
-          for (int n = max(done - C::KST, 0); n < done; ++n)
-            bounded_wait(bKfull + 8 * (n % C::KST), n / C::KST & 1, w, false);
-        if (lane == 0 && with_v)
-          for (int n = max(done - C::RST, 0); n < done; ++n)
-            bounded_wait(bRfull + 8 * (n % C::RST), n / C::RST & 1, w, false);
-      }
     } else {
       // ---------------------------------------------- Q rows
       w.role = kStatusProducer;
@@ -508,105 +381,39 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int g = 0; next_part(p, ctl, walk, x); ++g) {
         if (!__all_sync(~0u, g < 2 || bounded_wait(bQempty + 8 * (g & 1), ((g >> 1) - 1) & 1, w)))
           break;
-        uint8_t *tile = smem + C::OFF_Q + (g & 1) * C::QT;
-        if constexpr (C::kDirect) {
-          // Q as a sum of e4m3 numbers, four significant bits each, of elements scaled to
-          // 256 at most: two hold bf16's eight bits, three fp16's eleven, of elements that
-          // are not far below the row's largest (each is off by 2^-10 at most, half of
-          // e4m3's smallest step, 2^-17 of the largest).  A row with an infinity becomes
-          // NaN, as e4m3 has none.  A lane takes 16 elements of a row.
-          constexpr int kLanes = D / 16, kRows = 32 / kLanes, kAt = 2;
-          const int u = lane % kLanes;
+        uint8_t *tile = smem + C::OFF_Q + (g & 1) * C::TILE;
 #pragma unroll 1
-          for (int r0 = lane / kLanes; r0 < R; r0 += kAt * kRows) {
-            uint4 q[kAt][2];
-#pragma unroll
-            for (int n = 0; n < kAt; ++n) {
-              const int r = r0 + n * kRows;
-              const int ti = r / p.group, tj = r - ti * p.group, i = x.qt * ctl.tokens + ti;
-              const bool in = ti < ctl.tokens && i < x.s.nq;
-              const uint4 *src = reinterpret_cast<const uint4 *>(
-                  static_cast<const T *>(p.q) +
-                  (in ? (static_cast<long long>(x.s.r0 + i) * p.Hq + x.h * p.group + tj) * D : 0));
-              q[n][0] = in ? __ldg(src + 2 * u) : make_uint4(0, 0, 0, 0);
-              q[n][1] = in ? __ldg(src + 2 * u + 1) : make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int n = 0; n < kAt; ++n) {
-              const int r = r0 + n * kRows;
-              using P = std::conditional_t<std::is_same_v<T, __half>, __half2, __nv_bfloat162>;
-              const P *f = reinterpret_cast<const P *>(q[n]);
-              P top = __habs2(f[0]);
-#pragma unroll
-              for (int c = 1; c < 8; ++c) top = __hmax2(top, __habs2(f[c]));
-              float amax = fmaxf(static_cast<float>(top.x), static_cast<float>(top.y));
-#pragma unroll
-              for (int c = 1; c < kLanes; c *= 2) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, c));
-              const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -119), 127);
-              const float mul =
-                  pow2(7 - e) * (amax == INFINITY ? __int_as_float(0x7FC00000) : sign);
-              uint32_t y[8];  // pairs, in fp16
-#pragma unroll
-              for (int c = 0; c < 8; ++c)
-                y[c] = pack_f16x2(static_cast<float>(f[c].x) * mul, static_cast<float>(f[c].y) * mul);
-              // 128-byte rows swizzle by the row in eight, 64-byte rows by its half
-              uint8_t *to = tile + r * D + (D == 128 ? u ^ (r & 7) : u ^ (r >> 1 & 3)) * 16;
-#pragma unroll
-              for (int term = 0; term < C::TERMS; ++term) {
-                uint32_t v[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                  uint32_t part[2];
-#pragma unroll
-                  for (int z = 0; z < 2; ++z) {  // four significant bits, and the rest
-                    const uint32_t all = y[2 * c + z];
-                    const uint32_t head = term + 1 < C::TERMS ? all & 0xFF80FF80u : all;
-                    part[z] = f16x2_e4m3x2(head);
-                    if (term + 1 < C::TERMS) y[2 * c + z] = hsub2(all, head);
-                  }
-                  v[c] = part[0] | part[1] << 16;
-                }
-                *reinterpret_cast<uint4 *>(to + term * C::RAW) = make_uint4(v[0], v[1], v[2], v[3]);
-              }
-              if (u == 0)  // the row is scaled by 2^(7 - e)
-                reinterpret_cast<int8_t *>(smem + C::OFF_QE)[g % C::QES * 128 + r] =
-                    static_cast<int8_t>(e - 7);
-            }
-          }
-        } else {
-#pragma unroll 1
-          for (int n = 0; n < 2; ++n) {
-            const int r = (threadIdx.x & 63) + 64 * n;
-            const int ti = r / p.group, tj = r - ti * p.group, i = x.qt * ctl.tokens + ti;
-            const bool in = ti < ctl.tokens && i < x.s.nq;
-            float amax = 0.f;
-            const uint4 *src = reinterpret_cast<const uint4 *>(
-                static_cast<const T *>(p.q) +
-                (in ? (static_cast<long long>(x.s.r0 + i) * p.Hq + x.h * p.group + tj) * D : 0));
+        for (int n = 0; n < 2; ++n) {
+          const int r = (threadIdx.x & 63) + 64 * n;
+          const int ti = r / p.group, tj = r - ti * p.group, i = x.qt * ctl.tokens + ti;
+          const bool in = ti < ctl.tokens && i < x.s.nq;
+          float amax = 0.f;
+          const uint4 *src = reinterpret_cast<const uint4 *>(
+              static_cast<const T *>(p.q) +
+              (in ? (static_cast<long long>(x.s.r0 + i) * p.Hq + x.h * p.group + tj) * D : 0));
 #pragma unroll 4
-            for (int u = 0; u < D / 8; ++u) {
-              const uint4 q = in ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
-              const T *f = reinterpret_cast<const T *>(&q);
+          for (int u = 0; u < D / 8; ++u) {
+            const uint4 q = in ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
+            const T *f = reinterpret_cast<const T *>(&q);
 #pragma unroll
-              for (int y = 0; y < 8; ++y) amax = fmaxf(amax, fabsf(static_cast<float>(f[y])));
-            }
-            // 2^e brings the row's largest element to 1 .. 2 (an exact scaling)
-            const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -126), 126);
-            const float mul = pow2(-e) * sign;
-#pragma unroll 4
-            for (int u = 0; u < D / 8; ++u) {
-              const uint4 q = in ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
-              const T *f = reinterpret_cast<const T *>(&q);
-              uint4 v;
-              v.x = pack_f16x2(static_cast<float>(f[0]) * mul, static_cast<float>(f[1]) * mul);
-              v.y = pack_f16x2(static_cast<float>(f[2]) * mul, static_cast<float>(f[3]) * mul);
-              v.z = pack_f16x2(static_cast<float>(f[4]) * mul, static_cast<float>(f[5]) * mul);
-              v.w = pack_f16x2(static_cast<float>(f[6]) * mul, static_cast<float>(f[7]) * mul);
-              *reinterpret_cast<uint4 *>(tile + (u >> 3) * C::CHUNK + r * 128 +
-                                         (((u & 7) ^ (r & 7)) << 4)) = v;
-            }
-            reinterpret_cast<int8_t *>(smem + C::OFF_QE)[g % C::QES * 128 + r] = static_cast<int8_t>(e);
+            for (int y = 0; y < 8; ++y) amax = fmaxf(amax, fabsf(static_cast<float>(f[y])));
           }
+          // 2^e brings the row's largest element to 1 .. 2 (an exact scaling)
+          const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -126), 126);
+          const float mul = pow2(-e) * sign;
+#pragma unroll 4
+          for (int u = 0; u < D / 8; ++u) {
+            const uint4 q = in ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
+            const T *f = reinterpret_cast<const T *>(&q);
+            uint4 v;
+            v.x = pack_f16x2(static_cast<float>(f[0]) * mul, static_cast<float>(f[1]) * mul);
+            v.y = pack_f16x2(static_cast<float>(f[2]) * mul, static_cast<float>(f[3]) * mul);
+            v.z = pack_f16x2(static_cast<float>(f[4]) * mul, static_cast<float>(f[5]) * mul);
+            v.w = pack_f16x2(static_cast<float>(f[6]) * mul, static_cast<float>(f[7]) * mul);
+            *reinterpret_cast<uint4 *>(tile + (u >> 3) * C::CHUNK + r * 128 +
+                                       (((u & 7) ^ (r & 7)) << 4)) = v;
+          }
+          reinterpret_cast<int8_t *>(smem + C::OFF_QE)[g % C::QES * 128 + r] = static_cast<int8_t>(e);
         }
         fence_proxy_async_smem();
         mbar_arrive(bQfull + 8 * (g & 1));
@@ -617,127 +424,85 @@ __global__ void __launch_bounds__(kThreads, 1)
     setmaxnreg_dec<kRegExpand>();
     // ------------------------------------------------ codes -> fp16 rows
     w.role = kStatusProducer;
-    if constexpr (C::kDirect) {
-      // Of V alone, 16 tokens a warp, from shared memory.  A lane takes 16 codes of every
-      // kRows-th token.  V is relative to the largest scale of the step's 128 tokens (exact
-      // for powers of two 2^15 apart); tokens that are not there become zeros.
-      constexpr int kLanes = D / 16, kRows = 32 / kLanes, kAt = 16 / kRows;
-      const int group = warp - 4, y0 = lane / kLanes, steps = static_cast<int>(min(share, 2147483647ll));
-      int st = 0, ph = 0, sr = 0, rph = 0;
-      // 8 codes make a unit of 16 bytes, at u ^ (row & 7) of its chunk.  The lanes of a
-      // row's second half store theirs in the other order, so that eight lanes at a time
-      // meet every bank once.
-      const int u = 2 * (lane % kLanes);
-      const bool swap = u >= 8;
-      if (ctl.skip_load) {  // test hook: the P V issuer's wait runs out
-        if (threadIdx.x == 128) atomicOr(ctl.status, kStatusInjected);
-      } else {
-#pragma unroll 1
-        for (int step = 0; step < steps; ++step) {
-          if (!__all_sync(~0u, bounded_wait(bRfull + 8 * sr, rph, w))) break;
-          const uint8_t *scales = smem + C::OFF_SCALE + step % C::MASKS * C::SCALES;
-          const uint32_t f = reinterpret_cast<const uint32_t *>(scales)[8 + group];
-          const unsigned there = reinterpret_cast<const uint16_t *>(scales)[32 + group] >> y0;
-          const uint4 *from = reinterpret_cast<const uint4 *>(
-              smem + C::OFF_RAW + sr * C::RAW + (16 * group + y0) * D + lane % kLanes * 16);
-          uint4 c[kAt];
-#pragma unroll
-          for (int n = 0; n < kAt; ++n) {
-            c[n] = from[n * kRows * D / 16];
-            if (!(there >> (n * kRows) & 1)) c[n] = make_uint4(0, 0, 0, 0);
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bRempty + 8 * sr);
-          if (++sr == C::RST) sr = 0, rph ^= 1;
-          if (!__all_sync(~0u, step < C::VST || bounded_wait(bVempty + 8 * st, ph ^ 1, w))) break;
-          uint8_t *to = smem + C::OFF_V + st * C::TILE + (16 * group + y0) * 128 + (u >> 3) * C::CHUNK;
-#pragma unroll
-          for (int n = 0; n < kAt; ++n) {
-            const uint32_t e[4] = {swap ? c[n].z : c[n].x, swap ? c[n].w : c[n].y,
-                                   swap ? c[n].x : c[n].z, swap ? c[n].y : c[n].w};
-            const int low = (n * kRows + y0) & 7;
-#pragma unroll
-            for (int y = 0; y < 2; ++y)
-              *reinterpret_cast<uint4 *>(to + n * kRows * 128 +
-                                         ((((u + (y != swap)) & 7) ^ low) << 4)) =
-                  make_uint4(hmul2(e4m3x2_f16x2(e[2 * y]), f),
-                             hmul2(e4m3x2_f16x2(e[2 * y] >> 16), f),
-                             hmul2(e4m3x2_f16x2(e[2 * y + 1]), f),
-                             hmul2(e4m3x2_f16x2(e[2 * y + 1] >> 16), f));
-          }
-          fence_proxy_async_smem();
-          mbar_arrive(bVfull + 8 * st);
-          if (++st == C::VST) st = 0, ph ^= 1;
-        }
-      }
-    } else {
-      const bool is_v = warp >= 8;
-      const int r = threadIdx.x & 127;  // token of the tile
-      const uint8_t *codes = is_v ? p.c.v_codes : p.c.k_codes;
-      const uint8_t *scales = is_v ? p.c.v_scales : p.c.k_scales;
-      uint8_t *tiles = smem + (is_v ? C::OFF_V : C::OFF_K);
-      const uint32_t full = is_v ? bVfull : bKfull, empty = is_v ? bVempty : bKempty;
-      bool past = false;
-      struct Row : F::Row {
-        bool valid, past;  // past: behind the sequence
-      };
-      auto load = [&](Row &x, long long row) {
-        x.valid = row >= 0;
-        x.past = past;
+    const bool is_v = warp >= 8;
+    const int r = threadIdx.x & 127;  // token of the tile
+    const uint8_t *codes = is_v ? p.c.v_codes : p.c.k_codes;
+    const uint8_t *scales = is_v ? p.c.v_scales : p.c.k_scales;
+    uint8_t *tiles = smem + (is_v ? C::OFF_V : C::OFF_K);
+    const uint32_t full = is_v ? bVfull : bKfull, empty = is_v ? bVempty : bKempty;
+    bool past = false;
+    struct Row : F::Row {
+      bool valid, past;  // past: behind the sequence
+    };
+    auto load = [&](Row &x, long long row) {
+      x.valid = row >= 0;
+      x.past = past;
+      if constexpr (!F::kStreams)
         if (row >= 0) x.load(codes, scales, row);
-      };
-      // The cursor runs over the steps of all parts, two ahead of the one that
-      // is written: its page is on its way while the step before it is loaded.
-      Part x;
-      bool have = next_part(p, ctl, walk, x);
-      int j = have ? x.lo : 0, id = -1, off = 0, head = 0;
-      const int bs = 1 << p.c.bs_log2;
-      auto lookup = [&]() {  // the cursor's page, then one step on; whether there was a step
-        const bool was = have;
-        const int t = j * 128 + r;
-        past = t >= x.s.nk;
-        id = have && !past
-                 ? __ldg(p.table + static_cast<long long>(x.b) * p.width + (t >> p.c.bs_log2))
-                 : -1;
-        off = t & (bs - 1);
-        head = x.h;
-        if (have && ++j >= x.hi) {
-          have = next_part(p, ctl, walk, x);
-          j = x.lo;
-        }
-        return was;
-      };
-      auto row_of = [&]() -> long long {
-        if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.c.num_blocks)) return -1;
-        return ((static_cast<long long>(id) * p.c.Hk + head) << p.c.bs_log2) + off;
-      };
-      const int stages = is_v ? C::VST : C::KST;
-      Row row;
-      bool now = lookup();
-      load(row, row_of());
-      bool next = lookup();
-      for (int step = 0, st = 0, ph = 0; now; ++step) {
-        if (is_v && ctl.skip_load && step == 0) {  // test hook: the P V issuer's wait runs out
-          if (r == 0) atomicOr(ctl.status, kStatusInjected);
-          break;
-        }
-        if (!__all_sync(~0u, step < stages || bounded_wait(empty + 8 * st, ph ^ 1, w))) break;
-        if (!is_v) {
-          const unsigned bits = __ballot_sync(~0u, row.valid || row.past);
-          if (lane == 0)
-            reinterpret_cast<unsigned *>(smem + C::OFF_MASK)[(step % C::MASKS) * 4 + warp - 4] = bits;
-        }
+      if constexpr (F::kBlockScales)
+        if (!is_v && (r & 15) == 0) x.load_scales(p.c, row);
+    };
+    // The cursor runs over the steps of all parts, two ahead of the one that
+    // is written: its page is on its way while the step before it is loaded.
+    Part x;
+    bool have = next_part(p, ctl, walk, x);
+    int j = have ? x.lo : 0, id = -1, off = 0, head = 0;
+    const int bs = 1 << p.c.bs_log2;
+    auto lookup = [&]() {  // the cursor's page, then one step on; whether there was a step
+      const bool was = have;
+      const int t = j * 128 + r;
+      past = t >= x.s.nk;
+      id = have && !past
+               ? __ldg(p.table + static_cast<long long>(x.b) * p.width + (t >> p.c.bs_log2))
+               : -1;
+      off = t & (bs - 1);
+      head = x.h;
+      if (have && ++j >= x.hi) {
+        have = next_part(p, ctl, walk, x);
+        j = x.lo;
+      }
+      return was;
+    };
+    auto row_of = [&]() -> long long {
+      if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.c.num_blocks)) return -1;
+      return ((static_cast<long long>(id) * p.c.Hk + head) << p.c.bs_log2) + off;
+    };
+    const int stages = is_v ? C::VST : C::KST;
+    Row row;
+    bool now = lookup();
+    load(row, row_of());
+    if constexpr (F::kStreams) row.begin(codes, row_of());
+    bool next = lookup();
+    for (int step = 0, st = 0, ph = 0; now; ++step) {
+      if (is_v && ctl.skip_load && step == 0) {  // test hook: the P V issuer's wait runs out
+        if (r == 0) atomicOr(ctl.status, kStatusInjected);
+        break;
+      }
+      if (!__all_sync(~0u, step < stages || bounded_wait(empty + 8 * st, ph ^ 1, w))) break;
+      if (!is_v) {
+        const unsigned bits = __ballot_sync(~0u, row.valid || row.past);
+        if (lane == 0)
+          reinterpret_cast<unsigned *>(smem + C::OFF_MASK)[(step % C::MASKS) * 4 + warp - 4] = bits;
+        if constexpr (F::kBlockScales)
+          if ((r & 15) == 0)
+            reinterpret_cast<float4 *>(smem + C::OFF_SCALE +
+                                       step % C::MASKS * C::SCALES)[r / 16] = row.scales();
+      }
+      // unit u of a chunk of row y is at u ^ (y & 7)
+      uint8_t *tile = tiles + st * C::TILE;
+      if constexpr (F::kStreams)
+        row.stream(codes, next ? row_of() : -1, tile + (r & ~31) * 128, C::CHUNK);
+      else
         row.expand(row.valid, [&](int unit) {
-          return reinterpret_cast<uint4 *>(tiles + st * C::TILE + (unit >> 3) * C::CHUNK + r * 128 +
+          return reinterpret_cast<uint4 *>(tile + (unit >> 3) * C::CHUNK + r * 128 +
                                            (((unit & 7) ^ (r & 7)) << 4));
         });
-        fence_proxy_async_smem();
-        mbar_arrive(full + 8 * st);
-        if (++st == stages) st = 0, ph ^= 1;
-        if (next) load(row, row_of());
-        now = next;
-        next = next && lookup();
-      }
+      fence_proxy_async_smem();
+      mbar_arrive(full + 8 * st);
+      if (++st == stages) st = 0, ph ^= 1;
+      if (next) load(row, row_of());
+      now = next;
+      next = next && lookup();
     }
   } else {
     setmaxnreg_inc<kRegSoftmax>();
@@ -803,22 +568,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         // seen nothing yet, take the maximum first.
         constexpr float kSumLimit = 32768.f;
         bool with_max = __any_sync(~0u, m_used == -INFINITY), formed = false;
-        float tsum = 0.f;
-        // factor of the scores of columns 16 n and on (positive, for the -inf of a masked
-        // one), log2 of what the values are relative to, and its inverse
-        float mul[C::kDirect ? 8 : 1], add = 0.f, inv = 1.f;
-        mul[0] = sl2;
-        if constexpr (C::kDirect) {
-          const float4 *from =
-              reinterpret_cast<const float4 *>(smem + C::OFF_SCALE + step % C::MASKS * C::SCALES);
-          reinterpret_cast<float4 *>(mul)[0] = from[0];
-          reinterpret_cast<float4 *>(mul)[1] = from[1];
-#pragma unroll
-          for (int n = 0; n < 8; ++n) mul[n] = fmaxf(mul[n] * sl2, FLT_MIN);
-          const float2 v = *reinterpret_cast<const float2 *>(from + 5);
-          add = v.x;
-          inv = v.y;
-        }
+        float tsum = 0.f, wsum = 0.f;
+        // the scales of columns 16 n and on, K's a factor of the score (positive, for the
+        // -inf of a masked one)
+        auto scale_at = [&](int n) {
+          float4 x = reinterpret_cast<const float4 *>(smem + C::OFF_SCALE +
+                                                      step % C::MASKS * C::SCALES)[n];
+          x.x = fmaxf(x.x * sl2, FLT_MIN);
+          return x;
+        };
         for (;;) {
           if (with_max) {
             float part[8];
@@ -826,17 +584,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int n = 0; n < 8; ++n) part[n] = -INFINITY;
 #pragma unroll
             for (int c = 0; c < 128; c += 2) {
-              const int n = C::kDirect ? c / 16 : (c >> 1) & 7;
+              const int n = F::kBlockScales ? c / 16 : (c >> 1) & 7;
               part[n] = max3f(part[n], S(c), S(c + 1));
             }
-            if constexpr (C::kDirect) {
+            if constexpr (F::kBlockScales) {
 #pragma unroll
-              for (int n = 0; n < 8; ++n) part[n] *= mul[n];
+              for (int n = 0; n < 8; ++n) {
+                const float4 x = scale_at(n);
+                part[n] = fmaf(part[n], x.x, x.y);
+              }
             }
             const float mx = max3f(max3f(part[0], part[1], part[2]),
                                    max3f(part[3], part[4], part[5]), fmaxf(part[6], part[7]));
             const float m_new =
-                fmaxf(m_used, C::kDirect ? mx + (add - kHeadroom) : fmaf(mx, sl2, -kHeadroom));
+                fmaxf(m_used, F::kBlockScales ? mx - kHeadroom : fmaf(mx, sl2, -kHeadroom));
             if (j == x.lo) {
               m_used = m_new;
             } else {
@@ -874,34 +635,49 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          const float off = m_used == -INFINITY ? 0.f : add - m_used;
-          const uint64_t off_2 = pk2(off, off);
+          const float off = m_used == -INFINITY ? 0.f : -m_used;
+          uint64_t sl2_2 = pk2(sl2, sl2), nm_2 = pk2(off, off);
           uint64_t acc[2] = {0ull, 0ull};
+          float4 scale = {};
+          if constexpr (F::kBlockScales) tsum = wsum = 0.f;
 #pragma unroll
           for (int blk = 0; blk < 2; ++blk) {
             uint32_t pk[32];
 #pragma unroll
             for (int n = 0; n < 32; ++n) {
               const int c0 = 2 * (blk * 32 + n);
-              const float f = mul[C::kDirect ? c0 / 16 : 0];
+              if (F::kBlockScales && n % 8 == 0) {
+                scale = scale_at(c0 / 16);
+                sl2_2 = pk2(scale.x, scale.x);
+                nm_2 = pk2(scale.y + off, scale.y + off);
+                acc[0] = acc[1] = 0ull;
+              }
               float x0, x1;
-              upk2(ffma2(pk2(S(c0), S(c0 + 1)), pk2(f, f), off_2), x0, x1);
+              upk2(ffma2(pk2(S(c0), S(c0 + 1)), sl2_2, nm_2), x0, x1);
               const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
               acc[n & 1] = fadd2(acc[n & 1], pk2(p0, p1));
               pk[n] = pack_f16x2(p0, p1);
+              if (F::kBlockScales && n % 8 == 7) {
+                float a0, a1;
+                upk2(fadd2(acc[0], acc[1]), a0, a1);
+                tsum += a0 + a1;
+                wsum = fmaf(a0 + a1, scale.z, wsum);
+              }
             }
             tmem_st32(s_tm + blk * 32, pk);
           }
-          float a0, a1, b0, b1;
-          upk2(acc[0], a0, a1);
-          upk2(acc[1], b0, b1);
-          tsum = (a0 + a1) + (b0 + b1);
+          if constexpr (!F::kBlockScales) {
+            float a0, a1, b0, b1;
+            upk2(acc[0], a0, a1);
+            upk2(acc[1], b0, b1);
+            tsum = (a0 + a1) + (b0 + b1);
+          }
           if (with_max || __all_sync(~0u, tsum <= kSumLimit)) break;
           with_max = formed = true;
           tmem_st_wait();  // the second pass rewrites the same columns
         }
         if (!ok) break;
-        l = C::kDirect ? fmaf(tsum, inv, l) : l + tsum;
+        l += F::kBlockScales ? wsum : tsum;
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(bPfull + 8 * buf);
@@ -980,10 +756,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <typename T, class F>
-cudaError_t launch_many(const KvAttn &p, const ManyCtl &ctl, float *ws,
-                        const typename F::Keys &keys, int ctas, cudaStream_t s) {
+cudaError_t launch_many(const KvAttn &p, const ManyCtl &ctl, float *ws, int ctas, cudaStream_t s) {
   static std::atomic<unsigned long long> attr_done{0};
-  constexpr int smem = ManyCfg<F, T>::SMEM;
+  constexpr int smem = ManyCfg<F>::SMEM;
   cudaError_t e = smem_attr_once(fa_kv_many_kernel<T, F>, smem, &attr_done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -996,7 +771,7 @@ cudaError_t launch_many(const KvAttn &p, const ManyCtl &ctl, float *ws,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, fa_kv_many_kernel<T, F>, p, ctl, ws, keys);
+  e = cudaLaunchKernelEx(&cfg, fa_kv_many_kernel<T, F>, p, ctl, ws);
   if (e != cudaSuccess || ctas == 1) return e;
   cfg.gridDim = dim3(static_cast<unsigned>(ctas - 1), R / kJoinRows);
   cfg.blockDim = dim3(kJoinThreads);

@@ -5,7 +5,6 @@
 
 #include <cstddef>
 #include <cstdint>
-#include <cuda.h>
 #include <cuda_runtime.h>
 
 namespace fa {
@@ -19,10 +18,6 @@ int api_device_status(unsigned **status);
 int api_sm_count();
 unsigned long long api_wait_limit();
 int api_skip_load();  // the test hook of fa_set_test_hooks
-// A map of bytes [blocks][rows][row of 64 or 128], boxes of box_rows, plain or
-// swizzled by the row's length; FA_OK or a failure.  (Host work alone.)
-int api_encode_bytes(CUtensorMap *map, const void *base, int row, long long rows, long long blocks,
-                     int box_rows, bool swizzled);
 
 // ------------------------------------------------------------ block tables
 struct PlanParams {

@@ -101,16 +101,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
       : "memory");
 }
 
-// The same without a cache policy.
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar,
-                                            int c0, int c1, int c2) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
-      : "memory");
-}
-
 // 3-D tiled store shared -> global (rows outside the tensor are clipped).
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, uint32_t src, int c0, int c1,
                                              int c2) {
@@ -198,16 +188,6 @@ __device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint64_t a_desc, uint64
   }
 }
 
-// D[tmem] (+)= A[smem desc] * B[smem desc]^T, 8-bit operands, one UMMA of 32 elements.
-__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                        uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 // D[tmem] (+)= A[tmem] * B[smem desc], one UMMA with A read from tensor memory.
 template <bool TF32>
 __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
@@ -236,19 +216,8 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t addr, uint32_t lbo, uin
          (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
 }
 
-// The same for K-major tiles whose rows are 128 or 64 bytes, swizzled by that length
-// (swizzle 4 = 64B): groups of eight rows follow one another.
-template <int kRow>
-__device__ __forceinline__ uint64_t sdesc_bytes(uint32_t addr) {
-  static_assert(kRow == 64 || kRow == 128, "a swizzle of the row's length");
-  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (1ull << 16) |
-         (static_cast<uint64_t>(8 * kRow >> 4) << 32) | (1ull << 46) |
-         ((kRow == 128 ? 2ull : 4ull) << 61);
-}
-
-// Instruction descriptor for kind::f16 / kind::tf32 / kind::f8f6f4 with an fp32
-// accumulator.  ab_fmt: 0 = fp16, 1 = bf16 (kind::f16), 2 = tf32 (kind::tf32), 0 = e4m3
-// (kind::f8f6f4).  *_mn: 0 = K-major,
+// Instruction descriptor for kind::f16 / kind::tf32 with an fp32 accumulator.
+// ab_fmt: 1 = bf16 (kind::f16), 2 = tf32 (kind::tf32).  *_mn: 0 = K-major,
 // 1 = MN-major.  N at bits 17-22 (>>3), M at bits 24-28 (>>4).
 __host__ __device__ constexpr uint32_t make_idesc(uint32_t ab_fmt, uint32_t M, uint32_t N,
                                                   uint32_t a_mn, uint32_t b_mn) {
