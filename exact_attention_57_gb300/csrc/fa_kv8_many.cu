@@ -8,6 +8,16 @@
 namespace fa {
 namespace {
 
+// 16 bytes that this SM reads once (without a place in L1: 535 instead of 541 us for two
+// chunks of 2048 queries, up to 8192 keys).
+__device__ __forceinline__ uint4 load_once(const uint8_t *p) {
+  uint4 x;
+  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+      : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+      : "l"(p));
+  return x;
+}
+
 template <int D_>
 struct Many8 {
   static constexpr int D = D_;
@@ -34,7 +44,7 @@ struct Many8 {
       __device__ __forceinline__ uint4 piece(int i) const {
         constexpr int kHalf = kAt / 2;
         return good >> (i * kRows) & 1
-                   ? __ldg(reinterpret_cast<const uint4 *>(half[i / kHalf] + i % kHalf * kRows * D))
+                   ? load_once(half[i / kHalf] + i % kHalf * kRows * D)
                    : make_uint4(0, 0, 0, 0);
       }
     };
@@ -70,10 +80,10 @@ struct Many8 {
       ks = __ldg(reinterpret_cast<const float *>(p.k_scales) + (row >> p.bs_log2));
       vs = __ldg(reinterpret_cast<const float *>(p.v_scales) + (row >> p.bs_log2));
     }
-    __device__ __forceinline__ float4 scales() const {
+    __device__ __forceinline__ BlockScale scales() const {
       BlockScale s;
       s.set(ks, vs);
-      return make_float4(s.k, s.v_log, s.v_inv, 0.f);
+      return s;
     }
   };
 };

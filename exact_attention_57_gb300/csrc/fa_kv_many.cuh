@@ -79,7 +79,8 @@ struct ManyCfg {
   // last S of tile g - 2 is complete, and with tiles of one step the softmax
   // may then still be at tile g - 4 (three score buffers).
   static constexpr int QES = 5;
-  // Of 16 keys each, eight to a step: K's scale, log2 of V's, its inverse, nothing.
+  // Of 16 keys each, eight to a step: K's scale twice (for pairs of columns), log2 of V's,
+  // its inverse.
   static constexpr int SCALES = F::kBlockScales ? 8 * 16 : 0;
   static constexpr int OFF_SCALE = OFF_MASK + MASKS * 16;
   static constexpr int OFF_QE = OFF_SCALE + MASKS * SCALES;
@@ -484,9 +485,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0)
           reinterpret_cast<unsigned *>(smem + C::OFF_MASK)[(step % C::MASKS) * 4 + warp - 4] = bits;
         if constexpr (F::kBlockScales)
-          if ((r & 15) == 0)
-            reinterpret_cast<float4 *>(smem + C::OFF_SCALE +
-                                       step % C::MASKS * C::SCALES)[r / 16] = row.scales();
+          if ((r & 15) == 0) {
+            const auto x = row.scales();
+            reinterpret_cast<float4 *>(smem + C::OFF_SCALE + step % C::MASKS * C::SCALES)[r / 16] =
+                make_float4(x.k, x.k, x.v_log, x.v_inv);
+          }
       }
       // unit u of a chunk of row y is at u ^ (y & 7)
       uint8_t *tile = tiles + st * C::TILE;
@@ -568,14 +571,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         // seen nothing yet, take the maximum first.
         constexpr float kSumLimit = 32768.f;
         bool with_max = __any_sync(~0u, m_used == -INFINITY), formed = false;
-        float tsum = 0.f, wsum = 0.f;
-        // the scales of columns 16 n and on, K's a factor of the score (positive, for the
-        // -inf of a masked one)
+        float tsum = 0.f;  // (of the weights without their values' scales)
+        // of columns 16 n and on: the scores' factor, twice (positive, for the -inf of a masked
+        // one), log2 of V's scale, its inverse
         auto scale_at = [&](int n) {
-          float4 x = reinterpret_cast<const float4 *>(smem + C::OFF_SCALE +
+          return reinterpret_cast<const ulonglong2 *>(smem + C::OFF_SCALE +
                                                       step % C::MASKS * C::SCALES)[n];
-          x.x = fmaxf(x.x * sl2, FLT_MIN);
-          return x;
+        };
+        auto factor = [&](uint64_t k) {
+          return ffma2(k, pk2(sl2, sl2), pk2(FLT_MIN, FLT_MIN));
         };
         for (;;) {
           if (with_max) {
@@ -590,8 +594,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (F::kBlockScales) {
 #pragma unroll
               for (int n = 0; n < 8; ++n) {
-                const float4 x = scale_at(n);
-                part[n] = fmaf(part[n], x.x, x.y);
+                const ulonglong2 x = scale_at(n);
+                float by, log, unused;
+                upk2(factor(x.x), by, unused);
+                upk2(x.y, log, unused);
+                part[n] = fmaf(part[n], by, log);
               }
             }
             const float mx = max3f(max3f(part[0], part[1], part[2]),
@@ -638,8 +645,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float off = m_used == -INFINITY ? 0.f : -m_used;
           uint64_t sl2_2 = pk2(sl2, sl2), nm_2 = pk2(off, off);
           uint64_t acc[2] = {0ull, 0ull};
-          float4 scale = {};
-          if constexpr (F::kBlockScales) tsum = wsum = 0.f;
+          // with scales: those of the next columns, loaded ahead; the weights' factor in the
+          // sum, and the least such factor, which bounds the weights by the sum
+          ulonglong2 ahead = {};
+          uint64_t inv_2 = 0ull;
+          float least = F::kBlockScales ? INFINITY : 1.f;
+          if constexpr (F::kBlockScales) ahead = scale_at(0);
 #pragma unroll
           for (int blk = 0; blk < 2; ++blk) {
             uint32_t pk[32];
@@ -647,37 +658,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int n = 0; n < 32; ++n) {
               const int c0 = 2 * (blk * 32 + n);
               if (F::kBlockScales && n % 8 == 0) {
-                scale = scale_at(c0 / 16);
-                sl2_2 = pk2(scale.x, scale.x);
-                nm_2 = pk2(scale.y + off, scale.y + off);
-                acc[0] = acc[1] = 0ull;
+                float log, inv;
+                upk2(ahead.y, log, inv);
+                sl2_2 = factor(ahead.x);
+                nm_2 = pk2(log + off, log + off);
+                inv_2 = pk2(inv, inv);
+                least = fminf(least, inv);
+                if (c0 < 112) ahead = scale_at(c0 / 16 + 1);
               }
               float x0, x1;
               upk2(ffma2(pk2(S(c0), S(c0 + 1)), sl2_2, nm_2), x0, x1);
               const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-              acc[n & 1] = fadd2(acc[n & 1], pk2(p0, p1));
+              acc[n & 1] = F::kBlockScales ? ffma2(pk2(p0, p1), inv_2, acc[n & 1])
+                                           : fadd2(acc[n & 1], pk2(p0, p1));
               pk[n] = pack_f16x2(p0, p1);
-              if (F::kBlockScales && n % 8 == 7) {
-                float a0, a1;
-                upk2(fadd2(acc[0], acc[1]), a0, a1);
-                tsum += a0 + a1;
-                wsum = fmaf(a0 + a1, scale.z, wsum);
-              }
             }
             tmem_st32(s_tm + blk * 32, pk);
           }
-          if constexpr (!F::kBlockScales) {
-            float a0, a1, b0, b1;
-            upk2(acc[0], a0, a1);
-            upk2(acc[1], b0, b1);
-            tsum = (a0 + a1) + (b0 + b1);
-          }
-          if (with_max || __all_sync(~0u, tsum <= kSumLimit)) break;
+          float a0, a1, b0, b1;
+          upk2(acc[0], a0, a1);
+          upk2(acc[1], b0, b1);
+          tsum = (a0 + a1) + (b0 + b1);
+          if (with_max || __all_sync(~0u, tsum <= kSumLimit * least)) break;
           with_max = formed = true;
           tmem_st_wait();  // the second pass rewrites the same columns
         }
         if (!ok) break;
-        l += F::kBlockScales ? wsum : tsum;
+        l += tsum;
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(bPfull + 8 * buf);
