@@ -20,6 +20,12 @@
 //     the maximum, which the team shares through shared memory, and the codes;
 //   many (new tokens of many requests): a warp takes a run, lanes and registers spread
 //     over the pairs.
+//
+// 30299 rows of 4 prompts (8 heads of 128, fp16) take 49 us, 3.8 TB/s or 56% of the copy
+// rate: 61% of the issue slots are busy, with a maximum, a scaling and a conversion an
+// element, and a warp's next loads wait for its codes.  A warp a run and pair, with
+// divisions in line, took 105.  Reading 30299 rows back takes 30 us, 6.3 TB/s (93%);
+// one row of each of 64 requests 3.9 us and reading them back 1.8, a launch each.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -458,7 +464,11 @@ cudaError_t append(const void *k, const void *v, long long ks, long long vs,
   Append<T> p = {static_cast<const T *>(k), static_cast<const T *>(v), ks, vs, slots, T_, 0, 0, 0, c};
   // Windows of a row a warp where the rows are few, since each may begin a run, else of
   // 16 rows a warp, as teams take them; about a thousand CTAs, but no fewer pairs each
-  // than a warp's lanes hold of one row.
+  // than a warp's lanes hold of one row.  (In us, windows of 8 / 16 / 32 / 64 / 128 rows:
+  // 8192 rows of one prompt 47 / 29 / 20 / 25 / 21, of four prompts 30299 rows 262 / 58 /
+  // 54 / 57 / 49; one row of each of 4500 requests 26 / 30 / 38 / 45 / 53, of 2504 17 / 24 /
+  // 24 / 27 / -: batches above 4096 requests pay for the prompts.  About 1800 CTAs instead
+  // of a thousand: 53 for the 49.)
   p.window = T_ <= 4096 ? kWarps : 16 * kWarps;
   const long long windows = (T_ + p.window - 1LL) / p.window;
   const int per = 32 / (c.d / 8), pairs = 2 * c.Hk, most = (pairs + per - 1) / per;

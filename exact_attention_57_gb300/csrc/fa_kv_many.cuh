@@ -53,7 +53,6 @@ struct ManyCtl {
   int skip_load, tile_rows, tokens;  // tokens of a tile
 };
 
-
 constexpr int WALK_BYTES = 80;
 
 template <class F>

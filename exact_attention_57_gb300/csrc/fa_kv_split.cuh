@@ -1,4 +1,4 @@
-// fa_kv_split.cuh — how the attention kernels over the 4-bit cache deal their
+// fa_kv_split.cuh — how the attention kernels over a cache of codes deal their
 // work: all tiles of all sequences lie in one line of units (a unit is a step
 // along the keys), every CTA takes an equal share of the line, and tiles that
 // shares cut are joined by a second kernel from parts in the workspace.
