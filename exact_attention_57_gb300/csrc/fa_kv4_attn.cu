@@ -39,6 +39,7 @@ struct Cache4 {
     static constexpr int kWarps = NT == 4 && D == 64 ? 4 : 8;
     static constexpr int kCtas = NT == 1 || D == 64 ? 2 : 1;
     static constexpr int kLead = NT == 1 ? 3 : NT == 2 && D == 64 ? 4 : 6;
+    static constexpr int kMost = kClusterUnits;
   };
 
   struct Tile {

@@ -30,12 +30,19 @@ struct Cache8 {
   //            D = 64: 2 x 8 57, 2 x 10 53, 2 x 12 54 (registers spill)
   //   16 rows  (4 key heads) 1 x 8 67, 1 x 10 91 (registers spill)
   //   32 rows  D = 64 alone, 1 x 8
+  // Units of a CTA of a cluster: for CTAs that take a sequence and key head alone (CL = 1)
+  // 16 instead of 8, cluster and line in us: 37 x 1023 keys, 8 key heads of 128 11.7 and
+  // 14.4, 37 x 1536 16.6 and 17.9, of 64 37 x 2048 13.3 and 15.8, 20 x 1500 9.3 and 10.5 (20
+  // x 2500, half a wave, 14.2 and 12.4); 16 rows 18 x 2048 15.5 and 18.6; with 24, 32 x
+  // 2048 21.8 and 21.0.  With 16 for wider clusters: 1 x 16384 14.1 and 12.5, 4 x 8192
+  // 16.2 and 15.5.
   template <int NT, int CL>
   struct Shape {
     static constexpr bool kLine = NT == 1 && CL < 2;
     static constexpr int kWarps = !kLine ? 8 : D == 128 ? 6 : 10;
     static constexpr int kCtas = kLine || (D == 64 && NT <= 2) ? 2 : 1;
     static constexpr int kLead = NT == 1 ? 3 : NT == 2 && D == 64 ? 4 : 6;
+    static constexpr int kMost = CL == 1 ? 16 : kClusterUnits;
   };
 
   struct Tile {

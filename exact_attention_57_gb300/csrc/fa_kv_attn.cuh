@@ -35,8 +35,8 @@
 // memory.
 //
 // A format F has:
-//   D, Shape<NT, CL>  head dim; kWarps, kCtas and kLead for tiles of 8 NT rows in
-//                  clusters of CL (0: along the line)
+//   D, Shape<NT, CL>  head dim; kWarps, kCtas, kLead and kMost (units of a CTA of a
+//                  cluster) for tiles of 8 NT rows in clusters of CL (0: along the line)
 //   Tile           16 tokens of one page as lane (r, c) holds them
 //   Lane           where that lane reads; load() fills a Tile
 //   scores()       S^T of a Tile, without its scale_of()
@@ -522,12 +522,12 @@ long long units_for(int max_k) {
 }
 
 // A cluster of CL CTAs for each of `heads` sequences and key heads, if one wave holds
-// them and that leaves a CTA at most kClusterUnits units: one launch.
+// them and that leaves a CTA at most kMost units: one launch.
 template <class F, int NT, int CL>
 bool cluster_grid(long long heads, int max_k, int num_sms, KvGrid *g) {
   using S = Shape<F, NT, CL>;
   if (heads * CL > static_cast<long long>(num_sms) * S::kCtas ||
-      units_for<S>(max_k) > CL * kClusterUnits)
+      units_for<S>(max_k) > CL * S::kMost)
     return false;
   g->cluster = CL;
   g->ctas = static_cast<int>(heads * CL);
