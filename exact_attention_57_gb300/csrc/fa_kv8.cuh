@@ -24,6 +24,14 @@ __device__ __forceinline__ uint32_t f32x2_e4m3x2(float lo, float hi) {
   return r;
 }
 
+// Two fp16 as e4m3 numbers in the low 16 bits, likewise; a NaN stays one.
+__device__ __forceinline__ uint32_t f16x2_e4m3x2(uint32_t x) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 h;\n\tcvt.rn.satfinite.e4m3x2.f16x2 h, %1;\n\tcvt.u32.u16 %0, h;\n\t}\n"
+      : "=r"(r) : "r"(x));
+  return r;
+}
+
 // Exponents of the scales that are stored.
 constexpr int kScaleExp = 40;
 

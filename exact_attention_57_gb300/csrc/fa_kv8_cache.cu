@@ -21,14 +21,17 @@
 //   many (new tokens of many requests): a warp takes a run, lanes and registers spread
 //     over the pairs.
 //
-// 30299 rows of 4 prompts (8 heads of 128, fp16) take 49 us, 3.8 TB/s or 56% of the copy
-// rate: 61% of the issue slots are busy, with a maximum, a scaling and a conversion an
-// element, and a warp's next loads wait for its codes.  A warp a run and pair, with
-// divisions in line, took 105.  Reading 30299 rows back takes 30 us, 6.3 TB/s (93%);
-// one row of each of 64 requests 3.9 us and reading them back 1.8, a launch each.
+// 30299 rows of 4 prompts (8 heads of 128, fp16) take 45 us, 4.1 TB/s or 61% of the copy
+// rate: a CTA finds its runs, loads, meets its team, converts and stores in turn, and the
+// three of an SM cover for one another only in part.  A warp a run and pair, with divisions
+// in line, took 105; slots read anew for every 32 rows of the window 48; the next pair's
+// loads into registers as they fall free 49 (registers spill; with two CTAs 51).  Reading
+// 30299 rows back takes 30 us, 6.3 TB/s (93%); one row of each of 64 requests 3.8 us and
+// reading them back 1.8, a launch each.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cfloat>
 #include <type_traits>
 
 #include "fa.h"
@@ -55,39 +58,95 @@ __device__ __forceinline__ Eight<T> load_eight(const T *p) {
   return x;
 }
 
-// The larger of `top` and the elements' sizes; NaNs do not count, infinities only
-// where asked.
-template <bool kFinite, typename T>
-__device__ __forceinline__ float size_of(const Eight<T> &x, float top) {
-  if constexpr (!kFinite && sizeof(T) == 2) {
-    using P = std::conditional_t<std::is_same_v<T, __half>, __half2, __nv_bfloat162>;
-    const P *p = reinterpret_cast<const P *>(&x);
-    const P m = __hmax2(__hmax2(__habs2(p[0]), __habs2(p[1])), __hmax2(__habs2(p[2]), __habs2(p[3])));
-    return fmaxf(top, fmaxf(static_cast<float>(m.x), static_cast<float>(m.y)));
+// The largest size among elements; infinity if there is one or, of 16 bits, a NaN among
+// them (of 32 bits, NaNs do not count).
+template <typename T>
+struct Largest {
+  using P = std::conditional_t<std::is_same_v<T, __half>, __half2, __nv_bfloat162>;
+  std::conditional_t<sizeof(T) == 4, float, P> top;
+
+  __device__ __forceinline__ Largest() {
+    if constexpr (sizeof(T) == 4) top = 0.f;
+    else top = pair(0.f);
   }
+  static __device__ __forceinline__ P pair(float x) {
+    if constexpr (std::is_same_v<T, __half>) return __float2half2_rn(x);
+    else return __float2bfloat162_rn(x);
+  }
+  __device__ __forceinline__ void add(const Eight<T> &x) {
+    if constexpr (sizeof(T) == 4) {
+      const float *e = reinterpret_cast<const float *>(&x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(e[j]));
+    } else {
+      const P *p = reinterpret_cast<const P *>(&x);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) top = __hmax2_nan(top, __habs2(p[j]));
+    }
+  }
+  __device__ __forceinline__ float get() const {
+    if constexpr (sizeof(T) == 4) {
+      return top;
+    } else {
+      const float a = static_cast<float>(top.x), b = static_cast<float>(top.y);
+      return a <= FLT_MAX && b <= FLT_MAX ? fmaxf(a, b) : INFINITY;
+    }
+  }
+};
+// The larger of `top` and the elements' finite sizes.
+template <typename T>
+__device__ __forceinline__ float finite_size(const Eight<T> &x, float top) {
   const T *e = reinterpret_cast<const T *>(&x);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float a = fabsf(static_cast<float>(e[j]));
-    top = fmaxf(top, kFinite && a == INFINITY ? 0.f : a);
+    top = fmaxf(top, a == INFINITY ? 0.f : a);
   }
   return top;
 }
 
-// Eight codes, by 1 / scale, where the scale is a power of two, or by the scale itself
-// (not inlined: eight correctly rounded divisions, which the caches that
-// fa_kv8_append fills never need; in line, they made the kernel's every element pay for
-// their branches).  A NaN becomes 448.
+__device__ __forceinline__ bool power_of_two(float scale) {  // (and not subnormal: 2^-40 at least)
+  return (__float_as_uint(scale) & 0x7FFFFFu) == 0;
+}
+
+// Whether codes_by does for elements whose largest size is not infinity (`plain`).  The
+// caches that fa_kv8_append fills have no other scales than powers of two; fp16 elements
+// are scaled in fp16, so 1 / scale has to be one of its normal numbers.
+template <typename T>
+__device__ __forceinline__ bool quick(float scale, bool plain) {
+  return plain && power_of_two(scale) &&
+         (!std::is_same_v<T, __half> || (scale >= 0x1p-15f && scale <= 0x1p14f));
+}
+
+// Eight codes, by 1 / scale, a power of two: an exact product (of fp16 elements, unless
+// it is below 2^-14, where every code is zero).  An fp32 NaN becomes 448.
 template <typename T>
 __device__ __forceinline__ uint2 codes_by(const Eight<T> &x, float inv) {
-  const T *e = reinterpret_cast<const T *>(&x);
   uint32_t c[4];
+  if constexpr (std::is_same_v<T, __half>) {
+    const __half2 by = __float2half2_rn(inv);
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    c[j] = f32x2_e4m3x2(fminf(static_cast<float>(e[2 * j]) * inv, 448.f),
-                        fminf(static_cast<float>(e[2 * j + 1]) * inv, 448.f));
+    for (int j = 0; j < 4; ++j) {
+      const __half2 y = __hmul2(reinterpret_cast<const __half2 *>(&x)[j], by);
+      c[j] = f16x2_e4m3x2(reinterpret_cast<const uint32_t &>(y));
+    }
+  } else if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+    const __nv_bfloat162 by = __float2bfloat162_rn(inv);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 y = __bfloat1622float2(__hmul2(reinterpret_cast<const __nv_bfloat162 *>(&x)[j], by));
+      c[j] = f32x2_e4m3x2(y.x, y.y);
+    }
+  } else {
+    const float *e = reinterpret_cast<const float *>(&x);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      c[j] = f32x2_e4m3x2(fminf(e[2 * j] * inv, 448.f), fminf(e[2 * j + 1] * inv, 448.f));
+  }
   return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
+// For any scale and elements, a NaN becoming 448 (not inlined: eight correctly rounded
+// divisions; in line, they made the kernel's every element pay for their branches).
 template <typename T>
 __device__ __noinline__ uint2 codes_over(Eight<T> x, float scale) {
   const T *e = reinterpret_cast<const T *>(&x);
@@ -97,9 +156,6 @@ __device__ __noinline__ uint2 codes_over(Eight<T> x, float scale) {
     c[j] = f32x2_e4m3x2(fminf(__fdiv_rn(static_cast<float>(e[2 * j]), scale), 448.f),
                         fminf(__fdiv_rn(static_cast<float>(e[2 * j + 1]), scale), 448.f));
   return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
-}
-__device__ __forceinline__ bool power_of_two(float scale) {  // (and not subnormal: 2^-40 at least)
-  return (__float_as_uint(scale) & 0x7FFFFFu) == 0;
 }
 
 // Eight codes times `by`, as codes.
@@ -155,6 +211,19 @@ struct Append {
   }
 };
 
+// The slots of rows, those of a CTA's window and behind it, kThreads in all, from shared
+// memory.
+template <typename T>
+struct Slots {
+  const Append<T> &p;
+  const long long *near;
+  long long w0;
+  __device__ __forceinline__ long long operator()(long long t) const {
+    const unsigned long long i = static_cast<unsigned long long>(t - w0);
+    return i < kThreads ? near[i] : p.slot(t);
+  }
+};
+
 // The scale of a block that held `old`; *by: what its codes are multiplied with.
 __device__ __forceinline__ float grown(float old, float fit, float *by) {
   old = old > 0.f && old < INFINITY ? old : 0.f;
@@ -181,29 +250,30 @@ struct Run {
     more = stop == 0 && from + 32 < p.T_;
   }
   template <typename T>
-  __device__ __forceinline__ Run next(const Append<T> &p) const {
-    return Run(p, base + 32, p.slot(base + 32 + (threadIdx.x & 31)), 0, block);
+  __device__ __forceinline__ Run next(const Slots<T> &slots) const {
+    return Run(slots.p, base + 32, slots(base + 32 + (threadIdx.x & 31)), 0, block);
   }
 };
 
 // f(row, token of the block) for each row of a run, by the whole warp.
 template <typename T, typename F>
-__device__ __forceinline__ void for_rows(const Append<T> &p, Run run, F f) {
-  const int off_mask = (1 << p.c.bs_log2) - 1;
+__device__ __forceinline__ void for_rows(const Slots<T> &slots, Run run, F f) {
+  const int off_mask = (1 << slots.p.c.bs_log2) - 1;
   for (;;) {
     for (unsigned in = run.in; in; in &= in - 1) {
       const int j = __ffs(in) - 1;
       f(run.base + j, static_cast<int>(__shfl_sync(~0u, run.slot, j)) & off_mask);
     }
     if (!run.more) break;
-    run = run.next(p);
+    run = run.next(slots);
   }
 }
 
 // A run by one warp, pairs [n0, n1): `lanes` (a power of two) lanes a row, as many pairs
 // side by side as there are lanes for.
 template <typename T>
-__device__ __forceinline__ void append_across(const Append<T> &p, const Run &run, int n0, int n1) {
+__device__ __forceinline__ void append_across(const Slots<T> &slots, const Run &run, int n0, int n1) {
+  const Append<T> &p = slots.p;
   const int lane = threadIdx.x & 31, per_row = p.c.d / 8;
   const int lanes = 1 << (32 - __clz(per_row - 1)), per = 32 / lanes;  // (per_row 2 .. 32)
   const int sub = lane / lanes, x = lane - sub * lanes, col = x * 8;
@@ -213,19 +283,21 @@ __device__ __forceinline__ void append_across(const Append<T> &p, const Run &run
     const long long stride = p.stride(on ? n : n0), at = p.at(on ? n : n0, run.block);
     const float old = p.scales(on ? n : n0)[at];
     Eight<T> e;
-    float top = 0.f;
+    Largest<T> largest;
     int low = 1 << p.c.bs_log2, rows = 0;
-    for_rows(p, run, [&](long long row, int off) {
+    for_rows(slots, run, [&](long long row, int off) {
       low = min(low, off);
       ++rows;
       e = load_eight(src + row * stride);
-      if (on) top = size_of<false>(e, top);
+      if (on) largest.add(e);
     });
+    float top = largest.get();
     for (int o = 1; o < lanes; o *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    if (__any_sync(~0u, top == INFINITY)) {  // infinities, which do not count
+    const bool plain = top < INFINITY;
+    if (__any_sync(~0u, !plain)) {  // infinities, which do not count
       top = 0.f;
-      for_rows(p, run, [&](long long row, int) {
-        if (on) top = size_of<true>(load_eight(src + row * stride), top);
+      for_rows(slots, run, [&](long long row, int) {
+        if (on) top = finite_size(load_eight(src + row * stride), top);
       });
       for (int o = 1; o < lanes; o *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
     }
@@ -239,11 +311,11 @@ __device__ __forceinline__ void append_across(const Append<T> &p, const Run &run
       }
     }
     const float inv = __frcp_rn(scale);
-    for_rows(p, run, [&](long long row, int off) {
+    for_rows(slots, run, [&](long long row, int off) {
       if (rows > 1) e = load_eight(src + row * stride);
       if (on)
         *reinterpret_cast<uint2 *>(to + off * p.c.d) =
-            power_of_two(scale) ? codes_by(e, inv) : codes_over(e, scale);
+            quick<T>(scale, plain) ? codes_by(e, inv) : codes_over(e, scale);
     });
     __syncwarp();  // (all lanes have read the old scales)
     if (on && x == 0) p.scales(n)[at] = scale;
@@ -254,8 +326,9 @@ __device__ __forceinline__ void append_across(const Append<T> &p, const Run &run
 // mate and on.  kSteps: rounds of loads for 16 rows.  map: 16 rows a warp; top_of: a
 // number a warp, twice, in turn.
 template <typename T, int kSteps>
-__device__ __forceinline__ void append_along(const Append<T> &p, const Run &whole, int n0, int n1,
+__device__ __forceinline__ void append_along(const Slots<T> &slots, const Run &whole, int n0, int n1,
                                              int *map, float (*top_of)[kWarps], int *turn) {
+  const Append<T> &p = slots.p;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int team_log2 = p.c.bs_log2 - 4, team = warp >> team_log2;
   const int mate = warp - (team << team_log2), off_mask = (1 << p.c.bs_log2) - 1;
@@ -265,7 +338,7 @@ __device__ __forceinline__ void append_along(const Append<T> &p, const Run &whol
   if (lane < 16) map[lane] = -1;
   __syncwarp();
   int low = off_mask;
-  for (Run run = whole;; run = run.next(p)) {
+  for (Run run = whole;; run = run.next(slots)) {
     if (run.in >> lane & 1) {
       const int off = static_cast<int>(run.slot) & off_mask;
       low = min(low, off);
@@ -291,15 +364,17 @@ __device__ __forceinline__ void append_along(const Append<T> &p, const Run &whol
         for (uint4 &w : e[i].w) w = make_uint4(0, 0, 0, 0);
     }
     const float old = p.scales(n)[at];
-    float top = 0.f;
+    Largest<T> largest;
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) top = size_of<false>(e[i], top);
+    for (int i = 0; i < kSteps; ++i) largest.add(e[i]);
+    float top = largest.get();
     for (int o = 16; o; o /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    if (top == INFINITY) {
+    const bool plain = top < INFINITY;
+    if (!plain) {
       top = 0.f;
 #pragma unroll 1
       for (int i = 0; i < kSteps; ++i)
-        if (row_of(i) >= 0) top = size_of<true>(load_eight(src + row_of(i) * stride), top);
+        if (row_of(i) >= 0) top = finite_size(load_eight(src + row_of(i) * stride), top);
       for (int o = 16; o; o /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
     }
     if (team_log2 > 0) {
@@ -317,7 +392,7 @@ __device__ __forceinline__ void append_along(const Append<T> &p, const Run &whol
         if (sub < per) *c = rescaled(*c, by);
       }
     }
-    if (power_of_two(scale)) {
+    if (quick<T>(scale, plain)) {
       const float inv = __frcp_rn(scale);
 #pragma unroll
       for (int i = 0; i < kSteps; ++i)
@@ -340,6 +415,7 @@ __global__ void __launch_bounds__(kThreads, kSteps * sizeof(T) <= 16 ? 3 : kStep
     fa_kv8_append_kernel(const __grid_constant__ Append<T> p) {
   __shared__ int s_map[kWarps][16];
   __shared__ float s_top[2][kWarps];
+  __shared__ long long s_slots[kThreads];
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -347,18 +423,22 @@ __global__ void __launch_bounds__(kThreads, kSteps * sizeof(T) <= 16 ? 3 : kStep
   const int group = static_cast<int>(blockIdx.x % p.groups);
   const long long w0 = static_cast<long long>(blockIdx.x / p.groups) * p.window;
   const int n0 = group * p.per_cta, n1 = min(n0 + p.per_cta, 2 * p.c.Hk);
+  s_slots[threadIdx.x] = p.slot(w0 + threadIdx.x);
+  const Slots<T> slots = {p, s_slots, w0};
+  // (with the loads of the window's own: mostly it is the row ahead that tells)
+  const long long ahead = p.slot(w0 - 32 + lane);
+  __syncthreads();
   int runs = 0, turn = 0;
   long long before = -1;  // the block of the last row that counts ahead of the rows at hand
   for (int part = 0; part < p.window; part += 32) {
     const long long t0 = w0 + part;
     if (t0 >= p.T_) break;
-    const long long mine = p.slot(t0 + lane);  // (also behind the window)
-    // (with the loads of the window's own: mostly it is the row ahead that tells)
-    const long long ahead = before < 0 ? p.slot(t0 - 32 + lane) : -1;
+    const long long mine = slots(t0 + lane);  // (also behind the window)
     const unsigned own = p.window - part < 32 ? (1u << (p.window - part)) - 1u : ~0u;
     const unsigned there = __ballot_sync(~0u, mine >= 0) & own;
     if (there == 0) continue;
-    for (long long t = t0, s = ahead; before < 0 && t > 0; t -= 32, s = p.slot(t - 32 + lane)) {
+    // (while `before` is -1, no row of the window ahead of t0 counts)
+    for (long long t = w0, s = ahead; before < 0 && t > 0; t -= 32, s = p.slot(t - 32 + lane)) {
       const unsigned some = __ballot_sync(~0u, s >= 0);
       if (some) before = __shfl_sync(~0u, s, 31 - __clz(some)) >> p.c.bs_log2;
     }
@@ -375,9 +455,9 @@ __global__ void __launch_bounds__(kThreads, kSteps * sizeof(T) <= 16 ? 3 : kStep
       if (runs++ % (many ? kWarps : teams) != (many ? warp : team)) continue;
       const Run run(p, t0, mine, first, __shfl_sync(~0u, mine, first) >> p.c.bs_log2);
       if (many)
-        append_across(p, run, n0, n1);
+        append_across(slots, run, n0, n1);
       else
-        append_along<T, kSteps>(p, run, n0, n1, s_map[warp], s_top, &turn);
+        append_along<T, kSteps>(slots, run, n0, n1, s_map[warp], s_top, &turn);
     }
   }
 }
@@ -464,11 +544,12 @@ cudaError_t append(const void *k, const void *v, long long ks, long long vs,
   Append<T> p = {static_cast<const T *>(k), static_cast<const T *>(v), ks, vs, slots, T_, 0, 0, 0, c};
   // Windows of a row a warp where the rows are few, since each may begin a run, else of
   // 16 rows a warp, as teams take them; about a thousand CTAs, but no fewer pairs each
-  // than a warp's lanes hold of one row.  (In us, windows of 8 / 16 / 32 / 64 / 128 rows:
-  // 8192 rows of one prompt 47 / 29 / 20 / 25 / 21, of four prompts 30299 rows 262 / 58 /
-  // 54 / 57 / 49; one row of each of 4500 requests 26 / 30 / 38 / 45 / 53, of 2504 17 / 24 /
-  // 24 / 27 / -: batches above 4096 requests pay for the prompts.  About 1800 CTAs instead
-  // of a thousand: 53 for the 49.)
+  // than a warp's lanes hold of one row.  (In us when the prompts above took 49, windows of
+  // 8 / 16 / 32 / 64 / 128 rows: 8192 rows of one prompt 47 / 29 / 20 / 25 / 21, those
+  // prompts 262 / 58 / 54 / 57 / 49; one row of each of 4500 requests 26 / 30 / 38 / 45 / 53,
+  // of 2504 17 / 24 / 24 / 27 / -: batches above 4096 requests pay for the prompts.  Now 512
+  // / 640 / 1024 / 1800 CTAs: 44 / 44 / 45 / 47, the same in blocks of 16 tokens 49 / 49 / 45
+  // / -, 2048 rows of one prompt 19 / 16 / 13 / -.)
   p.window = T_ <= 4096 ? kWarps : 16 * kWarps;
   const long long windows = (T_ + p.window - 1LL) / p.window;
   const int per = 32 / (c.d / 8), pairs = 2 * c.Hk, most = (pairs + per - 1) / per;

@@ -161,6 +161,34 @@ def test_append_of_what_is_not_finite(dtype):
     assert all((c.view(torch.uint8) & 127 != 127).all() for c in (cache[0], cache[2]))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("none", [False, True])
+def test_append_under_scales_of_any_size(dtype, rows, none):
+    """Blocks whose old scales are powers of two from 2^-40 to 2^40, rows of numbers from
+    the type's smallest to 448 times the scale, with a NaN among them or not."""
+    exps = [-40, -24, -17, -16, -15, -14, -13, 0, 1, 8, 13, 14, 15, 16, 24, 40]
+    bs, d = 64, 32
+    g = gen(rows)
+    before = k8.random_store(len(exps), 1, bs, d, g)
+    before[1][:, 0] = torch.tensor([2.0 ** e for e in exps])
+    x = torch.randn(len(exps), rows, 1, d, generator=g)
+    x = x * 2.0 ** torch.randint(-12, 1, x.shape, generator=g) * 64 * before[1][:, None, :, None]
+    x[:, 0, 0, :4] = torch.tensor([0.0, -0.0, 2.0 ** -24, -2.0 ** -133])
+    top = torch.finfo(DT[dtype]).max
+    x = x.clamp(-top, top).to(DT[dtype])
+    if none:
+        x[:, rows // 2, 0, 7] = math.nan
+    slots = (torch.arange(len(exps))[:, None] * bs + 3 + torch.arange(rows)).flatten()
+    want = k8.append(x.flatten(0, 1), slots, *before)
+    cache = k8.on(before + before, DEV)
+    y = x.flatten(0, 1).to(DEV)
+    fa.kv8_append(y, y, slots.to(DEV), *cache)
+    got = raw(cache)
+    for i in (0, 2):
+        assert same_codes(got[i], want[0]) and torch.equal(got[i + 1], want[1])
+
+
 def test_append_of_the_smallest_and_largest_numbers():
     """Scales end at 2^-40 and 2^40: what lies outside becomes 0 or saturates."""
     x = torch.tensor([1e-38, 448 * 2.0 ** -40, 448 * 2.0 ** 40, 3e38, 0.0, 2.0 ** -50, 2.0 ** -49.0])
