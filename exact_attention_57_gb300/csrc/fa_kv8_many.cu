@@ -9,21 +9,21 @@
 // step's codes is issued a step ahead, into the register that its predecessor left.
 //
 // Two prompts' chunks of 2048 queries (32 query heads on 8 key heads of 128, causal, up
-// to 8192 keys) take 533 us, 886 TFLOP/s; 1024 queries on 65536 keys 1128 us, 967
-// TFLOP/s; the first at d = 64 435 us.  Softmax and expanding bound it together: without
-// any loads the first took 509 (of 541 then), without exponentials 528, without scales
-// the last took 386 (of 448); issue slots are 52% busy.  Against 546 then: scales
-// applied by the expanding warps took 630 us, two steps of codes in registers 1650 (they
-// spill), codes of K as e4m3 operands with Q as a sum of two or three e4m3 numbers and
-// codes of V by way of shared memory 670 (0.1 us less a step and 24 us more a tile).
+// to 8192 keys) take 540 us, 875 TFLOP/s; 1024 queries on 65536 keys 1130 us, 965
+// TFLOP/s; the first at d = 64 439 us.  Softmax and expanding bound it together: of 541
+// with queries of zeros, 509 were left without any loads, 528 without exponentials, and
+// of 448 at d = 64 386 without scales; issue slots are 52% busy.  Against 546 then:
+// scales applied by the expanding warps took 630 us, two steps of codes in registers 1650
+// (they spill), codes of K as e4m3 operands with Q as a sum of two or three e4m3 numbers
+// and codes of V by way of shared memory 670 (0.1 us less a step and 24 us more a tile).
 #include "fa_kv8.cuh"
 #include "fa_kv_many.cuh"
 
 namespace fa {
 namespace {
 
-// 16 bytes that this SM reads once (without a place in L1: 535 instead of 541 us for two
-// chunks of 2048 queries, up to 8192 keys).
+// 16 bytes that this SM reads once (without a place in L1: 535 instead of 541 us for the
+// two chunks above, with queries of zeros).
 __device__ __forceinline__ uint4 load_once(const uint8_t *p) {
   uint4 x;
   asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
