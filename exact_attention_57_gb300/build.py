@@ -171,7 +171,7 @@ def ptxas_summary(log_path: str | None = None) -> str:
     at launch).  Kernel names are demangled with c++filt when it is present."""
     import re
     text = open(log_path or os.path.join(BUILD, "ptxas.log")).read()
-    rows, cur = [], None
+    rows, cur, own = [], None, False
     for line in text.splitlines():
         m = re.search(r"Compiling entry function '(\S+)'", line)
         if m:
@@ -181,9 +181,12 @@ def ptxas_summary(log_path: str | None = None) -> str:
             continue
         if cur is None:
             continue
+        m = re.search(r"Function properties for (\S+)", line)
+        if m:  # of the kernel, or of a function that it calls
+            own = m.group(1) == cur["name"]
         m = re.search(r"(\d+) bytes stack frame, (\d+) bytes spill stores, (\d+) bytes spill loads",
                       line)
-        if m:
+        if m and own:
             cur["stack"], cur["spill_st"], cur["spill_ld"] = m.groups()
         m = re.search(r"Used (\d+) registers", line)
         if m:
