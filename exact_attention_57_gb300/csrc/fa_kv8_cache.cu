@@ -158,8 +158,10 @@ __device__ __noinline__ uint2 codes_over(Eight<T> x, float scale) {
   return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
 
-// Eight codes times `by`, as codes.
+// Eight codes times `by`, as codes; with a scale that does not count, `by` is 0, and a
+// NaN among them (of memory that nobody has written, say) is none of its values.
 __device__ __forceinline__ uint2 rescaled(uint2 c, float by) {
+  if (by == 0.f) return make_uint2(0, 0);
   uint32_t r[2] = {c.x, c.y};
 #pragma unroll
   for (int n = 0; n < 2; ++n) {
