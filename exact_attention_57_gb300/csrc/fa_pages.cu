@@ -17,8 +17,10 @@
 // then (256 rows of 128 entries) 7.8, one cluster's chain of dependent steps: marks,
 // counts, lists.  Compacting 32 requests of up to 8192 tokens takes 49.6 us, 42.7 by its
 // bytes, about 6 of it the plan ahead of the copies.  Nine small pages: 1.6 us.
+#include <atomic>
 #include <cstdint>
 
+#include "fa_internal.h"
 #include "fa_serve.h"
 #include "ptx.cuh"
 
@@ -483,12 +485,9 @@ int words_per_cta(int num_blocks, int cluster) {
   return (words + cluster - 1) / cluster;
 }
 
-template <typename Kernel>
-cudaError_t sweep_attr(Kernel kern, int smem) {
-  return smem > 48 * 1024 - static_cast<int>(sizeof(SweepShared))
-             ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)
-             : cudaSuccess;
-}
+// What a kernel may ask for is a property of the kernel, not of a launch, and other
+// threads launch it for caches of other sizes: the most that any of them needs.
+constexpr int kSweepSmem = kMaxSweep / 32 / 8 * 4;
 
 }  // namespace
 
@@ -514,7 +513,8 @@ cudaError_t launch_kv_free(const FreeParams &p, cudaStream_t s) {
   const int cl = sweep_cluster(p.B, p.width, p.num_blocks);
   const int per_cta = words_per_cta(p.num_blocks, cl), smem = per_cta * 4;
   if (cl == 1) return launch(fa_kv_free_kernel<1>, 1, kSweepThreads, smem, 1, s, p, per_cta);
-  const cudaError_t e = sweep_attr(fa_kv_free_kernel<8>, smem);
+  static std::atomic<unsigned long long> attr_done{0};
+  const cudaError_t e = smem_attr_once(fa_kv_free_kernel<8>, kSweepSmem, &attr_done);
   return e != cudaSuccess ? e : launch(fa_kv_free_kernel<8>, 8, kSweepThreads, smem, 8, s, p, per_cta);
 }
 
@@ -525,7 +525,8 @@ cudaError_t launch_kv_compact(const Pages &pages, const CompactParams &p, int nu
   if (cl == 1) {
     e = launch(fa_kv_compact_kernel<1>, 1, kSweepThreads, smem, 1, s, p, per_cta);
   } else {
-    e = sweep_attr(fa_kv_compact_kernel<8>, smem);
+    static std::atomic<unsigned long long> attr_done{0};
+    e = smem_attr_once(fa_kv_compact_kernel<8>, kSweepSmem, &attr_done);
     if (e == cudaSuccess) e = launch(fa_kv_compact_kernel<8>, 8, kSweepThreads, smem, 8, s, p, per_cta);
   }
   if (e != cudaSuccess) return e;
