@@ -20,6 +20,9 @@
 //     the maximum, which the team shares through shared memory, and the codes;
 //   many (new tokens of many requests): a warp takes a run, lanes and registers spread
 //     over the pairs.
+// Rows that are skipped, as those that fill a padded batch, are looked at by the whole
+// CTA, once: 64 new tokens in a batch of 4096 rows take 9.8 us (187 when each warp walked
+// to the end of its run, 32 rows a step, for each of its pairs), in one of 8192 25 (135).
 //
 // 30299 rows of 4 prompts (8 heads of 128, fp16) take 45 us, 4.1 TB/s or 61% of the copy
 // rate: a CTA finds its runs, loads, meets its team, converts and stores in turn, and the
@@ -213,18 +216,90 @@ struct Append {
   }
 };
 
-// The slots of rows, those of a CTA's window and behind it, kThreads in all, from shared
-// memory.
-template <typename T>
+constexpr int kMostTokens = 128;  // of a block
+
+// The rows that a CTA looks at, numbered from its window's first: kThreads of them, which
+// follow one another, and where the window's last run goes on behind those, the rest of
+// its rows, kThreads + t being that of token t of the block.  All in shared memory, so that
+// a run is walked at no cost for the rows that are skipped on its way.
 struct Slots {
-  const Append<T> &p;
-  const long long *near;
-  long long w0;
-  __device__ __forceinline__ long long operator()(long long t) const {
-    const unsigned long long i = static_cast<unsigned long long>(t - w0);
-    return i < kThreads ? near[i] : p.slot(t);
+  const long long *near;  // [kThreads]
+  const int *far;         // [kMostTokens]: a row, or -1
+  long long w0;           // the window's first row
+  int end;                // behind the last that counts
+
+  // The slot of row i, which may be one of the last run's, in `block`.
+  __device__ __forceinline__ long long at(int i, long long block, int bs_log2) const {
+    if (i < kThreads) return near[i];
+    return far[i - kThreads] >= 0 ? (block << bs_log2) + (i - kThreads) : -1;
+  }
+  __device__ __forceinline__ long long row(int i) const {
+    return i < kThreads ? w0 + i : far[i - kThreads];
   }
 };
+
+// Rows that a thread looks at side by side, outside the window.
+constexpr int kAtOnce = 16;
+
+// The least of `x` over the CTA.
+__device__ __forceinline__ unsigned least_of(unsigned x, unsigned *least) {
+  x = __reduce_min_sync(~0u, x);
+  if ((threadIdx.x & 31) == 0) least[threadIdx.x / 32] = x;
+  __syncthreads();
+  for (int w = 0; w < kWarps; ++w) x = min(x, least[w]);
+  return x;
+}
+
+// Notes the rows of `block` from row `from` on, up to the first of another block, in far
+// (of -1 before), by the whole CTA; whether there are any.
+template <typename T>
+__device__ __noinline__ bool find_far(const Append<T> &p, long long from, long long block, int *far,
+                                      unsigned *least) {
+  constexpr unsigned kChunk = kAtOnce * kThreads;
+  const int off_mask = (1 << p.c.bs_log2) - 1;
+  bool found = false;
+  for (; from < p.T_; from += kChunk) {
+    long long s[kAtOnce];
+    unsigned other = kChunk;  // the first row of another block
+    bool some = false;
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) s[i] = p.slot(from + i * kThreads + threadIdx.x);
+#pragma unroll
+    for (int i = kAtOnce - 1; i >= 0; --i) {
+      some |= s[i] >= 0;
+      if (s[i] >= 0 && s[i] >> p.c.bs_log2 != block) other = i * kThreads + threadIdx.x;
+    }
+    if (!__syncthreads_or(some)) continue;
+    other = least_of(other, least);
+    bool mine = false;
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const unsigned n = i * kThreads + threadIdx.x;
+      if (s[i] >= 0 && s[i] >> p.c.bs_log2 == block && n < other) {
+        far[static_cast<int>(s[i]) & off_mask] = static_cast<int>(from + n);
+        mine = true;
+      }
+    }
+    found |= __syncthreads_or(mine) != 0;
+    if (other < kChunk) break;
+  }
+  return found;
+}
+
+// The block of the last row that counts ahead of row `to`, or -1, by the whole CTA.
+template <typename T>
+__device__ __noinline__ long long find_back(const Append<T> &p, long long to, unsigned *least) {
+  constexpr unsigned kChunk = kAtOnce * kThreads;
+  for (; to > 0; to -= kChunk) {
+    unsigned back = kChunk;
+#pragma unroll
+    for (int i = kAtOnce - 1; i >= 0; --i)
+      if (p.slot(to - 1 - i * kThreads - threadIdx.x) >= 0) back = i * kThreads + threadIdx.x;
+    if (!__syncthreads_or(back < kChunk)) continue;
+    return p.slot(to - 1 - least_of(back, least)) >> p.c.bs_log2;
+  }
+  return -1;
+}
 
 // The scale of a block that held `old`; *by: what its codes are multiplied with.
 __device__ __forceinline__ float grown(float old, float fit, float *by) {
@@ -237,45 +312,45 @@ __device__ __forceinline__ float grown(float old, float fit, float *by) {
 // A run: the rows of one block that follow one another.  Of rows base .. base + 31 the
 // lanes hold the slots, and `in` has those of the run; `more`: it may go on behind them.
 struct Run {
-  long long base, slot, block;
+  int base;
+  long long slot, block;
   unsigned in;
   bool more;
 
-  // The part of it among rows `from` .. `from` + 31.
-  template <typename T>
-  __device__ __forceinline__ Run(const Append<T> &p, long long from, long long slot, int first,
+  // The part of it among rows `from` .. `from` + 31 of `slots`.
+  __device__ __forceinline__ Run(const Slots &slots, int bs_log2, int from, long long slot, int first,
                                  long long block)
       : base(from), slot(slot), block(block) {
     const bool ahead = (threadIdx.x & 31) < first;
-    const unsigned stop = __ballot_sync(~0u, !ahead && slot >= 0 && (slot >> p.c.bs_log2) != block);
+    const unsigned stop = __ballot_sync(~0u, !ahead && slot >= 0 && (slot >> bs_log2) != block);
     in = __ballot_sync(~0u, !ahead && slot >= 0) & (stop ? (stop & (0u - stop)) - 1u : ~0u);
-    more = stop == 0 && from + 32 < p.T_;
+    more = stop == 0 && from + 32 < slots.end;
   }
-  template <typename T>
-  __device__ __forceinline__ Run next(const Slots<T> &slots) const {
-    return Run(slots.p, base + 32, slots(base + 32 + (threadIdx.x & 31)), 0, block);
+  __device__ __forceinline__ Run next(const Slots &slots, int bs_log2) const {
+    return Run(slots, bs_log2, base + 32, slots.at(base + 32 + (threadIdx.x & 31), block, bs_log2), 0,
+               block);
   }
 };
 
 // f(row, token of the block) for each row of a run, by the whole warp.
-template <typename T, typename F>
-__device__ __forceinline__ void for_rows(const Slots<T> &slots, Run run, F f) {
-  const int off_mask = (1 << slots.p.c.bs_log2) - 1;
+template <typename F>
+__device__ __forceinline__ void for_rows(const Slots &slots, int bs_log2, Run run, F f) {
+  const int off_mask = (1 << bs_log2) - 1;
   for (;;) {
     for (unsigned in = run.in; in; in &= in - 1) {
       const int j = __ffs(in) - 1;
-      f(run.base + j, static_cast<int>(__shfl_sync(~0u, run.slot, j)) & off_mask);
+      f(slots.row(run.base + j), static_cast<int>(__shfl_sync(~0u, run.slot, j)) & off_mask);
     }
     if (!run.more) break;
-    run = run.next(slots);
+    run = run.next(slots, bs_log2);
   }
 }
 
 // A run by one warp, pairs [n0, n1): `lanes` (a power of two) lanes a row, as many pairs
 // side by side as there are lanes for.
 template <typename T>
-__device__ __forceinline__ void append_across(const Slots<T> &slots, const Run &run, int n0, int n1) {
-  const Append<T> &p = slots.p;
+__device__ __forceinline__ void append_across(const Append<T> &p, const Slots &slots, const Run &run,
+                                              int n0, int n1) {
   const int lane = threadIdx.x & 31, per_row = p.c.d / 8;
   const int lanes = 1 << (32 - __clz(per_row - 1)), per = 32 / lanes;  // (per_row 2 .. 32)
   const int sub = lane / lanes, x = lane - sub * lanes, col = x * 8;
@@ -287,7 +362,7 @@ __device__ __forceinline__ void append_across(const Slots<T> &slots, const Run &
     Eight<T> e;
     Largest<T> largest;
     int low = 1 << p.c.bs_log2, rows = 0;
-    for_rows(slots, run, [&](long long row, int off) {
+    for_rows(slots, p.c.bs_log2, run, [&](long long row, int off) {
       low = min(low, off);
       ++rows;
       e = load_eight(src + row * stride);
@@ -298,7 +373,7 @@ __device__ __forceinline__ void append_across(const Slots<T> &slots, const Run &
     const bool plain = top < INFINITY;
     if (__any_sync(~0u, !plain)) {  // infinities, which do not count
       top = 0.f;
-      for_rows(slots, run, [&](long long row, int) {
+      for_rows(slots, p.c.bs_log2, run, [&](long long row, int) {
         if (on) top = finite_size(load_eight(src + row * stride), top);
       });
       for (int o = 1; o < lanes; o *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
@@ -313,7 +388,7 @@ __device__ __forceinline__ void append_across(const Slots<T> &slots, const Run &
       }
     }
     const float inv = __frcp_rn(scale);
-    for_rows(slots, run, [&](long long row, int off) {
+    for_rows(slots, p.c.bs_log2, run, [&](long long row, int off) {
       if (rows > 1) e = load_eight(src + row * stride);
       if (on)
         *reinterpret_cast<uint2 *>(to + off * p.c.d) =
@@ -328,9 +403,9 @@ __device__ __forceinline__ void append_across(const Slots<T> &slots, const Run &
 // mate and on.  kSteps: rounds of loads for 16 rows.  map: 16 rows a warp; top_of: a
 // number a warp, twice, in turn.
 template <typename T, int kSteps>
-__device__ __forceinline__ void append_along(const Slots<T> &slots, const Run &whole, int n0, int n1,
-                                             int *map, float (*top_of)[kWarps], int *turn) {
-  const Append<T> &p = slots.p;
+__device__ __forceinline__ void append_along(const Append<T> &p, const Slots &slots, const Run &whole,
+                                             int n0, int n1, int *map, float (*top_of)[kWarps],
+                                             int *turn) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int team_log2 = p.c.bs_log2 - 4, team = warp >> team_log2;
   const int mate = warp - (team << team_log2), off_mask = (1 << p.c.bs_log2) - 1;
@@ -340,11 +415,11 @@ __device__ __forceinline__ void append_along(const Slots<T> &slots, const Run &w
   if (lane < 16) map[lane] = -1;
   __syncwarp();
   int low = off_mask;
-  for (Run run = whole;; run = run.next(slots)) {
+  for (Run run = whole;; run = run.next(slots, p.c.bs_log2)) {
     if (run.in >> lane & 1) {
       const int off = static_cast<int>(run.slot) & off_mask;
       low = min(low, off);
-      if (off >> 4 == mate) map[off & 15] = static_cast<int>(run.base + lane);
+      if (off >> 4 == mate) map[off & 15] = static_cast<int>(slots.row(run.base + lane));
     }
     if (!run.more) break;
   }
@@ -418,48 +493,71 @@ __global__ void __launch_bounds__(kThreads, kSteps * sizeof(T) <= 16 ? 3 : kStep
   __shared__ int s_map[kWarps][16];
   __shared__ float s_top[2][kWarps];
   __shared__ long long s_slots[kThreads];
+  __shared__ unsigned s_there[kWarps], s_least[kWarps];  // rows of s_slots that count
+  __shared__ int s_far[kMostTokens];
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int team_log2 = p.c.bs_log2 - 4, team = warp >> team_log2, teams = kWarps >> team_log2;
+  const int bs_log2 = p.c.bs_log2, team_log2 = bs_log2 - 4;
+  const int team = warp >> team_log2, teams = kWarps >> team_log2;
   const int group = static_cast<int>(blockIdx.x % p.groups);
   const long long w0 = static_cast<long long>(blockIdx.x / p.groups) * p.window;
   const int n0 = group * p.per_cta, n1 = min(n0 + p.per_cta, 2 * p.c.Hk);
-  s_slots[threadIdx.x] = p.slot(w0 + threadIdx.x);
-  const Slots<T> slots = {p, s_slots, w0};
+  const long long near = p.slot(w0 + threadIdx.x);
+  s_slots[threadIdx.x] = near;
+  const unsigned counts = __ballot_sync(~0u, near >= 0);
+  if (lane == 0) s_there[warp] = counts;
   // (with the loads of the window's own: mostly it is the row ahead that tells)
   const long long ahead = p.slot(w0 - 32 + lane);
   __syncthreads();
+  // the last row that counts in the window, and among the rows at hand
+  const unsigned at_hand = lane < kWarps ? s_there[lane] : 0u;
+  const int left = p.window - 32 * lane;
+  const unsigned inside = left >= 32 ? at_hand : left > 0 ? at_hand & ((1u << left) - 1u) : 0u;
+  auto last_of = [](unsigned rows) {  // of 32 rows a lane
+    const int at = 31 - __clz(__ballot_sync(~0u, rows != 0));
+    return 32 * at + 31 - __clz(__shfl_sync(~0u, rows, at & 31));
+  };
+  if (!__any_sync(~0u, inside != 0)) return;
+  const int last = last_of(inside), last_near = last_of(at_hand);
+  // the block of the last row that counts ahead of the window's
+  long long before = -1;
+  if (w0 > 0) {
+    const unsigned some = __ballot_sync(~0u, ahead >= 0);
+    before = some ? __shfl_sync(~0u, ahead, 31 - __clz(some | 1u)) >> bs_log2
+                  : find_back(p, w0 - 32, s_least);
+  }
+  // The window's last run may go on behind the rows at hand, if no other block's follow:
+  // skipped rows may lie between its rows.
+  const long long block = s_slots[last] >> bs_log2;
+  Slots slots = {s_slots, s_far, w0, last_near + 1};
+  if (s_slots[last_near] >> bs_log2 == block && w0 + kThreads < p.T_) {
+    if (threadIdx.x < kMostTokens) s_far[threadIdx.x] = -1;
+    __syncthreads();
+    if (find_far(p, w0 + kThreads, block, s_far, s_least)) slots.end = kThreads + (1 << bs_log2);
+  }
   int runs = 0, turn = 0;
-  long long before = -1;  // the block of the last row that counts ahead of the rows at hand
   for (int part = 0; part < p.window; part += 32) {
-    const long long t0 = w0 + part;
-    if (t0 >= p.T_) break;
-    const long long mine = slots(t0 + lane);  // (also behind the window)
+    const long long mine = s_slots[part + lane];  // (also behind the window)
     const unsigned own = p.window - part < 32 ? (1u << (p.window - part)) - 1u : ~0u;
     const unsigned there = __ballot_sync(~0u, mine >= 0) & own;
     if (there == 0) continue;
-    // (while `before` is -1, no row of the window ahead of t0 counts)
-    for (long long t = w0, s = ahead; before < 0 && t > 0; t -= 32, s = p.slot(t - 32 + lane)) {
-      const unsigned some = __ballot_sync(~0u, s >= 0);
-      if (some) before = __shfl_sync(~0u, s, 31 - __clz(some)) >> p.c.bs_log2;
-    }
     const unsigned lower = there & ((1u << lane) - 1u);
-    const long long prev = __shfl_sync(~0u, mine, lower ? 31 - __clz(lower) : 0) >> p.c.bs_log2;
-    const bool leads = (there >> lane & 1) && (mine >> p.c.bs_log2) != (lower ? prev : before);
+    const long long prev = __shfl_sync(~0u, mine, lower ? 31 - __clz(lower) : 0) >> bs_log2;
+    const bool leads = (there >> lane & 1) && (mine >> bs_log2) != (lower ? prev : before);
     unsigned leaders = __ballot_sync(~0u, leads);
-    before = __shfl_sync(~0u, mine, 31 - __clz(there)) >> p.c.bs_log2;
+    before = __shfl_sync(~0u, mine, 31 - __clz(there)) >> bs_log2;
     // runs of up to four rows, on average: a warp each
     const bool many = __popc(leaders) * 4 >= __popc(there);
     while (leaders) {
       const int first = __ffs(leaders) - 1;
       leaders &= leaders - 1;
       if (runs++ % (many ? kWarps : teams) != (many ? warp : team)) continue;
-      const Run run(p, t0, mine, first, __shfl_sync(~0u, mine, first) >> p.c.bs_log2);
+      const Run run(slots, bs_log2, part, mine, first, __shfl_sync(~0u, mine, first) >> bs_log2);
       if (many)
-        append_across(slots, run, n0, n1);
+        append_across(p, slots, run, n0, n1);
       else
-        append_along<T, kSteps>(slots, run, n0, n1, s_map[warp], s_top, &turn);
+        append_along<T, kSteps>(p, slots, run, n0, n1, s_map[warp], s_top, &turn);
     }
   }
 }
