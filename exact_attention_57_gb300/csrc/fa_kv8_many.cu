@@ -3,16 +3,20 @@
 // of tokens of a key head.  Rows become fp16 by one conversion for two elements; the
 // scales go to the softmax, three numbers for 16 keys (BlockScale).
 //
-// The products of a 128 x 128 step need about 1000 cycles of the tensor pipe, the
-// exponentials alone 1024 of a scheduler's unit for them, expanding K and V 16 loads
-// and 32 stores of 16 bytes and 128 conversions a lane of two warps on it; a load of a
-// step's codes is issued a step ahead, into the register that its predecessor left.
+// The products of a 128 x 128 step need about 1000 of the 2660 cycles that it takes, the
+// unit for exponentials is in use for 550 of them (20.5% of 995,000 over 374 steps a CTA),
+// expanding K and V takes 16 loads and 32 stores of 16 bytes and 128 conversions a lane of
+// two warps a scheduler; a load of a step's codes is issued a step ahead, into the register
+// that its predecessor left.
 //
 // Two prompts' chunks of 2048 queries (32 query heads on 8 key heads of 128, causal, up
 // to 8192 keys) take 540 us, 875 TFLOP/s; 1024 queries on 65536 keys 1130 us, 965
-// TFLOP/s; the first at d = 64 439 us.  Softmax and expanding bound it together: of 541
+// TFLOP/s; the first at d = 64 439 us.  Of the 540 this kernel is 508, joining its parts 20,
+// the launch for sequences of few rows, of which there are none, the most of the rest.
+// Softmax and expanding bound it together: of 541
 // with queries of zeros, 509 were left without any loads, 528 without exponentials, and
-// of 448 at d = 64 386 without scales; issue slots are 52% busy.  Against 546 then:
+// of 448 at d = 64 386 without scales; issue slots are 53% busy, the tensor pipe 38%, and
+// 36 bytes a thread are spilled at either head dim (72 loaded).  Against 546 then:
 // scales applied by the expanding warps took 630 us, two steps of codes in registers 1650
 // (they spill), codes of K as e4m3 operands with Q as a sum of two or three e4m3 numbers
 // and codes of V by way of shared memory 670 (0.1 us less a step and 24 us more a tile).

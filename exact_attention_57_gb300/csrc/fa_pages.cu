@@ -13,7 +13,7 @@
 // Pages are copied by items of 16 KB dealt to the CTAs of one wave, 64 bytes in flight
 // a thread.  In captured graphs, pages of 8 heads of 128 and 64 tokens: 938 of a 4-bit
 // cache take 23.0 us, 6.0 TB/s or 89% of the copy rate; forking 64 requests into 256 (256
-// pages of an 8-bit cache) 12.6, of 9.8 that the bytes need, and listing what is free
+// pages of an 8-bit cache, of 64) 12.6, of 6.2 that the bytes need, and listing what is free
 // then (256 rows of 128 entries) 7.8, one cluster's chain of dependent steps: marks,
 // counts, lists.  Compacting 32 requests of up to 8192 tokens takes 49.6 us, 42.7 by its
 // bytes, about 6 of it the plan ahead of the copies.  Nine small pages: 1.6 us.
@@ -476,7 +476,16 @@ int pieces_of(const Pages &p) {
 // carries), more as one of kMaxArrays.
 constexpr int kFewArrays = 8;
 
-// A cluster of eight where the marking or the sweeping is long.
+// A cluster of eight where the marking or the sweeping is long.  Entries of the table, blocks,
+// and the us of fa_kv_free and of fa_kv_compact (tables alone) with one CTA and with eight,
+// in captured graphs:
+//      512     600   2.4  4.7    4.2  8.0        512   32768   4.8  7.7    4.7  8.3
+//     4096    8192   3.4  6.4    4.7  8.6        512   65536   7.3 11.1    4.9  8.6
+//     8192    8192   4.1  7.1    5.1  8.9        512  131072  12.3 16.4    5.7  9.8
+//    16384   16384   5.1  8.9    5.9  9.9      32768   65536  13.5 23.4    8.4 13.3
+//    32768   16384   9.6 12.9    7.8 11.4      32768  262144  27.7 52.0    9.7 16.6
+// Two and four CTAs are behind one of the others in nearly all of these (at 16384 entries
+// 7.6 12.5 and 6.6 10.8, at 65536 blocks 6.3 10.4 and 5.2 9.0).
 int sweep_cluster(int B, int width, int num_blocks) {
   return static_cast<long long>(B) * width > 8192 || num_blocks > 32768 ? 8 : 1;
 }

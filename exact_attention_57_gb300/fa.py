@@ -763,7 +763,8 @@ def attention_kv8(q, k_codes, k_scales, v_codes, v_scales, block_table, seq_lens
 def kv_copy(src, dst, caches, to=None, stream=None):
     """Copy page src[i] to page dst[i] (int32 [n] each; ids outside the cache skip
     a pair) of every array in caches, contiguous tensors [num_blocks, ...] such as
-    those of kv4_cache() or kv8_cache(), of all layers; to: arrays of another cache
+    those of kv4_cache() or kv8_cache(), of all layers (256 arrays a call at most;
+    several calls with the same inputs take more); to: arrays of another cache
     with the same pages, to write to.  Pages written differ, from one another and
     from those read.  Raises FaError on failure."""
     _done((_torch or _bind()).kv_copy(src, dst, tuple(caches), to if to is None else tuple(to),
@@ -776,7 +777,7 @@ def kv_fork(block_table, seq_lens, parents, free_blocks, block_size: int, caches
     """Requests begun from others' caches: child i continues row parents[i] (int32
     [n]) of block_table [B, max_blocks] at its length; it shares the full blocks and
     gets a copy of the last, partly filled one in a block from free_blocks (with
-    parents_end, a parent's first child keeps that block instead).  caches: the
+    parents_end, a parent's first child takes that entry over instead).  caches: the
     arrays to copy in (kv_copy's).  Returns (block_table [n, max_blocks], seq_lens
     [n], counts [2]: blocks needed, entries of free_blocks used up); out: those
     three tensors, to write to.  Raises FaError on failure."""
@@ -804,7 +805,7 @@ def kv_compact(block_table, seq_lens, caches, block_size: int, num_blocks: int |
     in every array of caches (kv_copy's) and returns (block_table with the new ids,
     new_ids int32 [num_blocks]: -1 for blocks not held, counts [2]: blocks held,
     pages moved); out: those three tensors, to write to (block_table itself may be
-    one).  The workspace (fa_kv_compact_workspace bytes) is allocated with torch
+    one, in the last call where more than 256 arrays take several).  The workspace (fa_kv_compact_workspace bytes) is allocated with torch
     unless given.  Raises FaError on failure."""
     return _done((_torch or _bind()).kv_compact(block_table, seq_lens, tuple(caches), num_blocks,
                                                 block_size, out if out is None else tuple(out),

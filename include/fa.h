@@ -573,8 +573,9 @@ FA_API int fa_kv8_append(const void *k, const void *v, long long k_stride, long 
 
 /*
  * fa_kv8_gather — R rows of the 8-bit cache as bf16, fp16 or fp32; slots, k_out and
- * v_out as for fa_kv4_gather.  code * scale is rounded once, and exact with scales
- * that are powers of two unless it leaves the type's range.
+ * v_out as for fa_kv4_gather.  code * scale is computed in fp32, then rounded to the
+ * type; with scales that are powers of two both are exact unless the value leaves the
+ * type's range.
  */
 FA_API int fa_kv8_gather(const long long *slots, int R, const void *k_codes, const float *k_scales,
                   const void *v_codes, const float *v_scales, void *k_out, void *v_out,
@@ -583,9 +584,10 @@ FA_API int fa_kv8_gather(const long long *slots, int R, const void *k_codes, con
 /*
  * fa_fwd_kv8 — attention of new queries over the 8-bit paged cache: fa_fwd_kv4's
  * arguments without the exponents, its rules and its workspace's (fa_fwd_kv8_workspace
- * bytes).  Queries and weights are rounded as there, codes are exact in the products,
- * and the scales are applied in fp32; a weight is rounded relative to the largest
- * weight times value scale of its row, so that blocks of any scales may meet in a
+ * bytes).  Queries and weights are rounded to fp16 as there (2^-11 of a weight at most,
+ * which in fp16 outputs is about as much as their own rounding), codes are exact in the
+ * products, and the scales are applied in fp32; a weight is rounded relative to the
+ * largest weight times value scale of its row, so that blocks of any scales may meet in a
  * sequence.  Scales of values count as the nearest in 2^-40 .. 2^40, a key's scale that
  * is not positive as 0.  A NaN among the codes of a key shows in the rows that see it;
  * one among those of a value in every query of its sequence (fa_kv8_append stores
@@ -619,7 +621,9 @@ FA_API int fa_fwd_kv8_schedule(int B, int Hq, int Hk, int max_seqlen_q, int max_
  * sizes (1 .. 2^31 - 1 bytes), each array being num_blocks contiguous pages; up to 256
  * (more: FA_ERR_UNSUPPORTED), which overlap neither one another nor the call's other
  * buffers.  So the four arrays of a 4-bit or an 8-bit cache, whose first dimension is
- * num_blocks, or any others.  Pages of whole 16-byte units, so aligned, are copied
+ * num_blocks, or any others.  Of more than 256 arrays (more than 64 layers of either
+ * cache) every 256 take a call of their own with the same inputs, which then writes the
+ * same tables: so only the last of several fa_kv_compact renumbers a table in place.  Pages of whole 16-byte units, so aligned, are copied
  * faster.
  * ------------------------------------------------------------------------ */
 
@@ -646,12 +650,13 @@ FA_API int fa_kv_copy(const int *src, const int *dst, int n, const void *const *
  *              the rest of a row is -1.  Lengths are the parents', at most
  *              max_blocks * block_size.
  * free_blocks, free_head, num_free  as for fa_kv_plan; read, not advanced.
- * parents_end  1: the parents do not go on; the first child of each keeps its last
- *              block, without a copy.
+ * parents_end  1: the parents do not go on; the first child of each takes its last
+ *              entry over as it stands, without a copy.
  * counts       int32 [2], out: blocks needed; entries of free_blocks used up
  *              (free_head for the next call, num_free at most).
  * Where the list runs out, or holds an id outside [0, num_blocks), the child's last
- * entry is -1.  A parent's last entry outside the cache makes its children's -1.
+ * entry is -1.  A parent's last entry outside the cache makes its children's -1, but for
+ * the one that takes it over with parents_end.
  * B and n 1 .. 65535; max_blocks * block_size <= 2^31 - 1.  num_arrays may be 0: tables
  * alone.
  */
