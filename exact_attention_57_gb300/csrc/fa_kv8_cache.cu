@@ -21,16 +21,16 @@
 //   many (new tokens of many requests): a warp takes a run, lanes and registers spread
 //     over the pairs.
 // Rows that are skipped, as those that fill a padded batch, are looked at by the whole
-// CTA, once: 64 new tokens in a batch of 4096 rows take 9.8 us (187 when each warp walked
-// to the end of its run, 32 rows a step, for each of its pairs), in one of 8192 25 (135).
+// CTA, once: 64 new tokens in a batch of 4096 rows take 7.8 us (187 when each warp walked
+// to the end of its run, 32 rows a step, for each of its pairs), in one of 8192 20 (135).
 //
 // 30299 rows of 4 prompts (8 heads of 128, fp16) take 44 us, 4.2 TB/s or 62% of the copy
-// rate (fp32 62; its variant of four steps spills 72 bytes a thread): a CTA finds its runs, loads, meets its team, converts and stores in turn, and the
-// three of an SM cover for one another only in part.  A warp a run and pair, with divisions
-// in line, took 105; slots read anew for every 32 rows of the window 48; the next pair's
-// loads into registers as they fall free 49 (registers spill; with two CTAs 51).  Reading
-// 30299 rows back takes 30 us, 6.3 TB/s (93%); one row of each of 64 requests 3.8 us and
-// reading them back 1.8, a launch each.
+// rate (fp32 62; its variant of four steps spills 72 bytes a thread): a CTA finds its runs,
+// loads, meets its team, converts and stores in turn, and the three of an SM cover for one
+// another only in part.  A warp a run and pair, with divisions in line, took 105; slots read
+// anew for every 32 rows of the window 48; the next pair's loads into registers as they fall
+// free 49 (registers spill; with two CTAs 51).  Reading 30299 rows back takes 30 us, 6.3 TB/s
+// (93%); one row of each of 64 requests 3.7 us and reading them back 1.8, a launch each.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -212,7 +212,10 @@ struct Append {
   // The slot of row t, -1 for rows that are skipped.
   __device__ __forceinline__ long long slot(long long t) const {
     const long long s = t >= 0 && t < T_ ? __ldg(slots + t) : -1;
-    return s < static_cast<long long>(c.num_blocks) << c.bs_log2 ? s : -1;
+    return s < limit() ? s : -1;
+  }
+  __device__ __forceinline__ long long limit() const {
+    return static_cast<long long>(c.num_blocks) << c.bs_log2;
   }
 };
 
@@ -241,6 +244,23 @@ struct Slots {
 // Rows that a thread looks at side by side, outside the window.
 constexpr int kAtOnce = 16;
 
+// The slots of rows from + step * (thread, thread + kThreads, ...), as far as there are rows
+// (else -1): all loads ahead of what is made of them (one after the other they took 4.4 us
+// for a CTA's 4096 rows).
+__device__ __forceinline__ void look(const long long *slots, int T, long long limit, long long from,
+                                     int step, long long (&s)[kAtOnce]) {
+#pragma unroll
+  for (int i = 0; i < kAtOnce; ++i) {
+    const long long t = from + step * static_cast<int>(i * kThreads + threadIdx.x);
+    s[i] = __ldg(slots + min(max(t, 0LL), T - 1LL));
+  }
+#pragma unroll
+  for (int i = 0; i < kAtOnce; ++i) {
+    const long long t = from + step * static_cast<int>(i * kThreads + threadIdx.x);
+    s[i] = t >= 0 && t < T && s[i] < limit ? s[i] : -1;
+  }
+}
+
 // The least of `x` over the CTA.
 __device__ __forceinline__ unsigned least_of(unsigned x, unsigned *least) {
   x = __reduce_min_sync(~0u, x);
@@ -252,22 +272,20 @@ __device__ __forceinline__ unsigned least_of(unsigned x, unsigned *least) {
 
 // Notes the rows of `block` from row `from` on, up to the first of another block, in far
 // (of -1 before), by the whole CTA; whether there are any.
-template <typename T>
-__device__ __noinline__ bool find_far(const Append<T> &p, long long from, long long block, int *far,
-                                      unsigned *least) {
+__device__ __noinline__ bool find_far(const long long *slots, int T, long long limit, int bs_log2,
+                                      long long from, long long block, int *far, unsigned *least) {
   constexpr unsigned kChunk = kAtOnce * kThreads;
-  const int off_mask = (1 << p.c.bs_log2) - 1;
+  const int off_mask = (1 << bs_log2) - 1;
   bool found = false;
-  for (; from < p.T_; from += kChunk) {
+  for (; from < T; from += kChunk) {
     long long s[kAtOnce];
+    look(slots, T, limit, from, 1, s);
     unsigned other = kChunk;  // the first row of another block
     bool some = false;
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) s[i] = p.slot(from + i * kThreads + threadIdx.x);
-#pragma unroll
     for (int i = kAtOnce - 1; i >= 0; --i) {
       some |= s[i] >= 0;
-      if (s[i] >= 0 && s[i] >> p.c.bs_log2 != block) other = i * kThreads + threadIdx.x;
+      if (s[i] >= 0 && s[i] >> bs_log2 != block) other = i * kThreads + threadIdx.x;
     }
     if (!__syncthreads_or(some)) continue;
     other = least_of(other, least);
@@ -275,7 +293,7 @@ __device__ __noinline__ bool find_far(const Append<T> &p, long long from, long l
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) {
       const unsigned n = i * kThreads + threadIdx.x;
-      if (s[i] >= 0 && s[i] >> p.c.bs_log2 == block && n < other) {
+      if (s[i] >= 0 && s[i] >> bs_log2 == block && n < other) {
         far[static_cast<int>(s[i]) & off_mask] = static_cast<int>(from + n);
         mine = true;
       }
@@ -286,17 +304,18 @@ __device__ __noinline__ bool find_far(const Append<T> &p, long long from, long l
   return found;
 }
 
-// The block of the last row that counts ahead of row `to`, or -1, by the whole CTA.
-template <typename T>
-__device__ __noinline__ long long find_back(const Append<T> &p, long long to, unsigned *least) {
+// The slot of the last row that counts ahead of row `to`, or -1, by the whole CTA.
+__device__ __noinline__ long long find_back(const long long *slots, int T, long long limit,
+                                            long long to, unsigned *least) {
   constexpr unsigned kChunk = kAtOnce * kThreads;
   for (; to > 0; to -= kChunk) {
+    long long s[kAtOnce];
+    look(slots, T, limit, to - 1, -1, s);
     unsigned back = kChunk;
 #pragma unroll
     for (int i = kAtOnce - 1; i >= 0; --i)
-      if (p.slot(to - 1 - i * kThreads - threadIdx.x) >= 0) back = i * kThreads + threadIdx.x;
-    if (!__syncthreads_or(back < kChunk)) continue;
-    return p.slot(to - 1 - least_of(back, least)) >> p.c.bs_log2;
+      if (s[i] >= 0) back = i * kThreads + threadIdx.x;
+    if (__syncthreads_or(back < kChunk)) return __ldg(slots + (to - 1 - least_of(back, least)));
   }
   return -1;
 }
@@ -525,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, kSteps * sizeof(T) <= 16 ? 3 : kStep
   if (w0 > 0) {
     const unsigned some = __ballot_sync(~0u, ahead >= 0);
     before = some ? __shfl_sync(~0u, ahead, 31 - __clz(some | 1u)) >> bs_log2
-                  : find_back(p, w0 - 32, s_least);
+                  : find_back(p.slots, p.T_, p.limit(), w0 - 32, s_least) >> bs_log2;
   }
   // The window's last run may go on behind the rows at hand, if no other block's follow:
   // skipped rows may lie between its rows.
@@ -534,7 +553,8 @@ __global__ void __launch_bounds__(kThreads, kSteps * sizeof(T) <= 16 ? 3 : kStep
   if (s_slots[last_near] >> bs_log2 == block && w0 + kThreads < p.T_) {
     if (threadIdx.x < kMostTokens) s_far[threadIdx.x] = -1;
     __syncthreads();
-    if (find_far(p, w0 + kThreads, block, s_far, s_least)) slots.end = kThreads + (1 << bs_log2);
+    if (find_far(p.slots, p.T_, p.limit(), bs_log2, w0 + kThreads, block, s_far, s_least))
+      slots.end = kThreads + (1 << bs_log2);
   }
   int runs = 0, turn = 0;
   for (int part = 0; part < p.window; part += 32) {
