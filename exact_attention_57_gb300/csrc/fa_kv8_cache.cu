@@ -304,9 +304,10 @@ __device__ __noinline__ bool find_far(const long long *slots, int T, long long l
   return found;
 }
 
-// The slot of the last row that counts ahead of row `to`, or -1, by the whole CTA.
+// The slot of the last row that counts ahead of row `to`, or -1, by the whole CTA.  (Read
+// once, as all slots are: warps that saw different ones would wait for one another in vain.)
 __device__ __noinline__ long long find_back(const long long *slots, int T, long long limit,
-                                            long long to, unsigned *least) {
+                                            long long to, unsigned *least, long long *found) {
   constexpr unsigned kChunk = kAtOnce * kThreads;
   for (; to > 0; to -= kChunk) {
     long long s[kAtOnce];
@@ -315,7 +316,13 @@ __device__ __noinline__ long long find_back(const long long *slots, int T, long 
 #pragma unroll
     for (int i = kAtOnce - 1; i >= 0; --i)
       if (s[i] >= 0) back = i * kThreads + threadIdx.x;
-    if (__syncthreads_or(back < kChunk)) return __ldg(slots + (to - 1 - least_of(back, least)));
+    if (!__syncthreads_or(back < kChunk)) continue;
+    back = least_of(back, least);
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i)
+      if (back == i * kThreads + threadIdx.x) *found = s[i];
+    __syncthreads();
+    return *found;
   }
   return -1;
 }
@@ -511,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, kSteps * sizeof(T) <= 16 ? 3 : kStep
     fa_kv8_append_kernel(const __grid_constant__ Append<T> p) {
   __shared__ int s_map[kWarps][16];
   __shared__ float s_top[2][kWarps];
-  __shared__ long long s_slots[kThreads];
+  __shared__ long long s_slots[kThreads], s_ahead[32];
   __shared__ unsigned s_there[kWarps], s_least[kWarps];  // rows of s_slots that count
   __shared__ int s_far[kMostTokens];
   griddep_wait();
@@ -523,11 +530,12 @@ __global__ void __launch_bounds__(kThreads, kSteps * sizeof(T) <= 16 ? 3 : kStep
   const long long w0 = static_cast<long long>(blockIdx.x / p.groups) * p.window;
   const int n0 = group * p.per_cta, n1 = min(n0 + p.per_cta, 2 * p.c.Hk);
   const long long near = p.slot(w0 + threadIdx.x);
+  // (with the loads of the window's own: mostly it is the row ahead that tells)
+  const long long ahead = p.slot(w0 - 32 + lane);
   s_slots[threadIdx.x] = near;
   const unsigned counts = __ballot_sync(~0u, near >= 0);
   if (lane == 0) s_there[warp] = counts;
-  // (with the loads of the window's own: mostly it is the row ahead that tells)
-  const long long ahead = p.slot(w0 - 32 + lane);
+  if (warp == 0) s_ahead[lane] = ahead;
   __syncthreads();
   // the last row that counts in the window, and among the rows at hand
   const unsigned at_hand = lane < kWarps ? s_there[lane] : 0u;
@@ -542,9 +550,9 @@ __global__ void __launch_bounds__(kThreads, kSteps * sizeof(T) <= 16 ? 3 : kStep
   // the block of the last row that counts ahead of the window's
   long long before = -1;
   if (w0 > 0) {
-    const unsigned some = __ballot_sync(~0u, ahead >= 0);
-    before = some ? __shfl_sync(~0u, ahead, 31 - __clz(some | 1u)) >> bs_log2
-                  : find_back(p.slots, p.T_, p.limit(), w0 - 32, s_least) >> bs_log2;
+    const unsigned some = __ballot_sync(~0u, s_ahead[lane] >= 0);
+    before = (some ? s_ahead[31 - __clz(some)]
+                   : find_back(p.slots, p.T_, p.limit(), w0 - 32, s_least, s_ahead)) >> bs_log2;
   }
   // The window's last run may go on behind the rows at hand, if no other block's follow:
   // skipped rows may lie between its rows.

@@ -805,8 +805,9 @@ def kv_compact(block_table, seq_lens, caches, block_size: int, num_blocks: int |
     in every array of caches (kv_copy's) and returns (block_table with the new ids,
     new_ids int32 [num_blocks]: -1 for blocks not held, counts [2]: blocks held,
     pages moved); out: those three tensors, to write to (block_table itself may be
-    one, in the last call where more than 256 arrays take several).  The workspace (fa_kv_compact_workspace bytes) is allocated with torch
-    unless given.  Raises FaError on failure."""
+    one, in the last call where more than 256 arrays take several).  The workspace
+    (fa_kv_compact_workspace bytes) is allocated with torch unless given.  Raises
+    FaError on failure."""
     return _done((_torch or _bind()).kv_compact(block_table, seq_lens, tuple(caches), num_blocks,
                                                 block_size, out if out is None else tuple(out),
                                                 workspace, stream), "fa_kv_compact")

@@ -623,8 +623,8 @@ FA_API int fa_fwd_kv8_schedule(int B, int Hq, int Hk, int max_seqlen_q, int max_
  * buffers.  So the four arrays of a 4-bit or an 8-bit cache, whose first dimension is
  * num_blocks, or any others.  Of more than 256 arrays (more than 64 layers of either
  * cache) every 256 take a call of their own with the same inputs, which then writes the
- * same tables: so only the last of several fa_kv_compact renumbers a table in place.  Pages of whole 16-byte units, so aligned, are copied
- * faster.
+ * same tables: so only the last of several fa_kv_compact renumbers a table in place.
+ * Pages of whole 16-byte units, so aligned, are copied faster.
  * ------------------------------------------------------------------------ */
 
 /*
