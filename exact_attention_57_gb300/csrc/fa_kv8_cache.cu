@@ -25,7 +25,7 @@
 // to the end of its run, 32 rows a step, for each of its pairs), in one of 8192 20 (135).
 //
 // 30299 rows of 4 prompts (8 heads of 128, fp16) take 44 us, 4.2 TB/s or 62% of the copy
-// rate (fp32 62; its variant of four steps spills 72 bytes a thread): a CTA finds its runs,
+// rate (fp32 62; its variant of four steps spills 64 bytes a thread): a CTA finds its runs,
 // loads, meets its team, converts and stores in turn, and the three of an SM cover for one
 // another only in part.  A warp a run and pair, with divisions in line, took 105; slots read
 // anew for every 32 rows of the window 48; the next pair's loads into registers as they fall
